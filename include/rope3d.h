@@ -393,6 +393,196 @@ int rope3d_testing_na3d_last_kernel(void);
 int rope3d_testing_na3d_per_cta(int32_t on);
 int rope3d_testing_na3d_wait_timeouts(int64_t *count, int32_t reset);
 
+/* ---- the rest of a transformer block --------------------------------------
+ *
+ * The two operators a block needs around its attention: the norms before and
+ * after each of its halves, with the modulation, gate and residual scale of a
+ * diffusion block or the paired norms of the Gemma3 text encoder's layers, and
+ * the gated feed-forward. Each has its backward pass. They are extensions: the
+ * pages describe the blocks' attention path (RoPE, layout, attention) and give
+ * no code for these, so the formulas below are the definition.
+ *
+ * Rows are tokens. Every matrix is row-major with contiguous rows' elements and
+ * a row stride in elements (>= its columns). Outputs must not overlap any other
+ * argument (judged by address range), except where in-place use is named.
+ */
+
+/* normalisations */
+#define ROPE3D_NORM_NONE  0   /* the identity                                  */
+#define ROPE3D_NORM_RMS   1   /* v * rsqrt(mean(v^2) + eps)                    */
+#define ROPE3D_NORM_LAYER 2   /* (v - mean) * rsqrt(mean((v - mean)^2) + eps)  */
+
+/* activations */
+#define ROPE3D_ACT_SILU      0   /* g * sigmoid(g)                             */
+#define ROPE3D_ACT_GELU_TANH 1   /* 0.5 g (1 + tanh(sqrt(2/pi)(g + 0.044715 g^3))) */
+#define ROPE3D_ACT_GELU_ERF  2   /* 0.5 g (1 + erf(g / sqrt(2)))               */
+
+#define ROPE3D_MAX_CHANNELS 65536   /* rope3d_block_norm: more -> ROPE3D_ERR_SHAPE */
+
+/*
+ * rope3d_block_norm -- the end of one half of a transformer block and the start
+ * of the next, in one pass:
+ *     r = residual_scale * x + gate_g * post(y) * (post_weight + weight_offset)
+ *     n = pre(r) * (pre_weight + weight_offset) * (1 + scale_g) + shift_g
+ * post and pre are one of ROPE3D_NORM_*; gate_g, scale_g and shift_g are rows
+ * of one sample: row i of x belongs to group g = i / rows_per_group. Absent
+ * parts (NULL) are left out: y (then r = residual_scale * x), the weights, gate,
+ * scale, shift; r or n (not both) is not computed when NULL. So y = NULL is a
+ * norm before a block, n = NULL a norm after one with its gate and residual,
+ * and both together end one block and begin the next.
+ * Everything is computed in fp32 (the statistics too; n from the unrounded r)
+ * and rounded once to the output's type.
+ *
+ *   x, y, r, n   device, [rows, channels] of `dtype`
+ *   post_weight, pre_weight   [channels] of `param_dtype`; a weight of an absent
+ *                or identity norm must be NULL for post (ROPE3D_ERR_ARG), and is
+ *                applied for pre
+ *   gate, scale, shift        [groups, channels] of `param_dtype`, groups =
+ *                ceil(rows / rows_per_group), row strides gate_stride, ...
+ *   param_dtype  dtype or ROPE3D_F32
+ *   weight_offset  added to both weights (Gemma3's norms store w - 1: 1.0)
+ *   eps          finite, >= 0
+ * In place: r and n may each be exactly x or exactly y (same address and row
+ * stride); they never overlap otherwise. One kernel on `stream`, asynchronous.
+ * Errors: NULL (args, x, or both r and n), SHAPE (a size <= 0, channels or a
+ * stride out of range), DTYPE, ALIGN (a pointer not aligned to its element),
+ * ARG (kinds, eps, residual_scale or weight_offset not finite, a post weight or
+ * gate without y), ALIAS, DEVICE, CUDA.
+ */
+typedef struct rope3d_block_norm_args {
+    const void *x, *y;
+    const void *post_weight, *gate, *pre_weight, *scale, *shift;
+    void *r, *n;
+    int64_t rows, channels, rows_per_group;
+    int64_t x_stride, y_stride, r_stride, n_stride;
+    int64_t gate_stride, scale_stride, shift_stride;
+    double eps, residual_scale, weight_offset;
+    int32_t dtype, param_dtype, post_kind, pre_kind;
+} rope3d_block_norm_args;
+
+int rope3d_block_norm(const rope3d_block_norm_args *args, void *stream);
+/* The checks of rope3d_block_norm without a launch; check_device = 0 skips the
+ * device-memory query. */
+int rope3d_block_norm_check(const rope3d_block_norm_args *args, int32_t check_device);
+
+/*
+ * rope3d_block_norm_backward -- the gradients of rope3d_block_norm from x, y
+ * and the gradients dr of r and dn of n (either may be NULL: zero). Nothing else
+ * is kept from the forward pass: the statistics are computed again from x and y
+ * while they are in registers.
+ *
+ *   fwd     the forward call's arguments; r and n are not used
+ *   dr, dn  [rows, channels] of `dtype`
+ *   dx, dy  [rows, channels] of `dtype`; dy is required exactly when y is given
+ *   d_post_weight, d_pre_weight   [channels] of `param_dtype`
+ *   d_gate, d_scale, d_shift      [groups, channels] of `param_dtype`, row
+ *           stride grad_stride
+ *           Each may be NULL (not wanted); one whose parameter is absent must be.
+ *   workspace  device, 256-byte aligned, of at least the size that
+ *           rope3d_block_norm_backward_workspace gives for the same arguments
+ *           (0: none needed, NULL allowed); its contents are not kept
+ * Column sums are added in a fixed order: the same arguments give the same bits.
+ * dx may be exactly dr or dn, dy exactly dn or dr (same address and row stride;
+ * never both the same one). Asynchronous on `stream`.
+ * Errors: as rope3d_block_norm; SCRATCH (workspace too small).
+ */
+typedef struct rope3d_block_norm_backward_args {
+    rope3d_block_norm_args fwd;
+    const void *dr, *dn;
+    void *dx, *dy;
+    void *d_post_weight, *d_gate, *d_pre_weight, *d_scale, *d_shift;
+    int64_t dr_stride, dn_stride, dx_stride, dy_stride, grad_stride;
+    void *workspace;
+    int64_t workspace_bytes;
+} rope3d_block_norm_backward_args;
+
+int rope3d_block_norm_backward(const rope3d_block_norm_backward_args *args, void *stream);
+int rope3d_block_norm_backward_check(const rope3d_block_norm_backward_args *args, int32_t check_device);
+int rope3d_block_norm_backward_workspace(const rope3d_block_norm_backward_args *args, int64_t *bytes);
+
+/* Which kernel this thread's last norm call used: 1 the vector kernel (rows in
+ * registers), 2 the general one, 0 none yet. */
+int rope3d_block_norm_last_kernel(void);
+
+/*
+ * rope3d_gated_ffn -- the gated feed-forward of a transformer block:
+ *     g = x w_gate^T,  u = x w_up^T,  y = (act(g) * u) w_down^T
+ *
+ *   x            device, [tokens, width] of `dtype` (ROPE3D_BF16 or ROPE3D_F16)
+ *   w_gate, w_up [hidden, width] (the halves of one [2 hidden, width] matrix, or
+ *                two matrices); w_down [width, hidden]; all of `dtype`
+ *   y            [tokens, width] of `dtype`
+ *   gate_pre, up_pre   both or neither: g and u, [tokens, hidden], kept for the
+ *                backward pass in `pre_dtype` (dtype or ROPE3D_F32), row stride
+ *                pre_stride
+ *   workspace    device, 256-byte aligned, of at least the size that
+ *                rope3d_gated_ffn_workspace gives for the same arguments; its
+ *                contents are not kept. Calls that may run at the same time
+ *                need workspaces of their own.
+ * Products accumulate in fp32; act(g) * u is computed in fp32 from the unrounded
+ * accumulators and rounded once to `dtype` (in fp16 it overflows beyond 65504),
+ * as an operand of the second product, and y is rounded once.
+ * Any strides and element-aligned addresses are taken. A matrix whose rows do
+ * not all start on 16-byte boundaries is first copied into the workspace, which
+ * costs a pass over it.
+ * Errors: NULL, SHAPE (a size <= 0, width or hidden above 2^20, tokens above
+ * 2^28, a stride below its row or above 2^31), DTYPE, ARG (act), ALIGN, ALIAS,
+ * SCRATCH (workspace too small), DEVICE, CUDA.
+ */
+typedef struct rope3d_gated_ffn_args {
+    const void *x, *w_gate, *w_up, *w_down;
+    void *y, *gate_pre, *up_pre;
+    int64_t tokens, width, hidden;
+    int64_t x_stride, w_gate_stride, w_up_stride, w_down_stride, y_stride, pre_stride;
+    void *workspace;
+    int64_t workspace_bytes;
+    int32_t dtype, pre_dtype, act;
+} rope3d_gated_ffn_args;
+
+int rope3d_gated_ffn(const rope3d_gated_ffn_args *args, void *stream);
+/* The checks without a launch; check_device = 0 skips the device-memory query. */
+int rope3d_gated_ffn_check(const rope3d_gated_ffn_args *args, int32_t check_device);
+/* The workspace's size; args->workspace and workspace_bytes are not read. */
+int rope3d_gated_ffn_workspace(const rope3d_gated_ffn_args *args, int64_t *bytes);
+
+/*
+ * rope3d_gated_ffn_backward -- its gradients from dy:
+ *     dh = dy w_down, dg = dh * u * act'(g), du = dh * act(g)
+ *     dx = dg w_gate + du w_up
+ *     dw_gate = dg^T x, dw_up = du^T x, dw_down = dy^T (act(g) * u)
+ *
+ *   gate_pre, up_pre   as the forward pass kept them, or both NULL: computed
+ *                again from x (a third more work, no memory kept in between)
+ *   dx           [tokens, width]; dw_gate and dw_up [hidden, width] (both or
+ *                neither); dw_down [width, hidden]; each may be NULL (not
+ *                wanted), not all. Written, not added to.
+ * dg, du and act(g) * u are computed in fp32 and rounded once to `dtype`, as
+ * operands of the products; those accumulate in fp32 in a fixed order.
+ * Workspace and errors as rope3d_gated_ffn.
+ */
+typedef struct rope3d_gated_ffn_backward_args {
+    const void *dy, *x, *w_gate, *w_up, *w_down, *gate_pre, *up_pre;
+    void *dx, *dw_gate, *dw_up, *dw_down;
+    int64_t tokens, width, hidden;
+    int64_t dy_stride, x_stride, w_gate_stride, w_up_stride, w_down_stride, pre_stride;
+    int64_t dx_stride, dw_gate_stride, dw_up_stride, dw_down_stride;
+    void *workspace;
+    int64_t workspace_bytes;
+    int32_t dtype, pre_dtype, act;
+} rope3d_gated_ffn_backward_args;
+
+int rope3d_gated_ffn_backward(const rope3d_gated_ffn_backward_args *args, void *stream);
+int rope3d_gated_ffn_backward_check(const rope3d_gated_ffn_backward_args *args, int32_t check_device);
+int rope3d_gated_ffn_backward_workspace(const rope3d_gated_ffn_backward_args *args, int64_t *bytes);
+
+/* Which kernel computed this thread's last feed-forward (its products with the
+ * weights): 1 tiles of many tokens, 2 weights streamed for few, 0 none yet. */
+int rope3d_gated_ffn_last_kernel(void);
+/* How many bounded waits of the feed-forward's kernels ran out (0 unless
+ * something is badly wrong; such a launch's output is not to be used); reset
+ * clears the count. Synchronises with the device. Errors: NULL, CUDA. */
+int rope3d_testing_ffn_wait_timeouts(int64_t *count, int32_t reset);
+
 /*
  * rope3d_apply_pair_host -- the same rotation for HOST buffers: the library
  * streams Q and K to the GPU in token chunks, rotates each chunk with the same

@@ -34,6 +34,10 @@ __all__ = [
     "rope3d_testing_debug_shrink_tables", "rope3d_dit_freqs_host", "rope3d_cache_retired",
     "rope3d_testing_na3d_kernel", "rope3d_testing_na3d_last_kernel", "rope3d_testing_na3d_per_cta",
     "rope3d_testing_na3d_wait_timeouts",
+    "NORM_NONE", "NORM_RMS", "NORM_LAYER", "ACT_SILU", "ACT_GELU_TANH", "ACT_GELU_ERF",
+    "rope3d_gated_ffn", "rope3d_gated_ffn_backward", "rope3d_gated_ffn_check",
+    "rope3d_gated_ffn_backward_check", "rope3d_gated_ffn_last_kernel",
+    "rope3d_testing_ffn_wait_timeouts",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -43,6 +47,8 @@ LIB_PATH = os.environ.get("ROPE3D_LIB") or os.path.join(HERE, "_build", "librope
 
 BF16, F32, F16 = 0, 1, 2
 GATE_OFF, GATE_FIRST = 0, 1
+NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
+ACT_SILU, ACT_GELU_TANH, ACT_GELU_ERF = 0, 1, 2
 STATUS = {
     0: "OK", -1: "ERR_NULL", -2: "ERR_SHAPE", -3: "ERR_DTYPE", -4: "ERR_ALIGN",
     -5: "ERR_ALIAS", -6: "ERR_DEVICE", -7: "ERR_PARITY", -8: "ERR_CUDA", -9: "ERR_TABLES",
@@ -59,6 +65,28 @@ class Rope3dError(RuntimeError):
         self.name = STATUS.get(status, str(status))
         msg = rope3d_status_string(status) if _lib is not None else self.name
         super().__init__(f"{what}: {msg}" if what else msg)
+
+
+def _struct(name, *fields):
+    """A ctypes structure from "type: field field ..." lines."""
+    kinds = {"p": ctypes.c_void_p, "i64": ctypes.c_int64, "i32": ctypes.c_int32, "f64": ctypes.c_double}
+    out = []
+    for line in fields:
+        kind, names = line.split(":")
+        out += [(n, kinds[kind]) for n in names.split()]
+    return type(name, (ctypes.Structure,), {"_fields_": out})
+
+
+_FfnArgs = _struct(
+    "rope3d_gated_ffn_args", "p:x w_gate w_up w_down y gate_pre up_pre", "i64:tokens width hidden",
+    "i64:x_stride w_gate_stride w_up_stride w_down_stride y_stride pre_stride",
+    "p:workspace", "i64:workspace_bytes", "i32:dtype pre_dtype act")
+_FfnBackArgs = _struct(
+    "rope3d_gated_ffn_backward_args", "p:dy x w_gate w_up w_down gate_pre up_pre",
+    "p:dx dw_gate dw_up dw_down", "i64:tokens width hidden",
+    "i64:dy_stride x_stride w_gate_stride w_up_stride w_down_stride pre_stride",
+    "i64:dx_stride dw_gate_stride dw_up_stride dw_down_stride",
+    "p:workspace", "i64:workspace_bytes", "i32:dtype pre_dtype act")
 
 
 def _declare(lib):
@@ -110,6 +138,14 @@ def _declare(lib):
         "rope3d_na3d": ([vp] * 5 + [i64] * 6 + [vp, vp, i32, vp], c.c_int),
         "rope3d_na3d_rotate_once": ([vp] * 6 + [i64] * 6 + [vp, vp, vp], c.c_int),
         "rope3d_na3d_preflight": ([vp] * 6 + [i64] * 6 + [vp, vp, i32, i32], c.c_int),
+        "rope3d_gated_ffn": ([vp, vp], c.c_int),
+        "rope3d_gated_ffn_check": ([vp, i32], c.c_int),
+        "rope3d_gated_ffn_workspace": ([vp, vp], c.c_int),
+        "rope3d_gated_ffn_backward": ([vp, vp], c.c_int),
+        "rope3d_gated_ffn_backward_check": ([vp, i32], c.c_int),
+        "rope3d_gated_ffn_backward_workspace": ([vp, vp], c.c_int),
+        "rope3d_gated_ffn_last_kernel": ([], c.c_int),
+        "rope3d_testing_ffn_wait_timeouts": ([vp, i32], c.c_int),
         "rope3d_preflight_strided": ([vp, vp, vp, vp, vp] + [i64] * 6 + [vp, i32] + [vp] * 4 + [i32],
                                      c.c_int),
     }
@@ -563,6 +599,150 @@ def rope3d_na3d_preflight(q, k, v, k_rot, out, tables, B, T, H, W, heads, kernel
         int(W), int(heads), int(head_dim), _split(split) if split is not None else None, ks,
         1 if apply_rope else 0, 1 if check_device else 0)
     return STATUS.get(rc, str(rc))
+
+
+def _matrix(name, t, rows=None, cols=None, dtype=None):
+    """(rows, cols, row stride) of a matrix: the last dimension contiguous, the
+    others viewable as one."""
+    if t.dim() < 2 or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must be a matrix with contiguous rows")
+    c = int(t.shape[-1])
+    if t.dim() == 2:
+        r, ld = int(t.shape[0]), int(t.stride(0))
+        if r <= 1:
+            ld = max(ld, c)
+    else:
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous, or a 2-D view with contiguous rows")
+        r, ld = (t.numel() // c if c else 0), c
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {rows if rows is not None else r} rows "
+                         f"of {cols if cols is not None else c}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    return r, c, ld
+
+
+def _scratch(nbytes: int, like, stream):
+    """Device memory for one call: freed for other work only after what `stream`
+    holds so far."""
+    import torch
+
+    ws = torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=like.device)
+    if stream is not None:
+        handle = _stream(stream)
+        if handle != int(torch.cuda.current_stream(like.device).cuda_stream):
+            ws.record_stream(torch.cuda.ExternalStream(handle, device=like.device))
+    return ws
+
+
+def _ffn_args(x, w_gate, w_up, w_down, y, gate_pre, up_pre, act, keep_like=None):
+    tokens, width, ldx = _matrix("x", x)
+    hidden = int(w_gate.shape[0])
+    a = _FfnArgs(x=_ptr(x), w_gate=_ptr(w_gate), w_up=_ptr(w_up), w_down=_ptr(w_down), y=_ptr(y),
+                 gate_pre=_ptr(gate_pre), up_pre=_ptr(up_pre), tokens=tokens, width=width, hidden=hidden,
+                 x_stride=ldx, w_gate_stride=_matrix("w_gate", w_gate, hidden, width, x.dtype)[2],
+                 w_up_stride=_matrix("w_up", w_up, hidden, width, x.dtype)[2],
+                 w_down_stride=_matrix("w_down", w_down, width, hidden, x.dtype)[2],
+                 y_stride=_matrix("y", y, tokens, width, x.dtype)[2],
+                 dtype=_dtype_code(x), pre_dtype=_dtype_code(x), act=int(act))
+    if (gate_pre is None) != (up_pre is None):
+        raise ValueError("gate_pre and up_pre come together")
+    if gate_pre is not None:
+        a.pre_stride = _matrix("gate_pre", gate_pre, tokens, hidden)[2]
+        if _matrix("up_pre", up_pre, tokens, hidden, gate_pre.dtype)[2] != a.pre_stride:
+            raise ValueError("gate_pre and up_pre must have one row stride")
+        a.pre_dtype = _dtype_code(gate_pre)
+    return a
+
+
+def rope3d_gated_ffn(x, w_gate, w_up, w_down, act: int = ACT_GELU_TANH, y=None, keep=False,
+                     gate_pre=None, up_pre=None, workspace=None, stream=None):
+    """Gated feed-forward: (act(x w_gate^T) * (x w_up^T)) w_down^T for x [tokens,
+    width] (or [..., width]), w_gate and w_up [hidden, width], w_down [width,
+    hidden], bf16 or fp16 on the device. keep: also return the two projections
+    [tokens, hidden] for the backward pass, in float32 (True) or in a given dtype
+    (float32 or x's); gate_pre / up_pre take them instead of new tensors. Returns
+    y, or (y, gate_pre, up_pre). workspace: a uint8 device tensor of at least the
+    bytes the call needs (allocated when None)."""
+    import torch
+
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if (keep is not False and keep is not None) and gate_pre is None and up_pre is None:
+        dt = torch.float32 if keep is True else keep
+        shape = (*x.shape[:-1], int(w_gate.shape[0]))
+        gate_pre = torch.empty(shape, dtype=dt, device=x.device)
+        up_pre = torch.empty(shape, dtype=dt, device=x.device)
+    lib = load_library()
+    a = _ffn_args(x, w_gate, w_up, w_down, y, gate_pre, up_pre, act)
+    need = ctypes.c_int64()
+    _check(lib.rope3d_gated_ffn_workspace(ctypes.byref(a), ctypes.byref(need)), "rope3d_gated_ffn")
+    ws = _scratch(need.value, x, stream) if workspace is None else workspace
+    a.workspace, a.workspace_bytes = _ptr(ws), ws.numel() * ws.element_size()
+    _check(lib.rope3d_gated_ffn(ctypes.byref(a), _stream(stream, x)), "rope3d_gated_ffn")
+    return y if gate_pre is None else (y, gate_pre, up_pre)
+
+
+def rope3d_gated_ffn_backward(dy, x, w_gate, w_up, w_down, gate_pre=None, up_pre=None,
+                              act: int = ACT_GELU_TANH, dx=None, dw_gate=None, dw_up=None, dw_down=None,
+                              need=(True, True, True), workspace=None, stream=None):
+    """The gradients of rope3d_gated_ffn: (dx, dw_gate, dw_up, dw_down). gate_pre
+    and up_pre as the forward pass kept them; None computes them again. need: which
+    of dx, (dw_gate, dw_up) and dw_down to compute; the others are None."""
+    import torch
+
+    if need[0] and dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if need[1]:
+        dw_gate = torch.empty(w_gate.shape, dtype=x.dtype, device=x.device) if dw_gate is None else dw_gate
+        dw_up = torch.empty(w_up.shape, dtype=x.dtype, device=x.device) if dw_up is None else dw_up
+    if need[2] and dw_down is None:
+        dw_down = torch.empty(w_down.shape, dtype=x.dtype, device=x.device)
+    dx, dw_gate, dw_up, dw_down = (t if n else None for t, n in
+                                   ((dx, need[0]), (dw_gate, need[1]), (dw_up, need[1]), (dw_down, need[2])))
+    f = _ffn_args(x, w_gate, w_up, w_down, x, gate_pre, up_pre, act)
+    M, D, F = f.tokens, f.width, f.hidden
+    ld = lambda name, t, r, c: 0 if t is None else _matrix(name, t, r, c, x.dtype)[2]  # noqa: E731
+    a = _FfnBackArgs(dy=_ptr(dy), x=f.x, w_gate=f.w_gate, w_up=f.w_up, w_down=f.w_down, gate_pre=f.gate_pre,
+                     up_pre=f.up_pre, dx=_ptr(dx), dw_gate=_ptr(dw_gate), dw_up=_ptr(dw_up),
+                     dw_down=_ptr(dw_down), tokens=M, width=D, hidden=F, dy_stride=ld("dy", dy, M, D),
+                     x_stride=f.x_stride, w_gate_stride=f.w_gate_stride, w_up_stride=f.w_up_stride,
+                     w_down_stride=f.w_down_stride, pre_stride=f.pre_stride, dx_stride=ld("dx", dx, M, D),
+                     dw_gate_stride=ld("dw_gate", dw_gate, F, D), dw_up_stride=ld("dw_up", dw_up, F, D),
+                     dw_down_stride=ld("dw_down", dw_down, D, F), dtype=f.dtype, pre_dtype=f.pre_dtype, act=f.act)
+    lib = load_library()
+    nb = ctypes.c_int64()
+    _check(lib.rope3d_gated_ffn_backward_workspace(ctypes.byref(a), ctypes.byref(nb)), "rope3d_gated_ffn_backward")
+    ws = _scratch(nb.value, x, stream) if workspace is None else workspace
+    a.workspace, a.workspace_bytes = _ptr(ws), ws.numel() * ws.element_size()
+    _check(lib.rope3d_gated_ffn_backward(ctypes.byref(a), _stream(stream, x)), "rope3d_gated_ffn_backward")
+    return dx, dw_gate, dw_up, dw_down
+
+
+def rope3d_gated_ffn_check(check_device: bool = False, **fields) -> str:
+    """Status name of rope3d_gated_ffn's checks for the given argument fields
+    (pointers may be plain integers)."""
+    return STATUS[load_library().rope3d_gated_ffn_check(ctypes.byref(_FfnArgs(**fields)), int(check_device))]
+
+
+def rope3d_gated_ffn_backward_check(check_device: bool = False, **fields) -> str:
+    """Status name of rope3d_gated_ffn_backward's checks."""
+    return STATUS[load_library().rope3d_gated_ffn_backward_check(ctypes.byref(_FfnBackArgs(**fields)),
+                                                                 int(check_device))]
+
+
+def rope3d_gated_ffn_last_kernel() -> int:
+    """Kernel of this thread's last feed-forward: 1 tiles, 2 streamed weights (few tokens)."""
+    return int(load_library().rope3d_gated_ffn_last_kernel())
+
+
+def rope3d_testing_ffn_wait_timeouts(reset: bool = True) -> int:
+    """Bounded waits of the feed-forward's kernels that ran out (0 in a sound run)."""
+    n = ctypes.c_int64()
+    _check(load_library().rope3d_testing_ffn_wait_timeouts(ctypes.byref(n), 1 if reset else 0),
+           "rope3d_testing_ffn_wait_timeouts")
+    return int(n.value)
 
 
 def rope3d_preflight(q, k, q_out, k_out, tables, B, T, H, W, heads, head_dim, split, dtype,

@@ -1,0 +1,1277 @@
+// rope3d_ffn.cu -- the gated feed-forward of a transformer block and its
+// backward pass: rope3d_gated_ffn, rope3d_gated_ffn_backward.
+//
+//   g = x Wg^T, u = x Wu^T, h = act(g) * u, y = h Wd^T
+// with x [tokens, width], Wg and Wu [hidden, width], Wd [width, hidden]; and,
+// for a gradient dy of y,
+//   dh = dy Wd, dg = dh * u * act'(g), du = dh * act(g),
+//   dx = dg Wg + du Wu, dWg = dg^T x, dWu = du^T x, dWd = dy^T h.
+//
+// Every product is one of three forms of C[i, j] = sum_k A(i, k) B(j, k):
+//   x Wg^T | x Wu^T and h Wd^T     both operands K-major (rows along k)
+//   dy Wd, dg Wg + du Wu           A K-major, B MN-major (rows across k)
+//   dg^T x, du^T x, dy^T h         both MN-major
+// which the fifth-generation tensor cores read as they lie in memory, so no
+// matrix is ever transposed. Two kernels compute them:
+//   ffn_tile_kernel    pairs of CTAs, 256-row tiles (many tokens; the weights'
+//                      gradients always): bound by the tensor cores
+//   ffn_stream_kernel  few tokens: a tile is 128 weight rows by all the tokens,
+//                      its k range split over a cluster: bound by reading the
+//                      weights from memory
+// Products accumulate in fp32 in tensor memory; g and u reach the activation
+// there without a rounding. The roundings to 16 bits are the operands of the
+// next product (h, dg, du: the tensor cores take 16-bit operands) and the
+// outputs.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/rope3d.h"
+#include "rope3d_internal.h"
+#include "rope3d_tc.cuh"
+
+namespace {
+
+using namespace rope3d_tc;
+
+// Bounded waits that ran out (rope3d_testing_ffn_wait_timeouts).
+__device__ unsigned int g_ffn_wait_timeouts;
+
+// ---- the element-wise part ---------------------------------------------------
+
+__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
+
+// act(g) and, where kGrad, act'(g). GELU's tanh form is g * sigmoid(2 z) with
+// z = sqrt(2 / pi) (g + 0.044715 g^3), from 1 + tanh(z) = 2 sigmoid(2 z); past
+// |g| = 50 the sigmoid is 0 or 1 and its slope 0 in fp32, and the clamp keeps
+// g^3 finite.
+template <bool kGrad>
+__device__ __forceinline__ float activation(float g, int act, float *grad) {
+    if (act == ROPE3D_ACT_SILU) {
+        const float q = sigmoid(g);
+        if constexpr (kGrad) *grad = q * (1.0f + g * (1.0f - q));
+        return g * q;
+    }
+    if (act == ROPE3D_ACT_GELU_TANH) {
+        const float c = fminf(fmaxf(g, -50.0f), 50.0f);
+        const float s = c * c;
+        const float q = sigmoid(c * (1.5957691216f + 0.0713548163f * s));
+        if constexpr (kGrad) *grad = q + g * (q * (1.0f - q) * (1.5957691216f + 0.2140644488f * s));
+        return g * q;
+    }
+    const float cdf = 0.5f * (1.0f + erff(g * 0.7071067812f));
+    if constexpr (kGrad) *grad = cdf + g * (0.3989422804f * __expf(-0.5f * g * g));
+    return g * cdf;
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b, bool f16) {
+    uint32_t w;
+    if (f16) {
+        const __half2 h = __floats2half2_rn(a, b);
+        memcpy(&w, &h, 4);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        memcpy(&w, &h, 4);
+    }
+    return w;
+}
+
+__device__ __forceinline__ float2 unpack2(uint32_t w, bool f16) {
+    if (f16) {
+        __half2 h;
+        memcpy(&h, &w, 4);
+        return __half22float2(h);
+    }
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+__device__ __forceinline__ uint16_t pack1(float a, bool f16) {
+    return f16 ? __half_as_ushort(__float2half_rn(a)) : __bfloat16_as_ushort(__float2bfloat16_rn(a));
+}
+
+__device__ __forceinline__ float unpack1(uint16_t v, bool f16) {
+    return f16 ? __half2float(__ushort_as_half(v)) : __uint_as_float(uint32_t(v) << 16);
+}
+
+// ---- launch description ---------------------------------------------------------
+
+enum Epi { kPlain = 0, kGated = 1, kBack = 2 };
+// operand layouts: K-major (0) or MN-major (1)
+constexpr int kKK = 0, kKM = 1, kMM = 2;
+
+// A matrix written by an epilogue: rows of 16-bit or fp32 elements.
+struct Out {
+    void *p;          // null: not written
+    long long ld;     // elements from row to row
+    int f32;
+    int tma;          // rows are 16-byte multiples: stored through the tensor map
+};
+
+struct Maps {
+    CUtensorMap a[2], b[2];   // operands of segments 0 and 1 (gated: b = Wg, Wu)
+    CUtensorMap c[3];         // outputs
+};
+
+struct Params {
+    int m, n;                 // output rows and columns (of one half where gated)
+    int nk0, nk1;             // 64-wide k blocks of the two segments
+    int tiles_m, tiles_n, batch;
+    int f16, act;
+    Out out[3];               // plain: one a batch; gated: h, g, u; back: dg, du, h
+    const void *g, *u;        // back: the kept projections
+    long long ldp;
+    int pre_f32, pre_vec;     // they are fp32; their rows are 16-byte multiples
+    int rows_n, stages;       // stream kernel: MMA N, ring slots
+};
+
+// 16 consecutive elements of a kept projection, zeros past its end.
+__device__ __forceinline__ void load_pre16(float *v, const void *base, long long off, int valid,
+                                           const Params &p) {
+    if (p.pre_vec && valid >= 16) {
+        if (p.pre_f32) {
+            const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + off);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 t = s[i];
+                v[4 * i] = t.x; v[4 * i + 1] = t.y; v[4 * i + 2] = t.z; v[4 * i + 3] = t.w;
+            }
+        } else {
+            const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + off);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint4 t = s[i];
+                const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = unpack2(w[j], p.f16);
+                    v[8 * i + 2 * j] = f.x;
+                    v[8 * i + 2 * j + 1] = f.y;
+                }
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        v[i] = 0.0f;
+        if (i < valid)
+            v[i] = p.pre_f32 ? static_cast<const float *>(base)[off + i]
+                             : unpack1(static_cast<const uint16_t *>(base)[off + i], p.f16);
+    }
+}
+
+// ---- many tokens: 256-row tiles of CTA pairs -------------------------------------
+//
+// A pair of CTAs (one cluster) computes 256 x kBN of C with cta_group::2 MMAs:
+// each CTA holds 128 rows of A and kBN / 2 rows of B in shared memory, and the
+// accumulators of its own 128 rows, kBN fp32 columns, in tensor memory. Both
+// CTAs read both halves of B through the pair, so a stage costs each SM 16 KB
+// of A and kBN / 2 * 128 B of B for 256 x kBN x 64 products of the pair.
+// Gated: B's two halves are kBN / 2 rows of Wg and the same rows of Wu, so one
+// thread finds g and u of an element in its own lane and no extra pass runs.
+//
+// Roles (384 threads): warp 0 TMA producer, warp 1 MMA issuer (of the pair's
+// first CTA), warp 2 tensor memory, warps 4-11 the epilogue: warp w reads
+// tensor memory lanes 32 (w % 4) + lane, half of the columns. Accumulators are
+// double-buffered, so the epilogue of a tile runs under the next tile's MMAs.
+// Persistent: cluster c computes tiles c, c + clusters, ... in an order that
+// walks groups of 8 tile rows, so that the tiles in flight share operands in L2.
+//
+// Epilogue stores go through 2 KB staging boxes (32 rows x 64 bytes, the
+// 64-byte swizzle keeps the writes free of bank conflicts) and TMA, four boxes
+// in flight a warp; rows that TMA cannot address are stored element by element.
+constexpr int kThreads = 384;
+constexpr int kEpiWarps = 8;
+constexpr int kStages = 5;
+constexpr int kABytes = 128 * 128;              // 128 rows x 64 elements
+constexpr int kBoxBytes = 2048, kBoxes = 4;     // staging of one warp
+constexpr int kGroupRows = 8;                   // tile rows of a raster group
+
+template <int kBN>
+constexpr int tile_smem() {
+    return kStages * (kABytes + kBN / 2 * 128) + kEpiWarps * kBoxes * kBoxBytes + 256 + 1024;
+}
+
+struct Tile {
+    int z, m0, n0;   // batch, first row and first column, in tiles
+};
+
+__device__ __forceinline__ Tile tile_at(const Params &p, int t) {
+    const int per = p.tiles_m * p.tiles_n;
+    Tile x;
+    x.z = t / per;
+    t -= x.z * per;
+    const int group = t / (kGroupRows * p.tiles_n);
+    const int first = group * kGroupRows;
+    const int rows = min(kGroupRows, p.tiles_m - first);
+    t -= first * p.tiles_n;
+    x.m0 = first + t % rows;
+    x.n0 = t / rows;
+    return x;
+}
+
+// Epilogue stores of one warp.
+struct Boxes {
+    uint32_t base;   // shared-memory address of the warp's boxes
+    int next;
+    int lane;
+};
+
+// 16 words (64 bytes: 32 16-bit or 16 fp32 elements) of each lane's row, from
+// column `col` of output o; the warp's rows are row0 .. row0 + 31.
+__device__ __forceinline__ void store_words(Boxes &bx, const uint32_t *w, const Out &o,
+                                            const CUtensorMap *map, int row0, int col, int m, int n) {
+    if (!o.p || row0 >= m || col >= n) return;
+    if (o.tma) {
+        const uint32_t box = bx.base + uint32_t(bx.next & (kBoxes - 1)) * kBoxBytes;
+        ++bx.next;
+        if (bx.lane == 0) bulk_wait_read<kBoxes - 1>();
+        __syncwarp();
+        const uint32_t row = box + uint32_t(bx.lane) * 64, sw = (uint32_t(bx.lane) >> 1) & 3;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                         ::"r"(row + ((uint32_t(c) ^ sw) << 4)), "r"(w[4 * c]), "r"(w[4 * c + 1]),
+                           "r"(w[4 * c + 2]), "r"(w[4 * c + 3]) : "memory");
+        fence_async_smem();
+        __syncwarp();
+        if (bx.lane == 0) {
+            tma_store2(map, box, col, row0);
+            bulk_commit();
+        }
+        return;
+    }
+    const int row = row0 + bx.lane;
+    if (row >= m) return;
+    if (o.f32) {
+        float *d = static_cast<float *>(o.p) + row * o.ld + col;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (col + i < n) d[i] = __uint_as_float(w[i]);
+    } else {
+        uint16_t *d = static_cast<uint16_t *>(o.p) + row * o.ld + col;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (col + 2 * i < n) d[2 * i] = uint16_t(w[i]);
+            if (col + 2 * i + 1 < n) d[2 * i + 1] = uint16_t(w[i] >> 16);
+        }
+    }
+}
+
+// A kept projection, 32 columns of each lane's row, in its own type.
+__device__ __forceinline__ void store_pre32(Boxes &bx, const float *v, const Out &o,
+                                            const CUtensorMap *map, int row0, int col,
+                                            const Params &p) {
+    if (!o.p) return;
+    uint32_t w[16];
+    if (o.f32) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[16 * h + i]);
+            store_words(bx, w, o, map, row0, col + 16 * h, p.m, p.n);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1], p.f16);
+        store_words(bx, w, o, map, row0, col, p.m, p.n);
+    }
+}
+
+template <int kBN, int kLayout, int kEpi>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+ffn_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
+    constexpr bool kAMn = kLayout == kMM, kBMn = kLayout != kKK;
+    constexpr int kBRows = kBN / 2;                       // rows of B in this CTA
+    constexpr uint32_t kBBytes = kBRows * 128;
+    constexpr uint32_t kStageBytes = kABytes + kBBytes;
+    extern __shared__ uint8_t raw[];
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    const uint32_t boxes = base + kStages * kStageBytes;
+    const uint32_t bars = boxes + kEpiWarps * kBoxes * kBoxBytes;
+    auto full = [&](int s) { return bars + 8u * uint32_t(s); };
+    auto empty = [&](int s) { return bars + 8u * uint32_t(kStages + s); };
+    auto acc_full = [&](int b) { return bars + 8u * uint32_t(2 * kStages + b); };
+    auto acc_empty = [&](int b) { return bars + 8u * uint32_t(2 * kStages + 2 + b); };
+    const uint32_t slot = bars + 8u * (2 * kStages + 4);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_rank();
+    const int nk = p.nk0 + p.nk1;
+    const int tiles = p.tiles_m * p.tiles_n * p.batch;
+    const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(acc_full(b), 1);
+            mbar_init(acc_empty(b), 2 * kEpiWarps);
+        }
+        mbar_fence_init();
+        prefetch_map(&maps.a[0]);
+        prefetch_map(&maps.b[0]);
+    }
+    if (warp == 2) tmem_alloc<true>(slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // both CTAs' barriers exist before any copy or commit names them
+    tc_fence_after();
+    uint32_t tmem;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(slot) : "memory");
+    // results of earlier kernels are visible from here; only then may a later
+    // kernel start (so that what runs beside this one has all older writes)
+    grid_wait();
+    grid_release();
+    bool dead = false;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int it = 0;
+            for (int t = first; t < tiles && !dead; t += step) {
+                const Tile x = tile_at(p, t);
+                const int m0 = x.m0 * 256 + int(rank) * 128;
+                // gated: this CTA's rows are of Wg (rank 0) or Wu (rank 1)
+                const int n0 = kEpi == kGated ? x.n0 * kBRows : x.n0 * kBN + int(rank) * kBRows;
+                for (int kb = 0; kb < nk; ++kb, ++it) {
+                    const int s = it % kStages;
+                    const uint32_t use = uint32_t(it / kStages);
+                    if (it >= kStages && !mbar_wait(empty(s), (use - 1) & 1u, dead, &g_ffn_wait_timeouts)) break;
+                    const int seg = kb >= p.nk0;
+                    const int k = (seg ? kb - p.nk0 : kb) * 64;
+                    const CUtensorMap *ma = &maps.a[kLayout == kMM ? x.z : seg];
+                    const CUtensorMap *mb = &maps.b[kEpi == kGated ? int(rank) : kLayout == kMM ? x.z : seg];
+                    const uint32_t sa = base + uint32_t(s) * kStageBytes, sb = sa + kABytes;
+                    // the pair's copies complete on the first CTA's barrier
+                    const uint32_t bar = map_rank(full(s), 0);
+                    if (rank == 0) mbar_expect_tx(full(s), 2 * kStageBytes);
+                    if constexpr (kAMn) {
+                        tma_load2<true>(sa, ma, m0, k, bar);
+                        tma_load2<true>(sa + 8192, ma, m0 + 64, k, bar);
+                    } else {
+                        tma_load2<true>(sa, ma, k, m0, bar);
+                    }
+                    if constexpr (kBMn) {
+#pragma unroll
+                        for (int j = 0; j < kBRows / 64; ++j)
+                            tma_load2<true>(sb + 8192 * j, mb, n0 + 64 * j, k, bar);
+                    } else {
+                        tma_load2<true>(sb, mb, k, n0, bar);
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (rank == 0 && lane == 0) {
+            const uint32_t id = idesc(256, kBN, !p.f16, kAMn, kBMn);
+            int it = 0, i = 0;
+            for (int t = first; t < tiles && !dead; t += step, ++i) {
+                const int b = i & 1;
+                if (i >= 2 && !mbar_wait(acc_empty(b), uint32_t(i / 2 - 1) & 1u, dead, &g_ffn_wait_timeouts)) break;
+                tc_fence_after();
+                const uint32_t d = tmem + uint32_t(b) * 256;
+                for (int kb = 0; kb < nk; ++kb, ++it) {
+                    const int s = it % kStages;
+                    if (!mbar_wait(full(s), uint32_t(it / kStages) & 1u, dead, &g_ffn_wait_timeouts)) break;
+                    tc_fence_after();
+                    const uint32_t sa = base + uint32_t(s) * kStageBytes, sb = sa + kABytes;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        // 16 elements of k: 32 bytes of a K-major row, 16 rows of an MN-major tile
+                        const uint64_t da = kAMn ? sdesc(sa + j * 2048, 8192, 1024) : sdesc(sa + j * 32, 16, 1024);
+                        const uint64_t db = kBMn ? sdesc(sb + j * 2048, 8192, 1024) : sdesc(sb + j * 32, 16, 1024);
+                        mma<true>(d, da, db, id, (kb | j) != 0);
+                    }
+                    commit_pair(empty(s));
+                }
+                commit_pair(acc_full(b));
+            }
+        }
+    } else if (warp >= 4) {
+        const int quad = warp & 3, half = (warp - 4) >> 2;
+        Boxes bx{boxes + uint32_t(warp - 4) * kBoxes * kBoxBytes, 0, lane};
+        int i = 0;
+        for (int t = first; t < tiles && !dead; t += step, ++i) {
+            const Tile x = tile_at(p, t);
+            const int b = i & 1;
+            const int row0 = x.m0 * 256 + int(rank) * 128 + quad * 32;
+            const int row = row0 + lane;
+            const uint32_t d = tmem + uint32_t(b) * 256 + (uint32_t(quad) << 21);
+            const bool row_ok = row < p.m;
+            if (!mbar_wait(acc_full(b), uint32_t(i / 2) & 1u, dead, &g_ffn_wait_timeouts)) break;
+            tc_fence_after();
+            constexpr int kCols = kEpi == kGated ? kBRows / 2 : kBN / 2;   // columns of this warp
+            const int c0 = half * kCols;
+            const int n0 = x.n0 * (kEpi == kGated ? kBRows : kBN) + c0;
+#pragma unroll 1
+            for (int c = 0; c < kCols; c += 32) {
+                const int col = n0 + c;
+                float v[32];
+                tmem_ld16(v, d + uint32_t(c0 + c));
+                tmem_ld16(v + 16, d + uint32_t(c0 + c + 16));
+                if constexpr (kEpi == kGated) {
+                    float u[32];
+                    tmem_ld16(u, d + uint32_t(kBRows + c0 + c));
+                    tmem_ld16(u + 16, d + uint32_t(kBRows + c0 + c + 16));
+                    tmem_wait();
+                    tmem_tie16(v);
+                    tmem_tie16(v + 16);
+                    tmem_tie16(u);
+                    tmem_tie16(u + 16);
+                    store_pre32(bx, v, p.out[1], &maps.c[1], row0, col, p);
+                    store_pre32(bx, u, p.out[2], &maps.c[2], row0, col, p);
+                    if (p.out[0].p) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float h0 = activation<false>(v[2 * e], p.act, nullptr) * u[2 * e];
+                            const float h1 = activation<false>(v[2 * e + 1], p.act, nullptr) * u[2 * e + 1];
+                            w[e] = pack2(h0, h1, p.f16);
+                        }
+                        store_words(bx, w, p.out[0], &maps.c[0], row0, col, p.m, p.n);
+                    }
+                } else if constexpr (kEpi == kBack) {
+                    uint32_t wg[16], wu[16], wh[16];
+                    tmem_wait();
+                    tmem_tie16(v);
+                    tmem_tie16(v + 16);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        float g[16], u[16];
+                        const int valid = row_ok ? p.n - (col + 16 * q) : 0;
+                        const long long off = row * p.ldp + col + 16 * q;
+                        load_pre16(g, p.g, off, valid, p);
+                        load_pre16(u, p.u, off, valid, p);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            float dg[2], du[2], hh[2];
+#pragma unroll
+                            for (int o = 0; o < 2; ++o) {
+                                const float dh = v[16 * q + 2 * e + o];
+                                float slope;
+                                const float a = activation<true>(g[2 * e + o], p.act, &slope);
+                                dg[o] = dh * u[2 * e + o] * slope;
+                                du[o] = dh * a;
+                                hh[o] = a * u[2 * e + o];
+                            }
+                            wg[8 * q + e] = pack2(dg[0], dg[1], p.f16);
+                            wu[8 * q + e] = pack2(du[0], du[1], p.f16);
+                            wh[8 * q + e] = pack2(hh[0], hh[1], p.f16);
+                        }
+                    }
+                    store_words(bx, wg, p.out[0], &maps.c[0], row0, col, p.m, p.n);
+                    store_words(bx, wu, p.out[1], &maps.c[1], row0, col, p.m, p.n);
+                    store_words(bx, wh, p.out[2], &maps.c[2], row0, col, p.m, p.n);
+                } else {
+                    tmem_wait();
+                    tmem_tie16(v);
+                    tmem_tie16(v + 16);
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) w[e] = pack2(v[2 * e], v[2 * e + 1], p.f16);
+                    const int z = kLayout == kMM ? x.z : 0;
+                    store_words(bx, w, p.out[z], &maps.c[z], row0, col, p.m, p.n);
+                }
+            }
+            // this warp's reads of the accumulators are done
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_rank(acc_empty(b), 0));
+        }
+        if (lane == 0) bulk_wait_all();
+    }
+    // neither CTA leaves while the other may still name its shared memory,
+    // barriers or tensor memory
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == 2) tmem_free<true>(tmem, 512);
+}
+
+// ---- few tokens: weights streamed once ---------------------------------------------
+//
+// With few tokens the weights' bytes bound every product, so a tile is turned
+// over: 128 weight rows are the MMA's M and all the tokens (rounded up to 16)
+// its N. A cluster of CTAs splits the k range of a tile, so that enough CTAs
+// read at once also where the tiles are few; each leaves its fp32 partial sums
+// in shared memory and the cluster adds them in rank order (always the same
+// order) through distributed shared memory, with the activation on the way out.
+// Warp 0: TMA, warp 1: MMAs, all four warps: the epilogue.
+// The second product of a forward pass starts its weight copies while the first
+// still runs, and waits for h alone.
+constexpr int kStreamThreads = 128;
+constexpr int kStreamTokens = 128;   // most tokens of this kernel
+constexpr int kMaxSplit = 8;
+
+template <bool kAMn, int kEpi>
+__global__ void __launch_bounds__(kStreamThreads)
+ffn_stream_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
+    constexpr int kAcc = kEpi == kGated ? 2 : 1;
+    extern __shared__ uint8_t raw[];
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    const uint32_t stage_bytes = kAcc * kABytes + uint32_t(p.rows_n) * 128;
+    const uint32_t bars = base + uint32_t(p.stages) * stage_bytes;
+    auto full = [&](int s) { return bars + 16u * uint32_t(s); };
+    auto empty = [&](int s) { return bars + 16u * uint32_t(s) + 8u; };
+    const uint32_t done = bars + 16u * uint32_t(p.stages), slot = done + 8;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_rank();
+    uint32_t split;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(split));
+    const int tile = blockIdx.x / split;
+    const int f0 = tile * 128;
+    const int nk = p.nk0 + p.nk1;
+    const int k_lo = int(int64_t(nk) * rank / split), k_hi = int(int64_t(nk) * (rank + 1) / split);
+    uint32_t cols = 32;
+    while (cols < uint32_t(kAcc * p.rows_n)) cols *= 2;
+
+    if (tid == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        mbar_init(done, 1);
+        mbar_fence_init();
+    }
+    if (warp == 2) tmem_alloc<false>(slot, cols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    uint32_t tmem;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(slot) : "memory");
+    bool dead = false;
+
+    auto load_weights = [&](int kb, int s) {
+        const int seg = kb >= p.nk0;
+        const int k = (seg ? kb - p.nk0 : kb) * 64;
+        const uint32_t sa = base + uint32_t(s) * stage_bytes;
+        mbar_expect_tx(full(s), stage_bytes);
+#pragma unroll
+        for (int a = 0; a < kAcc; ++a) {
+            const CUtensorMap *ma = &maps.a[kEpi == kGated ? a : seg];
+            if constexpr (kAMn) {
+                tma_load2<false>(sa + a * kABytes, ma, f0, k, full(s));
+                tma_load2<false>(sa + a * kABytes + 8192, ma, f0 + 64, k, full(s));
+            } else {
+                tma_load2<false>(sa + a * kABytes, ma, k, f0, full(s));
+            }
+        }
+    };
+    auto load_tokens = [&](int kb, int s) {
+        const int seg = kb >= p.nk0;
+        const int k = (seg ? kb - p.nk0 : kb) * 64;
+        tma_load2<false>(base + uint32_t(s) * stage_bytes + kAcc * kABytes, &maps.b[seg], k, 0, full(s));
+    };
+
+    if (warp == 0 && lane == 0) {
+        const int n = k_hi - k_lo, ahead = min(n, p.stages);
+        // the plain product's weights are no earlier kernel's output that may
+        // still be in flight: the kernel before it waited for all older ones
+        if constexpr (kEpi == kPlain && !kAMn) {
+            for (int i = 0; i < ahead; ++i) load_weights(k_lo + i, i);
+            grid_wait();
+            for (int i = 0; i < ahead; ++i) load_tokens(k_lo + i, i);
+        } else {
+            grid_wait();
+            for (int i = 0; i < ahead; ++i) {
+                load_weights(k_lo + i, i);
+                load_tokens(k_lo + i, i);
+            }
+        }
+        for (int i = ahead; i < n; ++i) {
+            const int s = i % p.stages;
+            if (!mbar_wait(empty(s), uint32_t(i / p.stages - 1) & 1u, dead, &g_ffn_wait_timeouts)) break;
+            load_weights(k_lo + i, s);
+            load_tokens(k_lo + i, s);
+        }
+    } else if (warp == 1 && lane == 0) {
+        const uint32_t id = idesc(128, uint32_t(p.rows_n), !p.f16, kAMn, false);
+        for (int i = 0; i < k_hi - k_lo; ++i) {
+            const int s = i % p.stages;
+            if (!mbar_wait(full(s), uint32_t(i / p.stages) & 1u, dead, &g_ffn_wait_timeouts)) break;
+            tc_fence_after();
+            const uint32_t sa = base + uint32_t(s) * stage_bytes, sb = sa + kAcc * kABytes;
+#pragma unroll
+            for (int a = 0; a < kAcc; ++a)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t w = sa + a * kABytes;
+                    mma<false>(tmem + uint32_t(a * p.rows_n),
+                               kAMn ? sdesc(w + j * 2048, 8192, 1024) : sdesc(w + j * 32, 16, 1024),
+                               sdesc(sb + j * 32, 16, 1024), id, (i | j) != 0);
+                }
+            commit(empty(s));
+        }
+        commit(done);
+    }
+    if (warp >= 2) {
+        // results of earlier kernels are visible from here; only then may a
+        // later kernel start (so that what runs beside this one has all older
+        // writes, and the one after may copy its weights early)
+        grid_wait();
+        grid_release();
+    }
+    __syncwarp();
+    grid_wait();      // every thread: outputs of earlier kernels are read and overwritten below
+    // all copies have landed and been read (each was waited for by its MMAs):
+    // the ring's memory takes the partial sums, [accumulator][token][128 rows]
+    mbar_wait(done, 0, dead, &g_ffn_wait_timeouts);
+    tc_fence_after();
+    const int row = warp * 32 + lane;
+    for (int c = 0; c < kAcc * p.rows_n; c += 16) {
+        float v[16];
+        tmem_ld16(v, tmem + (uint32_t(warp) << 21) + uint32_t(c));
+        tmem_wait();
+        tmem_tie16(v);
+        const bool any = k_hi > k_lo;   // an empty k range has no MMA: its tensor memory is not defined
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + uint32_t((c + i) * 128 + row) * 4),
+                         "f"(any ? v[i] : 0.0f) : "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    // 32 rows of one token at a time, shared out over the cluster's warps
+    for (int unit = int(rank) * 4 + warp; unit < p.n * 4; unit += int(split) * 4) {
+        const int tok = unit >> 2, f = (unit & 3) * 32 + lane;
+        float acc[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int a = 0; a < kAcc; ++a) {
+            const uint32_t at = base + uint32_t((a * p.rows_n + tok) * 128 + f) * 4;
+            float part[kMaxSplit];
+#pragma unroll
+            for (int r = 0; r < kMaxSplit; ++r)
+                part[r] = r < int(split) ? ld_cluster_f32(map_rank(at, uint32_t(r))) : 0.0f;
+#pragma unroll
+            for (int r = 0; r < kMaxSplit; ++r) acc[a] += part[r];
+        }
+        const int col = f0 + f;
+        if (col >= p.m) continue;
+        auto put = [&](const Out &o, float v) {
+            if (!o.p) return;
+            const long long at = tok * o.ld + col;
+            if (o.f32) static_cast<float *>(o.p)[at] = v;
+            else static_cast<uint16_t *>(o.p)[at] = pack1(v, p.f16);
+        };
+        if constexpr (kEpi == kGated) {
+            put(p.out[1], acc[0]);
+            put(p.out[2], acc[1]);
+            put(p.out[0], activation<false>(acc[0], p.act, nullptr) * acc[1]);
+        } else if constexpr (kEpi == kBack) {
+            const long long at = tok * p.ldp + col;
+            const float g = p.pre_f32 ? static_cast<const float *>(p.g)[at]
+                                      : unpack1(static_cast<const uint16_t *>(p.g)[at], p.f16);
+            const float u = p.pre_f32 ? static_cast<const float *>(p.u)[at]
+                                      : unpack1(static_cast<const uint16_t *>(p.u)[at], p.f16);
+            float slope;
+            const float a = activation<true>(g, p.act, &slope);
+            put(p.out[0], acc[0] * u * slope);
+            put(p.out[1], acc[0] * a);
+            put(p.out[2], a * u);
+        } else {
+            put(p.out[0], acc[0]);
+        }
+    }
+    cluster_sync();   // partial sums stay until every CTA of the cluster has read them
+    if (warp == 2) tmem_free<false>(tmem, cols);
+}
+
+// ---- rows that TMA cannot address ----------------------------------------------------
+
+// 16-bit rows copied to rows that start on 16-byte boundaries (dst_ld a
+// multiple of 8). One block a row segment; consecutive threads, consecutive
+// elements.
+__global__ void __launch_bounds__(256)
+ffn_align_kernel(const uint16_t *src, long long src_ld, uint16_t *dst, long long dst_ld, int cols,
+                 long long rows) {
+    grid_wait();
+    grid_release();
+    for (long long r = blockIdx.y; r < rows; r += gridDim.y)
+        for (int c = blockIdx.x * 2048 + threadIdx.x, i = 0; i < 8 && c < cols; ++i, c += 256)
+            dst[r * dst_ld + c] = src[r * src_ld + c];
+}
+
+// ---- host ---------------------------------------------------------------------------
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_tiled() {
+    static const EncodeTiledFn fn = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                             &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            return EncodeTiledFn(nullptr);
+        }
+        return reinterpret_cast<EncodeTiledFn>(ptr);
+    }();
+    return fn;
+}
+
+// A row-major matrix of 16-bit elements in device memory.
+struct Mat {
+    const void *p;
+    int64_t rows, cols, ld;
+};
+
+bool tma_ok(const void *p, int64_t ld, int elem_bytes) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * elem_bytes % 16 == 0;
+}
+
+bool make_map(CUtensorMap *map, const void *p, int64_t rows, int64_t cols, int64_t ld, int elem_bytes,
+              bool f16, int box_cols, int box_rows, bool swizzle128) {
+    const EncodeTiledFn fn = encode_tiled();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(ld) * cuuint64_t(elem_bytes)};
+    const cuuint32_t box[2] = {cuuint32_t(box_cols), cuuint32_t(box_rows)};
+    const cuuint32_t elem[2] = {1, 1};
+    const CUtensorMapDataType type = elem_bytes == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : f16           ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                     : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    return fn(map, type, 2, const_cast<void *>(p), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// An operand's map: boxes of 64 along the contiguous axis. K-major: `rows`
+// rows of a tile; MN-major: 64 rows (of k).
+bool operand_map(CUtensorMap *map, const Mat &x, bool mn, int rows, bool f16) {
+    return make_map(map, x.p, x.rows, x.cols, x.ld, 2, f16, 64, mn ? 64 : rows, true);
+}
+
+// The outputs [rows, cols]; `maps_too`: with tensor maps for the tile kernel's
+// stores (the stream kernel stores element by element).
+int set_outs(Params &p, Maps &maps, const Out *outs, int count, int64_t rows, int64_t cols, bool maps_too) {
+    for (int i = 0; i < count; ++i) {
+        p.out[i] = outs[i];
+        Out &o = p.out[i];
+        const int es = o.f32 ? 4 : 2;
+        o.tma = maps_too && o.p && tma_ok(o.p, o.ld, es);
+        if (o.tma && !make_map(&maps.c[i], o.p, rows, cols, o.ld, es, p.f16, o.f32 ? 16 : 32, 32, false))
+            return ROPE3D_ERR_CUDA;
+    }
+    return ROPE3D_OK;
+}
+
+// How many pairs of CTAs the device holds at once (asked once a device).
+template <int kBN, int kLayout, int kEpi>
+bool tile_ready(int *clusters) {
+    static std::atomic<int> known[64];   // per device, 0 = not asked yet
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    int c = known[dev].load(std::memory_order_acquire);
+    if (c == 0) {
+        auto *fn = ffn_tile_kernel<kBN, kLayout, kEpi>;
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, tile_smem<kBN>()) != cudaSuccess) {
+            cudaGetLastError();
+            return false;
+        }
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = tile_smem<kBN>();
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 2;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&c, fn, &cfg) != cudaSuccess || c < 1) {
+            cudaGetLastError();
+            return false;
+        }
+        known[dev].store(c, std::memory_order_release);
+    }
+    *clusters = c;
+    return true;
+}
+
+template <int kBN, int kLayout, int kEpi>
+int launch_tile_as(Params &p, Maps &maps, const Mat *a, const Mat *b, int segs, cudaStream_t st) {
+    int clusters = 0;
+    if (!tile_ready<kBN, kLayout, kEpi>(&clusters)) return ROPE3D_ERR_CUDA;
+    constexpr bool kAMn = kLayout == kMM, kBMn = kLayout != kKK;
+    const int nb = kEpi == kGated ? 2 : segs;
+    for (int i = 0; i < segs; ++i)
+        if (!operand_map(&maps.a[i], a[i], kAMn, 128, p.f16)) return ROPE3D_ERR_CUDA;
+    for (int i = 0; i < nb; ++i)
+        if (!operand_map(&maps.b[i], b[i], kBMn, kBN / 2, p.f16)) return ROPE3D_ERR_CUDA;
+    const int64_t tn = kEpi == kGated ? kBN / 2 : kBN;
+    const int64_t tiles_m = (int64_t(p.m) + 255) / 256, tiles_n = (int64_t(p.n) + tn - 1) / tn;
+    if (tiles_m * tiles_n * p.batch > (int64_t(1) << 30)) return ROPE3D_ERR_SHAPE;
+    p.tiles_m = int(tiles_m);
+    p.tiles_n = int(tiles_n);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(2 * std::min<int64_t>(clusters, tiles_m * tiles_n * p.batch)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = tile_smem<kBN>();
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, ffn_tile_kernel<kBN, kLayout, kEpi>, maps, p) != cudaSuccess) {
+        cudaGetLastError();
+        return ROPE3D_ERR_CUDA;
+    }
+    return ROPE3D_OK;
+}
+
+int sm_count() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    return n;
+}
+
+// 256 columns a tile, or 128 where that fills the last round of clusters
+// better: a tile of 128 columns takes a little over half of the time of one of
+// 256 (the pair then reads A's bytes for half of the products).
+template <int kLayout, int kEpi>
+int launch_tile(Params &p, Maps &maps, const Mat *a, const Mat *b, int segs, cudaStream_t st) {
+    const int sms = sm_count();
+    if (sms <= 0) return ROPE3D_ERR_CUDA;
+    const int64_t pairs = std::max(1, sms / 2);
+    auto rounds = [&](int64_t tn) {
+        const int64_t tiles = (int64_t(p.m) + 255) / 256 * ((int64_t(p.n) + tn - 1) / tn) * p.batch;
+        return (tiles + pairs - 1) / pairs;
+    };
+    const int64_t wide = kEpi == kGated ? 128 : 256;
+    if (rounds(wide / 2) * 54 < rounds(wide) * 100)
+        return launch_tile_as<128, kLayout, kEpi>(p, maps, a, b, segs, st);
+    return launch_tile_as<256, kLayout, kEpi>(p, maps, a, b, segs, st);
+}
+
+// Few tokens. w: the weights (two where gated or of two segments), x: the
+// tokens' rows; p.m = weight rows, p.n = tokens.
+template <bool kAMn, int kEpi>
+int launch_stream(Params &p, Maps &maps, const Mat *w, const Mat *x, int segs, cudaStream_t st) {
+    constexpr int kAcc = kEpi == kGated ? 2 : 1;
+    const int sms = sm_count();
+    if (sms <= 0) return ROPE3D_ERR_CUDA;
+    p.rows_n = (p.n + 15) / 16 * 16;
+    for (int i = 0; i < (kEpi == kGated ? 2 : segs); ++i)
+        if (!operand_map(&maps.a[i], w[i], kAMn, 128, p.f16)) return ROPE3D_ERR_CUDA;
+    for (int i = 0; i < segs; ++i)
+        if (!operand_map(&maps.b[i], x[i], false, p.rows_n, p.f16)) return ROPE3D_ERR_CUDA;
+    // shared memory: two CTAs an SM where three slots of the ring fit half of
+    // it (and the partial sums fit the ring), else one
+    const int stage = kAcc * kABytes + p.rows_n * 128, sums = kAcc * p.rows_n * 512;
+    const int extra = 1024 + 512;
+    int stages = (112 * 1024 - extra) / stage, per_sm = 2;
+    if (stages < 3 || stages * stage < sums) {
+        stages = (226 * 1024 - extra) / stage;
+        per_sm = 1;
+    }
+    stages = std::min(stages, 8);
+    p.stages = stages;
+    const int nk = p.nk0 + p.nk1;
+    const int64_t tiles = (int64_t(p.m) + 127) / 128;
+    int split = 1;
+    while (split < kMaxSplit && tiles * split * 2 <= int64_t(sms) * per_sm && nk / (split * 2) >= 2) split *= 2;
+    const int smem = stages * stage + extra;
+    auto *fn = ffn_stream_kernel<kAMn, kEpi>;
+    static std::atomic<int> set[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return ROPE3D_ERR_CUDA;
+    if (!set[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess) {
+            cudaGetLastError();
+            return ROPE3D_ERR_CUDA;
+        }
+        set[dev].store(1, std::memory_order_release);
+    }
+    if (tiles * split > (int64_t(1) << 30)) return ROPE3D_ERR_SHAPE;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(tiles * split));
+    cfg.blockDim = dim3(kStreamThreads);
+    cfg.dynamicSmemBytes = size_t(smem);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(split);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, fn, maps, p) != cudaSuccess) {
+        cudaGetLastError();
+        return ROPE3D_ERR_CUDA;
+    }
+    return ROPE3D_OK;
+}
+
+int blocks64(int64_t k) { return int((k + 63) / 64); }
+int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+
+// Workspace: pieces in a fixed order, each at a multiple of 256 bytes.
+struct Carver {
+    char *base;
+    int64_t used = 0;
+    void *take(int64_t bytes) {
+        void *p = base ? base + used : nullptr;
+        used += up(bytes, 256);
+        return p;
+    }
+};
+
+// x as TMA can read it: itself, or a copy in the workspace with its rows on
+// 16-byte boundaries (launched unless only the size is asked for).
+int aligned(Mat &x, Carver &ws, bool launch, cudaStream_t st) {
+    if (tma_ok(x.p, x.ld, 2)) return ROPE3D_OK;
+    const int64_t ld = up(x.cols, 8);
+    void *dst = ws.take(x.rows * ld * 2);
+    if (launch) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(unsigned((x.cols + 2047) / 2048), unsigned(std::min<int64_t>(x.rows, 65535)));
+        cfg.blockDim = dim3(256);
+        cfg.stream = st;
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, ffn_align_kernel, static_cast<const uint16_t *>(x.p), (long long)x.ld,
+                               static_cast<uint16_t *>(dst), (long long)ld, int(x.cols),
+                               (long long)x.rows) != cudaSuccess) {
+            cudaGetLastError();
+            return ROPE3D_ERR_CUDA;
+        }
+    }
+    x.p = dst;
+    x.ld = ld;
+    return ROPE3D_OK;
+}
+
+bool on_device(const void *p, int device) {
+    cudaPointerAttributes attr{};
+    if (cudaPointerGetAttributes(&attr, p) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    if (attr.type == cudaMemoryTypeManaged) return true;
+    return attr.type == cudaMemoryTypeDevice && attr.device == device;
+}
+
+// One argument's memory: [p, p + bytes), bytes = 0 for an absent one.
+struct Span {
+    const void *p;
+    int64_t bytes;
+    int align;
+};
+
+Span span(const void *p, int64_t rows, int64_t cols, int64_t ld, int es) {
+    return Span{p, p ? ((rows - 1) * ld + cols) * es : 0, es};
+}
+
+bool overlap(const Span &a, const Span &b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && x < y + uint64_t(b.bytes) && y < x + uint64_t(a.bytes);
+}
+
+// Alignment, overlap (outputs overlap nothing) and device memory.
+int check_spans(const Span *in, int nin, const Span *out, int nout, bool check_device) {
+    for (int i = 0; i < nin + nout; ++i) {
+        const Span &s = i < nin ? in[i] : out[i - nin];
+        if (s.p && reinterpret_cast<uintptr_t>(s.p) % uintptr_t(s.align) != 0) return ROPE3D_ERR_ALIGN;
+    }
+    for (int o = 0; o < nout; ++o) {
+        for (int i = 0; i < nin; ++i)
+            if (overlap(out[o], in[i])) return ROPE3D_ERR_ALIAS;
+        for (int j = o + 1; j < nout; ++j)
+            if (overlap(out[o], out[j])) return ROPE3D_ERR_ALIAS;
+    }
+    if (!check_device) return ROPE3D_OK;
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) {
+        cudaGetLastError();
+        return ROPE3D_ERR_CUDA;
+    }
+    for (int i = 0; i < nin + nout; ++i) {
+        const Span &s = i < nin ? in[i] : out[i - nin];
+        if (s.p && !on_device(s.p, device)) return ROPE3D_ERR_DEVICE;
+    }
+    return ROPE3D_OK;
+}
+
+constexpr int64_t kMaxDim = int64_t(1) << 20, kMaxTokens = int64_t(1) << 28, kMaxLd = int64_t(1) << 31;
+
+bool bad_ld(int64_t ld, int64_t cols) { return ld < cols || ld > kMaxLd; }
+
+int check_shape(int64_t tokens, int64_t width, int64_t hidden, int32_t dtype, int32_t act) {
+    if (tokens <= 0 || width <= 0 || hidden <= 0 || tokens > kMaxTokens || width > kMaxDim || hidden > kMaxDim)
+        return ROPE3D_ERR_SHAPE;
+    if (dtype != ROPE3D_BF16 && dtype != ROPE3D_F16) return ROPE3D_ERR_DTYPE;
+    if (act != ROPE3D_ACT_SILU && act != ROPE3D_ACT_GELU_TANH && act != ROPE3D_ACT_GELU_ERF) return ROPE3D_ERR_ARG;
+    return ROPE3D_OK;
+}
+
+int check_pre(int32_t pre_dtype, int32_t dtype) {
+    return pre_dtype == ROPE3D_F32 || pre_dtype == dtype ? ROPE3D_OK : ROPE3D_ERR_DTYPE;
+}
+
+Params base_params(int32_t dtype, int32_t act) {
+    Params p{};
+    p.f16 = dtype == ROPE3D_F16;
+    p.act = act;
+    p.batch = 1;
+    return p;
+}
+
+thread_local int t_ffn_kernel = 0;   // 1 tile, 2 stream kernel: this thread's last forward or dx product
+
+// h (may be null), g, u (may be null) of x.
+int project(const Mat &x, const Mat &wg, const Mat &wu, Out h, Out g, Out u, int32_t dtype, int32_t act,
+            cudaStream_t st) {
+    Maps maps;
+    Params p = base_params(dtype, act);
+    const Out outs[3] = {h, g, u};
+    const Mat w[2] = {wg, wu};
+    p.nk0 = blocks64(x.cols);
+    const int rc = set_outs(p, maps, outs, 3, x.rows, wg.rows, x.rows > kStreamTokens);
+    if (rc != ROPE3D_OK) return rc;
+    if (x.rows <= kStreamTokens) {
+        p.m = int(wg.rows);
+        p.n = int(x.rows);
+        return launch_stream<false, kGated>(p, maps, w, &x, 1, st);
+    }
+    p.m = int(x.rows);
+    p.n = int(wg.rows);
+    return launch_tile<kKK, kGated>(p, maps, &x, w, 1, st);
+}
+
+// One body for the call and for its workspace query (launch = false; *need
+// receives the bytes).
+int forward(const rope3d_gated_ffn_args *a, bool launch, bool check_device, int64_t *need, cudaStream_t st) {
+    if (!a || !a->x || !a->w_gate || !a->w_up || !a->w_down || !a->y) return ROPE3D_ERR_NULL;
+    if ((a->gate_pre == nullptr) != (a->up_pre == nullptr)) return ROPE3D_ERR_NULL;
+    const int64_t M = a->tokens, D = a->width, F = a->hidden;
+    int rc = check_shape(M, D, F, a->dtype, a->act);
+    if (rc != ROPE3D_OK) return rc;
+    if (a->gate_pre && (rc = check_pre(a->pre_dtype, a->dtype)) != ROPE3D_OK) return rc;
+    if (bad_ld(a->x_stride, D) || bad_ld(a->w_gate_stride, D) || bad_ld(a->w_up_stride, D) ||
+        bad_ld(a->w_down_stride, F) || bad_ld(a->y_stride, D) || (a->gate_pre && bad_ld(a->pre_stride, F)))
+        return ROPE3D_ERR_SHAPE;
+    const int pre_es = a->pre_dtype == ROPE3D_F32 ? 4 : 2;
+    Mat x{a->x, M, D, a->x_stride}, wg{a->w_gate, F, D, a->w_gate_stride}, wu{a->w_up, F, D, a->w_up_stride},
+        wd{a->w_down, D, F, a->w_down_stride};
+    Carver size{nullptr};
+    {
+        Mat t[4] = {x, wg, wu, wd};
+        for (Mat &m : t) aligned(m, size, false, st);
+        size.take(M * up(F, 64) * 2);
+    }
+    if (need) *need = size.used;
+    const Span in[4] = {span(x.p, M, D, x.ld, 2), span(wg.p, F, D, wg.ld, 2), span(wu.p, F, D, wu.ld, 2),
+                        span(wd.p, D, F, wd.ld, 2)};
+    Span out[4] = {span(a->y, M, D, a->y_stride, 2), span(a->gate_pre, M, F, a->pre_stride, pre_es),
+                   span(a->up_pre, M, F, a->pre_stride, pre_es), Span{a->workspace, size.used, 256}};
+    rc = check_spans(in, 4, out, need ? 3 : 4, check_device);
+    if (rc != ROPE3D_OK || need) return rc;
+    if (!a->workspace) return ROPE3D_ERR_NULL;
+    if (a->workspace_bytes < size.used) return ROPE3D_ERR_SCRATCH;
+    if (!launch) return ROPE3D_OK;
+
+    Carver ws{static_cast<char *>(a->workspace)};
+    for (Mat *m : {&x, &wg, &wu, &wd})
+        if ((rc = aligned(*m, ws, true, st)) != ROPE3D_OK) return rc;
+    const int64_t hld = up(F, 64);
+    void *hbuf = ws.take(M * hld * 2);
+    const int f32 = a->gate_pre && a->pre_dtype == ROPE3D_F32;
+    rc = project(x, wg, wu, Out{hbuf, hld, 0, 0}, Out{a->gate_pre, a->pre_stride, f32, 0},
+                 Out{a->up_pre, a->pre_stride, f32, 0}, a->dtype, a->act, st);
+    if (rc != ROPE3D_OK) return rc;
+    const Mat h{hbuf, M, F, hld};
+    Maps maps;
+    Params p = base_params(a->dtype, a->act);
+    const Out y{a->y, a->y_stride, 0, 0};
+    p.nk0 = blocks64(F);
+    if ((rc = set_outs(p, maps, &y, 1, M, D, M > kStreamTokens)) != ROPE3D_OK) return rc;
+    t_ffn_kernel = M <= kStreamTokens ? 2 : 1;
+    if (M <= kStreamTokens) {
+        p.m = int(D);
+        p.n = int(M);
+        return launch_stream<false, kPlain>(p, maps, &wd, &h, 1, st);
+    }
+    p.m = int(M);
+    p.n = int(D);
+    return launch_tile<kKK, kPlain>(p, maps, &h, &wd, 1, st);
+}
+
+int backward(const rope3d_gated_ffn_backward_args *a, bool launch, bool check_device, int64_t *need,
+             cudaStream_t st) {
+    if (!a || !a->dy || !a->x || !a->w_gate || !a->w_up || !a->w_down) return ROPE3D_ERR_NULL;
+    if ((a->gate_pre == nullptr) != (a->up_pre == nullptr)) return ROPE3D_ERR_NULL;
+    if ((a->dw_gate == nullptr) != (a->dw_up == nullptr)) return ROPE3D_ERR_NULL;
+    if (!a->dx && !a->dw_gate && !a->dw_down) return ROPE3D_ERR_NULL;
+    const int64_t M = a->tokens, D = a->width, F = a->hidden;
+    int rc = check_shape(M, D, F, a->dtype, a->act);
+    if (rc != ROPE3D_OK) return rc;
+    if (a->gate_pre && (rc = check_pre(a->pre_dtype, a->dtype)) != ROPE3D_OK) return rc;
+    if (bad_ld(a->dy_stride, D) || bad_ld(a->x_stride, D) || bad_ld(a->w_gate_stride, D) ||
+        bad_ld(a->w_up_stride, D) || bad_ld(a->w_down_stride, F) || (a->gate_pre && bad_ld(a->pre_stride, F)) ||
+        (a->dx && bad_ld(a->dx_stride, D)) ||
+        (a->dw_gate && (bad_ld(a->dw_gate_stride, D) || bad_ld(a->dw_up_stride, D))) ||
+        (a->dw_down && bad_ld(a->dw_down_stride, F)))
+        return ROPE3D_ERR_SHAPE;
+    const bool again = !a->gate_pre;   // the projections are computed again, kept in fp32
+    const int pre_es = again || a->pre_dtype == ROPE3D_F32 ? 4 : 2;
+    Mat dy{a->dy, M, D, a->dy_stride}, x{a->x, M, D, a->x_stride}, wg{a->w_gate, F, D, a->w_gate_stride},
+        wu{a->w_up, F, D, a->w_up_stride}, wd{a->w_down, D, F, a->w_down_stride};
+    const int64_t hld = up(F, 64);
+    Carver size{nullptr};
+    {
+        Mat t[5] = {dy, x, wg, wu, wd};
+        for (Mat &m : t) aligned(m, size, false, st);
+        for (int i = 0; i < 3; ++i) size.take(M * hld * 2);
+        if (again)
+            for (int i = 0; i < 2; ++i) size.take(M * hld * 4);
+    }
+    if (need) *need = size.used;
+    const Span in[7] = {span(dy.p, M, D, dy.ld, 2), span(x.p, M, D, x.ld, 2), span(wg.p, F, D, wg.ld, 2),
+                        span(wu.p, F, D, wu.ld, 2), span(wd.p, D, F, wd.ld, 2),
+                        span(a->gate_pre, M, F, a->pre_stride, pre_es), span(a->up_pre, M, F, a->pre_stride, pre_es)};
+    const Span out[5] = {span(a->dx, M, D, a->dx_stride, 2), span(a->dw_gate, F, D, a->dw_gate_stride, 2),
+                         span(a->dw_up, F, D, a->dw_up_stride, 2), span(a->dw_down, D, F, a->dw_down_stride, 2),
+                         Span{a->workspace, size.used, 256}};
+    rc = check_spans(in, 7, out, need ? 4 : 5, check_device);
+    if (rc != ROPE3D_OK || need) return rc;
+    if (!a->workspace) return ROPE3D_ERR_NULL;
+    if (a->workspace_bytes < size.used) return ROPE3D_ERR_SCRATCH;
+    if (!launch) return ROPE3D_OK;
+
+    Carver ws{static_cast<char *>(a->workspace)};
+    for (Mat *m : {&dy, &x, &wg, &wu, &wd})
+        if ((rc = aligned(*m, ws, true, st)) != ROPE3D_OK) return rc;
+    void *dgb = ws.take(M * hld * 2), *dub = ws.take(M * hld * 2), *hb = ws.take(M * hld * 2);
+    const void *g = a->gate_pre, *u = a->up_pre;
+    int64_t ldp = a->pre_stride;
+    if (again) {
+        void *gb = ws.take(M * hld * 4), *ub = ws.take(M * hld * 4);
+        rc = project(x, wg, wu, Out{nullptr, 0, 0, 0}, Out{gb, hld, 1, 0}, Out{ub, hld, 1, 0}, a->dtype, a->act, st);
+        if (rc != ROPE3D_OK) return rc;
+        g = gb;
+        u = ub;
+        ldp = hld;
+    }
+    const bool few = M <= kStreamTokens;
+    t_ffn_kernel = few ? 2 : 1;
+    Maps maps;
+    {
+        // dh = dy Wd, and from it dg, du and h
+        Params p = base_params(a->dtype, a->act);
+        const Out outs[3] = {Out{dgb, hld, 0, 0}, Out{dub, hld, 0, 0}, Out{a->dw_down ? hb : nullptr, hld, 0, 0}};
+        if ((rc = set_outs(p, maps, outs, 3, M, F, !few)) != ROPE3D_OK) return rc;
+        p.nk0 = blocks64(D);
+        p.g = g;
+        p.u = u;
+        p.ldp = ldp;
+        p.pre_f32 = pre_es == 4;
+        p.pre_vec = tma_ok(g, ldp, pre_es) && tma_ok(u, ldp, pre_es);
+        p.m = int(few ? F : M);
+        p.n = int(few ? M : F);
+        rc = few ? launch_stream<true, kBack>(p, maps, &wd, &dy, 1, st)
+                 : launch_tile<kKM, kBack>(p, maps, &dy, &wd, 1, st);
+        if (rc != ROPE3D_OK) return rc;
+    }
+    const Mat dg{dgb, M, F, hld}, du{dub, M, F, hld}, h{hb, M, F, hld};
+    if (a->dx) {
+        Params p = base_params(a->dtype, a->act);
+        const Out o{a->dx, a->dx_stride, 0, 0};
+        const Mat t[2] = {dg, du}, w[2] = {wg, wu};
+        if ((rc = set_outs(p, maps, &o, 1, M, D, !few)) != ROPE3D_OK) return rc;
+        p.nk0 = p.nk1 = blocks64(F);
+        p.m = int(few ? D : M);
+        p.n = int(few ? M : D);
+        rc = few ? launch_stream<true, kPlain>(p, maps, w, t, 2, st) : launch_tile<kKM, kPlain>(p, maps, t, w, 2, st);
+        if (rc != ROPE3D_OK) return rc;
+    }
+    if (a->dw_gate) {
+        // both in one launch: a batch of two products
+        Params p = base_params(a->dtype, a->act);
+        const Out o[2] = {Out{a->dw_gate, a->dw_gate_stride, 0, 0}, Out{a->dw_up, a->dw_up_stride, 0, 0}};
+        const Mat t[2] = {dg, du}, xs[2] = {x, x};
+        if ((rc = set_outs(p, maps, o, 2, F, D, true)) != ROPE3D_OK) return rc;
+        p.nk0 = blocks64(M);
+        p.m = int(F);
+        p.n = int(D);
+        p.batch = 2;
+        if ((rc = launch_tile<kMM, kPlain>(p, maps, t, xs, 2, st)) != ROPE3D_OK) return rc;
+    }
+    if (a->dw_down) {
+        Params p = base_params(a->dtype, a->act);
+        const Out o{a->dw_down, a->dw_down_stride, 0, 0};
+        if ((rc = set_outs(p, maps, &o, 1, D, F, true)) != ROPE3D_OK) return rc;
+        p.nk0 = blocks64(M);
+        p.m = int(D);
+        p.n = int(F);
+        if ((rc = launch_tile<kMM, kPlain>(p, maps, &dy, &h, 1, st)) != ROPE3D_OK) return rc;
+    }
+    return ROPE3D_OK;
+}
+
+}  // namespace
+
+extern "C" int rope3d_gated_ffn(const rope3d_gated_ffn_args *args, void *stream) {
+    return forward(args, true, true, nullptr, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int rope3d_gated_ffn_check(const rope3d_gated_ffn_args *args, int32_t check_device) {
+    return forward(args, false, check_device != 0, nullptr, nullptr);
+}
+
+extern "C" int rope3d_gated_ffn_workspace(const rope3d_gated_ffn_args *args, int64_t *bytes) {
+    if (!bytes) return ROPE3D_ERR_NULL;
+    return forward(args, false, false, bytes, nullptr);
+}
+
+extern "C" int rope3d_gated_ffn_backward(const rope3d_gated_ffn_backward_args *args, void *stream) {
+    return backward(args, true, true, nullptr, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int rope3d_gated_ffn_backward_check(const rope3d_gated_ffn_backward_args *args, int32_t check_device) {
+    return backward(args, false, check_device != 0, nullptr, nullptr);
+}
+
+extern "C" int rope3d_gated_ffn_backward_workspace(const rope3d_gated_ffn_backward_args *args, int64_t *bytes) {
+    if (!bytes) return ROPE3D_ERR_NULL;
+    return backward(args, false, false, bytes, nullptr);
+}
+
+extern "C" int rope3d_gated_ffn_last_kernel(void) { return t_ffn_kernel; }
+
+extern "C" int rope3d_testing_ffn_wait_timeouts(int64_t *count, int32_t reset) {
+    if (!count) return ROPE3D_ERR_NULL;
+    unsigned int n = 0;
+    if (cudaMemcpyFromSymbol(&n, g_ffn_wait_timeouts, sizeof(n)) != cudaSuccess) {
+        cudaGetLastError();
+        return ROPE3D_ERR_CUDA;
+    }
+    if (reset) {
+        const unsigned int zero = 0;
+        if (cudaMemcpyToSymbol(g_ffn_wait_timeouts, &zero, sizeof(zero)) != cudaSuccess) {
+            cudaGetLastError();
+            return ROPE3D_ERR_CUDA;
+        }
+    }
+    *count = n;
+    return ROPE3D_OK;
+}
