@@ -37,7 +37,8 @@ __all__ = [
     "NORM_NONE", "NORM_RMS", "NORM_LAYER", "ACT_SILU", "ACT_GELU_TANH", "ACT_GELU_ERF",
     "rope3d_gated_ffn", "rope3d_gated_ffn_backward", "rope3d_gated_ffn_check",
     "rope3d_gated_ffn_backward_check", "rope3d_gated_ffn_last_kernel",
-    "rope3d_testing_ffn_wait_timeouts",
+    "rope3d_testing_ffn_wait_timeouts", "rope3d_block_norm", "rope3d_block_norm_backward",
+    "rope3d_block_norm_check", "rope3d_block_norm_backward_check", "rope3d_block_norm_last_kernel",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -77,6 +78,15 @@ def _struct(name, *fields):
     return type(name, (ctypes.Structure,), {"_fields_": out})
 
 
+_NORM_FIELDS = (
+    "p:x y post_weight gate pre_weight scale shift r n", "i64:rows channels rows_per_group",
+    "i64:x_stride y_stride r_stride n_stride gate_stride scale_stride shift_stride",
+    "f64:eps residual_scale weight_offset", "i32:dtype param_dtype post_kind pre_kind")
+_NormArgs = _struct("rope3d_block_norm_args", *_NORM_FIELDS)
+_NormBackArgs = _struct(   # the forward call's arguments come first
+    "rope3d_block_norm_backward_args", *_NORM_FIELDS, "p:dr dn dx dy",
+    "p:d_post_weight d_gate d_pre_weight d_scale d_shift",
+    "i64:dr_stride dn_stride dx_stride dy_stride grad_stride", "p:workspace", "i64:workspace_bytes")
 _FfnArgs = _struct(
     "rope3d_gated_ffn_args", "p:x w_gate w_up w_down y gate_pre up_pre", "i64:tokens width hidden",
     "i64:x_stride w_gate_stride w_up_stride w_down_stride y_stride pre_stride",
@@ -138,6 +148,12 @@ def _declare(lib):
         "rope3d_na3d": ([vp] * 5 + [i64] * 6 + [vp, vp, i32, vp], c.c_int),
         "rope3d_na3d_rotate_once": ([vp] * 6 + [i64] * 6 + [vp, vp, vp], c.c_int),
         "rope3d_na3d_preflight": ([vp] * 6 + [i64] * 6 + [vp, vp, i32, i32], c.c_int),
+        "rope3d_block_norm": ([vp, vp], c.c_int),
+        "rope3d_block_norm_check": ([vp, i32], c.c_int),
+        "rope3d_block_norm_backward": ([vp, vp], c.c_int),
+        "rope3d_block_norm_backward_check": ([vp, i32], c.c_int),
+        "rope3d_block_norm_backward_workspace": ([vp, vp], c.c_int),
+        "rope3d_block_norm_last_kernel": ([], c.c_int),
         "rope3d_gated_ffn": ([vp, vp], c.c_int),
         "rope3d_gated_ffn_check": ([vp, i32], c.c_int),
         "rope3d_gated_ffn_workspace": ([vp, vp], c.c_int),
@@ -634,6 +650,126 @@ def _scratch(nbytes: int, like, stream):
         if handle != int(torch.cuda.current_stream(like.device).cuda_stream):
             ws.record_stream(torch.cuda.ExternalStream(handle, device=like.device))
     return ws
+
+
+def _norm_fields(a, x, y, post, pre, post_weight, gate, pre_weight, scale, shift, rows_per_group, eps,
+                 residual_scale, weight_offset):
+    """The fields that forward and backward share."""
+    rows, channels, a.x_stride = _matrix("x", x)
+    a.rows, a.channels, a.dtype = rows, channels, _dtype_code(x)
+    a.x = _ptr(x)
+    if y is not None:
+        a.y, a.y_stride = _ptr(y), _matrix("y", y, rows, channels, x.dtype)[2]
+    params = [t for t in (post_weight, gate, pre_weight, scale, shift) if t is not None]
+    if params and any(t.dtype != params[0].dtype for t in params):
+        raise TypeError("weights, gate, scale and shift must have one dtype")
+    a.param_dtype = _dtype_code(params[0]) if params else a.dtype
+    for name, t in (("post_weight", post_weight), ("pre_weight", pre_weight)):
+        if t is not None:
+            if t.dim() != 1 or t.numel() != channels or (channels > 1 and t.stride(0) != 1):
+                raise ValueError(f"{name} must be contiguous, [{channels}]")
+            setattr(a, name, _ptr(t))
+    groups = None
+    for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
+        if t is None:
+            continue
+        g, _, ld = _matrix(name, t.unsqueeze(0) if t.dim() == 1 else t, groups, channels)
+        groups = g
+        setattr(a, name, _ptr(t))
+        setattr(a, name + "_stride", ld)
+    if rows_per_group is None:
+        if groups is not None and (groups == 0 or rows % groups):
+            raise ValueError(f"{rows} rows are not whole groups of {groups}: give rows_per_group")
+        rows_per_group = rows // groups if groups else rows
+    elif groups is not None and rows_per_group > 0 and -(-rows // rows_per_group) != groups:
+        raise ValueError(f"{rows} rows in groups of {rows_per_group} do not make {groups} groups")
+    a.rows_per_group, a.eps = int(rows_per_group), float(eps)
+    a.residual_scale, a.weight_offset = float(residual_scale), float(weight_offset)
+    a.post_kind, a.pre_kind = int(post), int(pre)
+    return rows, channels
+
+
+def rope3d_block_norm(x, y=None, post: int = NORM_NONE, pre=NORM_RMS, post_weight=None, gate=None,
+                      pre_weight=None, scale=None, shift=None, rows_per_group=None, eps: float = 1e-6,
+                      residual_scale: float = 1.0, weight_offset: float = 0.0, r=None, n=None, stream=None):
+    """The norms around a transformer block, in one pass over x and y [..., channels]:
+        r = residual_scale * x + gate * post(y) * (post_weight + weight_offset)
+        n = pre(r) * (pre_weight + weight_offset) * (1 + scale) + shift
+    gate, scale and shift are [groups, channels], one row for each rows_per_group
+    rows of x (rows / groups when None). y None: r is residual_scale * x and only
+    computed into a given r; pre None: n is not computed. r and n may be x or y
+    (in place). Returns (r, n), None for what is not computed."""
+    import torch
+
+    if r is None and y is not None:
+        r = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if n is None and pre is not None:
+        n = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    a = _NormArgs()
+    rows, channels = _norm_fields(a, x, y, post, NORM_NONE if pre is None else pre, post_weight, gate, pre_weight,
+                                  scale, shift, rows_per_group, eps, residual_scale, weight_offset)
+    for name, t in (("r", r), ("n", n)):
+        if t is not None:
+            setattr(a, name, _ptr(t))
+            setattr(a, name + "_stride", _matrix(name, t, rows, channels, x.dtype)[2])
+    _check(load_library().rope3d_block_norm(ctypes.byref(a), _stream(stream, x)), "rope3d_block_norm")
+    return r, n
+
+
+def rope3d_block_norm_backward(x, y=None, dr=None, dn=None, post: int = NORM_NONE, pre=NORM_RMS,
+                               post_weight=None, gate=None, pre_weight=None, scale=None, shift=None,
+                               rows_per_group=None, eps: float = 1e-6, residual_scale: float = 1.0,
+                               weight_offset: float = 0.0, dx=None, dy=None, param_grads: bool = True,
+                               workspace=None, stream=None):
+    """The gradients of rope3d_block_norm with the same arguments, from dr and dn
+    (either may be None: zero). Returns a dict: dx, dy (with y) and, with
+    param_grads, d_post_weight, d_gate, d_pre_weight, d_scale, d_shift for the
+    parameters given, in their dtype."""
+    import torch
+
+    a = _NormBackArgs()
+    rows, channels = _norm_fields(a, x, y, post, NORM_NONE if pre is None else pre, post_weight, gate, pre_weight,
+                                  scale, shift, rows_per_group, eps, residual_scale, weight_offset)
+    out = {"dx": torch.empty(x.shape, dtype=x.dtype, device=x.device) if dx is None else dx}
+    if y is not None:
+        out["dy"] = torch.empty(x.shape, dtype=x.dtype, device=x.device) if dy is None else dy
+    for name, t in (("dr", dr), ("dn", dn), *out.items()):
+        if t is not None:
+            setattr(a, name, _ptr(t))
+            setattr(a, name + "_stride", _matrix(name, t, rows, channels, x.dtype)[2])
+    if param_grads:
+        a.grad_stride = channels
+        for name, t in (("post_weight", post_weight), ("gate", gate), ("pre_weight", pre_weight), ("scale", scale),
+                        ("shift", shift)):
+            if t is not None:
+                out["d_" + name] = torch.empty(t.shape, dtype=t.dtype, device=t.device)
+                setattr(a, "d_" + name, _ptr(out["d_" + name]))
+    lib = load_library()
+    need = ctypes.c_int64()
+    _check(lib.rope3d_block_norm_backward_workspace(ctypes.byref(a), ctypes.byref(need)), "rope3d_block_norm_backward")
+    if workspace is None and need.value:
+        workspace = _scratch(need.value, x, stream)
+    if workspace is not None:
+        a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
+    _check(lib.rope3d_block_norm_backward(ctypes.byref(a), _stream(stream, x)), "rope3d_block_norm_backward")
+    return out
+
+
+def rope3d_block_norm_check(check_device: bool = False, **fields) -> str:
+    """Status name of rope3d_block_norm's checks for the given argument fields
+    (pointers may be plain integers)."""
+    return STATUS[load_library().rope3d_block_norm_check(ctypes.byref(_NormArgs(**fields)), int(check_device))]
+
+
+def rope3d_block_norm_backward_check(check_device: bool = False, **fields) -> str:
+    """Status name of rope3d_block_norm_backward's checks."""
+    return STATUS[load_library().rope3d_block_norm_backward_check(ctypes.byref(_NormBackArgs(**fields)),
+                                                                  int(check_device))]
+
+
+def rope3d_block_norm_last_kernel() -> int:
+    """Kernel of this thread's last norm call: 1 rows in registers, 2 the general one."""
+    return int(load_library().rope3d_block_norm_last_kernel())
 
 
 def _ffn_args(x, w_gate, w_up, w_down, y, gate_pre, up_pre, act, keep_like=None):

@@ -25,6 +25,7 @@ SOURCES = [
     os.path.join(CSRC, "rope3d_patchify.cu"),
     os.path.join(CSRC, "rope3d_neox.cu"),
     os.path.join(CSRC, "rope3d_na3d.cu"),
+    os.path.join(CSRC, "rope3d_norm.cu"),
     os.path.join(CSRC, "rope3d_ffn.cu"),
     os.path.join(CSRC, "rope3d_tc.cuh"),
     os.path.join(CSRC, "rope3d_api.cpp"),
@@ -87,14 +88,22 @@ def commands(out_dir: str = BUILD, extra_nvcc: list[str] | None = None,
         "-Xptxas", "-v", *(extra_nvcc or []),
         "-c", os.path.join(CSRC, "rope3d_ffn.cu"), "-o", ffn_o,
     ]
+    norm_o = os.path.join(out_dir, "rope3d_norm.o")
+    nvcc_norm = [
+        _nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", *dbg, "-Xcompiler", "-fPIC",
+        "-Xptxas", "-v", *(extra_nvcc or []),
+        "-c", os.path.join(CSRC, "rope3d_norm.cu"), "-o", norm_o,
+    ]
     gxx_compile = [
         "g++", "-std=c++17", "-O2", "-fPIC", "-ffp-contract=off", "-fno-fast-math", *dbg,
         "-pthread", "-Wall", "-Wno-unused-function", f"-I{cuda}/include",
         "-c", os.path.join(CSRC, "rope3d_api.cpp"), "-o", api_o,
     ]
     link = [_nvcc(), *ARCH, "-shared", kern_o, api_o, noalloc_o, patch_o, neox_o, na_o, ffn_o,
+            norm_o,
             "-o", os.path.join(out_dir, "librope3d.so"), "-Xcompiler", "-pthread"]
-    return [nvcc_compile, gxx_compile, nvcc_noalloc, nvcc_patch, nvcc_neox, nvcc_na, nvcc_ffn], link
+    return [nvcc_compile, gxx_compile, nvcc_noalloc, nvcc_patch, nvcc_neox, nvcc_na, nvcc_ffn,
+            nvcc_norm], link
 
 
 def up_to_date(lib: str = LIB) -> bool:

@@ -1,0 +1,121 @@
+"""rope3d_block_norm and its backward pass on the GPU against 64 bits, within
+bounds derived rounding by rounding (block_reference.py): both norms, each alone,
+with and without weights, gate, scale and shift, groups of every size down to one
+row, rows of one channel to rows too long for registers, unaligned and strided
+views, in place."""
+from __future__ import annotations
+
+import itertools
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover - CPU hosts
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import rope_rope3d_apply_gb300 as r  # noqa: E402
+from tests import block_reference as ref  # noqa: E402
+
+DEV = torch.device("cuda:0")
+DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+
+
+def make(rows, channels, dtype, groups=1, y=True, post=1, pre=1, weights=True, mod=True, params=None, rpg=None, seed=0,
+         **kw):
+    """Keyword arguments of a call, and dr, dn. groups: rows / groups rows each,
+    or rpg rows each (the last shorter)."""
+    g = torch.Generator(device=DEV).manual_seed(seed + 31 * rows + channels)
+    dt, pt = DT[dtype], DT[params or dtype]
+    rpg = rpg or rows // groups
+    n_groups = -(-rows // rpg)
+
+    def normal(shape, dtype, scale=1.0, shift=0.0):
+        return (torch.randn(shape, generator=g, device=DEV) * scale + shift).to(dtype)
+
+    a = dict(x=normal((rows, channels), dt, 2.0, 0.3), y=normal((rows, channels), dt, 0.7, -0.2) if y else None,
+             post=post, pre=pre, rows_per_group=rpg, **kw)
+    off = kw.get("weight_offset", 0.0)
+    if weights:
+        a["pre_weight"] = normal((channels,), pt, 0.1, 1.0 - off)
+        if y and post:
+            a["post_weight"] = normal((channels,), pt, 0.1, 1.0 - off)
+    if mod:
+        m = normal((n_groups, 3, channels), pt, 0.3)   # rows of one modulation tensor: strided views
+        a["scale"], a["shift"] = m[:, 0], m[:, 1]
+        if y:
+            a["gate"] = m[:, 2]
+    return a, normal((rows, channels), dt, 0.5), normal((rows, channels), dt, 0.5)
+
+
+def both(a, dr, dn, kernel):
+    got = dict(zip(("r", "n"), r.rope3d_block_norm(**a)))
+    assert r.rope3d_block_norm_last_kernel() == kernel
+    want = ref.norm64(**a)
+    for name, t in got.items():
+        if t is not None:
+            ref.check(t, want[name], name)
+    got = r.rope3d_block_norm_backward(dr=dr, dn=dn, **a)
+    assert r.rope3d_block_norm_last_kernel() == kernel
+    torch.cuda.synchronize()
+    want = ref.norm64(dr=dr, dn=dn, grads=True, **a)
+    assert set(got) == set(want)
+    for name, t in got.items():
+        ref.check(t, want[name], name)
+    again = r.rope3d_block_norm_backward(dr=dr, dn=dn, **a)
+    for name, t in got.items():
+        assert torch.equal(t, again[name]), name
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("post,pre", list(itertools.product((0, 1, 2), (0, 1, 2))))
+@pytest.mark.parametrize("channels,kernel", [(256, 1), (77, 2)])
+def test_kinds(post, pre, channels, kernel, dtype):
+    both(*make(37, channels, dtype, post=post, pre=pre, residual_scale=0.5), kernel)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("y,weights,mod", list(itertools.product((True, False), repeat=3)))
+@pytest.mark.parametrize("channels,kernel", [(512, 1), (130, None)])
+def test_absent_parts(y, weights, mod, channels, kernel, dtype):
+    kernel = kernel or 2
+    both(*make(24, channels, dtype, groups=3, y=y, weights=weights, mod=mod, weight_offset=1.0), kernel)
+
+
+@pytest.mark.parametrize("dtype,channels,kernel", [
+    # one channel, one vector, whole warps and their neighbours, each team size, the longest rows in registers, longer
+    ("bf16", 1, 2), ("f32", 3, 2), ("bf16", 8, 1), ("f32", 4, 1), ("bf16", 248, 1), ("bf16", 264, 1), ("f16", 520, 1),
+    ("bf16", 1000, 1), ("bf16", 1032, 1), ("f32", 1028, 1), ("bf16", 2048, 1), ("f16", 4096, 1), ("bf16", 4104, 1),
+    ("bf16", 8192, 1), ("f32", 2052, 1), ("f32", 4096, 1), ("f32", 8192, 1), ("bf16", 65536, 2), ("f16", 20001, 2),
+])
+def test_channels(dtype, channels, kernel):
+    both(*make(5, channels, dtype, post=2, pre=2), kernel)
+
+
+def test_long_rows_forward_in_registers():
+    """Forward rows of up to 2048 vectors stay in registers; the backward pass of
+    those takes the general kernel."""
+    a, dr, dn = make(3, 16384, "bf16")
+    want = ref.norm64(**a)
+    out = r.rope3d_block_norm(**a)
+    assert r.rope3d_block_norm_last_kernel() == 1
+    ref.check(out[0], want["r"], "r")
+    ref.check(out[1], want["n"], "n")
+    got = r.rope3d_block_norm_backward(dr=dr, dn=dn, **a)
+    assert r.rope3d_block_norm_last_kernel() == 2
+    want = ref.norm64(dr=dr, dn=dn, grads=True, **a)
+    for name, t in got.items():
+        ref.check(t, want[name], name)
+
+
+@pytest.mark.parametrize("params", ["f32", None])
+@pytest.mark.parametrize("dtype,channels,kernel", [("bf16", 320, 1), ("f16", 1152, 1), ("bf16", 45, 2)])
+@pytest.mark.parametrize("rows,rpg", [(1, 1), (2, 1), (700, 1), (700, 3), (700, 64), (701, 350), (3000, 1500), (3000, 7)])
+def test_groups(rows, rpg, dtype, channels, kernel, params):
+    both(*make(rows, channels, dtype, rpg=rpg, params=params), kernel)
+
+
+def test_many_rows():
+    both(*make(20000, 128, "bf16", groups=2), 1)
+    both(*make(6000, 2048, "f16", y=True, weights=True, mod=False, weight_offset=1.0), 1)
