@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 __all__ = [
@@ -69,13 +70,18 @@ class Rope3dError(RuntimeError):
 
 
 def _struct(name, *fields):
-    """A ctypes structure from "type: field field ..." lines."""
-    kinds = {"p": ctypes.c_void_p, "i64": ctypes.c_int64, "i32": ctypes.c_int32, "f64": ctypes.c_double}
-    out = []
+    """A C structure from "type: field field ..." lines: its ctypes class, with a
+    packer of all fields in order (a call packs its arguments in one go)."""
+    kinds = {"p": (ctypes.c_void_p, "Q"), "i64": (ctypes.c_int64, "q"), "i32": (ctypes.c_int32, "i"),
+             "f64": (ctypes.c_double, "d")}
+    out, codes = [], "@"
     for line in fields:
         kind, names = line.split(":")
-        out += [(n, kinds[kind]) for n in names.split()]
-    return type(name, (ctypes.Structure,), {"_fields_": out})
+        out += [(n, kinds[kind][0]) for n in names.split()]
+        codes += kinds[kind][1] * len(names.split())
+    cls = type(name, (ctypes.Structure,), {"_fields_": out})
+    cls.pack = struct.Struct(codes + "0q").pack
+    return cls
 
 
 _NORM_FIELDS = (
@@ -175,6 +181,8 @@ def _declare(lib):
 def load_library(path: str | None = None):
     """Load the built library (fails loudly when it is missing)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             p = path or LIB_PATH
@@ -617,76 +625,117 @@ def rope3d_na3d_preflight(q, k, v, k_rot, out, tables, B, T, H, W, heads, kernel
     return STATUS.get(rc, str(rc))
 
 
-def _matrix(name, t, rows=None, cols=None, dtype=None):
-    """(rows, cols, row stride) of a matrix: the last dimension contiguous, the
+_torch = None
+
+
+def _use_torch():
+    global _torch
+    if _torch is None:
+        import torch
+
+        _torch = torch
+    return _torch
+
+
+def _raw_stream(stream, like) -> int:
+    """The cudaStream_t of `stream`, or of the current stream of `like`'s device."""
+    if stream is None and like.is_cuda:
+        return _torch._C._cuda_getCurrentRawStream(like.device.index)
+    return _stream(stream, like)
+
+
+def _code(t) -> int:
+    """The dtype code of a tensor."""
+    dt = t.dtype
+    return BF16 if dt is _torch.bfloat16 else F16 if dt is _torch.float16 else \
+        F32 if dt is _torch.float32 else _dtype_code(t)
+
+
+def _matrix(name, t):
+    """(rows, columns, row stride) of a matrix: the last dimension contiguous, the
     others viewable as one."""
-    if t.dim() < 2 or (t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{name} must be a matrix with contiguous rows")
-    c = int(t.shape[-1])
-    if t.dim() == 2:
-        r, ld = int(t.shape[0]), int(t.stride(0))
-        if r <= 1:
-            ld = max(ld, c)
-    else:
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous, or a 2-D view with contiguous rows")
-        r, ld = (t.numel() // c if c else 0), c
-    if (rows is not None and r != rows) or (cols is not None and c != cols):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {rows if rows is not None else r} rows "
-                         f"of {cols if cols is not None else c}")
-    if dtype is not None and t.dtype != dtype:
+    shape, st = t.shape, t.stride()
+    if len(shape) == 2:
+        r, c = shape
+        if c > 1 and st[1] != 1:
+            raise ValueError(f"{name} must have contiguous rows")
+        return r, c, st[0] if r > 1 else max(st[0], c)
+    if len(shape) < 2 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a matrix: contiguous, or a 2-D view with contiguous rows")
+    c = shape[-1]
+    return (t.numel() // c if c else 0), c, c
+
+
+def _stride(name, t, rows, cols, dtype) -> int:
+    """The row stride of a [rows, cols] matrix of `dtype` (0 for None)."""
+    if t is None:
+        return 0
+    r, c, ld = _matrix(name, t)
+    if r != rows or c != cols:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {rows} rows of {cols}")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
-    return r, c, ld
+    return ld
 
 
 def _scratch(nbytes: int, like, stream):
-    """Device memory for one call: freed for other work only after what `stream`
-    holds so far."""
-    import torch
-
-    ws = torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=like.device)
-    if stream is not None:
-        handle = _stream(stream)
-        if handle != int(torch.cuda.current_stream(like.device).cuda_stream):
-            ws.record_stream(torch.cuda.ExternalStream(handle, device=like.device))
+    """Device memory for one call on the raw stream `stream`: given to other work
+    only after what that stream holds so far."""
+    ws = _torch.empty(nbytes, dtype=_torch.uint8, device=like.device)
+    if stream != _torch._C._cuda_getCurrentRawStream(like.device.index):
+        ws.record_stream(_torch.cuda.ExternalStream(stream, device=like.device))
     return ws
 
 
-def _norm_fields(a, x, y, post, pre, post_weight, gate, pre_weight, scale, shift, rows_per_group, eps,
-                 residual_scale, weight_offset):
-    """The fields that forward and backward share."""
-    rows, channels, a.x_stride = _matrix("x", x)
-    a.rows, a.channels, a.dtype = rows, channels, _dtype_code(x)
-    a.x = _ptr(x)
-    if y is not None:
-        a.y, a.y_stride = _ptr(y), _matrix("y", y, rows, channels, x.dtype)[2]
-    params = [t for t in (post_weight, gate, pre_weight, scale, shift) if t is not None]
-    if params and any(t.dtype != params[0].dtype for t in params):
-        raise TypeError("weights, gate, scale and shift must have one dtype")
-    a.param_dtype = _dtype_code(params[0]) if params else a.dtype
+def _workspace(cls, fields, query, what, given, like, stream):
+    """The packed arguments of a call (`fields` ends before workspace), with its
+    workspace: `given`, or new memory of the size that `query` gives."""
+    body, tail = fields
+    lib = load_library()
+    need = ctypes.c_int64()
+    if given is None:
+        _check(getattr(lib, query)(cls.pack(*body, 0, 0, *tail), ctypes.byref(need)), what)
+        if not need.value:
+            return cls.pack(*body, 0, 0, *tail), None
+        given = _scratch(need.value, like, stream)
+        return cls.pack(*body, given.data_ptr(), need.value, *tail), given
+    return cls.pack(*body, given.data_ptr(), given.numel() * given.element_size(), *tail), given
+
+
+def _norm_fields(x, y, post, pre, post_weight, gate, pre_weight, scale, shift, rows_per_group, eps,
+                 residual_scale, weight_offset, r, n):
+    """The packed fields of rope3d_block_norm_args."""
+    rows, channels, ldx = _matrix("x", x)
+    dt = x.dtype
+    code = pcode = _code(x)
+    pdt = None
     for name, t in (("post_weight", post_weight), ("pre_weight", pre_weight)):
         if t is not None:
-            if t.dim() != 1 or t.numel() != channels or (channels > 1 and t.stride(0) != 1):
+            if pdt is None:
+                pdt, pcode = t.dtype, _code(t)
+            elif t.dtype is not pdt:
+                raise TypeError("weights, gate, scale and shift must have one dtype")
+            if t.dim() != 1 or t.shape[0] != channels or (channels > 1 and t.stride(0) != 1):
                 raise ValueError(f"{name} must be contiguous, [{channels}]")
-            setattr(a, name, _ptr(t))
-    groups = None
-    for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
-        if t is None:
-            continue
-        g, _, ld = _matrix(name, t.unsqueeze(0) if t.dim() == 1 else t, groups, channels)
-        groups = g
-        setattr(a, name, _ptr(t))
-        setattr(a, name + "_stride", ld)
+    groups, lds = None, [0, 0, 0]
+    for i, (name, t) in enumerate((("gate", gate), ("scale", scale), ("shift", shift))):
+        if t is not None:
+            if pdt is None:
+                pdt, pcode = t.dtype, _code(t)
+            if groups is None:
+                groups = t.shape[0] if t.dim() == 2 else 1
+            lds[i] = _stride(name, t if t.dim() != 1 else t.unsqueeze(0), groups, channels, pdt)
     if rows_per_group is None:
         if groups is not None and (groups == 0 or rows % groups):
             raise ValueError(f"{rows} rows are not whole groups of {groups}: give rows_per_group")
         rows_per_group = rows // groups if groups else rows
     elif groups is not None and rows_per_group > 0 and -(-rows // rows_per_group) != groups:
         raise ValueError(f"{rows} rows in groups of {rows_per_group} do not make {groups} groups")
-    a.rows_per_group, a.eps = int(rows_per_group), float(eps)
-    a.residual_scale, a.weight_offset = float(residual_scale), float(weight_offset)
-    a.post_kind, a.pre_kind = int(post), int(pre)
-    return rows, channels
+    ptr = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
+    return (x.data_ptr(), ptr(y), ptr(post_weight), ptr(gate), ptr(pre_weight), ptr(scale), ptr(shift), ptr(r),
+            ptr(n), rows, channels, rows_per_group, ldx, _stride("y", y, rows, channels, dt),
+            _stride("r", r, rows, channels, dt), _stride("n", n, rows, channels, dt), *lds, eps, residual_scale,
+            weight_offset, code, pcode, post, pre)
 
 
 def rope3d_block_norm(x, y=None, post: int = NORM_NONE, pre=NORM_RMS, post_weight=None, gate=None,
@@ -699,20 +748,18 @@ def rope3d_block_norm(x, y=None, post: int = NORM_NONE, pre=NORM_RMS, post_weigh
     rows of x (rows / groups when None). y None: r is residual_scale * x and only
     computed into a given r; pre None: n is not computed. r and n may be x or y
     (in place). Returns (r, n), None for what is not computed."""
-    import torch
-
+    torch = _use_torch()
     if r is None and y is not None:
-        r = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if n is None and pre is not None:
-        n = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    a = _NormArgs()
-    rows, channels = _norm_fields(a, x, y, post, NORM_NONE if pre is None else pre, post_weight, gate, pre_weight,
-                                  scale, shift, rows_per_group, eps, residual_scale, weight_offset)
-    for name, t in (("r", r), ("n", n)):
-        if t is not None:
-            setattr(a, name, _ptr(t))
-            setattr(a, name + "_stride", _matrix(name, t, rows, channels, x.dtype)[2])
-    _check(load_library().rope3d_block_norm(ctypes.byref(a), _stream(stream, x)), "rope3d_block_norm")
+        r = torch.empty_like(x, memory_format=torch.contiguous_format)
+    if pre is None:
+        n, pre = None, NORM_NONE
+    elif n is None:
+        n = torch.empty_like(x, memory_format=torch.contiguous_format)
+    args = _NormArgs.pack(*_norm_fields(x, y, post, pre, post_weight, gate, pre_weight, scale, shift, rows_per_group,
+                                        eps, residual_scale, weight_offset, r, n))
+    rc = load_library().rope3d_block_norm(args, _raw_stream(stream, x))
+    if rc:
+        raise Rope3dError(rc, "rope3d_block_norm")
     return r, n
 
 
@@ -725,33 +772,28 @@ def rope3d_block_norm_backward(x, y=None, dr=None, dn=None, post: int = NORM_NON
     (either may be None: zero). Returns a dict: dx, dy (with y) and, with
     param_grads, d_post_weight, d_gate, d_pre_weight, d_scale, d_shift for the
     parameters given, in their dtype."""
-    import torch
-
-    a = _NormBackArgs()
-    rows, channels = _norm_fields(a, x, y, post, NORM_NONE if pre is None else pre, post_weight, gate, pre_weight,
-                                  scale, shift, rows_per_group, eps, residual_scale, weight_offset)
-    out = {"dx": torch.empty(x.shape, dtype=x.dtype, device=x.device) if dx is None else dx}
+    torch = _use_torch()
+    fwd = _norm_fields(x, y, post, NORM_NONE if pre is None else pre, post_weight, gate, pre_weight, scale, shift,
+                       rows_per_group, eps, residual_scale, weight_offset, None, None)
+    rows, channels, dt = fwd[9], fwd[10], x.dtype
+    fresh = lambda t: torch.empty_like(t, memory_format=torch.contiguous_format)  # noqa: E731
+    out = {"dx": fresh(x) if dx is None else dx}
     if y is not None:
-        out["dy"] = torch.empty(x.shape, dtype=x.dtype, device=x.device) if dy is None else dy
-    for name, t in (("dr", dr), ("dn", dn), *out.items()):
-        if t is not None:
-            setattr(a, name, _ptr(t))
-            setattr(a, name + "_stride", _matrix(name, t, rows, channels, x.dtype)[2])
+        out["dy"] = fresh(x) if dy is None else dy
+    grads = [0, 0, 0, 0, 0]
     if param_grads:
-        a.grad_stride = channels
-        for name, t in (("post_weight", post_weight), ("gate", gate), ("pre_weight", pre_weight), ("scale", scale),
-                        ("shift", shift)):
+        for i, (name, t) in enumerate((("d_post_weight", post_weight), ("d_gate", gate), ("d_pre_weight", pre_weight),
+                                       ("d_scale", scale), ("d_shift", shift))):
             if t is not None:
-                out["d_" + name] = torch.empty(t.shape, dtype=t.dtype, device=t.device)
-                setattr(a, "d_" + name, _ptr(out["d_" + name]))
-    lib = load_library()
-    need = ctypes.c_int64()
-    _check(lib.rope3d_block_norm_backward_workspace(ctypes.byref(a), ctypes.byref(need)), "rope3d_block_norm_backward")
-    if workspace is None and need.value:
-        workspace = _scratch(need.value, x, stream)
-    if workspace is not None:
-        a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
-    _check(lib.rope3d_block_norm_backward(ctypes.byref(a), _stream(stream, x)), "rope3d_block_norm_backward")
+                out[name] = fresh(t)
+                grads[i] = out[name].data_ptr()
+    ptr = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
+    dx, dy = out["dx"], out.get("dy")
+    ld = [_stride(name, t, rows, channels, dt) for name, t in (("dr", dr), ("dn", dn), ("dx", dx), ("dy", dy))]
+    st = _raw_stream(stream, x)
+    args, ws = _workspace(_NormBackArgs, ((*fwd, ptr(dr), ptr(dn), dx.data_ptr(), ptr(dy), *grads, *ld, channels), ()),
+                          "rope3d_block_norm_backward_workspace", "rope3d_block_norm_backward", workspace, x, st)
+    _check(load_library().rope3d_block_norm_backward(args, st), "rope3d_block_norm_backward")
     return out
 
 
@@ -772,24 +814,16 @@ def rope3d_block_norm_last_kernel() -> int:
     return int(load_library().rope3d_block_norm_last_kernel())
 
 
-def _ffn_args(x, w_gate, w_up, w_down, y, gate_pre, up_pre, act, keep_like=None):
-    tokens, width, ldx = _matrix("x", x)
-    hidden = int(w_gate.shape[0])
-    a = _FfnArgs(x=_ptr(x), w_gate=_ptr(w_gate), w_up=_ptr(w_up), w_down=_ptr(w_down), y=_ptr(y),
-                 gate_pre=_ptr(gate_pre), up_pre=_ptr(up_pre), tokens=tokens, width=width, hidden=hidden,
-                 x_stride=ldx, w_gate_stride=_matrix("w_gate", w_gate, hidden, width, x.dtype)[2],
-                 w_up_stride=_matrix("w_up", w_up, hidden, width, x.dtype)[2],
-                 w_down_stride=_matrix("w_down", w_down, width, hidden, x.dtype)[2],
-                 y_stride=_matrix("y", y, tokens, width, x.dtype)[2],
-                 dtype=_dtype_code(x), pre_dtype=_dtype_code(x), act=int(act))
+def _pre_fields(gate_pre, up_pre, tokens, hidden, code):
+    """(row stride, dtype code) of the kept projections."""
     if (gate_pre is None) != (up_pre is None):
         raise ValueError("gate_pre and up_pre come together")
-    if gate_pre is not None:
-        a.pre_stride = _matrix("gate_pre", gate_pre, tokens, hidden)[2]
-        if _matrix("up_pre", up_pre, tokens, hidden, gate_pre.dtype)[2] != a.pre_stride:
-            raise ValueError("gate_pre and up_pre must have one row stride")
-        a.pre_dtype = _dtype_code(gate_pre)
-    return a
+    if gate_pre is None:
+        return 0, code
+    ld = _stride("gate_pre", gate_pre, tokens, hidden, gate_pre.dtype)
+    if _stride("up_pre", up_pre, tokens, hidden, gate_pre.dtype) != ld:
+        raise ValueError("gate_pre and up_pre must have one row stride")
+    return ld, _code(gate_pre)
 
 
 def rope3d_gated_ffn(x, w_gate, w_up, w_down, act: int = ACT_GELU_TANH, y=None, keep=False,
@@ -801,22 +835,24 @@ def rope3d_gated_ffn(x, w_gate, w_up, w_down, act: int = ACT_GELU_TANH, y=None, 
     (float32 or x's); gate_pre / up_pre take them instead of new tensors. Returns
     y, or (y, gate_pre, up_pre). workspace: a uint8 device tensor of at least the
     bytes the call needs (allocated when None)."""
-    import torch
-
+    torch = _use_torch()
+    tokens, width, ldx = _matrix("x", x)
+    hidden, dt, code = w_gate.shape[0], x.dtype, _code(x)
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if (keep is not False and keep is not None) and gate_pre is None and up_pre is None:
-        dt = torch.float32 if keep is True else keep
-        shape = (*x.shape[:-1], int(w_gate.shape[0]))
-        gate_pre = torch.empty(shape, dtype=dt, device=x.device)
-        up_pre = torch.empty(shape, dtype=dt, device=x.device)
-    lib = load_library()
-    a = _ffn_args(x, w_gate, w_up, w_down, y, gate_pre, up_pre, act)
-    need = ctypes.c_int64()
-    _check(lib.rope3d_gated_ffn_workspace(ctypes.byref(a), ctypes.byref(need)), "rope3d_gated_ffn")
-    ws = _scratch(need.value, x, stream) if workspace is None else workspace
-    a.workspace, a.workspace_bytes = _ptr(ws), ws.numel() * ws.element_size()
-    _check(lib.rope3d_gated_ffn(ctypes.byref(a), _stream(stream, x)), "rope3d_gated_ffn")
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    if keep is not False and keep is not None and gate_pre is None and up_pre is None:
+        shape, kept = (*x.shape[:-1], hidden), torch.float32 if keep is True else keep
+        gate_pre = torch.empty(shape, dtype=kept, device=x.device)
+        up_pre = torch.empty(shape, dtype=kept, device=x.device)
+    pre_ld, pre_code = _pre_fields(gate_pre, up_pre, tokens, hidden, code)
+    body = (x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), y.data_ptr(),
+            0 if gate_pre is None else gate_pre.data_ptr(), 0 if up_pre is None else up_pre.data_ptr(), tokens, width,
+            hidden, ldx, _stride("w_gate", w_gate, hidden, width, dt), _stride("w_up", w_up, hidden, width, dt),
+            _stride("w_down", w_down, width, hidden, dt), _stride("y", y, tokens, width, dt), pre_ld)
+    st = _raw_stream(stream, x)
+    args, ws = _workspace(_FfnArgs, (body, (code, pre_code, act)), "rope3d_gated_ffn_workspace", "rope3d_gated_ffn",
+                          workspace, x, st)
+    _check(load_library().rope3d_gated_ffn(args, st), "rope3d_gated_ffn")
     return y if gate_pre is None else (y, gate_pre, up_pre)
 
 
@@ -826,34 +862,30 @@ def rope3d_gated_ffn_backward(dy, x, w_gate, w_up, w_down, gate_pre=None, up_pre
     """The gradients of rope3d_gated_ffn: (dx, dw_gate, dw_up, dw_down). gate_pre
     and up_pre as the forward pass kept them; None computes them again. need: which
     of dx, (dw_gate, dw_up) and dw_down to compute; the others are None."""
-    import torch
+    torch = _use_torch()
+    tokens, width, ldx = _matrix("x", x)
+    hidden, dt, code = w_gate.shape[0], x.dtype, _code(x)
+    ld_w = (_stride("w_gate", w_gate, hidden, width, dt), _stride("w_up", w_up, hidden, width, dt),
+            _stride("w_down", w_down, width, hidden, dt))
+    pre_ld, pre_code = _pre_fields(gate_pre, up_pre, tokens, hidden, code)
 
-    if need[0] and dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if need[1]:
-        dw_gate = torch.empty(w_gate.shape, dtype=x.dtype, device=x.device) if dw_gate is None else dw_gate
-        dw_up = torch.empty(w_up.shape, dtype=x.dtype, device=x.device) if dw_up is None else dw_up
-    if need[2] and dw_down is None:
-        dw_down = torch.empty(w_down.shape, dtype=x.dtype, device=x.device)
-    dx, dw_gate, dw_up, dw_down = (t if n else None for t, n in
-                                   ((dx, need[0]), (dw_gate, need[1]), (dw_up, need[1]), (dw_down, need[2])))
-    f = _ffn_args(x, w_gate, w_up, w_down, x, gate_pre, up_pre, act)
-    M, D, F = f.tokens, f.width, f.hidden
-    ld = lambda name, t, r, c: 0 if t is None else _matrix(name, t, r, c, x.dtype)[2]  # noqa: E731
-    a = _FfnBackArgs(dy=_ptr(dy), x=f.x, w_gate=f.w_gate, w_up=f.w_up, w_down=f.w_down, gate_pre=f.gate_pre,
-                     up_pre=f.up_pre, dx=_ptr(dx), dw_gate=_ptr(dw_gate), dw_up=_ptr(dw_up),
-                     dw_down=_ptr(dw_down), tokens=M, width=D, hidden=F, dy_stride=ld("dy", dy, M, D),
-                     x_stride=f.x_stride, w_gate_stride=f.w_gate_stride, w_up_stride=f.w_up_stride,
-                     w_down_stride=f.w_down_stride, pre_stride=f.pre_stride, dx_stride=ld("dx", dx, M, D),
-                     dw_gate_stride=ld("dw_gate", dw_gate, F, D), dw_up_stride=ld("dw_up", dw_up, F, D),
-                     dw_down_stride=ld("dw_down", dw_down, D, F), dtype=f.dtype, pre_dtype=f.pre_dtype, act=f.act)
-    lib = load_library()
-    nb = ctypes.c_int64()
-    _check(lib.rope3d_gated_ffn_backward_workspace(ctypes.byref(a), ctypes.byref(nb)), "rope3d_gated_ffn_backward")
-    ws = _scratch(nb.value, x, stream) if workspace is None else workspace
-    a.workspace, a.workspace_bytes = _ptr(ws), ws.numel() * ws.element_size()
-    _check(lib.rope3d_gated_ffn_backward(ctypes.byref(a), _stream(stream, x)), "rope3d_gated_ffn_backward")
-    return dx, dw_gate, dw_up, dw_down
+    def out(wanted, given, like):
+        return None if not wanted else torch.empty_like(like, memory_format=torch.contiguous_format) \
+            if given is None else given
+
+    grads = (out(need[0], dx, x), out(need[1], dw_gate, w_gate), out(need[1], dw_up, w_up),
+             out(need[2], dw_down, w_down))
+    ptr = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
+    ld_g = (_stride("dx", grads[0], tokens, width, dt), _stride("dw_gate", grads[1], hidden, width, dt),
+            _stride("dw_up", grads[2], hidden, width, dt), _stride("dw_down", grads[3], width, hidden, dt))
+    body = (dy.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), ptr(gate_pre),
+            ptr(up_pre), *map(ptr, grads), tokens, width, hidden, _stride("dy", dy, tokens, width, dt), ldx, *ld_w,
+            pre_ld, *ld_g)
+    st = _raw_stream(stream, x)
+    args, ws = _workspace(_FfnBackArgs, (body, (code, pre_code, act)), "rope3d_gated_ffn_backward_workspace",
+                          "rope3d_gated_ffn_backward", workspace, x, st)
+    _check(load_library().rope3d_gated_ffn_backward(args, st), "rope3d_gated_ffn_backward")
+    return grads
 
 
 def rope3d_gated_ffn_check(check_device: bool = False, **fields) -> str:
