@@ -500,9 +500,14 @@ int rope3d_block_norm_backward(const rope3d_block_norm_backward_args *args, void
 int rope3d_block_norm_backward_check(const rope3d_block_norm_backward_args *args, int32_t check_device);
 int rope3d_block_norm_backward_workspace(const rope3d_block_norm_backward_args *args, int64_t *bytes);
 
-/* Which kernel this thread's last norm call used: 1 the vector kernel (rows in
- * registers), 2 the general one, 0 none yet. */
+/* Which kernel this thread's last norm call used: 1 rows in registers, 2 the
+ * general one (any size and alignment), 3 rows through a ring in shared memory
+ * (many rows), 0 none yet. */
 int rope3d_block_norm_last_kernel(void);
+/* How many bounded waits of the norms' ring kernels ran out (0 unless something
+ * is badly wrong; such a launch's output is not to be used); reset clears the
+ * count. Synchronises with the device. Errors: NULL, CUDA. */
+int rope3d_testing_norm_wait_timeouts(int64_t *count, int32_t reset);
 
 /*
  * rope3d_gated_ffn -- the gated feed-forward of a transformer block:

@@ -40,6 +40,7 @@ __all__ = [
     "rope3d_gated_ffn_backward_check", "rope3d_gated_ffn_last_kernel",
     "rope3d_testing_ffn_wait_timeouts", "rope3d_block_norm", "rope3d_block_norm_backward",
     "rope3d_block_norm_check", "rope3d_block_norm_backward_check", "rope3d_block_norm_last_kernel",
+    "rope3d_testing_norm_wait_timeouts",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -160,6 +161,7 @@ def _declare(lib):
         "rope3d_block_norm_backward_check": ([vp, i32], c.c_int),
         "rope3d_block_norm_backward_workspace": ([vp, vp], c.c_int),
         "rope3d_block_norm_last_kernel": ([], c.c_int),
+        "rope3d_testing_norm_wait_timeouts": ([vp, i32], c.c_int),
         "rope3d_gated_ffn": ([vp, vp], c.c_int),
         "rope3d_gated_ffn_check": ([vp, i32], c.c_int),
         "rope3d_gated_ffn_workspace": ([vp, vp], c.c_int),
@@ -810,8 +812,17 @@ def rope3d_block_norm_backward_check(check_device: bool = False, **fields) -> st
 
 
 def rope3d_block_norm_last_kernel() -> int:
-    """Kernel of this thread's last norm call: 1 rows in registers, 2 the general one."""
+    """Kernel of this thread's last norm call: 1 rows in registers, 2 the general one, 3
+    rows through shared memory (many rows)."""
     return int(load_library().rope3d_block_norm_last_kernel())
+
+
+def rope3d_testing_norm_wait_timeouts(reset: bool = True) -> int:
+    """Bounded waits of the norms' kernels that ran out (0 in a sound run)."""
+    n = ctypes.c_int64()
+    _check(load_library().rope3d_testing_norm_wait_timeouts(ctypes.byref(n), 1 if reset else 0),
+           "rope3d_testing_norm_wait_timeouts")
+    return int(n.value)
 
 
 def _pre_fields(gate_pre, up_pre, tokens, hidden, code):

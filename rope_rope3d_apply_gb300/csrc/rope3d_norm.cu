@@ -36,8 +36,20 @@
 
 #include "../../include/rope3d.h"
 #include "rope3d_internal.h"
+#include "rope3d_tc.cuh"
 
 namespace {
+
+using rope3d_tc::grid_release;
+using rope3d_tc::grid_wait;
+using rope3d_tc::mbar_expect_tx;
+using rope3d_tc::mbar_fence_init;
+using rope3d_tc::mbar_init;
+using rope3d_tc::mbar_wait;
+using rope3d_tc::smem_u32;
+
+// Bounded waits that ran out (rope3d_testing_norm_wait_timeouts).
+__device__ unsigned int g_norm_wait_timeouts;
 
 struct NormParams {
     const void *x, *y, *post_weight, *gate, *pre_weight, *scale, *shift;
@@ -55,12 +67,8 @@ struct NormParams {
     float *stats;         // general kernels: [rows][6]
     int chunk_rows, chunks_per_group, groups_per_chunk, chunks;
     int sums;             // column sums are wanted
+    int stages;           // ring kernels: rows in shared memory
 };
-
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_release() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
 
 // ---- elements -------------------------------------------------------------------
 
@@ -624,6 +632,590 @@ block_norm_back_vec_kernel(const __grid_constant__ NormParams p) {
     }
 }
 
+// ---- many rows: rows through a ring in shared memory -------------------------------------------
+//
+// A row's bytes have to arrive before its statistics, and its statistics before
+// its results, so a team that loads a row when it gets to it waits for memory in
+// every row. Here one thread keeps a ring of whole rows on the way into shared
+// memory (bulk copies that complete on an mbarrier), a few rows ahead of the
+// team, and several teams share an SM. Forward, a block takes a contiguous range
+// of rows; backward, one chunk. Of the parameters a row needs only
+//   m = gate * wp,  q = wq * (1 + scale)  (and shift, forward),
+// which stay in shared memory until the group changes. A thread owns 16 channels
+// and works on pairs of them with packed fp32 arithmetic: the kernels would
+// otherwise be bound by instruction issue, not by memory.
+constexpr int kRingE = 16;
+constexpr int kRingBars = 8;   // most stages
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long x, y, z, d;
+    memcpy(&x, &a, 8);
+    memcpy(&y, &b, 8);
+    memcpy(&z, &c, 8);
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
+    memcpy(&a, &d, 8);
+    return a;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    unsigned long long x, y, d;
+    memcpy(&x, &a, 8);
+    memcpy(&y, &b, 8);
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+    memcpy(&a, &d, 8);
+    return a;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    unsigned long long x, y, d;
+    memcpy(&x, &a, 8);
+    memcpy(&y, &b, 8);
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+    memcpy(&a, &d, 8);
+    return a;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+template <int kT>
+__device__ __forceinline__ void unpack2(const uint4 &v, float2 *f) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (kT == ROPE3D_F32) {
+        f[0] = make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+        f[1] = make_float2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (kT == ROPE3D_BF16) {
+                f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+            } else {
+                __half2 h;
+                memcpy(&h, &w[i], 4);
+                f[i] = __half22float2(h);
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void bulk_row(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+
+// This thread's 16 values of one fp32 array in shared memory: 16-byte pieces,
+// each piece contiguous over the threads.
+struct Kept {
+    uint32_t base;   // + this thread's 16 bytes
+    uint32_t step;   // bytes of one piece of all threads
+    __device__ __forceinline__ void load(float2 *f) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint4 v = lds128(base + uint32_t(i) * step);
+            f[2 * i] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+            f[2 * i + 1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+        }
+    }
+    __device__ __forceinline__ void store(const float *f) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(base + uint32_t(i) * step), "f"(f[4 * i]),
+                         "f"(f[4 * i + 1]), "f"(f[4 * i + 2]), "f"(f[4 * i + 3]) : "memory");
+    }
+};
+
+// Sums over a block of kN values a thread, like Sums; the second step adds the
+// warps' sums in order, read as vectors.
+template <int kN>
+struct BlockSums {
+    float *red;   // [2][kN][16]
+    int slot, warps;
+    __device__ __forceinline__ void operator()(float *v) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < kN; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        float *s = red + slot * kN * 16;
+        slot ^= 1;
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int i = 0; i < kN; ++i) s[i * 16 + (threadIdx.x >> 5)] = v[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            v[i] = 0.0f;
+            for (int w = 0; w < warps; w += 4) {   // slots past the last warp stay zero
+                const float4 t = *reinterpret_cast<const float4 *>(s + i * 16 + w);
+                v[i] += (t.x + t.y) + (t.z + t.w);
+            }
+        }
+    }
+};
+
+struct Ring {
+    uint32_t base, bars, row_bytes, stage_bytes;
+    int stages;
+    // Thread 0: the rows of up to four arrays into stage s.
+    __device__ __forceinline__ void fill(int s, const void *const *src, int streams) const {
+        const uint32_t bar = bars + 8u * uint32_t(s);
+        mbar_expect_tx(bar, row_bytes * uint32_t(streams));
+        for (int i = 0; i < streams; ++i) bulk_row(base + uint32_t(s) * stage_bytes + uint32_t(i) * row_bytes, src[i], row_bytes, bar);
+    }
+};
+
+// One element pair's worth of statistics of v (pairs of 16 elements a thread):
+// mean (layer) and 1 / std.
+template <int kVecs, int kN>
+__device__ __forceinline__ void ring_stats(const float2 *v, int kind, const bool *real, float inv_c, float eps,
+                                           BlockSums<kN> &sum, float *mean, float *k) {
+    constexpr int P = kRingE / 2 / kVecs;   // pairs of a vector
+    *mean = 0.0f;
+    *k = 1.0f;
+    if (kind == ROPE3D_NORM_NONE) return;
+    float s[kN] = {};
+    if (kind == ROPE3D_NORM_LAYER) {
+        float2 t = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < kRingE / 2; ++i) t = add2(t, v[i]);
+        s[0] = t.x + t.y;
+        sum(s);
+        *mean = s[0] * inv_c;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) s[i] = 0.0f;
+    }
+    float2 t = make_float2(0.0f, 0.0f);
+    const float2 m = both(-*mean);
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j)
+        if (real[j])
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const float2 d = add2(v[j * P + i], m);
+                t = fma2(d, d, t);
+            }
+    s[0] = t.x + t.y;
+    sum(s);
+    *k = rsqrtf(s[0] * inv_c + eps);
+}
+
+template <int kT>
+__global__ void __launch_bounds__(512) block_norm_ring_kernel(const __grid_constant__ NormParams p) {
+    constexpr int V = kPer<kT>, kVecs = kRingE / V, P = V / 2, kBytes = 16 / V;
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(16) float red[2 * 16];
+    __shared__ __align__(8) unsigned long long bars[kRingBars];
+    const int size = int(blockDim.x), tid = int(threadIdx.x);
+    const uint32_t base = (smem_u32(raw) + 127u) & ~127u;
+    const uint32_t row_bytes = uint32_t(p.channels) * kBytes;
+    const int streams = p.y ? 2 : 1;
+    const Ring ring{base + uint32_t(size) * 3 * 64, smem_u32(bars), row_bytes, row_bytes * uint32_t(streams), p.stages};
+    const Kept km{base + 16u * uint32_t(tid), 16u * uint32_t(size)}, kq{km.base + 4 * km.step, km.step},
+        ks{kq.base + 4 * km.step, km.step};
+    BlockSums<1> sum{red, 0, (size + 31) >> 5};
+    const int n_vec = p.channels / V;
+    const float inv_c = 1.0f / float(p.channels);
+    bool real[kVecs];
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) real[j] = tid + j * size < n_vec;
+    for (int i = tid; i < 2 * 16; i += size) red[i] = 0.0f;
+    if (tid == 0) {
+        for (int s = 0; s < p.stages; ++s) mbar_init(ring.bars + 8u * uint32_t(s), 1);
+        mbar_fence_init();
+    }
+    __syncthreads();
+    grid_wait();
+    grid_release();
+    const long long lo = (long long)p.rows * blockIdx.x / gridDim.x, hi = (long long)p.rows * (blockIdx.x + 1) / gridDim.x;
+    auto fill = [&](int s, long long row) {
+        const void *src[2] = {static_cast<const char *>(p.x) + row * p.ldx * kBytes,
+                              static_cast<const char *>(p.y) + row * p.ldy * kBytes};
+        ring.fill(s, src, streams);
+    };
+    if (tid == 0)
+        for (int s = 0; s < p.stages && lo + s < hi; ++s) fill(s, lo + s);
+    bool dead = false;
+    int g = int(uint32_t(lo) / uint32_t(p.rows_per_group)) - 1;
+    long long group_end = lo;   // the first row starts a group
+    for (long long row = lo; row < hi; ++row) {
+        if (row == group_end) {
+            ++g;
+            group_end = (long long)(g + 1) * p.rows_per_group;
+            float m[kRingE], q[kRingE], sh[kRingE];
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
+                const int c = real[j] ? (tid + j * size) * V : 0;
+                float a[V];
+                ld_weight<kT>(p.post_weight, c, p.param_f32, p.offset, m + j * V);
+                ld_param<kT>(p.gate, g * p.ldg + c, p.param_f32, 1.0f, a);
+#pragma unroll
+                for (int i = 0; i < V; ++i) m[j * V + i] *= a[i];
+                ld_weight<kT>(p.pre_weight, c, p.param_f32, p.offset, q + j * V);
+                ld_param<kT>(p.scale, g * p.ldsc + c, p.param_f32, 0.0f, a);
+#pragma unroll
+                for (int i = 0; i < V; ++i) q[j * V + i] *= 1.0f + a[i];
+                ld_param<kT>(p.shift, g * p.ldsh + c, p.param_f32, 0.0f, sh + j * V);
+            }
+            km.store(m);   // read back by this thread alone
+            kq.store(q);
+            ks.store(sh);
+        }
+        const int s = int((row - lo) % p.stages);
+        mbar_wait(ring.bars + 8u * uint32_t(s), uint32_t((row - lo) / p.stages) & 1u, dead, &g_norm_wait_timeouts);
+        const uint32_t at = ring.base + uint32_t(s) * ring.stage_bytes + 16u * uint32_t(tid);
+        float2 v[kRingE / 2];
+        uint4 yv[kVecs];
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+            uint4 xv = make_uint4(0, 0, 0, 0);
+            yv[j] = xv;
+            if (real[j]) {
+                xv = lds128(at + uint32_t(j * size) * 16u);
+                if (p.y) yv[j] = lds128(at + row_bytes + uint32_t(j * size) * 16u);
+            }
+            unpack2<kT>(xv, v + j * P);
+        }
+        bool synced = false;   // every thread has read its part of the stage
+        const float2 res = both(p.res);
+        if (p.y) {
+            float2 y[kRingE / 2];
+            float mean, k;
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) unpack2<kT>(yv[j], y + j * P);
+            ring_stats<kVecs>(y, p.post, real, inv_c, p.eps, sum, &mean, &k);
+            synced = p.post != ROPE3D_NORM_NONE;
+            float2 m[kRingE / 2];
+            km.load(m);
+            const float2 k2 = both(k), mk = both(-mean * k);
+#pragma unroll
+            for (int i = 0; i < kRingE / 2; ++i) v[i] = fma2(m[i], fma2(y[i], k2, mk), mul2(res, v[i]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < kRingE / 2; ++i) v[i] = mul2(res, v[i]);
+        }
+        if (p.n && p.pre != ROPE3D_NORM_NONE) {
+            // absent channels of a layer norm's y are not zero any more
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j)
+                if (!real[j])
+#pragma unroll
+                    for (int i = 0; i < P; ++i) v[j * P + i] = make_float2(0.0f, 0.0f);
+        }
+        if (p.r) {
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j)
+                if (real[j])
+                    st_row(p.r, row * p.ldr + (tid + j * size) * V, kBytes, pack<kT>(reinterpret_cast<const float *>(v + j * P)));
+        }
+        if (p.n) {
+            float mean, k;
+            ring_stats<kVecs>(v, p.pre, real, inv_c, p.eps, sum, &mean, &k);
+            synced = synced || p.pre != ROPE3D_NORM_NONE;
+            float2 q[kRingE / 2], sh[kRingE / 2];
+            kq.load(q);
+            ks.load(sh);
+            const float2 k2 = both(k), mk = both(-mean * k);
+#pragma unroll
+            for (int i = 0; i < kRingE / 2; ++i) v[i] = fma2(fma2(v[i], k2, mk), q[i], sh[i]);
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j)
+                if (real[j])
+                    st_row(p.n, row * p.ldn + (tid + j * size) * V, kBytes, pack<kT>(reinterpret_cast<const float *>(v + j * P)));
+        }
+        if (!synced) __syncthreads();
+        if (tid == 0 && row + p.stages < hi && !dead) fill(s, row + p.stages);
+    }
+}
+
+template <int kT>
+__global__ void __launch_bounds__(512) block_norm_back_ring_kernel(const __grid_constant__ NormParams p) {
+    constexpr int V = kPer<kT>, kVecs = kRingE / V, P = V / 2, H = kRingE / 2, kBytes = 16 / V;
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(16) float red[2 * 2 * 16];
+    __shared__ __align__(8) unsigned long long bars[kRingBars];
+    const int size = int(blockDim.x), tid = int(threadIdx.x);
+    const uint32_t base = (smem_u32(raw) + 127u) & ~127u;
+    const uint32_t row_bytes = uint32_t(p.channels) * kBytes;
+    // the arrays that a stage holds, in this order
+    const int at_y = 1, at_n = 1 + (p.y != nullptr), at_r = at_n + (p.dn != nullptr);
+    const int streams = at_r + (p.dr != nullptr);
+    // m, q and, where a chunk is whole groups, the weights' sums
+    const Ring ring{base + uint32_t(size) * (p.groups_per_chunk ? 4 : 2) * 64, smem_u32(bars), row_bytes,
+                    row_bytes * uint32_t(streams), p.stages};
+    const Kept km{base + 16u * uint32_t(tid), 16u * uint32_t(size)}, kq{km.base + 4 * km.step, km.step},
+        kwq{kq.base + 4 * km.step, km.step}, kwp{kwq.base + 4 * km.step, km.step};
+    BlockSums<2> sum{red, 0, (size + 31) >> 5};
+    const int n_vec = p.channels / V;
+    const float inv_c = 1.0f / float(p.channels);
+    bool real[kVecs];
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) real[j] = tid + j * size < n_vec;
+    for (int i = tid; i < 2 * 2 * 16; i += size) red[i] = 0.0f;
+    if (tid == 0) {
+        for (int s = 0; s < p.stages; ++s) mbar_init(ring.bars + 8u * uint32_t(s), 1);
+        mbar_fence_init();
+    }
+    __syncthreads();
+    grid_wait();
+    grid_release();
+    const int chunk = int(blockIdx.x);
+    long long lo, hi;
+    chunk_range(p, chunk, &lo, &hi);
+    auto fill = [&](int s, long long row) {
+        const void *src[4];
+        src[0] = static_cast<const char *>(p.x) + row * p.ldx * kBytes;
+        if (p.y) src[at_y] = static_cast<const char *>(p.y) + row * p.ldy * kBytes;
+        if (p.dn) src[at_n] = static_cast<const char *>(p.dn) + row * p.lddn * kBytes;
+        if (p.dr) src[at_r] = static_cast<const char *>(p.dr) + row * p.lddr * kBytes;
+        ring.fill(s, src, streams);
+    };
+    if (tid == 0)
+        for (int s = 0; s < p.stages && lo + s < hi; ++s) fill(s, lo + s);
+    bool dead = false;
+    const float2 zero = make_float2(0.0f, 0.0f), res = both(p.res);
+    float2 S[H], T[H], U[H];
+#pragma unroll
+    for (int i = 0; i < H; ++i) S[i] = T[i] = U[i] = zero;
+    if (p.groups_per_chunk) {
+        float z[kRingE] = {};
+        kwq.store(z);
+        kwp.store(z);
+    }
+    int g = int(uint32_t(lo) / uint32_t(p.rows_per_group)) - 1;
+    long long group_end = lo;
+    for (long long row = lo; row < hi; ++row) {
+        if (row == group_end) {
+            ++g;
+            group_end = (long long)(g + 1) * p.rows_per_group;
+            float m[kRingE], q[kRingE];
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
+                const int c = real[j] ? (tid + j * size) * V : 0;
+                float a[V];
+                ld_weight<kT>(p.post_weight, c, p.param_f32, p.offset, m + j * V);
+                ld_param<kT>(p.gate, g * p.ldg + c, p.param_f32, 1.0f, a);
+#pragma unroll
+                for (int i = 0; i < V; ++i) m[j * V + i] = real[j] ? m[j * V + i] * a[i] : 0.0f;
+                ld_weight<kT>(p.pre_weight, c, p.param_f32, p.offset, q + j * V);
+                ld_param<kT>(p.scale, g * p.ldsc + c, p.param_f32, 0.0f, a);
+#pragma unroll
+                for (int i = 0; i < V; ++i) q[j * V + i] = real[j] ? q[j * V + i] * (1.0f + a[i]) : 0.0f;
+            }
+            km.store(m);   // zero for absent channels: they drop out of every sum
+            kq.store(q);
+        }
+        const int s = int((row - lo) % p.stages);
+        mbar_wait(ring.bars + 8u * uint32_t(s), uint32_t((row - lo) / p.stages) & 1u, dead, &g_norm_wait_timeouts);
+        const uint32_t at = ring.base + uint32_t(s) * ring.stage_bytes + 16u * uint32_t(tid);
+        auto read = [&](int stream, int j) {
+            return real[j] ? lds128(at + uint32_t(stream) * row_bytes + uint32_t(j * size) * 16u) : make_uint4(0, 0, 0, 0);
+        };
+        float my = 0.0f, ky = 1.0f;
+        float2 r[H], e[H];
+        uint4 yv[kVecs];
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) yv[j] = make_uint4(0, 0, 0, 0);
+        if (p.y) {
+            float2 y[H];
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
+                yv[j] = read(at_y, j);
+                unpack2<kT>(yv[j], y + j * P);
+            }
+            ring_stats<kVecs>(y, p.post, real, inv_c, p.eps, sum, &my, &ky);
+        }
+        const float2 ky2 = both(ky), myk = both(-my * ky);
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+            unpack2<kT>(read(0, j), r + j * P);
+            if (p.dn) unpack2<kT>(read(at_n, j), e + j * P);
+            else
+#pragma unroll
+                for (int i = 0; i < P; ++i) e[j * P + i] = zero;
+        }
+        {
+            float2 q[H];
+            kq.load(q);
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                r[i] = mul2(res, r[i]);
+                e[i] = mul2(e[i], q[i]);
+            }
+        }
+        if (p.y) {
+            float2 m[H];
+            km.load(m);
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
+                float2 y[P];
+                unpack2<kT>(yv[j], y);
+#pragma unroll
+                for (int i = 0; i < P; ++i) r[j * P + i] = fma2(m[j * P + i], fma2(y[i], ky2, myk), r[j * P + i]);
+            }
+        }
+        float mr = 0.0f, kr = 1.0f, me = 0.0f, mez = 0.0f;
+        if (p.pre != ROPE3D_NORM_NONE) {
+            float t[2];
+            if (p.pre == ROPE3D_NORM_LAYER) {
+                float2 a = zero, b = zero;
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    a = add2(a, r[i]);
+                    b = add2(b, e[i]);
+                }
+                t[0] = a.x + a.y;
+                t[1] = b.x + b.y;
+                sum(t);
+                mr = t[0] * inv_c;
+                me = t[1] * inv_c;
+            }
+            float2 a = zero, b = zero;
+            const float2 nm = both(-mr);
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j)
+                if (real[j])
+#pragma unroll
+                    for (int i = 0; i < P; ++i) {
+                        const float2 d = add2(r[j * P + i], nm);
+                        a = fma2(d, d, a);
+                        b = fma2(d, e[j * P + i], b);
+                    }
+            t[0] = a.x + a.y;
+            t[1] = b.x + b.y;
+            sum(t);
+            kr = rsqrtf(t[0] * inv_c + p.eps);
+            mez = t[1] * inv_c * kr;
+        }
+        // e becomes the whole gradient of r, and r becomes f
+        {
+            const bool plain = p.pre == ROPE3D_NORM_NONE;
+            const float2 kr2 = both(kr), mrk = both(-mr * kr), nme = both(plain ? 0.0f : -me), nmez = both(plain ? 0.0f : -mez);
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
+                float2 dn[P], dr[P];
+                if (p.dn) unpack2<kT>(read(at_n, j), dn);
+                if (p.dr) unpack2<kT>(read(at_r, j), dr);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const int x = j * P + i;
+                    if (!p.dn) dn[i] = zero;
+                    if (!p.dr) dr[i] = zero;
+                    const float2 z = fma2(r[x], kr2, mrk);
+                    S[x] = fma2(dn[i], z, S[x]);
+                    T[x] = add2(T[x], dn[i]);
+                    e[x] = fma2(kr2, fma2(z, nmez, add2(e[x], nme)), dr[i]);
+                }
+                if (real[j]) {
+                    float2 o[P];
+#pragma unroll
+                    for (int i = 0; i < P; ++i) o[i] = mul2(res, e[j * P + i]);
+                    st_row(p.dx, row * p.lddx + (tid + j * size) * V, kBytes, pack<kT>(reinterpret_cast<const float *>(o)));
+                }
+            }
+        }
+        if (p.y) {
+            float2 m[H], a = zero, b = zero;
+            km.load(m);
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
+                float2 y[P];
+                unpack2<kT>(yv[j], y);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const int x = j * P + i;
+                    const float2 yh = fma2(y[i], ky2, myk);
+                    U[x] = fma2(e[x], yh, U[x]);
+                    r[x] = mul2(e[x], m[x]);   // m is zero for absent channels
+                    a = add2(a, r[x]);
+                    b = fma2(r[x], yh, b);
+                }
+            }
+            float t[2] = {a.x + a.y, b.x + b.y};
+            if (p.post != ROPE3D_NORM_NONE) sum(t);
+            else __syncthreads();
+            if (tid == 0 && row + p.stages < hi && !dead) fill(s, row + p.stages);
+            const bool plain = p.post == ROPE3D_NORM_NONE;
+            const float2 nmf = both(p.post == ROPE3D_NORM_LAYER ? -t[0] * inv_c : 0.0f), nmfy = both(plain ? 0.0f : -t[1] * inv_c);
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
+                if (!real[j]) continue;
+                float2 y[P], o[P];
+                unpack2<kT>(yv[j], y);
+#pragma unroll
+                for (int i = 0; i < P; ++i)
+                    o[i] = plain ? r[j * P + i]
+                                 : mul2(ky2, fma2(fma2(y[i], ky2, myk), nmfy, add2(r[j * P + i], nmf)));
+                st_row(p.dy, row * p.lddy + (tid + j * size) * V, kBytes, pack<kT>(reinterpret_cast<const float *>(o)));
+            }
+        } else {
+            __syncthreads();
+            if (tid == 0 && row + p.stages < hi && !dead) fill(s, row + p.stages);
+        }
+        if (p.groups_per_chunk && p.sums && (row + 1 == group_end || row + 1 == hi)) {
+            // a whole group is done: its gradients, and its part of the weights'
+            float wq[kRingE], wp[kRingE];
+            float2 t[H];
+            kwq.load(t);
+            memcpy(wq, t, sizeof(wq));
+            kwp.load(t);
+            memcpy(wp, t, sizeof(wp));
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
+                const int c = real[j] ? (tid + j * size) * V : 0;
+                const float *Sj = reinterpret_cast<const float *>(S + j * P), *Uj = reinterpret_cast<const float *>(U + j * P);
+                float a[V], o[V];
+                if (p.d_scale && real[j]) {
+                    ld_weight<kT>(p.pre_weight, c, p.param_f32, p.offset, a);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) o[i] = a[i] * Sj[i];
+                    st_param<kT>(p.d_scale, g * p.ldgrad + c, p.param_f32, o);
+                }
+                if (p.d_shift && real[j])
+                    st_param<kT>(p.d_shift, g * p.ldgrad + c, p.param_f32, reinterpret_cast<const float *>(T + j * P));
+                if (p.d_gate && real[j]) {
+                    ld_weight<kT>(p.post_weight, c, p.param_f32, p.offset, a);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) o[i] = a[i] * Uj[i];
+                    st_param<kT>(p.d_gate, g * p.ldgrad + c, p.param_f32, o);
+                }
+                ld_param<kT>(p.scale, g * p.ldsc + c, p.param_f32, 0.0f, a);
+#pragma unroll
+                for (int i = 0; i < V; ++i) wq[j * V + i] += (1.0f + a[i]) * Sj[i];
+                ld_param<kT>(p.gate, g * p.ldg + c, p.param_f32, 1.0f, a);
+#pragma unroll
+                for (int i = 0; i < V; ++i) wp[j * V + i] += a[i] * Uj[i];
+            }
+            kwq.store(wq);
+            kwp.store(wp);
+#pragma unroll
+            for (int i = 0; i < H; ++i) S[i] = T[i] = U[i] = zero;
+        }
+    }
+    if (p.part) {
+        if (p.groups_per_chunk) {
+            kwq.load(S);
+            kwp.load(U);
+        }
+        float *dst = p.part + (long long)chunk * 3 * p.channels;
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+            if (!real[j]) continue;
+            const int c = (tid + j * size) * V;
+#pragma unroll
+            for (int i = 0; i < P; i += 2) {
+                *reinterpret_cast<float4 *>(dst + c + 2 * i) =
+                    make_float4(S[j * P + i].x, S[j * P + i].y, S[j * P + i + 1].x, S[j * P + i + 1].y);
+                *reinterpret_cast<float4 *>(dst + p.channels + c + 2 * i) =
+                    make_float4(T[j * P + i].x, T[j * P + i].y, T[j * P + i + 1].x, T[j * P + i + 1].y);
+                *reinterpret_cast<float4 *>(dst + 2 * p.channels + c + 2 * i) =
+                    make_float4(U[j * P + i].x, U[j * P + i].y, U[j * P + i + 1].x, U[j * P + i + 1].y);
+            }
+        }
+    }
+}
+
 // ---- backward, any row: dx, dy and the rows' statistics, then the columns --------------------
 
 __global__ void __launch_bounds__(kGeneralThreads) block_norm_back_any_kernel(const __grid_constant__ NormParams p) {
@@ -969,6 +1561,38 @@ NormFn backward_fn(const Team &t) {
     }
 }
 
+// The ring kernels' shape for rows of `channels` elements of es bytes: threads of
+// a block, blocks an SM, stages (0: the rows do not fit).
+struct RingShape {
+    int threads, per_sm, stages, smem;
+};
+
+RingShape ring_shape(int64_t channels, int es, int streams, int kept, int threads_per_sm) {
+    RingShape r{};
+    r.threads = int(up((channels + kRingE - 1) / kRingE, 32));
+    if (r.threads > 512) return r;
+    const int stage = int(channels) * es * streams, keep = r.threads * 64 * kept;
+    for (r.per_sm = threads_per_sm / r.threads; r.per_sm >= 1; --r.per_sm) {
+        r.stages = std::min(kRingBars, (227 * 1024 / r.per_sm - 1024 - 1024 - keep - 128) / stage);
+        if (r.stages >= 2) break;
+    }
+    if (r.stages < 2) r.stages = 0;
+    r.stages = std::min(r.stages, 4);
+    r.smem = keep + r.stages * stage + 128;
+    return r;
+}
+
+template <typename Fn>
+int launch_ring(Fn fn, unsigned grid, const RingShape &shape, NormParams &p, cudaStream_t st) {
+    p.stages = shape.stages;
+    if (shape.smem > 48 * 1024 &&
+        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024) != cudaSuccess) {
+        cudaGetLastError();
+        return ROPE3D_ERR_CUDA;
+    }
+    return launch(fn, dim3(grid), dim3(unsigned(shape.threads)), size_t(shape.smem), p, st);
+}
+
 int forward(const rope3d_block_norm_args *a, bool run, bool check_device, cudaStream_t st) {
     if (!a || (!a->r && !a->n)) return ROPE3D_ERR_NULL;
     NormParams p;
@@ -999,6 +1623,14 @@ int forward(const rope3d_block_norm_args *a, bool run, bool check_device, cudaSt
         t_norm_kernel = 2;
         return launch(block_norm_any_kernel, dim3(unsigned(std::min<int64_t>(R, int64_t(sms) * 8))),
                       dim3(kGeneralThreads), 0, p, st);
+    }
+    const RingShape shape = ring_shape(C, es, a->y ? 2 : 1, 3, 896);   // 64-66 registers a thread
+    if (shape.stages && R >= int64_t(kSms) * shape.per_sm * 2) {
+        t_norm_kernel = 3;
+        const NormFn fn = a->dtype == ROPE3D_BF16 ? block_norm_ring_kernel<ROPE3D_BF16>
+                          : a->dtype == ROPE3D_F16 ? block_norm_ring_kernel<ROPE3D_F16>
+                                                   : block_norm_ring_kernel<ROPE3D_F32>;
+        return launch_ring(fn, unsigned(sms * shape.per_sm), shape, p, st);
     }
     t_norm_kernel = 1;
     const NormFn fn = a->dtype == ROPE3D_BF16 ? forward_fn<ROPE3D_BF16>(t)
@@ -1060,10 +1692,14 @@ int backward(const rope3d_block_norm_backward_args *a, bool run, bool check_devi
     p.ldgrad = a->grad_stride;
     p.sums = group_grads || a->d_post_weight || a->d_pre_weight;
     const Team t = vectors(all, 16, C, vec) ? backward_team(C / vec, vec) : Team{0, 0, false};
-    // Chunks: about as many as the GPU runs teams at once (two blocks an SM, or
-    // the general kernel's column blocks), each of whole groups or a part of one.
+    const int streams = 1 + (f.y != nullptr) + (a->dn != nullptr) + (a->dr != nullptr);
+    const RingShape shape = ring_shape(C, es, streams, 4, 512);   // 128 registers a thread
+    const bool ring = t.vecs && shape.stages && R >= kSms * shape.per_sm * 2;
+    // Chunks: about as many as the GPU runs teams at once (or the general
+    // kernel's column blocks), each of whole groups or a part of one.
     const int64_t target =
-        t.vecs ? (t.warp ? kSms * 16 : kSms * (t.threads > 256 ? 2 : t.threads > 128 ? 4 : 8))
+        ring     ? kSms * shape.per_sm
+        : t.vecs ? (t.warp ? kSms * 16 : kSms * (t.threads > 256 ? 2 : t.threads > 128 ? 4 : 8))
                : std::max<int64_t>(1, kSms * 8 / ((C + kGeneralThreads - 1) / kGeneralThreads));
     const int64_t L = std::max<int64_t>(1, (R + target - 1) / target), rpg = p.rows_per_group;
     if (rpg >= L) {
@@ -1097,7 +1733,14 @@ int backward(const rope3d_block_norm_backward_args *a, bool run, bool check_devi
     if (rc != ROPE3D_OK || !run) return rc;
     char *ws = static_cast<char *>(a->workspace);
     p.part = partial ? reinterpret_cast<float *>(ws) : nullptr;
-    if (t.vecs) {
+    if (ring) {
+        t_norm_kernel = 3;
+        const NormFn fn = f.dtype == ROPE3D_BF16 ? block_norm_back_ring_kernel<ROPE3D_BF16>
+                          : f.dtype == ROPE3D_F16 ? block_norm_back_ring_kernel<ROPE3D_F16>
+                                                  : block_norm_back_ring_kernel<ROPE3D_F32>;
+        rc = launch_ring(fn, unsigned(p.chunks), shape, p, st);
+        if (rc != ROPE3D_OK) return rc;
+    } else if (t.vecs) {
         t_norm_kernel = 1;
         const NormFn fn = f.dtype == ROPE3D_BF16 ? backward_fn<ROPE3D_BF16>(t)
                           : f.dtype == ROPE3D_F16 ? backward_fn<ROPE3D_F16>(t)
@@ -1152,3 +1795,21 @@ extern "C" int rope3d_block_norm_backward_workspace(const rope3d_block_norm_back
 }
 
 extern "C" int rope3d_block_norm_last_kernel(void) { return t_norm_kernel; }
+
+extern "C" int rope3d_testing_norm_wait_timeouts(int64_t *count, int32_t reset) {
+    if (!count) return ROPE3D_ERR_NULL;
+    unsigned int n = 0;
+    if (cudaMemcpyFromSymbol(&n, g_norm_wait_timeouts, sizeof(n)) != cudaSuccess) {
+        cudaGetLastError();
+        return ROPE3D_ERR_CUDA;
+    }
+    if (reset) {
+        const unsigned int zero = 0;
+        if (cudaMemcpyToSymbol(g_norm_wait_timeouts, &zero, sizeof(zero)) != cudaSuccess) {
+            cudaGetLastError();
+            return ROPE3D_ERR_CUDA;
+        }
+    }
+    *count = n;
+    return ROPE3D_OK;
+}

@@ -49,15 +49,27 @@ def make(rows, channels, dtype, groups=1, y=True, post=1, pre=1, weights=True, m
     return a, normal((rows, channels), dt, 0.5), normal((rows, channels), dt, 0.5)
 
 
+@pytest.fixture(autouse=True)
+def no_timeouts():
+    yield
+    assert r.rope3d_testing_norm_wait_timeouts() == 0
+
+
 def both(a, dr, dn, kernel):
+    """Forward and backward against 64 bits. kernel 1: rows in registers or (many
+    rows) through shared memory, 2: the general kernels, 3: through shared memory."""
+    def last():
+        k = r.rope3d_block_norm_last_kernel()
+        return k == kernel or (kernel == 1 and k == 3)
+
     got = dict(zip(("r", "n"), r.rope3d_block_norm(**a)))
-    assert r.rope3d_block_norm_last_kernel() == kernel
+    assert last()
     want = ref.norm64(**a)
     for name, t in got.items():
         if t is not None:
             ref.check(t, want[name], name)
     got = r.rope3d_block_norm_backward(dr=dr, dn=dn, **a)
-    assert r.rope3d_block_norm_last_kernel() == kernel
+    assert last()
     torch.cuda.synchronize()
     want = ref.norm64(dr=dr, dn=dn, grads=True, **a)
     assert set(got) == set(want)
@@ -116,6 +128,32 @@ def test_groups(rows, rpg, dtype, channels, kernel, params):
     both(*make(rows, channels, dtype, rpg=rpg, params=params), kernel)
 
 
-def test_many_rows():
-    both(*make(20000, 128, "bf16", groups=2), 1)
-    both(*make(6000, 2048, "f16", y=True, weights=True, mod=False, weight_offset=1.0), 1)
+RING = [
+    # rows, channels, dtype, groups: one warp a row, absent threads, each type's longest rows, one and several groups
+    (20000, 128, "bf16", 2), (12000, 8, "bf16", 1), (6000, 2048, "f16", 1), (5000, 1032, "bf16", 4),
+    (3000, 4096, "bf16", 3), (12000, 4, "f32", 5), (3000, 1156, "f32", 2), (700, 8192, "bf16", 1), (700, 8192, "f32", 1),
+    (2432, 2048, "bf16", 2432), (5000, 520, "f16", 1000),
+]
+
+
+@pytest.mark.parametrize("rows,channels,dtype,groups", RING)
+@pytest.mark.parametrize("post,pre,weights,mod", [(1, 1, True, False), (0, 1, False, True), (2, 2, True, True)])
+def test_many_rows(rows, channels, dtype, groups, post, pre, weights, mod):
+    a, dr, dn = make(rows, channels, dtype, groups=groups, post=post, pre=pre, weights=weights, mod=mod,
+                     residual_scale=0.75)
+    both(a, dr, dn, 1 if channels == 8192 else 3)
+
+
+@pytest.mark.parametrize("y,pre", [(False, 1), (False, 2), (True, 0), (False, 0)])
+def test_many_rows_absent_parts(y, pre):
+    a, dr, dn = make(5000, 768, "bf16", groups=2, y=y, post=0, pre=pre)
+    both(a, dr, dn, 3)
+    # no gradient of one output, or of the parameters
+    for d in (dict(dr=dr), dict(dn=dn)):
+        want = ref.norm64(grads=True, **d, **a)
+        for name, t in r.rope3d_block_norm_backward(**d, **a).items():
+            ref.check(t, want[name], name)
+    got = r.rope3d_block_norm_backward(dr=dr, dn=dn, param_grads=False, **a)
+    want = ref.norm64(dr=dr, dn=dn, grads=True, **a)
+    for name, t in got.items():
+        ref.check(t, want[name], name)
