@@ -727,100 +727,154 @@ struct Kept {
     }
 };
 
-// Sums over a block of kN values a thread, like Sums; the second step adds the
-// warps' sums in order, read as vectors.
-template <int kN>
+// Sums over a block of two values a thread: the warp's by shuffles that fold
+// both values into one (the halves of a warp take one value each), then the
+// warps' pairs in order, read as vectors. Two alternating slots: one barrier a
+// sum. `warps` rounded up to an even number; a slot past the last warp is zero.
 struct BlockSums {
-    float *red;   // [2][kN][16]
+    float2 *red;   // [2][16]
     int slot, warps;
-    __device__ __forceinline__ void operator()(float *v) {
+    __device__ __forceinline__ float2 operator()(float a, float b) {
+        const bool upper = threadIdx.x & 16;
+        const float other = __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
+        float v = (upper ? b : a) + other;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-            for (int i = 0; i < kN; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-        float *s = red + slot * kN * 16;
+        for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        float2 *s = red + slot * 16;
         slot ^= 1;
-        if ((threadIdx.x & 31) == 0)
-#pragma unroll
-            for (int i = 0; i < kN; ++i) s[i * 16 + (threadIdx.x >> 5)] = v[i];
+        if ((threadIdx.x & 15) == 0) reinterpret_cast<float *>(s + (threadIdx.x >> 5))[upper ? 1 : 0] = v;
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            v[i] = 0.0f;
-            for (int w = 0; w < warps; w += 4) {   // slots past the last warp stay zero
-                const float4 t = *reinterpret_cast<const float4 *>(s + i * 16 + w);
-                v[i] += (t.x + t.y) + (t.z + t.w);
-            }
+        float2 t = make_float2(0.0f, 0.0f);
+        for (int w = 0; w < warps; w += 2) {
+            const float4 q = *reinterpret_cast<const float4 *>(s + w);
+            t = add2(t, add2(make_float2(q.x, q.y), make_float2(q.z, q.w)));
         }
+        return t;
+    }
+    __device__ __forceinline__ float one(float a) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+        float *s = reinterpret_cast<float *>(red + slot * 16);
+        slot ^= 1;
+        if ((threadIdx.x & 31) == 0) s[2 * (threadIdx.x >> 5)] = a;
+        __syncthreads();
+        float t = 0.0f;
+        for (int w = 0; w < warps; w += 2) {
+            const float4 q = *reinterpret_cast<const float4 *>(s + 2 * w);
+            t += q.x + q.z;
+        }
+        return t;
     }
 };
+
+__device__ __forceinline__ float fold(float2 v) { return v.x + v.y; }
 
 struct Ring {
     uint32_t base, bars, row_bytes, stage_bytes;
     int stages;
-    // Thread 0: the rows of up to four arrays into stage s.
-    __device__ __forceinline__ void fill(int s, const void *const *src, int streams) const {
-        const uint32_t bar = bars + 8u * uint32_t(s);
-        mbar_expect_tx(bar, row_bytes * uint32_t(streams));
-        for (int i = 0; i < streams; ++i) bulk_row(base + uint32_t(s) * stage_bytes + uint32_t(i) * row_bytes, src[i], row_bytes, bar);
+};
+
+// What the two ring kernels share: the ring, the group's parameters in shared
+// memory, this thread's channels. kFull: every thread owns 16 channels (else
+// some own fewer, and `real` says which vectors exist).
+template <int kT, bool kFull>
+struct RingTeam {
+    static constexpr int V = kPer<kT>, kVecs = kRingE / V, P = V / 2, H = kRingE / 2, kBytes = 16 / V;
+    const NormParams &p;
+    int size, tid;
+    bool real_[kVecs];
+    float inv_c;
+    uint32_t base;
+
+    __device__ __forceinline__ RingTeam(const NormParams &params, const uint8_t *raw)
+        : p(params), size(int(blockDim.x)), tid(int(threadIdx.x)), inv_c(1.0f / float(params.channels)),
+          base((smem_u32(raw) + 127u) & ~127u) {
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) real_[j] = tid + j * size < params.channels / V;
+    }
+    __device__ __forceinline__ bool real(int j) const { return kFull || real_[j]; }
+    __device__ __forceinline__ int channel(int j) const { return (tid + j * size) * V; }
+    __device__ __forceinline__ Kept kept(int i) const {
+        return Kept{base + uint32_t(i) * 64u * uint32_t(size) + 16u * uint32_t(tid), 16u * uint32_t(size)};
+    }
+    // vector j of this thread in a row in shared memory; zeros where absent
+    __device__ __forceinline__ uint4 read(uint32_t row, int j) const {
+        return real(j) ? lds128(row + 16u * uint32_t(tid + j * size)) : make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void unpack_row(uint32_t row, float2 *f) const {
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) unpack2<kT>(read(row, j), f + j * P);
+    }
+    __device__ __forceinline__ void write(void *out, long long at, const float2 *f) const {
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j)
+            if (real(j)) st_row(out, at + channel(j), kBytes, pack<kT>(reinterpret_cast<const float *>(f + j * P)));
+    }
+    // m = gate * wp and q = wq * (1 + scale) of group g; zero for absent channels
+    __device__ __forceinline__ void group(int g, float *m, float *q) const {
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+            const int c = real(j) ? channel(j) : 0;
+            float a[V];
+            ld_weight<kT>(p.post_weight, c, p.param_f32, p.offset, m + j * V);
+            ld_param<kT>(p.gate, g * p.ldg + c, p.param_f32, 1.0f, a);
+#pragma unroll
+            for (int i = 0; i < V; ++i) m[j * V + i] = real(j) ? m[j * V + i] * a[i] : 0.0f;
+            ld_weight<kT>(p.pre_weight, c, p.param_f32, p.offset, q + j * V);
+            ld_param<kT>(p.scale, g * p.ldsc + c, p.param_f32, 0.0f, a);
+#pragma unroll
+            for (int i = 0; i < V; ++i) q[j * V + i] = real(j) ? q[j * V + i] * (1.0f + a[i]) : 0.0f;
+        }
+    }
+    // v minus its mean (layer norm): absent channels stay zero
+    __device__ __forceinline__ void center(float2 *v, float mean) const {
+        const float2 m = both(-mean);
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j)
+            if (real(j))
+#pragma unroll
+                for (int i = 0; i < P; ++i) v[j * P + i] = add2(v[j * P + i], m);
+    }
+    static __device__ __forceinline__ float total(const float2 *v) {
+        float2 t = v[0];
+#pragma unroll
+        for (int i = 1; i < H; ++i) t = add2(t, v[i]);
+        return fold(t);
+    }
+    static __device__ __forceinline__ float dot(const float2 *v, const float2 *w) {
+        float2 t = mul2(v[0], w[0]);
+#pragma unroll
+        for (int i = 1; i < H; ++i) t = fma2(v[i], w[i], t);
+        return fold(t);
+    }
+    // v normalised in place; returns 1 / std
+    template <bool kLayer>
+    __device__ __forceinline__ float normalise(float2 *v, int kind, BlockSums &sum) const {
+        if (kLayer && kind == ROPE3D_NORM_LAYER) center(v, sum.one(total(v)) * inv_c);
+        const float k = rsqrtf(sum.one(dot(v, v)) * inv_c + p.eps);
+        const float2 k2 = both(k);
+#pragma unroll
+        for (int i = 0; i < H; ++i) v[i] = mul2(v[i], k2);
+        return k;
     }
 };
 
-// One element pair's worth of statistics of v (pairs of 16 elements a thread):
-// mean (layer) and 1 / std.
-template <int kVecs, int kN>
-__device__ __forceinline__ void ring_stats(const float2 *v, int kind, const bool *real, float inv_c, float eps,
-                                           BlockSums<kN> &sum, float *mean, float *k) {
-    constexpr int P = kRingE / 2 / kVecs;   // pairs of a vector
-    *mean = 0.0f;
-    *k = 1.0f;
-    if (kind == ROPE3D_NORM_NONE) return;
-    float s[kN] = {};
-    if (kind == ROPE3D_NORM_LAYER) {
-        float2 t = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int i = 0; i < kRingE / 2; ++i) t = add2(t, v[i]);
-        s[0] = t.x + t.y;
-        sum(s);
-        *mean = s[0] * inv_c;
-#pragma unroll
-        for (int i = 0; i < kN; ++i) s[i] = 0.0f;
-    }
-    float2 t = make_float2(0.0f, 0.0f);
-    const float2 m = both(-*mean);
-#pragma unroll
-    for (int j = 0; j < kVecs; ++j)
-        if (real[j])
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const float2 d = add2(v[j * P + i], m);
-                t = fma2(d, d, t);
-            }
-    s[0] = t.x + t.y;
-    sum(s);
-    *k = rsqrtf(s[0] * inv_c + eps);
-}
-
-template <int kT>
-__global__ void __launch_bounds__(512) block_norm_ring_kernel(const __grid_constant__ NormParams p) {
-    constexpr int V = kPer<kT>, kVecs = kRingE / V, P = V / 2, kBytes = 16 / V;
+// kLayer: one of the norms is a layer norm.
+template <int kT, bool kLayer, bool kFull>
+__global__ void __maxnreg__(80) block_norm_ring_kernel(const __grid_constant__ NormParams p) {
+    using Team = RingTeam<kT, kFull>;
+    constexpr int H = Team::H, kBytes = Team::kBytes;
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(16) float red[2 * 16];
+    __shared__ __align__(16) float2 red[2 * 16];
     __shared__ __align__(8) unsigned long long bars[kRingBars];
-    const int size = int(blockDim.x), tid = int(threadIdx.x);
-    const uint32_t base = (smem_u32(raw) + 127u) & ~127u;
+    const Team team(p, raw);
+    const int tid = team.tid;
     const uint32_t row_bytes = uint32_t(p.channels) * kBytes;
     const int streams = p.y ? 2 : 1;
-    const Ring ring{base + uint32_t(size) * 3 * 64, smem_u32(bars), row_bytes, row_bytes * uint32_t(streams), p.stages};
-    const Kept km{base + 16u * uint32_t(tid), 16u * uint32_t(size)}, kq{km.base + 4 * km.step, km.step},
-        ks{kq.base + 4 * km.step, km.step};
-    BlockSums<1> sum{red, 0, (size + 31) >> 5};
-    const int n_vec = p.channels / V;
-    const float inv_c = 1.0f / float(p.channels);
-    bool real[kVecs];
-#pragma unroll
-    for (int j = 0; j < kVecs; ++j) real[j] = tid + j * size < n_vec;
-    for (int i = tid; i < 2 * 16; i += size) red[i] = 0.0f;
+    const Ring ring{team.base + uint32_t(team.size) * 3 * 64, smem_u32(bars), row_bytes, row_bytes * uint32_t(streams), p.stages};
+    const Kept km = team.kept(0), kq = team.kept(1), ks = team.kept(2);
+    BlockSums sum{red, 0, ((team.size >> 5) + 1) & ~1};
+    for (int i = tid; i < 2 * 16; i += team.size) red[i] = make_float2(0.0f, 0.0f);
     if (tid == 0) {
         for (int s = 0; s < p.stages; ++s) mbar_init(ring.bars + 8u * uint32_t(s), 1);
         mbar_fence_init();
@@ -830,129 +884,92 @@ __global__ void __launch_bounds__(512) block_norm_ring_kernel(const __grid_const
     grid_release();
     const long long lo = (long long)p.rows * blockIdx.x / gridDim.x, hi = (long long)p.rows * (blockIdx.x + 1) / gridDim.x;
     auto fill = [&](int s, long long row) {
-        const void *src[2] = {static_cast<const char *>(p.x) + row * p.ldx * kBytes,
-                              static_cast<const char *>(p.y) + row * p.ldy * kBytes};
-        ring.fill(s, src, streams);
+        const uint32_t bar = ring.bars + 8u * uint32_t(s), at = ring.base + uint32_t(s) * ring.stage_bytes;
+        mbar_expect_tx(bar, ring.stage_bytes);
+        bulk_row(at, static_cast<const char *>(p.x) + row * p.ldx * kBytes, row_bytes, bar);
+        if (p.y) bulk_row(at + row_bytes, static_cast<const char *>(p.y) + row * p.ldy * kBytes, row_bytes, bar);
     };
     if (tid == 0)
         for (int s = 0; s < p.stages && lo + s < hi; ++s) fill(s, lo + s);
     bool dead = false;
+    const float2 res = both(p.res);
     int g = int(uint32_t(lo) / uint32_t(p.rows_per_group)) - 1;
     long long group_end = lo;   // the first row starts a group
+    int s = 0;
+    uint32_t phase = 0;
     for (long long row = lo; row < hi; ++row) {
         if (row == group_end) {
             ++g;
             group_end = (long long)(g + 1) * p.rows_per_group;
-            float m[kRingE], q[kRingE], sh[kRingE];
-#pragma unroll
-            for (int j = 0; j < kVecs; ++j) {
-                const int c = real[j] ? (tid + j * size) * V : 0;
-                float a[V];
-                ld_weight<kT>(p.post_weight, c, p.param_f32, p.offset, m + j * V);
-                ld_param<kT>(p.gate, g * p.ldg + c, p.param_f32, 1.0f, a);
-#pragma unroll
-                for (int i = 0; i < V; ++i) m[j * V + i] *= a[i];
-                ld_weight<kT>(p.pre_weight, c, p.param_f32, p.offset, q + j * V);
-                ld_param<kT>(p.scale, g * p.ldsc + c, p.param_f32, 0.0f, a);
-#pragma unroll
-                for (int i = 0; i < V; ++i) q[j * V + i] *= 1.0f + a[i];
-                ld_param<kT>(p.shift, g * p.ldsh + c, p.param_f32, 0.0f, sh + j * V);
-            }
+            float m[kRingE], q[kRingE];
+            team.group(g, m, q);
             km.store(m);   // read back by this thread alone
             kq.store(q);
-            ks.store(sh);
-        }
-        const int s = int((row - lo) % p.stages);
-        mbar_wait(ring.bars + 8u * uint32_t(s), uint32_t((row - lo) / p.stages) & 1u, dead, &g_norm_wait_timeouts);
-        const uint32_t at = ring.base + uint32_t(s) * ring.stage_bytes + 16u * uint32_t(tid);
-        float2 v[kRingE / 2];
-        uint4 yv[kVecs];
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j) {
-            uint4 xv = make_uint4(0, 0, 0, 0);
-            yv[j] = xv;
-            if (real[j]) {
-                xv = lds128(at + uint32_t(j * size) * 16u);
-                if (p.y) yv[j] = lds128(at + row_bytes + uint32_t(j * size) * 16u);
-            }
-            unpack2<kT>(xv, v + j * P);
+            for (int j = 0; j < Team::kVecs; ++j)
+                ld_param<kT>(p.shift, g * p.ldsh + (team.real(j) ? team.channel(j) : 0), p.param_f32, 0.0f, m + j * Team::V);
+            ks.store(m);
         }
+        mbar_wait(ring.bars + 8u * uint32_t(s), phase, dead, &g_norm_wait_timeouts);
+        const uint32_t at = ring.base + uint32_t(s) * ring.stage_bytes;
+        float2 v[H];
+        team.unpack_row(at, v);
         bool synced = false;   // every thread has read its part of the stage
-        const float2 res = both(p.res);
+#pragma unroll
+        for (int i = 0; i < H; ++i) v[i] = mul2(res, v[i]);
         if (p.y) {
-            float2 y[kRingE / 2];
-            float mean, k;
-#pragma unroll
-            for (int j = 0; j < kVecs; ++j) unpack2<kT>(yv[j], y + j * P);
-            ring_stats<kVecs>(y, p.post, real, inv_c, p.eps, sum, &mean, &k);
-            synced = p.post != ROPE3D_NORM_NONE;
-            float2 m[kRingE / 2];
+            float2 y[H], m[H];
+            team.unpack_row(at + row_bytes, y);
+            if (p.post != ROPE3D_NORM_NONE) {
+                team.template normalise<kLayer>(y, p.post, sum);
+                synced = true;
+            }
             km.load(m);
-            const float2 k2 = both(k), mk = both(-mean * k);
 #pragma unroll
-            for (int i = 0; i < kRingE / 2; ++i) v[i] = fma2(m[i], fma2(y[i], k2, mk), mul2(res, v[i]));
-        } else {
-#pragma unroll
-            for (int i = 0; i < kRingE / 2; ++i) v[i] = mul2(res, v[i]);
+            for (int i = 0; i < H; ++i) v[i] = fma2(m[i], y[i], v[i]);
         }
-        if (p.n && p.pre != ROPE3D_NORM_NONE) {
-            // absent channels of a layer norm's y are not zero any more
-#pragma unroll
-            for (int j = 0; j < kVecs; ++j)
-                if (!real[j])
-#pragma unroll
-                    for (int i = 0; i < P; ++i) v[j * P + i] = make_float2(0.0f, 0.0f);
-        }
-        if (p.r) {
-#pragma unroll
-            for (int j = 0; j < kVecs; ++j)
-                if (real[j])
-                    st_row(p.r, row * p.ldr + (tid + j * size) * V, kBytes, pack<kT>(reinterpret_cast<const float *>(v + j * P)));
-        }
+        if (p.r) team.write(p.r, row * p.ldr, v);
         if (p.n) {
-            float mean, k;
-            ring_stats<kVecs>(v, p.pre, real, inv_c, p.eps, sum, &mean, &k);
-            synced = synced || p.pre != ROPE3D_NORM_NONE;
-            float2 q[kRingE / 2], sh[kRingE / 2];
+            if (p.pre != ROPE3D_NORM_NONE) {
+                team.template normalise<kLayer>(v, p.pre, sum);
+                synced = true;
+            }
+            float2 q[H], sh[H];
             kq.load(q);
             ks.load(sh);
-            const float2 k2 = both(k), mk = both(-mean * k);
 #pragma unroll
-            for (int i = 0; i < kRingE / 2; ++i) v[i] = fma2(fma2(v[i], k2, mk), q[i], sh[i]);
-#pragma unroll
-            for (int j = 0; j < kVecs; ++j)
-                if (real[j])
-                    st_row(p.n, row * p.ldn + (tid + j * size) * V, kBytes, pack<kT>(reinterpret_cast<const float *>(v + j * P)));
+            for (int i = 0; i < H; ++i) v[i] = fma2(v[i], q[i], sh[i]);
+            team.write(p.n, row * p.ldn, v);
         }
         if (!synced) __syncthreads();
         if (tid == 0 && row + p.stages < hi && !dead) fill(s, row + p.stages);
+        if (++s == p.stages) {
+            s = 0;
+            phase ^= 1;
+        }
     }
 }
 
-template <int kT>
+// kShift: d_shift is wanted (its sums are one more array of registers).
+template <int kT, bool kLayer, bool kFull, bool kShift>
 __global__ void __launch_bounds__(512) block_norm_back_ring_kernel(const __grid_constant__ NormParams p) {
-    constexpr int V = kPer<kT>, kVecs = kRingE / V, P = V / 2, H = kRingE / 2, kBytes = 16 / V;
+    using Team = RingTeam<kT, kFull>;
+    constexpr int V = Team::V, kVecs = Team::kVecs, P = Team::P, H = Team::H, kBytes = Team::kBytes;
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(16) float red[2 * 2 * 16];
+    __shared__ __align__(16) float2 red[2 * 16];
     __shared__ __align__(8) unsigned long long bars[kRingBars];
-    const int size = int(blockDim.x), tid = int(threadIdx.x);
-    const uint32_t base = (smem_u32(raw) + 127u) & ~127u;
+    const Team team(p, raw);
+    const int tid = team.tid;
     const uint32_t row_bytes = uint32_t(p.channels) * kBytes;
     // the arrays that a stage holds, in this order
-    const int at_y = 1, at_n = 1 + (p.y != nullptr), at_r = at_n + (p.dn != nullptr);
-    const int streams = at_r + (p.dr != nullptr);
+    const uint32_t at_y = row_bytes, at_n = at_y + (p.y ? row_bytes : 0), at_r = at_n + (p.dn ? row_bytes : 0);
+    const uint32_t stage_bytes = at_r + (p.dr ? row_bytes : 0);
     // m, q and, where a chunk is whole groups, the weights' sums
-    const Ring ring{base + uint32_t(size) * (p.groups_per_chunk ? 4 : 2) * 64, smem_u32(bars), row_bytes,
-                    row_bytes * uint32_t(streams), p.stages};
-    const Kept km{base + 16u * uint32_t(tid), 16u * uint32_t(size)}, kq{km.base + 4 * km.step, km.step},
-        kwq{kq.base + 4 * km.step, km.step}, kwp{kwq.base + 4 * km.step, km.step};
-    BlockSums<2> sum{red, 0, (size + 31) >> 5};
-    const int n_vec = p.channels / V;
-    const float inv_c = 1.0f / float(p.channels);
-    bool real[kVecs];
-#pragma unroll
-    for (int j = 0; j < kVecs; ++j) real[j] = tid + j * size < n_vec;
-    for (int i = tid; i < 2 * 2 * 16; i += size) red[i] = 0.0f;
+    const Ring ring{team.base + uint32_t(team.size) * (p.groups_per_chunk ? 4 : 2) * 64, smem_u32(bars), row_bytes,
+                    stage_bytes, p.stages};
+    const Kept km = team.kept(0), kq = team.kept(1), kwq = team.kept(2), kwp = team.kept(3);
+    BlockSums sum{red, 0, ((team.size >> 5) + 1) & ~1};
+    for (int i = tid; i < 2 * 16; i += team.size) red[i] = make_float2(0.0f, 0.0f);
     if (tid == 0) {
         for (int s = 0; s < p.stages; ++s) mbar_init(ring.bars + 8u * uint32_t(s), 1);
         mbar_fence_init();
@@ -964,20 +981,22 @@ __global__ void __launch_bounds__(512) block_norm_back_ring_kernel(const __grid_
     long long lo, hi;
     chunk_range(p, chunk, &lo, &hi);
     auto fill = [&](int s, long long row) {
-        const void *src[4];
-        src[0] = static_cast<const char *>(p.x) + row * p.ldx * kBytes;
-        if (p.y) src[at_y] = static_cast<const char *>(p.y) + row * p.ldy * kBytes;
-        if (p.dn) src[at_n] = static_cast<const char *>(p.dn) + row * p.lddn * kBytes;
-        if (p.dr) src[at_r] = static_cast<const char *>(p.dr) + row * p.lddr * kBytes;
-        ring.fill(s, src, streams);
+        const uint32_t bar = ring.bars + 8u * uint32_t(s), at = ring.base + uint32_t(s) * ring.stage_bytes;
+        mbar_expect_tx(bar, ring.stage_bytes);
+        bulk_row(at, static_cast<const char *>(p.x) + row * p.ldx * kBytes, row_bytes, bar);
+        if (p.y) bulk_row(at + at_y, static_cast<const char *>(p.y) + row * p.ldy * kBytes, row_bytes, bar);
+        if (p.dn) bulk_row(at + at_n, static_cast<const char *>(p.dn) + row * p.lddn * kBytes, row_bytes, bar);
+        if (p.dr) bulk_row(at + at_r, static_cast<const char *>(p.dr) + row * p.lddr * kBytes, row_bytes, bar);
     };
     if (tid == 0)
         for (int s = 0; s < p.stages && lo + s < hi; ++s) fill(s, lo + s);
     bool dead = false;
     const float2 zero = make_float2(0.0f, 0.0f), res = both(p.res);
-    float2 S[H], T[H], U[H];
+    float2 S[H], U[H], T[kShift ? H : 1];
 #pragma unroll
-    for (int i = 0; i < H; ++i) S[i] = T[i] = U[i] = zero;
+    for (int i = 0; i < H; ++i) S[i] = U[i] = zero;
+#pragma unroll
+    for (int i = 0; i < (kShift ? H : 1); ++i) T[i] = zero;
     if (p.groups_per_chunk) {
         float z[kRingE] = {};
         kwq.store(z);
@@ -985,173 +1004,117 @@ __global__ void __launch_bounds__(512) block_norm_back_ring_kernel(const __grid_
     }
     int g = int(uint32_t(lo) / uint32_t(p.rows_per_group)) - 1;
     long long group_end = lo;
+    int s = 0;
+    uint32_t phase = 0;
     for (long long row = lo; row < hi; ++row) {
         if (row == group_end) {
             ++g;
             group_end = (long long)(g + 1) * p.rows_per_group;
             float m[kRingE], q[kRingE];
-#pragma unroll
-            for (int j = 0; j < kVecs; ++j) {
-                const int c = real[j] ? (tid + j * size) * V : 0;
-                float a[V];
-                ld_weight<kT>(p.post_weight, c, p.param_f32, p.offset, m + j * V);
-                ld_param<kT>(p.gate, g * p.ldg + c, p.param_f32, 1.0f, a);
-#pragma unroll
-                for (int i = 0; i < V; ++i) m[j * V + i] = real[j] ? m[j * V + i] * a[i] : 0.0f;
-                ld_weight<kT>(p.pre_weight, c, p.param_f32, p.offset, q + j * V);
-                ld_param<kT>(p.scale, g * p.ldsc + c, p.param_f32, 0.0f, a);
-#pragma unroll
-                for (int i = 0; i < V; ++i) q[j * V + i] = real[j] ? q[j * V + i] * (1.0f + a[i]) : 0.0f;
-            }
-            km.store(m);   // zero for absent channels: they drop out of every sum
+            team.group(g, m, q);
+            km.store(m);
             kq.store(q);
         }
-        const int s = int((row - lo) % p.stages);
-        mbar_wait(ring.bars + 8u * uint32_t(s), uint32_t((row - lo) / p.stages) & 1u, dead, &g_norm_wait_timeouts);
-        const uint32_t at = ring.base + uint32_t(s) * ring.stage_bytes + 16u * uint32_t(tid);
-        auto read = [&](int stream, int j) {
-            return real[j] ? lds128(at + uint32_t(stream) * row_bytes + uint32_t(j * size) * 16u) : make_uint4(0, 0, 0, 0);
-        };
-        float my = 0.0f, ky = 1.0f;
-        float2 r[H], e[H];
-        uint4 yv[kVecs];
-#pragma unroll
-        for (int j = 0; j < kVecs; ++j) yv[j] = make_uint4(0, 0, 0, 0);
+        mbar_wait(ring.bars + 8u * uint32_t(s), phase, dead, &g_norm_wait_timeouts);
+        const uint32_t at = ring.base + uint32_t(s) * ring.stage_bytes;
+        // y normalised, r = res x + m y, dn
+        float2 y[H], r[H], d[H];
+        float ky = 1.0f;
         if (p.y) {
-            float2 y[H];
-#pragma unroll
-            for (int j = 0; j < kVecs; ++j) {
-                yv[j] = read(at_y, j);
-                unpack2<kT>(yv[j], y + j * P);
-            }
-            ring_stats<kVecs>(y, p.post, real, inv_c, p.eps, sum, &my, &ky);
+            team.unpack_row(at + at_y, y);
+            if (p.post != ROPE3D_NORM_NONE) ky = team.template normalise<kLayer>(y, p.post, sum);
         }
-        const float2 ky2 = both(ky), myk = both(-my * ky);
+        team.unpack_row(at, r);
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j) {
-            unpack2<kT>(read(0, j), r + j * P);
-            if (p.dn) unpack2<kT>(read(at_n, j), e + j * P);
-            else
-#pragma unroll
-                for (int i = 0; i < P; ++i) e[j * P + i] = zero;
-        }
-        {
-            float2 q[H];
-            kq.load(q);
-#pragma unroll
-            for (int i = 0; i < H; ++i) {
-                r[i] = mul2(res, r[i]);
-                e[i] = mul2(e[i], q[i]);
-            }
-        }
+        for (int i = 0; i < H; ++i) r[i] = mul2(res, r[i]);
         if (p.y) {
             float2 m[H];
             km.load(m);
 #pragma unroll
-            for (int j = 0; j < kVecs; ++j) {
-                float2 y[P];
-                unpack2<kT>(yv[j], y);
-#pragma unroll
-                for (int i = 0; i < P; ++i) r[j * P + i] = fma2(m[j * P + i], fma2(y[i], ky2, myk), r[j * P + i]);
-            }
+            for (int i = 0; i < H; ++i) r[i] = fma2(m[i], y[i], r[i]);
         }
-        float mr = 0.0f, kr = 1.0f, me = 0.0f, mez = 0.0f;
-        if (p.pre != ROPE3D_NORM_NONE) {
-            float t[2];
-            if (p.pre == ROPE3D_NORM_LAYER) {
-                float2 a = zero, b = zero;
+        if (p.dn) {
+            team.unpack_row(at + at_n, d);
+        } else {
 #pragma unroll
-                for (int i = 0; i < H; ++i) {
-                    a = add2(a, r[i]);
-                    b = add2(b, e[i]);
-                }
-                t[0] = a.x + a.y;
-                t[1] = b.x + b.y;
-                sum(t);
-                mr = t[0] * inv_c;
-                me = t[1] * inv_c;
+            for (int i = 0; i < H; ++i) d[i] = zero;
+        }
+        float kr = 1.0f, me = 0.0f, mez = 0.0f;
+        if (p.pre != ROPE3D_NORM_NONE) {
+            // 1 / std of r and the means of e = dn q and e z, from one pair of sums
+            float2 q[H];
+            kq.load(q);
+            if (kLayer && p.pre == ROPE3D_NORM_LAYER) {
+                const float2 t = sum(Team::total(r), Team::dot(d, q));
+                team.center(r, t.x * team.inv_c);
+                me = t.y * team.inv_c;
             }
             float2 a = zero, b = zero;
-            const float2 nm = both(-mr);
 #pragma unroll
-            for (int j = 0; j < kVecs; ++j)
-                if (real[j])
-#pragma unroll
-                    for (int i = 0; i < P; ++i) {
-                        const float2 d = add2(r[j * P + i], nm);
-                        a = fma2(d, d, a);
-                        b = fma2(d, e[j * P + i], b);
-                    }
-            t[0] = a.x + a.y;
-            t[1] = b.x + b.y;
-            sum(t);
-            kr = rsqrtf(t[0] * inv_c + p.eps);
-            mez = t[1] * inv_c * kr;
-        }
-        // e becomes the whole gradient of r, and r becomes f
-        {
-            const bool plain = p.pre == ROPE3D_NORM_NONE;
-            const float2 kr2 = both(kr), mrk = both(-mr * kr), nme = both(plain ? 0.0f : -me), nmez = both(plain ? 0.0f : -mez);
-#pragma unroll
-            for (int j = 0; j < kVecs; ++j) {
-                float2 dn[P], dr[P];
-                if (p.dn) unpack2<kT>(read(at_n, j), dn);
-                if (p.dr) unpack2<kT>(read(at_r, j), dr);
-#pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    const int x = j * P + i;
-                    if (!p.dn) dn[i] = zero;
-                    if (!p.dr) dr[i] = zero;
-                    const float2 z = fma2(r[x], kr2, mrk);
-                    S[x] = fma2(dn[i], z, S[x]);
-                    T[x] = add2(T[x], dn[i]);
-                    e[x] = fma2(kr2, fma2(z, nmez, add2(e[x], nme)), dr[i]);
-                }
-                if (real[j]) {
-                    float2 o[P];
-#pragma unroll
-                    for (int i = 0; i < P; ++i) o[i] = mul2(res, e[j * P + i]);
-                    st_row(p.dx, row * p.lddx + (tid + j * size) * V, kBytes, pack<kT>(reinterpret_cast<const float *>(o)));
-                }
+            for (int i = 0; i < H; ++i) {
+                a = fma2(r[i], r[i], a);
+                b = fma2(r[i], mul2(d[i], q[i]), b);
             }
+            const float2 t = sum(fold(a), fold(b));
+            kr = rsqrtf(t.x * team.inv_c + p.eps);
+            mez = t.y * team.inv_c * kr;
+        }
+        // d becomes the whole gradient of r, r becomes f = d m
+        {
+            float2 q[H], dr[H];
+            kq.load(q);
+            if (p.dr) {
+                team.unpack_row(at + at_r, dr);
+            } else {
+#pragma unroll
+                for (int i = 0; i < H; ++i) dr[i] = zero;
+            }
+            const float2 kr2 = both(kr), nme = both(-kr * me), nmez = both(-kr * mez);
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                const float2 z = mul2(r[i], kr2);
+                S[i] = fma2(d[i], z, S[i]);
+                if constexpr (kShift) T[i] = add2(T[i], d[i]);
+                if constexpr (kLayer) dr[i] = add2(dr[i], nme);
+                d[i] = fma2(kr2, mul2(d[i], q[i]), fma2(z, nmez, dr[i]));
+                r[i] = mul2(res, d[i]);
+            }
+            team.write(p.dx, row * p.lddx, r);
         }
         if (p.y) {
             float2 m[H], a = zero, b = zero;
             km.load(m);
 #pragma unroll
-            for (int j = 0; j < kVecs; ++j) {
-                float2 y[P];
-                unpack2<kT>(yv[j], y);
+            for (int i = 0; i < H; ++i) {
+                U[i] = fma2(d[i], y[i], U[i]);
+                r[i] = mul2(d[i], m[i]);   // m is zero for absent channels
+                if constexpr (kLayer) a = add2(a, r[i]);
+                b = fma2(r[i], y[i], b);
+            }
+            // the stage has been read by every thread once they meet in this sum
+            if (p.post != ROPE3D_NORM_NONE) {
+                float2 t = make_float2(0.0f, 0.0f);
+                if (kLayer && p.post == ROPE3D_NORM_LAYER) t = sum(fold(a), fold(b));
+                else t.y = sum.one(fold(b));
+                if (tid == 0 && row + p.stages < hi && !dead) fill(s, row + p.stages);
+                const float2 ky2 = both(ky), nmf = both(-ky * t.x * team.inv_c), nmfy = both(-ky * t.y * team.inv_c);
 #pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    const int x = j * P + i;
-                    const float2 yh = fma2(y[i], ky2, myk);
-                    U[x] = fma2(e[x], yh, U[x]);
-                    r[x] = mul2(e[x], m[x]);   // m is zero for absent channels
-                    a = add2(a, r[x]);
-                    b = fma2(r[x], yh, b);
+                for (int i = 0; i < H; ++i) {
+                    if constexpr (kLayer) r[i] = fma2(ky2, r[i], fma2(y[i], nmfy, nmf));
+                    else r[i] = fma2(ky2, r[i], mul2(y[i], nmfy));
                 }
+            } else {
+                __syncthreads();
+                if (tid == 0 && row + p.stages < hi && !dead) fill(s, row + p.stages);
             }
-            float t[2] = {a.x + a.y, b.x + b.y};
-            if (p.post != ROPE3D_NORM_NONE) sum(t);
-            else __syncthreads();
-            if (tid == 0 && row + p.stages < hi && !dead) fill(s, row + p.stages);
-            const bool plain = p.post == ROPE3D_NORM_NONE;
-            const float2 nmf = both(p.post == ROPE3D_NORM_LAYER ? -t[0] * inv_c : 0.0f), nmfy = both(plain ? 0.0f : -t[1] * inv_c);
-#pragma unroll
-            for (int j = 0; j < kVecs; ++j) {
-                if (!real[j]) continue;
-                float2 y[P], o[P];
-                unpack2<kT>(yv[j], y);
-#pragma unroll
-                for (int i = 0; i < P; ++i)
-                    o[i] = plain ? r[j * P + i]
-                                 : mul2(ky2, fma2(fma2(y[i], ky2, myk), nmfy, add2(r[j * P + i], nmf)));
-                st_row(p.dy, row * p.lddy + (tid + j * size) * V, kBytes, pack<kT>(reinterpret_cast<const float *>(o)));
-            }
+            team.write(p.dy, row * p.lddy, r);
         } else {
             __syncthreads();
             if (tid == 0 && row + p.stages < hi && !dead) fill(s, row + p.stages);
+        }
+        if (++s == p.stages) {
+            s = 0;
+            phase ^= 1;
         }
         if (p.groups_per_chunk && p.sums && (row + 1 == group_end || row + 1 == hi)) {
             // a whole group is done: its gradients, and its part of the weights'
@@ -1163,18 +1126,19 @@ __global__ void __launch_bounds__(512) block_norm_back_ring_kernel(const __grid_
             memcpy(wp, t, sizeof(wp));
 #pragma unroll
             for (int j = 0; j < kVecs; ++j) {
-                const int c = real[j] ? (tid + j * size) * V : 0;
+                const int c = team.real(j) ? team.channel(j) : 0;
                 const float *Sj = reinterpret_cast<const float *>(S + j * P), *Uj = reinterpret_cast<const float *>(U + j * P);
                 float a[V], o[V];
-                if (p.d_scale && real[j]) {
+                if (p.d_scale && team.real(j)) {
                     ld_weight<kT>(p.pre_weight, c, p.param_f32, p.offset, a);
 #pragma unroll
                     for (int i = 0; i < V; ++i) o[i] = a[i] * Sj[i];
                     st_param<kT>(p.d_scale, g * p.ldgrad + c, p.param_f32, o);
                 }
-                if (p.d_shift && real[j])
-                    st_param<kT>(p.d_shift, g * p.ldgrad + c, p.param_f32, reinterpret_cast<const float *>(T + j * P));
-                if (p.d_gate && real[j]) {
+                if constexpr (kShift)
+                    if (team.real(j))
+                        st_param<kT>(p.d_shift, g * p.ldgrad + c, p.param_f32, reinterpret_cast<const float *>(T + j * P));
+                if (p.d_gate && team.real(j)) {
                     ld_weight<kT>(p.post_weight, c, p.param_f32, p.offset, a);
 #pragma unroll
                     for (int i = 0; i < V; ++i) o[i] = a[i] * Uj[i];
@@ -1190,7 +1154,9 @@ __global__ void __launch_bounds__(512) block_norm_back_ring_kernel(const __grid_
             kwq.store(wq);
             kwp.store(wp);
 #pragma unroll
-            for (int i = 0; i < H; ++i) S[i] = T[i] = U[i] = zero;
+            for (int i = 0; i < H; ++i) S[i] = U[i] = zero;
+#pragma unroll
+            for (int i = 0; i < (kShift ? H : 1); ++i) T[i] = zero;
         }
     }
     if (p.part) {
@@ -1199,20 +1165,18 @@ __global__ void __launch_bounds__(512) block_norm_back_ring_kernel(const __grid_
             kwp.load(U);
         }
         float *dst = p.part + (long long)chunk * 3 * p.channels;
+        auto put = [&](float *to, const float2 *v) {
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j) {
-            if (!real[j]) continue;
-            const int c = (tid + j * size) * V;
+            for (int j = 0; j < kVecs; ++j)
+                if (team.real(j))
 #pragma unroll
-            for (int i = 0; i < P; i += 2) {
-                *reinterpret_cast<float4 *>(dst + c + 2 * i) =
-                    make_float4(S[j * P + i].x, S[j * P + i].y, S[j * P + i + 1].x, S[j * P + i + 1].y);
-                *reinterpret_cast<float4 *>(dst + p.channels + c + 2 * i) =
-                    make_float4(T[j * P + i].x, T[j * P + i].y, T[j * P + i + 1].x, T[j * P + i + 1].y);
-                *reinterpret_cast<float4 *>(dst + 2 * p.channels + c + 2 * i) =
-                    make_float4(U[j * P + i].x, U[j * P + i].y, U[j * P + i + 1].x, U[j * P + i + 1].y);
-            }
-        }
+                    for (int i = 0; i < P; i += 2)
+                        *reinterpret_cast<float4 *>(to + team.channel(j) + 2 * i) =
+                            make_float4(v[j * P + i].x, v[j * P + i].y, v[j * P + i + 1].x, v[j * P + i + 1].y);
+        };
+        put(dst, S);
+        if constexpr (kShift) put(dst + p.channels, T);
+        put(dst + 2ll * p.channels, U);
     }
 }
 
@@ -1348,7 +1312,8 @@ __global__ void __launch_bounds__(32 * kFinishRows) block_norm_finish_kernel(con
             for (int i = ty; i < per; i += kFinishRows) {
                 const float *src = p.part + ((long long)g * per + i) * 3 * p.channels + c;
 #pragma unroll
-                for (int k = 0; k < 3; ++k) s[k] += src[(long long)k * p.channels];
+                for (int k = 0; k < 3; ++k)
+                    if (k != 1 || p.d_shift) s[k] += src[(long long)k * p.channels];   // the shift's sums may be absent
             }
 #pragma unroll
         for (int k = 0; k < 3; ++k) part[k][ty][lane] = s[k];
@@ -1582,6 +1547,24 @@ RingShape ring_shape(int64_t channels, int es, int streams, int kept, int thread
     return r;
 }
 
+template <int kT>
+NormFn ring_fn(bool layer, bool full) {
+    if (layer) return full ? block_norm_ring_kernel<kT, true, true> : block_norm_ring_kernel<kT, true, false>;
+    return full ? block_norm_ring_kernel<kT, false, true> : block_norm_ring_kernel<kT, false, false>;
+}
+
+template <int kT, bool kLayer>
+NormFn ring_back_of(bool full, bool shift) {
+    if (full)
+        return shift ? block_norm_back_ring_kernel<kT, kLayer, true, true> : block_norm_back_ring_kernel<kT, kLayer, true, false>;
+    return shift ? block_norm_back_ring_kernel<kT, kLayer, false, true> : block_norm_back_ring_kernel<kT, kLayer, false, false>;
+}
+
+template <int kT>
+NormFn ring_back_fn(bool layer, bool full, bool shift) {
+    return layer ? ring_back_of<kT, true>(full, shift) : ring_back_of<kT, false>(full, shift);
+}
+
 template <typename Fn>
 int launch_ring(Fn fn, unsigned grid, const RingShape &shape, NormParams &p, cudaStream_t st) {
     p.stages = shape.stages;
@@ -1624,12 +1607,13 @@ int forward(const rope3d_block_norm_args *a, bool run, bool check_device, cudaSt
         return launch(block_norm_any_kernel, dim3(unsigned(std::min<int64_t>(R, int64_t(sms) * 8))),
                       dim3(kGeneralThreads), 0, p, st);
     }
-    const RingShape shape = ring_shape(C, es, a->y ? 2 : 1, 3, 896);   // 64-66 registers a thread
+    const RingShape shape = ring_shape(C, es, a->y ? 2 : 1, 3, 768);   // 80 registers a thread
     if (shape.stages && R >= int64_t(kSms) * shape.per_sm * 2) {
         t_norm_kernel = 3;
-        const NormFn fn = a->dtype == ROPE3D_BF16 ? block_norm_ring_kernel<ROPE3D_BF16>
-                          : a->dtype == ROPE3D_F16 ? block_norm_ring_kernel<ROPE3D_F16>
-                                                   : block_norm_ring_kernel<ROPE3D_F32>;
+        const bool layer = p.post == ROPE3D_NORM_LAYER || p.pre == ROPE3D_NORM_LAYER, full = C == shape.threads * kRingE;
+        const NormFn fn = a->dtype == ROPE3D_BF16 ? ring_fn<ROPE3D_BF16>(layer, full)
+                          : a->dtype == ROPE3D_F16 ? ring_fn<ROPE3D_F16>(layer, full)
+                                                   : ring_fn<ROPE3D_F32>(layer, full);
         return launch_ring(fn, unsigned(sms * shape.per_sm), shape, p, st);
     }
     t_norm_kernel = 1;
@@ -1693,8 +1677,8 @@ int backward(const rope3d_block_norm_backward_args *a, bool run, bool check_devi
     p.sums = group_grads || a->d_post_weight || a->d_pre_weight;
     const Team t = vectors(all, 16, C, vec) ? backward_team(C / vec, vec) : Team{0, 0, false};
     const int streams = 1 + (f.y != nullptr) + (a->dn != nullptr) + (a->dr != nullptr);
-    const RingShape shape = ring_shape(C, es, streams, 4, 512);   // 128 registers a thread
-    const bool ring = t.vecs && shape.stages && R >= kSms * shape.per_sm * 2;
+    RingShape shape = ring_shape(C, es, streams, 2, 512);   // 128 registers a thread
+    bool ring = t.vecs && shape.stages && R >= kSms * shape.per_sm * 2;
     // Chunks: about as many as the GPU runs teams at once (or the general
     // kernel's column blocks), each of whole groups or a part of one.
     const int64_t target =
@@ -1711,6 +1695,10 @@ int backward(const rope3d_block_norm_backward_args *a, bool run, bool check_devi
     } else {
         p.groups_per_chunk = int(L / rpg);
         p.chunks = int((G + p.groups_per_chunk - 1) / p.groups_per_chunk);
+    }
+    if (ring && p.groups_per_chunk) {   // the weights' sums take shared memory too
+        shape = ring_shape(C, es, streams, 4, 512);
+        ring = shape.stages > 0;
     }
     const bool partial = p.sums && (!p.groups_per_chunk || a->d_post_weight || a->d_pre_weight);
     const int64_t part_bytes = partial ? up(int64_t(p.chunks) * 3 * C * 4, 256) : 0;
@@ -1735,9 +1723,10 @@ int backward(const rope3d_block_norm_backward_args *a, bool run, bool check_devi
     p.part = partial ? reinterpret_cast<float *>(ws) : nullptr;
     if (ring) {
         t_norm_kernel = 3;
-        const NormFn fn = f.dtype == ROPE3D_BF16 ? block_norm_back_ring_kernel<ROPE3D_BF16>
-                          : f.dtype == ROPE3D_F16 ? block_norm_back_ring_kernel<ROPE3D_F16>
-                                                  : block_norm_back_ring_kernel<ROPE3D_F32>;
+        const bool layer = p.post == ROPE3D_NORM_LAYER || p.pre == ROPE3D_NORM_LAYER, full = C == shape.threads * kRingE;
+        const NormFn fn = f.dtype == ROPE3D_BF16 ? ring_back_fn<ROPE3D_BF16>(layer, full, p.d_shift)
+                          : f.dtype == ROPE3D_F16 ? ring_back_fn<ROPE3D_F16>(layer, full, p.d_shift)
+                                                  : ring_back_fn<ROPE3D_F32>(layer, full, p.d_shift);
         rc = launch_ring(fn, unsigned(p.chunks), shape, p, st);
         if (rc != ROPE3D_OK) return rc;
     } else if (t.vecs) {
