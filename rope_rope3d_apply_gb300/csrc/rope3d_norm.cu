@@ -64,6 +64,7 @@ struct NormParams {
     int dtype, param_f32;
     // backward: chunks of rows and their partial column sums
     float *part;          // [chunks][3][channels]: sums of a part of a group, or the weights' sums of whole groups
+    float *group_sums;    // [groups][2][channels]: the groups' parts of the weights' gradients
     float *stats;         // general kernels: [rows][6]
     int chunk_rows, chunks_per_group, groups_per_chunk, chunks;
     int sums;             // column sums are wanted
@@ -711,6 +712,16 @@ __device__ __forceinline__ void bulk_row(uint32_t dst, const void *src, uint32_t
 struct Kept {
     uint32_t base;   // + this thread's 16 bytes
     uint32_t step;   // bytes of one piece of all threads
+    // kPairs pairs from pair kPairs * j on
+    template <int kPairs>
+    __device__ __forceinline__ void load_part(int j, float2 *f) const {
+#pragma unroll
+        for (int i = 0; i < kPairs / 2; ++i) {
+            const uint4 v = lds128(base + uint32_t(j * kPairs / 2 + i) * step);
+            f[2 * i] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+            f[2 * i + 1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+        }
+    }
     __device__ __forceinline__ void load(float2 *f) const {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -1024,72 +1035,98 @@ __global__ void __launch_bounds__(512) block_norm_back_ring_kernel(const __grid_
             team.unpack_row(at + at_y, y);
             if (p.post != ROPE3D_NORM_NONE) ky = team.template normalise<kLayer>(y, p.post, sum);
         }
-        team.unpack_row(at, r);
+        // (one vector at a time here and below: the sums leave few registers)
 #pragma unroll
-        for (int i = 0; i < H; ++i) r[i] = mul2(res, r[i]);
-        if (p.y) {
-            float2 m[H];
-            km.load(m);
+        for (int j = 0; j < kVecs; ++j) {
+            float2 *rj = r + j * P;
+            unpack2<kT>(team.read(at, j), rj);
 #pragma unroll
-            for (int i = 0; i < H; ++i) r[i] = fma2(m[i], y[i], r[i]);
-        }
-        if (p.dn) {
-            team.unpack_row(at + at_n, d);
-        } else {
+            for (int i = 0; i < P; ++i) rj[i] = mul2(res, rj[i]);
+            if (p.y) {
+                float2 m[P];
+                km.load_part<P>(j, m);
 #pragma unroll
-            for (int i = 0; i < H; ++i) d[i] = zero;
+                for (int i = 0; i < P; ++i) rj[i] = fma2(m[i], y[j * P + i], rj[i]);
+            }
+            if (p.dn) {
+                unpack2<kT>(team.read(at + at_n, j), d + j * P);
+            } else {
+#pragma unroll
+                for (int i = 0; i < P; ++i) d[j * P + i] = zero;
+            }
         }
         float kr = 1.0f, me = 0.0f, mez = 0.0f;
         if (p.pre != ROPE3D_NORM_NONE) {
             // 1 / std of r and the means of e = dn q and e z, from one pair of sums
-            float2 q[H];
-            kq.load(q);
             if (kLayer && p.pre == ROPE3D_NORM_LAYER) {
-                const float2 t = sum(Team::total(r), Team::dot(d, q));
+                float2 b = zero;
+#pragma unroll
+                for (int j = 0; j < kVecs; ++j) {
+                    float2 q[P];
+                    kq.load_part<P>(j, q);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) b = fma2(d[j * P + i], q[i], b);
+                }
+                const float2 t = sum(Team::total(r), fold(b));
                 team.center(r, t.x * team.inv_c);
                 me = t.y * team.inv_c;
             }
             float2 a = zero, b = zero;
 #pragma unroll
-            for (int i = 0; i < H; ++i) {
-                a = fma2(r[i], r[i], a);
-                b = fma2(r[i], mul2(d[i], q[i]), b);
+            for (int j = 0; j < kVecs; ++j) {
+                float2 q[P];
+                kq.load_part<P>(j, q);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    a = fma2(r[j * P + i], r[j * P + i], a);
+                    b = fma2(r[j * P + i], mul2(d[j * P + i], q[i]), b);
+                }
             }
             const float2 t = sum(fold(a), fold(b));
             kr = rsqrtf(t.x * team.inv_c + p.eps);
             mez = t.y * team.inv_c * kr;
         }
-        // d becomes the whole gradient of r, r becomes f = d m
+        // d becomes the whole gradient of r
         {
-            float2 q[H], dr[H];
-            kq.load(q);
-            if (p.dr) {
-                team.unpack_row(at + at_r, dr);
-            } else {
-#pragma unroll
-                for (int i = 0; i < H; ++i) dr[i] = zero;
-            }
             const float2 kr2 = both(kr), nme = both(-kr * me), nmez = both(-kr * mez);
 #pragma unroll
-            for (int i = 0; i < H; ++i) {
-                const float2 z = mul2(r[i], kr2);
-                S[i] = fma2(d[i], z, S[i]);
-                if constexpr (kShift) T[i] = add2(T[i], d[i]);
-                if constexpr (kLayer) dr[i] = add2(dr[i], nme);
-                d[i] = fma2(kr2, mul2(d[i], q[i]), fma2(z, nmez, dr[i]));
-                r[i] = mul2(res, d[i]);
+            for (int j = 0; j < kVecs; ++j) {
+                float2 q[P], dr[P];
+                kq.load_part<P>(j, q);
+                if (p.dr) {
+                    unpack2<kT>(team.read(at + at_r, j), dr);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < P; ++i) dr[i] = zero;
+                }
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const int x = j * P + i;
+                    const float2 z = mul2(r[x], kr2);
+                    S[x] = fma2(d[x], z, S[x]);
+                    if constexpr (kShift) T[x] = add2(T[x], d[x]);
+                    if constexpr (kLayer) dr[i] = add2(dr[i], nme);
+                    d[x] = fma2(kr2, mul2(d[x], q[i]), fma2(z, nmez, dr[i]));
+                    dr[i] = mul2(res, d[x]);
+                }
+                if (team.real(j))
+                    st_row(p.dx, row * p.lddx + team.channel(j), kBytes, pack<kT>(reinterpret_cast<const float *>(dr)));
             }
-            team.write(p.dx, row * p.lddx, r);
         }
         if (p.y) {
-            float2 m[H], a = zero, b = zero;
-            km.load(m);
+            float2 a = zero, b = zero;
 #pragma unroll
-            for (int i = 0; i < H; ++i) {
-                U[i] = fma2(d[i], y[i], U[i]);
-                r[i] = mul2(d[i], m[i]);   // m is zero for absent channels
-                if constexpr (kLayer) a = add2(a, r[i]);
-                b = fma2(r[i], y[i], b);
+            for (int j = 0; j < kVecs; ++j) {
+                float2 m[P];
+                km.load_part<P>(j, m);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const int x = j * P + i;
+                    U[x] = fma2(d[x], y[x], U[x]);
+                    r[x] = mul2(d[x], m[i]);   // f; m is zero for absent channels
+                    if constexpr (kLayer) a = add2(a, r[x]);
+                    b = fma2(r[x], y[x], b);
+                }
             }
             // the stage has been read by every thread once they meet in this sum
             if (p.post != ROPE3D_NORM_NONE) {
@@ -1293,56 +1330,83 @@ __global__ void __launch_bounds__(kGeneralThreads) block_norm_back_cols_kernel(c
     }
 }
 
-// The chunks' partial sums, added in chunk order: 32 channels a block, 16 rows
-// of threads each over every 16th chunk of a group, then those in order.
+// The chunks' partial sums of one group (blockIdx.y), or the weights' of all
+// chunks, 32 channels a block: 16 rows of threads each add every 16th chunk,
+// several loads in flight, then those sums in order. Where several groups make
+// up the weights' gradients, their parts go to p.group_sums, [groups][2][channels],
+// and block_norm_groups_kernel adds them.
 constexpr int kFinishRows = 16;
 
 __global__ void __launch_bounds__(32 * kFinishRows) block_norm_finish_kernel(const __grid_constant__ NormParams p) {
     __shared__ float part[3][kFinishRows][32];
     grid_wait();
     grid_release();
-    const int lane = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, ty = threadIdx.x >> 5, g = int(blockIdx.y);
     const int c = int(blockIdx.x) * 32 + lane;
     const int param_type = p.param_f32 ? ROPE3D_F32 : p.dtype;
-    float wq = 0.0f, wp = 0.0f;
-    const int sets = p.groups_per_chunk ? 1 : p.groups, per = p.groups_per_chunk ? p.chunks : p.chunks_per_group;
-    for (int g = 0; g < sets; ++g) {
-        float s[3] = {0.0f, 0.0f, 0.0f};
-        if (c < p.channels)
-            for (int i = ty; i < per; i += kFinishRows) {
-                const float *src = p.part + ((long long)g * per + i) * 3 * p.channels + c;
+    const int per = p.groups_per_chunk ? p.chunks : p.chunks_per_group;
+    // which of the three sums exist: S with a pre weight or scale, and so on
+    const bool want[3] = {p.d_pre_weight || p.d_scale, p.d_shift != nullptr, p.d_post_weight || p.d_gate};
+    float s[3] = {0.0f, 0.0f, 0.0f};
+    if (c < p.channels) {
+        const float *src = p.part + (long long)g * per * 3 * p.channels + c;
+        const long long step = 3ll * p.channels;
 #pragma unroll
-                for (int k = 0; k < 3; ++k)
-                    if (k != 1 || p.d_shift) s[k] += src[(long long)k * p.channels];   // the shift's sums may be absent
-            }
+        for (int k = 0; k < 3; ++k) {
+            if (!want[k]) continue;
+            int i = ty;
+            for (; i + 7 * kFinishRows < per; i += 8 * kFinishRows) {
+                float v[8];
 #pragma unroll
-        for (int k = 0; k < 3; ++k) part[k][ty][lane] = s[k];
-        __syncthreads();
-        if (ty == 0 && c < p.channels) {
+                for (int u = 0; u < 8; ++u) v[u] = __ldcs(src + (i + u * kFinishRows) * step + (long long)k * p.channels);
 #pragma unroll
-            for (int k = 0; k < 3; ++k) {
-                s[k] = 0.0f;
-                for (int i = 0; i < kFinishRows; ++i) s[k] += part[k][i][lane];
+                for (int u = 0; u < 8; ++u) s[k] += v[u];
             }
-            if (p.groups_per_chunk) {
-                wq += s[0];
-                wp += s[2];
-            } else {
-                RowOps og{p, 0, g, 0.0f, 1.0f, 0.0f, 1.0f};
-                const long long at = g * p.ldgrad + c;
-                if (p.d_scale) store1(p.d_scale, at, og.wq(c) * s[0], param_type);
-                if (p.d_shift) store1(p.d_shift, at, s[1], param_type);
-                if (p.d_gate) store1(p.d_gate, at, og.wp(c) * s[2], param_type);
-                wq += og.scale1(c) * s[0];
-                wp += og.gate(c) * s[2];
-            }
+            for (; i < per; i += kFinishRows) s[k] += __ldcs(src + i * step + (long long)k * p.channels);
         }
-        __syncthreads();
     }
-    if (ty == 0 && c < p.channels) {
-        if (p.d_pre_weight) store1(p.d_pre_weight, c, wq, param_type);
-        if (p.d_post_weight) store1(p.d_post_weight, c, wp, param_type);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) part[k][ty][lane] = s[k];
+    __syncthreads();
+    if (ty != 0 || c >= p.channels) return;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        s[k] = 0.0f;
+        for (int i = 0; i < kFinishRows; ++i) s[k] += part[k][i][lane];
     }
+    float wq = s[0], wp = s[2];
+    if (!p.groups_per_chunk) {
+        const RowOps og{p, 0, g, 0.0f, 1.0f, 0.0f, 1.0f};
+        const long long at = g * p.ldgrad + c;
+        if (p.d_scale) store1(p.d_scale, at, og.wq(c) * s[0], param_type);
+        if (p.d_shift) store1(p.d_shift, at, s[1], param_type);
+        if (p.d_gate) store1(p.d_gate, at, og.wp(c) * s[2], param_type);
+        wq *= og.scale1(c);
+        wp *= og.gate(c);
+        if (p.group_sums) {
+            float *dst = p.group_sums + (long long)g * 2 * p.channels + c;
+            dst[0] = wq;
+            dst[p.channels] = wp;
+            return;
+        }
+    }
+    if (p.d_pre_weight) store1(p.d_pre_weight, c, wq, param_type);
+    if (p.d_post_weight) store1(p.d_post_weight, c, wp, param_type);
+}
+
+__global__ void __launch_bounds__(128) block_norm_groups_kernel(const __grid_constant__ NormParams p) {
+    grid_wait();
+    grid_release();
+    const int c = int(blockIdx.x * 128 + threadIdx.x);
+    if (c >= p.channels) return;
+    const int param_type = p.param_f32 ? ROPE3D_F32 : p.dtype;
+    float wq = 0.0f, wp = 0.0f;
+    for (int g = 0; g < p.groups; ++g) {
+        wq += p.group_sums[(long long)g * 2 * p.channels + c];
+        wp += p.group_sums[((long long)g * 2 + 1) * p.channels + c];
+    }
+    if (p.d_pre_weight) store1(p.d_pre_weight, c, wq, param_type);
+    if (p.d_post_weight) store1(p.d_post_weight, c, wp, param_type);
 }
 
 // ---- host ------------------------------------------------------------------------------------
@@ -1703,14 +1767,16 @@ int backward(const rope3d_block_norm_backward_args *a, bool run, bool check_devi
     const bool partial = p.sums && (!p.groups_per_chunk || a->d_post_weight || a->d_pre_weight);
     const int64_t part_bytes = partial ? up(int64_t(p.chunks) * 3 * C * 4, 256) : 0;
     const int64_t stat_bytes = t.vecs || !p.sums ? 0 : up(R * 8 * 4, 256);
+    const bool by_group = partial && !p.groups_per_chunk && G > 1 && (a->d_post_weight || a->d_pre_weight);
+    const int64_t group_bytes = by_group ? up(G * 2 * C * 4, 256) : 0, bytes = part_bytes + stat_bytes + group_bytes;
     if (need) {
-        *need = part_bytes + stat_bytes;
+        *need = bytes;
         return ROPE3D_OK;
     }
-    if (part_bytes + stat_bytes) {
+    if (bytes) {
         if (!a->workspace) return ROPE3D_ERR_NULL;
-        if (a->workspace_bytes < part_bytes + stat_bytes) return ROPE3D_ERR_SCRATCH;
-        s[16] = Span{a->workspace, part_bytes + stat_bytes, 0, 256};
+        if (a->workspace_bytes < bytes) return ROPE3D_ERR_SCRATCH;
+        s[16] = Span{a->workspace, bytes, 0, 256};
         for (int i = 0; i < 16; ++i)
             if (overlap(s[16], s[i])) return ROPE3D_ERR_ALIAS;
     } else {
@@ -1721,6 +1787,7 @@ int backward(const rope3d_block_norm_backward_args *a, bool run, bool check_devi
     if (rc != ROPE3D_OK || !run) return rc;
     char *ws = static_cast<char *>(a->workspace);
     p.part = partial ? reinterpret_cast<float *>(ws) : nullptr;
+    p.group_sums = by_group ? reinterpret_cast<float *>(ws + part_bytes + stat_bytes) : nullptr;
     if (ring) {
         t_norm_kernel = 3;
         const bool layer = p.post == ROPE3D_NORM_LAYER || p.pre == ROPE3D_NORM_LAYER, full = C == shape.threads * kRingE;
@@ -1755,9 +1822,12 @@ int backward(const rope3d_block_norm_backward_args *a, bool run, bool check_devi
             if (rc != ROPE3D_OK) return rc;
         }
     }
-    if (partial)
-        return launch(block_norm_finish_kernel, dim3(unsigned((C + 31) / 32)), dim3(32 * kFinishRows), 0, p, st);
-    return ROPE3D_OK;
+    if (!partial) return ROPE3D_OK;
+    // in split mode the groups are at most the chunks' target: far below 65535
+    rc = launch(block_norm_finish_kernel, dim3(unsigned((C + 31) / 32), unsigned(p.groups_per_chunk ? 1 : G)),
+                dim3(32 * kFinishRows), 0, p, st);
+    if (rc != ROPE3D_OK || !by_group) return rc;
+    return launch(block_norm_groups_kernel, dim3(unsigned((C + 127) / 128)), dim3(128), 0, p, st);
 }
 
 }  // namespace
