@@ -109,7 +109,8 @@ struct Out {
     void *p;          // null: not written
     long long ld;     // elements from row to row
     int f32;
-    int tma;          // rows are 16-byte multiples: stored through the tensor map
+    int vec;          // rows start on 16-byte boundaries
+    int tma;          // and are stored through the tensor map
 };
 
 struct Maps {
@@ -125,45 +126,51 @@ struct Params {
     Out out[3];               // plain: one a batch; gated: h, g, u; back: dg, du, h
     const void *g, *u;        // back: the kept projections
     long long ldp;
-    int pre_f32, pre_vec;     // they are fp32; their rows are 16-byte multiples
+    int pre_f32, pre_vec;     // they are fp32; their rows start on 32-byte boundaries
     int rows_n, stages;       // stream kernel: MMA N, ring slots
+    // tile kernel: tiles computed by one pair each, then the rest, `split` units
+    // each of a part of the k range; the units' fp32 sums
+    int whole, split, units;
+    float *part;
 };
 
-// 16 consecutive elements of a kept projection, zeros past its end.
-__device__ __forceinline__ void load_pre16(float *v, const void *base, long long off, int valid,
-                                           const Params &p) {
-    if (p.pre_vec && valid >= 16) {
-        if (p.pre_f32) {
-            const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + off);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float4 t = s[i];
-                v[4 * i] = t.x; v[4 * i + 1] = t.y; v[4 * i + 2] = t.z; v[4 * i + 3] = t.w;
+// 16 consecutive elements of a kept projection on their way: the bits as they
+// lie in memory (32 bytes of 16-bit or 64 bytes of fp32 values).
+struct Pre16 {
+    uint32_t w[16];
+    __device__ __forceinline__ void load8(int at, const void *src) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[at]), "=r"(w[at + 1]), "=r"(w[at + 2]), "=r"(w[at + 3]), "=r"(w[at + 4]),
+                       "=r"(w[at + 5]), "=r"(w[at + 6]), "=r"(w[at + 7])
+                     : "l"(src));
+    }
+    // elements off .. off + 15 of `base`, the first `valid` of which exist
+    __device__ __forceinline__ void load(const void *base, long long off, int valid, const Params &p) {
+        if (p.pre_vec && valid >= 16) {
+            if (p.pre_f32) {
+                load8(0, static_cast<const float *>(base) + off);
+                load8(8, static_cast<const float *>(base) + off + 8);
+            } else {
+                load8(0, static_cast<const uint16_t *>(base) + off);
             }
+            return;
+        }
+        if (p.pre_f32) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                w[i] = i < valid ? __float_as_uint(static_cast<const float *>(base)[off + i]) : 0u;
         } else {
-            const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + off);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint4 t = s[i];
-                const uint32_t w[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 f = unpack2(w[j], p.f16);
-                    v[8 * i + 2 * j] = f.x;
-                    v[8 * i + 2 * j + 1] = f.y;
-                }
+            for (int i = 0; i < 8; ++i) {
+                const uint16_t *s = static_cast<const uint16_t *>(base) + off + 2 * i;
+                w[i] = (2 * i < valid ? uint32_t(s[0]) : 0u) | (2 * i + 1 < valid ? uint32_t(s[1]) << 16 : 0u);
             }
         }
-        return;
     }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        v[i] = 0.0f;
-        if (i < valid)
-            v[i] = p.pre_f32 ? static_cast<const float *>(base)[off + i]
-                             : unpack1(static_cast<const uint16_t *>(base)[off + i], p.f16);
+    __device__ __forceinline__ float2 pair(int i, const Params &p) const {
+        return p.pre_f32 ? make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])) : unpack2(w[i], p.f16);
     }
-}
+};
 
 // ---- many tokens: 256-row tiles of CTA pairs -------------------------------------
 //
@@ -181,6 +188,11 @@ __device__ __forceinline__ void load_pre16(float *v, const void *base, long long
 // double-buffered, so the epilogue of a tile runs under the next tile's MMAs.
 // Persistent: cluster c computes tiles c, c + clusters, ... in an order that
 // walks groups of 8 tile rows, so that the tiles in flight share operands in L2.
+//
+// The tiles that would leave most pairs idle in the last round are split along k
+// where that is faster (launch_tile): `split` units each leave the fp32 sums of
+// their part in the workspace, and ffn_finish_kernel adds them in order and runs
+// the epilogue. No pair waits for another.
 //
 // Epilogue stores go through 2 KB staging boxes (32 rows x 64 bytes, the
 // 64-byte swizzle keeps the writes free of bank conflicts) and TMA, four boxes
@@ -213,6 +225,18 @@ __device__ __forceinline__ Tile tile_at(const Params &p, int t) {
     x.m0 = first + t % rows;
     x.n0 = t / rows;
     return x;
+}
+
+// A unit of work: a tile, or (part >= 0) a part of one tile's k range.
+struct Unit {
+    int tile, part, k_lo, k_hi;
+};
+
+__device__ __forceinline__ Unit unit_at(const Params &p, int u) {
+    const int nk = p.nk0 + p.nk1;
+    if (u < p.whole) return Unit{u, -1, 0, nk};
+    const int i = u - p.whole, t = i / p.split, part = i - t * p.split;
+    return Unit{p.whole + t, i, int((long long)nk * part / p.split), int((long long)nk * (part + 1) / p.split)};
 }
 
 // Epilogue stores of one warp.
@@ -248,6 +272,12 @@ __device__ __forceinline__ void store_words(Boxes &bx, const uint32_t *w, const 
     }
     const int row = row0 + bx.lane;
     if (row >= m) return;
+    if (o.vec && col + (o.f32 ? 16 : 32) <= n) {
+        uint4 *d = reinterpret_cast<uint4 *>(static_cast<char *>(o.p) + (row * o.ld + col) * (o.f32 ? 4 : 2));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        return;
+    }
     if (o.f32) {
         float *d = static_cast<float *>(o.p) + row * o.ld + col;
 #pragma unroll
@@ -283,6 +313,51 @@ __device__ __forceinline__ void store_pre32(Boxes &bx, const float *v, const Out
     }
 }
 
+// The epilogues, on 32 columns of each lane's row (row0 + lane), from `col` on.
+__device__ __forceinline__ void finish_plain(Boxes &bx, const float *v, const Params &p, const CUtensorMap *c, int z,
+                                             int row0, int col) {
+    uint32_t w[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) w[e] = pack2(v[2 * e], v[2 * e + 1], p.f16);
+    store_words(bx, w, p.out[z], c + z, row0, col, p.m, p.n);
+}
+
+__device__ __forceinline__ void finish_gated(Boxes &bx, const float *g, const float *u, const Params &p,
+                                             const CUtensorMap *c, int row0, int col) {
+    store_pre32(bx, g, p.out[1], c + 1, row0, col, p);
+    store_pre32(bx, u, p.out[2], c + 2, row0, col, p);
+    if (!p.out[0].p) return;
+    uint32_t w[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const float h0 = activation<false>(g[2 * e], p.act, nullptr) * u[2 * e];
+        const float h1 = activation<false>(g[2 * e + 1], p.act, nullptr) * u[2 * e + 1];
+        w[e] = pack2(h0, h1, p.f16);
+    }
+    store_words(bx, w, p.out[0], c, row0, col, p.m, p.n);
+}
+
+// dg, du and h of 16 columns, packed, from dh and the kept projections.
+__device__ __forceinline__ void back16(const float *dh, const Pre16 &g, const Pre16 &u, const Params &p, uint32_t *wg,
+                                       uint32_t *wu, uint32_t *wh) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float2 gg = g.pair(e, p), uu = u.pair(e, p);
+        float s0, s1;
+        const float a0 = activation<true>(gg.x, p.act, &s0), a1 = activation<true>(gg.y, p.act, &s1);
+        wg[e] = pack2(dh[2 * e] * uu.x * s0, dh[2 * e + 1] * uu.y * s1, p.f16);
+        wu[e] = pack2(dh[2 * e] * a0, dh[2 * e + 1] * a1, p.f16);
+        wh[e] = pack2(a0 * uu.x, a1 * uu.y, p.f16);
+    }
+}
+
+__device__ __forceinline__ void store_back(Boxes &bx, const uint32_t *wg, const uint32_t *wu, const uint32_t *wh,
+                                           const Params &p, const CUtensorMap *c, int row0, int col) {
+    store_words(bx, wg, p.out[0], c, row0, col, p.m, p.n);
+    store_words(bx, wu, p.out[1], c + 1, row0, col, p.m, p.n);
+    store_words(bx, wh, p.out[2], c + 2, row0, col, p.m, p.n);
+}
+
 template <int kBN, int kLayout, int kEpi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 ffn_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
@@ -302,8 +377,6 @@ ffn_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Param
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_rank();
-    const int nk = p.nk0 + p.nk1;
-    const int tiles = p.tiles_m * p.tiles_n * p.batch;
     const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
     if (tid == 0) {
@@ -335,12 +408,13 @@ ffn_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Param
     if (warp == 0) {
         if (lane == 0) {
             int it = 0;
-            for (int t = first; t < tiles && !dead; t += step) {
-                const Tile x = tile_at(p, t);
+            for (int t = first; t < p.units && !dead; t += step) {
+                const Unit un = unit_at(p, t);
+                const Tile x = tile_at(p, un.tile);
                 const int m0 = x.m0 * 256 + int(rank) * 128;
                 // gated: this CTA's rows are of Wg (rank 0) or Wu (rank 1)
                 const int n0 = kEpi == kGated ? x.n0 * kBRows : x.n0 * kBN + int(rank) * kBRows;
-                for (int kb = 0; kb < nk; ++kb, ++it) {
+                for (int kb = un.k_lo; kb < un.k_hi; ++kb, ++it) {
                     const int s = it % kStages;
                     const uint32_t use = uint32_t(it / kStages);
                     if (it >= kStages && !mbar_wait(empty(s), (use - 1) & 1u, dead, &g_ffn_wait_timeouts)) break;
@@ -372,12 +446,13 @@ ffn_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Param
         if (rank == 0 && lane == 0) {
             const uint32_t id = idesc(256, kBN, !p.f16, kAMn, kBMn);
             int it = 0, i = 0;
-            for (int t = first; t < tiles && !dead; t += step, ++i) {
+            for (int t = first; t < p.units && !dead; t += step, ++i) {
+                const Unit un = unit_at(p, t);
                 const int b = i & 1;
                 if (i >= 2 && !mbar_wait(acc_empty(b), uint32_t(i / 2 - 1) & 1u, dead, &g_ffn_wait_timeouts)) break;
                 tc_fence_after();
                 const uint32_t d = tmem + uint32_t(b) * 256;
-                for (int kb = 0; kb < nk; ++kb, ++it) {
+                for (int kb = un.k_lo; kb < un.k_hi; ++kb, ++it) {
                     const int s = it % kStages;
                     if (!mbar_wait(full(s), uint32_t(it / kStages) & 1u, dead, &g_ffn_wait_timeouts)) break;
                     tc_fence_after();
@@ -387,7 +462,7 @@ ffn_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Param
                         // 16 elements of k: 32 bytes of a K-major row, 16 rows of an MN-major tile
                         const uint64_t da = kAMn ? sdesc(sa + j * 2048, 8192, 1024) : sdesc(sa + j * 32, 16, 1024);
                         const uint64_t db = kBMn ? sdesc(sb + j * 2048, 8192, 1024) : sdesc(sb + j * 32, 16, 1024);
-                        mma<true>(d, da, db, id, (kb | j) != 0);
+                        mma<true>(d, da, db, id, kb > un.k_lo || j > 0);
                     }
                     commit_pair(empty(s));
                 }
@@ -398,86 +473,76 @@ ffn_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Param
         const int quad = warp & 3, half = (warp - 4) >> 2;
         Boxes bx{boxes + uint32_t(warp - 4) * kBoxes * kBoxBytes, 0, lane};
         int i = 0;
-        for (int t = first; t < tiles && !dead; t += step, ++i) {
-            const Tile x = tile_at(p, t);
+        for (int t = first; t < p.units && !dead; t += step, ++i) {
+            const Unit un = unit_at(p, t);
+            const Tile x = tile_at(p, un.tile);
             const int b = i & 1;
             const int row0 = x.m0 * 256 + int(rank) * 128 + quad * 32;
-            const int row = row0 + lane;
             const uint32_t d = tmem + uint32_t(b) * 256 + (uint32_t(quad) << 21);
-            const bool row_ok = row < p.m;
-            if (!mbar_wait(acc_full(b), uint32_t(i / 2) & 1u, dead, &g_ffn_wait_timeouts)) break;
-            tc_fence_after();
             constexpr int kCols = kEpi == kGated ? kBRows / 2 : kBN / 2;   // columns of this warp
             const int c0 = half * kCols;
             const int n0 = x.n0 * (kEpi == kGated ? kBRows : kBN) + c0;
+            [[maybe_unused]] Pre16 g[2], u[2];
+            [[maybe_unused]] auto fetch = [&](int c, int to) {   // the kept projections of 16 columns
+                const int row = row0 + lane, col = n0 + c;
+                const int valid = row < p.m ? p.n - col : 0;
+                g[to].load(p.g, row * p.ldp + col, valid, p);
+                u[to].load(p.u, row * p.ldp + col, valid, p);
+            };
+            if (kEpi == kBack && un.part < 0) fetch(0, 0);   // on their way while the products finish
+            if (!mbar_wait(acc_full(b), uint32_t(i / 2) & 1u, dead, &g_ffn_wait_timeouts)) break;
+            tc_fence_after();
+            if (un.part >= 0) {
+                // fp32 sums of this part: [8 groups of 32 rows][kBN columns][32 rows]
+                float *dst = p.part + ((long long)un.part * 8 + rank * 4 + quad) * (kBN * 32) + lane;
 #pragma unroll 1
-            for (int c = 0; c < kCols; c += 32) {
-                const int col = n0 + c;
-                float v[32];
-                tmem_ld16(v, d + uint32_t(c0 + c));
-                tmem_ld16(v + 16, d + uint32_t(c0 + c + 16));
-                if constexpr (kEpi == kGated) {
-                    float u[32];
-                    tmem_ld16(u, d + uint32_t(kBRows + c0 + c));
-                    tmem_ld16(u + 16, d + uint32_t(kBRows + c0 + c + 16));
+                for (int c = 0; c < kBN / 2; c += 16) {
+                    float v[16];
+                    const int at = half * (kBN / 2) + c;
+                    tmem_ld16(v, d + uint32_t(at));
                     tmem_wait();
                     tmem_tie16(v);
-                    tmem_tie16(v + 16);
-                    tmem_tie16(u);
-                    tmem_tie16(u + 16);
-                    store_pre32(bx, v, p.out[1], &maps.c[1], row0, col, p);
-                    store_pre32(bx, u, p.out[2], &maps.c[2], row0, col, p);
-                    if (p.out[0].p) {
-                        uint32_t w[16];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float h0 = activation<false>(v[2 * e], p.act, nullptr) * u[2 * e];
-                            const float h1 = activation<false>(v[2 * e + 1], p.act, nullptr) * u[2 * e + 1];
-                            w[e] = pack2(h0, h1, p.f16);
-                        }
-                        store_words(bx, w, p.out[0], &maps.c[0], row0, col, p.m, p.n);
-                    }
-                } else if constexpr (kEpi == kBack) {
+                    for (int e = 0; e < 16; ++e) dst[(at + e) * 32] = v[e];
+                }
+            } else if constexpr (kEpi == kBack) {
+                // 16 columns at a time, the next ones' projections on their way
+#pragma unroll 1
+                for (int c = 0; c < kCols; c += 32) {
                     uint32_t wg[16], wu[16], wh[16];
-                    tmem_wait();
-                    tmem_tie16(v);
-                    tmem_tie16(v + 16);
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        float g[16], u[16];
-                        const int valid = row_ok ? p.n - (col + 16 * q) : 0;
-                        const long long off = row * p.ldp + col + 16 * q;
-                        load_pre16(g, p.g, off, valid, p);
-                        load_pre16(u, p.u, off, valid, p);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            float dg[2], du[2], hh[2];
-#pragma unroll
-                            for (int o = 0; o < 2; ++o) {
-                                const float dh = v[16 * q + 2 * e + o];
-                                float slope;
-                                const float a = activation<true>(g[2 * e + o], p.act, &slope);
-                                dg[o] = dh * u[2 * e + o] * slope;
-                                du[o] = dh * a;
-                                hh[o] = a * u[2 * e + o];
-                            }
-                            wg[8 * q + e] = pack2(dg[0], dg[1], p.f16);
-                            wu[8 * q + e] = pack2(du[0], du[1], p.f16);
-                            wh[8 * q + e] = pack2(hh[0], hh[1], p.f16);
-                        }
+                        float v[16];
+                        tmem_ld16(v, d + uint32_t(c0 + c + 16 * q));
+                        if (c + 16 * q + 16 < kCols) fetch(c + 16 * q + 16, 1 - q);
+                        tmem_wait();
+                        tmem_tie16(v);
+                        back16(v, g[q], u[q], p, wg + 8 * q, wu + 8 * q, wh + 8 * q);
                     }
-                    store_words(bx, wg, p.out[0], &maps.c[0], row0, col, p.m, p.n);
-                    store_words(bx, wu, p.out[1], &maps.c[1], row0, col, p.m, p.n);
-                    store_words(bx, wh, p.out[2], &maps.c[2], row0, col, p.m, p.n);
-                } else {
-                    tmem_wait();
-                    tmem_tie16(v);
-                    tmem_tie16(v + 16);
-                    uint32_t w[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) w[e] = pack2(v[2 * e], v[2 * e + 1], p.f16);
-                    const int z = kLayout == kMM ? x.z : 0;
-                    store_words(bx, w, p.out[z], &maps.c[z], row0, col, p.m, p.n);
+                    store_back(bx, wg, wu, wh, p, maps.c, row0, n0 + c);
+                }
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < kCols; c += 32) {
+                    float v[32];
+                    tmem_ld16(v, d + uint32_t(c0 + c));
+                    tmem_ld16(v + 16, d + uint32_t(c0 + c + 16));
+                    if constexpr (kEpi == kGated) {
+                        float w[32];
+                        tmem_ld16(w, d + uint32_t(kBRows + c0 + c));
+                        tmem_ld16(w + 16, d + uint32_t(kBRows + c0 + c + 16));
+                        tmem_wait();
+                        tmem_tie16(v);
+                        tmem_tie16(v + 16);
+                        tmem_tie16(w);
+                        tmem_tie16(w + 16);
+                        finish_gated(bx, v, w, p, maps.c, row0, n0 + c);
+                    } else {
+                        tmem_wait();
+                        tmem_tie16(v);
+                        tmem_tie16(v + 16);
+                        finish_plain(bx, v, p, maps.c, kLayout == kMM ? x.z : 0, row0, n0 + c);
+                    }
                 }
             }
             // this warp's reads of the accumulators are done
@@ -494,6 +559,52 @@ ffn_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Param
     cluster_sync();
     tc_fence_after();
     if (warp == 2) tmem_free<true>(tmem, 512);
+}
+
+// The split tiles: each warp adds the parts' sums of 32 rows x 32 columns (of
+// both halves where gated) in order and runs the epilogue on them.
+template <int kBN, int kEpi>
+__global__ void __launch_bounds__(128) ffn_finish_kernel(const __grid_constant__ Params p) {
+    grid_wait();
+    grid_release();
+    constexpr int kTileCols = kEpi == kGated ? kBN / 2 : kBN, kChunks = kTileCols / 32;
+    const int lane = threadIdx.x & 31;
+    int w = int(blockIdx.x) * 4 + int(threadIdx.x >> 5);   // (split tile, group of rows, chunk of columns)
+    const int chunk = w % kChunks;
+    w /= kChunks;
+    const int rows = w & 7, tile = w >> 3;
+    const Tile x = tile_at(p, p.whole + tile);
+    const int row0 = x.m0 * 256 + rows * 32, col = x.n0 * kTileCols + chunk * 32;
+    if (row0 >= p.m || col >= p.n) return;
+    auto sums = [&](float *v, int c) {
+        const float *src = p.part + ((long long)tile * p.split * 8 + rows) * (kBN * 32) + c * 32 + lane;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = 0.0f;
+        for (int i = 0; i < p.split; ++i, src += 8ll * kBN * 32)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] += __ldcs(src + e * 32);
+    };
+    Boxes bx{0, 0, lane};   // no staging: the outputs' tma is off
+    float v[32];
+    sums(v, chunk * 32);
+    if constexpr (kEpi == kGated) {
+        float u[32];
+        sums(u, kBN / 2 + chunk * 32);
+        finish_gated(bx, v, u, p, nullptr, row0, col);
+    } else if constexpr (kEpi == kBack) {
+        uint32_t wg[16], wu[16], wh[16];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            Pre16 g, u;
+            const int row = row0 + lane, valid = row < p.m ? p.n - (col + 16 * q) : 0;
+            g.load(p.g, row * p.ldp + col + 16 * q, valid, p);
+            u.load(p.u, row * p.ldp + col + 16 * q, valid, p);
+            back16(v + 16 * q, g, u, p, wg + 8 * q, wu + 8 * q, wh + 8 * q);
+        }
+        store_back(bx, wg, wu, wh, p, nullptr, row0, col);
+    } else {
+        finish_plain(bx, v, p, nullptr, x.z, row0, col);
+    }
 }
 
 // ---- few tokens: weights streamed once ---------------------------------------------
@@ -728,9 +839,11 @@ struct Mat {
     int64_t rows, cols, ld;
 };
 
-bool tma_ok(const void *p, int64_t ld, int elem_bytes) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * elem_bytes % 16 == 0;
+bool rows_on(const void *p, int64_t ld, int elem_bytes, int boundary) {
+    return reinterpret_cast<uintptr_t>(p) % uintptr_t(boundary) == 0 && ld * elem_bytes % boundary == 0;
 }
+
+bool tma_ok(const void *p, int64_t ld, int elem_bytes) { return rows_on(p, ld, elem_bytes, 16); }
 
 bool make_map(CUtensorMap *map, const void *p, int64_t rows, int64_t cols, int64_t ld, int elem_bytes,
               bool f16, int box_cols, int box_rows, bool swizzle128) {
@@ -761,7 +874,8 @@ int set_outs(Params &p, Maps &maps, const Out *outs, int count, int64_t rows, in
         p.out[i] = outs[i];
         Out &o = p.out[i];
         const int es = o.f32 ? 4 : 2;
-        o.tma = maps_too && o.p && tma_ok(o.p, o.ld, es);
+        o.vec = o.p && tma_ok(o.p, o.ld, es);
+        o.tma = maps_too && o.vec;
         if (o.tma && !make_map(&maps.c[i], o.p, rows, cols, o.ld, es, p.f16, o.f32 ? 16 : 32, 32, false))
             return ROPE3D_ERR_CUDA;
     }
@@ -801,8 +915,57 @@ bool tile_ready(int *clusters) {
     return true;
 }
 
+// How a product of the tile kernel is divided: the tile's width, the tiles that
+// one pair of CTAs computes each, and into how many parts of k the others are
+// split.
+struct Plan {
+    int bn, cols;            // MMA N; columns of a tile (half of it where gated)
+    int64_t tiles, whole;
+    int split;
+    int64_t units() const { return whole + (tiles - whole) * split; }
+    int64_t part_bytes() const { return (tiles - whole) * split * 256 * bn * 4; }
+};
+
+// The fastest division by a model of the time in microseconds: `kPairs` pairs
+// run rounds of tiles; 64 of k cost a pair 0.355 us at 256 columns and 0.28 us at
+// 128 (4096 x 4096 of k = 16384, bf16: the narrow tile reads the operands from L2
+// at the same rate for half of the products), a tile's start and end about 1.5;
+// split tiles add a kernel (3) and their sums' bytes, written and read. Measured:
+// 8192 x 2048 of k = 8192 takes 256 us at 128 columns in 7 rounds, 181 us at 256
+// in 4 and 165 us with the last round's 28 tiles split in two.
+// The GB300's 76 pairs are written here, not asked, so that the workspace's size
+// is known without a device; the kernel's units run on any number of pairs.
+constexpr int64_t kPairs = 76;
+
+Plan plan_tiles(int64_t m, int64_t n, int64_t batch, int nk, bool gated) {
+    Plan best{};
+    double best_time = 1e30;
+    for (int bn : {256, 128}) {
+        Plan c{};
+        c.bn = bn;
+        c.cols = gated ? bn / 2 : bn;
+        c.tiles = (m + 255) / 256 * ((n + c.cols - 1) / c.cols) * batch;
+        const double per_k = bn == 256 ? 0.355 : 0.28;
+        const int64_t rounds = c.tiles / kPairs, rest = c.tiles % kPairs;
+        for (int s = 1; s <= 32; ++s) {
+            if (s > 1 && (rest == 0 || nk / s < 4)) break;
+            double t = double(rounds) * (nk * per_k + 1.5);
+            if (rest) t += double((rest * s + kPairs - 1) / kPairs) * (double((nk + s - 1) / s) * per_k + 1.5);
+            if (s > 1) t += 3.0 + double(rest * s) * 256 * bn * 8 / 4.0e6;
+            if (t < best_time) {
+                best_time = t;
+                best = c;
+                best.split = s;
+                best.whole = s > 1 ? c.tiles - rest : c.tiles;
+            }
+        }
+    }
+    return best;
+}
+
 template <int kBN, int kLayout, int kEpi>
-int launch_tile_as(Params &p, Maps &maps, const Mat *a, const Mat *b, int segs, cudaStream_t st) {
+int launch_tile_as(const Plan &plan, Params &p, Maps &maps, const Mat *a, const Mat *b, int segs, void *part,
+                   cudaStream_t st) {
     int clusters = 0;
     if (!tile_ready<kBN, kLayout, kEpi>(&clusters)) return ROPE3D_ERR_CUDA;
     constexpr bool kAMn = kLayout == kMM, kBMn = kLayout != kKK;
@@ -811,13 +974,14 @@ int launch_tile_as(Params &p, Maps &maps, const Mat *a, const Mat *b, int segs, 
         if (!operand_map(&maps.a[i], a[i], kAMn, 128, p.f16)) return ROPE3D_ERR_CUDA;
     for (int i = 0; i < nb; ++i)
         if (!operand_map(&maps.b[i], b[i], kBMn, kBN / 2, p.f16)) return ROPE3D_ERR_CUDA;
-    const int64_t tn = kEpi == kGated ? kBN / 2 : kBN;
-    const int64_t tiles_m = (int64_t(p.m) + 255) / 256, tiles_n = (int64_t(p.n) + tn - 1) / tn;
-    if (tiles_m * tiles_n * p.batch > (int64_t(1) << 30)) return ROPE3D_ERR_SHAPE;
-    p.tiles_m = int(tiles_m);
-    p.tiles_n = int(tiles_n);
+    p.tiles_m = int((int64_t(p.m) + 255) / 256);
+    p.tiles_n = int((int64_t(p.n) + plan.cols - 1) / plan.cols);
+    p.whole = int(plan.whole);
+    p.split = plan.split;
+    p.units = int(plan.units());
+    p.part = static_cast<float *>(part);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(2 * std::min<int64_t>(clusters, tiles_m * tiles_n * p.batch)));
+    cfg.gridDim = dim3(unsigned(2 * std::min(clusters, p.units)));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = tile_smem<kBN>();
     cfg.stream = st;
@@ -827,6 +991,17 @@ int launch_tile_as(Params &p, Maps &maps, const Mat *a, const Mat *b, int segs, 
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, ffn_tile_kernel<kBN, kLayout, kEpi>, maps, p) != cudaSuccess) {
+        cudaGetLastError();
+        return ROPE3D_ERR_CUDA;
+    }
+    if (plan.whole == plan.tiles) return ROPE3D_OK;
+    Params f = p;
+    for (Out &o : f.out) o.tma = 0;
+    const int64_t warps = (plan.tiles - plan.whole) * 8 * (plan.cols / 32);
+    cfg.gridDim = dim3(unsigned(warps / 4));
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
+    if (cudaLaunchKernelEx(&cfg, ffn_finish_kernel<kBN, kEpi>, f) != cudaSuccess) {
         cudaGetLastError();
         return ROPE3D_ERR_CUDA;
     }
@@ -841,22 +1016,12 @@ int sm_count() {
     return n;
 }
 
-// 256 columns a tile, or 128 where that fills the last round of clusters
-// better: a tile of 128 columns takes a little over half of the time of one of
-// 256 (the pair then reads A's bytes for half of the products).
 template <int kLayout, int kEpi>
-int launch_tile(Params &p, Maps &maps, const Mat *a, const Mat *b, int segs, cudaStream_t st) {
-    const int sms = sm_count();
-    if (sms <= 0) return ROPE3D_ERR_CUDA;
-    const int64_t pairs = std::max(1, sms / 2);
-    auto rounds = [&](int64_t tn) {
-        const int64_t tiles = (int64_t(p.m) + 255) / 256 * ((int64_t(p.n) + tn - 1) / tn) * p.batch;
-        return (tiles + pairs - 1) / pairs;
-    };
-    const int64_t wide = kEpi == kGated ? 128 : 256;
-    if (rounds(wide / 2) * 54 < rounds(wide) * 100)
-        return launch_tile_as<128, kLayout, kEpi>(p, maps, a, b, segs, st);
-    return launch_tile_as<256, kLayout, kEpi>(p, maps, a, b, segs, st);
+int launch_tile(Params &p, Maps &maps, const Mat *a, const Mat *b, int segs, void *part, cudaStream_t st) {
+    const Plan plan = plan_tiles(p.m, p.n, p.batch, p.nk0 + p.nk1, kEpi == kGated);
+    if (plan.units() > (int64_t(1) << 30)) return ROPE3D_ERR_SHAPE;
+    if (plan.bn == 128) return launch_tile_as<128, kLayout, kEpi>(plan, p, maps, a, b, segs, part, st);
+    return launch_tile_as<256, kLayout, kEpi>(plan, p, maps, a, b, segs, part, st);
 }
 
 // Few tokens. w: the weights (two where gated or of two segments), x: the
@@ -1039,7 +1204,7 @@ Params base_params(int32_t dtype, int32_t act) {
 thread_local int t_ffn_kernel = 0;   // 1 tile, 2 stream kernel: this thread's last forward or dx product
 
 // h (may be null), g, u (may be null) of x.
-int project(const Mat &x, const Mat &wg, const Mat &wu, Out h, Out g, Out u, int32_t dtype, int32_t act,
+int project(const Mat &x, const Mat &wg, const Mat &wu, Out h, Out g, Out u, int32_t dtype, int32_t act, void *part,
             cudaStream_t st) {
     Maps maps;
     Params p = base_params(dtype, act);
@@ -1055,7 +1220,7 @@ int project(const Mat &x, const Mat &wg, const Mat &wu, Out h, Out g, Out u, int
     }
     p.m = int(x.rows);
     p.n = int(wg.rows);
-    return launch_tile<kKK, kGated>(p, maps, &x, w, 1, st);
+    return launch_tile<kKK, kGated>(p, maps, &x, w, 1, part, st);
 }
 
 // One body for the call and for its workspace query (launch = false; *need
@@ -1073,11 +1238,16 @@ int forward(const rope3d_gated_ffn_args *a, bool launch, bool check_device, int6
     const int pre_es = a->pre_dtype == ROPE3D_F32 ? 4 : 2;
     Mat x{a->x, M, D, a->x_stride}, wg{a->w_gate, F, D, a->w_gate_stride}, wu{a->w_up, F, D, a->w_up_stride},
         wd{a->w_down, D, F, a->w_down_stride};
+    const int nkd = blocks64(D), nkf = blocks64(F);
+    const int64_t part_bytes = M <= kStreamTokens ? 0
+                                                  : std::max(plan_tiles(M, F, 1, nkd, true).part_bytes(),
+                                                             plan_tiles(M, D, 1, nkf, false).part_bytes());
     Carver size{nullptr};
     {
         Mat t[4] = {x, wg, wu, wd};
         for (Mat &m : t) aligned(m, size, false, st);
         size.take(M * up(F, 64) * 2);
+        size.take(part_bytes);
     }
     if (need) *need = size.used;
     const Span in[4] = {span(x.p, M, D, x.ld, 2), span(wg.p, F, D, wg.ld, 2), span(wu.p, F, D, wu.ld, 2),
@@ -1094,15 +1264,15 @@ int forward(const rope3d_gated_ffn_args *a, bool launch, bool check_device, int6
     for (Mat *m : {&x, &wg, &wu, &wd})
         if ((rc = aligned(*m, ws, true, st)) != ROPE3D_OK) return rc;
     const int64_t hld = up(F, 64);
-    void *hbuf = ws.take(M * hld * 2);
+    void *hbuf = ws.take(M * hld * 2), *part = ws.take(part_bytes);
     const int f32 = a->gate_pre && a->pre_dtype == ROPE3D_F32;
-    rc = project(x, wg, wu, Out{hbuf, hld, 0, 0}, Out{a->gate_pre, a->pre_stride, f32, 0},
-                 Out{a->up_pre, a->pre_stride, f32, 0}, a->dtype, a->act, st);
+    rc = project(x, wg, wu, Out{hbuf, hld, 0, 0, 0}, Out{a->gate_pre, a->pre_stride, f32, 0, 0},
+                 Out{a->up_pre, a->pre_stride, f32, 0, 0}, a->dtype, a->act, part, st);
     if (rc != ROPE3D_OK) return rc;
     const Mat h{hbuf, M, F, hld};
     Maps maps;
     Params p = base_params(a->dtype, a->act);
-    const Out y{a->y, a->y_stride, 0, 0};
+    const Out y{a->y, a->y_stride, 0, 0, 0};
     p.nk0 = blocks64(F);
     if ((rc = set_outs(p, maps, &y, 1, M, D, M > kStreamTokens)) != ROPE3D_OK) return rc;
     t_ffn_kernel = M <= kStreamTokens ? 2 : 1;
@@ -1113,7 +1283,7 @@ int forward(const rope3d_gated_ffn_args *a, bool launch, bool check_device, int6
     }
     p.m = int(M);
     p.n = int(D);
-    return launch_tile<kKK, kPlain>(p, maps, &h, &wd, 1, st);
+    return launch_tile<kKK, kPlain>(p, maps, &h, &wd, 1, part, st);
 }
 
 int backward(const rope3d_gated_ffn_backward_args *a, bool launch, bool check_device, int64_t *need,
@@ -1137,6 +1307,20 @@ int backward(const rope3d_gated_ffn_backward_args *a, bool launch, bool check_de
     Mat dy{a->dy, M, D, a->dy_stride}, x{a->x, M, D, a->x_stride}, wg{a->w_gate, F, D, a->w_gate_stride},
         wu{a->w_up, F, D, a->w_up_stride}, wd{a->w_down, D, F, a->w_down_stride};
     const int64_t hld = up(F, 64);
+    const bool few = M <= kStreamTokens;
+    const int nkd = blocks64(D), nkf = blocks64(F), nkm = blocks64(M);
+    // the split products' sums, one product at a time
+    int64_t part_bytes = 0;
+    auto need_part = [&](int64_t m, int64_t n, int64_t batch, int nk, bool gated) {
+        part_bytes = std::max(part_bytes, plan_tiles(m, n, batch, nk, gated).part_bytes());
+    };
+    if (!few) {
+        if (again) need_part(M, F, 1, nkd, true);
+        need_part(M, F, 1, nkd, false);
+        need_part(M, D, 1, 2 * nkf, false);
+    }
+    need_part(F, D, 2, nkm, false);
+    need_part(D, F, 1, nkm, false);
     Carver size{nullptr};
     {
         Mat t[5] = {dy, x, wg, wu, wd};
@@ -1144,6 +1328,7 @@ int backward(const rope3d_gated_ffn_backward_args *a, bool launch, bool check_de
         for (int i = 0; i < 3; ++i) size.take(M * hld * 2);
         if (again)
             for (int i = 0; i < 2; ++i) size.take(M * hld * 4);
+        size.take(part_bytes);
     }
     if (need) *need = size.used;
     const Span in[7] = {span(dy.p, M, D, dy.ld, 2), span(x.p, M, D, x.ld, 2), span(wg.p, F, D, wg.ld, 2),
@@ -1164,66 +1349,67 @@ int backward(const rope3d_gated_ffn_backward_args *a, bool launch, bool check_de
     void *dgb = ws.take(M * hld * 2), *dub = ws.take(M * hld * 2), *hb = ws.take(M * hld * 2);
     const void *g = a->gate_pre, *u = a->up_pre;
     int64_t ldp = a->pre_stride;
+    void *gb = again ? ws.take(M * hld * 4) : nullptr, *ub = again ? ws.take(M * hld * 4) : nullptr;
+    void *part = ws.take(part_bytes);
     if (again) {
-        void *gb = ws.take(M * hld * 4), *ub = ws.take(M * hld * 4);
-        rc = project(x, wg, wu, Out{nullptr, 0, 0, 0}, Out{gb, hld, 1, 0}, Out{ub, hld, 1, 0}, a->dtype, a->act, st);
+        rc = project(x, wg, wu, Out{nullptr, 0, 0, 0, 0}, Out{gb, hld, 1, 0, 0}, Out{ub, hld, 1, 0, 0}, a->dtype, a->act, part, st);
         if (rc != ROPE3D_OK) return rc;
         g = gb;
         u = ub;
         ldp = hld;
     }
-    const bool few = M <= kStreamTokens;
     t_ffn_kernel = few ? 2 : 1;
     Maps maps;
     {
         // dh = dy Wd, and from it dg, du and h
         Params p = base_params(a->dtype, a->act);
-        const Out outs[3] = {Out{dgb, hld, 0, 0}, Out{dub, hld, 0, 0}, Out{a->dw_down ? hb : nullptr, hld, 0, 0}};
+        const Out outs[3] = {Out{dgb, hld, 0, 0, 0}, Out{dub, hld, 0, 0, 0},
+                             Out{a->dw_down ? hb : nullptr, hld, 0, 0, 0}};
         if ((rc = set_outs(p, maps, outs, 3, M, F, !few)) != ROPE3D_OK) return rc;
         p.nk0 = blocks64(D);
         p.g = g;
         p.u = u;
         p.ldp = ldp;
         p.pre_f32 = pre_es == 4;
-        p.pre_vec = tma_ok(g, ldp, pre_es) && tma_ok(u, ldp, pre_es);
+        p.pre_vec = rows_on(g, ldp, pre_es, 32) && rows_on(u, ldp, pre_es, 32);
         p.m = int(few ? F : M);
         p.n = int(few ? M : F);
         rc = few ? launch_stream<true, kBack>(p, maps, &wd, &dy, 1, st)
-                 : launch_tile<kKM, kBack>(p, maps, &dy, &wd, 1, st);
+                 : launch_tile<kKM, kBack>(p, maps, &dy, &wd, 1, part, st);
         if (rc != ROPE3D_OK) return rc;
     }
     const Mat dg{dgb, M, F, hld}, du{dub, M, F, hld}, h{hb, M, F, hld};
     if (a->dx) {
         Params p = base_params(a->dtype, a->act);
-        const Out o{a->dx, a->dx_stride, 0, 0};
+        const Out o{a->dx, a->dx_stride, 0, 0, 0};
         const Mat t[2] = {dg, du}, w[2] = {wg, wu};
         if ((rc = set_outs(p, maps, &o, 1, M, D, !few)) != ROPE3D_OK) return rc;
         p.nk0 = p.nk1 = blocks64(F);
         p.m = int(few ? D : M);
         p.n = int(few ? M : D);
-        rc = few ? launch_stream<true, kPlain>(p, maps, w, t, 2, st) : launch_tile<kKM, kPlain>(p, maps, t, w, 2, st);
+        rc = few ? launch_stream<true, kPlain>(p, maps, w, t, 2, st) : launch_tile<kKM, kPlain>(p, maps, t, w, 2, part, st);
         if (rc != ROPE3D_OK) return rc;
     }
     if (a->dw_gate) {
         // both in one launch: a batch of two products
         Params p = base_params(a->dtype, a->act);
-        const Out o[2] = {Out{a->dw_gate, a->dw_gate_stride, 0, 0}, Out{a->dw_up, a->dw_up_stride, 0, 0}};
+        const Out o[2] = {Out{a->dw_gate, a->dw_gate_stride, 0, 0, 0}, Out{a->dw_up, a->dw_up_stride, 0, 0, 0}};
         const Mat t[2] = {dg, du}, xs[2] = {x, x};
         if ((rc = set_outs(p, maps, o, 2, F, D, true)) != ROPE3D_OK) return rc;
         p.nk0 = blocks64(M);
         p.m = int(F);
         p.n = int(D);
         p.batch = 2;
-        if ((rc = launch_tile<kMM, kPlain>(p, maps, t, xs, 2, st)) != ROPE3D_OK) return rc;
+        if ((rc = launch_tile<kMM, kPlain>(p, maps, t, xs, 2, part, st)) != ROPE3D_OK) return rc;
     }
     if (a->dw_down) {
         Params p = base_params(a->dtype, a->act);
-        const Out o{a->dw_down, a->dw_down_stride, 0, 0};
+        const Out o{a->dw_down, a->dw_down_stride, 0, 0, 0};
         if ((rc = set_outs(p, maps, &o, 1, D, F, true)) != ROPE3D_OK) return rc;
         p.nk0 = blocks64(M);
         p.m = int(D);
         p.n = int(F);
-        if ((rc = launch_tile<kMM, kPlain>(p, maps, &dy, &h, 1, st)) != ROPE3D_OK) return rc;
+        if ((rc = launch_tile<kMM, kPlain>(p, maps, &dy, &h, 1, part, st)) != ROPE3D_OK) return rc;
     }
     return ROPE3D_OK;
 }
