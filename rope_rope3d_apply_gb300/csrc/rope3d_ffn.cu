@@ -44,34 +44,48 @@ __device__ unsigned int g_ffn_wait_timeouts;
 
 // ---- the element-wise part ---------------------------------------------------
 
-__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
+__device__ __forceinline__ float rcp(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ float sigmoid(float v) { return rcp(1.0f + __expf(-v)); }
 
 // act(g) and, where kGrad, act'(g). GELU's tanh form is g * sigmoid(2 z) with
 // z = sqrt(2 / pi) (g + 0.044715 g^3), from 1 + tanh(z) = 2 sigmoid(2 z); past
 // |g| = 50 the sigmoid is 0 or 1 and its slope 0 in fp32, and the clamp keeps
 // g^3 finite.
-template <bool kGrad>
-__device__ __forceinline__ float activation(float g, int act, float *grad) {
-    if (act == ROPE3D_ACT_SILU) {
+template <int kAct, bool kGrad>
+__device__ __forceinline__ float activation(float g, float *grad) {
+    if constexpr (kAct == ROPE3D_ACT_SILU) {
         const float q = sigmoid(g);
         if constexpr (kGrad) *grad = q * (1.0f + g * (1.0f - q));
         return g * q;
-    }
-    if (act == ROPE3D_ACT_GELU_TANH) {
+    } else if constexpr (kAct == ROPE3D_ACT_GELU_TANH) {
         const float c = fminf(fmaxf(g, -50.0f), 50.0f);
         const float s = c * c;
         const float q = sigmoid(c * (1.5957691216f + 0.0713548163f * s));
         if constexpr (kGrad) *grad = q + g * (q * (1.0f - q) * (1.5957691216f + 0.2140644488f * s));
         return g * q;
+    } else {
+        const float cdf = 0.5f * (1.0f + erff(g * 0.7071067812f));
+        if constexpr (kGrad) *grad = cdf + g * (0.3989422804f * __expf(-0.5f * g * g));
+        return g * cdf;
     }
-    const float cdf = 0.5f * (1.0f + erff(g * 0.7071067812f));
-    if constexpr (kGrad) *grad = cdf + g * (0.3989422804f * __expf(-0.5f * g * g));
-    return g * cdf;
 }
 
-__device__ __forceinline__ uint32_t pack2(float a, float b, bool f16) {
+template <bool kGrad>
+__device__ __forceinline__ float activation_of(float g, int act, float *grad) {
+    return act == ROPE3D_ACT_SILU        ? activation<ROPE3D_ACT_SILU, kGrad>(g, grad)
+           : act == ROPE3D_ACT_GELU_TANH ? activation<ROPE3D_ACT_GELU_TANH, kGrad>(g, grad)
+                                         : activation<ROPE3D_ACT_GELU_ERF, kGrad>(g, grad);
+}
+
+template <bool kF16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
     uint32_t w;
-    if (f16) {
+    if constexpr (kF16) {
         const __half2 h = __floats2half2_rn(a, b);
         memcpy(&w, &h, 4);
     } else {
@@ -81,13 +95,15 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, bool f16) {
     return w;
 }
 
-__device__ __forceinline__ float2 unpack2(uint32_t w, bool f16) {
-    if (f16) {
+template <bool kF16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+    if constexpr (kF16) {
         __half2 h;
         memcpy(&h, &w, 4);
         return __half22float2(h);
+    } else {
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
     }
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
 __device__ __forceinline__ uint16_t pack1(float a, bool f16) {
@@ -167,8 +183,19 @@ struct Pre16 {
             }
         }
     }
-    __device__ __forceinline__ float2 pair(int i, const Params &p) const {
-        return p.pre_f32 ? make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])) : unpack2(w[i], p.f16);
+    template <bool kF16>
+    __device__ __forceinline__ void values(float *v, const Params &p) const {
+        if (p.pre_f32) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(w[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 f = unpack2<kF16>(w[i]);
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            }
+        }
     }
 };
 
@@ -247,53 +274,63 @@ struct Boxes {
 };
 
 // 16 words (64 bytes: 32 16-bit or 16 fp32 elements) of each lane's row, from
-// column `col` of output o; the warp's rows are row0 .. row0 + 31.
+// column `col` of output o; the warp's rows are row0 .. row0 + 31. Through a
+// staging box: a TMA store, or where TMA cannot address the rows, stores of
+// consecutive elements by consecutive lanes.
 __device__ __forceinline__ void store_words(Boxes &bx, const uint32_t *w, const Out &o,
                                             const CUtensorMap *map, int row0, int col, int m, int n) {
     if (!o.p || row0 >= m || col >= n) return;
-    if (o.tma) {
-        const uint32_t box = bx.base + uint32_t(bx.next & (kBoxes - 1)) * kBoxBytes;
-        ++bx.next;
-        if (bx.lane == 0) bulk_wait_read<kBoxes - 1>();
-        __syncwarp();
-        const uint32_t row = box + uint32_t(bx.lane) * 64, sw = (uint32_t(bx.lane) >> 1) & 3;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                         ::"r"(row + ((uint32_t(c) ^ sw) << 4)), "r"(w[4 * c]), "r"(w[4 * c + 1]),
-                           "r"(w[4 * c + 2]), "r"(w[4 * c + 3]) : "memory");
-        fence_async_smem();
-        __syncwarp();
-        if (bx.lane == 0) {
-            tma_store2(map, box, col, row0);
-            bulk_commit();
-        }
-        return;
-    }
-    const int row = row0 + bx.lane;
-    if (row >= m) return;
-    if (o.vec && col + (o.f32 ? 16 : 32) <= n) {
-        uint4 *d = reinterpret_cast<uint4 *>(static_cast<char *>(o.p) + (row * o.ld + col) * (o.f32 ? 4 : 2));
+    if (!o.tma && o.vec && col + (o.f32 ? 16 : 32) <= n) {
+        if (row0 + bx.lane >= m) return;
+        uint4 *d = reinterpret_cast<uint4 *>(static_cast<char *>(o.p) +
+                                             ((row0 + bx.lane) * o.ld + col) * (o.f32 ? 4 : 2));
 #pragma unroll
         for (int i = 0; i < 4; ++i) d[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         return;
     }
-    if (o.f32) {
-        float *d = static_cast<float *>(o.p) + row * o.ld + col;
+    const uint32_t box = bx.base + uint32_t(bx.next & (kBoxes - 1)) * kBoxBytes;
+    ++bx.next;
+    if (bx.lane == 0) bulk_wait_read<kBoxes - 1>();
+    __syncwarp();
+    const uint32_t row = box + uint32_t(bx.lane) * 64, sw = (uint32_t(bx.lane) >> 1) & 3;
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (col + i < n) d[i] = __uint_as_float(w[i]);
+    for (int c = 0; c < 4; ++c)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                     ::"r"(row + ((uint32_t(c) ^ sw) << 4)), "r"(w[4 * c]), "r"(w[4 * c + 1]),
+                       "r"(w[4 * c + 2]), "r"(w[4 * c + 3]) : "memory");
+    if (o.tma) {
+        fence_async_smem();
+        __syncwarp();
+        if (bx.lane == 0) tma_store2(map, box, col, row0);
     } else {
-        uint16_t *d = static_cast<uint16_t *>(o.p) + row * o.ld + col;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            if (col + 2 * i < n) d[2 * i] = uint16_t(w[i]);
-            if (col + 2 * i + 1 < n) d[2 * i + 1] = uint16_t(w[i] >> 16);
+        __syncwarp();
+        const int rows = min(32, m - row0);
+        if (o.f32) {   // two rows at a time
+            const int e = bx.lane & 15;
+            for (int i = bx.lane >> 4; i < rows; i += 2) {
+                float v;
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v)
+                             : "r"(box + uint32_t(i) * 64 + (((uint32_t(e) >> 2) ^ ((uint32_t(i) >> 1) & 3)) << 4) + (e & 3) * 4)
+                             : "memory");
+                if (col + e < n) static_cast<float *>(o.p)[(row0 + i) * o.ld + col + e] = v;
+            }
+        } else {
+            const int e = bx.lane;
+            for (int i = 0; i < rows; ++i) {
+                uint16_t v;
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v)
+                             : "r"(box + uint32_t(i) * 64 + (((uint32_t(e) >> 3) ^ ((uint32_t(i) >> 1) & 3)) << 4) + (e & 7) * 2)
+                             : "memory");
+                if (col + e < n) static_cast<uint16_t *>(o.p)[(row0 + i) * o.ld + col + e] = v;
+            }
         }
+        __syncwarp();
     }
+    if (bx.lane == 0) bulk_commit();   // (an empty group where nothing was copied: boxes are counted by groups)
 }
 
 // A kept projection, 32 columns of each lane's row, in its own type.
+template <bool kF16>
 __device__ __forceinline__ void store_pre32(Boxes &bx, const float *v, const Out &o,
                                             const CUtensorMap *map, int row0, int col,
                                             const Params &p) {
@@ -308,46 +345,51 @@ __device__ __forceinline__ void store_pre32(Boxes &bx, const float *v, const Out
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1], p.f16);
+        for (int i = 0; i < 16; ++i) w[i] = pack2<kF16>(v[2 * i], v[2 * i + 1]);
         store_words(bx, w, o, map, row0, col, p.m, p.n);
     }
 }
 
 // The epilogues, on 32 columns of each lane's row (row0 + lane), from `col` on.
+template <bool kF16>
 __device__ __forceinline__ void finish_plain(Boxes &bx, const float *v, const Params &p, const CUtensorMap *c, int z,
                                              int row0, int col) {
     uint32_t w[16];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) w[e] = pack2(v[2 * e], v[2 * e + 1], p.f16);
+    for (int e = 0; e < 16; ++e) w[e] = pack2<kF16>(v[2 * e], v[2 * e + 1]);
     store_words(bx, w, p.out[z], c + z, row0, col, p.m, p.n);
 }
 
+template <bool kF16, int kAct>
 __device__ __forceinline__ void finish_gated(Boxes &bx, const float *g, const float *u, const Params &p,
                                              const CUtensorMap *c, int row0, int col) {
-    store_pre32(bx, g, p.out[1], c + 1, row0, col, p);
-    store_pre32(bx, u, p.out[2], c + 2, row0, col, p);
+    store_pre32<kF16>(bx, g, p.out[1], c + 1, row0, col, p);
+    store_pre32<kF16>(bx, u, p.out[2], c + 2, row0, col, p);
     if (!p.out[0].p) return;
     uint32_t w[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-        const float h0 = activation<false>(g[2 * e], p.act, nullptr) * u[2 * e];
-        const float h1 = activation<false>(g[2 * e + 1], p.act, nullptr) * u[2 * e + 1];
-        w[e] = pack2(h0, h1, p.f16);
+        const float h0 = activation<kAct, false>(g[2 * e], nullptr) * u[2 * e];
+        const float h1 = activation<kAct, false>(g[2 * e + 1], nullptr) * u[2 * e + 1];
+        w[e] = pack2<kF16>(h0, h1);
     }
     store_words(bx, w, p.out[0], c, row0, col, p.m, p.n);
 }
 
 // dg, du and h of 16 columns, packed, from dh and the kept projections.
+template <bool kF16, int kAct>
 __device__ __forceinline__ void back16(const float *dh, const Pre16 &g, const Pre16 &u, const Params &p, uint32_t *wg,
                                        uint32_t *wu, uint32_t *wh) {
+    float gv[16], uv[16];
+    g.values<kF16>(gv, p);
+    u.values<kF16>(uv, p);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const float2 gg = g.pair(e, p), uu = u.pair(e, p);
         float s0, s1;
-        const float a0 = activation<true>(gg.x, p.act, &s0), a1 = activation<true>(gg.y, p.act, &s1);
-        wg[e] = pack2(dh[2 * e] * uu.x * s0, dh[2 * e + 1] * uu.y * s1, p.f16);
-        wu[e] = pack2(dh[2 * e] * a0, dh[2 * e + 1] * a1, p.f16);
-        wh[e] = pack2(a0 * uu.x, a1 * uu.y, p.f16);
+        const float a0 = activation<kAct, true>(gv[2 * e], &s0), a1 = activation<kAct, true>(gv[2 * e + 1], &s1);
+        wg[e] = pack2<kF16>(dh[2 * e] * uv[2 * e] * s0, dh[2 * e + 1] * uv[2 * e + 1] * s1);
+        wu[e] = pack2<kF16>(dh[2 * e] * a0, dh[2 * e + 1] * a1);
+        wh[e] = pack2<kF16>(a0 * uv[2 * e], a1 * uv[2 * e + 1]);
     }
 }
 
@@ -358,7 +400,7 @@ __device__ __forceinline__ void store_back(Boxes &bx, const uint32_t *wg, const 
     store_words(bx, wh, p.out[2], c + 2, row0, col, p.m, p.n);
 }
 
-template <int kBN, int kLayout, int kEpi>
+template <int kBN, int kLayout, int kEpi, bool kF16, int kAct>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 ffn_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
     constexpr bool kAMn = kLayout == kMM, kBMn = kLayout != kKK;
@@ -444,7 +486,7 @@ ffn_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Param
         }
     } else if (warp == 1) {
         if (rank == 0 && lane == 0) {
-            const uint32_t id = idesc(256, kBN, !p.f16, kAMn, kBMn);
+            const uint32_t id = idesc(256, kBN, !kF16, kAMn, kBMn);
             int it = 0, i = 0;
             for (int t = first; t < p.units && !dead; t += step, ++i) {
                 const Unit un = unit_at(p, t);
@@ -489,7 +531,19 @@ ffn_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Param
                 g[to].load(p.g, row * p.ldp + col, valid, p);
                 u[to].load(p.u, row * p.ldp + col, valid, p);
             };
-            if (kEpi == kBack && un.part < 0) fetch(0, 0);   // on their way while the products finish
+            // ... and 32 columns on their way to L2, two chunks before they are fetched
+            [[maybe_unused]] auto ahead = [&](int c) {
+                const int row = row0 + lane, col = n0 + c;
+                if (c >= kCols || row >= p.m || col >= p.n) return;
+                const long long off = (row * p.ldp + col) * (p.pre_f32 ? 4 : 2);
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char *>(p.g) + off));
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char *>(p.u) + off));
+            };
+            if (kEpi == kBack && un.part < 0) {   // on their way while the products finish
+                fetch(0, 0);
+                ahead(32);
+                ahead(64);
+            }
             if (!mbar_wait(acc_full(b), uint32_t(i / 2) & 1u, dead, &g_ffn_wait_timeouts)) break;
             tc_fence_after();
             if (un.part >= 0) {
@@ -510,6 +564,7 @@ ffn_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Param
 #pragma unroll 1
                 for (int c = 0; c < kCols; c += 32) {
                     uint32_t wg[16], wu[16], wh[16];
+                    ahead(c + 96);
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         float v[16];
@@ -517,7 +572,7 @@ ffn_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Param
                         if (c + 16 * q + 16 < kCols) fetch(c + 16 * q + 16, 1 - q);
                         tmem_wait();
                         tmem_tie16(v);
-                        back16(v, g[q], u[q], p, wg + 8 * q, wu + 8 * q, wh + 8 * q);
+                        back16<kF16, kAct>(v, g[q], u[q], p, wg + 8 * q, wu + 8 * q, wh + 8 * q);
                     }
                     store_back(bx, wg, wu, wh, p, maps.c, row0, n0 + c);
                 }
@@ -536,12 +591,12 @@ ffn_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Param
                         tmem_tie16(v + 16);
                         tmem_tie16(w);
                         tmem_tie16(w + 16);
-                        finish_gated(bx, v, w, p, maps.c, row0, n0 + c);
+                        finish_gated<kF16, kAct>(bx, v, w, p, maps.c, row0, n0 + c);
                     } else {
                         tmem_wait();
                         tmem_tie16(v);
                         tmem_tie16(v + 16);
-                        finish_plain(bx, v, p, maps.c, kLayout == kMM ? x.z : 0, row0, n0 + c);
+                        finish_plain<kF16>(bx, v, p, maps.c, kLayout == kMM ? x.z : 0, row0, n0 + c);
                     }
                 }
             }
@@ -563,11 +618,12 @@ ffn_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Param
 
 // The split tiles: each warp adds the parts' sums of 32 rows x 32 columns (of
 // both halves where gated) in order and runs the epilogue on them.
-template <int kBN, int kEpi>
+template <int kBN, int kEpi, bool kF16, int kAct>
 __global__ void __launch_bounds__(128) ffn_finish_kernel(const __grid_constant__ Params p) {
     grid_wait();
     grid_release();
     constexpr int kTileCols = kEpi == kGated ? kBN / 2 : kBN, kChunks = kTileCols / 32;
+    __shared__ __align__(1024) uint8_t staging[4 * kBoxes * kBoxBytes];
     const int lane = threadIdx.x & 31;
     int w = int(blockIdx.x) * 4 + int(threadIdx.x >> 5);   // (split tile, group of rows, chunk of columns)
     const int chunk = w % kChunks;
@@ -584,13 +640,13 @@ __global__ void __launch_bounds__(128) ffn_finish_kernel(const __grid_constant__
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] += __ldcs(src + e * 32);
     };
-    Boxes bx{0, 0, lane};   // no staging: the outputs' tma is off
+    Boxes bx{smem_u32(staging) + uint32_t(threadIdx.x >> 5) * kBoxes * kBoxBytes, 0, lane};   // (the outputs' tma is off)
     float v[32];
     sums(v, chunk * 32);
     if constexpr (kEpi == kGated) {
         float u[32];
         sums(u, kBN / 2 + chunk * 32);
-        finish_gated(bx, v, u, p, nullptr, row0, col);
+        finish_gated<kF16, kAct>(bx, v, u, p, nullptr, row0, col);
     } else if constexpr (kEpi == kBack) {
         uint32_t wg[16], wu[16], wh[16];
 #pragma unroll
@@ -599,11 +655,11 @@ __global__ void __launch_bounds__(128) ffn_finish_kernel(const __grid_constant__
             const int row = row0 + lane, valid = row < p.m ? p.n - (col + 16 * q) : 0;
             g.load(p.g, row * p.ldp + col + 16 * q, valid, p);
             u.load(p.u, row * p.ldp + col + 16 * q, valid, p);
-            back16(v + 16 * q, g, u, p, wg + 8 * q, wu + 8 * q, wh + 8 * q);
+            back16<kF16, kAct>(v + 16 * q, g, u, p, wg + 8 * q, wu + 8 * q, wh + 8 * q);
         }
         store_back(bx, wg, wu, wh, p, nullptr, row0, col);
     } else {
-        finish_plain(bx, v, p, nullptr, x.z, row0, col);
+        finish_plain<kF16>(bx, v, p, nullptr, x.z, row0, col);
     }
 }
 
@@ -776,7 +832,7 @@ ffn_stream_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Par
         if constexpr (kEpi == kGated) {
             put(p.out[1], acc[0]);
             put(p.out[2], acc[1]);
-            put(p.out[0], activation<false>(acc[0], p.act, nullptr) * acc[1]);
+            put(p.out[0], activation_of<false>(acc[0], p.act, nullptr) * acc[1]);
         } else if constexpr (kEpi == kBack) {
             const long long at = tok * p.ldp + col;
             const float g = p.pre_f32 ? static_cast<const float *>(p.g)[at]
@@ -784,7 +840,7 @@ ffn_stream_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Par
             const float u = p.pre_f32 ? static_cast<const float *>(p.u)[at]
                                       : unpack1(static_cast<const uint16_t *>(p.u)[at], p.f16);
             float slope;
-            const float a = activation<true>(g, p.act, &slope);
+            const float a = activation_of<true>(g, p.act, &slope);
             put(p.out[0], acc[0] * u * slope);
             put(p.out[1], acc[0] * a);
             put(p.out[2], a * u);
@@ -798,17 +854,45 @@ ffn_stream_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Par
 
 // ---- rows that TMA cannot address ----------------------------------------------------
 
-// 16-bit rows copied to rows that start on 16-byte boundaries (dst_ld a
-// multiple of 8). One block a row segment; consecutive threads, consecutive
-// elements.
-__global__ void __launch_bounds__(256)
-ffn_align_kernel(const uint16_t *src, long long src_ld, uint16_t *dst, long long dst_ld, int cols,
-                 long long rows) {
+// 16-bit matrices copied to rows that start on 16-byte boundaries (dst_ld a
+// multiple of 8), up to five in one launch. A thread makes 8 elements of a row:
+// eight 2-byte loads (consecutive threads read consecutive bytes), one 16-byte
+// store; what a row has past its last column is not written.
+struct AlignJob {
+    const uint16_t *src;
+    uint16_t *dst;
+    long long src_ld, dst_ld;
+    int cols, vecs;              // 8-element vectors of a row
+    long long first, rows;       // the job's first vector in the launch
+};
+
+struct AlignJobs {
+    AlignJob job[5];
+    int count;
+    long long total;
+};
+
+__global__ void __launch_bounds__(256) ffn_align_kernel(const __grid_constant__ AlignJobs jobs) {
     grid_wait();
     grid_release();
-    for (long long r = blockIdx.y; r < rows; r += gridDim.y)
-        for (int c = blockIdx.x * 2048 + threadIdx.x, i = 0; i < 8 && c < cols; ++i, c += 256)
-            dst[r * dst_ld + c] = src[r * src_ld + c];
+    const long long stride = (long long)gridDim.x * 256;
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < jobs.total; i += stride) {
+        int k = 0;
+        while (k + 1 < jobs.count && i >= jobs.job[k + 1].first) ++k;
+        const AlignJob &j = jobs.job[k];
+        const long long v = i - j.first, row = v / j.vecs;
+        const int c = int(v - row * j.vecs) * 8;
+        const uint16_t *s = j.src + row * j.src_ld + c;
+        uint16_t *d = j.dst + row * j.dst_ld + c;
+        if (c + 8 <= j.cols) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = uint32_t(s[2 * e]) | uint32_t(s[2 * e + 1]) << 16;
+            *reinterpret_cast<uint4 *>(d) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+            for (int e = 0; c + e < j.cols; ++e) d[e] = s[e];
+        }
+    }
 }
 
 // ---- host ---------------------------------------------------------------------------
@@ -883,14 +967,14 @@ int set_outs(Params &p, Maps &maps, const Out *outs, int count, int64_t rows, in
 }
 
 // How many pairs of CTAs the device holds at once (asked once a device).
-template <int kBN, int kLayout, int kEpi>
+template <int kBN, int kLayout, int kEpi, bool kF16, int kAct>
 bool tile_ready(int *clusters) {
     static std::atomic<int> known[64];   // per device, 0 = not asked yet
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
     int c = known[dev].load(std::memory_order_acquire);
     if (c == 0) {
-        auto *fn = ffn_tile_kernel<kBN, kLayout, kEpi>;
+        auto *fn = ffn_tile_kernel<kBN, kLayout, kEpi, kF16, kAct>;
         if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, tile_smem<kBN>()) != cudaSuccess) {
             cudaGetLastError();
             return false;
@@ -963,11 +1047,11 @@ Plan plan_tiles(int64_t m, int64_t n, int64_t batch, int nk, bool gated) {
     return best;
 }
 
-template <int kBN, int kLayout, int kEpi>
+template <int kBN, int kLayout, int kEpi, bool kF16, int kAct>
 int launch_tile_as(const Plan &plan, Params &p, Maps &maps, const Mat *a, const Mat *b, int segs, void *part,
                    cudaStream_t st) {
     int clusters = 0;
-    if (!tile_ready<kBN, kLayout, kEpi>(&clusters)) return ROPE3D_ERR_CUDA;
+    if (!tile_ready<kBN, kLayout, kEpi, kF16, kAct>(&clusters)) return ROPE3D_ERR_CUDA;
     constexpr bool kAMn = kLayout == kMM, kBMn = kLayout != kKK;
     const int nb = kEpi == kGated ? 2 : segs;
     for (int i = 0; i < segs; ++i)
@@ -990,7 +1074,7 @@ int launch_tile_as(const Plan &plan, Params &p, Maps &maps, const Mat *a, const 
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, ffn_tile_kernel<kBN, kLayout, kEpi>, maps, p) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, ffn_tile_kernel<kBN, kLayout, kEpi, kF16, kAct>, maps, p) != cudaSuccess) {
         cudaGetLastError();
         return ROPE3D_ERR_CUDA;
     }
@@ -1001,7 +1085,7 @@ int launch_tile_as(const Plan &plan, Params &p, Maps &maps, const Mat *a, const 
     cfg.gridDim = dim3(unsigned(warps / 4));
     cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = 0;
-    if (cudaLaunchKernelEx(&cfg, ffn_finish_kernel<kBN, kEpi>, f) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, ffn_finish_kernel<kBN, kEpi, kF16, kAct>, f) != cudaSuccess) {
         cudaGetLastError();
         return ROPE3D_ERR_CUDA;
     }
@@ -1016,12 +1100,28 @@ int sm_count() {
     return n;
 }
 
+template <int kValue>
+struct Const {
+    static constexpr int value = kValue;
+};
+
 template <int kLayout, int kEpi>
 int launch_tile(Params &p, Maps &maps, const Mat *a, const Mat *b, int segs, void *part, cudaStream_t st) {
     const Plan plan = plan_tiles(p.m, p.n, p.batch, p.nk0 + p.nk1, kEpi == kGated);
     if (plan.units() > (int64_t(1) << 30)) return ROPE3D_ERR_SHAPE;
-    if (plan.bn == 128) return launch_tile_as<128, kLayout, kEpi>(plan, p, maps, a, b, segs, part, st);
-    return launch_tile_as<256, kLayout, kEpi>(plan, p, maps, a, b, segs, part, st);
+    auto as = [&](auto bn, auto f16, auto act) {
+        return launch_tile_as<decltype(bn)::value, kLayout, kEpi, decltype(f16)::value, decltype(act)::value>(
+            plan, p, maps, a, b, segs, part, st);
+    };
+    auto with_act = [&](auto bn, auto f16) {
+        if constexpr (kEpi != kPlain) {   // (the plain product has no activation)
+            if (p.act == ROPE3D_ACT_GELU_TANH) return as(bn, f16, Const<ROPE3D_ACT_GELU_TANH>{});
+            if (p.act == ROPE3D_ACT_GELU_ERF) return as(bn, f16, Const<ROPE3D_ACT_GELU_ERF>{});
+        }
+        return as(bn, f16, Const<ROPE3D_ACT_SILU>{});
+    };
+    auto with_type = [&](auto bn) { return p.f16 ? with_act(bn, Const<1>{}) : with_act(bn, Const<0>{}); };
+    return plan.bn == 128 ? with_type(Const<128>{}) : with_type(Const<256>{});
 }
 
 // Few tokens. w: the weights (two where gated or of two segments), x: the
@@ -1099,30 +1199,37 @@ struct Carver {
 };
 
 // x as TMA can read it: itself, or a copy in the workspace with its rows on
-// 16-byte boundaries (launched unless only the size is asked for).
-int aligned(Mat &x, Carver &ws, bool launch, cudaStream_t st) {
-    if (tma_ok(x.p, x.ld, 2)) return ROPE3D_OK;
+// 16-byte boundaries, added to `jobs`.
+void aligned(Mat &x, Carver &ws, AlignJobs *jobs) {
+    if (tma_ok(x.p, x.ld, 2)) return;
     const int64_t ld = up(x.cols, 8);
     void *dst = ws.take(x.rows * ld * 2);
-    if (launch) {
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(unsigned((x.cols + 2047) / 2048), unsigned(std::min<int64_t>(x.rows, 65535)));
-        cfg.blockDim = dim3(256);
-        cfg.stream = st;
-        cudaLaunchAttribute attr{};
-        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr.val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        if (cudaLaunchKernelEx(&cfg, ffn_align_kernel, static_cast<const uint16_t *>(x.p), (long long)x.ld,
-                               static_cast<uint16_t *>(dst), (long long)ld, int(x.cols),
-                               (long long)x.rows) != cudaSuccess) {
-            cudaGetLastError();
-            return ROPE3D_ERR_CUDA;
-        }
+    if (jobs) {
+        jobs->job[jobs->count++] = AlignJob{static_cast<const uint16_t *>(x.p), static_cast<uint16_t *>(dst),
+                                            x.ld, ld, int(x.cols), int(ld / 8), jobs->total, x.rows};
+        jobs->total += x.rows * (ld / 8);
     }
     x.p = dst;
     x.ld = ld;
+}
+
+int launch_align(const AlignJobs &jobs, cudaStream_t st) {
+    if (!jobs.count) return ROPE3D_OK;
+    const int sms = sm_count();
+    if (sms <= 0) return ROPE3D_ERR_CUDA;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(std::min<int64_t>((jobs.total + 255) / 256, int64_t(sms) * 8)));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, ffn_align_kernel, jobs) != cudaSuccess) {
+        cudaGetLastError();
+        return ROPE3D_ERR_CUDA;
+    }
     return ROPE3D_OK;
 }
 
@@ -1245,7 +1352,7 @@ int forward(const rope3d_gated_ffn_args *a, bool launch, bool check_device, int6
     Carver size{nullptr};
     {
         Mat t[4] = {x, wg, wu, wd};
-        for (Mat &m : t) aligned(m, size, false, st);
+        for (Mat &m : t) aligned(m, size, nullptr);
         size.take(M * up(F, 64) * 2);
         size.take(part_bytes);
     }
@@ -1261,8 +1368,9 @@ int forward(const rope3d_gated_ffn_args *a, bool launch, bool check_device, int6
     if (!launch) return ROPE3D_OK;
 
     Carver ws{static_cast<char *>(a->workspace)};
-    for (Mat *m : {&x, &wg, &wu, &wd})
-        if ((rc = aligned(*m, ws, true, st)) != ROPE3D_OK) return rc;
+    AlignJobs jobs{};
+    for (Mat *m : {&x, &wg, &wu, &wd}) aligned(*m, ws, &jobs);
+    if ((rc = launch_align(jobs, st)) != ROPE3D_OK) return rc;
     const int64_t hld = up(F, 64);
     void *hbuf = ws.take(M * hld * 2), *part = ws.take(part_bytes);
     const int f32 = a->gate_pre && a->pre_dtype == ROPE3D_F32;
@@ -1324,7 +1432,7 @@ int backward(const rope3d_gated_ffn_backward_args *a, bool launch, bool check_de
     Carver size{nullptr};
     {
         Mat t[5] = {dy, x, wg, wu, wd};
-        for (Mat &m : t) aligned(m, size, false, st);
+        for (Mat &m : t) aligned(m, size, nullptr);
         for (int i = 0; i < 3; ++i) size.take(M * hld * 2);
         if (again)
             for (int i = 0; i < 2; ++i) size.take(M * hld * 4);
@@ -1344,8 +1452,9 @@ int backward(const rope3d_gated_ffn_backward_args *a, bool launch, bool check_de
     if (!launch) return ROPE3D_OK;
 
     Carver ws{static_cast<char *>(a->workspace)};
-    for (Mat *m : {&dy, &x, &wg, &wu, &wd})
-        if ((rc = aligned(*m, ws, true, st)) != ROPE3D_OK) return rc;
+    AlignJobs jobs{};
+    for (Mat *m : {&dy, &x, &wg, &wu, &wd}) aligned(*m, ws, &jobs);
+    if ((rc = launch_align(jobs, st)) != ROPE3D_OK) return rc;
     void *dgb = ws.take(M * hld * 2), *dub = ws.take(M * hld * 2), *hb = ws.take(M * hld * 2);
     const void *g = a->gate_pre, *u = a->up_pre;
     int64_t ldp = a->pre_stride;
