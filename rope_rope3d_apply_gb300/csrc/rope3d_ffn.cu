@@ -117,8 +117,9 @@ __device__ __forceinline__ float unpack1(uint16_t v, bool f16) {
 // ---- launch description ---------------------------------------------------------
 
 enum Epi { kPlain = 0, kGated = 1, kBack = 2 };
-// operand layouts: K-major (0) or MN-major (1)
-constexpr int kKK = 0, kKM = 1, kMM = 2;
+// operand layouts: both K-major; A K-major and B MN-major; or (the gradients'
+// launch) the latter for dx and both MN-major for the weights' gradients
+constexpr int kKK = 0, kKM = 1, kGrads = 2;
 
 // A matrix written by an epilogue: rows of 16-bit or fp32 elements.
 struct Out {
@@ -130,24 +131,34 @@ struct Out {
 };
 
 struct Maps {
-    CUtensorMap a[2], b[2];   // operands of segments 0 and 1 (gated: b = Wg, Wu)
-    CUtensorMap c[3];         // outputs
+    CUtensorMap a[5], b[5];   // operands: segments 0 and 1 (gated: b = Wg, Wu), then the weights' gradients
+    CUtensorMap c[4];         // outputs
+};
+
+// One product of a launch: its output's size, in elements and in tiles.
+struct Sub {
+    int m, n, tiles_m, tiles_n;
+    __host__ __device__ int tiles() const { return tiles_m * tiles_n; }
 };
 
 struct Params {
-    int m, n;                 // output rows and columns (of one half where gated)
+    int m, n;                 // stream kernel: weight rows, tokens
     int nk0, nk1;             // 64-wide k blocks of the two segments
-    int tiles_m, tiles_n, batch;
     int f16, act;
-    Out out[3];               // plain: one a batch; gated: h, g, u; back: dg, du, h
+    Out out[4];               // gated: h, g, u; back: dg, du, h; else one a product
     const void *g, *u;        // back: the kept projections
     long long ldp;
     int pre_f32, pre_vec;     // they are fp32; their rows start on 32-byte boundaries
     int rows_n, stages;       // stream kernel: MMA N, ring slots
-    // tile kernel: tiles computed by one pair each, then the rest, `split` units
-    // each of a part of the k range; the units' fp32 sums
+    // tile kernel: the products (gradients: dx, dWg, dWu, dWd); of the first
+    // one the tiles computed by one pair each, then the rest, `split` units each
+    // of a part of the k range; the units' fp32 sums
+    Sub sub[4];
     int whole, split, units;
     float *part;
+    // gradients: the weights' tiles and their k blocks; whether dx's units are
+    // the longer ones, and how many of the shorter ones a longer one is worth
+    int weight_units, nkw, dx_first, lag;
 };
 
 // 16 consecutive elements of a kept projection on their way: the bits as they
@@ -237,33 +248,65 @@ constexpr int tile_smem() {
 }
 
 struct Tile {
-    int z, m0, n0;   // batch, first row and first column, in tiles
+    int m0, n0;   // first row and first column, in tiles
 };
 
-__device__ __forceinline__ Tile tile_at(const Params &p, int t) {
-    const int per = p.tiles_m * p.tiles_n;
-    Tile x;
-    x.z = t / per;
-    t -= x.z * per;
+__device__ __forceinline__ Tile tile_at(const Sub &p, int t) {
     const int group = t / (kGroupRows * p.tiles_n);
     const int first = group * kGroupRows;
     const int rows = min(kGroupRows, p.tiles_m - first);
     t -= first * p.tiles_n;
-    x.m0 = first + t % rows;
-    x.n0 = t / rows;
-    return x;
+    return Tile{first + t % rows, t / rows};
 }
 
-// A unit of work: a tile, or (part >= 0) a part of one tile's k range.
+// A unit of work: a tile of a product, or (part >= 0) a part of its k range.
 struct Unit {
-    int tile, part, k_lo, k_hi;
+    int sub, tile, part, k_lo, k_hi;
 };
 
 __device__ __forceinline__ Unit unit_at(const Params &p, int u) {
     const int nk = p.nk0 + p.nk1;
-    if (u < p.whole) return Unit{u, -1, 0, nk};
+    if (u < p.whole) return Unit{0, u, -1, 0, nk};
     const int i = u - p.whole, t = i / p.split, part = i - t * p.split;
-    return Unit{p.whole + t, i, int((long long)nk * part / p.split), int((long long)nk * (part + 1) / p.split)};
+    return Unit{0, p.whole + t, i, int((long long)nk * part / p.split), int((long long)nk * (part + 1) / p.split)};
+}
+
+// The i-th unit of this pair of CTAs; false past its last one. Units go to the
+// pairs in turn. In the gradients' launch the longer kind goes first; the pairs
+// that the last round of it leaves out start on the shorter kind at once and get
+// as many of those more (`lag` each) as the others' last long unit takes.
+template <int kLayout>
+__device__ __forceinline__ bool next_unit(const Params &p, int i, Unit &un) {
+    const int c = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    if constexpr (kLayout != kGrads) {
+        const int u = c + i * pairs;
+        if (u >= p.units) return false;
+        un = unit_at(p, u);
+        return true;
+    } else {
+        const int longs = p.dx_first ? p.units : p.weight_units, shorts = p.dx_first ? p.weight_units : p.units;
+        const int r = longs % pairs, own = longs / pairs + (c < r);
+        int u;
+        bool dx = p.dx_first;
+        if (i < own) {
+            u = c + i * pairs;
+        } else {
+            int j = i - own;
+            const int first = r ? min(shorts, p.lag * (pairs - r)) : 0;   // shared by pairs r ... alone
+            const int mine = c >= r && first > c - r ? (first - (c - r) - 1) / (pairs - r) + 1 : 0;
+            u = j < mine ? (c - r) + j * (pairs - r) : first + c + (j - mine) * pairs;
+            if (u >= shorts) return false;
+            dx = !dx;
+        }
+        if (dx) {
+            un = unit_at(p, u);
+        } else {
+            int z = 1;
+            while (z < 3 && u >= p.sub[z].tiles()) u -= p.sub[z++].tiles();
+            un = Unit{z, u, -1, 0, p.nkw};
+        }
+        return true;
+    }
 }
 
 // Epilogue stores of one warp.
@@ -333,7 +376,7 @@ __device__ __forceinline__ void store_words(Boxes &bx, const uint32_t *w, const 
 template <bool kF16>
 __device__ __forceinline__ void store_pre32(Boxes &bx, const float *v, const Out &o,
                                             const CUtensorMap *map, int row0, int col,
-                                            const Params &p) {
+                                            const Sub &p) {
     if (!o.p) return;
     uint32_t w[16];
     if (o.f32) {
@@ -357,14 +400,14 @@ __device__ __forceinline__ void finish_plain(Boxes &bx, const float *v, const Pa
     uint32_t w[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) w[e] = pack2<kF16>(v[2 * e], v[2 * e + 1]);
-    store_words(bx, w, p.out[z], c + z, row0, col, p.m, p.n);
+    store_words(bx, w, p.out[z], c + z, row0, col, p.sub[z].m, p.sub[z].n);
 }
 
 template <bool kF16, int kAct>
 __device__ __forceinline__ void finish_gated(Boxes &bx, const float *g, const float *u, const Params &p,
                                              const CUtensorMap *c, int row0, int col) {
-    store_pre32<kF16>(bx, g, p.out[1], c + 1, row0, col, p);
-    store_pre32<kF16>(bx, u, p.out[2], c + 2, row0, col, p);
+    store_pre32<kF16>(bx, g, p.out[1], c + 1, row0, col, p.sub[0]);
+    store_pre32<kF16>(bx, u, p.out[2], c + 2, row0, col, p.sub[0]);
     if (!p.out[0].p) return;
     uint32_t w[16];
 #pragma unroll
@@ -373,7 +416,7 @@ __device__ __forceinline__ void finish_gated(Boxes &bx, const float *g, const fl
         const float h1 = activation<kAct, false>(g[2 * e + 1], nullptr) * u[2 * e + 1];
         w[e] = pack2<kF16>(h0, h1);
     }
-    store_words(bx, w, p.out[0], c, row0, col, p.m, p.n);
+    store_words(bx, w, p.out[0], c, row0, col, p.sub[0].m, p.sub[0].n);
 }
 
 // dg, du and h of 16 columns, packed, from dh and the kept projections.
@@ -395,15 +438,15 @@ __device__ __forceinline__ void back16(const float *dh, const Pre16 &g, const Pr
 
 __device__ __forceinline__ void store_back(Boxes &bx, const uint32_t *wg, const uint32_t *wu, const uint32_t *wh,
                                            const Params &p, const CUtensorMap *c, int row0, int col) {
-    store_words(bx, wg, p.out[0], c, row0, col, p.m, p.n);
-    store_words(bx, wu, p.out[1], c + 1, row0, col, p.m, p.n);
-    store_words(bx, wh, p.out[2], c + 2, row0, col, p.m, p.n);
+    store_words(bx, wg, p.out[0], c, row0, col, p.sub[0].m, p.sub[0].n);
+    store_words(bx, wu, p.out[1], c + 1, row0, col, p.sub[0].m, p.sub[0].n);
+    store_words(bx, wh, p.out[2], c + 2, row0, col, p.sub[0].m, p.sub[0].n);
 }
 
 template <int kBN, int kLayout, int kEpi, bool kF16, int kAct>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 ffn_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
-    constexpr bool kAMn = kLayout == kMM, kBMn = kLayout != kKK;
+    constexpr bool kBMn = kLayout != kKK;                 // (A: K-major but for the weights' gradients)
     constexpr int kBRows = kBN / 2;                       // rows of B in this CTA
     constexpr uint32_t kBBytes = kBRows * 128;
     constexpr uint32_t kStageBytes = kABytes + kBBytes;
@@ -419,7 +462,6 @@ ffn_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Param
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_rank();
-    const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -431,8 +473,10 @@ ffn_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Param
             mbar_init(acc_empty(b), 2 * kEpiWarps);
         }
         mbar_fence_init();
-        prefetch_map(&maps.a[0]);
-        prefetch_map(&maps.b[0]);
+        if (p.units > 0) {
+            prefetch_map(&maps.a[0]);
+            prefetch_map(&maps.b[0]);
+        }
     }
     if (warp == 2) tmem_alloc<true>(slot, 512);
     tc_fence_before();
@@ -450,9 +494,10 @@ ffn_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Param
     if (warp == 0) {
         if (lane == 0) {
             int it = 0;
-            for (int t = first; t < p.units && !dead; t += step) {
-                const Unit un = unit_at(p, t);
-                const Tile x = tile_at(p, un.tile);
+            Unit un;
+            for (int i = 0; !dead && next_unit<kLayout>(p, i, un); ++i) {
+                const Tile x = tile_at(p.sub[un.sub], un.tile);
+                const bool a_mn = kLayout == kGrads && un.sub > 0;
                 const int m0 = x.m0 * 256 + int(rank) * 128;
                 // gated: this CTA's rows are of Wg (rank 0) or Wu (rank 1)
                 const int n0 = kEpi == kGated ? x.n0 * kBRows : x.n0 * kBN + int(rank) * kBRows;
@@ -460,15 +505,15 @@ ffn_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Param
                     const int s = it % kStages;
                     const uint32_t use = uint32_t(it / kStages);
                     if (it >= kStages && !mbar_wait(empty(s), (use - 1) & 1u, dead, &g_ffn_wait_timeouts)) break;
-                    const int seg = kb >= p.nk0;
+                    const int seg = un.sub == 0 && kb >= p.nk0;
                     const int k = (seg ? kb - p.nk0 : kb) * 64;
-                    const CUtensorMap *ma = &maps.a[kLayout == kMM ? x.z : seg];
-                    const CUtensorMap *mb = &maps.b[kEpi == kGated ? int(rank) : kLayout == kMM ? x.z : seg];
+                    const CUtensorMap *ma = &maps.a[un.sub ? 1 + un.sub : seg];
+                    const CUtensorMap *mb = &maps.b[kEpi == kGated ? int(rank) : un.sub ? 1 + un.sub : seg];
                     const uint32_t sa = base + uint32_t(s) * kStageBytes, sb = sa + kABytes;
                     // the pair's copies complete on the first CTA's barrier
                     const uint32_t bar = map_rank(full(s), 0);
                     if (rank == 0) mbar_expect_tx(full(s), 2 * kStageBytes);
-                    if constexpr (kAMn) {
+                    if (a_mn) {
                         tma_load2<true>(sa, ma, m0, k, bar);
                         tma_load2<true>(sa + 8192, ma, m0 + 64, k, bar);
                     } else {
@@ -486,10 +531,13 @@ ffn_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Param
         }
     } else if (warp == 1) {
         if (rank == 0 && lane == 0) {
-            const uint32_t id = idesc(256, kBN, !kF16, kAMn, kBMn);
-            int it = 0, i = 0;
-            for (int t = first; t < p.units && !dead; t += step, ++i) {
-                const Unit un = unit_at(p, t);
+            int it = 0;
+            Unit un;
+            for (int i = 0; !dead && next_unit<kLayout>(p, i, un); ++i) {
+                const bool a_mn = kLayout == kGrads && un.sub > 0;
+                const uint32_t id = idesc(256, kBN, !kF16, a_mn, kBMn);
+                // 16 elements of k: 32 bytes of a K-major row, 16 rows of an MN-major tile
+                const uint32_t a_step = a_mn ? 2048 : 32, a_lbo = a_mn ? 8192 : 16;
                 const int b = i & 1;
                 if (i >= 2 && !mbar_wait(acc_empty(b), uint32_t(i / 2 - 1) & 1u, dead, &g_ffn_wait_timeouts)) break;
                 tc_fence_after();
@@ -501,8 +549,7 @@ ffn_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Param
                     const uint32_t sa = base + uint32_t(s) * kStageBytes, sb = sa + kABytes;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        // 16 elements of k: 32 bytes of a K-major row, 16 rows of an MN-major tile
-                        const uint64_t da = kAMn ? sdesc(sa + j * 2048, 8192, 1024) : sdesc(sa + j * 32, 16, 1024);
+                        const uint64_t da = sdesc(sa + j * a_step, a_lbo, 1024);
                         const uint64_t db = kBMn ? sdesc(sb + j * 2048, 8192, 1024) : sdesc(sb + j * 32, 16, 1024);
                         mma<true>(d, da, db, id, kb > un.k_lo || j > 0);
                     }
@@ -514,10 +561,9 @@ ffn_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Param
     } else if (warp >= 4) {
         const int quad = warp & 3, half = (warp - 4) >> 2;
         Boxes bx{boxes + uint32_t(warp - 4) * kBoxes * kBoxBytes, 0, lane};
-        int i = 0;
-        for (int t = first; t < p.units && !dead; t += step, ++i) {
-            const Unit un = unit_at(p, t);
-            const Tile x = tile_at(p, un.tile);
+        Unit un;
+        for (int i = 0; !dead && next_unit<kLayout>(p, i, un); ++i) {
+            const Tile x = tile_at(p.sub[un.sub], un.tile);
             const int b = i & 1;
             const int row0 = x.m0 * 256 + int(rank) * 128 + quad * 32;
             const uint32_t d = tmem + uint32_t(b) * 256 + (uint32_t(quad) << 21);
@@ -527,14 +573,14 @@ ffn_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Param
             [[maybe_unused]] Pre16 g[2], u[2];
             [[maybe_unused]] auto fetch = [&](int c, int to) {   // the kept projections of 16 columns
                 const int row = row0 + lane, col = n0 + c;
-                const int valid = row < p.m ? p.n - col : 0;
+                const int valid = row < p.sub[0].m ? p.sub[0].n - col : 0;
                 g[to].load(p.g, row * p.ldp + col, valid, p);
                 u[to].load(p.u, row * p.ldp + col, valid, p);
             };
             // ... and 32 columns on their way to L2, two chunks before they are fetched
             [[maybe_unused]] auto ahead = [&](int c) {
                 const int row = row0 + lane, col = n0 + c;
-                if (c >= kCols || row >= p.m || col >= p.n) return;
+                if (c >= kCols || row >= p.sub[0].m || col >= p.sub[0].n) return;
                 const long long off = (row * p.ldp + col) * (p.pre_f32 ? 4 : 2);
                 asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char *>(p.g) + off));
                 asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char *>(p.u) + off));
@@ -596,7 +642,7 @@ ffn_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Param
                         tmem_wait();
                         tmem_tie16(v);
                         tmem_tie16(v + 16);
-                        finish_plain<kF16>(bx, v, p, maps.c, kLayout == kMM ? x.z : 0, row0, n0 + c);
+                        finish_plain<kF16>(bx, v, p, maps.c, un.sub, row0, n0 + c);
                     }
                 }
             }
@@ -629,9 +675,9 @@ __global__ void __launch_bounds__(128) ffn_finish_kernel(const __grid_constant__
     const int chunk = w % kChunks;
     w /= kChunks;
     const int rows = w & 7, tile = w >> 3;
-    const Tile x = tile_at(p, p.whole + tile);
+    const Tile x = tile_at(p.sub[0], p.whole + tile);
     const int row0 = x.m0 * 256 + rows * 32, col = x.n0 * kTileCols + chunk * 32;
-    if (row0 >= p.m || col >= p.n) return;
+    if (row0 >= p.sub[0].m || col >= p.sub[0].n) return;
     auto sums = [&](float *v, int c) {
         const float *src = p.part + ((long long)tile * p.split * 8 + rows) * (kBN * 32) + c * 32 + lane;
 #pragma unroll
@@ -652,14 +698,14 @@ __global__ void __launch_bounds__(128) ffn_finish_kernel(const __grid_constant__
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             Pre16 g, u;
-            const int row = row0 + lane, valid = row < p.m ? p.n - (col + 16 * q) : 0;
+            const int row = row0 + lane, valid = row < p.sub[0].m ? p.sub[0].n - (col + 16 * q) : 0;
             g.load(p.g, row * p.ldp + col + 16 * q, valid, p);
             u.load(p.u, row * p.ldp + col + 16 * q, valid, p);
             back16<kF16, kAct>(v + 16 * q, g, u, p, wg + 8 * q, wu + 8 * q, wh + 8 * q);
         }
         store_back(bx, wg, wu, wh, p, nullptr, row0, col);
     } else {
-        finish_plain<kF16>(bx, v, p, nullptr, x.z, row0, col);
+        finish_plain<kF16>(bx, v, p, nullptr, 0, row0, col);
     }
 }
 
@@ -953,8 +999,9 @@ bool operand_map(CUtensorMap *map, const Mat &x, bool mn, int rows, bool f16) {
 
 // The outputs [rows, cols]; `maps_too`: with tensor maps for the tile kernel's
 // stores (the stream kernel stores element by element).
-int set_outs(Params &p, Maps &maps, const Out *outs, int count, int64_t rows, int64_t cols, bool maps_too) {
-    for (int i = 0; i < count; ++i) {
+int set_outs(Params &p, Maps &maps, const Out *outs, int first, int count, int64_t rows, int64_t cols, bool maps_too) {
+    outs -= first;
+    for (int i = first; i < first + count; ++i) {
         p.out[i] = outs[i];
         Out &o = p.out[i];
         const int es = o.f32 ? 4 : 2;
@@ -1020,22 +1067,25 @@ struct Plan {
 // The GB300's 76 pairs are written here, not asked, so that the workspace's size
 // is known without a device; the kernel's units run on any number of pairs.
 constexpr int64_t kPairs = 76;
+constexpr double kPerK256 = 0.355, kPerK128 = 0.28, kTileStart = 1.5, kFinish = 3.0;
 
-Plan plan_tiles(int64_t m, int64_t n, int64_t batch, int nk, bool gated) {
+int64_t tiles_of(int64_t m, int64_t n, int64_t cols) { return (m + 255) / 256 * ((n + cols - 1) / cols); }
+
+Plan plan_tiles(int64_t m, int64_t n, int nk, bool gated) {
     Plan best{};
     double best_time = 1e30;
     for (int bn : {256, 128}) {
         Plan c{};
         c.bn = bn;
         c.cols = gated ? bn / 2 : bn;
-        c.tiles = (m + 255) / 256 * ((n + c.cols - 1) / c.cols) * batch;
-        const double per_k = bn == 256 ? 0.355 : 0.28;
+        c.tiles = tiles_of(m, n, c.cols);
+        const double per_k = bn == 256 ? kPerK256 : kPerK128;
         const int64_t rounds = c.tiles / kPairs, rest = c.tiles % kPairs;
         for (int s = 1; s <= 32; ++s) {
             if (s > 1 && (rest == 0 || nk / s < 4)) break;
-            double t = double(rounds) * (nk * per_k + 1.5);
-            if (rest) t += double((rest * s + kPairs - 1) / kPairs) * (double((nk + s - 1) / s) * per_k + 1.5);
-            if (s > 1) t += 3.0 + double(rest * s) * 256 * bn * 8 / 4.0e6;
+            double t = double(rounds) * (nk * per_k + kTileStart);
+            if (rest) t += double((rest * s + kPairs - 1) / kPairs) * (double((nk + s - 1) / s) * per_k + kTileStart);
+            if (s > 1) t += kFinish + double(rest * s) * 256 * bn * 8 / 4.0e6;
             if (t < best_time) {
                 best_time = t;
                 best = c;
@@ -1047,25 +1097,55 @@ Plan plan_tiles(int64_t m, int64_t n, int64_t batch, int nk, bool gated) {
     return best;
 }
 
+// The gradients' launch: dx of `dx_tokens` tokens (0: no dx) and the weights'
+// gradients that are wanted. Every pair works until all is done, so what counts
+// is the whole work, or the longest unit of dx where that is longer; dx is split
+// where that pays.
+Plan plan_grads(int64_t tokens, int64_t width, int64_t hidden, bool dx, bool gate_up, bool down) {
+    Plan best{};
+    double best_time = 1e30;
+    const int nk = int((hidden + 63) / 64) * 2, nkw = int((tokens + 63) / 64);
+    for (int bn : {256, 128}) {
+        Plan c{};
+        c.bn = c.cols = bn;
+        c.tiles = dx ? tiles_of(tokens, width, bn) : 0;
+        const int64_t weights = (gate_up ? 2 * tiles_of(hidden, width, bn) : 0) + (down ? tiles_of(width, hidden, bn) : 0);
+        const double per_k = bn == 256 ? kPerK256 : kPerK128;
+        const int64_t rest = c.tiles % kPairs;
+        for (int s = 1; s <= 32; ++s) {
+            if (s > 1 && (rest == 0 || nk / s < 4)) break;
+            const double work = double(c.tiles - rest) * (nk * per_k + kTileStart) +
+                                double(rest * s) * (double(nk) / s * per_k + kTileStart) +
+                                double(weights) * (nkw * per_k + kTileStart);
+            double t = std::max(work / kPairs, rest ? double((nk + s - 1) / s) * per_k + kTileStart : 0.0);
+            if (s > 1) t += kFinish + double(rest * s) * 256 * bn * 8 / 4.0e6;
+            if (t < best_time) {
+                best_time = t;
+                best = c;
+                best.split = s;
+                best.whole = s > 1 ? c.tiles - rest : c.tiles;
+            }
+        }
+    }
+    return best;
+}
+
+Sub make_sub(int64_t m, int64_t n, int64_t cols) {
+    return Sub{int(m), int(n), int((m + 255) / 256), int((n + cols - 1) / cols)};
+}
+
+// Launches the tile kernel (operands' and outputs' maps and p.sub are set) and,
+// where tiles are split, the kernel that finishes them.
 template <int kBN, int kLayout, int kEpi, bool kF16, int kAct>
-int launch_tile_as(const Plan &plan, Params &p, Maps &maps, const Mat *a, const Mat *b, int segs, void *part,
-                   cudaStream_t st) {
+int launch_tile_as(const Plan &plan, Params &p, const Maps &maps, void *part, cudaStream_t st) {
     int clusters = 0;
     if (!tile_ready<kBN, kLayout, kEpi, kF16, kAct>(&clusters)) return ROPE3D_ERR_CUDA;
-    constexpr bool kAMn = kLayout == kMM, kBMn = kLayout != kKK;
-    const int nb = kEpi == kGated ? 2 : segs;
-    for (int i = 0; i < segs; ++i)
-        if (!operand_map(&maps.a[i], a[i], kAMn, 128, p.f16)) return ROPE3D_ERR_CUDA;
-    for (int i = 0; i < nb; ++i)
-        if (!operand_map(&maps.b[i], b[i], kBMn, kBN / 2, p.f16)) return ROPE3D_ERR_CUDA;
-    p.tiles_m = int((int64_t(p.m) + 255) / 256);
-    p.tiles_n = int((int64_t(p.n) + plan.cols - 1) / plan.cols);
     p.whole = int(plan.whole);
     p.split = plan.split;
     p.units = int(plan.units());
     p.part = static_cast<float *>(part);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(2 * std::min(clusters, p.units)));
+    cfg.gridDim = dim3(unsigned(2 * std::min(clusters, p.units + p.weight_units)));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = tile_smem<kBN>();
     cfg.stream = st;
@@ -1106,12 +1186,11 @@ struct Const {
 };
 
 template <int kLayout, int kEpi>
-int launch_tile(Params &p, Maps &maps, const Mat *a, const Mat *b, int segs, void *part, cudaStream_t st) {
-    const Plan plan = plan_tiles(p.m, p.n, p.batch, p.nk0 + p.nk1, kEpi == kGated);
-    if (plan.units() > (int64_t(1) << 30)) return ROPE3D_ERR_SHAPE;
+int launch_plan(const Plan &plan, Params &p, const Maps &maps, void *part, cudaStream_t st) {
+    if (plan.units() + p.weight_units > (int64_t(1) << 30)) return ROPE3D_ERR_SHAPE;
     auto as = [&](auto bn, auto f16, auto act) {
         return launch_tile_as<decltype(bn)::value, kLayout, kEpi, decltype(f16)::value, decltype(act)::value>(
-            plan, p, maps, a, b, segs, part, st);
+            plan, p, maps, part, st);
     };
     auto with_act = [&](auto bn, auto f16) {
         if constexpr (kEpi != kPlain) {   // (the plain product has no activation)
@@ -1122,6 +1201,18 @@ int launch_tile(Params &p, Maps &maps, const Mat *a, const Mat *b, int segs, voi
     };
     auto with_type = [&](auto bn) { return p.f16 ? with_act(bn, Const<1>{}) : with_act(bn, Const<0>{}); };
     return plan.bn == 128 ? with_type(Const<128>{}) : with_type(Const<256>{});
+}
+
+// One product of `m` rows and `n` columns (of each half where gated): a and b
+// hold its operands, two of b where gated.
+template <int kLayout, int kEpi>
+int launch_tile(int64_t m, int64_t n, Params &p, Maps &maps, const Mat &a, const Mat *b, void *part, cudaStream_t st) {
+    const Plan plan = plan_tiles(m, n, p.nk0 + p.nk1, kEpi == kGated);
+    if (!operand_map(&maps.a[0], a, false, 128, p.f16)) return ROPE3D_ERR_CUDA;
+    for (int i = 0; i < (kEpi == kGated ? 2 : 1); ++i)
+        if (!operand_map(&maps.b[i], b[i], kLayout != kKK, plan.bn / 2, p.f16)) return ROPE3D_ERR_CUDA;
+    p.sub[0] = make_sub(m, n, plan.cols);
+    return launch_plan<kLayout, kEpi>(plan, p, maps, part, st);
 }
 
 // Few tokens. w: the weights (two where gated or of two segments), x: the
@@ -1304,7 +1395,6 @@ Params base_params(int32_t dtype, int32_t act) {
     Params p{};
     p.f16 = dtype == ROPE3D_F16;
     p.act = act;
-    p.batch = 1;
     return p;
 }
 
@@ -1318,16 +1408,14 @@ int project(const Mat &x, const Mat &wg, const Mat &wu, Out h, Out g, Out u, int
     const Out outs[3] = {h, g, u};
     const Mat w[2] = {wg, wu};
     p.nk0 = blocks64(x.cols);
-    const int rc = set_outs(p, maps, outs, 3, x.rows, wg.rows, x.rows > kStreamTokens);
+    const int rc = set_outs(p, maps, outs, 0, 3, x.rows, wg.rows, x.rows > kStreamTokens);
     if (rc != ROPE3D_OK) return rc;
     if (x.rows <= kStreamTokens) {
         p.m = int(wg.rows);
         p.n = int(x.rows);
         return launch_stream<false, kGated>(p, maps, w, &x, 1, st);
     }
-    p.m = int(x.rows);
-    p.n = int(wg.rows);
-    return launch_tile<kKK, kGated>(p, maps, &x, w, 1, part, st);
+    return launch_tile<kKK, kGated>(x.rows, wg.rows, p, maps, x, w, part, st);
 }
 
 // One body for the call and for its workspace query (launch = false; *need
@@ -1347,8 +1435,8 @@ int forward(const rope3d_gated_ffn_args *a, bool launch, bool check_device, int6
         wd{a->w_down, D, F, a->w_down_stride};
     const int nkd = blocks64(D), nkf = blocks64(F);
     const int64_t part_bytes = M <= kStreamTokens ? 0
-                                                  : std::max(plan_tiles(M, F, 1, nkd, true).part_bytes(),
-                                                             plan_tiles(M, D, 1, nkf, false).part_bytes());
+                                                  : std::max(plan_tiles(M, F, nkd, true).part_bytes(),
+                                                             plan_tiles(M, D, nkf, false).part_bytes());
     Carver size{nullptr};
     {
         Mat t[4] = {x, wg, wu, wd};
@@ -1382,16 +1470,14 @@ int forward(const rope3d_gated_ffn_args *a, bool launch, bool check_device, int6
     Params p = base_params(a->dtype, a->act);
     const Out y{a->y, a->y_stride, 0, 0, 0};
     p.nk0 = blocks64(F);
-    if ((rc = set_outs(p, maps, &y, 1, M, D, M > kStreamTokens)) != ROPE3D_OK) return rc;
+    if ((rc = set_outs(p, maps, &y, 0, 1, M, D, M > kStreamTokens)) != ROPE3D_OK) return rc;
     t_ffn_kernel = M <= kStreamTokens ? 2 : 1;
     if (M <= kStreamTokens) {
         p.m = int(D);
         p.n = int(M);
         return launch_stream<false, kPlain>(p, maps, &wd, &h, 1, st);
     }
-    p.m = int(M);
-    p.n = int(D);
-    return launch_tile<kKK, kPlain>(p, maps, &h, &wd, 1, part, st);
+    return launch_tile<kKK, kPlain>(M, D, p, maps, h, &wd, part, st);
 }
 
 int backward(const rope3d_gated_ffn_backward_args *a, bool launch, bool check_device, int64_t *need,
@@ -1416,19 +1502,13 @@ int backward(const rope3d_gated_ffn_backward_args *a, bool launch, bool check_de
         wu{a->w_up, F, D, a->w_up_stride}, wd{a->w_down, D, F, a->w_down_stride};
     const int64_t hld = up(F, 64);
     const bool few = M <= kStreamTokens;
-    const int nkd = blocks64(D), nkf = blocks64(F), nkm = blocks64(M);
-    // the split products' sums, one product at a time
-    int64_t part_bytes = 0;
-    auto need_part = [&](int64_t m, int64_t n, int64_t batch, int nk, bool gated) {
-        part_bytes = std::max(part_bytes, plan_tiles(m, n, batch, nk, gated).part_bytes());
-    };
+    // the split products' sums, one launch at a time
+    const Plan grads = plan_grads(M, D, F, a->dx && !few, a->dw_gate != nullptr, a->dw_down != nullptr);
+    int64_t part_bytes = grads.part_bytes();
     if (!few) {
-        if (again) need_part(M, F, 1, nkd, true);
-        need_part(M, F, 1, nkd, false);
-        need_part(M, D, 1, 2 * nkf, false);
+        part_bytes = std::max(part_bytes, plan_tiles(M, F, blocks64(D), false).part_bytes());
+        if (again) part_bytes = std::max(part_bytes, plan_tiles(M, F, blocks64(D), true).part_bytes());
     }
-    need_part(F, D, 2, nkm, false);
-    need_part(D, F, 1, nkm, false);
     Carver size{nullptr};
     {
         Mat t[5] = {dy, x, wg, wu, wd};
@@ -1474,53 +1554,70 @@ int backward(const rope3d_gated_ffn_backward_args *a, bool launch, bool check_de
         Params p = base_params(a->dtype, a->act);
         const Out outs[3] = {Out{dgb, hld, 0, 0, 0}, Out{dub, hld, 0, 0, 0},
                              Out{a->dw_down ? hb : nullptr, hld, 0, 0, 0}};
-        if ((rc = set_outs(p, maps, outs, 3, M, F, !few)) != ROPE3D_OK) return rc;
+        if ((rc = set_outs(p, maps, outs, 0, 3, M, F, !few)) != ROPE3D_OK) return rc;
         p.nk0 = blocks64(D);
         p.g = g;
         p.u = u;
         p.ldp = ldp;
         p.pre_f32 = pre_es == 4;
         p.pre_vec = rows_on(g, ldp, pre_es, 32) && rows_on(u, ldp, pre_es, 32);
-        p.m = int(few ? F : M);
-        p.n = int(few ? M : F);
+        p.m = int(F);
+        p.n = int(M);
         rc = few ? launch_stream<true, kBack>(p, maps, &wd, &dy, 1, st)
-                 : launch_tile<kKM, kBack>(p, maps, &dy, &wd, 1, part, st);
+                 : launch_tile<kKM, kBack>(M, F, p, maps, dy, &wd, part, st);
         if (rc != ROPE3D_OK) return rc;
     }
     const Mat dg{dgb, M, F, hld}, du{dub, M, F, hld}, h{hb, M, F, hld};
-    if (a->dx) {
+    const Out dx{a->dx, a->dx_stride, 0, 0, 0};
+    if (a->dx && few) {
         Params p = base_params(a->dtype, a->act);
-        const Out o{a->dx, a->dx_stride, 0, 0, 0};
         const Mat t[2] = {dg, du}, w[2] = {wg, wu};
-        if ((rc = set_outs(p, maps, &o, 1, M, D, !few)) != ROPE3D_OK) return rc;
+        if ((rc = set_outs(p, maps, &dx, 0, 1, M, D, false)) != ROPE3D_OK) return rc;
         p.nk0 = p.nk1 = blocks64(F);
-        p.m = int(few ? D : M);
-        p.n = int(few ? M : D);
-        rc = few ? launch_stream<true, kPlain>(p, maps, w, t, 2, st) : launch_tile<kKM, kPlain>(p, maps, t, w, 2, part, st);
-        if (rc != ROPE3D_OK) return rc;
+        p.m = int(D);
+        p.n = int(M);
+        if ((rc = launch_stream<true, kPlain>(p, maps, w, t, 2, st)) != ROPE3D_OK) return rc;
+    }
+    const bool tile_dx = a->dx && !few;
+    if (!tile_dx && !a->dw_gate && !a->dw_down) return ROPE3D_OK;
+    // dx (of many tokens) and the weights' gradients in one launch
+    Params p = base_params(a->dtype, a->act);
+    p.nk0 = p.nk1 = blocks64(F);
+    p.nkw = blocks64(M);
+    if (tile_dx) {
+        const Mat t[2] = {dg, du}, w[2] = {wg, wu};
+        for (int i = 0; i < 2; ++i)
+            if (!operand_map(&maps.a[i], t[i], false, 128, p.f16) || !operand_map(&maps.b[i], w[i], true, 64, p.f16))
+                return ROPE3D_ERR_CUDA;
+        if ((rc = set_outs(p, maps, &dx, 0, 1, M, D, true)) != ROPE3D_OK) return rc;
+        p.sub[0] = make_sub(M, D, grads.cols);
     }
     if (a->dw_gate) {
-        // both in one launch: a batch of two products
-        Params p = base_params(a->dtype, a->act);
+        const Mat t[2] = {dg, du};
         const Out o[2] = {Out{a->dw_gate, a->dw_gate_stride, 0, 0, 0}, Out{a->dw_up, a->dw_up_stride, 0, 0, 0}};
-        const Mat t[2] = {dg, du}, xs[2] = {x, x};
-        if ((rc = set_outs(p, maps, o, 2, F, D, true)) != ROPE3D_OK) return rc;
-        p.nk0 = blocks64(M);
-        p.m = int(F);
-        p.n = int(D);
-        p.batch = 2;
-        if ((rc = launch_tile<kMM, kPlain>(p, maps, t, xs, 2, part, st)) != ROPE3D_OK) return rc;
+        for (int i = 0; i < 2; ++i) {
+            if (!operand_map(&maps.a[2 + i], t[i], true, 64, p.f16) || !operand_map(&maps.b[2 + i], x, true, 64, p.f16))
+                return ROPE3D_ERR_CUDA;
+            p.sub[1 + i] = make_sub(F, D, grads.cols);
+        }
+        if ((rc = set_outs(p, maps, o, 1, 2, F, D, true)) != ROPE3D_OK) return rc;
     }
     if (a->dw_down) {
-        Params p = base_params(a->dtype, a->act);
         const Out o{a->dw_down, a->dw_down_stride, 0, 0, 0};
-        if ((rc = set_outs(p, maps, &o, 1, D, F, true)) != ROPE3D_OK) return rc;
-        p.nk0 = blocks64(M);
-        p.m = int(D);
-        p.n = int(F);
-        if ((rc = launch_tile<kMM, kPlain>(p, maps, &dy, &h, 1, part, st)) != ROPE3D_OK) return rc;
+        if (!operand_map(&maps.a[4], dy, true, 64, p.f16) || !operand_map(&maps.b[4], h, true, 64, p.f16))
+            return ROPE3D_ERR_CUDA;
+        if ((rc = set_outs(p, maps, &o, 3, 1, D, F, true)) != ROPE3D_OK) return rc;
+        p.sub[3] = make_sub(D, F, grads.cols);
     }
-    return ROPE3D_OK;
+    int64_t weight_units = 0;
+    for (int z = 1; z < 4; ++z) weight_units += int64_t(p.sub[z].tiles_m) * p.sub[z].tiles_n;
+    if (weight_units > (int64_t(1) << 30)) return ROPE3D_ERR_SHAPE;
+    p.weight_units = int(weight_units);
+    // the length of the last round's units of dx against a tile of the weights'
+    const int last = (p.nk0 + p.nk1) / (grads.whole == grads.tiles ? 1 : grads.split);
+    p.dx_first = last >= p.nkw;
+    p.lag = p.dx_first ? (last + p.nkw / 2) / p.nkw : (p.nkw + last / 2) / last;
+    return launch_plan<kGrads, kPlain>(grads, p, maps, part, st);
 }
 
 }  // namespace
