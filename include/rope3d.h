@@ -580,8 +580,9 @@ int rope3d_gated_ffn_backward(const rope3d_gated_ffn_backward_args *args, void *
 int rope3d_gated_ffn_backward_check(const rope3d_gated_ffn_backward_args *args, int32_t check_device);
 int rope3d_gated_ffn_backward_workspace(const rope3d_gated_ffn_backward_args *args, int64_t *bytes);
 
-/* Which kernel computed this thread's last feed-forward (its products with the
- * weights): 1 tiles of many tokens, 2 weights streamed for few, 0 none yet. */
+/* Which kernel computed the first product with the weights of this thread's last
+ * feed-forward call (x w_gate^T, or dy w_down): 1 tiles of many tokens, 2 weights
+ * streamed for few, 0 none yet. */
 int rope3d_gated_ffn_last_kernel(void);
 /* How many bounded waits of the feed-forward's kernels ran out (0 unless
  * something is badly wrong; such a launch's output is not to be used); reset

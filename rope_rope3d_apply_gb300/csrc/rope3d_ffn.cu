@@ -717,11 +717,17 @@ __global__ void __launch_bounds__(128) ffn_finish_kernel(const __grid_constant__
 // read at once also where the tiles are few; each leaves its fp32 partial sums
 // in shared memory and the cluster adds them in rank order (always the same
 // order) through distributed shared memory, with the activation on the way out.
-// Warp 0: TMA, warp 1: MMAs, all four warps: the epilogue.
+// Warp 0: TMA, warp 1: MMAs, all eight warps: the epilogue (warps w and w + 4
+// share tensor-memory lanes and take half of the columns each).
 // The second product of a forward pass starts its weight copies while the first
 // still runs, and waits for h alone.
-constexpr int kStreamThreads = 128;
-constexpr int kStreamTokens = 128;   // most tokens of this kernel
+constexpr int kStreamThreads = 256;
+// Most tokens of this kernel: of the gated product (two accumulators to add up)
+// and of the others. Measured, bf16, the whole forward pass: width 2048, hidden
+// 8192: 96 tokens 30.3 us (gated product by tiles 34), 128: 33.6 (34); 320, 2944:
+// 128: 18.2 (13.9). dx at 2048, 8192: 160 tokens 42.8 us (by tiles 54.8), 192:
+// 63.4 (55.4).
+constexpr int kStreamGated = 96, kStreamTokens = 160;
 constexpr int kMaxSplit = 8;
 
 template <bool kAMn, int kEpi>
@@ -838,58 +844,87 @@ ffn_stream_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Par
     // the ring's memory takes the partial sums, [accumulator][token][128 rows]
     mbar_wait(done, 0, dead, &g_ffn_wait_timeouts);
     tc_fence_after();
-    const int row = warp * 32 + lane;
-    for (int c = 0; c < kAcc * p.rows_n; c += 16) {
+    const int row = (warp & 3) * 32 + lane;
+    for (int c = (warp >> 2) * 16; c < kAcc * p.rows_n; c += 32) {
         float v[16];
-        tmem_ld16(v, tmem + (uint32_t(warp) << 21) + uint32_t(c));
+        tmem_ld16(v, tmem + (uint32_t(warp & 3) << 21) + uint32_t(c));
         tmem_wait();
         tmem_tie16(v);
-        const bool any = k_hi > k_lo;   // an empty k range has no MMA: its tensor memory is not defined
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + uint32_t((c + i) * 128 + row) * 4),
-                         "f"(any ? v[i] : 0.0f) : "memory");
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + uint32_t((c + i) * 128 + row) * 4), "f"(v[i]) : "memory");
     }
     tc_fence_before();
     __syncthreads();
     cluster_sync();
-    // 32 rows of one token at a time, shared out over the cluster's warps
-    for (int unit = int(rank) * 4 + warp; unit < p.n * 4; unit += int(split) * 4) {
-        const int tok = unit >> 2, f = (unit & 3) * 32 + lane;
-        float acc[2] = {0.0f, 0.0f};
+    // one token at a time, four weight rows a lane, shared out over the cluster's warps
+    for (int tok = int(rank) * 8 + warp; tok < p.n; tok += int(split) * 8) {
+        float acc[kAcc][4];
 #pragma unroll
         for (int a = 0; a < kAcc; ++a) {
-            const uint32_t at = base + uint32_t((a * p.rows_n + tok) * 128 + f) * 4;
-            float part[kMaxSplit];
+            const uint32_t at = base + uint32_t((a * p.rows_n + tok) * 128 + lane * 4) * 4;
+            float4 part[kMaxSplit];
 #pragma unroll
             for (int r = 0; r < kMaxSplit; ++r)
-                part[r] = r < int(split) ? ld_cluster_f32(map_rank(at, uint32_t(r))) : 0.0f;
+                part[r] = r < int(split) ? ld_cluster_v4(map_rank(at, uint32_t(r))) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-            for (int r = 0; r < kMaxSplit; ++r) acc[a] += part[r];
+            for (int i = 0; i < 4; ++i) acc[a][i] = 0.0f;
+#pragma unroll
+            for (int r = 0; r < kMaxSplit; ++r) {
+                acc[a][0] += part[r].x;
+                acc[a][1] += part[r].y;
+                acc[a][2] += part[r].z;
+                acc[a][3] += part[r].w;
+            }
         }
-        const int col = f0 + f;
-        if (col >= p.m) continue;
-        auto put = [&](const Out &o, float v) {
+        const int col = f0 + lane * 4, valid = min(4, p.m - col);
+        if (valid <= 0) continue;
+        auto put = [&](const Out &o, const float *v) {
             if (!o.p) return;
             const long long at = tok * o.ld + col;
-            if (o.f32) static_cast<float *>(o.p)[at] = v;
-            else static_cast<uint16_t *>(o.p)[at] = pack1(v, p.f16);
+            if (o.vec && valid == 4) {   // (four elements from a multiple of four on)
+                if (o.f32) {
+                    *reinterpret_cast<float4 *>(static_cast<float *>(o.p) + at) = make_float4(v[0], v[1], v[2], v[3]);
+                } else {
+                    const uint2 w = p.f16 ? make_uint2(pack2<true>(v[0], v[1]), pack2<true>(v[2], v[3]))
+                                          : make_uint2(pack2<false>(v[0], v[1]), pack2<false>(v[2], v[3]));
+                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(o.p) + at) = w;
+                }
+                return;
+            }
+            for (int i = 0; i < valid; ++i) {
+                if (o.f32) static_cast<float *>(o.p)[at + i] = v[i];
+                else static_cast<uint16_t *>(o.p)[at + i] = pack1(v[i], p.f16);
+            }
         };
         if constexpr (kEpi == kGated) {
             put(p.out[1], acc[0]);
             put(p.out[2], acc[1]);
-            put(p.out[0], activation_of<false>(acc[0], p.act, nullptr) * acc[1]);
+            if (p.out[0].p) {
+                float h[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) h[i] = activation_of<false>(acc[0][i], p.act, nullptr) * acc[1][i];
+                put(p.out[0], h);
+            }
         } else if constexpr (kEpi == kBack) {
             const long long at = tok * p.ldp + col;
-            const float g = p.pre_f32 ? static_cast<const float *>(p.g)[at]
-                                      : unpack1(static_cast<const uint16_t *>(p.g)[at], p.f16);
-            const float u = p.pre_f32 ? static_cast<const float *>(p.u)[at]
-                                      : unpack1(static_cast<const uint16_t *>(p.u)[at], p.f16);
-            float slope;
-            const float a = activation_of<true>(g, p.act, &slope);
-            put(p.out[0], acc[0] * u * slope);
-            put(p.out[1], acc[0] * a);
-            put(p.out[2], a * u);
+            float dg[4] = {}, du[4] = {}, h[4] = {};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i >= valid) break;
+                const float g = p.pre_f32 ? static_cast<const float *>(p.g)[at + i]
+                                          : unpack1(static_cast<const uint16_t *>(p.g)[at + i], p.f16);
+                const float u = p.pre_f32 ? static_cast<const float *>(p.u)[at + i]
+                                          : unpack1(static_cast<const uint16_t *>(p.u)[at + i], p.f16);
+                float slope;
+                const float a = activation_of<true>(g, p.act, &slope);
+                dg[i] = acc[0][i] * u * slope;
+                du[i] = acc[0][i] * a;
+                h[i] = a * u;
+            }
+            put(p.out[0], dg);
+            put(p.out[1], du);
+            put(p.out[2], h);
         } else {
             put(p.out[0], acc[0]);
         }
@@ -1408,9 +1443,9 @@ int project(const Mat &x, const Mat &wg, const Mat &wu, Out h, Out g, Out u, int
     const Out outs[3] = {h, g, u};
     const Mat w[2] = {wg, wu};
     p.nk0 = blocks64(x.cols);
-    const int rc = set_outs(p, maps, outs, 0, 3, x.rows, wg.rows, x.rows > kStreamTokens);
+    const int rc = set_outs(p, maps, outs, 0, 3, x.rows, wg.rows, x.rows > kStreamGated);
     if (rc != ROPE3D_OK) return rc;
-    if (x.rows <= kStreamTokens) {
+    if (x.rows <= kStreamGated) {
         p.m = int(wg.rows);
         p.n = int(x.rows);
         return launch_stream<false, kGated>(p, maps, w, &x, 1, st);
@@ -1434,9 +1469,8 @@ int forward(const rope3d_gated_ffn_args *a, bool launch, bool check_device, int6
     Mat x{a->x, M, D, a->x_stride}, wg{a->w_gate, F, D, a->w_gate_stride}, wu{a->w_up, F, D, a->w_up_stride},
         wd{a->w_down, D, F, a->w_down_stride};
     const int nkd = blocks64(D), nkf = blocks64(F);
-    const int64_t part_bytes = M <= kStreamTokens ? 0
-                                                  : std::max(plan_tiles(M, F, nkd, true).part_bytes(),
-                                                             plan_tiles(M, D, nkf, false).part_bytes());
+    int64_t part_bytes = M <= kStreamGated ? 0 : plan_tiles(M, F, nkd, true).part_bytes();
+    if (M > kStreamTokens) part_bytes = std::max(part_bytes, plan_tiles(M, D, nkf, false).part_bytes());
     Carver size{nullptr};
     {
         Mat t[4] = {x, wg, wu, wd};
@@ -1471,7 +1505,7 @@ int forward(const rope3d_gated_ffn_args *a, bool launch, bool check_device, int6
     const Out y{a->y, a->y_stride, 0, 0, 0};
     p.nk0 = blocks64(F);
     if ((rc = set_outs(p, maps, &y, 0, 1, M, D, M > kStreamTokens)) != ROPE3D_OK) return rc;
-    t_ffn_kernel = M <= kStreamTokens ? 2 : 1;
+    t_ffn_kernel = M <= kStreamGated ? 2 : 1;
     if (M <= kStreamTokens) {
         p.m = int(D);
         p.n = int(M);
@@ -1505,10 +1539,8 @@ int backward(const rope3d_gated_ffn_backward_args *a, bool launch, bool check_de
     // the split products' sums, one launch at a time
     const Plan grads = plan_grads(M, D, F, a->dx && !few, a->dw_gate != nullptr, a->dw_down != nullptr);
     int64_t part_bytes = grads.part_bytes();
-    if (!few) {
-        part_bytes = std::max(part_bytes, plan_tiles(M, F, blocks64(D), false).part_bytes());
-        if (again) part_bytes = std::max(part_bytes, plan_tiles(M, F, blocks64(D), true).part_bytes());
-    }
+    if (!few) part_bytes = std::max(part_bytes, plan_tiles(M, F, blocks64(D), false).part_bytes());
+    if (again && M > kStreamGated) part_bytes = std::max(part_bytes, plan_tiles(M, F, blocks64(D), true).part_bytes());
     Carver size{nullptr};
     {
         Mat t[5] = {dy, x, wg, wu, wd};

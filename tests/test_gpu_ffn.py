@@ -42,7 +42,7 @@ SHAPES = [
     (1, 64, 128), (1, 8, 8), (1, 2048, 512), (2, 136, 264), (17, 512, 1024), (33, 72, 1000), (64, 256, 640),
     (100, 320, 192), (128, 128, 256),
     # ... and tiles of many
-    (129, 64, 128), (256, 128, 256), (300, 200, 328), (515, 136, 264), (777, 520, 1096), (1024, 1024, 2048),
+    (129, 64, 128), (150, 1032, 392), (200, 72, 520), (256, 128, 256), (257, 96, 64), (300, 200, 328), (515, 136, 264), (777, 520, 1096), (1024, 1024, 2048),
 ]
 ODD = [(1, 1, 1), (1, 37, 131), (5, 129, 1), (40, 67, 259), (130, 1, 3), (200, 131, 259), (333, 77, 130)]
 
@@ -54,7 +54,7 @@ def test_forward(shape, dtype, act):
     w, _ = make(*shape, dtype)
     y, g, u = r.rope3d_gated_ffn(**w, act=act, keep=True)
     torch.cuda.synchronize()
-    assert r.rope3d_gated_ffn_last_kernel() == (2 if shape[0] <= 128 else 1)
+    assert r.rope3d_gated_ffn_last_kernel() == (2 if shape[0] <= 96 else 1)
     want = ref.ffn64(**w, act=act)
     ref.check(g, want["g"], "gate_pre")
     ref.check(u, want["u"], "up_pre")
