@@ -26,6 +26,8 @@ SOURCES = [
     os.path.join(CSRC, "rope3d_neox.cu"),
     os.path.join(CSRC, "rope3d_na3d.cu"),
     os.path.join(CSRC, "rope3d_norm.cu"),
+    os.path.join(CSRC, "rope3d_norm_back.cu"),
+    os.path.join(CSRC, "rope3d_norm.cuh"),
     os.path.join(CSRC, "rope3d_ffn.cu"),
     os.path.join(CSRC, "rope3d_tc.cuh"),
     os.path.join(CSRC, "rope3d_api.cpp"),
@@ -94,16 +96,18 @@ def commands(out_dir: str = BUILD, extra_nvcc: list[str] | None = None,
         "-Xptxas", "-v", *(extra_nvcc or []),
         "-c", os.path.join(CSRC, "rope3d_norm.cu"), "-o", norm_o,
     ]
+    norm_back_o = os.path.join(out_dir, "rope3d_norm_back.o")
+    nvcc_norm_back = [*nvcc_norm[:-3], os.path.join(CSRC, "rope3d_norm_back.cu"), "-o", norm_back_o]
     gxx_compile = [
         "g++", "-std=c++17", "-O2", "-fPIC", "-ffp-contract=off", "-fno-fast-math", *dbg,
         "-pthread", "-Wall", "-Wno-unused-function", f"-I{cuda}/include",
         "-c", os.path.join(CSRC, "rope3d_api.cpp"), "-o", api_o,
     ]
     link = [_nvcc(), *ARCH, "-shared", kern_o, api_o, noalloc_o, patch_o, neox_o, na_o, ffn_o,
-            norm_o,
+            norm_o, norm_back_o,
             "-o", os.path.join(out_dir, "librope3d.so"), "-Xcompiler", "-pthread"]
     return [nvcc_compile, gxx_compile, nvcc_noalloc, nvcc_patch, nvcc_neox, nvcc_na, nvcc_ffn,
-            nvcc_norm], link
+            nvcc_norm, nvcc_norm_back], link
 
 
 def up_to_date(lib: str = LIB) -> bool:

@@ -82,22 +82,22 @@ def both(a, dr, dn, kernel):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("post,pre", list(itertools.product((0, 1, 2), (0, 1, 2))))
-@pytest.mark.parametrize("channels,kernel", [(256, 1), (77, 2)])
+@pytest.mark.parametrize("channels,kernel", [(256, 1), (77, 1), (20000, 2)])
 def test_kinds(post, pre, channels, kernel, dtype):
-    both(*make(37, channels, dtype, post=post, pre=pre, residual_scale=0.5), kernel)
+    both(*make(37 if channels < 1000 else 5, channels, dtype, post=post, pre=pre, residual_scale=0.5), kernel)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("y,weights,mod", list(itertools.product((True, False), repeat=3)))
-@pytest.mark.parametrize("channels,kernel", [(512, 1), (130, None)])
+@pytest.mark.parametrize("channels,kernel", [(512, 1), (130, 1), (16390, 2)])
 def test_absent_parts(y, weights, mod, channels, kernel, dtype):
-    kernel = kernel or 2
     both(*make(24, channels, dtype, groups=3, y=y, weights=weights, mod=mod, weight_offset=1.0), kernel)
 
 
 @pytest.mark.parametrize("dtype,channels,kernel", [
     # one channel, one vector, whole warps and their neighbours, each team size, the longest rows in registers, longer
-    ("bf16", 1, 2), ("f32", 3, 2), ("bf16", 8, 1), ("f32", 4, 1), ("bf16", 248, 1), ("bf16", 264, 1), ("f16", 520, 1),
+    ("bf16", 1, 1), ("f32", 3, 1), ("f16", 63, 1), ("bf16", 65, 1), ("f32", 257, 1), ("bf16", 511, 1), ("f16", 513, 1),
+    ("f32", 1157, 1), ("bf16", 2047, 1), ("f32", 2049, 1), ("f32", 4097, 1), ("f32", 8191, 1), ("bf16", 8, 1), ("f32", 4, 1), ("bf16", 248, 1), ("bf16", 264, 1), ("f16", 520, 1),
     ("bf16", 1000, 1), ("bf16", 1032, 1), ("f32", 1028, 1), ("bf16", 2048, 1), ("f16", 4096, 1), ("bf16", 4104, 1),
     ("bf16", 8192, 1), ("f32", 2052, 1), ("f32", 4096, 1), ("f32", 8192, 1), ("bf16", 65536, 2), ("f16", 20001, 2),
 ])
@@ -105,24 +105,26 @@ def test_channels(dtype, channels, kernel):
     both(*make(5, channels, dtype, post=2, pre=2), kernel)
 
 
-def test_long_rows_forward_in_registers():
-    """Forward rows of up to 2048 vectors stay in registers; the backward pass of
-    those takes the general kernel."""
-    a, dr, dn = make(3, 16384, "bf16")
+@pytest.mark.parametrize("dtype,channels,forward,backward", [
+    ("bf16", 16384, 1, 2), ("f32", 9001, 1, 2), ("bf16", 4097, 2, 1), ("f16", 6635, 2, 1), ("bf16", 2049, 2, 1),
+])
+def test_other_kernel_backward(dtype, channels, forward, backward):
+    """Sizes whose forward and backward passes take different kernels."""
+    a, dr, dn = make(3, channels, dtype)
     want = ref.norm64(**a)
     out = r.rope3d_block_norm(**a)
-    assert r.rope3d_block_norm_last_kernel() == 1
+    assert r.rope3d_block_norm_last_kernel() == forward
     ref.check(out[0], want["r"], "r")
     ref.check(out[1], want["n"], "n")
     got = r.rope3d_block_norm_backward(dr=dr, dn=dn, **a)
-    assert r.rope3d_block_norm_last_kernel() == 2
+    assert r.rope3d_block_norm_last_kernel() == backward
     want = ref.norm64(dr=dr, dn=dn, grads=True, **a)
     for name, t in got.items():
         ref.check(t, want[name], name)
 
 
 @pytest.mark.parametrize("params", ["f32", None])
-@pytest.mark.parametrize("dtype,channels,kernel", [("bf16", 320, 1), ("f16", 1152, 1), ("bf16", 45, 2)])
+@pytest.mark.parametrize("dtype,channels,kernel", [("bf16", 320, 1), ("f16", 1152, 1), ("bf16", 45, 1), ("f16", 64, 1), ("f32", 700, 1)])
 @pytest.mark.parametrize("rows,rpg", [(1, 1), (2, 1), (700, 1), (700, 3), (700, 64), (701, 350), (3000, 1500), (3000, 7)])
 def test_groups(rows, rpg, dtype, channels, kernel, params):
     both(*make(rows, channels, dtype, rpg=rpg, params=params), kernel)
@@ -132,7 +134,7 @@ RING = [
     # rows, channels, dtype, groups: one warp a row, absent threads, each type's longest rows, one and several groups
     (20000, 128, "bf16", 2), (12000, 8, "bf16", 1), (6000, 2048, "f16", 1), (5000, 1032, "bf16", 4),
     (3000, 4096, "bf16", 3), (12000, 4, "f32", 5), (3000, 1156, "f32", 2), (700, 8192, "bf16", 1), (700, 8192, "f32", 1),
-    (2432, 2048, "bf16", 2432), (5000, 520, "f16", 1000),
+    (2432, 2048, "bf16", 2432), (5000, 520, "f16", 1000), (3001, 777, "f32", 1), (30000, 33, "bf16", 3), (4000, 1999, "f16", 1),
 ]
 
 
@@ -141,7 +143,7 @@ RING = [
 def test_many_rows(rows, channels, dtype, groups, post, pre, weights, mod):
     a, dr, dn = make(rows, channels, dtype, groups=groups, post=post, pre=pre, weights=weights, mod=mod,
                      residual_scale=0.75)
-    both(a, dr, dn, 1 if channels == 8192 else 3)
+    both(a, dr, dn, 3 if 384 <= channels < 8192 and channels % 4 == 0 else 1)
 
 
 @pytest.mark.parametrize("y,pre", [(False, 1), (False, 2), (True, 0), (False, 0)])
