@@ -656,12 +656,13 @@ def _code(t) -> int:
 def _matrix(name, t):
     """(rows, columns, row stride) of a matrix: the last dimension contiguous, the
     others viewable as one."""
-    shape, st = t.shape, t.stride()
+    shape = t.shape
     if len(shape) == 2:
         r, c = shape
-        if c > 1 and st[1] != 1:
+        ld, one = t.stride()
+        if one != 1 and c > 1:
             raise ValueError(f"{name} must have contiguous rows")
-        return r, c, st[0] if r > 1 else max(st[0], c)
+        return r, c, ld if r > 1 or ld > c else c
     if len(shape) < 2 or not t.is_contiguous():
         raise ValueError(f"{name} must be a matrix: contiguous, or a 2-D view with contiguous rows")
     c = shape[-1]
@@ -672,12 +673,28 @@ def _stride(name, t, rows, cols, dtype) -> int:
     """The row stride of a [rows, cols] matrix of `dtype` (0 for None)."""
     if t is None:
         return 0
+    shape = t.shape
+    if len(shape) == 2 and t.dtype is dtype and shape[0] == rows and shape[1] == cols:
+        ld, one = t.stride()
+        if one == 1 or cols <= 1:
+            return ld if rows > 1 or ld > cols else cols
     r, c, ld = _matrix(name, t)
     if r != rows or c != cols:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {rows} rows of {cols}")
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected {rows} rows of {cols}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
     return ld
+
+
+def _ptr_of(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _fresh(like):
+    """A new contiguous tensor of the shape and type of `like`."""
+    if like.is_contiguous():
+        return _torch.empty_like(like)
+    return _torch.empty(like.shape, dtype=like.dtype, device=like.device)
 
 
 def _scratch(nbytes: int, like, stream):
@@ -693,7 +710,7 @@ def _workspace(cls, fields, query, what, given, like, stream):
     """The packed arguments of a call (`fields` ends before workspace), with its
     workspace: `given`, or new memory of the size that `query` gives."""
     body, tail = fields
-    lib = load_library()
+    lib = _lib or load_library()
     need = ctypes.c_int64()
     if given is None:
         _check(getattr(lib, query)(cls.pack(*body, 0, 0, *tail), ctypes.byref(need)), what)
@@ -711,33 +728,42 @@ def _norm_fields(x, y, post, pre, post_weight, gate, pre_weight, scale, shift, r
     dt = x.dtype
     code = pcode = _code(x)
     pdt = None
-    for name, t in (("post_weight", post_weight), ("pre_weight", pre_weight)):
-        if t is not None:
-            if pdt is None:
-                pdt, pcode = t.dtype, _code(t)
-            elif t.dtype is not pdt:
-                raise TypeError("weights, gate, scale and shift must have one dtype")
-            if t.dim() != 1 or t.shape[0] != channels or (channels > 1 and t.stride(0) != 1):
-                raise ValueError(f"{name} must be contiguous, [{channels}]")
-    groups, lds = None, [0, 0, 0]
-    for i, (name, t) in enumerate((("gate", gate), ("scale", scale), ("shift", shift))):
-        if t is not None:
-            if pdt is None:
-                pdt, pcode = t.dtype, _code(t)
-            if groups is None:
-                groups = t.shape[0] if t.dim() == 2 else 1
-            lds[i] = _stride(name, t if t.dim() != 1 else t.unsqueeze(0), groups, channels, pdt)
+    if post_weight is not None:
+        pdt = _weight("post_weight", post_weight, channels, pdt)
+    if pre_weight is not None:
+        pdt = _weight("pre_weight", pre_weight, channels, pdt)
+    groups, lds = None, (0, 0, 0)
+    if gate is not None or scale is not None or shift is not None:
+        mods = tuple(t if t is None or t.dim() != 1 else t.unsqueeze(0) for t in (gate, scale, shift))
+        first = next(t for t in mods if t is not None)
+        pdt = pdt or first.dtype
+        groups = first.shape[0]
+        lds = (_stride("gate", mods[0], groups, channels, pdt), _stride("scale", mods[1], groups, channels, pdt),
+               _stride("shift", mods[2], groups, channels, pdt))
+    if pdt is not None and pdt is not dt:
+        pcode = F32 if pdt is _torch.float32 else BF16 if pdt is _torch.bfloat16 else F16 if pdt is _torch.float16 else -1
     if rows_per_group is None:
-        if groups is not None and (groups == 0 or rows % groups):
+        if groups is None:
+            rows_per_group = rows
+        elif groups == 0 or rows % groups:
             raise ValueError(f"{rows} rows are not whole groups of {groups}: give rows_per_group")
-        rows_per_group = rows // groups if groups else rows
+        else:
+            rows_per_group = rows // groups
     elif groups is not None and rows_per_group > 0 and -(-rows // rows_per_group) != groups:
         raise ValueError(f"{rows} rows in groups of {rows_per_group} do not make {groups} groups")
-    ptr = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
-    return (x.data_ptr(), ptr(y), ptr(post_weight), ptr(gate), ptr(pre_weight), ptr(scale), ptr(shift), ptr(r),
-            ptr(n), rows, channels, rows_per_group, ldx, _stride("y", y, rows, channels, dt),
-            _stride("r", r, rows, channels, dt), _stride("n", n, rows, channels, dt), *lds, eps, residual_scale,
-            weight_offset, code, pcode, post, pre)
+    return (x.data_ptr(), _ptr_of(y), _ptr_of(post_weight), _ptr_of(gate), _ptr_of(pre_weight), _ptr_of(scale),
+            _ptr_of(shift), _ptr_of(r), _ptr_of(n), rows, channels, rows_per_group, ldx,
+            _stride("y", y, rows, channels, dt), _stride("r", r, rows, channels, dt),
+            _stride("n", n, rows, channels, dt), *lds, eps, residual_scale, weight_offset, code, pcode, post, pre)
+
+
+def _weight(name, t, channels, dtype):
+    """Checks a norm's weight; its dtype."""
+    if len(t.shape) != 1 or t.shape[0] != channels or (channels > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be contiguous, [{channels}]")
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError("weights, gate, scale and shift must have one dtype")
+    return t.dtype
 
 
 def rope3d_block_norm(x, y=None, post: int = NORM_NONE, pre=NORM_RMS, post_weight=None, gate=None,
@@ -750,16 +776,16 @@ def rope3d_block_norm(x, y=None, post: int = NORM_NONE, pre=NORM_RMS, post_weigh
     rows of x (rows / groups when None). y None: r is residual_scale * x and only
     computed into a given r; pre None: n is not computed. r and n may be x or y
     (in place). Returns (r, n), None for what is not computed."""
-    torch = _use_torch()
+    _torch or _use_torch()
     if r is None and y is not None:
-        r = torch.empty_like(x, memory_format=torch.contiguous_format)
+        r = _fresh(x)
     if pre is None:
         n, pre = None, NORM_NONE
     elif n is None:
-        n = torch.empty_like(x, memory_format=torch.contiguous_format)
+        n = _fresh(x)
     args = _NormArgs.pack(*_norm_fields(x, y, post, pre, post_weight, gate, pre_weight, scale, shift, rows_per_group,
                                         eps, residual_scale, weight_offset, r, n))
-    rc = load_library().rope3d_block_norm(args, _raw_stream(stream, x))
+    rc = (_lib or load_library()).rope3d_block_norm(args, _raw_stream(stream, x))
     if rc:
         raise Rope3dError(rc, "rope3d_block_norm")
     return r, n
@@ -774,26 +800,25 @@ def rope3d_block_norm_backward(x, y=None, dr=None, dn=None, post: int = NORM_NON
     (either may be None: zero). Returns a dict: dx, dy (with y) and, with
     param_grads, d_post_weight, d_gate, d_pre_weight, d_scale, d_shift for the
     parameters given, in their dtype."""
-    torch = _use_torch()
+    _torch or _use_torch()
     fwd = _norm_fields(x, y, post, NORM_NONE if pre is None else pre, post_weight, gate, pre_weight, scale, shift,
                        rows_per_group, eps, residual_scale, weight_offset, None, None)
     rows, channels, dt = fwd[9], fwd[10], x.dtype
-    fresh = lambda t: torch.empty_like(t, memory_format=torch.contiguous_format)  # noqa: E731
-    out = {"dx": fresh(x) if dx is None else dx}
+    out = {"dx": _fresh(x) if dx is None else dx}
     if y is not None:
-        out["dy"] = fresh(x) if dy is None else dy
+        out["dy"] = _fresh(x) if dy is None else dy
     grads = [0, 0, 0, 0, 0]
     if param_grads:
         for i, (name, t) in enumerate((("d_post_weight", post_weight), ("d_gate", gate), ("d_pre_weight", pre_weight),
                                        ("d_scale", scale), ("d_shift", shift))):
             if t is not None:
-                out[name] = fresh(t)
+                out[name] = _fresh(t)
                 grads[i] = out[name].data_ptr()
-    ptr = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
     dx, dy = out["dx"], out.get("dy")
-    ld = [_stride(name, t, rows, channels, dt) for name, t in (("dr", dr), ("dn", dn), ("dx", dx), ("dy", dy))]
+    ld = (_stride("dr", dr, rows, channels, dt), _stride("dn", dn, rows, channels, dt),
+          _stride("dx", dx, rows, channels, dt), _stride("dy", dy, rows, channels, dt))
     st = _raw_stream(stream, x)
-    args, ws = _workspace(_NormBackArgs, ((*fwd, ptr(dr), ptr(dn), dx.data_ptr(), ptr(dy), *grads, *ld, channels), ()),
+    args, ws = _workspace(_NormBackArgs, ((*fwd, _ptr_of(dr), _ptr_of(dn), dx.data_ptr(), _ptr_of(dy), *grads, *ld, channels), ()),
                           "rope3d_block_norm_backward_workspace", "rope3d_block_norm_backward", workspace, x, st)
     _check(load_library().rope3d_block_norm_backward(args, st), "rope3d_block_norm_backward")
     return out
@@ -846,18 +871,18 @@ def rope3d_gated_ffn(x, w_gate, w_up, w_down, act: int = ACT_GELU_TANH, y=None, 
     (float32 or x's); gate_pre / up_pre take them instead of new tensors. Returns
     y, or (y, gate_pre, up_pre). workspace: a uint8 device tensor of at least the
     bytes the call needs (allocated when None)."""
-    torch = _use_torch()
+    torch = _torch or _use_torch()
     tokens, width, ldx = _matrix("x", x)
     hidden, dt, code = w_gate.shape[0], x.dtype, _code(x)
     if y is None:
-        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+        y = _fresh(x)
     if keep is not False and keep is not None and gate_pre is None and up_pre is None:
         shape, kept = (*x.shape[:-1], hidden), torch.float32 if keep is True else keep
         gate_pre = torch.empty(shape, dtype=kept, device=x.device)
         up_pre = torch.empty(shape, dtype=kept, device=x.device)
     pre_ld, pre_code = _pre_fields(gate_pre, up_pre, tokens, hidden, code)
     body = (x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), y.data_ptr(),
-            0 if gate_pre is None else gate_pre.data_ptr(), 0 if up_pre is None else up_pre.data_ptr(), tokens, width,
+            _ptr_of(gate_pre), _ptr_of(up_pre), tokens, width,
             hidden, ldx, _stride("w_gate", w_gate, hidden, width, dt), _stride("w_up", w_up, hidden, width, dt),
             _stride("w_down", w_down, width, hidden, dt), _stride("y", y, tokens, width, dt), pre_ld)
     st = _raw_stream(stream, x)
@@ -873,7 +898,7 @@ def rope3d_gated_ffn_backward(dy, x, w_gate, w_up, w_down, gate_pre=None, up_pre
     """The gradients of rope3d_gated_ffn: (dx, dw_gate, dw_up, dw_down). gate_pre
     and up_pre as the forward pass kept them; None computes them again. need: which
     of dx, (dw_gate, dw_up) and dw_down to compute; the others are None."""
-    torch = _use_torch()
+    _torch or _use_torch()
     tokens, width, ldx = _matrix("x", x)
     hidden, dt, code = w_gate.shape[0], x.dtype, _code(x)
     ld_w = (_stride("w_gate", w_gate, hidden, width, dt), _stride("w_up", w_up, hidden, width, dt),
@@ -881,16 +906,14 @@ def rope3d_gated_ffn_backward(dy, x, w_gate, w_up, w_down, gate_pre=None, up_pre
     pre_ld, pre_code = _pre_fields(gate_pre, up_pre, tokens, hidden, code)
 
     def out(wanted, given, like):
-        return None if not wanted else torch.empty_like(like, memory_format=torch.contiguous_format) \
-            if given is None else given
+        return None if not wanted else _fresh(like) if given is None else given
 
     grads = (out(need[0], dx, x), out(need[1], dw_gate, w_gate), out(need[1], dw_up, w_up),
              out(need[2], dw_down, w_down))
-    ptr = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
     ld_g = (_stride("dx", grads[0], tokens, width, dt), _stride("dw_gate", grads[1], hidden, width, dt),
             _stride("dw_up", grads[2], hidden, width, dt), _stride("dw_down", grads[3], width, hidden, dt))
-    body = (dy.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), ptr(gate_pre),
-            ptr(up_pre), *map(ptr, grads), tokens, width, hidden, _stride("dy", dy, tokens, width, dt), ldx, *ld_w,
+    body = (dy.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), _ptr_of(gate_pre),
+            _ptr_of(up_pre), *map(_ptr_of, grads), tokens, width, hidden, _stride("dy", dy, tokens, width, dt), ldx, *ld_w,
             pre_ld, *ld_g)
     st = _raw_stream(stream, x)
     args, ws = _workspace(_FfnBackArgs, (body, (code, pre_code, act)), "rope3d_gated_ffn_backward_workspace",

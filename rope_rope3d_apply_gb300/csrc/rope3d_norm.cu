@@ -452,7 +452,7 @@ constexpr int64_t kRingChannels = 384;
 template <typename Fn>
 int launch_ring(Fn fn, unsigned grid, const RingShape &shape, NormParams &p, cudaStream_t st) {
     p.stages = shape.stages;
-    if (shape.smem > 48 * 1024 &&
+    if (shape.smem > 40 * 1024 &&
         cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024) != cudaSuccess) {
         cudaGetLastError();
         return ROPE3D_ERR_CUDA;
@@ -619,7 +619,7 @@ int backward(const rope3d_block_norm_backward_args *a, bool run, bool check_devi
         const NormFn fn = back_team_fn(f.dtype, vec, t.elems, t.team);
         // the teams' sums, or the weights' where a chunk is whole groups
         const size_t smem = p.sums && (p.groups_per_chunk || !is_block(t.team)) ? size_t(3) * t.elems * t.threads * 4 : 0;
-        if (smem > 48 * 1024 &&
+        if (smem > 40 * 1024 &&   // (with the kernel's own, past the default limit of 48 KB)
             cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024) != cudaSuccess) {
             cudaGetLastError();
             return ROPE3D_ERR_CUDA;

@@ -105,6 +105,21 @@ def test_channels(dtype, channels, kernel):
     both(*make(5, channels, dtype, post=2, pre=2), kernel)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("channels", [1, 64, 200, 500, 1024, 1157, 2048, 4096, 4001, 8192, 9000])
+@pytest.mark.parametrize("rows,rpg", [(1, 1), (2, 1), (3, 2)])
+def test_few_rows(rows, rpg, channels, dtype):
+    """One row a group: chunks of whole groups, at every team size."""
+    a, dr, dn = make(rows, channels, dtype, rpg=rpg)
+    want = ref.norm64(**a)
+    out = r.rope3d_block_norm(**a)
+    ref.check(out[0], want["r"], "r")
+    ref.check(out[1], want["n"], "n")
+    want = ref.norm64(dr=dr, dn=dn, grads=True, **a)
+    for name, t in r.rope3d_block_norm_backward(dr=dr, dn=dn, **a).items():
+        ref.check(t, want[name], name)
+
+
 @pytest.mark.parametrize("dtype,channels,forward,backward", [
     ("bf16", 16384, 1, 2), ("f32", 9001, 1, 2), ("bf16", 4097, 2, 1), ("f16", 6635, 2, 1), ("bf16", 2049, 2, 1),
 ])
