@@ -53,7 +53,8 @@ extern "C" {
 #define ROPE3D_ERR_NOMEM   -10  /* a device or host allocation failed             */
 #define ROPE3D_ERR_ARG     -11  /* another argument is out of range               */
 #define ROPE3D_ERR_SCRATCH -12  /* the tables do not fit the fixed table area of
-                                   rope3d_apply_pair_noalloc (64 KiB)             */
+                                   rope3d_apply_pair_noalloc (64 KiB), or a
+                                   workspace argument is too small                */
 
 /* ---- element types ----------------------------------------------------- */
 #define ROPE3D_BF16 0   /* bfloat16 in and out                                */
@@ -800,7 +801,9 @@ int rope3d_testing_max_units_per_launch(int64_t n);
  * its kernels compute (table entries, strided and permuted offsets, token
  * and key positions, shared-memory slots) before the access it guards; a
  * failed check adds one to an error count and skips the access, so the kernel
- * finishes. This takes the place of a memory checker where none can run.
+ * finishes. This takes the place of a memory checker where none can run. The
+ * norms and the feed-forward are the same in both builds: their accesses are
+ * bounded by the extents of their arguments in every build.
  *   errors  out: failed checks since the last reset (0 in a normal build)
  *   reset   nonzero: clear the count after reading it
  * Returns 1 when the library was built with the checks, 0 when not.

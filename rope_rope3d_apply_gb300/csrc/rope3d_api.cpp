@@ -1522,7 +1522,7 @@ extern "C" const char *rope3d_status_string(int status) {
         case ROPE3D_ERR_TABLES: return "ROPE3D_ERR_TABLES: the tables do not match (T, H, W, split)";
         case ROPE3D_ERR_NOMEM: return "ROPE3D_ERR_NOMEM: an allocation failed";
         case ROPE3D_ERR_ARG: return "ROPE3D_ERR_ARG: an argument is out of range";
-        case ROPE3D_ERR_SCRATCH: return "ROPE3D_ERR_SCRATCH: the tables exceed the 64 KiB static table area of rope3d_apply_pair_noalloc";
+        case ROPE3D_ERR_SCRATCH: return "ROPE3D_ERR_SCRATCH: the tables exceed the 64 KiB static table area of rope3d_apply_pair_noalloc, or a workspace is too small";
         default: return "ROPE3D: unknown status";
     }
 }

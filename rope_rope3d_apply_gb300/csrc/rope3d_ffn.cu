@@ -1479,15 +1479,14 @@ int forward(const rope3d_gated_ffn_args *a, bool launch, bool check_device, int6
         size.take(part_bytes);
     }
     if (need) *need = size.used;
+    else if (!a->workspace) return ROPE3D_ERR_NULL;
+    else if (a->workspace_bytes < size.used) return ROPE3D_ERR_SCRATCH;
     const Span in[4] = {span(x.p, M, D, x.ld, 2), span(wg.p, F, D, wg.ld, 2), span(wu.p, F, D, wu.ld, 2),
                         span(wd.p, D, F, wd.ld, 2)};
     Span out[4] = {span(a->y, M, D, a->y_stride, 2), span(a->gate_pre, M, F, a->pre_stride, pre_es),
                    span(a->up_pre, M, F, a->pre_stride, pre_es), Span{a->workspace, size.used, 256}};
     rc = check_spans(in, 4, out, need ? 3 : 4, check_device);
-    if (rc != ROPE3D_OK || need) return rc;
-    if (!a->workspace) return ROPE3D_ERR_NULL;
-    if (a->workspace_bytes < size.used) return ROPE3D_ERR_SCRATCH;
-    if (!launch) return ROPE3D_OK;
+    if (rc != ROPE3D_OK || need || !launch) return rc;
 
     Carver ws{static_cast<char *>(a->workspace)};
     AlignJobs jobs{};
@@ -1551,6 +1550,8 @@ int backward(const rope3d_gated_ffn_backward_args *a, bool launch, bool check_de
         size.take(part_bytes);
     }
     if (need) *need = size.used;
+    else if (!a->workspace) return ROPE3D_ERR_NULL;
+    else if (a->workspace_bytes < size.used) return ROPE3D_ERR_SCRATCH;
     const Span in[7] = {span(dy.p, M, D, dy.ld, 2), span(x.p, M, D, x.ld, 2), span(wg.p, F, D, wg.ld, 2),
                         span(wu.p, F, D, wu.ld, 2), span(wd.p, D, F, wd.ld, 2),
                         span(a->gate_pre, M, F, a->pre_stride, pre_es), span(a->up_pre, M, F, a->pre_stride, pre_es)};
@@ -1558,10 +1559,7 @@ int backward(const rope3d_gated_ffn_backward_args *a, bool launch, bool check_de
                          span(a->dw_up, F, D, a->dw_up_stride, 2), span(a->dw_down, D, F, a->dw_down_stride, 2),
                          Span{a->workspace, size.used, 256}};
     rc = check_spans(in, 7, out, need ? 4 : 5, check_device);
-    if (rc != ROPE3D_OK || need) return rc;
-    if (!a->workspace) return ROPE3D_ERR_NULL;
-    if (a->workspace_bytes < size.used) return ROPE3D_ERR_SCRATCH;
-    if (!launch) return ROPE3D_OK;
+    if (rc != ROPE3D_OK || need || !launch) return rc;
 
     Carver ws{static_cast<char *>(a->workspace)};
     AlignJobs jobs{};
