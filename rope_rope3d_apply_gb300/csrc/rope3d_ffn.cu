@@ -323,14 +323,6 @@ struct Boxes {
 __device__ __forceinline__ void store_words(Boxes &bx, const uint32_t *w, const Out &o,
                                             const CUtensorMap *map, int row0, int col, int m, int n) {
     if (!o.p || row0 >= m || col >= n) return;
-    if (!o.tma && o.vec && col + (o.f32 ? 16 : 32) <= n) {
-        if (row0 + bx.lane >= m) return;
-        uint4 *d = reinterpret_cast<uint4 *>(static_cast<char *>(o.p) +
-                                             ((row0 + bx.lane) * o.ld + col) * (o.f32 ? 4 : 2));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-        return;
-    }
     const uint32_t box = bx.base + uint32_t(bx.next & (kBoxes - 1)) * kBoxBytes;
     ++bx.next;
     if (bx.lane == 0) bulk_wait_read<kBoxes - 1>();
@@ -662,50 +654,92 @@ ffn_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Param
     if (warp == 2) tmem_free<true>(tmem, 512);
 }
 
-// The split tiles: each warp adds the parts' sums of 32 rows x 32 columns (of
-// both halves where gated) in order and runs the epilogue on them.
+// Eight values of one row from column `col` of output o (the first `valid` exist).
+template <bool kF16>
+__device__ __forceinline__ void store8(const Out &o, int row, int col, int valid, const float *v) {
+    if (!o.p) return;
+    const long long at = row * o.ld + col;
+    if (o.f32) {
+        float *d = static_cast<float *>(o.p) + at;
+        if (o.vec && valid >= 8) {
+            reinterpret_cast<float4 *>(d)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4 *>(d)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < valid) d[i] = v[i];
+        }
+    } else {
+        uint16_t *d = static_cast<uint16_t *>(o.p) + at;
+        if (o.vec && valid >= 8) {
+            *reinterpret_cast<uint4 *>(d) = make_uint4(pack2<kF16>(v[0], v[1]), pack2<kF16>(v[2], v[3]),
+                                                       pack2<kF16>(v[4], v[5]), pack2<kF16>(v[6], v[7]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < valid) d[i] = pack1(v[i], kF16);
+        }
+    }
+}
+
+// The split tiles: each warp adds the parts' sums of 32 rows x 8 columns (of both
+// halves where gated) in order and runs the epilogue on them, a row a lane.
 template <int kBN, int kEpi, bool kF16, int kAct>
 __global__ void __launch_bounds__(128) ffn_finish_kernel(const __grid_constant__ Params p) {
     grid_wait();
     grid_release();
-    constexpr int kTileCols = kEpi == kGated ? kBN / 2 : kBN, kChunks = kTileCols / 32;
-    __shared__ __align__(1024) uint8_t staging[4 * kBoxes * kBoxBytes];
+    constexpr int kTileCols = kEpi == kGated ? kBN / 2 : kBN, kChunks = kTileCols / 8;
     const int lane = threadIdx.x & 31;
     int w = int(blockIdx.x) * 4 + int(threadIdx.x >> 5);   // (split tile, group of rows, chunk of columns)
     const int chunk = w % kChunks;
     w /= kChunks;
     const int rows = w & 7, tile = w >> 3;
     const Tile x = tile_at(p.sub[0], p.whole + tile);
-    const int row0 = x.m0 * 256 + rows * 32, col = x.n0 * kTileCols + chunk * 32;
-    if (row0 >= p.sub[0].m || col >= p.sub[0].n) return;
+    const int row = x.m0 * 256 + rows * 32 + lane, col = x.n0 * kTileCols + chunk * 8;
+    const int valid = row < p.sub[0].m ? p.sub[0].n - col : 0;
     auto sums = [&](float *v, int c) {
         const float *src = p.part + ((long long)tile * p.split * 8 + rows) * (kBN * 32) + c * 32 + lane;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = 0.0f;
+        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+#pragma unroll 4
         for (int i = 0; i < p.split; ++i, src += 8ll * kBN * 32)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] += __ldcs(src + e * 32);
+            for (int e = 0; e < 8; ++e) v[e] += __ldcs(src + e * 32);
     };
-    Boxes bx{smem_u32(staging) + uint32_t(threadIdx.x >> 5) * kBoxes * kBoxBytes, 0, lane};   // (the outputs' tma is off)
-    float v[32];
-    sums(v, chunk * 32);
+    float v[8];
+    sums(v, chunk * 8);
     if constexpr (kEpi == kGated) {
-        float u[32];
-        sums(u, kBN / 2 + chunk * 32);
-        finish_gated<kF16, kAct>(bx, v, u, p, nullptr, row0, col);
-    } else if constexpr (kEpi == kBack) {
-        uint32_t wg[16], wu[16], wh[16];
+        float u[8], h[8];
+        sums(u, kBN / 2 + chunk * 8);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            Pre16 g, u;
-            const int row = row0 + lane, valid = row < p.sub[0].m ? p.sub[0].n - (col + 16 * q) : 0;
-            g.load(p.g, row * p.ldp + col + 16 * q, valid, p);
-            u.load(p.u, row * p.ldp + col + 16 * q, valid, p);
-            back16<kF16, kAct>(v + 16 * q, g, u, p, wg + 8 * q, wu + 8 * q, wh + 8 * q);
+        for (int i = 0; i < 8; ++i) h[i] = activation<kAct, false>(v[i], nullptr) * u[i];
+        if (valid > 0) {
+            store8<kF16>(p.out[0], row, col, valid, h);
+            store8<kF16>(p.out[1], row, col, valid, v);
+            store8<kF16>(p.out[2], row, col, valid, u);
         }
-        store_back(bx, wg, wu, wh, p, nullptr, row0, col);
-    } else {
-        finish_plain<kF16>(bx, v, p, nullptr, 0, row0, col);
+    } else if constexpr (kEpi == kBack) {
+        if (valid <= 0) return;
+        float dg[8], du[8], h[8];
+        const long long at = row * p.ldp + col;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i >= valid) continue;
+            const float g = p.pre_f32 ? static_cast<const float *>(p.g)[at + i]
+                                      : unpack1(static_cast<const uint16_t *>(p.g)[at + i], kF16);
+            const float u = p.pre_f32 ? static_cast<const float *>(p.u)[at + i]
+                                      : unpack1(static_cast<const uint16_t *>(p.u)[at + i], kF16);
+            float slope;
+            const float a = activation<kAct, true>(g, &slope);
+            dg[i] = v[i] * u * slope;
+            du[i] = v[i] * a;
+            h[i] = a * u;
+        }
+        store8<kF16>(p.out[0], row, col, valid, dg);
+        store8<kF16>(p.out[1], row, col, valid, du);
+        store8<kF16>(p.out[2], row, col, valid, h);
+    } else if (valid > 0) {
+        store8<kF16>(p.out[0], row, col, valid, v);
     }
 }
 
@@ -1194,13 +1228,11 @@ int launch_tile_as(const Plan &plan, Params &p, const Maps &maps, void *part, cu
         return ROPE3D_ERR_CUDA;
     }
     if (plan.whole == plan.tiles) return ROPE3D_OK;
-    Params f = p;
-    for (Out &o : f.out) o.tma = 0;
-    const int64_t warps = (plan.tiles - plan.whole) * 8 * (plan.cols / 32);
+    const int64_t warps = (plan.tiles - plan.whole) * 8 * (plan.cols / 8);
     cfg.gridDim = dim3(unsigned(warps / 4));
     cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = 0;
-    if (cudaLaunchKernelEx(&cfg, ffn_finish_kernel<kBN, kEpi, kF16, kAct>, f) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, ffn_finish_kernel<kBN, kEpi, kF16, kAct>, p) != cudaSuccess) {
         cudaGetLastError();
         return ROPE3D_ERR_CUDA;
     }

@@ -636,9 +636,8 @@ NormFn back_team_fn(int dtype, bool vec, int elems, int team);
 NormFn back_ring_fn(int dtype, bool layer, bool full, bool shift);
 NormFn back_any_fn();
 NormFn back_cols_fn();
-NormFn finish_fn();
+NormFn finish_fn(int rows);   // 8, 16 or 32 rows of 32 threads
 NormFn groups_fn();
-constexpr int kFinishRows = 16;   // rows of threads of the finish kernel (32 each)
 
 // The backward file's count of waits that ran out; a CUDA error code.
 int back_wait_timeouts(unsigned int *count, bool reset);

@@ -609,12 +609,13 @@ __global__ void __launch_bounds__(kGeneralThreads) block_norm_back_cols_kernel(c
 }
 
 // The chunks' partial sums of one group (blockIdx.y), or the weights' of all
-// chunks, 32 channels a block: 16 rows of threads each add every 16th chunk,
-// several loads in flight, then those sums in order. Where several groups make
-// up the weights' gradients, their parts go to p.group_sums, [groups][2][channels],
-// and block_norm_groups_kernel adds them.
-__global__ void __launch_bounds__(32 * kFinishRows) block_norm_finish_kernel(const __grid_constant__ NormParams p) {
-    __shared__ float part[3][kFinishRows][32];
+// chunks, 32 channels a block: n rows of threads each add every n-th chunk, up to
+// 16 of them in flight, then the rows' sums in order. Where several
+// groups make up the weights' gradients, their parts go to p.group_sums,
+// [groups][2][channels], and block_norm_groups_kernel adds them.
+template <int n>
+__global__ void __launch_bounds__(32 * n) block_norm_finish_kernel(const __grid_constant__ NormParams p) {
+    __shared__ float part[3][n][32];
     grid_wait();
     grid_release();
     const int lane = threadIdx.x & 31, ty = threadIdx.x >> 5, g = int(blockIdx.y);
@@ -630,15 +631,17 @@ __global__ void __launch_bounds__(32 * kFinishRows) block_norm_finish_kernel(con
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
             if (!want[k]) continue;
+            const float *col = src + (long long)k * p.channels;
             int i = ty;
-            for (; i + 7 * kFinishRows < per; i += 8 * kFinishRows) {
-                float v[8];
+            for (; i + 15 * n < per; i += 16 * n) {
+                float v[16];
 #pragma unroll
-                for (int u = 0; u < 8; ++u) v[u] = __ldcs(src + (i + u * kFinishRows) * step + (long long)k * p.channels);
+                for (int u = 0; u < 16; ++u) v[u] = __ldcs(col + (i + u * n) * step);
 #pragma unroll
-                for (int u = 0; u < 8; ++u) s[k] += v[u];
+                for (int u = 0; u < 16; ++u) s[k] += v[u];
             }
-            for (; i < per; i += kFinishRows) s[k] += __ldcs(src + i * step + (long long)k * p.channels);
+#pragma unroll 4
+            for (; i < per; i += n) s[k] += __ldcs(col + i * step);
         }
     }
 #pragma unroll
@@ -648,7 +651,7 @@ __global__ void __launch_bounds__(32 * kFinishRows) block_norm_finish_kernel(con
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
         s[k] = 0.0f;
-        for (int i = 0; i < kFinishRows; ++i) s[k] += part[k][i][lane];
+        for (int i = 0; i < n; ++i) s[k] += part[k][i][lane];
     }
     float wq = s[0], wp = s[2];
     if (!p.groups_per_chunk) {
@@ -729,7 +732,7 @@ NormFn back_ring_fn(int dtype, bool layer, bool full, bool shift) {
 
 NormFn back_any_fn() { return block_norm_back_any_kernel; }
 NormFn back_cols_fn() { return block_norm_back_cols_kernel; }
-NormFn finish_fn() { return block_norm_finish_kernel; }
+NormFn finish_fn(int rows) { return rows == 8 ? block_norm_finish_kernel<8> : rows == 16 ? block_norm_finish_kernel<16> : block_norm_finish_kernel<32>; }
 NormFn groups_fn() { return block_norm_groups_kernel; }
 
 int back_wait_timeouts(unsigned int *count, bool reset) {
