@@ -880,7 +880,8 @@ def rope3d_gated_ffn(x, w_gate, w_up, w_down, act: int = ACT_GELU_TANH, y=None, 
     width] (or [..., width]), w_gate and w_up [hidden, width], w_down [width,
     hidden], bf16 or fp16 on the device. keep: also return the two projections
     [tokens, hidden] for the backward pass, in float32 (True) or in a given dtype
-    (float32 or x's); gate_pre / up_pre take them instead of new tensors. Returns
+    (float32 or x's), as [tokens, hidden] views of padded rows where hidden is no
+    multiple of 16; gate_pre / up_pre take them instead of new tensors. Returns
     y, or (y, gate_pre, up_pre). workspace: a uint8 device tensor of at least the
     bytes the call needs (allocated when None)."""
     torch = _torch or _use_torch()
@@ -889,8 +890,13 @@ def rope3d_gated_ffn(x, w_gate, w_up, w_down, act: int = ACT_GELU_TANH, y=None, 
     if y is None:
         y = _fresh(x)
     if keep is not False and keep is not None and gate_pre is None and up_pre is None:
-        shape, kept = (*x.shape[:-1], hidden), torch.float32 if keep is True else keep
-        gate_pre, up_pre = _new(shape, kept, x), _new(shape, kept, x)
+        kept = torch.float32 if keep is True else keep
+        if hidden % 16 == 0:
+            shape = (*x.shape[:-1], hidden)
+            gate_pre, up_pre = _new(shape, kept, x), _new(shape, kept, x)
+        else:   # rows padded to a multiple of 16: on 32-byte boundaries, as the backward pass reads them best
+            pad = -(-hidden // 16) * 16
+            gate_pre, up_pre = (_new((tokens, pad), kept, x)[:, :hidden] for _ in range(2))
     pre_ld, pre_code = _pre_fields(gate_pre, up_pre, tokens, hidden, code)
     body = (x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), y.data_ptr(),
             _ptr_of(gate_pre), _ptr_of(up_pre), tokens, width,

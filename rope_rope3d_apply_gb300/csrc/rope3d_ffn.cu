@@ -69,8 +69,15 @@ __device__ __forceinline__ float activation(float g, float *grad) {
         if constexpr (kGrad) *grad = q + g * (q * (1.0f - q) * (1.5957691216f + 0.2140644488f * s));
         return g * q;
     } else {
-        const float cdf = 0.5f * (1.0f + erff(g * 0.7071067812f));
-        if constexpr (kGrad) *grad = cdf + g * (0.3989422804f * __expf(-0.5f * g * g));
+        // erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2), t = 1 / (1 + p x), x >= 0:
+        // Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26, off by
+        // at most 1.5e-7; here x = |g| / sqrt(2), and the slope needs the same
+        // exp(-g^2 / 2)
+        const float x = fabsf(g) * 0.7071067812f;
+        const float t = rcp(1.0f + 0.3275911f * x), e = __expf(-x * x);
+        const float poly = t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
+        const float tail = 0.5f * poly * e, cdf = g < 0.0f ? tail : 1.0f - tail;
+        if constexpr (kGrad) *grad = cdf + g * (0.3989422804f * e);
         return g * cdf;
     }
 }
@@ -340,23 +347,36 @@ __device__ __forceinline__ void store_words(Boxes &bx, const uint32_t *w, const 
     } else {
         __syncwarp();
         const int rows = min(32, m - row0);
+        // eight loads in flight: the loop would wait for each otherwise
         if (o.f32) {   // two rows at a time
-            const int e = bx.lane & 15;
-            for (int i = bx.lane >> 4; i < rows; i += 2) {
-                float v;
-                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v)
-                             : "r"(box + uint32_t(i) * 64 + (((uint32_t(e) >> 2) ^ ((uint32_t(i) >> 1) & 3)) << 4) + (e & 3) * 4)
-                             : "memory");
-                if (col + e < n) static_cast<float *>(o.p)[(row0 + i) * o.ld + col + e] = v;
+            const int e = bx.lane & 15, odd = bx.lane >> 4;
+            float *d = static_cast<float *>(o.p) + (row0 + odd) * o.ld + col + e;
+            for (int i = 0; i < rows; i += 16) {
+                float v[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const uint32_t r = uint32_t(i + 2 * u + odd);
+                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[u])
+                                 : "r"(box + r * 64 + (((uint32_t(e) >> 2) ^ ((r >> 1) & 3)) << 4) + (e & 3) * 4) : "memory");
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (i + 2 * u + odd < rows && col + e < n) d[(i + 2 * u) * o.ld] = v[u];
             }
         } else {
             const int e = bx.lane;
-            for (int i = 0; i < rows; ++i) {
-                uint16_t v;
-                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v)
-                             : "r"(box + uint32_t(i) * 64 + (((uint32_t(e) >> 3) ^ ((uint32_t(i) >> 1) & 3)) << 4) + (e & 7) * 2)
-                             : "memory");
-                if (col + e < n) static_cast<uint16_t *>(o.p)[(row0 + i) * o.ld + col + e] = v;
+            uint16_t *d = static_cast<uint16_t *>(o.p) + row0 * o.ld + col + e;
+            for (int i = 0; i < rows; i += 8) {
+                uint16_t v[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const uint32_t r = uint32_t(i + u);
+                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v[u])
+                                 : "r"(box + r * 64 + (((uint32_t(e) >> 3) ^ ((r >> 1) & 3)) << 4) + (e & 7) * 2) : "memory");
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (i + u < rows && col + e < n) d[(i + u) * o.ld] = v[u];
             }
         }
         __syncwarp();
@@ -654,31 +674,46 @@ ffn_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Param
     if (warp == 2) tmem_free<true>(tmem, 512);
 }
 
-// Eight values of one row from column `col` of output o (the first `valid` exist).
+// Eight values of each lane's row (row0 + lane) from column `col` of output o, the
+// first `valid` of which exist. The block's four warps hold 32 consecutive columns:
+// where rows do not start on 16-byte boundaries they are exchanged through shared
+// memory and stored row by row, consecutive elements by consecutive lanes.
 template <bool kF16>
-__device__ __forceinline__ void store8(const Out &o, int row, int col, int valid, const float *v) {
+__device__ __forceinline__ void store8(const Out &o, int row0, int col, int valid, const float *v, const Sub &sub,
+                                       float (*stage)[33]) {
     if (!o.p) return;
-    const long long at = row * o.ld + col;
-    if (o.f32) {
-        float *d = static_cast<float *>(o.p) + at;
-        if (o.vec && valid >= 8) {
-            reinterpret_cast<float4 *>(d)[0] = make_float4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<float4 *>(d)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (o.vec) {
+        const long long at = (row0 + lane) * o.ld + col;
+        if (valid >= 8 && o.f32) {
+            float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(o.p) + at);
+            d[0] = make_float4(v[0], v[1], v[2], v[3]);
+            d[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else if (valid >= 8) {
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(o.p) + at) =
+                make_uint4(pack2<kF16>(v[0], v[1]), pack2<kF16>(v[2], v[3]), pack2<kF16>(v[4], v[5]), pack2<kF16>(v[6], v[7]));
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (i < valid) d[i] = v[i];
+                if (i < valid) {
+                    if (o.f32) static_cast<float *>(o.p)[at + i] = v[i];
+                    else static_cast<uint16_t *>(o.p)[at + i] = pack1(v[i], kF16);
+                }
         }
-    } else {
-        uint16_t *d = static_cast<uint16_t *>(o.p) + at;
-        if (o.vec && valid >= 8) {
-            *reinterpret_cast<uint4 *>(d) = make_uint4(pack2<kF16>(v[0], v[1]), pack2<kF16>(v[2], v[3]),
-                                                       pack2<kF16>(v[4], v[5]), pack2<kF16>(v[6], v[7]));
-        } else {
+        return;
+    }
+    __syncthreads();
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < valid) d[i] = pack1(v[i], kF16);
-        }
+    for (int i = 0; i < 8; ++i) stage[lane][warp * 8 + i] = v[i];
+    __syncthreads();
+    const int c = col - warp * 8 + lane;
+    if (c >= sub.n) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int row = row0 + warp * 8 + i;
+        if (row >= sub.m) break;
+        if (o.f32) static_cast<float *>(o.p)[row * o.ld + c] = stage[warp * 8 + i][lane];
+        else static_cast<uint16_t *>(o.p)[row * o.ld + c] = pack1(stage[warp * 8 + i][lane], kF16);
     }
 }
 
@@ -695,7 +730,8 @@ __global__ void __launch_bounds__(128) ffn_finish_kernel(const __grid_constant__
     w /= kChunks;
     const int rows = w & 7, tile = w >> 3;
     const Tile x = tile_at(p.sub[0], p.whole + tile);
-    const int row = x.m0 * 256 + rows * 32 + lane, col = x.n0 * kTileCols + chunk * 8;
+    const int row0 = x.m0 * 256 + rows * 32, row = row0 + lane, col = x.n0 * kTileCols + chunk * 8;
+    __shared__ float stage[32][33];
     const int valid = row < p.sub[0].m ? p.sub[0].n - col : 0;
     auto sums = [&](float *v, int c) {
         const float *src = p.part + ((long long)tile * p.split * 8 + rows) * (kBN * 32) + c * 32 + lane;
@@ -713,14 +749,11 @@ __global__ void __launch_bounds__(128) ffn_finish_kernel(const __grid_constant__
         sums(u, kBN / 2 + chunk * 8);
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[i] = activation<kAct, false>(v[i], nullptr) * u[i];
-        if (valid > 0) {
-            store8<kF16>(p.out[0], row, col, valid, h);
-            store8<kF16>(p.out[1], row, col, valid, v);
-            store8<kF16>(p.out[2], row, col, valid, u);
-        }
+        store8<kF16>(p.out[0], row0, col, valid, h, p.sub[0], stage);
+        store8<kF16>(p.out[1], row0, col, valid, v, p.sub[0], stage);
+        store8<kF16>(p.out[2], row0, col, valid, u, p.sub[0], stage);
     } else if constexpr (kEpi == kBack) {
-        if (valid <= 0) return;
-        float dg[8], du[8], h[8];
+        float dg[8] = {}, du[8] = {}, h[8] = {};
         const long long at = row * p.ldp + col;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -735,11 +768,11 @@ __global__ void __launch_bounds__(128) ffn_finish_kernel(const __grid_constant__
             du[i] = v[i] * a;
             h[i] = a * u;
         }
-        store8<kF16>(p.out[0], row, col, valid, dg);
-        store8<kF16>(p.out[1], row, col, valid, du);
-        store8<kF16>(p.out[2], row, col, valid, h);
-    } else if (valid > 0) {
-        store8<kF16>(p.out[0], row, col, valid, v);
+        store8<kF16>(p.out[0], row0, col, valid, dg, p.sub[0], stage);
+        store8<kF16>(p.out[1], row0, col, valid, du, p.sub[0], stage);
+        store8<kF16>(p.out[2], row0, col, valid, h, p.sub[0], stage);
+    } else {
+        store8<kF16>(p.out[0], row0, col, valid, v, p.sub[0], stage);
     }
 }
 
