@@ -891,12 +891,10 @@ def rope3d_gated_ffn(x, w_gate, w_up, w_down, act: int = ACT_GELU_TANH, y=None, 
         y = _fresh(x)
     if keep is not False and keep is not None and gate_pre is None and up_pre is None:
         kept = torch.float32 if keep is True else keep
-        if hidden % 16 == 0:
-            shape = (*x.shape[:-1], hidden)
-            gate_pre, up_pre = _new(shape, kept, x), _new(shape, kept, x)
-        else:   # rows padded to a multiple of 16: on 32-byte boundaries, as the backward pass reads them best
-            pad = -(-hidden // 16) * 16
-            gate_pre, up_pre = (_new((tokens, pad), kept, x)[:, :hidden] for _ in range(2))
+        pad = -(-hidden // 16) * 16   # rows on 32-byte boundaries, as the backward pass reads them best
+        gate_pre, up_pre = _new((tokens, pad), kept, x), _new((tokens, pad), kept, x)
+        if pad != hidden:
+            gate_pre, up_pre = gate_pre[:, :hidden], up_pre[:, :hidden]
     pre_ld, pre_code = _pre_fields(gate_pre, up_pre, tokens, hidden, code)
     body = (x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), y.data_ptr(),
             _ptr_of(gate_pre), _ptr_of(up_pre), tokens, width,

@@ -364,17 +364,16 @@ struct Team {
     int elems, threads, team;
 };
 
-// Single elements (8000 rows, RMS before and after): fp32 1790 channels 53 us of
-// the general kernel's 145, 4001: 113 of 265; bf16 1001: 49 of 68, but 2049: 156
-// of 138, so longer 16-bit rows take the general kernel.
-Team forward_team(int64_t c, bool vec, int es) {
+// Single elements: fp32 8000 x 1790 takes 53 us of the general kernel's 145, 8000 x
+// 4001 113 of 265; bf16 8 x 4001 6.4 of 20, 1216 x 8003 52 of 75, fp16 4864 x 4001
+// without y 41 of 96. Past the L2 cache bf16 rows with y gain nothing (9728 x 4001
+// 316 us both, 4864 x 8003 336 of 320): partly written sectors bound both.
+Team forward_team(int64_t c, bool vec) {
     if (c <= 64) return Team{8, 128, 8};
     if (c <= 256) return Team{8, 128, 32};
     if (c <= 512) return Team{16, 128, 32};
     if (!vec) {
-        if (c <= 16 * 128) return Team{16, 128, 128};
-        if (es == 2) return Team{0, 0, 0};
-        for (int t : {256, 512})
+        for (int t : {128, 256, 512})
             if (c <= 16 * t) return Team{16, t, t};
         return c <= 32 * 512 ? Team{32, 512, 512} : Team{0, 0, 0};
     }
@@ -410,13 +409,9 @@ NormFn team_fn(const Team &t, bool vec) {
         case 8: return block_norm_team_kernel<kT, false, 8, 8>;
         case 32: return t.elems == 8 ? block_norm_team_kernel<kT, false, 8, 32> : block_norm_team_kernel<kT, false, 16, 32>;
         case 128: return block_norm_team_kernel<kT, false, 16, 128>;
-        default: break;
+        case 256: return block_norm_team_kernel<kT, false, 16, 256>;
+        default: return t.elems == 16 ? block_norm_team_kernel<kT, false, 16, 512> : block_norm_team_kernel<kT, false, 32, 512>;
     }
-    if constexpr (kT == ROPE3D_F32) {
-        if (t.team == 256) return block_norm_team_kernel<kT, false, 16, 256>;
-        return t.elems == 16 ? block_norm_team_kernel<kT, false, 16, 512> : block_norm_team_kernel<kT, false, 32, 512>;
-    }
-    return nullptr;   // (forward_team names no other)
 }
 
 // The ring kernels' shape for rows of `channels` elements of es bytes: threads of
@@ -485,7 +480,7 @@ int forward(const rope3d_block_norm_args *a, bool run, bool check_device, cudaSt
     const int sms = sm_count();
     if (sms <= 0) return ROPE3D_ERR_CUDA;
     const bool vec = vectors(all, 9, C, 16 / es);
-    const Team t = forward_team(C, vec, es);
+    const Team t = forward_team(C, vec);
     if (t.elems == 0) {
         t_norm_kernel = 2;
         return launch(block_norm_any_kernel, dim3(unsigned(std::min<int64_t>(R, int64_t(sms) * 8))),

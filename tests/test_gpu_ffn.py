@@ -63,6 +63,22 @@ def test_forward(shape, dtype, act):
     assert torch.equal(r.rope3d_gated_ffn(**w, act=act), y)
 
 
+@pytest.mark.parametrize("hidden", [1, 64, 250, 255])
+def test_kept_shapes(hidden):
+    """Kept projections are [tokens, hidden] for any shape of x, as the backward pass takes them."""
+    w, dy = make(6, 40, hidden, "bf16")
+    y, g, u = r.rope3d_gated_ffn(**w, keep=True)
+    x = w.pop("x").view(2, 3, 40)
+    y3, g3, u3 = r.rope3d_gated_ffn(x, **w, keep=True)
+    assert y3.shape == x.shape and g3.shape == u3.shape == (6, hidden)
+    assert torch.equal(y3.view(6, 40), y) and torch.equal(g3, g) and torch.equal(u3, u)
+    got = r.rope3d_gated_ffn_backward(dy.view(2, 3, 40), x, *w.values(), g3, u3)
+    want = r.rope3d_gated_ffn_backward(dy, x.view(6, 40), *w.values(), g.contiguous(), u.contiguous())
+    assert got[0].shape == x.shape
+    for a, b in zip(got, want):
+        assert torch.equal(a.view(b.shape), b)
+
+
 @pytest.mark.parametrize("kept", ["f32", "half", "again"])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("shape", SHAPES + ODD, ids=str)
