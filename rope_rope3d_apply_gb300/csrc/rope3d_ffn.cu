@@ -135,6 +135,7 @@ struct Out {
     int f32;
     int vec;          // rows start on 16-byte boundaries
     int tma;          // and are stored through the tensor map
+    int word;         // else: bytes (2, 4 or 8) that base and rows are multiples of
 };
 
 struct Maps {
@@ -323,10 +324,53 @@ struct Boxes {
     int lane;
 };
 
+// `bytes` of the first `rows` rows of a staging box to rows of `pitch` bytes at d,
+// which start on multiples of kW bytes: 64 / kW lanes a row, words of kW bytes,
+// eight loads in flight.
+template <int kW>
+__device__ __forceinline__ void copy_box(uint32_t box, char *d, long long pitch, int lane, int rows, int bytes) {
+    constexpr int kLanes = 64 / kW, kRows = kW / 2;
+    const int b = (lane % kLanes) * kW, first = lane / kLanes;
+    d += first * pitch + b;
+    for (int i = 0; i < rows; i += 8 * kRows) {
+        uint64_t v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const uint32_t r = uint32_t(i + u * kRows + first);
+            const uint32_t at = box + r * 64 + (((uint32_t(b) >> 4) ^ ((r >> 1) & 3)) << 4) + (uint32_t(b) & 15);
+            if constexpr (kW == 8) {
+                asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v[u]) : "r"(at) : "memory");
+            } else if constexpr (kW == 4) {
+                uint32_t w;
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
+                v[u] = w;
+            } else {
+                uint16_t w;
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(w) : "r"(at) : "memory");
+                v[u] = w;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if (i + u * kRows + first >= rows) break;
+            char *at = d + (i + u * kRows) * pitch;
+            if (b + kW <= bytes) {
+                if constexpr (kW == 8) *reinterpret_cast<uint64_t *>(at) = v[u];
+                else if constexpr (kW == 4) *reinterpret_cast<uint32_t *>(at) = uint32_t(v[u]);
+                else *reinterpret_cast<uint16_t *>(at) = uint16_t(v[u]);
+            } else if constexpr (kW > 2) {   // the row ends inside the word
+#pragma unroll
+                for (int h = 0; h < kW / 2; ++h)
+                    if (b + 2 * h < bytes) reinterpret_cast<uint16_t *>(at)[h] = uint16_t(v[u] >> (16 * h));
+            }
+        }
+    }
+}
+
 // 16 words (64 bytes: 32 16-bit or 16 fp32 elements) of each lane's row, from
 // column `col` of output o; the warp's rows are row0 .. row0 + 31. Through a
-// staging box: a TMA store, or where TMA cannot address the rows, stores of
-// consecutive elements by consecutive lanes.
+// staging box: a TMA store, or where TMA cannot address the rows, the widest
+// words that they are aligned to.
 __device__ __forceinline__ void store_words(Boxes &bx, const uint32_t *w, const Out &o,
                                             const CUtensorMap *map, int row0, int col, int m, int n) {
     if (!o.p || row0 >= m || col >= n) return;
@@ -346,39 +390,12 @@ __device__ __forceinline__ void store_words(Boxes &bx, const uint32_t *w, const 
         if (bx.lane == 0) tma_store2(map, box, col, row0);
     } else {
         __syncwarp();
-        const int rows = min(32, m - row0);
-        // eight loads in flight: the loop would wait for each otherwise
-        if (o.f32) {   // two rows at a time
-            const int e = bx.lane & 15, odd = bx.lane >> 4;
-            float *d = static_cast<float *>(o.p) + (row0 + odd) * o.ld + col + e;
-            for (int i = 0; i < rows; i += 16) {
-                float v[8];
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    const uint32_t r = uint32_t(i + 2 * u + odd);
-                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[u])
-                                 : "r"(box + r * 64 + (((uint32_t(e) >> 2) ^ ((r >> 1) & 3)) << 4) + (e & 3) * 4) : "memory");
-                }
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    if (i + 2 * u + odd < rows && col + e < n) d[(i + 2 * u) * o.ld] = v[u];
-            }
-        } else {
-            const int e = bx.lane;
-            uint16_t *d = static_cast<uint16_t *>(o.p) + row0 * o.ld + col + e;
-            for (int i = 0; i < rows; i += 8) {
-                uint16_t v[8];
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    const uint32_t r = uint32_t(i + u);
-                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v[u])
-                                 : "r"(box + r * 64 + (((uint32_t(e) >> 3) ^ ((r >> 1) & 3)) << 4) + (e & 7) * 2) : "memory");
-                }
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    if (i + u < rows && col + e < n) d[(i + u) * o.ld] = v[u];
-            }
-        }
+        const int rows = min(32, m - row0), bytes = min(64, (n - col) << (o.f32 ? 2 : 1));
+        char *d = static_cast<char *>(o.p) + ((row0 * o.ld + col) << (o.f32 ? 2 : 1));
+        const long long pitch = o.ld << (o.f32 ? 2 : 1);
+        if (o.word == 2) copy_box<2>(box, d, pitch, bx.lane, rows, bytes);
+        else if (o.word == 4) copy_box<4>(box, d, pitch, bx.lane, rows, bytes);
+        else copy_box<8>(box, d, pitch, bx.lane, rows, bytes);
         __syncwarp();
     }
     if (bx.lane == 0) bulk_commit();   // (an empty group where nothing was copied: boxes are counted by groups)
@@ -1004,13 +1021,14 @@ ffn_stream_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Par
 
 // 16-bit matrices copied to rows that start on 16-byte boundaries (dst_ld a
 // multiple of 8), up to five in one launch. A thread makes 8 elements of a row:
-// eight 2-byte loads (consecutive threads read consecutive bytes), one 16-byte
-// store; what a row has past its last column is not written.
+// loads of the widest words that the rows are aligned to (2, 4 or 8 bytes;
+// consecutive threads read consecutive bytes), one 16-byte store; what a row has
+// past its last column is not written.
 struct AlignJob {
     const uint16_t *src;
     uint16_t *dst;
     long long src_ld, dst_ld;
-    int cols, vecs;              // 8-element vectors of a row
+    int cols, vecs, word;        // vecs: 8-element vectors of a row; word: bytes of a load
     long long first, rows;       // the job's first vector in the launch
 };
 
@@ -1034,8 +1052,17 @@ __global__ void __launch_bounds__(256) ffn_align_kernel(const __grid_constant__ 
         uint16_t *d = j.dst + row * j.dst_ld + c;
         if (c + 8 <= j.cols) {
             uint32_t w[4];
+            if (j.word == 8) {
+                const uint2 *t = reinterpret_cast<const uint2 *>(s);
+                const uint2 lo = t[0], hi = t[1];
+                w[0] = lo.x; w[1] = lo.y; w[2] = hi.x; w[3] = hi.y;
+            } else if (j.word == 4) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = uint32_t(s[2 * e]) | uint32_t(s[2 * e + 1]) << 16;
+                for (int e = 0; e < 4; ++e) w[e] = reinterpret_cast<const uint32_t *>(s)[e];
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = uint32_t(s[2 * e]) | uint32_t(s[2 * e + 1]) << 16;
+            }
             *reinterpret_cast<uint4 *>(d) = make_uint4(w[0], w[1], w[2], w[3]);
         } else {
             for (int e = 0; c + e < j.cols; ++e) d[e] = s[e];
@@ -1063,6 +1090,13 @@ EncodeTiledFn encode_tiled() {
         return reinterpret_cast<EncodeTiledFn>(ptr);
     }();
     return fn;
+}
+
+// The widest of 8, 4 and 2 bytes that rows of `pitch` bytes at p all start on
+// multiples of.
+int word_of(const void *p, int64_t pitch) {
+    const uint64_t bits = reinterpret_cast<uintptr_t>(p) | uint64_t(pitch);
+    return bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : 2;
 }
 
 // A row-major matrix of 16-bit elements in device memory.
@@ -1109,6 +1143,7 @@ int set_outs(Params &p, Maps &maps, const Out *outs, int first, int count, int64
         const int es = o.f32 ? 4 : 2;
         o.vec = o.p && tma_ok(o.p, o.ld, es);
         o.tma = maps_too && o.vec;
+        o.word = word_of(o.p, o.ld * es);
         if (o.tma && !make_map(&maps.c[i], o.p, rows, cols, o.ld, es, p.f16, o.f32 ? 16 : 32, 32, false))
             return ROPE3D_ERR_CUDA;
     }
@@ -1397,7 +1432,7 @@ void aligned(Mat &x, Carver &ws, AlignJobs *jobs) {
     void *dst = ws.take(x.rows * ld * 2);
     if (jobs) {
         jobs->job[jobs->count++] = AlignJob{static_cast<const uint16_t *>(x.p), static_cast<uint16_t *>(dst),
-                                            x.ld, ld, int(x.cols), int(ld / 8), jobs->total, x.rows};
+                                            x.ld, ld, int(x.cols), int(ld / 8), word_of(x.p, x.ld * 2), jobs->total, x.rows};
         jobs->total += x.rows * (ld / 8);
     }
     x.p = dst;
