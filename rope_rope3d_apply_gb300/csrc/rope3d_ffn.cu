@@ -586,6 +586,7 @@ ffn_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Param
                 }
                 commit_pair(acc_full(b));
             }
+            if (dead) drain(full, it, kStages, &g_ffn_wait_timeouts);   // (the pair's copies: the other CTA waits below)
         }
     } else if (warp >= 4) {
         const int quad = warp & 3, half = (warp - 4) >> 2;
@@ -897,7 +898,8 @@ ffn_stream_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Par
         }
     } else if (warp == 1 && lane == 0) {
         const uint32_t id = idesc(128, uint32_t(p.rows_n), !p.f16, kAMn, false);
-        for (int i = 0; i < k_hi - k_lo; ++i) {
+        int i = 0;
+        for (; i < k_hi - k_lo; ++i) {
             const int s = i % p.stages;
             if (!mbar_wait(full(s), uint32_t(i / p.stages) & 1u, dead, &g_ffn_wait_timeouts)) break;
             tc_fence_after();
@@ -914,6 +916,7 @@ ffn_stream_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Par
             commit(empty(s));
         }
         commit(done);
+        if (dead) drain(full, i, p.stages, &g_ffn_wait_timeouts);
     }
     if (warp >= 2) {
         // results of earlier kernels are visible from here; only then may a

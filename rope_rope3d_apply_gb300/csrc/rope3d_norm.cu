@@ -166,6 +166,7 @@ __global__ void __maxnreg__(80) block_norm_ring_kernel(const __grid_constant__ N
     if (tid == 0)
         for (int s = 0; s < p.stages && lo + s < hi; ++s) fill(s, lo + s);
     bool dead = false;
+    int lost = -1;   // the first row whose wait ran out
     const float2 res = both(p.res);
     int g = int(uint32_t(lo) / uint32_t(p.rows_per_group)) - 1;
     long long group_end = lo;   // the first row starts a group
@@ -184,7 +185,7 @@ __global__ void __maxnreg__(80) block_norm_ring_kernel(const __grid_constant__ N
                 ld_param<kT>(p.shift, g * p.ldsh + (team.real(j) ? team.channel(j) : 0), p.param_f32, 0.0f, m + j * Team::V);
             ks.store(m);
         }
-        mbar_wait(ring.bars + 8u * uint32_t(s), phase, dead, &g_norm_wait_timeouts);
+        if (!mbar_wait(ring.bars + 8u * uint32_t(s), phase, dead, &g_norm_wait_timeouts) && lost < 0) lost = int(row - lo);
         const uint32_t at = ring.base + uint32_t(s) * ring.stage_bytes;
         float2 v[H];
         team.unpack_row(at, v);
@@ -222,6 +223,8 @@ __global__ void __maxnreg__(80) block_norm_ring_kernel(const __grid_constant__ N
             phase ^= 1;
         }
     }
+    if (tid == 0 && dead)
+        drain([&](int i) { return ring.bars + 8u * uint32_t(i); }, lost, p.stages, &g_norm_wait_timeouts);
 }
 
 // ---- host ------------------------------------------------------------------------------------

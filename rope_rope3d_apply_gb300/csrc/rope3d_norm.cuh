@@ -16,6 +16,7 @@
 
 namespace rope3d_norm {
 
+using rope3d_tc::drain;
 using rope3d_tc::grid_release;
 using rope3d_tc::grid_wait;
 using rope3d_tc::mbar_expect_tx;

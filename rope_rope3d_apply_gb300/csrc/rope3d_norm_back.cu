@@ -280,6 +280,7 @@ __global__ void __launch_bounds__(512) block_norm_back_ring_kernel(const __grid_
     if (tid == 0)
         for (int s = 0; s < p.stages && lo + s < hi; ++s) fill(s, lo + s);
     bool dead = false;
+    int lost = -1;   // the first row whose wait ran out
     const float2 zero = make_float2(0.0f, 0.0f), res = both(p.res);
     float2 S[H], U[H], T[kShift ? H : 1];
 #pragma unroll
@@ -304,7 +305,7 @@ __global__ void __launch_bounds__(512) block_norm_back_ring_kernel(const __grid_
             km.store(m);
             kq.store(q);
         }
-        mbar_wait(ring.bars + 8u * uint32_t(s), phase, dead, &g_norm_wait_timeouts);
+        if (!mbar_wait(ring.bars + 8u * uint32_t(s), phase, dead, &g_norm_wait_timeouts) && lost < 0) lost = int(row - lo);
         const uint32_t at = ring.base + uint32_t(s) * ring.stage_bytes;
         // y normalised, r = res x + m y, dn
         float2 y[H], r[H], d[H];
@@ -474,6 +475,8 @@ __global__ void __launch_bounds__(512) block_norm_back_ring_kernel(const __grid_
             for (int i = 0; i < (kShift ? H : 1); ++i) T[i] = zero;
         }
     }
+    if (tid == 0 && dead)
+        drain([&](int i) { return ring.bars + 8u * uint32_t(i); }, lost, p.stages, &g_norm_wait_timeouts);
     if (p.part) {
         if (p.groups_per_chunk) {
             kwq.load(S);

@@ -97,6 +97,17 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, bool &d
     }
 }
 
+// After a wait of this thread ran out: wait, each time with the same limit, for
+// the copies that may still be on their way, fills first .. first + stages - 1 of a
+// ring (fill i lands in slot i % stages), so that they do not outlive the block.
+template <typename Full>
+__device__ __forceinline__ void drain(Full full, int first, int stages, unsigned int *timeouts) {
+    for (int i = first; i < first + stages; ++i) {
+        bool late = false;
+        mbar_wait(full(i % stages), uint32_t(i / stages) & 1u, late, timeouts);
+    }
+}
+
 // ---- TMA -------------------------------------------------------------------------
 
 // One box of a 2-D tensor map into this CTA's shared memory. x (the contiguous
