@@ -117,8 +117,12 @@ __device__ __forceinline__ uint16_t pack1(float a, bool f16) {
     return f16 ? __half_as_ushort(__float2half_rn(a)) : __bfloat16_as_ushort(__float2bfloat16_rn(a));
 }
 
+// Two 16-bit loads in one word, and (unpack1) one value: without a shift right
+// behind a 16-bit load, which makes the loads wait for one another.
+__device__ __forceinline__ uint32_t word(uint32_t lo, uint32_t hi) { return __byte_perm(lo, hi, 0x5410); }
+
 __device__ __forceinline__ float unpack1(uint16_t v, bool f16) {
-    return f16 ? __half2float(__ushort_as_half(v)) : __uint_as_float(uint32_t(v) << 16);
+    return f16 ? __half2float(__ushort_as_half(v)) : __bfloat162float(__ushort_as_bfloat16(v));
 }
 
 // ---- launch description ---------------------------------------------------------
@@ -198,7 +202,7 @@ struct Pre16 {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const uint16_t *s = static_cast<const uint16_t *>(base) + off + 2 * i;
-                w[i] = (2 * i < valid ? uint32_t(s[0]) : 0u) | (2 * i + 1 < valid ? uint32_t(s[1]) << 16 : 0u);
+                w[i] = word(2 * i < valid ? s[0] : 0u, 2 * i + 1 < valid ? s[1] : 0u);
             }
         }
     }
@@ -1064,7 +1068,7 @@ __global__ void __launch_bounds__(256) ffn_align_kernel(const __grid_constant__ 
                 for (int e = 0; e < 4; ++e) w[e] = reinterpret_cast<const uint32_t *>(s)[e];
             } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = uint32_t(s[2 * e]) | uint32_t(s[2 * e + 1]) << 16;
+                for (int e = 0; e < 4; ++e) w[e] = word(s[2 * e], s[2 * e + 1]);
             }
             *reinterpret_cast<uint4 *>(d) = make_uint4(w[0], w[1], w[2], w[3]);
         } else {

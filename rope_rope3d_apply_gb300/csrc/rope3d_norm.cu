@@ -368,9 +368,8 @@ struct Team {
 };
 
 // Single elements: fp32 8000 x 1790 takes 53 us of the general kernel's 145, 8000 x
-// 4001 113 of 265; bf16 8 x 4001 6.4 of 20, 1216 x 8003 52 of 75, fp16 4864 x 4001
-// without y 41 of 96. Past the L2 cache bf16 rows with y gain nothing (9728 x 4001
-// 316 us both, 4864 x 8003 336 of 320): partly written sectors bound both.
+// 4001 113 of 265; bf16 8 x 4001 4.5 of 20, 1216 x 8003 34 of 75, 9728 x 4001 134 of
+// 316; fp16 4864 x 4001 without y 41 of 96.
 Team forward_team(int64_t c, bool vec) {
     if (c <= 64) return Team{8, 128, 8};
     if (c <= 256) return Team{8, 128, 32};

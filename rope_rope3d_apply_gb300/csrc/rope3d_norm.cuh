@@ -51,10 +51,14 @@ struct NormParams {
 
 // ---- elements -------------------------------------------------------------------
 
+// One bf16 value. (Not as bits << 16: right behind a 16-bit load that shift makes
+// the loads wait for one another; 8000 x 2049, backward: 375 us instead of 159.)
+__device__ __forceinline__ float from_bf16(uint16_t v) { return __bfloat162float(__ushort_as_bfloat16(v)); }
+
 __device__ __forceinline__ float load1(const void *p, long long i, int dtype) {
     if (dtype == ROPE3D_F32) return static_cast<const float *>(p)[i];
     const uint16_t v = static_cast<const uint16_t *>(p)[i];
-    return dtype == ROPE3D_F16 ? __half2float(__ushort_as_half(v)) : __uint_as_float(uint32_t(v) << 16);
+    return dtype == ROPE3D_F16 ? __half2float(__ushort_as_half(v)) : from_bf16(v);
 }
 
 __device__ __forceinline__ void store1(void *p, long long i, float v, int dtype) {
@@ -245,7 +249,7 @@ struct RowPart {
         for (int j = 0; j < PB; ++j) {
             if constexpr (kVec) unpack<kT>(raw[b * PB + j], f + j * W);
             else if constexpr (kT == ROPE3D_F32) f[j] = __uint_as_float(raw[b * PB + j]);
-            else if constexpr (kT == ROPE3D_BF16) f[j] = __uint_as_float(uint32_t(raw[b * PB + j]) << 16);
+            else if constexpr (kT == ROPE3D_BF16) f[j] = from_bf16(raw[b * PB + j]);
             else f[j] = __half2float(__ushort_as_half(raw[b * PB + j]));
         }
     }
@@ -288,7 +292,7 @@ struct RowPart {
                            ? (static_cast<const uint16_t *>(base) + at + lane)[(b * 8 + j) * size] : uint16_t(0);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                f[j] = kT == ROPE3D_BF16 ? __uint_as_float(uint32_t(w[j]) << 16) : __half2float(__ushort_as_half(w[j]));
+                f[j] = kT == ROPE3D_BF16 ? from_bf16(w[j]) : __half2float(__ushort_as_half(w[j]));
         }
     }
     static __device__ __forceinline__ void weight(const void *base, bool f32, float offset, int lane, int size, int channels,
