@@ -576,8 +576,14 @@ int backward(const rope3d_block_norm_backward_args *a, bool run, bool check_devi
         ring     ? kSms * shape.per_sm
         : t.elems ? kSms * (!is_block(t.team) ? 6 : t.threads > 256 ? 2 : t.threads > 128 ? 4 : 8)
                   : std::max<int64_t>(1, kSms * 8 / ((C + kGeneralThreads - 1) / kGeneralThreads));
-    // (four rows at least for each of a block's teams: fewer partial sums to add)
-    const int64_t least = !ring && t.elems && !is_block(t.team) ? 4 * t.threads / t.team : 1;
+    // Rows in registers: four rows at least for each of a block's teams, and for a team
+    // of a block as many up to four as leave one chunk an SM: fewer partial sums to
+    // add. (bf16, two RMS norms, rows a chunk: 600 x 4096 1 or 2: 32.7 us, 4: 23.9,
+    // 6: 25.0; 1000 x 2048 36.5, 25.3, 28.7; 300 x 2048 1: 22.1, 2: 20.5; 128 x 4096
+    // 1: 17.2, 2: 18.1.)
+    const int64_t least = ring || !t.elems      ? 1
+                          : !is_block(t.team) ? 4 * t.threads / t.team
+                                              : std::min<int64_t>(4, (R + kSms - 1) / kSms);
     const int64_t L = std::max<int64_t>(least, (R + target - 1) / target), rpg = p.rows_per_group;
     if (rpg >= L) {
         p.chunks_per_group = int((rpg + L - 1) / L);
