@@ -656,8 +656,8 @@ int backward(const rope3d_block_norm_backward_args *a, bool run, bool check_devi
     if (!partial) return ROPE3D_OK;
     // in split mode the groups are at most the chunks' target: far below 65535
     const int per = p.groups_per_chunk ? p.chunks : p.chunks_per_group;
-    // measured with the whole backward pass: 147 chunks of 4 groups (8192 x 2048 fp16)
-    // 54.0 us at 16 rows, 57.6 at 32; 2223 of one (20000 x 512 bf16) 43.3 and 37.4
+    // measured with the whole backward pass: 2223 chunks of one group (20000 x 512 bf16)
+    // 43 us at 16 rows, 38 at 32; 147 of each of 4 (8192 x 2048 fp16) 49 at 16
     const int rows = per <= 64 ? 8 : per <= 512 ? 16 : 32;
     rc = launch(finish_fn(rows), dim3(unsigned((C + 31) / 32), unsigned(p.groups_per_chunk ? 1 : G)), dim3(32 * rows), 0, p, st);
     if (rc != ROPE3D_OK || !by_group) return rc;

@@ -620,14 +620,16 @@ __global__ void __launch_bounds__(kGeneralThreads) block_norm_back_cols_kernel(c
 }
 
 // The chunks' partial sums of one group (blockIdx.y), or the weights' of all
-// chunks, 32 channels a block: n rows of threads each add every n-th chunk, up to
-// 16 of them in flight, then the rows' sums in order. Where several
+// chunks, 32 channels a block: n rows of threads each add every n-th chunk, then the
+// rows' sums in order. Few chunks: all of a thread's in flight, of all three sums;
+// many: 16 of one sum in flight (2223 chunks of 20000 x 512 bf16: 38 us with the
+// rows' kernel, 49 with eight of each sum). Where several
 // groups make up the weights' gradients, their parts go to p.group_sums,
 // [groups][2][channels], and block_norm_groups_kernel adds them. 304 chunks of 4096
-// channels, 10 MB, take 8 us: a chain of three dependent loads and sums.
+// channels, 10 MB, take 7 us: the latency of two rounds of loads and of the launch.
 template <int n>
 __global__ void __launch_bounds__(32 * n) block_norm_finish_kernel(const __grid_constant__ NormParams p) {
-    __shared__ float part[3][n][32];
+    __shared__ float part[3][n][32], param[4][32];
     grid_wait();
     grid_release();
     const int lane = threadIdx.x & 31, ty = threadIdx.x >> 5, g = int(blockIdx.y);
@@ -638,22 +640,43 @@ __global__ void __launch_bounds__(32 * n) block_norm_finish_kernel(const __grid_
     const bool want[3] = {p.d_pre_weight || p.d_scale, p.d_shift != nullptr, p.d_post_weight || p.d_gate};
     float s[3] = {0.0f, 0.0f, 0.0f};
     if (c < p.channels) {
+        if (ty < 4 && !p.groups_per_chunk) {   // a group's parameters, one a warp
+            const RowOps og{p, 0, g, 0.0f, 1.0f, 0.0f, 1.0f};
+            param[ty][lane] = ty == 0 ? og.scale1(c) : ty == 1 ? og.gate(c) : ty == 2 ? (p.d_scale ? og.wq(c) : 1.0f)
+                                                                                      : (p.d_gate ? og.wp(c) : 1.0f);
+        }
         const float *src = p.part + (long long)g * per * 3 * p.channels + c;
         const long long step = 3ll * p.channels;
+        if constexpr (n < 32) {
+            constexpr int kU = n == 8 ? 8 : 10;
+            for (int i = ty; i < per; i += kU * n) {
+                float v[3][kU];
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            if (!want[k]) continue;
-            const float *col = src + (long long)k * p.channels;
-            int i = ty;
-            for (; i + 15 * n < per; i += 16 * n) {
-                float v[16];
+                for (int u = 0; u < kU; ++u)
 #pragma unroll
-                for (int u = 0; u < 16; ++u) v[u] = __ldcs(col + (i + u * n) * step);
+                    for (int k = 0; k < 3; ++k)
+                        v[k][u] = want[k] && i + u * n < per ? __ldcs(src + (i + u * n) * step + (long long)k * p.channels) : 0.0f;
 #pragma unroll
-                for (int u = 0; u < 16; ++u) s[k] += v[u];
+                for (int u = 0; u < kU; ++u)
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) s[k] += v[k][u];
             }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                if (!want[k]) continue;
+                const float *col = src + (long long)k * p.channels;
+                int i = ty;
+                for (; i + 15 * n < per; i += 16 * n) {
+                    float v[16];
+#pragma unroll
+                    for (int u = 0; u < 16; ++u) v[u] = __ldcs(col + (i + u * n) * step);
+#pragma unroll
+                    for (int u = 0; u < 16; ++u) s[k] += v[u];
+                }
 #pragma unroll 4
-            for (; i < per; i += n) s[k] += __ldcs(col + i * step);
+                for (; i < per; i += n) s[k] += __ldcs(col + i * step);
+            }
         }
     }
 #pragma unroll
@@ -667,13 +690,12 @@ __global__ void __launch_bounds__(32 * n) block_norm_finish_kernel(const __grid_
     }
     float wq = s[0], wp = s[2];
     if (!p.groups_per_chunk) {
-        const RowOps og{p, 0, g, 0.0f, 1.0f, 0.0f, 1.0f};
         const long long at = g * p.ldgrad + c;
-        if (p.d_scale) store1(p.d_scale, at, og.wq(c) * s[0], param_type);
+        if (p.d_scale) store1(p.d_scale, at, param[2][lane] * s[0], param_type);
         if (p.d_shift) store1(p.d_shift, at, s[1], param_type);
-        if (p.d_gate) store1(p.d_gate, at, og.wp(c) * s[2], param_type);
-        wq *= og.scale1(c);
-        wp *= og.gate(c);
+        if (p.d_gate) store1(p.d_gate, at, param[3][lane] * s[2], param_type);
+        wq *= param[0][lane];
+        wp *= param[1][lane];
         if (p.group_sums) {
             float *dst = p.group_sums + (long long)g * 2 * p.channels + c;
             dst[0] = wq;
