@@ -1070,7 +1070,7 @@ __global__ void __launch_bounds__(256) ffn_align_kernel(const __grid_constant__ 
         int k = 0;
         while (k + 1 < jobs.count && i >= jobs.job[k + 1].first) ++k;
         const AlignJob &j = jobs.job[k];
-        const long long v = i - j.first, row = v / j.vecs;
+        const long long v = i - j.first, row = v >> 32 ? v / j.vecs : uint32_t(v) / uint32_t(j.vecs);
         const int c = int(v - row * j.vecs) * 8;
         const uint16_t *s = j.src + row * j.src_ld + c;
         uint16_t *d = j.dst + row * j.dst_ld + c;
