@@ -709,16 +709,28 @@ def _fresh(like):
     return _new(like.shape, like.dtype, like)
 
 
-def _scratch(nbytes: int, like, stream):
-    """Device memory for one call on the raw stream `stream`: given to other work
-    only after what that stream holds so far."""
-    ws = _new((nbytes,), _torch.uint8, like)
-    if stream != _torch._C._cuda_getCurrentRawStream(like.device.index):
-        ws.record_stream(_torch.cuda.ExternalStream(stream, device=like.device))
-    return ws
+def _elsewhere(call, args):
+    """The results of `call` (arguments by name) where its stream is not torch's
+    current one, else None. It then runs with that stream current, so that the memory
+    it allocates is that stream's. (The current stream's may be memory that its pending
+    work still reads.) What it returns is kept from other use until the current stream
+    has passed it too."""
+    torch = _torch or _use_torch()
+    x, stream = args["x"], args.pop("stream")
+    if not x.is_cuda or _raw_stream(stream, x) == torch._C._cuda_getCurrentRawStream(x.device.index):
+        return None
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_raw_stream(stream, x), device=x.device)
+    with torch.cuda.stream(stream):
+        out = call(**args)
+    here = torch.cuda.current_stream(x.device)
+    for t in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
+        if t is not None:
+            t.record_stream(here)
+    return out
 
 
-def _workspace(cls, fields, query, what, given, like, stream):
+def _workspace(cls, fields, query, what, given, like):
     """The packed arguments of a call (`fields` ends before workspace), with its
     workspace: `given`, or new memory of the size that `query` gives."""
     body, tail = fields
@@ -728,7 +740,7 @@ def _workspace(cls, fields, query, what, given, like, stream):
         _check(getattr(lib, query)(cls.pack(*body, 0, 0, *tail), ctypes.byref(need)), what)
         if not need.value:
             return cls.pack(*body, 0, 0, *tail), None
-        given = _scratch(need.value, like, stream)
+        given = _new((need.value,), _torch.uint8, like)
         return cls.pack(*body, given.data_ptr(), need.value, *tail), given
     return cls.pack(*body, given.data_ptr(), given.numel() * given.element_size(), *tail), given
 
@@ -780,7 +792,7 @@ def _weight(name, t, channels, dtype):
 
 def rope3d_block_norm(x, y=None, post: int = NORM_NONE, pre=NORM_RMS, post_weight=None, gate=None,
                       pre_weight=None, scale=None, shift=None, rows_per_group=None, eps: float = 1e-6,
-                      residual_scale: float = 1.0, weight_offset: float = 0.0, r=None, n=None, stream=None):
+                      residual_scale: float = 1.0, weight_offset: float = 0.0, r=None, n=None, *, stream=None):
     """The norms around a transformer block, in one pass over x and y [..., channels]:
         r = residual_scale * x + gate * post(y) * (post_weight + weight_offset)
         n = pre(r) * (pre_weight + weight_offset) * (1 + scale) + shift
@@ -788,6 +800,8 @@ def rope3d_block_norm(x, y=None, post: int = NORM_NONE, pre=NORM_RMS, post_weigh
     rows of x (rows / groups when None). y None: r is residual_scale * x and only
     computed into a given r; pre None: n is not computed. r and n may be x or y
     (in place). Returns (r, n), None for what is not computed."""
+    if stream is not None and (there := _elsewhere(rope3d_block_norm, dict(locals()))) is not None:
+        return there
     _torch or _use_torch()
     if r is None and y is not None:
         r = _fresh(x)
@@ -807,11 +821,13 @@ def rope3d_block_norm_backward(x, y=None, dr=None, dn=None, post: int = NORM_NON
                                post_weight=None, gate=None, pre_weight=None, scale=None, shift=None,
                                rows_per_group=None, eps: float = 1e-6, residual_scale: float = 1.0,
                                weight_offset: float = 0.0, dx=None, dy=None, param_grads: bool = True,
-                               workspace=None, stream=None):
+                               workspace=None, *, stream=None):
     """The gradients of rope3d_block_norm with the same arguments, from dr and dn
     (either may be None: zero). Returns a dict: dx, dy (with y) and, with
     param_grads, d_post_weight, d_gate, d_pre_weight, d_scale, d_shift for the
     parameters given, in their dtype."""
+    if stream is not None and (there := _elsewhere(rope3d_block_norm_backward, dict(locals()))) is not None:
+        return there
     _torch or _use_torch()
     fwd = _norm_fields(x, y, post, NORM_NONE if pre is None else pre, post_weight, gate, pre_weight, scale, shift,
                        rows_per_group, eps, residual_scale, weight_offset, None, None)
@@ -831,7 +847,7 @@ def rope3d_block_norm_backward(x, y=None, dr=None, dn=None, post: int = NORM_NON
           _stride("dx", dx, rows, channels, dt), _stride("dy", dy, rows, channels, dt))
     st = _raw_stream(stream, x)
     args, ws = _workspace(_NormBackArgs, ((*fwd, _ptr_of(dr), _ptr_of(dn), dx.data_ptr(), _ptr_of(dy), *grads, *ld, channels), ()),
-                          "rope3d_block_norm_backward_workspace", "rope3d_block_norm_backward", workspace, x, st)
+                          "rope3d_block_norm_backward_workspace", "rope3d_block_norm_backward", workspace, x)
     _check(load_library().rope3d_block_norm_backward(args, st), "rope3d_block_norm_backward")
     return out
 
@@ -875,7 +891,7 @@ def _pre_fields(gate_pre, up_pre, tokens, hidden, code):
 
 
 def rope3d_gated_ffn(x, w_gate, w_up, w_down, act: int = ACT_GELU_TANH, y=None, keep=False,
-                     gate_pre=None, up_pre=None, workspace=None, stream=None):
+                     gate_pre=None, up_pre=None, workspace=None, *, stream=None):
     """Gated feed-forward: (act(x w_gate^T) * (x w_up^T)) w_down^T for x [tokens,
     width] (or [..., width]), w_gate and w_up [hidden, width], w_down [width,
     hidden], bf16 or fp16 on the device. keep: also return the two projections
@@ -884,6 +900,8 @@ def rope3d_gated_ffn(x, w_gate, w_up, w_down, act: int = ACT_GELU_TANH, y=None, 
     multiple of 16; gate_pre / up_pre take them instead of new tensors. Returns
     y, or (y, gate_pre, up_pre). workspace: a uint8 device tensor of at least the
     bytes the call needs (allocated when None)."""
+    if stream is not None and (there := _elsewhere(rope3d_gated_ffn, dict(locals()))) is not None:
+        return there
     torch = _torch or _use_torch()
     tokens, width, ldx = _matrix("x", x)
     hidden, dt, code = w_gate.shape[0], x.dtype, _code(x)
@@ -902,17 +920,19 @@ def rope3d_gated_ffn(x, w_gate, w_up, w_down, act: int = ACT_GELU_TANH, y=None, 
             _stride("w_down", w_down, width, hidden, dt), _stride("y", y, tokens, width, dt), pre_ld)
     st = _raw_stream(stream, x)
     args, ws = _workspace(_FfnArgs, (body, (code, pre_code, act)), "rope3d_gated_ffn_workspace", "rope3d_gated_ffn",
-                          workspace, x, st)
+                          workspace, x)
     _check(load_library().rope3d_gated_ffn(args, st), "rope3d_gated_ffn")
     return y if gate_pre is None else (y, gate_pre, up_pre)
 
 
 def rope3d_gated_ffn_backward(dy, x, w_gate, w_up, w_down, gate_pre=None, up_pre=None,
                               act: int = ACT_GELU_TANH, dx=None, dw_gate=None, dw_up=None, dw_down=None,
-                              need=(True, True, True), workspace=None, stream=None):
+                              need=(True, True, True), workspace=None, *, stream=None):
     """The gradients of rope3d_gated_ffn: (dx, dw_gate, dw_up, dw_down). gate_pre
     and up_pre as the forward pass kept them; None computes them again. need: which
     of dx, (dw_gate, dw_up) and dw_down to compute; the others are None."""
+    if stream is not None and (there := _elsewhere(rope3d_gated_ffn_backward, dict(locals()))) is not None:
+        return there
     _torch or _use_torch()
     tokens, width, ldx = _matrix("x", x)
     hidden, dt, code = w_gate.shape[0], x.dtype, _code(x)
@@ -932,7 +952,7 @@ def rope3d_gated_ffn_backward(dy, x, w_gate, w_up, w_down, gate_pre=None, up_pre
             pre_ld, *ld_g)
     st = _raw_stream(stream, x)
     args, ws = _workspace(_FfnBackArgs, (body, (code, pre_code, act)), "rope3d_gated_ffn_backward_workspace",
-                          "rope3d_gated_ffn_backward", workspace, x, st)
+                          "rope3d_gated_ffn_backward", workspace, x)
     _check(load_library().rope3d_gated_ffn_backward(args, st), "rope3d_gated_ffn_backward")
     return grads
 

@@ -144,6 +144,47 @@ def test_other_streams():
         assert same(f[:2], want_f[:2]) and same(b.values(), want_b.values()), how
 
 
+def test_other_stream_takes_no_pending_memory():
+    """Memory freed on the current stream whose reader is still pending there is not
+    what a call on another stream writes to; what such a call returned is not given
+    away while the current stream still reads it."""
+    rows, channels, hidden = 512, 1024, 2048
+    g = gen(21)
+    x, y, w = normal(g, (rows, channels)), normal(g, (rows, channels)), ffn_weights(g, channels, hidden)
+    calls = {
+        "norm": lambda **k: r.rope3d_block_norm(x, y, post=r.NORM_RMS, **k),
+        "norm backward": lambda **k: tuple(r.rope3d_block_norm_backward(x, y, x, y, post=r.NORM_RMS, **k).values()),
+        "ffn": lambda **k: r.rope3d_gated_ffn(x, *w, keep=BF, **k),
+        "ffn backward": lambda **k: r.rope3d_gated_ffn_backward(y, x, *w, **k),
+    }
+    side = torch.cuda.Stream()
+    for name, call in calls.items():
+        want = call(stream=side)   # (memory of every size is there afterwards)
+        torch.cuda.synchronize()
+        sizes = [t.numel() for t in want] + [rows * hidden, rows * hidden * 2, 1 << 23]
+        held = [torch.full((n,), 3.0, dtype=BF, device=DEV) for n in sizes]
+        copies = [torch.empty_like(t) for t in held]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(200_000_000)
+        for c, t in zip(copies, held):
+            c.copy_(t)
+        del held, t
+        out = call(stream=side.cuda_stream)
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert all(bool((c == 3.0).all()) for c in copies), name
+        assert same(out, want), name
+        # read behind a delay on the current stream, freed before that, then other work on the side stream
+        torch.cuda._sleep(200_000_000)
+        copies = [t.clone() for t in out]
+        del out
+        with torch.cuda.stream(side):
+            for t in want:
+                torch.empty_like(t).fill_(-1.0)
+        torch.cuda.synchronize()
+        assert same(copies, want), name
+
+
 @pytest.mark.parametrize("tokens", [1, 50, 300])
 def test_captured_graphs(tokens):
     """Forward and backward captured and replayed with new inputs; a second graph of
