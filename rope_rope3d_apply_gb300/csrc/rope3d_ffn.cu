@@ -138,7 +138,7 @@ struct Out {
     long long ld;     // elements from row to row
     int f32;
     int vec;          // rows start on 16-byte boundaries
-    int tma;          // and are stored through the tensor map
+    int tma_cols;     // the columns before this one are stored through the tensor map
     int word;         // else: bytes (2, 4 or 8) that base and rows are multiples of
 };
 
@@ -383,8 +383,8 @@ __device__ __forceinline__ void copy_box(uint32_t box, char *d, long long pitch,
 
 // 16 words (64 bytes: 32 16-bit or 16 fp32 elements) of each lane's row, from
 // column `col` of output o; the warp's rows are row0 .. row0 + 31. Through a
-// staging box: a TMA store, or where TMA cannot address the rows, the widest
-// words that they are aligned to.
+// staging box: a TMA store, or where TMA cannot address the rows or the box's last
+// columns, the widest words that they are aligned to.
 __device__ __forceinline__ void store_words(Boxes &bx, const uint32_t *w, const Out &o,
                                             const CUtensorMap *map, int row0, int col, int m, int n) {
     if (!o.p || row0 >= m || col >= n) return;
@@ -398,7 +398,7 @@ __device__ __forceinline__ void store_words(Boxes &bx, const uint32_t *w, const 
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
                      ::"r"(row + ((uint32_t(c) ^ sw) << 4)), "r"(w[4 * c]), "r"(w[4 * c + 1]),
                        "r"(w[4 * c + 2]), "r"(w[4 * c + 3]) : "memory");
-    if (o.tma) {
+    if (col < o.tma_cols) {
         fence_async_smem();
         __syncwarp();
         if (bx.lane == 0) tma_store2(map, box, col, row0);
@@ -1166,9 +1166,10 @@ int set_outs(Params &p, Maps &maps, const Out *outs, int first, int count, int64
         Out &o = p.out[i];
         const int es = o.f32 ? 4 : 2;
         o.vec = o.p && tma_ok(o.p, o.ld, es);
-        o.tma = maps_too && o.vec;
+        // TMA stores whole 16-byte pieces: a last box that ends inside one goes without
+        o.tma_cols = !maps_too || !o.vec ? 0 : int(cols * es % 16 == 0 ? cols : cols * es / 64 * 64 / es);
         o.word = word_of(o.p, o.ld * es);
-        if (o.tma && !make_map(&maps.c[i], o.p, rows, cols, o.ld, es, p.f16, o.f32 ? 16 : 32, 32, false))
+        if (o.tma_cols && !make_map(&maps.c[i], o.p, rows, cols, o.ld, es, p.f16, o.f32 ? 16 : 32, 32, false))
             return ROPE3D_ERR_CUDA;
     }
     return ROPE3D_OK;

@@ -330,6 +330,42 @@ def test_ffn_strided_views_and_their_neighbours(tokens, width, hidden, off):
         assert bool((buf == 5.0).all()), name
 
 
+@pytest.mark.parametrize("pre", [BF, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("mod,off", [(2, 2), (4, 4), (4, 2), (6, 1), (1, 4), (0, 4), (0, 8)])
+@pytest.mark.parametrize("tokens,width,hidden", [(5, 67, 131), (140, 65, 130), (300, 131, 67), (600, 523, 1301)])
+def test_ffn_rows_of_every_alignment(tokens, width, hidden, mod, off, pre):
+    """Rows that start on 2, 4 and 8 bytes and end inside a word, and their neighbours."""
+    g = gen(tokens + mod + off)
+
+    def wide(rows, cols, fill=None, scale=1.0, dtype=BF):
+        ld = cols + off + 1
+        ld += (mod - ld) % 8
+        t = normal(g, (rows + 2, ld), BF, scale) if fill is None else torch.full((rows + 2, ld), fill, dtype=dtype, device=DEV)
+        return t, t[1:-1, off:off + cols]
+
+    x, dy = wide(tokens, width)[1], wide(tokens, width)[1]
+    wg, wu = (wide(hidden, width, scale=width ** -0.5)[1] for _ in range(2))
+    wd = wide(width, hidden, scale=hidden ** -0.5)[1]
+    bufs = {n: wide(rows, cols, 5.0, dtype=dt) for n, rows, cols, dt in (
+        ("y", tokens, width, BF), ("g", tokens, hidden, pre), ("u", tokens, hidden, pre), ("dx", tokens, width, BF),
+        ("dw_gate", hidden, width, BF), ("dw_up", hidden, width, BF), ("dw_down", width, hidden, BF))}
+    v = {k: b[1] for k, b in bufs.items()}
+    r.rope3d_gated_ffn(x, wg, wu, wd, act=r.ACT_SILU, y=v["y"], gate_pre=v["g"], up_pre=v["u"])
+    r.rope3d_gated_ffn_backward(dy, x, wg, wu, wd, v["g"], v["u"], act=r.ACT_SILU,
+                                **{k: v[k] for k in ("dx", "dw_gate", "dw_up", "dw_down")})
+    want = ref.ffn64(x, wg, wu, wd, 0)
+    ref.check(v["y"], want["y"], "y")
+    for k in "gu":
+        val, err = want[k]
+        ref.check(v[k], (val, err + (ref.half_step(BF) * val.abs() if pre is BF else 0.0)), k)
+    want = ref.ffn_backward64(dy, x, wg, wu, wd, 0, v["g"], v["u"])
+    for k in ("dx", "dw_gate", "dw_up", "dw_down"):
+        ref.check(v[k], want[k], k)
+    for name, (buf, view) in bufs.items():
+        view.fill_(5.0)
+        assert bool((buf == 5.0).all()), name
+
+
 @pytest.mark.parametrize("tokens", [5, 300])
 def test_special_values_stay_in_their_rows(tokens):
     """A NaN or an infinity in one token's row reaches that token's outputs alone."""
