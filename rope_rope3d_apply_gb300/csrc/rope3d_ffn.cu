@@ -917,6 +917,9 @@ ffn_stream_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Par
         }
     } else if (warp == 1 && lane == 0) {
         const uint32_t id = idesc(128, uint32_t(p.rows_n), !p.f16, kAMn, false);
+        // the tokens' copies start only then: a wait before it would spend its limit
+        // on an earlier kernel's time
+        grid_wait();
         int i = 0;
         for (; i < k_hi - k_lo; ++i) {
             const int s = i % p.stages;
