@@ -634,7 +634,10 @@ ffn_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Param
                 ahead(32);
                 ahead(64);
             }
-            if (!mbar_wait(acc_full(b), uint32_t(i / 2) & 1u, dead, &g_ffn_wait_timeouts)) break;
+            // one answer for the warp: where a wait ran out for some of its lanes alone,
+            // they would leave and the others wait for them in the next __syncwarp()
+            const bool ready = mbar_wait(acc_full(b), uint32_t(i / 2) & 1u, dead, &g_ffn_wait_timeouts);
+            if (!__all_sync(0xffffffffu, ready)) break;
             tc_fence_after();
             if (un.part >= 0) {
                 // fp32 sums of this part: [8 groups of 32 rows][kBN columns][32 rows]

@@ -2,6 +2,8 @@
 a run on an idle GPU does not show."""
 from __future__ import annotations
 
+import re
+
 import pytest
 
 from tests import kernel_source as src
@@ -22,3 +24,27 @@ def test_bounded_waits_begin_after_earlier_kernels(file, kernel):
     _, missing = src.before_each(body, "mbar_wait", "grid_wait")
     assert "mbar_wait" in src.flat(body)
     assert not missing, missing
+
+
+@pytest.mark.parametrize("file,kernel", [
+    (FFN, "ffn_tile_kernel"), (FFN, "ffn_stream_kernel"), (NORM, "block_norm_ring_kernel"),
+    (BACK, "block_norm_back_ring_kernel"),
+])
+def test_a_wait_that_runs_out_does_not_part_a_warp(file, kernel):
+    """Lanes of a warp try a barrier one by one: a wait can run out for some of them
+    while others see it complete. Where its result decides the way, either a single
+    lane waits or the warp takes one answer; else some lanes would leave and the
+    others wait for them, without a limit, in their next warp-wide operation."""
+    def walk(block, one_lane):
+        for part in block.parts:
+            if isinstance(part, str):
+                for m in re.finditer(r"if\s*\(\s*!\s*mbar_wait\(|=\s*mbar_wait\(", part):
+                    rest = part[m.start():]
+                    if one_lane or re.search(r"__all_sync\(0xffffffffu, ready\)\) break;", rest):
+                        continue
+                    # (a result that is only noted decides no way)
+                    assert re.match(r"if \(!mbar_wait\([^;]*\) && lost < 0\) lost = [^;]*;", rest), rest[:120]
+            else:
+                walk(part, one_lane or re.search(r"lane == 0\b", part.head) is not None)
+
+    walk(src.kernel(file, kernel), False)
