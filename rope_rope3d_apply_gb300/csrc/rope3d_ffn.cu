@@ -954,7 +954,10 @@ ffn_stream_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Par
     grid_wait();      // every thread: outputs of earlier kernels are read and overwritten below
     // all copies have landed and been read (each was waited for by its MMAs):
     // the ring's memory takes the partial sums, [accumulator][token][128 rows]
-    mbar_wait(done, 0, dead, &g_ffn_wait_timeouts);
+    // (one warp waits and the block meets behind it: eight warps that wait each for
+    // themselves and then bring their lanes together cost 0.4 us a product)
+    if (warp == 0) mbar_wait(done, 0, dead, &g_ffn_wait_timeouts);
+    __syncthreads();
     tc_fence_after();
     const int row = (warp & 3) * 32 + lane;
     for (int c = (warp >> 2) * 16; c < kAcc * p.rows_n; c += 32) {

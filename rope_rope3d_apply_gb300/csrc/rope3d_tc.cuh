@@ -1,6 +1,12 @@
 // rope3d_tc.cuh -- device helpers of the feed-forward's matrix products:
 // mbarriers with bounded waits, TMA tile copies, tcgen05 MMAs of one CTA or of
-// a CTA pair, tensor-memory reads, cluster addresses. Used by rope3d_ffn.cu.
+// a CTA pair, tensor-memory reads, cluster addresses. Used by rope3d_ffn.cu; its
+// bounded waits and launch order by rope3d_norm.cuh too.
+//
+// Instructions marked .aligned want all lanes of a warp at the same instruction.
+// What may stand before them (branches of one lane, waits that lanes leave one by
+// one, rows that end within a warp) does not promise that, so each of them is behind
+// a __syncwarp() of its own here.
 #pragma once
 
 #include <cuda.h>
@@ -32,6 +38,7 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
 // Every thread of every CTA of the cluster: writes before it are visible to
 // all of them after it.
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -206,6 +213,7 @@ __device__ __forceinline__ void tc_fence_after() {
 // address goes to *slot. kPair: the same in both CTAs of the pair.
 template <bool kPair>
 __device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t columns) {
+    __syncwarp();
     if constexpr (kPair) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
                      ::"r"(slot), "r"(columns) : "memory");
@@ -218,6 +226,7 @@ __device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t columns) {
 }
 template <bool kPair>
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns) {
+    __syncwarp();
     if constexpr (kPair)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
     else
@@ -227,6 +236,7 @@ __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns) {
 // 16 consecutive fp32 columns of the 32 tensor-memory lanes that this warp
 // reaches (32 * (warp % 4)), one lane a thread; complete after tmem_wait.
 __device__ __forceinline__ void tmem_ld16(float *v, uint32_t addr) {
+    __syncwarp();
     uint32_t *r = reinterpret_cast<uint32_t *>(v);
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
@@ -236,7 +246,10 @@ __device__ __forceinline__ void tmem_ld16(float *v, uint32_t addr) {
         : "r"(addr));
 }
 // The loads so far are complete; v (loaded by one of them) may be used after it.
-__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait() {
+    __syncwarp();
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void tmem_tie16(float *v) {
     asm volatile(""
                  : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),

@@ -2,6 +2,7 @@
 a run on an idle GPU does not show."""
 from __future__ import annotations
 
+import os
 import re
 
 import pytest
@@ -48,3 +49,20 @@ def test_a_wait_that_runs_out_does_not_part_a_warp(file, kernel):
                 walk(part, one_lane or re.search(r"lane == 0\b", part.head) is not None)
 
     walk(src.kernel(file, kernel), False)
+
+
+def test_warp_aligned_instructions_are_behind_a_syncwarp():
+    """PTX wants every lane of a warp at an .aligned instruction, and promises no
+    reconvergence behind branches and loops that lanes leave one by one. The helpers
+    that hold such instructions bring the lanes together themselves, and the kernels
+    have none outside of them."""
+    with open(os.path.join(src.CSRC, "rope3d_tc.cuh")) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    functions = re.split(r"(?=__device__ __forceinline__)", text)
+    aligned = [f for f in functions if ".aligned" in f]
+    assert len(aligned) == 5
+    for f in aligned:
+        assert re.search(r"\)\s*\{\s*(\w+ \*?\w+ = [^;]*;\s*)?__syncwarp\(\);", f), f[:120]
+    for name in (FFN, NORM, BACK, "rope3d_norm.cuh"):
+        with open(os.path.join(src.CSRC, name)) as f:
+            assert ".aligned" not in re.sub(r"//[^\n]*", "", f.read()), name
