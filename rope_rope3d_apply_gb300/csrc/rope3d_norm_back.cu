@@ -636,8 +636,10 @@ __global__ void __launch_bounds__(32 * n) block_norm_finish_kernel(const __grid_
     const int c = int(blockIdx.x) * 32 + lane;
     const int param_type = p.param_f32 ? ROPE3D_F32 : p.dtype;
     const int per = p.groups_per_chunk ? p.chunks : p.chunks_per_group;
-    // which of the three sums exist: S with a pre weight or scale, and so on
-    const bool want[3] = {p.d_pre_weight || p.d_scale, p.d_shift != nullptr, p.d_post_weight || p.d_gate};
+    // which of the three sums are needed: chunks of whole groups have written their
+    // groups' gradients and left the weights' sums alone
+    const bool split = !p.groups_per_chunk;
+    const bool want[3] = {p.d_pre_weight || (split && p.d_scale), split && p.d_shift, p.d_post_weight || (split && p.d_gate)};
     float s[3] = {0.0f, 0.0f, 0.0f};
     if (c < p.channels) {
         if (ty < 4 && !p.groups_per_chunk) {   // a group's parameters, one a warp

@@ -66,3 +66,20 @@ def test_warp_aligned_instructions_are_behind_a_syncwarp():
     for name in (FFN, NORM, BACK, "rope3d_norm.cuh"):
         with open(os.path.join(src.CSRC, name)) as f:
             assert ".aligned" not in re.sub(r"//[^\n]*", "", f.read()), name
+
+
+def test_finish_reads_only_sums_that_were_written():
+    """Chunks of whole groups finish their groups' gradients themselves and leave only
+    the weights' sums (1 and 3 of the three rows) for block_norm_finish_kernel. The
+    kernel's own expression says which rows it reads."""
+    want = re.search(r"const bool want\[3\] = \{([^;]*)\};", src.flat(src.kernel(BACK, "block_norm_finish_kernel"))).group(1)
+    names = ("d_pre_weight", "d_scale", "d_shift", "d_post_weight", "d_gate")
+    for bits in range(64):
+        given = {n: bool(bits >> i & 1) for i, n in enumerate(names)}
+        whole = bool(bits >> 5)
+        text = re.sub(r"p\.(\w+)\s*!=\s*nullptr", r"p.\1", want)
+        text = re.sub(r"p\.(\w+)", lambda m: str(whole if m.group(1) == "groups_per_chunk" else given[m.group(1)]), text)
+        text = text.replace("&&", " and ").replace("||", " or ").replace("!", " not ").replace("split", str(not whole))
+        read = eval("(" + text + ")")   # noqa: S307 (the kernel's own expression)
+        assert read == ((given["d_pre_weight"] or not whole and given["d_scale"]), not whole and given["d_shift"],
+                        (given["d_post_weight"] or not whole and given["d_gate"])), (given, whole)
