@@ -714,13 +714,19 @@ def _elsewhere(call, args):
     current one, else None. It then runs with that stream current, so that the memory
     it allocates is that stream's. (The current stream's may be memory that its pending
     work still reads.) What it returns is kept from other use until the current stream
-    has passed it too."""
+    has passed it too, and what it is given until its own stream has: a temporary may be
+    freed on return. (Not on streams that torch did not make, which may be gone by the
+    time the memory is freed: there the caller keeps the tensors.)"""
     torch = _torch or _use_torch()
     x, stream = args["x"], args.pop("stream")
     if not x.is_cuda or _raw_stream(stream, x) == torch._C._cuda_getCurrentRawStream(x.device.index):
         return None
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(_raw_stream(stream, x), device=x.device)
+    if not isinstance(stream, torch.cuda.ExternalStream):
+        for t in args.values():
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                t.record_stream(stream)
     with torch.cuda.stream(stream):
         out = call(**args)
     here = torch.cuda.current_stream(x.device)
@@ -799,7 +805,11 @@ def rope3d_block_norm(x, y=None, post: int = NORM_NONE, pre=NORM_RMS, post_weigh
     gate, scale and shift are [groups, channels], one row for each rows_per_group
     rows of x (rows / groups when None). y None: r is residual_scale * x and only
     computed into a given r; pre None: n is not computed. r and n may be x or y
-    (in place). Returns (r, n), None for what is not computed."""
+    (in place). Returns (r, n), None for what is not computed.
+    stream (this and the three calls below): a torch stream or a cudaStream_t, the
+    current one when None. Work that makes the inputs elsewhere is the caller's to wait
+    for; they may be freed after the call on a torch stream, and have to be kept until
+    it is done on another's."""
     if stream is not None and (there := _elsewhere(rope3d_block_norm, dict(locals()))) is not None:
         return there
     _torch or _use_torch()
