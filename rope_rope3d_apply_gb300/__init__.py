@@ -637,8 +637,10 @@ def _use_torch():
         import torch
 
         # a small call allocates its outputs in a fifth of torch.empty's time this
-        # way (two outputs and a launch: 5.4 us instead of 10.7)
-        _fast_empty = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+        # way (two outputs and a launch: 5.4 us instead of 10.7). Not where torch cannot
+        # say whether a dispatch mode is on, which has to see allocations
+        if hasattr(torch._C, "_len_torch_dispatch_stack"):
+            _fast_empty = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
         _torch = torch
     return _torch
 
@@ -696,11 +698,16 @@ def _ptr_of(t) -> int:
 
 def _new(shape, dtype, like):
     """A new contiguous tensor on the device of `like`."""
-    if _fast_empty is not None and like.is_cuda and like.device.index == _torch._C._cuda_getDevice():
-        if len(shape) == 2:
-            return _fast_empty((shape[0], shape[1]), (shape[1], 1), dtype)
-        if len(shape) == 1:
-            return _fast_empty((shape[0],), (1,), dtype)
+    global _fast_empty
+    if _fast_empty is not None and like.is_cuda and like.device.index == _torch._C._cuda_getDevice() and \
+            not _torch._C._len_torch_dispatch_stack():
+        try:
+            if len(shape) == 2:
+                return _fast_empty((shape[0], shape[1]), (shape[1], 1), dtype)
+            if len(shape) == 1:
+                return _fast_empty((shape[0],), (1,), dtype)
+        except TypeError:   # a torch whose function takes other arguments
+            _fast_empty = None
     return _torch.empty(tuple(shape), dtype=dtype, device=like.device)
 
 

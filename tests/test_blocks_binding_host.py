@@ -75,3 +75,58 @@ def test_inputs_of_a_call_on_another_stream_are_marked_as_used_there(stand_in):
     assert stand_in == [2, 3, 3] and out.used_on == [HERE, HERE]
     # the current stream needs none of it
     assert r._elsewhere(call, dict(x=x, stream=Stream(HERE))) is None
+
+
+@pytest.fixture
+def allocation(monkeypatch):
+    """Stand-ins for torch's allocation: its private function and torch.empty, and
+    how many dispatch modes are on."""
+    state = types.SimpleNamespace(modes=0, fast=[], plain=[])
+
+    def fast(shape, strides, dtype):
+        state.fast.append((shape, strides, dtype))
+        return "fast"
+
+    def empty(shape, dtype, device):
+        state.plain.append((shape, dtype))
+        return "plain"
+
+    torch = types.SimpleNamespace(empty=empty, _C=types.SimpleNamespace(
+        _cuda_getDevice=lambda: 0, _len_torch_dispatch_stack=lambda: state.modes))
+    monkeypatch.setattr(r, "_torch", torch)
+    monkeypatch.setattr(r, "_fast_empty", fast)
+    return state
+
+
+def test_allocation_under_a_dispatch_mode_is_seen_by_it(allocation):
+    assert r._new((3, 4), "t", Tensor()) == "fast" and allocation.fast == [((3, 4), (4, 1), "t")]
+    allocation.modes = 1
+    assert r._new((3, 4), "t", Tensor()) == "plain" and allocation.plain == [((3, 4), "t")]
+
+
+@pytest.mark.parametrize("error", [TypeError, RuntimeError])
+def test_allocation_falls_back_where_the_private_function_takes_other_arguments(allocation, monkeypatch, error):
+    tried = []
+
+    def fast(*args):
+        tried.append(args)
+        raise error("other arguments")
+
+    monkeypatch.setattr(r, "_fast_empty", fast)
+    if error is RuntimeError:   # (memory that runs out is not hidden)
+        with pytest.raises(RuntimeError):
+            r._new((5,), "t", Tensor())
+        assert r._fast_empty is fast
+        return
+    assert r._new((5,), "t", Tensor()) == "plain" and r._new((5, 2), "t", Tensor()) == "plain"
+    assert len(tried) == 1 and allocation.plain == [((5,), "t"), ((5, 2), "t")]
+
+
+def test_allocation_without_a_way_to_see_dispatch_modes(monkeypatch):
+    """A torch that cannot be asked for dispatch modes is not passed by."""
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(r, "_torch", None)
+    monkeypatch.setattr(r, "_fast_empty", None)
+    monkeypatch.delattr(torch._C, "_len_torch_dispatch_stack")
+    r._use_torch()
+    assert r._torch is torch and r._fast_empty is None
