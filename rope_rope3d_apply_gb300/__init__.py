@@ -755,6 +755,8 @@ def _workspace(cls, fields, query, what, given, like):
             return cls.pack(*body, 0, 0, *tail), None
         given = _new((need.value,), _torch.uint8, like)
         return cls.pack(*body, given.data_ptr(), need.value, *tail), given
+    if not given.is_contiguous():   # (its elements' bytes have to be there, one after the other)
+        raise ValueError("workspace must be contiguous")
     return cls.pack(*body, given.data_ptr(), given.numel() * given.element_size(), *tail), given
 
 
@@ -915,8 +917,8 @@ def rope3d_gated_ffn(x, w_gate, w_up, w_down, act: int = ACT_GELU_TANH, y=None, 
     [tokens, hidden] for the backward pass, in float32 (True) or in a given dtype
     (float32 or x's), as [tokens, hidden] views of padded rows where hidden is no
     multiple of 16; gate_pre / up_pre take them instead of new tensors. Returns
-    y, or (y, gate_pre, up_pre). workspace: a uint8 device tensor of at least the
-    bytes the call needs (allocated when None)."""
+    y, or (y, gate_pre, up_pre). workspace: a contiguous device tensor of at least
+    the bytes the call needs (allocated when None)."""
     if stream is not None and (there := _elsewhere(rope3d_gated_ffn, dict(locals()))) is not None:
         return there
     torch = _torch or _use_torch()

@@ -130,3 +130,18 @@ def test_allocation_without_a_way_to_see_dispatch_modes(monkeypatch):
     monkeypatch.delattr(torch._C, "_len_torch_dispatch_stack")
     r._use_torch()
     assert r._torch is torch and r._fast_empty is None
+
+
+def test_workspaces_that_are_less_than_they_seem_are_refused():
+    """A workspace's size is its number of elements: an expanded tensor has fewer
+    behind it, and a strided one has neighbours between them."""
+    torch = pytest.importorskip("torch")
+    x, w, d = (torch.zeros(s, dtype=torch.bfloat16) for s in ((4, 8), (6, 8), (8, 6)))
+    p = torch.zeros(8, dtype=torch.bfloat16)
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 20), torch.zeros(1 << 20, dtype=torch.uint8)[::2],
+               torch.zeros((64, 64), dtype=torch.float32).T):
+        for call in (lambda: r.rope3d_gated_ffn(x, w, w, d, workspace=ws),
+                     lambda: r.rope3d_gated_ffn_backward(x, x, w, w, d, workspace=ws),
+                     lambda: r.rope3d_block_norm_backward(x, dn=x, pre_weight=p, workspace=ws)):
+            with pytest.raises(ValueError, match="workspace"):
+                call()
