@@ -442,12 +442,13 @@ int rope3d_testing_na3d_wait_timeouts(int64_t *count, int32_t reset);
  *                ceil(rows / rows_per_group), row strides gate_stride, ...
  *   param_dtype  dtype or ROPE3D_F32
  *   weight_offset  added to both weights (Gemma3's norms store w - 1: 1.0)
- *   eps          finite, >= 0
+ *   eps          >= 0 and finite in fp32, and not a positive value that fp32
+ *                rounds to zero; residual_scale, weight_offset finite in fp32
  * In place: r and n may each be exactly x or exactly y (same address and row
  * stride); they never overlap otherwise. One kernel on `stream`, asynchronous.
  * Errors: NULL (args, x, or both r and n), SHAPE (a size <= 0, channels or a
  * stride out of range), DTYPE, ALIGN (a pointer not aligned to its element),
- * ARG (kinds, eps, residual_scale or weight_offset not finite, a post weight or
+ * ARG (kinds; eps, residual_scale or weight_offset as above; a post weight or
  * gate without y), ALIAS, DEVICE, CUDA.
  */
 typedef struct rope3d_block_norm_args {

@@ -287,7 +287,9 @@ int check_inputs(const rope3d_block_norm_args &a, NormParams &p, Span *in) {
     if (a.param_dtype != a.dtype && a.param_dtype != ROPE3D_F32) return ROPE3D_ERR_DTYPE;
     for (int kind : {a.post_kind, a.pre_kind})
         if (kind != ROPE3D_NORM_NONE && kind != ROPE3D_NORM_RMS && kind != ROPE3D_NORM_LAYER) return ROPE3D_ERR_ARG;
-    if (!std::isfinite(a.eps) || a.eps < 0.0 || !std::isfinite(a.residual_scale) || !std::isfinite(a.weight_offset))
+    // as the kernels have them, in fp32: not infinite there, nor an eps turned to zero
+    if (!std::isfinite(float(a.eps)) || a.eps < 0.0 || (a.eps > 0.0 && float(a.eps) == 0.0f) ||
+        !std::isfinite(float(a.residual_scale)) || !std::isfinite(float(a.weight_offset)))
         return ROPE3D_ERR_ARG;
     if (!a.y && (a.post_weight || a.gate)) return ROPE3D_ERR_ARG;
     if (a.post_weight && a.post_kind == ROPE3D_NORM_NONE) return ROPE3D_ERR_ARG;
