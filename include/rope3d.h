@@ -563,8 +563,9 @@ int rope3d_gated_ffn_workspace(const rope3d_gated_ffn_args *args, int64_t *bytes
  *   dx           [tokens, width]; dw_gate and dw_up [hidden, width] (both or
  *                neither); dw_down [width, hidden]; each may be NULL (not
  *                wanted), not all. Written, not added to.
- * dg, du and act(g) * u are computed in fp32 and rounded once to `dtype`, as
- * operands of the products; those accumulate in fp32 in a fixed order.
+ * dg, du and act(g) * u are computed in fp32 and rounded once to `dtype` (in fp16
+ * each of them overflows beyond 65504), as operands of the products; those
+ * accumulate in fp32 in a fixed order.
  * Workspace and errors as rope3d_gated_ffn.
  */
 typedef struct rope3d_gated_ffn_backward_args {
@@ -803,8 +804,9 @@ int rope3d_testing_max_units_per_launch(int64_t n);
  * and key positions, shared-memory slots) before the access it guards; a
  * failed check adds one to an error count and skips the access, so the kernel
  * finishes. This takes the place of a memory checker where none can run. The
- * norms and the feed-forward are the same in both builds: their accesses are
- * bounded by the extents of their arguments in every build.
+ * block norms' and the feed-forward's kernels have no such checks: they are the
+ * same in both builds, and what holds their accesses is their tests (results of
+ * every size class against 64 bits, the memory beside every output).
  *   errors  out: failed checks since the last reset (0 in a normal build)
  *   reset   nonzero: clear the count after reading it
  * Returns 1 when the library was built with the checks, 0 when not.

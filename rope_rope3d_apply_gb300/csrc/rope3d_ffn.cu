@@ -1268,10 +1268,14 @@ Plan plan_tiles(int64_t m, int64_t n, int nk, bool gated) {
     return best;
 }
 
-// The gradients' launch: dx of `dx_tokens` tokens (0: no dx) and the weights'
-// gradients that are wanted. Every pair works until all is done, so what counts
-// is the whole work, or the longest unit of dx where that is longer; dx is split
-// where that pays.
+// The gradients' launch: dx (where wanted) and the weights' gradients that are
+// wanted. The model takes the whole work in equal shares, or the longest unit of dx
+// where that is longer; dx is split where that pays. That is the time where units are
+// many (2048 x 2048 x 8192: 207.7 us by the model, 208.1 by next_unit's order of the
+// units at the same costs). It is too low where they are few or make one round and a
+// little: the weights' tiles are not split, and their longest one, all tokens deep, is
+// not in it (8192 x 256 x 1024, 12 such tiles: 12.9 us by the model, 46.9 by the
+// units' order, 37.3 with the narrow tile that it then does not choose).
 Plan plan_grads(int64_t tokens, int64_t width, int64_t hidden, bool dx, bool gate_up, bool down) {
     Plan best{};
     double best_time = 1e30;

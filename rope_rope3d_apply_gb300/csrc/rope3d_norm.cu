@@ -47,7 +47,8 @@ using namespace rope3d_norm;
 // ---- rows in registers -----------------------------------------------------------------
 
 // Bound by the latency of a row's loads and sums while the rows are few: one row of
-// 4096 bf16 3.5 us, 1021 x 1157 fp32 7.5 us; by memory past that (fp32 9528 x 1790
+// 4096 bf16 3.5 us, 1021 x 1157 fp32 7.5 us (124 registers a thread: four blocks an
+// SM, 608 rows at once, so two rounds); by memory past that (fp32 9528 x 1790
 // 53 us, 5,100 GB/s), except where 16-bit elements go one by one (bf16 9728 x 4001
 // 134 us, 2,300 GB/s: too few bytes in flight a thread).
 template <int kT, bool kVec, int kE, int kTeam>

@@ -43,7 +43,7 @@ struct NormParams {
     // backward: chunks of rows and their partial column sums
     float *part;          // [chunks][3][channels]: sums of a part of a group, or the weights' sums of whole groups
     float *group_sums;    // [groups][2][channels]: the groups' parts of the weights' gradients
-    float *stats;         // general kernels: [rows][6]
+    float *stats;         // general kernels: [rows][6], then [rows][2] (mean f, mean f yh)
     int chunk_rows, chunks_per_group, groups_per_chunk, chunks;
     int sums;             // column sums are wanted
     int stages;           // ring kernels: rows in shared memory

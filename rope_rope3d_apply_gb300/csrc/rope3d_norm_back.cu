@@ -244,8 +244,10 @@ block_norm_back_team_kernel(const __grid_constant__ NormParams p) {
 
 // kShift: d_shift is wanted (its sums are one more array of registers). Bound by
 // memory at one group: 16384 x 4096 bf16 135 us, 5,960 GB/s, 142 us with the finish;
-// 8192 x 2048 fp16 with a layer norm and four groups' modulation 50 us, 4,000 GB/s:
-// four sums a row in turn, and the finish a tenth of it.
+// 8192 x 2048 fp16 with a layer norm and four groups' modulation 50 us, 4,000 GB/s of
+// the bytes that have to move: its 588 chunks of 14 rows leave 14.4 MB of partial sums,
+// written and read again, and a row's two sums (of two values each) and barrier come
+// in turn.
 template <int kT, bool kLayer, bool kFull, bool kShift>
 __global__ void __launch_bounds__(512) block_norm_back_ring_kernel(const __grid_constant__ NormParams p) {
     using Team = RingTeam<kT, kFull>;
