@@ -44,3 +44,34 @@ def test_temporaries_may_be_dropped_after_the_call(tokens):
         torch.cuda.synchronize()
         del overwritten
         assert all(torch.equal(p, q) for p, q in zip(out, want)), name
+
+
+def test_captured_with_a_forked_stream():
+    """Calls on a side stream, by the argument, inside a graph captured on another:
+    temporaries dropped during the capture, replays with new inputs."""
+    g = torch.Generator(device=DEV).manual_seed(5)
+    normal = lambda *shape: (torch.randn(shape, generator=g, device=DEV) / shape[-1] ** 0.5).to(BF)  # noqa: E731
+    x, dy, w = normal(200, 256), normal(200, 256), (normal(512, 256), normal(512, 256), normal(256, 512))
+
+    def step(stream=None):
+        _, n = r.rope3d_block_norm(x * 2.0, stream=stream)
+        y, gp, up = r.rope3d_gated_ffn(n, *w, keep=True, stream=stream)
+        return (y, *r.rope3d_gated_ffn_backward(dy, n, *w, gp, up, stream=stream))
+
+    step()
+    torch.cuda.synchronize()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    doubled = torch.empty_like(x)
+    with torch.cuda.graph(graph):
+        torch.mul(x, 2.0, out=doubled)
+        side.wait_stream(torch.cuda.current_stream())
+        _, n = r.rope3d_block_norm(doubled, stream=side)
+        y, gp, up = r.rope3d_gated_ffn(n, *w, keep=True, stream=side)
+        out = (y, *r.rope3d_gated_ffn_backward(dy, n, *w, gp, up, stream=side))
+        del n, y, gp, up
+        torch.cuda.current_stream().wait_stream(side)
+    for seed in (1, 2):
+        x.copy_(torch.randn(x.shape, generator=torch.Generator(device=DEV).manual_seed(seed), device=DEV))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, step()))
