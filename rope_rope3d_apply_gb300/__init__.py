@@ -706,8 +706,10 @@ def _new(shape, dtype, like):
                 return _fast_empty((shape[0], shape[1]), (shape[1], 1), dtype)
             if len(shape) == 1:
                 return _fast_empty((shape[0],), (1,), dtype)
-        except TypeError:   # a torch whose function takes other arguments
-            _fast_empty = None
+        except TypeError:
+            out = _torch.empty(tuple(shape), dtype=dtype, device=like.device)   # (raises for the caller's mistake)
+            _fast_empty = None   # a torch whose function takes other arguments
+            return out
     return _torch.empty(tuple(shape), dtype=dtype, device=like.device)
 
 

@@ -122,6 +122,17 @@ def test_allocation_falls_back_where_the_private_function_takes_other_arguments(
     assert len(tried) == 1 and allocation.plain == [((5,), "t"), ((5, 2), "t")]
 
 
+def test_a_callers_mistake_does_not_turn_the_private_function_off(allocation, monkeypatch):
+    def refuse(*args, **kwargs):
+        raise TypeError("not a dtype")
+
+    monkeypatch.setattr(r, "_fast_empty", refuse)
+    monkeypatch.setattr(r._torch, "empty", refuse)
+    with pytest.raises(TypeError, match="not a dtype"):
+        r._new((5,), "no dtype", Tensor())
+    assert r._fast_empty is refuse
+
+
 def test_allocation_without_a_way_to_see_dispatch_modes(monkeypatch):
     """A torch that cannot be asked for dispatch modes is not passed by."""
     torch = pytest.importorskip("torch")
