@@ -592,6 +592,264 @@ int rope3d_gated_ffn_last_kernel(void);
  * clears the count. Synchronises with the device. Errors: NULL, CUDA. */
 int rope3d_testing_ffn_wait_timeouts(int64_t *count, int32_t reset);
 
+/* ---- a paged cache of keys and values --------------------------------------
+ *
+ * What a text model, or one of text, pictures and video, needs around its
+ * attention when it is served: rotary positions given token by token (with
+ * their gradient, for training), the append that rotates new tokens into a paged
+ * cache, attention of new tokens over the pages, and the copies that fork
+ * sequences and compact the cache. They are extensions: the pages give no code
+ * for these, so the formulas below are the definition.
+ *
+ * Layout. A cache holds `pages` pages of page_size places; a place holds a row
+ * of head_dim elements for each key/value head. k_cache and v_cache are views
+ * [pages, page_size, kv_heads, head_dim] with any strides (elements; contiguous
+ * channels), so heads may lie before places, and K and V may share a buffer.
+ * Row s of page_table names the pages of sequence s in order: its place i is in
+ * page page_table[s][i / page_size] at place i % page_size. Lengths, starts and
+ * tables are device memory and are read when the kernels run: a captured graph
+ * sees what they hold at each replay. Whatever they hold, no kernel reads or
+ * writes outside the memory that the arguments describe: starts and lengths are
+ * clamped to the call's tokens and the table's row, and a page number outside
+ * [0, pages) counts as absent (each operator says what it does then).
+ */
+
+/* which pairs of channels turn together */
+#define ROPE3D_PAIRS_INTERLEAVED 0   /* (2j, 2j + 1)                           */
+#define ROPE3D_PAIRS_HALVES      1   /* (j, j + pairs)                         */
+
+/* element types of positions */
+#define ROPE3D_POSITIONS_I64 0   /* exact up to 2^53 either side of 0          */
+#define ROPE3D_POSITIONS_I32 1
+#define ROPE3D_POSITIONS_F32 2   /* with fractions                             */
+
+/*
+ * rope3d_apply_axes -- rotary positions with up to three axes (time, height,
+ * width), given token by token: pair j of every head of token t turns by
+ *     angle = positions[axis(j)][t] * freqs[j],
+ *     y_a = a cos(angle) - b sin(angle),  y_b = a sin(angle) + b cos(angle)
+ * sections[x] pairs belong to axis x, in order; pairs = their sum, and channels
+ * from 2 * pairs on are copied. Where rope3d_apply_pair rotates whole grids that
+ * start at 0 from tables, this takes packed clips and pictures of any sizes,
+ * tiles at an offset, text among them, and K with fewer heads than Q. inverse = 1
+ * turns by -angle: the gradient of the operator from the gradient of its output.
+ *
+ *   q, q_out      device, [tokens, q_heads, head_dim] of `dtype` (BF16, F16 or
+ *                 F32), strides of tokens and heads in elements (any order of
+ *                 the two); outputs' rows must not overlap one another
+ *   k, k_out      the same with k_heads; both or neither
+ *   positions     device, up to three rows of tokens entries of position_type,
+ *                 row stride positions_stride; rows up to the last axis that has
+ *                 pairs are read
+ *   freqs         device, fp32 [pairs]: rope3d_dit_freqs_host, or
+ *                 base^(-2j/d) for each axis or for all
+ * The angle is reduced exactly before its cosine and sine are taken (their
+ * error is a few units of 2^-24 at any position); products and sums are rounded
+ * by themselves in fp32, and the result once to `dtype`.
+ * q_out may be exactly q, k_out exactly k (same strides); otherwise an output
+ * overlaps no argument. Views of one buffer that interleave (the thirds of a
+ * projection) do not overlap. One kernel on `stream`, asynchronous; a vector
+ * kernel where every row is whole 16-byte vectors and pairs do not split them,
+ * else single pairs.
+ * Errors: NULL, SHAPE (sizes, sections, strides), DTYPE, ARG (pairing), ALIGN (a
+ * pointer not aligned to its element), ALIAS, DEVICE, CUDA.
+ */
+typedef struct rope3d_apply_axes_args {
+    const void *q, *k;
+    void *q_out, *k_out;
+    const void *positions, *freqs;
+    int64_t tokens, q_heads, k_heads, head_dim;
+    int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride;
+    int64_t q_out_token_stride, q_out_head_stride, k_out_token_stride, k_out_head_stride;
+    int64_t positions_stride;
+    int32_t sections[3];
+    int32_t dtype, position_type, pairing, inverse;
+} rope3d_apply_axes_args;
+
+int rope3d_apply_axes(const rope3d_apply_axes_args *args, void *stream);
+/* The checks without a launch; check_device = 0 skips the device-memory query. */
+int rope3d_apply_axes_check(const rope3d_apply_axes_args *args, int32_t check_device);
+/* Kernel of this thread's last rope3d_apply_axes or rope3d_cache_append: 1
+ * 16-byte vectors, 2 single pairs, 0 none yet. */
+int rope3d_apply_axes_last_kernel(void);
+
+/* The sequences of a call: tokens [q_starts[s], q_starts[s + 1]) are the new
+ * tokens of sequence s, the last ones of its seq_lens[s] places. */
+typedef struct rope3d_paged_batch {
+    const int32_t *page_table;   /* [seqs][table_width], row stride table_stride  */
+    const int32_t *seq_lens;     /* [seqs], the new tokens included               */
+    const int32_t *q_starts;     /* [seqs + 1], not falling; NULL: tokens / seqs
+                                    tokens each (seqs must divide tokens)         */
+    int64_t seqs, table_width, table_stride, pages, page_size;
+} rope3d_paged_batch;
+
+/*
+ * rope3d_cache_append -- new tokens enter the cache: k rotated as by
+ * rope3d_apply_axes and written to its place, v copied to its place, and q, if
+ * given, rotated into q_out, in one launch.
+ *
+ *   q, q_out, k, v   [tokens, q_heads or kv_heads, head_dim] of `dtype`
+ *   k_cache, v_cache of `dtype`, strides of pages, places and heads
+ *   freqs NULL       no rotation: k is copied (q and positions must be NULL)
+ *   positions NULL   a token's place in its sequence is its position on every axis
+ *   invalid_count    optional int32: tokens whose place has no page (an absent one,
+ *                    or a sequence shorter than its new tokens) leave the cache
+ *                    alone and add one here; their q is rotated all the same
+ * Tokens behind the last sequence: nothing of theirs is read or written. A page
+ * that is written belongs to one sequence of the call (two that write one place
+ * race for it).
+ * Errors: as rope3d_apply_axes (ARG also: q or positions without freqs), SHAPE
+ * also for the batch (seqs must divide tokens where q_starts is NULL; table_width *
+ * page_size above 2^30).
+ */
+typedef struct rope3d_cache_append_args {
+    const void *q;
+    void *q_out;
+    const void *k, *v;
+    void *k_cache, *v_cache;
+    const void *positions, *freqs;
+    int32_t *invalid_count;
+    rope3d_paged_batch batch;
+    int64_t tokens, q_heads, kv_heads, head_dim;
+    int64_t q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride;
+    int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+    int64_t k_page_stride, k_slot_stride, k_cache_head_stride;
+    int64_t v_page_stride, v_slot_stride, v_cache_head_stride;
+    int64_t positions_stride;
+    int32_t sections[3];
+    int32_t dtype, position_type, pairing;
+} rope3d_cache_append_args;
+
+int rope3d_cache_append(const rope3d_cache_append_args *args, void *stream);
+int rope3d_cache_append_check(const rope3d_cache_append_args *args, int32_t check_device);
+
+/*
+ * rope3d_paged_attention -- attention of new tokens over the pages of their
+ * sequences: for query head h of token i of sequence s, at place
+ * P = seq_lens[s] - new tokens + i, over the keys j of key/value head
+ * h / (q_heads / kv_heads) with 0 <= j < seq_lens[s], j <= P where causal, and
+ * j > P - window where window > 0:
+ *     out = sum_j softmax_j(scale * q . k_j) v_j
+ *     lse = log sum_j exp(scale * q . k_j)            (optional)
+ * One token a sequence, whole prompts, chunks over a long cache and mixtures of
+ * them are one call. A row that sees no key gives zeros and lse = -inf. Keys on
+ * absent pages are left out.
+ *
+ *   q, out        [tokens, q_heads, head_dim] of `dtype` (BF16 or F16); strides
+ *                 and addresses multiples of 16 bytes
+ *   k_cache, v_cache   of `dtype`, likewise. What lies behind a sequence's length, on
+ *                 its last page too, may hold anything. (A value of V that is not
+ *                 finite, at a place that one row of a call sees, may reach rows of the
+ *                 same sequence and key/value head whose mask leaves it out.)
+ *   head_dim      a multiple of 8, up to 256; q_heads a multiple of kv_heads
+ *   lse           fp32 [tokens, q_heads], token stride lse_stride; NULL: not kept
+ *   scale         finite in fp32
+ *   window        0: none
+ *   max_new       at least the most new tokens of a sequence, for the choice of the
+ *                 kernel alone (results do not depend on it); 0: not known
+ *   workspace     device, 256-byte aligned, of at least the size that
+ *                 rope3d_paged_attention_workspace gives for the same arguments;
+ *                 its contents are not kept. Calls that may run at the same
+ *                 time need workspaces of their own.
+ * Scores, statistics and sums are fp32; the weights are rounded once to `dtype`
+ * as an operand of the second product, and out once. The same call gives the same
+ * bits. Rows of out and lse behind the last sequence are left as they were.
+ * Two kernels on `stream`, asynchronous.
+ * Errors: NULL, SHAPE, DTYPE, ARG (scale, causal, window, max_new), ALIGN, ALIAS,
+ * SCRATCH, DEVICE, CUDA.
+ */
+typedef struct rope3d_paged_attention_args {
+    const void *q, *k_cache, *v_cache;
+    void *out;
+    float *lse;
+    rope3d_paged_batch batch;
+    int64_t tokens, q_heads, kv_heads, head_dim;
+    int64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride, lse_stride;
+    int64_t k_page_stride, k_slot_stride, k_cache_head_stride;
+    int64_t v_page_stride, v_slot_stride, v_cache_head_stride;
+    int64_t window, max_new;
+    void *workspace;
+    int64_t workspace_bytes;
+    double scale;
+    int32_t dtype, causal;
+} rope3d_paged_attention_args;
+
+int rope3d_paged_attention(const rope3d_paged_attention_args *args, void *stream);
+int rope3d_paged_attention_check(const rope3d_paged_attention_args *args, int32_t check_device);
+/* The workspace's size; args->workspace and workspace_bytes are not read. */
+int rope3d_paged_attention_workspace(const rope3d_paged_attention_args *args, int64_t *bytes);
+/* Kernel of this thread's last attention over pages: 1 few rows (warp MMAs), 2
+ * tiles of 128 rows (tcgen05), 0 none yet. */
+int rope3d_paged_attention_last_kernel(void);
+/* How many bounded waits of its kernels ran out (0 unless something is badly
+ * wrong; such a launch's output is not to be used); reset clears the count.
+ * Synchronises with the device. Errors: NULL, CUDA. */
+int rope3d_testing_paged_wait_timeouts(int64_t *count, int32_t reset);
+
+/*
+ * rope3d_cache_fork -- sequence children[i] becomes a copy of sequence
+ * parents[i] that shares its full pages: with n = seq_lens[parent],
+ *     page_table[child][j] = page_table[parent][j]  for j < n / page_size
+ *     page_table[child][n / page_size] = new_pages[i], which receives a copy of
+ *         the parent's page there where n % page_size > 0 (else it is the child's
+ *         next page, with nothing in it)
+ *     seq_lens[child] = n
+ * for all layers at once: the cache is `planes` planes (a K or a V of a layer
+ * each) of `pages` pages of page_bytes contiguous bytes.
+ *
+ *   parents, children, new_pages  device int32 [forks]. One parent may have many
+ *                 children; no child is named twice or is a parent in the same call,
+ *                 and no new page is in use (calls that break this race)
+ *   invalid_count optional int32: a fork with a number out of range, with parent
+ *                 = child, whose parent's last page is absent, or whose parent
+ *                 fills its table's row, changes nothing and adds one here
+ *   page_bytes, strides, cache    multiples of 16 bytes
+ * One kernel on `stream`, asynchronous.
+ * Errors: NULL, SHAPE, ALIGN, ALIAS, DEVICE, CUDA.
+ */
+typedef struct rope3d_cache_fork_args {
+    void *cache;
+    int32_t *page_table, *seq_lens;
+    const int32_t *parents, *children, *new_pages;
+    int32_t *invalid_count;
+    int64_t planes, pages, page_bytes, plane_stride, page_stride;   /* strides in bytes */
+    int64_t seqs, table_width, table_stride, page_size, forks;
+} rope3d_cache_fork_args;
+
+int rope3d_cache_fork(const rope3d_cache_fork_args *args, void *stream);
+int rope3d_cache_fork_check(const rope3d_cache_fork_args *args, int32_t check_device);
+
+/*
+ * rope3d_cache_compact -- the pages in use move to the front of the cache, and
+ * all others are free. A page is in use when a row of the table names it among
+ * its first ceil((seq_lens[s] + reserve) / page_size) entries (a row of length
+ * 0 holds none), by one row or many. With U pages in use, those at U and above
+ * move, in order, to the pages below U that are not, in order; the others stay.
+ *
+ *   table_out     [seqs, table_width], row stride table_out_stride: the new
+ *                 numbers of the pages in use, -1 everywhere else. May be exactly
+ *                 page_table.
+ *   used          device int32: receives U. Pages [U, pages) are free afterwards.
+ *   pages         up to 2^20
+ *   workspace     device, 256-byte aligned, as rope3d_cache_compact_workspace gives
+ * Entries that are absent pages are -1 in table_out. Two kernels on `stream`,
+ * asynchronous.
+ * Errors: NULL, SHAPE, ALIGN, ALIAS, SCRATCH, DEVICE, CUDA.
+ */
+typedef struct rope3d_cache_compact_args {
+    void *cache;
+    const int32_t *page_table, *seq_lens;
+    int32_t *table_out, *used;
+    int64_t planes, pages, page_bytes, plane_stride, page_stride;   /* strides in bytes */
+    int64_t seqs, table_width, table_stride, table_out_stride, page_size, reserve;
+    void *workspace;
+    int64_t workspace_bytes;
+} rope3d_cache_compact_args;
+
+int rope3d_cache_compact(const rope3d_cache_compact_args *args, void *stream);
+int rope3d_cache_compact_check(const rope3d_cache_compact_args *args, int32_t check_device);
+int rope3d_cache_compact_workspace(const rope3d_cache_compact_args *args, int64_t *bytes);
+
 /*
  * rope3d_apply_pair_host -- the same rotation for HOST buffers: the library
  * streams Q and K to the GPU in token chunks, rotates each chunk with the same

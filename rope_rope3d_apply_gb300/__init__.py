@@ -41,6 +41,11 @@ __all__ = [
     "rope3d_testing_ffn_wait_timeouts", "rope3d_block_norm", "rope3d_block_norm_backward",
     "rope3d_block_norm_check", "rope3d_block_norm_backward_check", "rope3d_block_norm_last_kernel",
     "rope3d_testing_norm_wait_timeouts",
+    "PAIRS_INTERLEAVED", "PAIRS_HALVES", "POSITIONS_I64", "POSITIONS_I32", "POSITIONS_F32",
+    "rope3d_apply_axes", "rope3d_apply_axes_backward", "rope3d_apply_axes_check", "rope3d_apply_axes_last_kernel",
+    "rope3d_cache_append", "rope3d_cache_append_check", "rope3d_paged_attention", "rope3d_paged_attention_check",
+    "rope3d_paged_attention_last_kernel", "rope3d_testing_paged_wait_timeouts", "rope3d_cache_fork",
+    "rope3d_cache_fork_check", "rope3d_cache_compact", "rope3d_cache_compact_check",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -52,6 +57,8 @@ BF16, F32, F16 = 0, 1, 2
 GATE_OFF, GATE_FIRST = 0, 1
 NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
 ACT_SILU, ACT_GELU_TANH, ACT_GELU_ERF = 0, 1, 2
+PAIRS_INTERLEAVED, PAIRS_HALVES = 0, 1
+POSITIONS_I64, POSITIONS_I32, POSITIONS_F32 = 0, 1, 2
 STATUS = {
     0: "OK", -1: "ERR_NULL", -2: "ERR_SHAPE", -3: "ERR_DTYPE", -4: "ERR_ALIGN",
     -5: "ERR_ALIAS", -6: "ERR_DEVICE", -7: "ERR_PARITY", -8: "ERR_CUDA", -9: "ERR_TABLES",
@@ -104,6 +111,30 @@ _FfnBackArgs = _struct(
     "i64:dy_stride x_stride w_gate_stride w_up_stride w_down_stride pre_stride",
     "i64:dx_stride dw_gate_stride dw_up_stride dw_down_stride",
     "p:workspace", "i64:workspace_bytes", "i32:dtype pre_dtype act")
+
+_BATCH = ("p:page_table seq_lens q_starts", "i64:seqs table_width table_stride pages page_size")   # rope3d_paged_batch
+_CACHES = ("i64:k_page_stride k_slot_stride k_cache_head_stride", "i64:v_page_stride v_slot_stride v_cache_head_stride")
+_AxesArgs = _struct(
+    "rope3d_apply_axes_args", "p:q k q_out k_out positions freqs", "i64:tokens q_heads k_heads head_dim",
+    "i64:q_token_stride q_head_stride k_token_stride k_head_stride",
+    "i64:q_out_token_stride q_out_head_stride k_out_token_stride k_out_head_stride positions_stride",
+    "i32:section0 section1 section2 dtype position_type pairing inverse")
+_AppendArgs = _struct(
+    "rope3d_cache_append_args", "p:q q_out k v k_cache v_cache positions freqs invalid_count", *_BATCH,
+    "i64:tokens q_heads kv_heads head_dim", "i64:q_token_stride q_head_stride q_out_token_stride q_out_head_stride",
+    "i64:k_token_stride k_head_stride v_token_stride v_head_stride", *_CACHES, "i64:positions_stride",
+    "i32:section0 section1 section2 dtype position_type pairing")
+_AttentionArgs = _struct(
+    "rope3d_paged_attention_args", "p:q k_cache v_cache out lse", *_BATCH, "i64:tokens q_heads kv_heads head_dim",
+    "i64:q_token_stride q_head_stride out_token_stride out_head_stride lse_stride", *_CACHES, "i64:window max_new",
+    "p:workspace", "i64:workspace_bytes", "f64:scale", "i32:dtype causal")
+_ForkArgs = _struct(
+    "rope3d_cache_fork_args", "p:cache page_table seq_lens parents children new_pages invalid_count",
+    "i64:planes pages page_bytes plane_stride page_stride", "i64:seqs table_width table_stride page_size forks")
+_CompactArgs = _struct(
+    "rope3d_cache_compact_args", "p:cache page_table seq_lens table_out used",
+    "i64:planes pages page_bytes plane_stride page_stride",
+    "i64:seqs table_width table_stride table_out_stride page_size reserve", "p:workspace", "i64:workspace_bytes")
 
 
 def _declare(lib):
@@ -170,6 +201,21 @@ def _declare(lib):
         "rope3d_gated_ffn_backward_workspace": ([vp, vp], c.c_int),
         "rope3d_gated_ffn_last_kernel": ([], c.c_int),
         "rope3d_testing_ffn_wait_timeouts": ([vp, i32], c.c_int),
+        "rope3d_apply_axes": ([vp, vp], c.c_int),
+        "rope3d_apply_axes_check": ([vp, i32], c.c_int),
+        "rope3d_apply_axes_last_kernel": ([], c.c_int),
+        "rope3d_cache_append": ([vp, vp], c.c_int),
+        "rope3d_cache_append_check": ([vp, i32], c.c_int),
+        "rope3d_paged_attention": ([vp, vp], c.c_int),
+        "rope3d_paged_attention_check": ([vp, i32], c.c_int),
+        "rope3d_paged_attention_workspace": ([vp, vp], c.c_int),
+        "rope3d_paged_attention_last_kernel": ([], c.c_int),
+        "rope3d_testing_paged_wait_timeouts": ([vp, i32], c.c_int),
+        "rope3d_cache_fork": ([vp, vp], c.c_int),
+        "rope3d_cache_fork_check": ([vp, i32], c.c_int),
+        "rope3d_cache_compact": ([vp, vp], c.c_int),
+        "rope3d_cache_compact_check": ([vp, i32], c.c_int),
+        "rope3d_cache_compact_workspace": ([vp, vp], c.c_int),
         "rope3d_preflight_strided": ([vp, vp, vp, vp, vp] + [i64] * 6 + [vp, i32] + [vp] * 4 + [i32],
                                      c.c_int),
     }
@@ -706,6 +752,8 @@ def _new(shape, dtype, like):
                 return _fast_empty((shape[0], shape[1]), (shape[1], 1), dtype)
             if len(shape) == 1:
                 return _fast_empty((shape[0],), (1,), dtype)
+            if len(shape) == 3:
+                return _fast_empty((shape[0], shape[1], shape[2]), (shape[1] * shape[2], shape[2], 1), dtype)
         except TypeError:
             out = _torch.empty(tuple(shape), dtype=dtype, device=like.device)   # (raises for the caller's mistake)
             _fast_empty = None   # a torch whose function takes other arguments
@@ -718,16 +766,16 @@ def _fresh(like):
     return _new(like.shape, like.dtype, like)
 
 
-def _elsewhere(call, args):
-    """The results of `call` (arguments by name) where its stream is not torch's
-    current one, else None. It then runs with that stream current, so that the memory
+def _elsewhere(call, args, first="x"):
+    """The results of `call` (arguments by name, `first` on the call's device) where its
+    stream is not torch's current one, else None. It then runs with that stream current, so that the memory
     it allocates is that stream's. (The current stream's may be memory that its pending
     work still reads.) What it returns is kept from other use until the current stream
     has passed it too, and what it is given until its own stream has: a temporary may be
     freed on return. (Not on streams that torch did not make, which may be gone by the
     time the memory is freed: there the caller keeps the tensors.)"""
     torch = _torch or _use_torch()
-    x, stream = args["x"], args.pop("stream")
+    x, stream = args[first], args.pop("stream")
     if not x.is_cuda or _raw_stream(stream, x) == torch._C._cuda_getCurrentRawStream(x.device.index):
         return None
     if not isinstance(stream, torch.cuda.Stream):
@@ -1000,6 +1048,321 @@ def rope3d_testing_ffn_wait_timeouts(reset: bool = True) -> int:
     n = ctypes.c_int64()
     _check(load_library().rope3d_testing_ffn_wait_timeouts(ctypes.byref(n), 1 if reset else 0),
            "rope3d_testing_ffn_wait_timeouts")
+    return int(n.value)
+
+
+# ---- a paged cache ---------------------------------------------------------
+
+
+def _rows3(name, t, tokens, heads, dim, dtype):
+    """(token stride, head stride) of [tokens, heads, dim]; zeros for None."""
+    if t is None:
+        return 0, 0
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != tokens or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected {(tokens, heads, dim)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    a, b, one = t.stride()
+    if one != 1 and dim > 1:
+        raise ValueError(f"{name} must have contiguous channels")
+    return a, b
+
+
+def _cache4(name, t, heads, dim, dtype, like=None):
+    """(page stride, place stride, head stride) of [pages, page_size, heads, dim]."""
+    shape = t.shape
+    if len(shape) != 4 or shape[2] != heads or shape[3] != dim or (like is not None and like.shape != shape):
+        want = tuple(like.shape) if like is not None else ("pages", "page_size", heads, dim)
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected {want}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    a, b, c, one = t.stride()
+    if one != 1 and dim > 1:
+        raise ValueError(f"{name} must have contiguous channels")
+    return a, b, c
+
+
+def _ints(name, t, count=None):
+    """The address of a contiguous int32 vector (0 for None)."""
+    if t is None:
+        return 0
+    if t.dtype is not _torch.int32:
+        raise TypeError(f"{name} is {t.dtype}, expected torch.int32")
+    if len(t.shape) != 1 or (count is not None and t.shape[0] != count) or (t.shape[0] > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be contiguous, [{'n' if count is None else count}]")
+    return t.data_ptr()
+
+
+def _table(name, t, seqs):
+    """(entries of a row, row stride) of a page table [seqs, entries]."""
+    if t.dtype is not _torch.int32:
+        raise TypeError(f"{name} is {t.dtype}, expected torch.int32")
+    if len(t.shape) != 2 or t.shape[0] != seqs or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [{seqs}, entries] with contiguous rows")
+    return t.shape[1], t.stride(0) if seqs > 1 else max(t.shape[1], 1)
+
+
+def _counter(name, t):
+    """The address of an optional int32 counter."""
+    if t is not None and (t.dtype is not _torch.int32 or t.numel() != 1):
+        raise TypeError(f"{name} must be one int32")
+    return _ptr_of(t)
+
+
+def _batch_fields(page_table, seq_lens, q_starts, cache):
+    """The fields of rope3d_paged_batch: (addresses, sizes)."""
+    seqs = seq_lens.shape[0] if len(seq_lens.shape) == 1 else -1
+    width, ld = _table("page_table", page_table, seqs)
+    return ((page_table.data_ptr(), _ints("seq_lens", seq_lens), _ints("q_starts", q_starts, seqs + 1)),
+            (seqs, width, ld, cache.shape[0], cache.shape[1]))
+
+
+def _rotation_fields(positions, freqs, sections, tokens):
+    """(sections, position type, positions' row stride) of a rotation."""
+    if freqs.dtype is not _torch.float32 or len(freqs.shape) != 1 or (freqs.shape[0] > 1 and freqs.stride(0) != 1):
+        raise ValueError("freqs must be float32, contiguous, [pairs]")
+    sections = (freqs.shape[0], 0, 0) if sections is None else (*sections, 0, 0)[:3] if len(sections) <= 3 else None
+    if sections is None or sum(sections) != freqs.shape[0]:
+        raise ValueError("sections must be up to three counts of pairs that make up freqs")
+    if positions is None:
+        return sections, 0, 0
+    dt = positions.dtype
+    kind = POSITIONS_I64 if dt is _torch.int64 else POSITIONS_I32 if dt is _torch.int32 else \
+        POSITIONS_F32 if dt is _torch.float32 else None
+    if kind is None:
+        raise TypeError(f"positions is {dt}, expected int64, int32 or float32")
+    axes = 3 if sections[2] else 2 if sections[1] else 1
+    shape = positions.shape
+    if len(shape) == 1:
+        rows, count, ld, one = 1, shape[0], shape[0], positions.stride(0)
+    elif len(shape) == 2:
+        (rows, count), (ld, one) = shape, positions.stride()
+    else:
+        rows = 0
+    if rows < axes or count != tokens or (one != 1 and tokens > 1):
+        raise ValueError(f"positions must be [axes, {tokens}] with contiguous rows, at least {axes} of them")
+    return sections, kind, ld
+
+
+def rope3d_apply_axes(q, k, positions, freqs, sections=None, pairing: int = PAIRS_INTERLEAVED, q_out=None, k_out=None,
+                      inverse: bool = False, *, stream=None):
+    """Rotary positions with up to three axes, token by token: pair j of every head of
+    q [tokens, q_heads, head_dim] and k [tokens, k_heads, head_dim] (k may be None)
+    turns by positions[axis(j)][token] * freqs[j]. positions: [axes, tokens] (or
+    [tokens]) int64, int32 or float32; freqs: float32 [pairs]; sections: pairs of
+    each axis, in order (None: all on the first). Channels from 2 * pairs on are
+    copied. inverse turns back. Any strides of tokens and heads; q_out = q and k_out =
+    k rotate in place. Returns (q_out, k_out). stream as in rope3d_block_norm."""
+    if stream is not None and (there := _elsewhere(rope3d_apply_axes, dict(locals()), "q")) is not None:
+        return there
+    _torch or _use_torch()
+    if len(q.shape) != 3:
+        raise ValueError("q must be [tokens, heads, head_dim]")
+    (tokens, heads, dim), dt = q.shape, q.dtype
+    k_heads = 0 if k is None or len(k.shape) != 3 else k.shape[1]
+    sections, kind, ld = _rotation_fields(positions, freqs, sections, tokens)
+    q_out = _fresh(q) if q_out is None else q_out
+    if k is not None and k_out is None:
+        k_out = _fresh(k)
+    args = _AxesArgs.pack(
+        q.data_ptr(), _ptr_of(k), q_out.data_ptr(), _ptr_of(k_out), positions.data_ptr(), freqs.data_ptr(), tokens, heads,
+        k_heads, dim, *_rows3("q", q, tokens, heads, dim, dt), *_rows3("k", k, tokens, k_heads, dim, dt),
+        *_rows3("q_out", q_out, tokens, heads, dim, dt), *_rows3("k_out", k_out, tokens, k_heads, dim, dt), ld, *sections,
+        _code(q), kind, pairing, 1 if inverse else 0)
+    rc = (_lib or load_library()).rope3d_apply_axes(args, _raw_stream(stream, q))
+    if rc:
+        raise Rope3dError(rc, "rope3d_apply_axes")
+    return q_out, k_out
+
+
+def rope3d_apply_axes_backward(dq, dk, positions, freqs, sections=None, pairing: int = PAIRS_INTERLEAVED, dq_out=None,
+                               dk_out=None, *, stream=None):
+    """The gradients of rope3d_apply_axes for its q and k from those of its results: the
+    same rotation turned back. Returns (dq_out, dk_out)."""
+    return rope3d_apply_axes(dq, dk, positions, freqs, sections, pairing, dq_out, dk_out, True, stream=stream)
+
+
+def rope3d_cache_append(q, k, v, k_cache, v_cache, page_table, seq_lens, q_starts=None, freqs=None, positions=None,
+                        sections=None, pairing: int = PAIRS_INTERLEAVED, q_out=None, invalid_count=None, *, stream=None):
+    """New tokens enter a paged cache: k [tokens, kv_heads, head_dim] rotated as by
+    rope3d_apply_axes and v as it is are written to their places in k_cache and
+    v_cache [pages, page_size, kv_heads, head_dim], and q (or None) is rotated into
+    q_out. Tokens [q_starts[s], q_starts[s + 1]) are the last of the seq_lens[s] places
+    of sequence s (q_starts None: as many of each), whose pages row s of page_table
+    names; all three int32 on the device. positions None: a token's place; freqs None:
+    no rotation (then q is None). Tokens without a page are left out and counted in
+    invalid_count; rows behind the last sequence are left as they are. Returns q_out."""
+    if stream is not None and (there := _elsewhere(lambda **a: (rope3d_cache_append(**a),), dict(locals()), "k")) is not None:
+        return there[0]
+    _torch or _use_torch()
+    if len(k.shape) != 3:
+        raise ValueError("k must be [tokens, kv_heads, head_dim]")
+    (tokens, kv, dim), dt = k.shape, k.dtype
+    heads = 0 if q is None or len(q.shape) != 3 else q.shape[1]
+    if freqs is None:
+        if sections is not None:
+            raise ValueError("sections without freqs")
+        sections, kind, ld = (0, 0, 0), 0, 0
+    else:
+        sections, kind, ld = _rotation_fields(positions, freqs, sections, tokens)
+    if q is not None and q_out is None:
+        q_out = _fresh(q)
+    pointers, sizes = _batch_fields(page_table, seq_lens, q_starts, k_cache)
+    args = _AppendArgs.pack(
+        _ptr_of(q), _ptr_of(q_out), k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr_of(positions),
+        _ptr_of(freqs), _counter("invalid_count", invalid_count), *pointers, *sizes, tokens, heads, kv, dim,
+        *_rows3("q", q, tokens, heads, dim, dt), *_rows3("q_out", q_out, tokens, heads, dim, dt),
+        *_rows3("k", k, tokens, kv, dim, dt), *_rows3("v", v, tokens, kv, dim, dt),
+        *_cache4("k_cache", k_cache, kv, dim, dt), *_cache4("v_cache", v_cache, kv, dim, dt, k_cache), ld, *sections,
+        _code(k), kind, pairing)
+    rc = (_lib or load_library()).rope3d_cache_append(args, _raw_stream(stream, k))
+    if rc:
+        raise Rope3dError(rc, "rope3d_cache_append")
+    return q_out
+
+
+def rope3d_paged_attention(q, k_cache, v_cache, page_table, seq_lens, q_starts=None, scale=None, causal: bool = True,
+                           window: int = 0, max_new=None, out=None, lse=None, workspace=None, *, stream=None):
+    """Attention of new tokens q [tokens, q_heads, head_dim] (bf16 or fp16) over the
+    pages of their sequences, described as in rope3d_cache_append, after their
+    keys and values have entered the cache: softmax(scale * q k) v over the places of the
+    sequence, up to the token's own where causal, and its last `window` of them where
+    window > 0. scale None: head_dim ** -0.5. max_new: the most new tokens of a
+    sequence where the caller knows (a better choice of kernel, never another
+    result). lse: True, or a float32 [tokens, q_heads] tensor, for the rows' log sum
+    exp too. Rows that see no key are zeros (lse -inf); rows behind the last sequence
+    are left as they are. Returns out, or (out, lse). workspace: a contiguous device
+    tensor of at least the bytes the call needs (allocated when None)."""
+    if stream is not None and (there := _elsewhere(rope3d_paged_attention, dict(locals()), "q")) is not None:
+        return there
+    _torch or _use_torch()
+    if len(q.shape) != 3:
+        raise ValueError("q must be [tokens, heads, head_dim]")
+    (tokens, heads, dim), dt = q.shape, q.dtype
+    kv = k_cache.shape[2] if len(k_cache.shape) == 4 else -1
+    if out is None:
+        out = _fresh(q)
+    if lse is True:
+        lse = _new((tokens, heads), _torch.float32, q)
+    elif lse is False:
+        lse = None
+    pointers, sizes = _batch_fields(page_table, seq_lens, q_starts, k_cache)
+    body = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), _ptr_of(lse), *pointers, *sizes, tokens, heads,
+            kv, dim, *_rows3("q", q, tokens, heads, dim, dt), *_rows3("out", out, tokens, heads, dim, dt),
+            _stride("lse", lse, tokens, heads, _torch.float32), *_cache4("k_cache", k_cache, kv, dim, dt),
+            *_cache4("v_cache", v_cache, kv, dim, dt, k_cache), window, max_new or 0)
+    tail = (dim ** -0.5 if scale is None else scale, _code(q), 1 if causal else 0)
+    st = _raw_stream(stream, q)
+    args, ws = _workspace(_AttentionArgs, (body, tail), "rope3d_paged_attention_workspace", "rope3d_paged_attention", workspace, q)
+    _check((_lib or load_library()).rope3d_paged_attention(args, st), "rope3d_paged_attention")
+    return out if lse is None else (out, lse)
+
+
+def _planes(cache):
+    """(planes, pages, bytes of a page, plane and page strides in bytes) of a cache
+    [planes, pages, ...] of contiguous pages."""
+    shape, strides, size = cache.shape, cache.stride(), cache.element_size()
+    if len(shape) < 3:
+        raise ValueError("cache must be [planes, pages, ...]")
+    count = 1
+    for n, ld in zip(reversed(shape[2:]), reversed(strides[2:])):
+        if n != 1 and ld != count:
+            raise ValueError("cache must have contiguous pages")
+        count *= n
+    page = strides[1] if shape[1] > 1 else count
+    return shape[0], shape[1], count * size, (strides[0] if shape[0] > 1 else page * shape[1]) * size, page * size
+
+
+def rope3d_cache_fork(cache, page_table, seq_lens, parents, children, new_pages, *, page_size=None, invalid_count=None,
+                      stream=None):
+    """Sequences children[i] become copies of parents[i], for all layers at once: they
+    share the full pages and get a copy of the last, partly filled one in new_pages[i]
+    (with full pages only, it is the child's next page). cache: [planes, pages, ...]
+    with contiguous pages, a plane for the K or the V of each layer; page_size: places of a
+    page (None: cache.shape[2]). page_table and seq_lens are updated in place; forks
+    with numbers out of range change nothing and are counted in invalid_count."""
+    if stream is not None and _elsewhere(lambda **a: (rope3d_cache_fork(**a),), dict(locals()), "cache") is not None:
+        return
+    _torch or _use_torch()
+    forks = parents.shape[0] if len(parents.shape) == 1 else -1
+    seqs = seq_lens.shape[0] if len(seq_lens.shape) == 1 else -1
+    width, ld = _table("page_table", page_table, seqs)
+    args = _ForkArgs.pack(
+        cache.data_ptr(), page_table.data_ptr(), _ints("seq_lens", seq_lens), _ints("parents", parents, forks),
+        _ints("children", children, forks), _ints("new_pages", new_pages, forks), _counter("invalid_count", invalid_count),
+        *_planes(cache), seqs, width, ld, cache.shape[2] if page_size is None else page_size, forks)
+    _check((_lib or load_library()).rope3d_cache_fork(args, _raw_stream(stream, cache)), "rope3d_cache_fork")
+
+
+def rope3d_cache_compact(cache, page_table, seq_lens, *, page_size=None, reserve: int = 0, table_out=None, used=None,
+                         workspace=None, stream=None):
+    """The pages in use move to the front of cache (as in rope3d_cache_fork), for all
+    layers at once; all others are free. A row of page_table uses its first
+    ceil((seq_lens[s] + reserve) / page_size) pages, none where the length is 0. Returns
+    (table_out, used): the table with the pages' new numbers (-1 where it names no page
+    in use; table_out = page_table renumbers in place), and how many are in use, one
+    int32 on the device."""
+    if stream is not None and (there := _elsewhere(rope3d_cache_compact, dict(locals()), "cache")) is not None:
+        return there
+    _torch or _use_torch()
+    seqs = seq_lens.shape[0] if len(seq_lens.shape) == 1 else -1
+    width, ld = _table("page_table", page_table, seqs)
+    table_out = _fresh(page_table) if table_out is None else table_out
+    used = _new((1,), _torch.int32, cache) if used is None else used
+    width_out, ld_out = _table("table_out", table_out, seqs)
+    if width_out != width:
+        raise ValueError("table_out must have page_table's shape")
+    body = (cache.data_ptr(), page_table.data_ptr(), _ints("seq_lens", seq_lens), table_out.data_ptr(), _counter("used", used),
+            *_planes(cache), seqs, width, ld, ld_out, cache.shape[2] if page_size is None else page_size, reserve)
+    st = _raw_stream(stream, cache)
+    args, ws = _workspace(_CompactArgs, (body, ()), "rope3d_cache_compact_workspace", "rope3d_cache_compact", workspace, cache)
+    _check((_lib or load_library()).rope3d_cache_compact(args, st), "rope3d_cache_compact")
+    return table_out, used
+
+
+def rope3d_apply_axes_check(check_device: bool = False, **fields) -> str:
+    """Status name of rope3d_apply_axes's checks for the given argument fields
+    (pointers may be plain integers; sections are section0 to section2)."""
+    return STATUS[load_library().rope3d_apply_axes_check(ctypes.byref(_AxesArgs(**fields)), int(check_device))]
+
+
+def rope3d_cache_append_check(check_device: bool = False, **fields) -> str:
+    """Status name of rope3d_cache_append's checks."""
+    return STATUS[load_library().rope3d_cache_append_check(ctypes.byref(_AppendArgs(**fields)), int(check_device))]
+
+
+def rope3d_paged_attention_check(check_device: bool = False, **fields) -> str:
+    """Status name of rope3d_paged_attention's checks."""
+    return STATUS[load_library().rope3d_paged_attention_check(ctypes.byref(_AttentionArgs(**fields)), int(check_device))]
+
+
+def rope3d_cache_fork_check(check_device: bool = False, **fields) -> str:
+    """Status name of rope3d_cache_fork's checks."""
+    return STATUS[load_library().rope3d_cache_fork_check(ctypes.byref(_ForkArgs(**fields)), int(check_device))]
+
+
+def rope3d_cache_compact_check(check_device: bool = False, **fields) -> str:
+    """Status name of rope3d_cache_compact's checks."""
+    return STATUS[load_library().rope3d_cache_compact_check(ctypes.byref(_CompactArgs(**fields)), int(check_device))]
+
+
+def rope3d_apply_axes_last_kernel() -> int:
+    """Kernel of this thread's last rope3d_apply_axes or rope3d_cache_append: 1 vectors, 2
+    single pairs."""
+    return int(load_library().rope3d_apply_axes_last_kernel())
+
+
+def rope3d_paged_attention_last_kernel() -> int:
+    """Kernel of this thread's last attention over pages: 1 few rows, 2 tiles."""
+    return int(load_library().rope3d_paged_attention_last_kernel())
+
+
+def rope3d_testing_paged_wait_timeouts(reset: bool = True) -> int:
+    """Bounded waits of the attention over pages that ran out (0 in a sound run)."""
+    n = ctypes.c_int64()
+    _check(load_library().rope3d_testing_paged_wait_timeouts(ctypes.byref(n), 1 if reset else 0),
+           "rope3d_testing_paged_wait_timeouts")
     return int(n.value)
 
 

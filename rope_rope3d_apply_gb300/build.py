@@ -29,6 +29,12 @@ SOURCES = [
     os.path.join(CSRC, "rope3d_norm_back.cu"),
     os.path.join(CSRC, "rope3d_norm.cuh"),
     os.path.join(CSRC, "rope3d_ffn.cu"),
+    os.path.join(CSRC, "rope3d_axes.cu"),
+    os.path.join(CSRC, "rope3d_paged.cu"),
+    os.path.join(CSRC, "rope3d_paged_tc.cu"),
+    os.path.join(CSRC, "rope3d_paged.cuh"),
+    os.path.join(CSRC, "rope3d_paged.h"),
+    os.path.join(CSRC, "rope3d_pages.cu"),
     os.path.join(CSRC, "rope3d_tc.cuh"),
     os.path.join(CSRC, "rope3d_api.cpp"),
     os.path.join(CSRC, "rope3d_internal.h"),
@@ -98,16 +104,21 @@ def commands(out_dir: str = BUILD, extra_nvcc: list[str] | None = None,
     ]
     norm_back_o = os.path.join(out_dir, "rope3d_norm_back.o")
     nvcc_norm_back = [*nvcc_norm[:-3], os.path.join(CSRC, "rope3d_norm_back.cu"), "-o", norm_back_o]
+    # the operators around a paged cache
+    paged = [("rope3d_axes", ["-fmad=false"]), ("rope3d_paged", []), ("rope3d_paged_tc", []), ("rope3d_pages", [])]
+    paged_o = [os.path.join(out_dir, f"{name}.o") for name, _ in paged]
+    nvcc_paged = [[*nvcc_norm[:-3], *extra, os.path.join(CSRC, f"{name}.cu"), "-o", o]
+                  for (name, extra), o in zip(paged, paged_o)]
     gxx_compile = [
         "g++", "-std=c++17", "-O2", "-fPIC", "-ffp-contract=off", "-fno-fast-math", *dbg,
         "-pthread", "-Wall", "-Wno-unused-function", f"-I{cuda}/include",
         "-c", os.path.join(CSRC, "rope3d_api.cpp"), "-o", api_o,
     ]
     link = [_nvcc(), *ARCH, "-shared", kern_o, api_o, noalloc_o, patch_o, neox_o, na_o, ffn_o,
-            norm_o, norm_back_o,
+            norm_o, norm_back_o, *paged_o,
             "-o", os.path.join(out_dir, "librope3d.so"), "-Xcompiler", "-pthread"]
     return [nvcc_compile, gxx_compile, nvcc_noalloc, nvcc_patch, nvcc_neox, nvcc_na, nvcc_ffn,
-            nvcc_norm, nvcc_norm_back], link
+            nvcc_norm, nvcc_norm_back, *nvcc_paged], link
 
 
 def up_to_date(lib: str = LIB) -> bool:

@@ -1,0 +1,594 @@
+// rope3d_axes.cu -- rotary positions with several axes, given token by token:
+// rope3d_apply_axes (and, with `inverse`, its gradient) and rope3d_cache_append,
+// which writes the rotated keys and the values straight into the pages of a cache.
+//
+// Pair j of every head turns by angle = positions[axis(j)][token] * freqs[j]:
+//     y_a = a cos - b sin,  y_b = a sin + b cos
+// in fp32, each product and sum rounded by itself as in rope3d_apply_pair, then
+// one cast. A rotation's transpose is the rotation by -angle, so the gradient
+// is the same kernel with sin negated.
+//
+// The angle is never formed: what a turn leaves over, t = frac(position * freq /
+// 2 pi), is taken from an exact product (freq / 2 pi split into two floats, the
+// product's error by fma; in fp64 where a position has no exact float), and
+// sincospi takes it from there. The error is that of sincospi, at position 2^20 as
+// at 0.
+//
+// Each block takes tiles of a few tokens: cos and sin of the tile's tokens and pairs
+// go into shared memory once (64 sincospi a token instead of 64 for each of its
+// heads), then each thread moves 16-byte vectors, four loads in flight. What bounds it is
+// memory: 16 x 64 x 64 tokens of 2 x 16 heads of 128 in bf16 (1.07 GB) take what a
+// copy of them takes.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/rope3d.h"
+#include "rope3d_internal.h"
+#include "rope3d_paged.h"
+#include "rope3d_tc.cuh"
+
+namespace {
+
+using rope3d::FastDiv;
+using rope3d::make_fastdiv;
+using namespace rope3d_paged;
+
+constexpr int kThreads = 256;
+constexpr int kInFlight = 4;     // 16-byte units (or pairs of them) a thread has in flight
+constexpr int kMaxTile = 32;     // tokens of a tile
+
+__device__ __forceinline__ uint32_t fdiv(uint32_t n, const FastDiv &f) { return (__umulhi(n, f.mul) + n) >> f.shift; }
+
+// Where a token's heads lie.
+struct Rows {
+    const char *p;
+    int64_t token, head;   // bytes
+};
+
+struct AxesParams {
+    Rows in[3], out[3];        // q, k, v; out of k and v: the caches (token unused) in an append
+    int64_t slot[2], page[2];  // bytes: the caches' strides
+    const void *positions;
+    const float *freqs;
+    int64_t positions_stride;
+    int *invalid;
+    Batch batch;
+    int tokens, tile, pairs, head_dim;
+    int end0, end1;            // pairs of axis 0; of axes 0 and 1
+    int heads[3];              // q, k, v
+    int rotating;              // units of a head row that rotate; the rest are copied
+    FastDiv per_token, per_head;
+    int position_type;         // ROPE3D_POSITIONS_*; -1: the place in the sequence
+    float sign;
+};
+
+// ---- angles ----------------------------------------------------------------------
+
+constexpr double kInvTwoPi = 0.15915494309189533577;
+
+// cos and sin of 2 pi position freq / (2 pi), from freq / 2 pi = hi + lo.
+__device__ __forceinline__ float2 turn(float pos, float hi, float lo) {
+    const float a = __fmul_rn(pos, hi);
+    const float e = __fmaf_rn(pos, lo, __fmaf_rn(pos, hi, -a));   // what the product dropped
+    const float whole = __fsub_rn(a, rintf(a));                   // exact
+    const float t = __fadd_rn(whole, e);
+    const float rest = __fsub_rn(e, __fsub_rn(t, whole)) * 6.2831853f;
+    float s, c;
+    sincospif(2.0f * t, &s, &c);
+    return make_float2(__fmaf_rn(-s, rest, c), __fmaf_rn(c, rest, s));
+}
+
+__device__ float2 turn_far(double pos, float freq) {
+    const double a = pos * (double(freq) * kInvTwoPi);
+    const float t = float(a - rint(a));
+    float s, c;
+    sincospif(2.0f * t, &s, &c);
+    return make_float2(c, s);
+}
+
+// Position of token t on `axis`: as a float where it has one, else in fp64.
+__device__ __forceinline__ bool position(const AxesParams &p, int axis, int t, float &near, double &far) {
+    const int64_t at = axis * p.positions_stride + t;
+    if (p.position_type == ROPE3D_POSITIONS_F32) {
+        near = static_cast<const float *>(p.positions)[at];
+        return true;
+    }
+    const int64_t v = p.position_type == ROPE3D_POSITIONS_I64 ? static_cast<const int64_t *>(p.positions)[at]
+                                                              : static_cast<const int32_t *>(p.positions)[at];
+    near = float(v);
+    far = double(v);
+    return v >= -(1 << 24) && v <= (1 << 24);
+}
+
+// ---- elements --------------------------------------------------------------------
+
+template <int kType>
+__device__ __forceinline__ void widen(const uint4 &v, float *f) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (kType == ROPE3D_F32) {
+            f[i] = __uint_as_float(w[i]);
+        } else if constexpr (kType == ROPE3D_BF16) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        } else {
+            __half2 h;
+            memcpy(&h, &w[i], 4);
+            const float2 t = __half22float2(h);
+            f[2 * i] = t.x;
+            f[2 * i + 1] = t.y;
+        }
+    }
+}
+
+template <int kType>
+__device__ __forceinline__ uint4 narrow(const float *f) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (kType == ROPE3D_F32) {
+            w[i] = __float_as_uint(f[i]);
+        } else if constexpr (kType == ROPE3D_BF16) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            memcpy(&w[i], &b, 4);
+        } else {
+            const __half2 b = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+            memcpy(&w[i], &b, 4);
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int kType> struct Elem { using T = float; };
+template <> struct Elem<ROPE3D_BF16> { using T = __nv_bfloat16; };
+template <> struct Elem<ROPE3D_F16> { using T = __half; };
+
+template <int kType>
+__device__ __forceinline__ float load1(const char *p) {
+    if constexpr (kType == ROPE3D_F32) return *reinterpret_cast<const float *>(p);
+    else if constexpr (kType == ROPE3D_BF16) return __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(p));
+    else return __half2float(*reinterpret_cast<const __half *>(p));
+}
+
+template <int kType>
+__device__ __forceinline__ void store1(char *p, float v) {
+    if constexpr (kType == ROPE3D_F32) *reinterpret_cast<float *>(p) = v;
+    else if constexpr (kType == ROPE3D_BF16) *reinterpret_cast<__nv_bfloat16 *>(p) = __float2bfloat16_rn(v);
+    else *reinterpret_cast<__half *>(p) = __float2half_rn(v);
+}
+
+__device__ __forceinline__ float2 rotate(float a, float b, float2 cs) {
+    return make_float2(__fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y)),
+                       __fadd_rn(__fmul_rn(a, cs.y), __fmul_rn(b, cs.x)));
+}
+
+__device__ __forceinline__ uint4 ld_stream(const char *p) {   // coherent: in place is allowed
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+    return r;
+}
+
+// One work unit of a head row: where it reads and writes, and its first pair (-1:
+// copied as it is). kHalves: the pair's second parts lie `second` bytes further on.
+struct Unit {
+    const char *src;
+    char *dst;
+    int pair;
+    const float2 *cs;
+};
+
+// ---- the kernel ------------------------------------------------------------------
+
+// kVec: units of 16 bytes (kHalves: two of them, the parts of 16 bytes' worth of
+// pairs), else single pairs and elements.
+template <int kType, bool kHalves, bool kAppend, bool kVec>
+__global__ void __launch_bounds__(kThreads) axes_kernel(const __grid_constant__ AxesParams p) {
+    constexpr int kElem = kType == ROPE3D_F32 ? 4 : 2;
+    constexpr int kV = kVec ? 16 / kElem : 1;   // elements of a vector
+    extern __shared__ float2 s_cs[];            // [tile][pairs], then freq / 2 pi as (hi, lo) [pairs]
+    float2 *s_freq = s_cs + size_t(p.tile) * p.pairs;
+    __shared__ int64_t s_dst[2][kMaxTile];      // append: byte offsets in the caches, -1: nowhere
+    __shared__ int s_place[kMaxTile], s_live[kMaxTile];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    rope3d_tc::grid_release();
+    rope3d_tc::grid_wait();
+    for (int j = tid; j < p.pairs; j += kThreads) {
+        const double f = double(p.freqs[j]) * kInvTwoPi;
+        const float hi = float(f);
+        s_freq[j] = make_float2(hi, float(f - double(hi)));
+    }
+    const int64_t second = int64_t(p.pairs) * kElem;
+
+    for (int t0 = blockIdx.x * p.tile; t0 < p.tokens; t0 += gridDim.x * p.tile) {
+        const int count = min(p.tile, p.tokens - t0);
+        __syncthreads();   // the tile before is done with shared memory; s_freq is there
+        if constexpr (kAppend) {
+            if (tid < count) {
+                const Batch &b = p.batch;
+                const int t = t0 + tid;
+                int s = 0, lo, hi, len;
+                if (b.starts) {   // the last sequence that starts at or before t
+                    int above = b.seqs;
+                    while (above - s > 1) {
+                        const int mid = (s + above) >> 1;
+                        if (b.starts[mid] <= t) s = mid;
+                        else above = mid;
+                    }
+                } else {
+                    s = t / (b.tokens / b.seqs);
+                }
+                sequence(b, s, lo, hi, len);
+                const bool live = t >= lo && t < hi;
+                const int place = len - hi + t;
+                int64_t k = -1, v = -1;
+                if (live) {
+                    const int slot_page = place < 0 ? -1 : b.table[s * b.table_stride + place / b.page_size];
+                    if (slot_page >= 0 && slot_page < b.pages) {
+                        const int slot = place % b.page_size;
+                        k = slot_page * p.page[0] + slot * p.slot[0];
+                        v = slot_page * p.page[1] + slot * p.slot[1];
+                    } else if (p.invalid) {
+                        atomicAdd(p.invalid, 1);
+                    }
+                }
+                s_dst[0][tid] = k;
+                s_dst[1][tid] = v;
+                s_place[tid] = place;
+                s_live[tid] = live;
+            }
+            __syncthreads();
+        }
+        for (int i = warp; i < count; i += kThreads / 32) {
+            if (kAppend && !s_live[i]) continue;
+            for (int j = lane; j < p.pairs; j += 32) {
+                float near;
+                double far = 0.0;
+                bool exact = true;
+                if (kAppend && p.position_type < 0) {
+                    near = float(s_place[i]);
+                    far = double(s_place[i]);
+                    exact = s_place[i] <= (1 << 24);
+                } else {
+                    exact = position(p, j < p.end0 ? 0 : j < p.end1 ? 1 : 2, t0 + i, near, far);
+                }
+                float2 cs = exact ? turn(near, s_freq[j].x, s_freq[j].y) : turn_far(far, p.freqs[j]);
+                cs.y *= p.sign;
+                s_cs[i * p.pairs + j] = cs;
+            }
+        }
+        __syncthreads();
+
+        auto locate = [&](uint32_t u, Unit &n) {
+            const uint32_t i = fdiv(u, p.per_token), r = u - i * p.per_token.d;
+            uint32_t h = fdiv(r, p.per_head);
+            const int at = int(r - h * p.per_head.d);
+            int which = 0;
+            if (int(h) >= p.heads[0]) {
+                h -= p.heads[0];
+                which = 1;
+                if (kAppend && int(h) >= p.heads[1]) {
+                    h -= p.heads[1];
+                    which = 2;
+                }
+            }
+            const bool turns = which < 2 && at < p.rotating;
+            // a unit's first element: interleaved units are in order; halves' rotating ones are
+            // the first parts, behind which come the rows' second parts
+            int64_t first;
+            if constexpr (kHalves) first = at < p.rotating ? int64_t(at) * kV : int64_t(2 * p.pairs) + int64_t(at - p.rotating) * kV;
+            else if constexpr (kVec) first = int64_t(at) * kV;
+            else first = at < p.rotating ? 2 * at : at + p.rotating;
+            const int64_t off = first * kElem;
+            const Rows &in = p.in[which], &out = p.out[which];
+            n.src = in.p + (t0 + int(i)) * in.token + h * in.head + off;
+            n.pair = turns ? (kVec && !kHalves ? at * kV / 2 : at * kV) : -1;
+            n.cs = s_cs + i * p.pairs;
+            char *base = const_cast<char *>(out.p) + h * out.head + off;
+            if constexpr (kAppend) {
+                if (!s_live[i]) return false;
+                if (which == 0) {
+                    n.dst = base + (t0 + int(i)) * out.token;
+                } else {
+                    const int64_t d = s_dst[which - 1][i];
+                    if (d < 0) return false;
+                    n.dst = base + d;
+                }
+                // a head row of V rotates nothing: its two parts are copied by the same unit
+                if (kHalves && which == 2 && at < p.rotating) n.pair = -2;
+            } else {
+                n.dst = base + (t0 + int(i)) * out.token;
+            }
+            if (!kHalves && !kVec && which == 2 && at < p.rotating) n.pair = -2;
+            return true;
+        };
+
+        const uint32_t units = uint32_t(count) * p.per_token.d;
+        for (uint32_t u0 = tid; u0 < units; u0 += kThreads * kInFlight) {
+            Unit n[kInFlight];
+            bool on[kInFlight];
+            if constexpr (kVec) {
+                uint4 a[kInFlight], b[kInFlight];
+#pragma unroll
+                for (int q = 0; q < kInFlight; ++q) {
+                    const uint32_t u = u0 + q * kThreads;
+                    on[q] = u < units && locate(u, n[q]);
+                    if (on[q]) {
+                        a[q] = ld_stream(n[q].src);
+                        if (kHalves && n[q].pair != -1) b[q] = ld_stream(n[q].src + second);
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < kInFlight; ++q) {
+                    if (!on[q]) continue;
+                    if (n[q].pair >= 0) {
+                        float x[kV], y[kV];
+                        widen<kType>(a[q], x);
+                        if constexpr (kHalves) {
+                            widen<kType>(b[q], y);
+#pragma unroll
+                            for (int e = 0; e < kV; ++e) {
+                                const float2 r = rotate(x[e], y[e], n[q].cs[n[q].pair + e]);
+                                x[e] = r.x;
+                                y[e] = r.y;
+                            }
+                            b[q] = narrow<kType>(y);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < kV; e += 2) {
+                                const float2 r = rotate(x[e], x[e + 1], n[q].cs[n[q].pair + e / 2]);
+                                x[e] = r.x;
+                                x[e + 1] = r.y;
+                            }
+                        }
+                        a[q] = narrow<kType>(x);
+                    }
+                    __stcs(reinterpret_cast<uint4 *>(n[q].dst), a[q]);
+                    if (kHalves && n[q].pair != -1) __stcs(reinterpret_cast<uint4 *>(n[q].dst + second), b[q]);
+                }
+            } else {
+                const int64_t next = kHalves ? second : kElem;
+#pragma unroll
+                for (int q = 0; q < kInFlight; ++q) {
+                    const uint32_t u = u0 + q * kThreads;
+                    if (u >= units || !locate(u, n[q])) continue;
+                    const float x = load1<kType>(n[q].src);
+                    if (n[q].pair == -1) {
+                        store1<kType>(n[q].dst, x);
+                        continue;
+                    }
+                    const float y = load1<kType>(n[q].src + next);
+                    const float2 r = n[q].pair == -2 ? make_float2(x, y) : rotate(x, y, n[q].cs[n[q].pair]);
+                    store1<kType>(n[q].dst, r.x);
+                    store1<kType>(n[q].dst + next, r.y);
+                }
+            }
+        }
+    }
+}
+
+template <bool kAppend>
+using Kernel = void (*)(AxesParams);
+
+template <bool kAppend, int kType>
+Kernel<kAppend> kernel_of(bool halves, bool vec) {
+    if (halves) return vec ? axes_kernel<kType, true, kAppend, true> : axes_kernel<kType, true, kAppend, false>;
+    return vec ? axes_kernel<kType, false, kAppend, true> : axes_kernel<kType, false, kAppend, false>;
+}
+
+// ---- host --------------------------------------------------------------------------
+
+thread_local int t_axes_kernel = 0;   // 1 vectors, 2 single pairs: this thread's last call
+
+constexpr int64_t kMaxPairs = ROPE3D_MAX_HEAD_DIM / 2;
+
+int elem_of(int32_t dtype) { return dtype == ROPE3D_F32 ? 4 : dtype == ROPE3D_BF16 || dtype == ROPE3D_F16 ? 2 : 0; }
+
+int check_rotation(const int32_t *sections, int64_t head_dim, int32_t pairing, int *pairs) {
+    int64_t n = 0;
+    for (int i = 0; i < 3; ++i) {
+        if (sections[i] < 0 || sections[i] > kMaxPairs) return ROPE3D_ERR_SHAPE;
+        n += sections[i];
+    }
+    if (n <= 0 || 2 * n > head_dim) return ROPE3D_ERR_SHAPE;
+    if (pairing != ROPE3D_PAIRS_INTERLEAVED && pairing != ROPE3D_PAIRS_HALVES) return ROPE3D_ERR_ARG;
+    *pairs = int(n);
+    return ROPE3D_OK;
+}
+
+int position_bytes(int32_t type) {
+    return type == ROPE3D_POSITIONS_I64 ? 8 : type == ROPE3D_POSITIONS_I32 || type == ROPE3D_POSITIONS_F32 ? 4 : 0;
+}
+
+View positions_view(const void *p, int32_t type, const int32_t *sections, int64_t tokens, int64_t stride) {
+    int axes = 1;   // rows that are read: up to the last axis that has pairs
+    for (int i = 1; i < 3; ++i)
+        if (sections[i]) axes = i + 1;
+    return view(p, position_bytes(type), tokens, axes, stride);
+}
+
+Rows rows_of(const void *p, int64_t token, int64_t head, int elem) {
+    return Rows{static_cast<const char *>(p), token * elem, head * elem};
+}
+
+template <bool kAppend>
+int run(AxesParams &p, int32_t dtype, bool halves, bool vec, const int32_t *sections, cudaStream_t st) {
+    const int sms = sm_count();
+    if (sms <= 0) return ROPE3D_ERR_CUDA;
+    const int v = vec ? 16 / elem_of(dtype) : 1;
+    const int rest = (p.head_dim - 2 * p.pairs) / v;   // units that are only copied
+    p.rotating = halves || !vec ? p.pairs / v : 2 * p.pairs / v;
+    const uint32_t per_head = uint32_t(p.rotating + rest);
+    p.per_head = make_fastdiv(per_head);
+    p.per_token = make_fastdiv(per_head * uint32_t(p.heads[0] + p.heads[1] + p.heads[2]));
+    p.end0 = sections[0];
+    p.end1 = sections[0] + sections[1];
+    // a tile's cos and sin: 32 KB at most, and tokens for every block while there are any
+    int tile = std::min(kMaxTile, std::max(1, 4096 / std::max(p.pairs, 1)));
+    tile = std::min(tile, std::max(1, p.tokens / (4 * sms)));
+    p.tile = tile;
+    const size_t smem = size_t(tile + 1) * p.pairs * sizeof(float2);
+    const int tiles = (p.tokens + tile - 1) / tile;
+    const Kernel<kAppend> fn = dtype == ROPE3D_BF16  ? kernel_of<kAppend, ROPE3D_BF16>(halves, vec)
+                               : dtype == ROPE3D_F16 ? kernel_of<kAppend, ROPE3D_F16>(halves, vec)
+                                                     : kernel_of<kAppend, ROPE3D_F32>(halves, vec);
+    const int rc = launch(fn, dim3(unsigned(std::min(tiles, sms * 16))), kThreads, smem, st, p);
+    if (rc == ROPE3D_OK) t_axes_kernel = vec ? 1 : 2;
+    return rc;
+}
+
+int apply(const rope3d_apply_axes_args *a, bool go, bool check_device, cudaStream_t st) {
+    if (!a || !a->q || !a->q_out || !a->positions || !a->freqs || (a->k == nullptr) != (a->k_out == nullptr))
+        return ROPE3D_ERR_NULL;
+    const int64_t T = a->tokens, D = a->head_dim, H = a->q_heads, K = a->k ? a->k_heads : 0;
+    if (T <= 0 || T > kMaxTokens || D <= 0 || D > ROPE3D_MAX_HEAD_DIM || H <= 0 || H > kMaxHeads || K < 0 || K > kMaxHeads ||
+        (a->k && K == 0))
+        return ROPE3D_ERR_SHAPE;
+    const int es = elem_of(a->dtype);
+    if (!es || !position_bytes(a->position_type)) return ROPE3D_ERR_DTYPE;
+    AxesParams p{};
+    int rc = check_rotation(a->sections, D, a->pairing, &p.pairs);
+    if (rc != ROPE3D_OK) return rc;
+    const View q = view(a->q, es, D, T, a->q_token_stride, H, a->q_head_stride);
+    const View k = view(a->k, es, D, T, a->k_token_stride, K, a->k_head_stride);
+    const View qo = view(a->q_out, es, D, T, a->q_out_token_stride, H, a->q_out_head_stride);
+    const View ko = view(a->k_out, es, D, T, a->k_out_token_stride, K, a->k_out_head_stride);
+    const View pos = positions_view(a->positions, a->position_type, a->sections, T, a->positions_stride);
+    const View freqs = view(a->freqs, 4, p.pairs, 1, 0);
+    if (bad_strides(q) || bad_strides(qo) || (a->k && (bad_strides(k) || bad_strides(ko))) || bad_strides(pos)) return ROPE3D_ERR_SHAPE;
+    if (!rows_apart(qo) || (a->k && !rows_apart(ko))) return ROPE3D_ERR_SHAPE;
+    for (const View *v : {&q, &k, &qo, &ko, &pos, &freqs})
+        if (!aligned(v->p, v->elem)) return ROPE3D_ERR_ALIGN;
+    for (const View *out : {&qo, &ko}) {
+        const View &own = out == &qo ? q : k, &other = out == &qo ? k : q;
+        if (may_meet(*out, own) && !same_view(*out, own)) return ROPE3D_ERR_ALIAS;
+        if (may_meet(*out, other) || may_meet(*out, pos) || may_meet(*out, freqs)) return ROPE3D_ERR_ALIAS;
+    }
+    if (may_meet(qo, ko)) return ROPE3D_ERR_ALIAS;
+    if (check_device) {
+        const void *const all[] = {a->q, a->k, a->q_out, a->k_out, a->positions, a->freqs};
+        if ((rc = on_current_device(all, 6)) != ROPE3D_OK) return rc;
+    }
+    if (!go) return ROPE3D_OK;
+    const bool halves = a->pairing == ROPE3D_PAIRS_HALVES;
+    const int v = 16 / es;
+    const bool vec = vectors(q) && vectors(qo) && vectors(k) && vectors(ko) && (halves ? p.pairs : 2 * p.pairs) % v == 0;
+    p.in[0] = rows_of(a->q, a->q_token_stride, a->q_head_stride, es);
+    p.in[1] = rows_of(a->k, a->k_token_stride, a->k_head_stride, es);
+    p.out[0] = rows_of(a->q_out, a->q_out_token_stride, a->q_out_head_stride, es);
+    p.out[1] = rows_of(a->k_out, a->k_out_token_stride, a->k_out_head_stride, es);
+    p.positions = a->positions;
+    p.positions_stride = a->positions_stride;
+    p.position_type = a->position_type;
+    p.freqs = static_cast<const float *>(a->freqs);
+    p.tokens = int(T);
+    p.head_dim = int(D);
+    p.heads[0] = int(H);
+    p.heads[1] = int(K);
+    p.sign = a->inverse ? -1.0f : 1.0f;
+    return run<false>(p, a->dtype, halves, vec, a->sections, st);
+}
+
+int append(const rope3d_cache_append_args *a, bool go, bool check_device, cudaStream_t st) {
+    if (!a || !a->k || !a->v || !a->k_cache || !a->v_cache || (a->q == nullptr) != (a->q_out == nullptr))
+        return ROPE3D_ERR_NULL;
+    const rope3d_paged_batch &b = a->batch;
+    const int64_t T = a->tokens, D = a->head_dim, H = a->q ? a->q_heads : 0, K = a->kv_heads;
+    if (T <= 0 || T > kMaxTokens || D <= 0 || D > ROPE3D_MAX_HEAD_DIM || H < 0 || H > kMaxHeads || K <= 0 || K > kMaxHeads ||
+        (a->q && H == 0))
+        return ROPE3D_ERR_SHAPE;
+    int rc = check_batch(b, T);
+    if (rc != ROPE3D_OK) return rc;
+    const int es = elem_of(a->dtype);
+    if (!es || (a->positions && !position_bytes(a->position_type))) return ROPE3D_ERR_DTYPE;
+    AxesParams p{};
+    if (a->freqs) {
+        if ((rc = check_rotation(a->sections, D, a->pairing, &p.pairs)) != ROPE3D_OK) return rc;
+    } else if (a->q || a->positions) {
+        return ROPE3D_ERR_ARG;   // nothing to rotate by
+    }
+    const View q = view(a->q, es, D, T, a->q_token_stride, H, a->q_head_stride);
+    const View qo = view(a->q_out, es, D, T, a->q_out_token_stride, H, a->q_out_head_stride);
+    const View k = view(a->k, es, D, T, a->k_token_stride, K, a->k_head_stride);
+    const View v = view(a->v, es, D, T, a->v_token_stride, K, a->v_head_stride);
+    const View kc = view(a->k_cache, es, D, b.pages, a->k_page_stride, b.page_size, a->k_slot_stride, K, a->k_cache_head_stride);
+    const View vc = view(a->v_cache, es, D, b.pages, a->v_page_stride, b.page_size, a->v_slot_stride, K, a->v_cache_head_stride);
+    const View pos = a->positions ? positions_view(a->positions, a->position_type, a->sections, T, a->positions_stride)
+                                  : View{nullptr, 1, {1, 1, 1}, {0, 0, 0}, 4};
+    const View freqs = view(a->freqs, 4, std::max(p.pairs, 1), 1, 0);
+    const View table = view(b.page_table, 4, b.table_width, b.seqs, b.table_stride), lens = view(b.seq_lens, 4, b.seqs, 1, 0),
+               starts = view(b.q_starts, 4, b.seqs + 1, 1, 0), bad = view(a->invalid_count, 4, 1, 1, 0);
+    for (const View *w : {&q, &qo, &k, &v, &kc, &vc, &pos})
+        if (w->p && bad_strides(*w)) return ROPE3D_ERR_SHAPE;
+    if ((a->q && !rows_apart(qo)) || !rows_apart(kc) || !rows_apart(vc)) return ROPE3D_ERR_SHAPE;
+    for (const View *w : {&q, &qo, &k, &v, &kc, &vc, &pos, &freqs, &bad})
+        if (!aligned(w->p, w->elem)) return ROPE3D_ERR_ALIGN;
+    if (may_meet(qo, q) && !same_view(qo, q)) return ROPE3D_ERR_ALIAS;
+    for (const View *out : {&qo, &kc, &vc, &bad}) {
+        if (out != &qo && may_meet(*out, q)) return ROPE3D_ERR_ALIAS;
+        for (const View *in : {&k, &v, &pos, &freqs, &table, &lens, &starts})
+            if (may_meet(*out, *in)) return ROPE3D_ERR_ALIAS;
+    }
+    if (may_meet(qo, kc) || may_meet(qo, vc) || may_meet(kc, vc) || may_meet(bad, qo) || may_meet(bad, kc) || may_meet(bad, vc))
+        return ROPE3D_ERR_ALIAS;
+    if (check_device) {
+        const void *const all[] = {a->q, a->q_out, a->k, a->v, a->k_cache, a->v_cache, a->positions, a->freqs,
+                                   b.page_table, b.seq_lens, b.q_starts, a->invalid_count};
+        if ((rc = on_current_device(all, 12)) != ROPE3D_OK) return rc;
+    }
+    if (!go) return ROPE3D_OK;
+    const bool halves = a->freqs && a->pairing == ROPE3D_PAIRS_HALVES;
+    const int n = 16 / es;
+    const bool vec = vectors(q) && vectors(qo) && vectors(k) && vectors(v) && vectors(kc) && vectors(vc) &&
+                     (halves ? p.pairs : 2 * p.pairs) % n == 0;
+    p.in[0] = rows_of(a->q, a->q_token_stride, a->q_head_stride, es);
+    p.in[1] = rows_of(a->k, a->k_token_stride, a->k_head_stride, es);
+    p.in[2] = rows_of(a->v, a->v_token_stride, a->v_head_stride, es);
+    p.out[0] = rows_of(a->q_out, a->q_out_token_stride, a->q_out_head_stride, es);
+    p.out[1] = rows_of(a->k_cache, 0, a->k_cache_head_stride, es);
+    p.out[2] = rows_of(a->v_cache, 0, a->v_cache_head_stride, es);
+    p.page[0] = a->k_page_stride * es;
+    p.page[1] = a->v_page_stride * es;
+    p.slot[0] = a->k_slot_stride * es;
+    p.slot[1] = a->v_slot_stride * es;
+    p.positions = a->positions;
+    p.positions_stride = a->positions_stride;
+    p.position_type = a->positions ? a->position_type : -1;
+    p.freqs = static_cast<const float *>(a->freqs);   // (none: no pairs, and none is read)
+    p.invalid = a->invalid_count;
+    p.batch = device_batch(b, T);
+    p.tokens = int(T);
+    p.head_dim = int(D);
+    p.heads[0] = int(H);
+    p.heads[1] = p.heads[2] = int(K);
+    p.sign = 1.0f;
+    const int32_t none[3] = {0, 0, 0};
+    return run<true>(p, a->dtype, halves, vec, a->freqs ? a->sections : none, st);
+}
+
+}  // namespace
+
+extern "C" int rope3d_apply_axes(const rope3d_apply_axes_args *args, void *stream) {
+    return apply(args, true, true, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int rope3d_apply_axes_check(const rope3d_apply_axes_args *args, int32_t check_device) {
+    return apply(args, false, check_device != 0, nullptr);
+}
+
+extern "C" int rope3d_cache_append(const rope3d_cache_append_args *args, void *stream) {
+    return append(args, true, true, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int rope3d_cache_append_check(const rope3d_cache_append_args *args, int32_t check_device) {
+    return append(args, false, check_device != 0, nullptr);
+}
+
+extern "C" int rope3d_apply_axes_last_kernel(void) { return t_axes_kernel; }

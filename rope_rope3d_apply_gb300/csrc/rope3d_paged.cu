@@ -1,0 +1,598 @@
+// rope3d_paged.cu -- attention of new tokens over the pages of a cache:
+// rope3d_paged_attention, its kernel for few query rows and the kernel that adds
+// partial results. (rope3d_paged_tc.cu has the kernel for many rows, rope3d_paged.cuh
+// the division of the work.)
+//
+//     out_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i . k_j - m_i)
+// in one pass over the keys, with the maximum m_i so far: where it moves, the sums so
+// far are multiplied by exp(old - new).
+//
+// Few rows (one new token of a sequence and the query heads that share its keys): reading
+// the cache is all there is, 1 to 16 rows to 2 bytes an element. Every warp streams
+// places of its own through its own ring of shared memory (16 of every 64, by
+// 16-byte cp.async copies, rows outside the mask filled with zeros and not read) and
+// keeps a maximum, a sum and sums of V of its own, so that warps meet only at an
+// item's end. Products are warp MMAs (m16n8k16): at 16 rows the tensor cores have
+// next to nothing to do, and fragments come straight from the swizzled ring.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/rope3d.h"
+#include "rope3d_internal.h"
+#include "rope3d_paged.cuh"
+#include "rope3d_paged.h"
+#include "rope3d_tc.cuh"
+
+namespace {
+
+using namespace rope3d_paged;
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kWarpKeys = 16;                    // places of a block that one warp takes
+constexpr int kKeys = kWarpKeys * kWarps;        // places of a block
+constexpr int kRows = kFewRows;
+
+// Stages of a warp's ring, and blocks that fit an SM beside one another with them.
+template <int kD> constexpr int kStagesOf = kD == 64 ? 4 : 3;
+template <int kD> constexpr int kPerSm = kD == 256 ? 1 : kD == 128 ? 2 : 3;
+template <int kD> constexpr int kStageBytes = 2 * kWarpKeys * kD * 2;   // K, then V
+template <int kD> constexpr int kSmemBytes = kRows * kD * 2 + kWarps * kStagesOf<kD> * kStageBytes<kD>;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+template <bool kF16>
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (kF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <bool kF16>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+    uint32_t w;
+    if constexpr (kF16) {
+        const __half2 h = __floats2half2_rn(x, y);
+        memcpy(&w, &h, 4);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        memcpy(&w, &h, 4);
+    }
+    return w;
+}
+
+// Byte offset of 16-byte chunk c of row r in a tile of rows of kD elements: chunks
+// permuted within 128 bytes by the row, so that eight rows' chunks lie in
+// eight different bank groups.
+template <int kD>
+__device__ __forceinline__ uint32_t at(int r, int c) { return uint32_t(r * kD * 2 + ((c ^ (r & 7)) << 4)); }
+
+// log sum exp in base e of a row with maximum m (base 2) and sum l.
+__device__ __forceinline__ float lse_of(float m, float l) {
+    return l > 0.f ? (m + log2f(l)) * 0.69314718f : -INFINITY;
+}
+
+// Four results of a row, rounded.
+template <bool kF16>
+__device__ __forceinline__ void store4(char *to, float4 v, float inv) {
+    *reinterpret_cast<uint2 *>(to) = make_uint2(pack2<kF16>(v.x * inv, v.y * inv), pack2<kF16>(v.z * inv, v.w * inv));
+}
+
+template <bool kF16, int kD>
+__global__ void __launch_bounds__(kThreads) paged_rows_kernel(const __grid_constant__ AttnParams p) {
+    constexpr int kStages = kStagesOf<kD>, kChunks = kD / 8, kPass = 32 / kChunks;   // rows that the warp copies at once
+    constexpr int kHalf = kWarpKeys * kD * 2;   // bytes of a stage's K
+    extern __shared__ __align__(128) char sm[];
+    __shared__ Start s_start;
+    __shared__ long long s_sums[kWarps];
+    __shared__ uint32_t s_live[kWarps][kStages];
+    __shared__ float s_max[kWarps][kRows], s_sum[kWarps][kRows];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = lane >> 2, col = lane & 3;
+    const uint32_t sq = rope3d_tc::smem_u32(sm);
+    char *ring = sm + kRows * kD * 2 + warp * kStages * kStageBytes<kD>;
+    const uint32_t sring = rope3d_tc::smem_u32(ring);
+
+    rope3d_tc::grid_release();
+    rope3d_tc::grid_wait();
+    find_start<kRows, kKeys, kThreads>(p, blockIdx.x, &s_start, s_sums);
+    const Start st = s_start;
+    if (tid == 0) write_note<kRows, kKeys>(p, blockIdx.x, st);
+    const int chunks = p.head_dim / 8;
+
+    Walker<kRows, kKeys> walk(p, st);
+    Item it;
+    while (walk.next(it)) {
+        const int steps = it.end - it.begin;
+        const char *kbase = p.k + it.h * p.k_head, *vbase = p.v + it.h * p.v_head;
+        const int *table = p.batch.table + it.s * p.batch.table_stride;
+        const int place0 = it.begin * kKeys + warp * kWarpKeys;
+
+        // the page of this lane's place of a step (lanes 0-15); -1 where no row sees it
+        auto page_of = [&](int step) {
+            const int place = place0 + step * kKeys + (lane & 15);
+            int page = -1;
+            if (step < steps && place >= it.tile.k0 && place < it.tile.k1) page = table[place / p.batch.page_size];
+            return page;
+        };
+        auto issue = [&](int step, int page) {
+            const int slot_of = (place0 + step * kKeys + (lane & 15)) % p.batch.page_size;
+            const bool live = page >= 0 && page < p.batch.pages;
+            const uint32_t all = __ballot_sync(0xffffffffu, live) & 0xffffu;
+            const int slot = step % kStages;
+            if (lane == 0) s_live[warp][slot] = all;
+            if (step < steps) {
+                const int64_t ko = live ? page * p.k_page + slot_of * p.k_slot : 0;
+                const int64_t vo = live ? page * p.v_page + slot_of * p.v_slot : 0;
+                const uint32_t dst = sring + slot * kStageBytes<kD>;
+                const int c = lane % kChunks;
+#pragma unroll
+                for (int i = 0; i < kWarpKeys / kPass; ++i) {
+                    const int r = i * kPass + lane / kChunks;
+                    const bool on = (all >> r & 1u) && c < chunks;
+                    const int64_t off = __shfl_sync(0xffffffffu, ko, r);
+                    copy16(dst + at<kD>(r, c), kbase + (on ? off + c * 16 : 0), on);
+                }
+#pragma unroll
+                for (int i = 0; i < kWarpKeys / kPass; ++i) {
+                    const int r = i * kPass + lane / kChunks;
+                    const bool on = (all >> r & 1u) && c < chunks;
+                    const int64_t off = __shfl_sync(0xffffffffu, vo, r);
+                    copy16(dst + kHalf + at<kD>(r, c), vbase + (on ? off + c * 16 : 0), on);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+
+        int page = page_of(0);
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) {
+            const int after = page_of(i + 1);
+            issue(i, page);
+            page = after;
+        }
+
+        // the rows of q, behind one another, zeros past head_dim and past the item
+        __syncthreads();   // the item before is done with shared memory
+        for (int i = tid; i < kRows * kChunks; i += kThreads) {
+            const int r = i / kChunks, c = i % kChunks;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (r < it.rows && c < chunks) {
+                const RowOf o = row_of<kRows>(p, it, r);
+                v = *reinterpret_cast<const uint4 *>(p.q + o.token * p.q_token + o.head * p.q_head + c * 16);
+            }
+            *reinterpret_cast<uint4 *>(sm + at<kD>(r, c)) = v;
+        }
+        __syncthreads();
+        constexpr bool kKeepQ = kD <= 128;   // q's fragments in registers
+        uint32_t qf[kKeepQ ? kD / 16 : 1][4];
+        const int qr = (lane & 7) + (lane & 8), qc = lane >> 4;
+        if constexpr (kKeepQ) {
+#pragma unroll
+            for (int k = 0; k < kD / 16; ++k) ldm4(qf[k], sq + at<kD>(qr, 2 * k + qc));
+        }
+        const RowOf r0 = row_of<kRows>(p, it, quad), r1 = row_of<kRows>(p, it, quad + 8);
+
+        float o[kD / 8][4];
+#pragma unroll
+        for (int i = 0; i < kD / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+
+        for (int step = 0; step < steps; ++step) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+            __syncwarp();
+            const int slot = step % kStages;
+            const uint32_t sk = sring + slot * kStageBytes<kD>, sv = sk + kHalf;
+            const uint32_t live = s_live[warp][slot];
+            if (live) {
+                float sa[2][4] = {}, sb[2][4] = {};   // even and odd k: chains half as long
+#pragma unroll
+                for (int k = 0; k < kD / 16; ++k) {
+                    uint32_t b[4], a[4];
+                    ldm4(b, sk + at<kD>((lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
+                    if constexpr (kKeepQ) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) a[e] = qf[k][e];
+                    } else {
+                        ldm4(a, sq + at<kD>(qr, 2 * k + qc));
+                    }
+                    mma16<kF16>(k & 1 ? sb[0] : sa[0], a, b[0], b[1]);
+                    mma16<kF16>(k & 1 ? sb[1] : sa[1], a, b[2], b[3]);
+                }
+                float s[2][4], x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int key = n * 8 + col * 2 + (e & 1), place = place0 + step * kKeys + key;
+                        const RowOf &r = e < 2 ? r0 : r1;
+                        const bool sees = (live >> key & 1u) && place >= r.lo && place < r.hi;
+                        s[n][e] = sees ? (sa[n][e] + sb[n][e]) * p.scale_log2 : -INFINITY;
+                        if (e < 2) x0 = fmaxf(x0, s[n][e]);
+                        else x1 = fmaxf(x1, s[n][e]);
+                    }
+                x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
+                x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
+                x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
+                x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
+                const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+                const float z0 = n0 == -INFINITY ? 0.f : n0, z1 = n1 == -INFINITY ? 0.f : n1;
+                if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
+                    const float f0 = ex2(m0 - z0), f1 = ex2(m1 - z1);
+                    l0 *= f0;
+                    l1 *= f1;
+#pragma unroll
+                    for (int i = 0; i < kD / 8; ++i) {
+                        o[i][0] *= f0;
+                        o[i][1] *= f0;
+                        o[i][2] *= f1;
+                        o[i][3] *= f1;
+                    }
+                    m0 = n0;
+                    m1 = n1;
+                }
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        s[n][e] = ex2(s[n][e] - (e < 2 ? z0 : z1));
+                        if (e < 2) l0 += s[n][e];
+                        else l1 += s[n][e];
+                    }
+                const uint32_t pa[4] = {pack2<kF16>(s[0][0], s[0][1]), pack2<kF16>(s[0][2], s[0][3]),
+                                        pack2<kF16>(s[1][0], s[1][1]), pack2<kF16>(s[1][2], s[1][3])};
+#pragma unroll
+                for (int i = 0; i < kD / 16; ++i) {
+                    uint32_t b[4];
+                    ldm4t(b, sv + at<kD>((lane & 7) + (lane & 8), 2 * i + (lane >> 4)));
+                    mma16<kF16>(o[2 * i], pa, b[0], b[1]);
+                    mma16<kF16>(o[2 * i + 1], pa, b[2], b[3]);
+                }
+            }
+            __syncwarp();
+            const int after = page_of(step + kStages);
+            issue(step + kStages - 1, page);
+            page = after;
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+
+        // the warps' results joined: by each row's greatest maximum, in the warps' order
+        l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+        l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+        if (col == 0) {
+            s_max[warp][quad] = m0;
+            s_max[warp][quad + 8] = m1;
+            s_sum[warp][quad] = l0;
+            s_sum[warp][quad + 8] = l1;
+        }
+        __syncthreads();
+        float g0 = s_max[0][quad], g1 = s_max[0][quad + 8];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) {
+            g0 = fmaxf(g0, s_max[w][quad]);
+            g1 = fmaxf(g1, s_max[w][quad + 8]);
+        }
+        const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - g0), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - g1);
+        float *mine = reinterpret_cast<float *>(ring);
+        constexpr int kLd = kD + 8;   // floats between rows: quads of rows in different banks
+        static_assert(kRows * kLd * 4 <= kStagesOf<kD> * kStageBytes<kD>, "a warp's sums fit its ring");
+#pragma unroll
+        for (int i = 0; i < kD / 8; ++i) {
+            *reinterpret_cast<float2 *>(mine + quad * kLd + i * 8 + col * 2) = make_float2(o[i][0] * f0, o[i][1] * f0);
+            *reinterpret_cast<float2 *>(mine + (quad + 8) * kLd + i * 8 + col * 2) = make_float2(o[i][2] * f1, o[i][3] * f1);
+        }
+        __syncthreads();
+        float *slot = slot_of<kRows>(p, blockIdx.x, it.head);
+        const int vecs = p.head_dim / 4;
+        for (int i = tid; i < it.rows * vecs; i += kThreads) {
+            const int r = i / vecs, c = i % vecs;
+            float big = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) big = fmaxf(big, s_max[w][r]);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float4 x = *reinterpret_cast<const float4 *>(
+                    reinterpret_cast<const float *>(sm + kRows * kD * 2 + w * kStages * kStageBytes<kD>) + r * kLd + c * 4);
+                v.x += x.x;
+                v.y += x.y;
+                v.z += x.z;
+                v.w += x.w;
+                if (s_max[w][r] != -INFINITY) sum += s_sum[w][r] * ex2(s_max[w][r] - big);
+            }
+            if (it.whole) {
+                const RowOf row = row_of<kRows>(p, it, r);
+                store4<kF16>(p.out + row.token * p.out_token + row.head * p.out_head + c * 8, v, sum > 0.f ? 1.f / sum : sum);
+                if (c == 0 && p.lse) p.lse[row.token * p.lse_token + row.head] = lse_of(big, sum);
+            } else {
+                *reinterpret_cast<float4 *>(slot + (c * kRows + r) * 4) = v;
+                if (c == 0) {
+                    slot[vecs * kRows * 4 + r] = big;
+                    slot[vecs * kRows * 4 + kRows + r] = sum;
+                }
+            }
+        }
+    }
+}
+
+// ---- partial results ---------------------------------------------------------------
+
+constexpr int kJoinThreads = 512, kJoinRows = 16;
+
+// Block (c, y): if the cut at the beginning of part c is the first one in an item,
+// that item's rows 16 y .. 16 y + 15 from all parts that computed some of it, in
+// order. Where there are fewer vectors than threads, threads share a vector's parts.
+template <bool kF16, int kTile, int kKeysOf>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ AttnParams p) {
+    __shared__ float4 s_v[kJoinThreads];
+    __shared__ float s_l[kJoinThreads], s_m[kJoinThreads];
+    rope3d_tc::grid_release();
+    rope3d_tc::grid_wait();
+    const int c = blockIdx.x, tid = threadIdx.x;
+    const PartNote n = p.notes[c];
+    if (n.begin == n.end || n.begin == n.item) return;
+    int from = c - 1;   // the part before: the item's first part, or the cut is not its first
+    while (from > 0 && p.notes[from].begin == p.notes[from].end) --from;
+    if (p.notes[from].begin > n.item) return;
+    int to = c + 1;     // the parts of the item: from, c .. to - 1
+    while (to < p.parts && p.notes[to].begin < n.item + n.cost) ++to;
+
+    Item it;
+    it.s = n.s;
+    it.h = n.h;
+    it.t = n.t;
+    it.q = seq_of<kTile>(p, n.s);
+    it.rows = int(min(uint32_t(kTile), uint32_t(it.q.n) * p.group.d - uint32_t(n.t) * kTile));
+    const int row0 = blockIdx.y * kJoinRows, rows = min(kJoinRows, it.rows - row0);
+    if (rows <= 0) return;
+    const int vecs = p.head_dim / 4, count = rows * vecs, parts = to - c + 1;
+    int shares = 1;     // threads to a vector
+    while (2 * shares * count <= kJoinThreads && 2 * shares <= parts) shares *= 2;
+    for (int i0 = 0; i0 < count; i0 += kJoinThreads / shares) {
+        const int i = i0 + tid / shares, share = tid % shares;
+        const bool on = i < count;
+        const int r = on ? row0 + i % rows : row0, v4 = on ? i / rows : 0;
+        float m = -INFINITY, l = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (on) {
+            for (int k0 = share; k0 < parts; k0 += 4 * shares) {   // four parts' loads at a time
+                float pm[4], pl[4];
+                float4 pv[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int k = k0 + j * shares, part = k == 0 ? from : c + k - 1;
+                    pm[j] = -INFINITY;
+                    if (k >= parts || p.notes[part].begin == p.notes[part].end) continue;
+                    const float *slot = slot_of<kTile>(p, part, p.notes[part].begin > n.item);
+                    pm[j] = slot[vecs * kTile * 4 + r];
+                    pl[j] = slot[vecs * kTile * 4 + kTile + r];
+                    pv[j] = *reinterpret_cast<const float4 *>(slot + (v4 * kTile + r) * 4);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (pm[j] == -INFINITY) continue;
+                    const float big = fmaxf(m, pm[j]), a = m == -INFINITY ? 0.f : ex2(m - big), b = ex2(pm[j] - big);
+                    v.x = v.x * a + pv[j].x * b;
+                    v.y = v.y * a + pv[j].y * b;
+                    v.z = v.z * a + pv[j].z * b;
+                    v.w = v.w * a + pv[j].w * b;
+                    l = l * a + pl[j] * b;
+                    m = big;
+                }
+            }
+        }
+        if (shares > 1) {
+            __syncthreads();
+            s_v[tid] = v;
+            s_l[tid] = l;
+            s_m[tid] = m;
+            __syncthreads();
+            if (share == 0) {
+                for (int j = 1; j < shares; ++j) {
+                    const float pm = s_m[tid + j];
+                    if (pm == -INFINITY) continue;
+                    const float big = fmaxf(m, pm), a = m == -INFINITY ? 0.f : ex2(m - big), b = ex2(pm - big);
+                    const float4 x = s_v[tid + j];
+                    v.x = v.x * a + x.x * b;
+                    v.y = v.y * a + x.y * b;
+                    v.z = v.z * a + x.z * b;
+                    v.w = v.w * a + x.w * b;
+                    l = l * a + s_l[tid + j] * b;
+                    m = big;
+                }
+            }
+        }
+        if (on && share == 0) {
+            const RowOf row = row_of<kTile>(p, it, r);
+            store4<kF16>(p.out + row.token * p.out_token + row.head * p.out_head + v4 * 8, v, l > 0.f ? 1.f / l : l);
+            if (v4 == 0 && p.lse) p.lse[row.token * p.lse_token + row.head] = lse_of(m, l);
+        }
+    }
+}
+
+// ---- host --------------------------------------------------------------------------
+
+thread_local int t_paged_kernel = 0;   // 1 few rows, 2 tiles
+
+template <bool kF16, int kD>
+int launch_rows(const AttnParams &p, cudaStream_t st) {
+    static std::atomic<bool> ready[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return ROPE3D_ERR_CUDA;
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(paged_rows_kernel<kF16, kD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<kD>) !=
+            cudaSuccess) {
+            cudaGetLastError();
+            return ROPE3D_ERR_CUDA;
+        }
+        ready[dev].store(true, std::memory_order_release);
+    }
+    return launch(paged_rows_kernel<kF16, kD>, dim3(unsigned(p.parts)), kThreads, kSmemBytes<kD>, st, p);
+}
+
+template <bool kF16>
+int launch_rows(const AttnParams &p, cudaStream_t st) {
+    if (p.head_dim <= 64) return launch_rows<kF16, 64>(p, st);
+    return p.head_dim <= 128 ? launch_rows<kF16, 128>(p, st) : launch_rows<kF16, 256>(p, st);
+}
+
+int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
+
+// How a call is computed: the kernel, its parts and its workspace.
+struct Choice {
+    bool tiles;
+    int parts;
+    int64_t slots, bytes;
+};
+
+Choice choose(const rope3d_paged_attention_args &a) {
+    const rope3d_paged_batch &b = a.batch;
+    const int64_t group = a.q_heads / a.kv_heads;
+    int64_t most = b.q_starts ? a.tokens : a.tokens / b.seqs;
+    if (a.max_new) most = std::min(most, a.max_new);
+    Choice c{};
+    c.tiles = most * group > kFewRows && tiles_fit(a);
+    const int64_t rows = c.tiles ? kTileRows : kFewRows, keys = c.tiles ? 128 : kKeys;
+    const int limit = c.tiles ? kTileParts : 152 * (a.head_dim <= 64 ? kPerSm<64> : a.head_dim <= 128 ? kPerSm<128> : kPerSm<256>);
+    // no more parts than blocks there can be
+    const int64_t items = (a.tokens * group + rows - 1) / rows + std::min(b.seqs, a.tokens);
+    const int64_t blocks = (b.table_width * b.page_size + keys - 1) / keys;
+    const int64_t most_blocks = items > limit || blocks > limit ? limit : items * blocks * a.kv_heads;
+    c.parts = int(std::min<int64_t>(limit, most_blocks));
+    c.slots = up256(int64_t(c.parts) * int64_t(sizeof(PartNote)));
+    const int64_t floats = c.tiles ? slot_floats<kTileRows>(int(a.head_dim)) : slot_floats<kFewRows>(int(a.head_dim));
+    c.bytes = c.slots + up256(2 * c.parts * floats * 4);
+    return c;
+}
+
+int attention(const rope3d_paged_attention_args *a, bool go, bool check_device, int64_t *need, cudaStream_t st) {
+    if (!a || !a->q || !a->k_cache || !a->v_cache || !a->out) return ROPE3D_ERR_NULL;
+    const rope3d_paged_batch &b = a->batch;
+    const int64_t T = a->tokens, H = a->q_heads, K = a->kv_heads, D = a->head_dim;
+    if (T <= 0 || T > kMaxTokens || H <= 0 || H > kMaxHeads || K <= 0 || K > H || H % K != 0 || D <= 0 || D > 256 || D % 8 != 0 ||
+        T * H > 0x7fffffff)
+        return ROPE3D_ERR_SHAPE;
+    int rc = check_batch(b, T);
+    if (rc != ROPE3D_OK) return rc;
+    if (a->dtype != ROPE3D_BF16 && a->dtype != ROPE3D_F16) return ROPE3D_ERR_DTYPE;
+    const float scale = float(a->scale * 1.4426950408889634);
+    if (!(scale > 0.f) || !std::isfinite(scale) || (a->causal != 0 && a->causal != 1) || a->window < 0 || a->max_new < 0)
+        return ROPE3D_ERR_ARG;
+    const View q = view(a->q, 2, D, T, a->q_token_stride, H, a->q_head_stride);
+    const View out = view(a->out, 2, D, T, a->out_token_stride, H, a->out_head_stride);
+    const View k = view(a->k_cache, 2, D, b.pages, a->k_page_stride, b.page_size, a->k_slot_stride, K, a->k_cache_head_stride);
+    const View v = view(a->v_cache, 2, D, b.pages, a->v_page_stride, b.page_size, a->v_slot_stride, K, a->v_cache_head_stride);
+    const View lse = view(a->lse, 4, H, T, a->lse_stride);
+    const View table = view(b.page_table, 4, b.table_width, b.seqs, b.table_stride), lens = view(b.seq_lens, 4, b.seqs, 1, 0),
+               starts = view(b.q_starts, 4, b.seqs + 1, 1, 0);
+    if (bad_strides(q) || bad_strides(out) || bad_strides(k) || bad_strides(v) || !rows_apart(out) ||
+        (a->lse && (bad_strides(lse) || !rows_apart(lse))))
+        return ROPE3D_ERR_SHAPE;
+    if (!vectors(q) || !vectors(out) || !vectors(k) || !vectors(v) || !aligned(a->lse, 4)) return ROPE3D_ERR_ALIGN;
+    const Choice c = choose(*a);
+    if (need) *need = c.bytes;
+    else if (!a->workspace) return ROPE3D_ERR_NULL;
+    else if (a->workspace_bytes < c.bytes) return ROPE3D_ERR_SCRATCH;
+    if (!need && !aligned(a->workspace, 256)) return ROPE3D_ERR_ALIGN;
+    const View ws{need ? nullptr : a->workspace, c.bytes, {1, 1, 1}, {0, 0, 0}, 1};
+    for (const View *o : {&out, &lse, &ws})
+        for (const View *in : {&q, &k, &v, &table, &lens, &starts})
+            if (may_meet(*o, *in)) return ROPE3D_ERR_ALIAS;
+    if (may_meet(out, lse) || may_meet(out, ws) || may_meet(lse, ws)) return ROPE3D_ERR_ALIAS;
+    if (check_device) {
+        const void *const all[] = {a->q, a->k_cache, a->v_cache, a->out, a->lse, b.page_table, b.seq_lens, b.q_starts, a->workspace};
+        if ((rc = on_current_device(all, 9)) != ROPE3D_OK) return rc;
+    }
+    if (need || !go) return ROPE3D_OK;
+
+    AttnParams p{};
+    p.q = static_cast<const char *>(a->q);
+    p.k = static_cast<const char *>(a->k_cache);
+    p.v = static_cast<const char *>(a->v_cache);
+    p.out = static_cast<char *>(a->out);
+    p.lse = a->lse;
+    p.batch = device_batch(b, T);
+    p.group = rope3d::make_fastdiv(uint32_t(H / K));
+    p.kv_heads = int(K);
+    p.head_dim = int(D);
+    p.causal = a->causal;
+    p.window = int(std::min<int64_t>(a->window, kMaxPlaces));   // a longer one leaves nothing out
+    if (a->window > kMaxPlaces) p.window = 0;
+    p.q_token = a->q_token_stride * 2;
+    p.q_head = a->q_head_stride * 2;
+    p.out_token = a->out_token_stride * 2;
+    p.out_head = a->out_head_stride * 2;
+    p.lse_token = a->lse_stride;
+    p.k_page = a->k_page_stride * 2;
+    p.k_slot = a->k_slot_stride * 2;
+    p.k_head = a->k_cache_head_stride * 2;
+    p.v_page = a->v_page_stride * 2;
+    p.v_slot = a->v_slot_stride * 2;
+    p.v_head = a->v_cache_head_stride * 2;
+    p.scale_log2 = scale;
+    p.parts = c.parts;
+    p.notes = static_cast<PartNote *>(a->workspace);
+    p.partial = reinterpret_cast<float *>(static_cast<char *>(a->workspace) + c.slots);
+    const bool f16 = a->dtype == ROPE3D_F16;
+    if (c.tiles) rc = launch_tiles(p, *a, st);
+    else rc = f16 ? launch_rows<true>(p, st) : launch_rows<false>(p, st);
+    if (rc != ROPE3D_OK) return rc;
+    t_paged_kernel = c.tiles ? 2 : 1;
+    const dim3 grid(unsigned(c.parts), unsigned((c.tiles ? kTileRows : kFewRows) / kJoinRows));
+    auto *join = c.tiles ? (f16 ? paged_join_kernel<true, kTileRows, 128> : paged_join_kernel<false, kTileRows, 128>)
+                         : (f16 ? paged_join_kernel<true, kFewRows, kKeys> : paged_join_kernel<false, kFewRows, kKeys>);
+    return launch(join, grid, kJoinThreads, 0, st, p);
+}
+
+}  // namespace
+
+extern "C" int rope3d_paged_attention(const rope3d_paged_attention_args *args, void *stream) {
+    return attention(args, true, true, nullptr, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int rope3d_paged_attention_check(const rope3d_paged_attention_args *args, int32_t check_device) {
+    return attention(args, false, check_device != 0, nullptr, nullptr);
+}
+
+extern "C" int rope3d_paged_attention_workspace(const rope3d_paged_attention_args *args, int64_t *bytes) {
+    if (!bytes) return ROPE3D_ERR_NULL;
+    return attention(args, false, false, bytes, nullptr);
+}
+
+extern "C" int rope3d_paged_attention_last_kernel(void) { return t_paged_kernel; }
+
+extern "C" int rope3d_testing_paged_wait_timeouts(int64_t *count, int32_t reset) {
+    if (!count) return ROPE3D_ERR_NULL;
+    unsigned int n = 0;
+    if (tiles_wait_timeouts(&n, reset != 0) != 0) return ROPE3D_ERR_CUDA;
+    *count = n;
+    return ROPE3D_OK;
+}

@@ -1,0 +1,256 @@
+// rope3d_paged.cuh -- how the attention over pages divides its work; shared by its
+// kernels (rope3d_paged.cu, rope3d_paged_tc.cu).
+//
+// An item is a tile of query rows of one sequence and key/value head: row
+// g of the sequence's tokens * group rows is query head g % group of the group, of
+// token g / group, so the heads that share keys share their loads. An item's keys are
+// those that some row of it sees, in blocks of kKeys places; its cost is
+// their number (1 where there are none: zeros have to be written). The items in order
+// (sequence, key/value head, tile) make a line of blocks that is cut into as many
+// equal parts as there are thread blocks, wherever the cuts fall: a prompt, one
+// token over a long cache and ragged mixtures are divided alike, and nothing has to
+// be known on the host. An item that a cut divides leaves partial results (sums not
+// yet divided, with the row's maximum and sum) in the workspace, which a second
+// kernel adds in order.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "rope3d_internal.h"
+#include "rope3d_paged.h"
+
+namespace rope3d_paged {
+
+struct AttnParams {
+    const char *q, *k, *v;
+    char *out;
+    float *lse;
+    Batch batch;
+    rope3d::FastDiv group;          // query heads of a key/value head
+    int kv_heads, head_dim;
+    int causal, window;             // window 0: none
+    int64_t q_token, q_head, out_token, out_head, lse_token;   // bytes; lse_token in floats
+    int64_t k_page, k_slot, k_head, v_page, v_slot, v_head;    // bytes
+    float scale_log2;               // scale * log2(e), positive
+    int parts;                      // thread blocks the line of blocks is cut for
+    float *partial;                 // workspace: two slots a part
+    struct PartNote *notes;         // workspace: where each part's first cut fell
+};
+
+// What a part leaves for the kernel that adds the partial results: where its
+// range begins, and the item that the cut falls into.
+struct PartNote {
+    long long begin, end;           // the part's blocks on the line
+    long long item, cost;           // the first block and the blocks of the item at `begin`
+    int s, h, t, pad;
+};
+
+__device__ __forceinline__ uint32_t udiv(uint32_t n, const rope3d::FastDiv &f) { return (__umulhi(n, f.mul) + n) >> f.shift; }
+
+// A sequence as the line of blocks sees it.
+struct Seq {
+    int lo, n, len, tiles;
+};
+
+template <int kRows>
+__device__ __forceinline__ Seq seq_of(const AttnParams &p, int s) {
+    Seq q;
+    int hi;
+    sequence(p.batch, s, q.lo, hi, q.len);
+    q.n = hi - q.lo;
+    q.tiles = int((int64_t(q.n) * p.group.d + kRows - 1) / kRows);
+    return q;
+}
+
+// Blocks [b0, b1) of tile t; the places [k0, k1) that its rows see.
+struct Tile {
+    int b0, b1, k0, k1;
+    __device__ int cost() const { return max(b1 - b0, 1); }
+};
+
+template <int kRows, int kKeys>
+__device__ __forceinline__ Tile tile_of(const AttnParams &p, const Seq &q, int t) {
+    const uint32_t rows = uint32_t(q.n) * p.group.d, last = min(rows, uint32_t(t + 1) * kRows) - 1;
+    const int past = q.len - q.n;   // place of the first new token; negative where the length is too short
+    Tile r;
+    r.k1 = p.causal ? min(max(past + int(udiv(last, p.group)) + 1, 0), q.len) : q.len;
+    r.k0 = p.window ? min(max(past + int(udiv(uint32_t(t) * kRows, p.group)) - p.window + 1, 0), r.k1) : 0;
+    r.b0 = r.k0 / kKeys;
+    r.b1 = r.k1 > r.k0 ? (r.k1 + kKeys - 1) / kKeys : r.b0;
+    return r;
+}
+
+// Blocks of one key/value head of a sequence.
+template <int kRows, int kKeys>
+__device__ long long seq_cost(const AttnParams &p, const Seq &q) {
+    long long sum = 0;
+    for (int t = 0; t < q.tiles; ++t) sum += tile_of<kRows, kKeys>(p, q, t).cost();
+    return sum;
+}
+
+// Where part `part` begins (one answer for all threads of the block, by way of
+// shared memory): its range of the line and the item there.
+struct Start {
+    long long begin, end, item, cost;
+    int s, h, t, off;
+};
+
+template <int kRows, int kKeys, int kThreads>
+__device__ void find_start(const AttnParams &p, int part, Start *out, long long *s_sums) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int seqs = p.batch.seqs, each = (seqs + kThreads - 1) / kThreads;
+    const int first = min(tid * each, seqs), end = min(first + each, seqs);
+    long long sum = 0;
+    for (int s = first; s < end; ++s) sum += seq_cost<kRows, kKeys>(p, seq_of<kRows>(p, s)) * p.kv_heads;
+    long long inc = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += o;
+    }
+    if (lane == 31) s_sums[warp] = inc;
+    if (tid == 0) out->s = -1;
+    __syncthreads();
+    long long before = inc - sum, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += s_sums[w];
+        total += s_sums[w];
+    }
+    const long long begin = total * part / p.parts, stop = total * (part + 1) / p.parts;
+    if (begin < stop && begin >= before && begin < before + sum) {
+        for (int s = first; s < end; ++s) {
+            const Seq q = seq_of<kRows>(p, s);
+            const long long head = seq_cost<kRows, kKeys>(p, q), all = head * p.kv_heads;
+            if (begin >= before + all) {
+                before += all;
+                continue;
+            }
+            out->s = s;
+            out->h = int((begin - before) / head);
+            before += out->h * head;
+            int t = 0, cost = 0;
+            for (;; ++t) {
+                cost = tile_of<kRows, kKeys>(p, q, t).cost();
+                if (begin < before + cost) break;
+                before += cost;
+            }
+            out->t = t;
+            out->off = int(begin - before);
+            out->item = before;
+            out->cost = cost;
+            break;
+        }
+    }
+    if (tid == 0) {
+        out->begin = begin;
+        out->end = stop;
+    }
+    __syncthreads();
+}
+
+// One item, as far as a part computes it.
+struct Item {
+    int s, h, t;
+    Seq q;
+    Tile tile;
+    int begin, end;      // blocks this part computes
+    int rows;            // rows of the tile
+    bool whole;          // all of the item's blocks
+    bool head;           // an earlier part began it: the first of the part's two slots
+};
+
+// Walks the items of a part; every thread that does so takes the same steps.
+template <int kRows, int kKeys>
+struct Walker {
+    const AttnParams &p;
+    long long left;
+    int s, h, t, off;
+    Seq q;
+
+    __device__ Walker(const AttnParams &params, const Start &st)
+        : p(params), left(st.s < 0 ? 0 : st.end - st.begin), s(st.s), h(st.h), t(st.t), off(st.off) {
+        if (left) q = seq_of<kRows>(p, s);
+    }
+
+    __device__ bool next(Item &it) {
+        if (left <= 0) return false;
+        while (t >= q.tiles) {   // the next head, or the next sequence with tokens
+            t = 0;
+            if (q.tiles == 0 || ++h >= p.kv_heads) {
+                h = 0;
+                if (++s >= p.batch.seqs) return false;
+                q = seq_of<kRows>(p, s);
+            }
+        }
+        it.s = s;
+        it.h = h;
+        it.t = t;
+        it.q = q;
+        it.tile = tile_of<kRows, kKeys>(p, q, t);
+        const int cost = it.tile.cost(), take = int(min(left, (long long)(cost - off)));
+        it.begin = it.tile.b0 + off;
+        it.end = min(it.begin + take, it.tile.b1);
+        it.rows = int(min(uint32_t(kRows), uint32_t(q.n) * p.group.d - uint32_t(t) * kRows));
+        it.whole = off == 0 && take == cost;
+        it.head = off > 0;
+        left -= take;
+        off = 0;
+        ++t;
+        return true;
+    }
+};
+
+// The places [lo, hi) that row r of an item sees, its token and query head.
+struct RowOf {
+    int token, head, lo, hi;
+};
+
+template <int kRows>
+__device__ __forceinline__ RowOf row_of(const AttnParams &p, const Item &it, int r) {
+    const uint32_t g = uint32_t(it.t) * kRows + uint32_t(r), i = udiv(g, p.group);
+    RowOf o;
+    o.token = it.q.lo + int(i);
+    o.head = it.h * int(p.group.d) + int(g - i * p.group.d);
+    const int place = it.q.len - it.q.n + int(i);
+    o.hi = p.causal ? min(max(place + 1, 0), it.q.len) : it.q.len;
+    o.lo = p.window ? max(place - p.window + 1, 0) : 0;
+    if (r >= it.rows) o.hi = o.lo = 0;
+    return o;
+}
+
+// A slot of partial results: [head_dim / 4][kRows] vectors of sums, then the
+// rows' maxima and sums.
+template <int kRows>
+__host__ __device__ inline int64_t slot_floats(int head_dim) { return int64_t(kRows) * (((head_dim + 3) & ~3) + 2); }
+
+template <int kRows>
+__device__ __forceinline__ float *slot_of(const AttnParams &p, int part, bool head) {
+    return p.partial + (2 * int64_t(part) + (head ? 0 : 1)) * slot_floats<kRows>(p.head_dim);
+}
+
+template <int kRows, int kKeys>
+__device__ __forceinline__ void write_note(const AttnParams &p, int part, const Start &st) {
+    PartNote n;
+    n.begin = st.begin;
+    n.end = st.end;
+    n.item = st.item;
+    n.cost = st.cost;
+    n.s = st.s;
+    n.h = st.h;
+    n.t = st.t;
+    n.pad = 0;
+    p.notes[part] = n;
+}
+
+// Launches of rope3d_paged_tc.cu.
+int launch_tiles(const AttnParams &p, const rope3d_paged_attention_args &a, cudaStream_t st);
+bool tiles_fit(const rope3d_paged_attention_args &a);
+int tiles_wait_timeouts(unsigned int *count, bool reset);
+
+constexpr int kTileRows = 128;   // rows of an item on the tensor cores
+constexpr int kFewRows = 16;     // rows of an item of the kernel for few rows
+constexpr int kTileParts = 152;  // thread blocks of the former: the GB300's SMs
+
+}  // namespace rope3d_paged
