@@ -1,14 +1,657 @@
-// rope3d_paged_tc.cu -- the attention over pages for many rows on the tensor cores.
-// (Not there yet: every call takes the kernel for few rows.)
+// rope3d_paged_tc.cu -- the attention over pages for many query rows, on the tensor
+// cores (tcgen05). An item is 128 query rows of a sequence and key/value head (M =
+// 128; the query heads of a group side by side, so that its keys are loaded
+// once), its keys come in blocks of 128 places. One persistent block an SM walks its
+// part of the line of blocks (rope3d_paged.cuh); its 16 warps have one job each and
+// hand over through mbarriers, so that copies, products and softmax overlap, also
+// across items:
+//   warp 0: K by TMA, a copy for every run of places on a page and 64 channels (lanes
+//     issue side by side), into a ring of pieces; warp 3: V likewise. Rows of V
+//     that no row sees (behind a length, on an absent page) are zeroed: a weight of
+//     zero times what lies there may be NaN.
+//   warp 2 (one thread): S = Q K^T into one of kSBufs buffers of tensor memory
+//   warp 1 (one thread): O += P V, with P read from tensor memory
+//   warps 4-7: the next item's Q rows into shared memory; each item's result
+//   warps 8-15: the softmax, two threads a row (64 keys each; the pair's maxima meet
+//     in shared memory). The maximum that weights refer to moves only when
+//     it is exceeded by more than 2^kLazy, and O is rescaled in tensor memory then;
+//     weights are written over S as pairs of 16 bits.
+// head_dim is padded to 64, 128 or 256 channels by TMA's zero fill. At 256 a block's K
+// comes as two pieces of 128 channels and its V as two of 64 places, so that five
+// pieces of 32 KB fit beside Q.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/rope3d.h"
+#include "rope3d_internal.h"
 #include "rope3d_paged.cuh"
+#include "rope3d_paged.h"
+#include "rope3d_tc.cuh"
 
-namespace rope3d_paged {
+namespace {
 
-int launch_tiles(const AttnParams &, const rope3d_paged_attention_args &, cudaStream_t) { return ROPE3D_ERR_CUDA; }
-bool tiles_fit(const rope3d_paged_attention_args &) { return false; }
-int tiles_wait_timeouts(unsigned int *count, bool) {
-    *count = 0;
-    return 0;
+using namespace rope3d_paged;
+using namespace rope3d_tc;
+
+constexpr int kRows = kTileRows, kKeys = 128;
+constexpr int kThreads = 512, kSoftWarp = 8;
+constexpr float kLazy = 8.0f;
+constexpr uint32_t kColBlock = kRows * 128;   // bytes of 64 channels of 128 rows
+
+__device__ unsigned int g_paged_wait_timeouts;
+
+// Shared memory and tensor memory at kD channels.
+template <int kD>
+struct Lay {
+    static constexpr int kPieces = kD == 256 ? 2 : 1;             // pieces of a block's K, and of its V
+    static constexpr int kKSlots = kD == 256 ? 3 : kD == 128 ? 2 : 4, kVSlots = kD == 64 ? 4 : 2;
+    static constexpr uint32_t kPiece = kD == 64 ? 16384 : 32768;
+    static constexpr int kVRows = kKeys / kPieces;                // places of a V piece
+    static constexpr int kQBufs = kD == 256 ? 1 : 2;
+    static constexpr uint32_t kQBytes = kRows * kD * 2;
+    static constexpr int kSBufs = kD == 256 ? 2 : 3;
+    static constexpr uint32_t kColO = kSBufs * 128;
+    static constexpr uint32_t kOffK = kQBufs * kQBytes, kOffV = kOffK + kKSlots * kPiece;
+    static constexpr uint32_t kOffMax = kOffV + kVSlots * kPiece;   // float [2][128]: a row's two maxima
+    static constexpr uint32_t kOffSum = kOffMax + 2 * 128 * 4;      // float [2][128] sums, [128] maxima
+    static constexpr uint32_t kOffBar = kOffSum + 3 * 128 * 4;
+    static constexpr int kBars = 2 * kQBufs + 2 * kKSlots + 2 * kVSlots + 3 * kSBufs + 5;
+    static constexpr uint32_t kBytes = kOffBar + kBars * 8 + 16;
+    static_assert(kColO + kD <= 512, "S and O fit tensor memory");
+    static_assert(kBytes <= 232448, "one block an SM");
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-}  // namespace rope3d_paged
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+template <bool kF16>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+    uint32_t w;
+    if constexpr (kF16) {
+        const __half2 h = __floats2half2_rn(x, y);
+        memcpy(&w, &h, 4);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        memcpy(&w, &h, 4);
+    }
+    return w;
+}
+
+// A box of 64 channels by some places of one head and page.
+__device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap *map, int c, int slot, int head, int page, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(slot), "r"(head), "r"(page), "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// D += A B with A (128 x 16, pairs of 16 bits to a column) read from tensor memory.
+__device__ __forceinline__ void mma_ta(uint32_t tmem, uint32_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(tmem), "r"(a), "l"(b), "r"(id), "r"(accumulate) : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32(float *v, uint32_t addr) {
+    uint32_t r[32];
+    __syncwarp();
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr) : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// The loads so far are complete; uses of v stay behind this.
+template <int kN>
+__device__ __forceinline__ void tmem_hold(float *v) {
+    tmem_wait();
+#pragma unroll
+    for (int i = 0; i < kN; ++i) asm volatile("" : "+f"(v[i]));
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *w) {
+    __syncwarp();
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+        ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]),
+          "r"(w[9]), "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15]) : "memory");
+}
+
+__device__ __forceinline__ void tmem_stored() {
+    __syncwarp();
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// What the copies need besides the maps.
+struct Copies {
+    int box;      // places of a box: the greatest power of two that divides the page, 64 at most
+    int boxes;    // boxes of a block
+};
+
+template <bool kF16, int kD>
+__global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ Copies cp,
+                                                                 const __grid_constant__ CUtensorMap map_k,
+                                                                 const __grid_constant__ CUtensorMap map_v) {
+    using L = Lay<kD>;
+    extern __shared__ __align__(1024) char sm[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t base = smem_u32(sm), bars = base + L::kOffBar;
+    // barriers: of Q, K, V, S buffers, then single ones
+    constexpr int kB1 = 2 * L::kQBufs, kB2 = kB1 + 2 * L::kKSlots, kB3 = kB2 + 2 * L::kVSlots, kB4 = kB3 + 3 * L::kSBufs;
+    auto q_full = [&](int i) { return bars + 8u * uint32_t(2 * i); };
+    auto q_empty = [&](int i) { return bars + 8u * uint32_t(2 * i + 1); };
+    auto k_full = [&](int i) { return bars + 8u * uint32_t(kB1 + 2 * i); };
+    auto k_empty = [&](int i) { return bars + 8u * uint32_t(kB1 + 2 * i + 1); };
+    auto v_full = [&](int i) { return bars + 8u * uint32_t(kB2 + 2 * i); };
+    auto v_empty = [&](int i) { return bars + 8u * uint32_t(kB2 + 2 * i + 1); };
+    auto s_full = [&](int i) { return bars + 8u * uint32_t(kB3 + 3 * i); };
+    auto s_empty = [&](int i) { return bars + 8u * uint32_t(kB3 + 3 * i + 1); };
+    auto p_full = [&](int i) { return bars + 8u * uint32_t(kB3 + 3 * i + 2); };
+    const uint32_t o_full = bars + 8u * kB4, o_empty = o_full + 8, sum_full = o_full + 16, sum_empty = o_full + 24,
+                   v_land = o_full + 32;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::kOffBar + L::kBars * 8);
+    unsigned int *late = &g_paged_wait_timeouts;
+
+    grid_release();
+    grid_wait();
+    {   // where this part begins, by way of the (yet unused) Q buffer
+        Start *s_start = reinterpret_cast<Start *>(sm);
+        find_start<kRows, kKeys, kThreads>(p, blockIdx.x, s_start, reinterpret_cast<long long *>(sm + 256));
+    }
+    const Start st = *reinterpret_cast<Start *>(sm);
+    if (tid == 0) {
+        write_note<kRows, kKeys>(p, blockIdx.x, st);
+        for (int i = 0; i < L::kQBufs; ++i) {
+            mbar_init(q_full(i), 4);
+            mbar_init(q_empty(i), 1);
+        }
+        for (int i = 0; i < L::kKSlots; ++i) {
+            mbar_init(k_full(i), 1);
+            mbar_init(k_empty(i), 1);
+        }
+        for (int i = 0; i < L::kVSlots; ++i) {
+            mbar_init(v_full(i), 1);
+            mbar_init(v_empty(i), 1);
+        }
+        for (int i = 0; i < L::kSBufs; ++i) {
+            mbar_init(s_full(i), 1);
+            mbar_init(s_empty(i), 1);
+            mbar_init(p_full(i), 8);
+        }
+        mbar_init(o_full, 1);
+        mbar_init(o_empty, 4);
+        mbar_init(sum_full, 8);
+        mbar_init(sum_empty, 4);
+        mbar_init(v_land, 1);
+        mbar_fence_init();
+        prefetch_map(&map_k);
+        prefetch_map(&map_v);
+    }
+    if (warp == 1) tmem_alloc<false>(smem_u32(tmem_slot), 512);
+    tc_fence_before();
+    __syncthreads();   // (also: everyone has read `st`)
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    bool dead = false;
+    Walker<kRows, kKeys> walk(p, st);
+    Item it;
+
+    if (warp == 0 || warp == 3) {
+        // ---- copies of K (warp 0) or V (warp 3)
+        const bool is_v = warp == 3;
+        const CUtensorMap *map = is_v ? &map_v : &map_k;
+        const int slots = is_v ? L::kVSlots : L::kKSlots;
+        const uint32_t ring = base + (is_v ? L::kOffV : L::kOffK);
+        int n = 0, landings = 0;   // pieces so far; of them, those that were waited for here
+        while (walk.next(it)) {
+            const int *table = p.batch.table + it.s * p.batch.table_stride;
+            for (int b = it.begin; b < it.end; ++b) {
+                const int k0 = max(it.tile.k0 - b * kKeys, 0), k1 = min(it.tile.k1 - b * kKeys, kKeys);   // what rows see
+#pragma unroll
+                for (int piece = 0; piece < L::kPieces; ++piece, ++n) {
+                    const int slot = n % slots;
+                    const uint32_t full = is_v ? v_full(slot) : k_full(slot), empty = is_v ? v_empty(slot) : k_empty(slot);
+                    // boxes [from, to) of the block hold places of this piece that rows see
+                    const int row0 = is_v ? piece * L::kVRows : 0, rows = is_v ? L::kVRows : kKeys;
+                    const int from = max(k0, row0) / cp.box, to = (min(k1, row0 + rows) + cp.box - 1) / cp.box;
+                    const int count = max(to - from, 0), cols = is_v ? kD / 64 : min(kD, 128) / 64;
+                    if (n >= slots) mbar_wait(empty, uint32_t(n / slots - 1) & 1u, dead, late);
+                    dead = __any_sync(0xffffffffu, dead);
+                    const bool clean = !is_v || (k0 <= row0 && k1 >= row0 + rows);   // nothing to be zeroed
+                    const uint32_t bar = clean ? full : v_land;
+                    const uint32_t dst = ring + uint32_t(slot) * L::kPiece;
+                    if (count && !dead) {
+                        if (lane == 0) mbar_expect_tx(bar, uint32_t(count * cols * cp.box) * 128u);
+                        __syncwarp();
+                        for (int i = lane; i < count * cols; i += 32) {
+                            const int box = from + i / cols, col = i % cols;
+                            const int place = b * kKeys + box * cp.box, index = place / p.batch.page_size;
+                            int page = index < p.batch.width ? table[index] : -1;
+                            if (page < 0 || page >= p.batch.pages) page = p.batch.pages;   // outside: filled with zeros
+                            const int channel = (is_v ? 0 : piece * 128) + col * 64;
+                            tma_load4(dst + uint32_t(col * rows + box * cp.box - row0) * 128u, map, channel,
+                                      place - index * p.batch.page_size, it.h, page, bar);
+                        }
+                        __syncwarp();
+                    }
+                    if (!clean) {
+                        if (count && !dead) {
+                            mbar_wait(v_land, uint32_t(landings) & 1u, dead, late);
+                            dead = __any_sync(0xffffffffu, dead);
+                            ++landings;
+                        }
+                        const int a = min(max(k0 - row0, 0), rows), z = max(min(k1 - row0, rows), a);   // rows [a, z) are seen
+                        for (int i = lane; i < (rows - (z - a)) * 8 * cols; i += 32) {
+                            const int chunk = i % 8, col = i / 8 % cols, r = i / (8 * cols);
+                            const int row = r < a ? r : r + (z - a);
+                            *reinterpret_cast<uint4 *>(sm + (dst - base) + uint32_t(col * rows + row) * 128u + chunk * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        }
+                        fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) arrive(full);
+                    } else if (!count && lane == 0) {
+                        arrive(full);
+                    }
+                }
+            }
+        }
+        if (dead && lane == 0) {
+            const int first = max(n - slots, 0);
+            for (int i = first; i < n; ++i) {
+                bool gone = false;
+                mbar_wait(is_v ? v_full(i % slots) : k_full(i % slots), uint32_t(i / slots) & 1u, gone, late);
+            }
+            bool gone = false;
+            if (is_v && landings) mbar_wait(v_land, uint32_t(landings - 1) & 1u, gone, late);
+        }
+    } else if (warp == 1) {
+        // ---- O += P V
+        if (lane == 0) {
+            constexpr uint32_t id = idesc(kRows, kD, !kF16, false, true);
+            int g = 0, n = 0, items = 0;
+            while (walk.next(it)) {
+                if (it.begin >= it.end) continue;
+                if (items) mbar_wait(o_empty, uint32_t(items - 1) & 1u, dead, late);
+                ++items;
+                for (int b = it.begin; b < it.end; ++b, ++g) {
+                    const int sb = g % L::kSBufs;
+                    mbar_wait(p_full(sb), uint32_t(g / L::kSBufs) & 1u, dead, late);
+#pragma unroll
+                    for (int piece = 0; piece < L::kPieces; ++piece, ++n) {
+                        const int slot = n % L::kVSlots;
+                        mbar_wait(v_full(slot), uint32_t(n / L::kVSlots) & 1u, dead, late);
+                        tc_fence_after();
+                        const uint32_t v = base + L::kOffV + uint32_t(slot) * L::kPiece;
+                        const uint32_t pa = tmem + uint32_t(sb * 128 + piece * (L::kVRows / 2));
+#pragma unroll
+                        for (int j = 0; j < L::kVRows / 16; ++j)
+                            mma_ta(tmem + L::kColO, pa + uint32_t(8 * j), sdesc(v + uint32_t(j) * 2048u, L::kVRows * 128, 1024), id,
+                                   b > it.begin || piece > 0 || j > 0 ? 1u : 0u);
+                        commit(v_empty(slot));
+                    }
+                    commit(s_empty(sb));
+                    if (b == it.end - 1) commit(o_full);
+                }
+            }
+        }
+    } else if (warp == 2) {
+        // ---- S = Q K^T
+        if (lane == 0) {
+            constexpr uint32_t id = idesc(kRows, kKeys, !kF16, false, false);
+            int g = 0, n = 0, items = 0;
+            while (walk.next(it)) {
+                if (it.begin >= it.end) continue;
+                const int qb = items % L::kQBufs;
+                mbar_wait(q_full(qb), uint32_t(items / L::kQBufs) & 1u, dead, late);
+                ++items;
+                const uint32_t q = base + uint32_t(qb) * L::kQBytes;
+                for (int b = it.begin; b < it.end; ++b, ++g) {
+                    const int sb = g % L::kSBufs;
+                    if (g >= L::kSBufs) mbar_wait(s_empty(sb), uint32_t(g / L::kSBufs - 1) & 1u, dead, late);
+#pragma unroll
+                    for (int piece = 0; piece < L::kPieces; ++piece, ++n) {
+                        const int slot = n % L::kKSlots;
+                        mbar_wait(k_full(slot), uint32_t(n / L::kKSlots) & 1u, dead, late);
+                        tc_fence_after();
+                        const uint32_t k = base + L::kOffK + uint32_t(slot) * L::kPiece, qp = q + uint32_t(piece) * 2 * kColBlock;
+#pragma unroll
+                        for (int j = 0; j < (kD < 128 ? kD : 128) / 16; ++j) {
+                            const uint32_t off = uint32_t(j >> 2) * kColBlock + uint32_t(j & 3) * 32u;
+                            mma<false>(tmem + uint32_t(sb * 128), sdesc(qp + off, 16, 1024), sdesc(k + off, 16, 1024), id,
+                                       piece > 0 || j > 0 ? 1u : 0u);
+                        }
+                        commit(k_empty(slot));
+                    }
+                    commit(s_full(sb));
+                    if (b == it.end - 1) commit(q_empty(qb));
+                }
+            }
+        }
+    } else if (warp < kSoftWarp) {
+        // ---- Q in, results out
+        const int t = tid - 128, row = t;   // this thread's row of results
+        const uint32_t lanes = uint32_t(warp & 3) << 21;
+        constexpr int kChunks = kD / 8;
+        const int chunks = p.head_dim / 8;
+        int loads = 0, items = 0;
+        auto load_q = [&](const Item &of) {
+            if (of.begin >= of.end) return;
+            const int qb = loads % L::kQBufs;
+            if (loads >= L::kQBufs) mbar_wait(q_empty(qb), uint32_t(loads / L::kQBufs - 1) & 1u, dead, late);
+            ++loads;
+            char *to = sm + uint32_t(qb) * L::kQBytes;
+            constexpr int kAtOnce = 8;
+            for (int i0 = t; i0 < kRows * kChunks; i0 += 128 * kAtOnce) {
+                uint4 v[kAtOnce];
+#pragma unroll
+                for (int e = 0; e < kAtOnce; ++e) {
+                    const int i = i0 + e * 128, r = i / kChunks, c = i % kChunks;
+                    v[e] = make_uint4(0, 0, 0, 0);
+                    if (r < of.rows && c < chunks) {
+                        const RowOf o = row_of<kRows>(p, of, r);
+                        v[e] = __ldg(reinterpret_cast<const uint4 *>(p.q + o.token * p.q_token + o.head * p.q_head + c * 16));
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < kAtOnce; ++e) {
+                    const int i = i0 + e * 128, r = i / kChunks, c = i % kChunks;
+                    *reinterpret_cast<uint4 *>(to + uint32_t(c >> 3) * kColBlock + uint32_t(r) * 128u + uint32_t(((c & 7) ^ (r & 7)) << 4)) = v[e];
+                }
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive(q_full(qb));
+        };
+        const float *sums = reinterpret_cast<const float *>(sm + L::kOffSum);
+        auto finish = [&](const Item &of) {
+            const RowOf o = row_of<kRows>(p, of, row);
+            const bool on = row < of.rows;
+            char *out = p.out + o.token * p.out_token + o.head * p.out_head;
+            if (of.begin >= of.end) {   // no row sees a key
+                if (on) {
+                    for (int c = 0; c < chunks; ++c) *reinterpret_cast<uint4 *>(out + c * 16) = make_uint4(0, 0, 0, 0);
+                    if (p.lse) p.lse[o.token * p.lse_token + o.head] = -INFINITY;
+                }
+                return;
+            }
+            mbar_wait(sum_full, uint32_t(items) & 1u, dead, late);
+            const float sum = sums[row] + sums[128 + row], top = sums[256 + row];
+            mbar_wait(o_full, uint32_t(items) & 1u, dead, late);
+            ++items;
+            __syncwarp();
+            tc_fence_after();
+            if (lane == 0) arrive(sum_empty);
+            float *slot = slot_of<kRows>(p, blockIdx.x, of.head);
+            const float inv = sum > 0.f ? 1.f / sum : sum;
+            for (int c0 = 0; c0 < p.head_dim; c0 += 32) {
+                float v[32];
+                tmem_ld32(v, tmem + L::kColO + lanes + uint32_t(c0));
+                tmem_hold<32>(v);
+                if (!on) continue;
+                if (of.whole) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8)
+                        if (c0 + i < p.head_dim)
+                            *reinterpret_cast<uint4 *>(out + (c0 + i) * 2) =
+                                make_uint4(pack2<kF16>(v[i] * inv, v[i + 1] * inv), pack2<kF16>(v[i + 2] * inv, v[i + 3] * inv),
+                                           pack2<kF16>(v[i + 4] * inv, v[i + 5] * inv), pack2<kF16>(v[i + 6] * inv, v[i + 7] * inv));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        if (c0 + i < p.head_dim)
+                            *reinterpret_cast<float4 *>(slot + int64_t((c0 + i) / 4 * kRows + row) * 4) =
+                                make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                }
+            }
+            __syncwarp();
+            tc_fence_before();
+            if (lane == 0) arrive(o_empty);
+            if (!on) return;
+            if (of.whole) {
+                if (p.lse) p.lse[o.token * p.lse_token + o.head] = sum > 0.f ? (top + log2f(sum)) * 0.69314718f : -INFINITY;
+            } else {
+                slot[int64_t(p.head_dim) * kRows + row] = top;
+                slot[int64_t(p.head_dim) * kRows + kRows + row] = sum;
+            }
+        };
+        bool more = walk.next(it);
+        if (more) load_q(it);
+        while (more) {
+            const Item now = it;
+            more = walk.next(it);
+            if (more) load_q(it);
+            finish(now);
+        }
+    } else {
+        // ---- softmax: row `row`, keys 64 half .. 64 half + 63 of each block
+        const int half = (warp - kSoftWarp) >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = uint32_t(warp & 3) << 21;
+        float *maxima = reinterpret_cast<float *>(sm + L::kOffMax), *sums = reinterpret_cast<float *>(sm + L::kOffSum);
+        const int pair_bar = 1 + (warp & 3);
+        int g = 0, items = 0;
+        while (walk.next(it)) {
+            if (it.begin >= it.end) continue;
+            const RowOf ro = row_of<kRows>(p, it, row);
+            const bool any_row = (warp & 3) * 32 < it.rows;   // the same for the pair of warps
+            const int *table = p.batch.table + it.s * p.batch.table_stride;
+            float m = -INFINITY, l = 0.f;
+            for (int b = it.begin; b < it.end; ++b, ++g) {
+                const int sb = g % L::kSBufs;
+                const uint32_t s = tmem + uint32_t(sb * 128) + lanes;
+                const int place = b * kKeys + half * 64;
+                // eight places a lane: whether their page is there
+                uint32_t there = 0xffu;
+                if (any_row) {
+                    const int index = (place + (lane & 7) * 8) / p.batch.page_size;
+                    const int page = index < p.batch.width ? table[index] : -1;
+                    there = __ballot_sync(0xffffffffu, page >= 0 && page < p.batch.pages) & 0xffu;
+                }
+                mbar_wait(s_full(sb), uint32_t(g / L::kSBufs) & 1u, dead, late);
+                __syncwarp();
+                tc_fence_after();
+                if (any_row) {
+                    float x[64];
+                    tmem_ld32(x, s + uint32_t(half * 64));
+                    tmem_ld32(x + 32, s + uint32_t(half * 64 + 32));
+                    tmem_hold<64>(x);
+                    const int a = max(ro.lo - place, 0), z = min(ro.hi - place, 64);
+                    if (__any_sync(0xffffffffu, a > 0 || z < 64 || there != 0xffu)) {
+                        uint64_t sees = a < z ? (~0ull >> (64 - (z - a))) << a : 0ull;
+                        if (there != 0xffu)
+                            for (int e = 0; e < 8; ++e)
+                                if (!(there >> e & 1u)) sees &= ~(0xffull << (8 * e));
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) x[e] = sees >> e & 1u ? x[e] : -INFINITY;
+                    }
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int e = 0; e < 64; e += 8)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) top[j] = max3(top[j], x[e + 2 * j], x[e + 2 * j + 1]);
+                    const float mine = max3(top[0], top[1], fmaxf(top[2], top[3])) * p.scale_log2;
+                    maxima[half * 128 + row] = mine;
+                    asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
+                    const float both = fmaxf(mine, maxima[(half ^ 1) * 128 + row]);
+                    const bool move = both > m + kLazy || m == -INFINITY;
+                    const bool rescale = move && m != -INFINITY;
+                    float f = 1.f;
+                    if (move) {
+                        const float to = fmaxf(m, both);
+                        f = rescale ? ex2(m - to) : 0.f;
+                        m = to;
+                        l *= f;
+                    }
+                    const float neg = m == -INFINITY ? 0.f : -m;
+                    const float2 c2 = make_float2(p.scale_log2, p.scale_log2), n2 = make_float2(neg, neg);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    uint32_t w[32];
+#pragma unroll
+                    for (int e = 0; e < 64; e += 2) {
+                        const float2 y = __ffma2_rn(make_float2(x[e], x[e + 1]), c2, n2);
+                        const float u = ex2(y.x), v = ex2(y.y);
+                        sum[(e >> 1) & 1] = __fadd2_rn(sum[(e >> 1) & 1], make_float2(u, v));
+                        w[e / 2] = pack2<kF16>(u, v);
+                    }
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                    tmem_st16(s + uint32_t(half * 32), w);
+                    tmem_st16(s + uint32_t(half * 32 + 16), w + 16);
+                    if (__any_sync(0xffffffffu, rescale)) {   // O holds the blocks before
+                        mbar_wait(s_empty((g - 1) % L::kSBufs), uint32_t((g - 1) / L::kSBufs) & 1u, dead, late);
+                        __syncwarp();
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c0 = 0; c0 < kD / 2; c0 += 16) {
+                            float o[16];
+                            const uint32_t at = tmem + L::kColO + lanes + uint32_t(half * (kD / 2) + c0);
+                            tmem_ld16(o, at);
+                            tmem_wait();
+                            tmem_tie16(o);
+                            uint32_t u[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e] * f);
+                            tmem_st16(at, u);
+                        }
+                    }
+                    tmem_stored();
+                    // the pair has read both maxima before either writes the next block's
+                    asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive(p_full(sb));
+            }
+            if (items) mbar_wait(sum_empty, uint32_t(items - 1) & 1u, dead, late);
+            ++items;
+            sums[half * 128 + row] = l;
+            if (half == 0) sums[256 + row] = m;
+            __syncwarp();
+            if (lane == 0) arrive(sum_full);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) tmem_free<false>(tmem, 512);
+}
+
+// ---- host --------------------------------------------------------------------------
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                   const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_tiled() {
+    static const EncodeTiledFn fn = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            return EncodeTiledFn(nullptr);
+        }
+        return reinterpret_cast<EncodeTiledFn>(ptr);
+    }();
+    return fn;
+}
+
+// A cache as (channels, places of a page, heads, pages).
+bool make_map(CUtensorMap *map, const void *p, const rope3d_paged_attention_args &a, int64_t page, int64_t slot, int64_t head, int box) {
+    const EncodeTiledFn fn = encode_tiled();
+    if (!fn) return false;
+    const rope3d_paged_batch &b = a.batch;
+    const cuuint64_t dims[4] = {cuuint64_t(a.head_dim), cuuint64_t(b.page_size), cuuint64_t(a.kv_heads), cuuint64_t(b.pages)};
+    // (of a dimension of one, any stride)
+    const cuuint64_t row = cuuint64_t(a.head_dim) * 2;
+    const cuuint64_t strides[3] = {b.page_size > 1 ? cuuint64_t(slot) * 2 : row, a.kv_heads > 1 ? cuuint64_t(head) * 2 : row,
+                                   b.pages > 1 ? cuuint64_t(page) * 2 : row};
+    const cuuint32_t boxes[4] = {64, cuuint32_t(box), 1, 1}, one[4] = {1, 1, 1, 1};
+    return fn(map, a.dtype == ROPE3D_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p),
+              dims, strides, boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool kF16, int kD>
+int launch_tile(const AttnParams &p, const Copies &c, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t st) {
+    static std::atomic<bool> ready[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return ROPE3D_ERR_CUDA;
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(paged_tile_kernel<kF16, kD>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Lay<kD>::kBytes)) !=
+            cudaSuccess) {
+            cudaGetLastError();
+            return ROPE3D_ERR_CUDA;
+        }
+        ready[dev].store(true, std::memory_order_release);
+    }
+    return launch(paged_tile_kernel<kF16, kD>, dim3(unsigned(p.parts)), kThreads, Lay<kD>::kBytes, st, p, c, k, v);
+}
+
+template <bool kF16>
+int launch_tile(const AttnParams &p, const Copies &c, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t st) {
+    if (p.head_dim <= 64) return launch_tile<kF16, 64>(p, c, k, v, st);
+    return p.head_dim <= 128 ? launch_tile<kF16, 128>(p, c, k, v, st) : launch_tile<kF16, 256>(p, c, k, v, st);
+}
+
+}  // namespace
+
+// What the tensor maps can describe: pages of whole groups of eight places (the
+// swizzle's period in shared memory), strides above zero.
+bool rope3d_paged::tiles_fit(const rope3d_paged_attention_args &a) {
+    const rope3d_paged_batch &b = a.batch;
+    if (b.page_size % 8 != 0) return false;
+    for (const int64_t s : {a.k_slot_stride, a.v_slot_stride})
+        if (b.page_size > 1 && (s <= 0 || s * 2 >= kMaxStride)) return false;
+    for (const int64_t s : {a.k_cache_head_stride, a.v_cache_head_stride})
+        if (a.kv_heads > 1 && (s <= 0 || s * 2 >= kMaxStride)) return false;
+    for (const int64_t s : {a.k_page_stride, a.v_page_stride})
+        if (b.pages > 1 && (s <= 0 || s * 2 >= kMaxStride)) return false;
+    return true;
+}
+
+int rope3d_paged::launch_tiles(const AttnParams &p, const rope3d_paged_attention_args &a, cudaStream_t st) {
+    Copies c{};
+    c.box = 8;
+    while (c.box < 64 && a.batch.page_size % (2 * c.box) == 0) c.box *= 2;
+    c.boxes = kKeys / c.box;
+    CUtensorMap k, v;
+    if (!make_map(&k, a.k_cache, a, a.k_page_stride, a.k_slot_stride, a.k_cache_head_stride, c.box) ||
+        !make_map(&v, a.v_cache, a, a.v_page_stride, a.v_slot_stride, a.v_cache_head_stride, c.box))
+        return ROPE3D_ERR_CUDA;
+    return a.dtype == ROPE3D_F16 ? launch_tile<true>(p, c, k, v, st) : launch_tile<false>(p, c, k, v, st);
+}
+
+int rope3d_paged::tiles_wait_timeouts(unsigned int *count, bool reset) {
+    const unsigned int zero = 0;
+    if (cudaMemcpyFromSymbol(count, g_paged_wait_timeouts, sizeof(zero)) != cudaSuccess ||
+        (reset && cudaMemcpyToSymbol(g_paged_wait_timeouts, &zero, sizeof(zero)) != cudaSuccess)) {
+        cudaGetLastError();
+        return ROPE3D_ERR_CUDA;
+    }
+    return ROPE3D_OK;
+}
