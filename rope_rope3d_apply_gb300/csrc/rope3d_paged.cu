@@ -138,11 +138,12 @@ __global__ void __launch_bounds__(kThreads) paged_rows_kernel(const __grid_const
         auto page_of = [&](int step) {
             const int place = place0 + step * kKeys + (lane & 15);
             int page = -1;
-            if (step < steps && place >= it.tile.k0 && place < it.tile.k1) page = table[place / p.batch.page_size];
+            if (step < steps && place >= it.tile.k0 && place < it.tile.k1) page = table[udiv(uint32_t(place), p.page)];
             return page;
         };
         auto issue = [&](int step, int page) {
-            const int slot_of = (place0 + step * kKeys + (lane & 15)) % p.batch.page_size;
+            const uint32_t place = uint32_t(place0 + step * kKeys + (lane & 15));
+            const int slot_of = int(place - udiv(place, p.page) * p.page.d);
             const bool live = page >= 0 && page < p.batch.pages;
             const uint32_t all = __ballot_sync(0xffffffffu, live) & 0xffffu;
             const int slot = step % kStages;
@@ -358,10 +359,11 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     rope3d_tc::grid_wait();
     const int c = blockIdx.x, tid = threadIdx.x;
     const PartNote n = p.notes[c];
-    if (n.begin == n.end || n.begin == n.item) return;
+    const long long first = n.item + p.item_cost;   // the item's first block on the line
+    if (n.begin == n.end || n.begin <= first) return;
     int from = c - 1;   // the part before: the item's first part, or the cut is not its first
     while (from > 0 && p.notes[from].begin == p.notes[from].end) --from;
-    if (p.notes[from].begin > n.item) return;
+    if (p.notes[from].begin > first) return;
     int to = c + 1;     // the parts of the item: from, c .. to - 1
     while (to < p.parts && p.notes[to].begin < n.item + n.cost) ++to;
 
@@ -391,7 +393,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
                     const int k = k0 + j * shares, part = k == 0 ? from : c + k - 1;
                     pm[j] = -INFINITY;
                     if (k >= parts || p.notes[part].begin == p.notes[part].end) continue;
-                    const float *slot = slot_of<kTile>(p, part, p.notes[part].begin > n.item);
+                    const float *slot = slot_of<kTile>(p, part, p.notes[part].begin > first);
                     pm[j] = slot[vecs * kTile * 4 + r];
                     pl[j] = slot[vecs * kTile * 4 + kTile + r];
                     pv[j] = *reinterpret_cast<const float4 *>(slot + (v4 * kTile + r) * 4);
@@ -541,6 +543,9 @@ int attention(const rope3d_paged_attention_args *a, bool go, bool check_device, 
     p.lse = a->lse;
     p.batch = device_batch(b, T);
     p.group = rope3d::make_fastdiv(uint32_t(H / K));
+    p.page = rope3d::make_fastdiv(uint32_t(b.page_size));
+    // measured in _COST_
+    p.item_cost = 2;
     p.kv_heads = int(K);
     p.head_dim = int(D);
     p.causal = a->causal;

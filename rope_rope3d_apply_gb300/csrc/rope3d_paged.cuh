@@ -4,12 +4,12 @@
 // An item is a tile of query rows of one sequence and key/value head: row
 // g of the sequence's tokens * group rows is query head g % group of the group, of
 // token g / group, so the heads that share keys share their loads. An item's keys are
-// those that some row of it sees, in blocks of kKeys places; its cost is
-// their number (1 where there are none: zeros have to be written). The items in order
-// (sequence, key/value head, tile) make a line of blocks that is cut into as many
-// equal parts as there are thread blocks, wherever the cuts fall: a prompt, one
-// token over a long cache and ragged mixtures are divided alike, and nothing has to
-// be known on the host. An item that a cut divides leaves partial results (sums not
+// those that some row of it sees, in blocks of kKeys places (at least one, where there
+// are none zeros have to be written); its cost is their number and a constant for
+// beginning and ending an item. The items in order (sequence, key/value head, tile)
+// make a line that is cut into as many equal parts as there are thread blocks, wherever
+// the cuts fall: a prompt, one token over a long cache and ragged mixtures are
+// divided alike, and nothing has to be known on the host. An item that a cut divides leaves partial results (sums not
 // yet divided, with the row's maximum and sum) in the workspace, which a second
 // kernel adds in order.
 #pragma once
@@ -29,6 +29,8 @@ struct AttnParams {
     float *lse;
     Batch batch;
     rope3d::FastDiv group;          // query heads of a key/value head
+    rope3d::FastDiv page;           // places of a page
+    int item_cost;                  // what an item costs besides its blocks, in blocks
     int kv_heads, head_dim;
     int causal, window;             // window 0: none
     int64_t q_token, q_head, out_token, out_head, lse_token;   // bytes; lse_token in floats
@@ -42,8 +44,8 @@ struct AttnParams {
 // What a part leaves for the kernel that adds the partial results: where its
 // range begins, and the item that the cut falls into.
 struct PartNote {
-    long long begin, end;           // the part's blocks on the line
-    long long item, cost;           // the first block and the blocks of the item at `begin`
+    long long begin, end;           // the part's range of the line
+    long long item, cost;           // where the item at `begin` begins, and its cost
     int s, h, t, pad;
 };
 
@@ -67,7 +69,7 @@ __device__ __forceinline__ Seq seq_of(const AttnParams &p, int s) {
 // Blocks [b0, b1) of tile t; the places [k0, k1) that its rows see.
 struct Tile {
     int b0, b1, k0, k1;
-    __device__ int cost() const { return max(b1 - b0, 1); }
+    __device__ int blocks() const { return max(b1 - b0, 1); }
 };
 
 template <int kRows, int kKeys>
@@ -82,12 +84,43 @@ __device__ __forceinline__ Tile tile_of(const AttnParams &p, const Seq &q, int t
     return r;
 }
 
-// Blocks of one key/value head of a sequence.
+// The cost of tiles 0 .. t - 1 (t below the tiles) of one key/value head, without a
+// loop over them. With T rows a tile, K places a block, G rows a token and `past` places
+// before the new tokens, the last row of tile u < t sees ceil((past + 1 + floor((u T + T -
+// 1) / G)) / K) = floor((a + u) / D) blocks from place 0 on, where D = K G / T and a =
+// floor((G (past + K) + T - 1) / T), and a window leaves out floor((c + u) / D) of
+// them, c = floor(G (past - window + 1) / T): sums of floors in a row.
+__device__ __forceinline__ long long floors(long long n, int d) {   // sum of floor(i / d) over 0 <= i < n
+    const long long q = n / d;
+    return q * (q - 1) / 2 * d + q * (n - q * d);
+}
+
+template <int kRows, int kKeys>
+__device__ long long tiles_cost(const AttnParams &p, const Seq &q, int t) {
+    static_assert(kKeys % kRows == 0 && (kRows == 128 || kRows == 16), "D is whole");
+    const int d = kKeys / kRows * int(p.group.d);
+    const long long group = p.group.d, past = q.len - q.n;
+    long long sum;
+    if (p.causal) {   // at least 1 each
+        const long long a = (group * (past + kKeys) + kRows - 1) >> (kRows == 128 ? 7 : 4);
+        const long long ones = min(max(d - a, 0ll), (long long)t);
+        sum = ones + (t > ones ? floors(a + t, d) - floors(a + ones, d) : 0);
+    } else {
+        sum = (long long)max((q.len + kKeys - 1) / kKeys, 1) * t;
+    }
+    if (p.window) {
+        const long long c = group * (past - p.window + 1) >> (kRows == 128 ? 7 : 4);
+        if (c + t > 0) sum -= floors(c + t, d) - floors(max(c, 0ll), d);
+    }
+    return sum + (long long)t * p.item_cost;
+}
+
+// The cost of one key/value head of a sequence.
 template <int kRows, int kKeys>
 __device__ long long seq_cost(const AttnParams &p, const Seq &q) {
-    long long sum = 0;
-    for (int t = 0; t < q.tiles; ++t) sum += tile_of<kRows, kKeys>(p, q, t).cost();
-    return sum;
+    if (q.tiles == 0) return 0;
+    return (q.tiles > 1 ? tiles_cost<kRows, kKeys>(p, q, q.tiles - 1) : 0) + tile_of<kRows, kKeys>(p, q, q.tiles - 1).blocks() +
+           p.item_cost;
 }
 
 // Where part `part` begins (one answer for all threads of the block, by way of
@@ -130,16 +163,17 @@ __device__ void find_start(const AttnParams &p, int part, Start *out, long long 
             out->s = s;
             out->h = int((begin - before) / head);
             before += out->h * head;
-            int t = 0, cost = 0;
-            for (;; ++t) {
-                cost = tile_of<kRows, kKeys>(p, q, t).cost();
-                if (begin < before + cost) break;
-                before += cost;
+            int t = 0, above = q.tiles;   // the last tile that begins at or before the cut
+            while (above - t > 1) {
+                const int mid = (t + above) >> 1;
+                if (before + tiles_cost<kRows, kKeys>(p, q, mid) <= begin) t = mid;
+                else above = mid;
             }
+            if (t > 0) before += tiles_cost<kRows, kKeys>(p, q, t);
             out->t = t;
             out->off = int(begin - before);
             out->item = before;
-            out->cost = cost;
+            out->cost = tile_of<kRows, kKeys>(p, q, t).blocks() + p.item_cost;
             break;
         }
     }
@@ -161,7 +195,8 @@ struct Item {
     bool head;           // an earlier part began it: the first of the part's two slots
 };
 
-// Walks the items of a part; every thread that does so takes the same steps.
+// Walks the items of a part; every thread that does so takes the same steps. An item's
+// constant cost comes before its blocks: a cut within it leaves the item to the later part.
 template <int kRows, int kKeys>
 struct Walker {
     const AttnParams &p;
@@ -175,30 +210,33 @@ struct Walker {
     }
 
     __device__ bool next(Item &it) {
-        if (left <= 0) return false;
-        while (t >= q.tiles) {   // the next head, or the next sequence with tokens
-            t = 0;
-            if (q.tiles == 0 || ++h >= p.kv_heads) {
-                h = 0;
-                if (++s >= p.batch.seqs) return false;
-                q = seq_of<kRows>(p, s);
+        while (left > 0) {
+            while (t >= q.tiles) {   // the next head, or the next sequence with tokens
+                t = 0;
+                if (q.tiles == 0 || ++h >= p.kv_heads) {
+                    h = 0;
+                    if (++s >= p.batch.seqs) return false;
+                    q = seq_of<kRows>(p, s);
+                }
             }
+            it.tile = tile_of<kRows, kKeys>(p, q, t);
+            const int blocks = it.tile.blocks(), cost = blocks + p.item_cost, take = int(min(left, (long long)(cost - off)));
+            const int from = max(off - p.item_cost, 0), to = max(off + take - p.item_cost, 0);
+            it.s = s;
+            it.h = h;
+            it.t = t;
+            it.q = q;
+            it.begin = it.tile.b0 + from;
+            it.end = min(it.tile.b0 + to, it.tile.b1);
+            it.rows = int(min(uint32_t(kRows), uint32_t(q.n) * p.group.d - uint32_t(t) * kRows));
+            it.whole = from == 0 && to == blocks;
+            it.head = from > 0;
+            left -= take;
+            off = 0;
+            ++t;
+            if (to > from) return true;
         }
-        it.s = s;
-        it.h = h;
-        it.t = t;
-        it.q = q;
-        it.tile = tile_of<kRows, kKeys>(p, q, t);
-        const int cost = it.tile.cost(), take = int(min(left, (long long)(cost - off)));
-        it.begin = it.tile.b0 + off;
-        it.end = min(it.begin + take, it.tile.b1);
-        it.rows = int(min(uint32_t(kRows), uint32_t(q.n) * p.group.d - uint32_t(t) * kRows));
-        it.whole = off == 0 && take == cost;
-        it.head = off > 0;
-        left -= take;
-        off = 0;
-        ++t;
-        return true;
+        return false;
     }
 };
 

@@ -12,10 +12,13 @@
 //   warp 2 (one thread): S = Q K^T into one of kSBufs buffers of tensor memory
 //   warp 1 (one thread): O += P V, with P read from tensor memory
 //   warps 4-7: the next item's Q rows into shared memory; each item's result
-//   warps 8-15: the softmax, two threads a row (64 keys each; the pair's maxima meet
-//     in shared memory). The maximum that weights refer to moves only when
-//     it is exceeded by more than 2^kLazy, and O is rescaled in tensor memory then;
-//     weights are written over S as pairs of 16 bits.
+//   warps 8-15: the softmax, a thread a row, in two groups of four warps that take
+//     blocks in turn: one's exponentials run while the other waits for S, finds its maximum
+//     or hands over. The maximum that weights refer to goes from group to group through
+//     shared memory (before the exponentials); it moves only when it is exceeded by more
+//     than 2^kLazy, and O is rescaled in tensor memory then. A row's 128 scores stay in
+//     registers (the other warps give some of theirs up) from one read of tensor memory to
+//     the weights, which are written over S as pairs of 16 bits.
 // head_dim is padded to 64, 128 or 256 channels by TMA's zero fill. At 256 a block's K
 // comes as two pieces of 128 channels and its V as two of 64 places, so that five
 // pieces of 32 KB fit beside Q.
@@ -43,6 +46,10 @@ using namespace rope3d_tc;
 constexpr int kRows = kTileRows, kKeys = 128;
 constexpr int kThreads = 512, kSoftWarp = 8;
 constexpr float kLazy = 8.0f;
+// Registers of a thread: 512 threads have 128 each at launch; the softmax's 256 have
+// kSoftRegs and the others kOtherRegs, no more together.
+constexpr int kSoftRegs = 184, kOtherRegs = 72;
+static_assert(256 * (kSoftRegs + kOtherRegs) <= kThreads * 128, "no more registers than the block has");
 constexpr uint32_t kColBlock = kRows * 128;   // bytes of 64 channels of 128 rows
 
 __device__ unsigned int g_paged_wait_timeouts;
@@ -59,7 +66,7 @@ struct Lay {
     static constexpr int kSBufs = kD == 256 ? 2 : 3;
     static constexpr uint32_t kColO = kSBufs * 128;
     static constexpr uint32_t kOffK = kQBufs * kQBytes, kOffV = kOffK + kKSlots * kPiece;
-    static constexpr uint32_t kOffMax = kOffV + kVSlots * kPiece;   // float [2][128]: a row's two maxima
+    static constexpr uint32_t kOffMax = kOffV + kVSlots * kPiece;   // float [2][128]: a row's maximum, from each group
     static constexpr uint32_t kOffSum = kOffMax + 2 * 128 * 4;      // float [2][128] sums, [128] maxima
     static constexpr uint32_t kOffBar = kOffSum + 3 * 128 * 4;
     static constexpr int kBars = 2 * kQBufs + 2 * kKSlots + 2 * kVSlots + 3 * kSBufs + 5;
@@ -202,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
         for (int i = 0; i < L::kSBufs; ++i) {
             mbar_init(s_full(i), 1);
             mbar_init(s_empty(i), 1);
-            mbar_init(p_full(i), 8);
+            mbar_init(p_full(i), 4);
         }
         mbar_init(o_full, 1);
         mbar_init(o_empty, 4);
@@ -219,9 +226,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     bool dead = false;
+    __syncwarp();
     Walker<kRows, kKeys> walk(p, st);
     Item it;
 
+    if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == 0 || warp == 3) {
         // ---- copies of K (warp 0) or V (warp 3)
         const bool is_v = warp == 3;
@@ -251,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
                         __syncwarp();
                         for (int i = lane; i < count * cols; i += 32) {
                             const int box = from + i / cols, col = i % cols;
-                            const int place = b * kKeys + box * cp.box, index = place / p.batch.page_size;
+                            const int place = b * kKeys + box * cp.box, index = int(udiv(uint32_t(place), p.page));
                             int page = index < p.batch.width ? table[index] : -1;
                             if (page < 0 || page >= p.batch.pages) page = p.batch.pages;   // outside: filled with zeros
                             const int channel = (is_v ? 0 : piece * 128) + col * 64;
@@ -354,8 +364,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
                 }
             }
         }
+    }
     } else if (warp < kSoftWarp) {
         // ---- Q in, results out
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         const int t = tid - 128, row = t;   // this thread's row of results
         const uint32_t lanes = uint32_t(warp & 3) << 21;
         constexpr int kChunks = kD / 8;
@@ -366,25 +378,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
             const int qb = loads % L::kQBufs;
             if (loads >= L::kQBufs) mbar_wait(q_empty(qb), uint32_t(loads / L::kQBufs - 1) & 1u, dead, late);
             ++loads;
-            char *to = sm + uint32_t(qb) * L::kQBytes;
-            constexpr int kAtOnce = 8;
-            for (int i0 = t; i0 < kRows * kChunks; i0 += 128 * kAtOnce) {
-                uint4 v[kAtOnce];
-#pragma unroll
-                for (int e = 0; e < kAtOnce; ++e) {
-                    const int i = i0 + e * 128, r = i / kChunks, c = i % kChunks;
-                    v[e] = make_uint4(0, 0, 0, 0);
-                    if (r < of.rows && c < chunks) {
-                        const RowOf o = row_of<kRows>(p, of, r);
-                        v[e] = __ldg(reinterpret_cast<const uint4 *>(p.q + o.token * p.q_token + o.head * p.q_head + c * 16));
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < kAtOnce; ++e) {
-                    const int i = i0 + e * 128, r = i / kChunks, c = i % kChunks;
-                    *reinterpret_cast<uint4 *>(to + uint32_t(c >> 3) * kColBlock + uint32_t(r) * 128u + uint32_t(((c & 7) ^ (r & 7)) << 4)) = v[e];
-                }
+            // A warp copies kPer rows at once, rows kPer (4 e + warp % 4) + sub for e = 0, 1, ...;
+            // lane kPer e + sub finds where row (e, sub) lies.
+            constexpr int kPer = 32 / kChunks, kSteps = kRows / (4 * kPer);
+            static_assert(kSteps * kPer == 32, "a row to a lane");
+            const int mine = kPer * (4 * (lane / kPer) + (warp & 3)) + lane % kPer;
+            const RowOf o = row_of<kRows>(p, of, mine);
+            const long long at = mine < of.rows ? o.token * p.q_token + o.head * p.q_head : -1;
+            const int c = lane % kChunks;
+            const uint32_t to = base + uint32_t(qb) * L::kQBytes + uint32_t(c >> 3) * kColBlock;
+#pragma unroll 4
+            for (int e = 0; e < kSteps; ++e) {
+                const int r = kPer * (4 * e + (warp & 3)) + lane / kChunks;
+                const long long from = __shfl_sync(0xffffffffu, at, kPer * e + lane / kChunks);
+                const bool live = from >= 0 && c < chunks;   // zeros elsewhere
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                             ::"r"(to + uint32_t(r) * 128u + uint32_t(((c & 7) ^ (r & 7)) << 4)), "l"(p.q + (live ? from + c * 16 : 0)),
+                             "r"(live ? 16 : 0) : "memory");
             }
+            asm volatile("cp.async.wait_all;" ::: "memory");
             fence_async_smem();
             __syncwarp();
             if (lane == 0) arrive(q_full(qb));
@@ -450,86 +462,109 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
             finish(now);
         }
     } else {
-        // ---- softmax: row `row`, keys 64 half .. 64 half + 63 of each block
-        const int half = (warp - kSoftWarp) >> 2, row = (warp & 3) * 32 + lane;
+        // ---- softmax: row `row`, every second block
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        const int group = (warp - kSoftWarp) >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = uint32_t(warp & 3) << 21;
-        float *maxima = reinterpret_cast<float *>(sm + L::kOffMax), *sums = reinterpret_cast<float *>(sm + L::kOffSum);
-        const int pair_bar = 1 + (warp & 3);
+        float *passed = reinterpret_cast<float *>(sm + L::kOffMax), *sums = reinterpret_cast<float *>(sm + L::kOffSum);
+        // named barriers of the four pairs of warps, one for each direction
+        const int to_other = 1 + group * 4 + (warp & 3), from_other = 1 + (group ^ 1) * 4 + (warp & 3);
         int g = 0, items = 0;
         while (walk.next(it)) {
             if (it.begin >= it.end) continue;
             const RowOf ro = row_of<kRows>(p, it, row);
             const bool any_row = (warp & 3) * 32 < it.rows;   // the same for the pair of warps
             const int *table = p.batch.table + it.s * p.batch.table_stride;
+            auto page_at = [&](int b) {   // of eight places, by lane
+                const uint32_t index = udiv(uint32_t(b * kKeys + (lane & 15) * 8), p.page);
+                return b < it.end && index < uint32_t(p.batch.width) ? table[index] : -1;
+            };
             float m = -INFINITY, l = 0.f;
-            for (int b = it.begin; b < it.end; ++b, ++g) {
-                const int sb = g % L::kSBufs;
-                const uint32_t s = tmem + uint32_t(sb * 128) + lanes;
-                const int place = b * kKeys + half * 64;
-                // eight places a lane: whether their page is there
-                uint32_t there = 0xffu;
-                if (any_row) {
-                    const int index = (place + (lane & 7) * 8) / p.batch.page_size;
-                    const int page = index < p.batch.width ? table[index] : -1;
-                    there = __ballot_sync(0xffffffffu, page >= 0 && page < p.batch.pages) & 0xffu;
+            auto receive = [&] {   // the maximum that the other group's last block refers to
+                asm volatile("bar.sync %0, 64;" ::"r"(from_other) : "memory");
+                const float now = passed[(group ^ 1) * 128 + row];
+                if (now > m) {
+                    l *= m == -INFINITY ? 0.f : ex2(m - now);
+                    m = now;
                 }
+            };
+            const int mine = it.begin + ((g ^ group) & 1);   // this group's first block
+            int page = page_at(mine);
+            for (int b = it.begin; b < it.end; ++b, ++g) {
+                if ((g & 1) != group) continue;
+                const int sb = g % L::kSBufs, place = b * kKeys;
+                const uint32_t s = tmem + uint32_t(sb * 128) + lanes;
+                const uint32_t there = __ballot_sync(0xffffffffu, page >= 0 && page < p.batch.pages) & 0xffffu;
+                page = page_at(b + 2);
                 mbar_wait(s_full(sb), uint32_t(g / L::kSBufs) & 1u, dead, late);
                 __syncwarp();
                 tc_fence_after();
                 if (any_row) {
-                    float x[64];
-                    tmem_ld32(x, s + uint32_t(half * 64));
-                    tmem_ld32(x + 32, s + uint32_t(half * 64 + 32));
-                    tmem_hold<64>(x);
-                    const int a = max(ro.lo - place, 0), z = min(ro.hi - place, 64);
-                    if (__any_sync(0xffffffffu, a > 0 || z < 64 || there != 0xffu)) {
-                        uint64_t sees = a < z ? (~0ull >> (64 - (z - a))) << a : 0ull;
-                        if (there != 0xffu)
-                            for (int e = 0; e < 8; ++e)
-                                if (!(there >> e & 1u)) sees &= ~(0xffull << (8 * e));
-#pragma unroll
-                        for (int e = 0; e < 64; ++e) x[e] = sees >> e & 1u ? x[e] : -INFINITY;
-                    }
+                    const int a = max(ro.lo - place, 0), z = min(ro.hi - place, kKeys);
+                    const bool masked = __any_sync(0xffffffffu, a > 0 || z < kKeys || there != 0xffffu);
+                    auto sees = [&](int c) {   // of columns 32 c .. 32 c + 31
+                        const int from = max(a - 32 * c, 0), to = min(z - 32 * c, 32);
+                        uint32_t bits = from < to ? (0xffffffffu >> (32 - (to - from))) << from : 0u;
+                        const uint32_t four = there >> (4 * c) & 15u;
+                        if (four != 15u)
+                            for (int e = 0; e < 4; ++e)
+                                if (!(four >> e & 1u)) bits &= ~(0xffu << (8 * e));
+                        return bits;
+                    };
+                    float x[128];
                     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int e = 0; e < 64; e += 8)
+                    for (int c = 0; c < 4; ++c) tmem_ld32(x + 32 * c, s + uint32_t(32 * c));
+                    tmem_hold<128>(x);
+                    if (masked) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t bits = sees(c);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[32 * c + e] = bits >> e & 1u ? x[32 * c + e] : -INFINITY;
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 128; e += 8)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) top[j] = max3(top[j], x[e + 2 * j], x[e + 2 * j + 1]);
-                    const float mine = max3(top[0], top[1], fmaxf(top[2], top[3])) * p.scale_log2;
-                    maxima[half * 128 + row] = mine;
-                    asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
-                    const float both = fmaxf(mine, maxima[(half ^ 1) * 128 + row]);
-                    const bool move = both > m + kLazy || m == -INFINITY;
+                    const float best = max3(top[0], top[1], fmaxf(top[2], top[3])) * p.scale_log2;
+                    if (b > it.begin) receive();
+                    const bool move = best > m + kLazy || m == -INFINITY;
                     const bool rescale = move && m != -INFINITY;
                     float f = 1.f;
                     if (move) {
-                        const float to = fmaxf(m, both);
+                        const float to = fmaxf(m, best);
                         f = rescale ? ex2(m - to) : 0.f;
                         m = to;
                         l *= f;
                     }
+                    passed[group * 128 + row] = m;
+                    asm volatile("bar.arrive %0, 64;" ::"r"(to_other) : "memory");
                     const float neg = m == -INFINITY ? 0.f : -m;
                     const float2 c2 = make_float2(p.scale_log2, p.scale_log2), n2 = make_float2(neg, neg);
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                    uint32_t w[32];
 #pragma unroll
-                    for (int e = 0; e < 64; e += 2) {
-                        const float2 y = __ffma2_rn(make_float2(x[e], x[e + 1]), c2, n2);
-                        const float u = ex2(y.x), v = ex2(y.y);
-                        sum[(e >> 1) & 1] = __fadd2_rn(sum[(e >> 1) & 1], make_float2(u, v));
-                        w[e / 2] = pack2<kF16>(u, v);
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const float2 y = __ffma2_rn(make_float2(x[32 * c + e], x[32 * c + e + 1]), c2, n2);
+                            const float u = ex2(y.x), t = ex2(y.y);
+                            sum[(e >> 1) & 1] = __fadd2_rn(sum[(e >> 1) & 1], make_float2(u, t));
+                            w[e / 2] = pack2<kF16>(u, t);
+                        }
+                        tmem_st16(s + uint32_t(16 * c), w);
                     }
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                    tmem_st16(s + uint32_t(half * 32), w);
-                    tmem_st16(s + uint32_t(half * 32 + 16), w + 16);
                     if (__any_sync(0xffffffffu, rescale)) {   // O holds the blocks before
                         mbar_wait(s_empty((g - 1) % L::kSBufs), uint32_t((g - 1) / L::kSBufs) & 1u, dead, late);
                         __syncwarp();
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c0 = 0; c0 < kD / 2; c0 += 16) {
+                        for (int c0 = 0; c0 < kD; c0 += 16) {
                             float o[16];
-                            const uint32_t at = tmem + L::kColO + lanes + uint32_t(half * (kD / 2) + c0);
+                            const uint32_t at = tmem + L::kColO + lanes + uint32_t(c0);
                             tmem_ld16(o, at);
                             tmem_wait();
                             tmem_tie16(o);
@@ -540,17 +575,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
                         }
                     }
                     tmem_stored();
-                    // the pair has read both maxima before either writes the next block's
-                    asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) arrive(p_full(sb));
             }
+            const bool last = ((g - 1) & 1) == group;   // the item's last block was this group's
+            if (any_row && !last) receive();
             if (items) mbar_wait(sum_empty, uint32_t(items - 1) & 1u, dead, late);
             ++items;
-            sums[half * 128 + row] = l;
-            if (half == 0) sums[256 + row] = m;
+            sums[group * 128 + row] = l;
+            if (last) sums[256 + row] = m;
             __syncwarp();
             if (lane == 0) arrive(sum_full);
         }
