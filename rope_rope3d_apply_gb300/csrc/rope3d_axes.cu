@@ -16,9 +16,8 @@
 //
 // Each block takes tiles of a few tokens: cos and sin of the tile's tokens and pairs
 // go into shared memory once (64 sincospi a token instead of 64 for each of its
-// heads), then each thread moves 16-byte vectors, four loads in flight. What bounds it is
-// memory: 16 x 64 x 64 tokens of 2 x 16 heads of 128 in bf16 (1.07 GB) take what a
-// copy of them takes.
+// heads), then each thread moves 16-byte vectors at one place of head rows, four loads in
+// flight. What bounds it is memory.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -39,7 +38,7 @@ using rope3d::make_fastdiv;
 using namespace rope3d_paged;
 
 constexpr int kThreads = 256;
-constexpr int kInFlight = 4;     // 16-byte units (or pairs of them) a thread has in flight
+constexpr int kBlocks = 4;       // blocks that fit an SM beside one another
 constexpr int kMaxTile = 32;     // tokens of a tile
 
 __device__ __forceinline__ uint32_t fdiv(uint32_t n, const FastDiv &f) { return (__umulhi(n, f.mul) + n) >> f.shift; }
@@ -61,8 +60,10 @@ struct AxesParams {
     int tokens, tile, pairs, head_dim;
     int end0, end1;            // pairs of axis 0; of axes 0 and 1
     int heads[3];              // q, k, v
-    int rotating;              // units of a head row that rotate; the rest are copied
-    FastDiv per_token, per_head;
+    int per_head, rotating;    // units of a head row; those that rotate (the rest are copied)
+    FastDiv heads_all;         // head rows of a token
+    FastDiv lanes;             // threads to a head row
+    uint32_t rows_at_once;     // head rows of a block at a time
     int position_type;         // ROPE3D_POSITIONS_*; -1: the place in the sequence
     float sign;
 };
@@ -175,23 +176,15 @@ __device__ __forceinline__ uint4 ld_stream(const char *p) {   // coherent: in pl
     return r;
 }
 
-// One work unit of a head row: where it reads and writes, and its first pair (-1:
-// copied as it is). kHalves: the pair's second parts lie `second` bytes further on.
-struct Unit {
-    const char *src;
-    char *dst;
-    int pair;
-    const float2 *cs;
-};
-
 // ---- the kernel ------------------------------------------------------------------
 
 // kVec: units of 16 bytes (kHalves: two of them, the parts of 16 bytes' worth of
 // pairs), else single pairs and elements.
 template <int kType, bool kHalves, bool kAppend, bool kVec>
-__global__ void __launch_bounds__(kThreads) axes_kernel(const __grid_constant__ AxesParams p) {
+__global__ void __launch_bounds__(kThreads, kBlocks) axes_kernel(const __grid_constant__ AxesParams p) {
     constexpr int kElem = kType == ROPE3D_F32 ? 4 : 2;
     constexpr int kV = kVec ? 16 / kElem : 1;   // elements of a vector
+    constexpr int kInFlight = kVec && kHalves ? 2 : 4;   // units of a thread's loads in flight: 64 bytes
     extern __shared__ float2 s_cs[];            // [tile][pairs], then freq / 2 pi as (hi, lo) [pairs]
     float2 *s_freq = s_cs + size_t(p.tile) * p.pairs;
     __shared__ int64_t s_dst[2][kMaxTile];      // append: byte offsets in the caches, -1: nowhere
@@ -206,6 +199,8 @@ __global__ void __launch_bounds__(kThreads) axes_kernel(const __grid_constant__ 
         s_freq[j] = make_float2(hi, float(f - double(hi)));
     }
     const int64_t second = int64_t(p.pairs) * kElem;
+    const uint32_t row_at = fdiv(uint32_t(tid), p.lanes);
+    const int at0 = row_at < p.rows_at_once ? tid - int(row_at * p.lanes.d) : p.per_head;   // (the last few have no row)
 
     for (int t0 = blockIdx.x * p.tile; t0 < p.tokens; t0 += gridDim.x * p.tile) {
         const int count = min(p.tile, p.tokens - t0);
@@ -266,108 +261,110 @@ __global__ void __launch_bounds__(kThreads) axes_kernel(const __grid_constant__ 
         }
         __syncthreads();
 
-        auto locate = [&](uint32_t u, Unit &n) {
-            const uint32_t i = fdiv(u, p.per_token), r = u - i * p.per_token.d;
-            uint32_t h = fdiv(r, p.per_head);
-            const int at = int(r - h * p.per_head.d);
-            int which = 0;
-            if (int(h) >= p.heads[0]) {
-                h -= p.heads[0];
-                which = 1;
-                if (kAppend && int(h) >= p.heads[1]) {
-                    h -= p.heads[1];
-                    which = 2;
+        const uint32_t rows = uint32_t(count) * p.heads_all.d;
+        for (int at = at0; at < p.per_head; at += p.lanes.d) {
+            // this thread's part of each of its rows: its first element and, where it turns, its
+            // first pair (interleaved units lie in order; of halves', the first parts do, and behind
+            // the second parts come the units that are copied)
+            const bool turning = at < p.rotating;
+            const int first = kHalves ? (turning ? at : at + p.rotating) * kV
+                              : kVec  ? at * kV
+                                      : (turning ? 2 * at : at + p.rotating);
+            const int pair = kVec && !kHalves ? at * kV / 2 : at * kV;
+            // both parts of a pair, where they are two loads
+            const bool two = turning && (kHalves || !kVec);
+            const int64_t off = int64_t(first) * kElem;
+            auto locate = [&](uint32_t row, const char *&src, char *&dst, const float2 *&cs) {
+                const uint32_t i = fdiv(row, p.heads_all), t = uint32_t(t0) + i;
+                int h = int(row - i * p.heads_all.d), which = 0;
+                if (h >= p.heads[0]) {
+                    h -= p.heads[0];
+                    which = 1;
+                    if (kAppend && h >= p.heads[1]) {
+                        h -= p.heads[1];
+                        which = 2;
+                    }
                 }
-            }
-            const bool turns = which < 2 && at < p.rotating;
-            // a unit's first element: interleaved units are in order; halves' rotating ones are
-            // the first parts, behind which come the rows' second parts
-            int64_t first;
-            if constexpr (kHalves) first = at < p.rotating ? int64_t(at) * kV : int64_t(2 * p.pairs) + int64_t(at - p.rotating) * kV;
-            else if constexpr (kVec) first = int64_t(at) * kV;
-            else first = at < p.rotating ? 2 * at : at + p.rotating;
-            const int64_t off = first * kElem;
-            const Rows &in = p.in[which], &out = p.out[which];
-            n.src = in.p + (t0 + int(i)) * in.token + h * in.head + off;
-            n.pair = turns ? (kVec && !kHalves ? at * kV / 2 : at * kV) : -1;
-            n.cs = s_cs + i * p.pairs;
-            char *base = const_cast<char *>(out.p) + h * out.head + off;
-            if constexpr (kAppend) {
-                if (!s_live[i]) return false;
-                if (which == 0) {
-                    n.dst = base + (t0 + int(i)) * out.token;
-                } else {
+                src = p.in[which].p + t * p.in[which].token + h * p.in[which].head + off;
+                dst = const_cast<char *>(p.out[which].p) + h * p.out[which].head + off;
+                cs = turning && which < 2 ? s_cs + i * p.pairs + pair : nullptr;
+                if (kAppend && which > 0) {
                     const int64_t d = s_dst[which - 1][i];
-                    if (d < 0) return false;
-                    n.dst = base + d;
+                    dst += d;
+                    return d >= 0;
                 }
-                // a head row of V rotates nothing: its two parts are copied by the same unit
-                if (kHalves && which == 2 && at < p.rotating) n.pair = -2;
-            } else {
-                n.dst = base + (t0 + int(i)) * out.token;
-            }
-            if (!kHalves && !kVec && which == 2 && at < p.rotating) n.pair = -2;
-            return true;
-        };
-
-        const uint32_t units = uint32_t(count) * p.per_token.d;
-        for (uint32_t u0 = tid; u0 < units; u0 += kThreads * kInFlight) {
-            Unit n[kInFlight];
-            bool on[kInFlight];
-            if constexpr (kVec) {
-                uint4 a[kInFlight], b[kInFlight];
+                dst += t * p.out[which].token;
+                return !kAppend || s_live[i] != 0;
+            };
+            for (uint32_t row0 = row_at; row0 < rows; row0 += p.rows_at_once * kInFlight) {
+                const char *src;
+                char *dst[kInFlight];
+                const float2 *cs[kInFlight];
+                bool on[kInFlight];
+                if constexpr (kVec) {
+                    uint4 a[kInFlight], b[kHalves ? kInFlight : 1];
 #pragma unroll
-                for (int q = 0; q < kInFlight; ++q) {
-                    const uint32_t u = u0 + q * kThreads;
-                    on[q] = u < units && locate(u, n[q]);
-                    if (on[q]) {
-                        a[q] = ld_stream(n[q].src);
-                        if (kHalves && n[q].pair != -1) b[q] = ld_stream(n[q].src + second);
-                    }
-                }
-#pragma unroll
-                for (int q = 0; q < kInFlight; ++q) {
-                    if (!on[q]) continue;
-                    if (n[q].pair >= 0) {
-                        float x[kV], y[kV];
-                        widen<kType>(a[q], x);
-                        if constexpr (kHalves) {
-                            widen<kType>(b[q], y);
-#pragma unroll
-                            for (int e = 0; e < kV; ++e) {
-                                const float2 r = rotate(x[e], y[e], n[q].cs[n[q].pair + e]);
-                                x[e] = r.x;
-                                y[e] = r.y;
-                            }
-                            b[q] = narrow<kType>(y);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < kV; e += 2) {
-                                const float2 r = rotate(x[e], x[e + 1], n[q].cs[n[q].pair + e / 2]);
-                                x[e] = r.x;
-                                x[e + 1] = r.y;
-                            }
+                    for (int q = 0; q < kInFlight; ++q) {
+                        const uint32_t row = row0 + q * p.rows_at_once;
+                        on[q] = row < rows && locate(row, src, dst[q], cs[q]);
+                        if (on[q]) {
+                            a[q] = ld_stream(src);
+                            if constexpr (kHalves)
+                                if (two) b[q] = ld_stream(src + second);
                         }
-                        a[q] = narrow<kType>(x);
                     }
-                    __stcs(reinterpret_cast<uint4 *>(n[q].dst), a[q]);
-                    if (kHalves && n[q].pair != -1) __stcs(reinterpret_cast<uint4 *>(n[q].dst + second), b[q]);
-                }
-            } else {
-                const int64_t next = kHalves ? second : kElem;
 #pragma unroll
-                for (int q = 0; q < kInFlight; ++q) {
-                    const uint32_t u = u0 + q * kThreads;
-                    if (u >= units || !locate(u, n[q])) continue;
-                    const float x = load1<kType>(n[q].src);
-                    if (n[q].pair == -1) {
-                        store1<kType>(n[q].dst, x);
-                        continue;
+                    for (int q = 0; q < kInFlight; ++q) {
+                        if (!on[q]) continue;
+                        if (cs[q]) {
+                            float x[kV], y[kV];
+                            widen<kType>(a[q], x);
+                            if constexpr (kHalves) {
+                                widen<kType>(b[q], y);
+#pragma unroll
+                                for (int e = 0; e < kV; ++e) {
+                                    const float2 r = rotate(x[e], y[e], cs[q][e]);
+                                    x[e] = r.x;
+                                    y[e] = r.y;
+                                }
+                                b[q] = narrow<kType>(y);
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < kV; e += 2) {
+                                    const float2 r = rotate(x[e], x[e + 1], cs[q][e / 2]);
+                                    x[e] = r.x;
+                                    x[e + 1] = r.y;
+                                }
+                            }
+                            a[q] = narrow<kType>(x);
+                        }
+                        __stcs(reinterpret_cast<uint4 *>(dst[q]), a[q]);
+                        if constexpr (kHalves)
+                            if (two) __stcs(reinterpret_cast<uint4 *>(dst[q] + second), b[q]);
                     }
-                    const float y = load1<kType>(n[q].src + next);
-                    const float2 r = n[q].pair == -2 ? make_float2(x, y) : rotate(x, y, n[q].cs[n[q].pair]);
-                    store1<kType>(n[q].dst, r.x);
-                    store1<kType>(n[q].dst + next, r.y);
+                } else {
+                    const int64_t next = kHalves ? second : kElem;
+                    float x[kInFlight], y[kInFlight];
+#pragma unroll
+                    for (int q = 0; q < kInFlight; ++q) {
+                        const uint32_t row = row0 + q * p.rows_at_once;
+                        on[q] = row < rows && locate(row, src, dst[q], cs[q]);
+                        if (on[q]) {
+                            x[q] = load1<kType>(src);
+                            if (two) y[q] = load1<kType>(src + next);
+                        }
+                    }
+#pragma unroll
+                    for (int q = 0; q < kInFlight; ++q) {
+                        if (!on[q]) continue;
+                        if (cs[q]) {
+                            const float2 r = rotate(x[q], y[q], *cs[q]);
+                            x[q] = r.x;
+                            y[q] = r.y;
+                        }
+                        store1<kType>(dst[q], x[q]);
+                        if (two) store1<kType>(dst[q] + next, y[q]);
+                    }
                 }
             }
         }
@@ -425,21 +422,24 @@ int run(AxesParams &p, int32_t dtype, bool halves, bool vec, const int32_t *sect
     const int v = vec ? 16 / elem_of(dtype) : 1;
     const int rest = (p.head_dim - 2 * p.pairs) / v;   // units that are only copied
     p.rotating = halves || !vec ? p.pairs / v : 2 * p.pairs / v;
-    const uint32_t per_head = uint32_t(p.rotating + rest);
-    p.per_head = make_fastdiv(per_head);
-    p.per_token = make_fastdiv(per_head * uint32_t(p.heads[0] + p.heads[1] + p.heads[2]));
+    p.per_head = p.rotating + rest;
+    p.heads_all = make_fastdiv(uint32_t(p.heads[0] + p.heads[1] + p.heads[2]));
+    p.lanes = make_fastdiv(uint32_t(std::min(p.per_head, kThreads)));
+    p.rows_at_once = kThreads / p.lanes.d;
     p.end0 = sections[0];
     p.end1 = sections[0] + sections[1];
-    // a tile's cos and sin: 32 KB at most, and tokens for every block while there are any
-    int tile = std::min(kMaxTile, std::max(1, 4096 / std::max(p.pairs, 1)));
-    tile = std::min(tile, std::max(1, p.tokens / (4 * sms)));
+    // Tiles of one size for every resident block: cos and sin of a tile take 16 KB,
+    // or a token's, and their frequencies as much as a token's.
+    const int most = std::min(kMaxTile, std::max(1, 2048 / std::max(p.pairs, 1))), blocks = sms * kBlocks;
+    const int rounds = int((int64_t(p.tokens) + int64_t(blocks) * most - 1) / (int64_t(blocks) * most));
+    const int tile = int((int64_t(p.tokens) + int64_t(blocks) * rounds - 1) / (int64_t(blocks) * rounds));
     p.tile = tile;
     const size_t smem = size_t(tile + 1) * p.pairs * sizeof(float2);
     const int tiles = (p.tokens + tile - 1) / tile;
     const Kernel<kAppend> fn = dtype == ROPE3D_BF16  ? kernel_of<kAppend, ROPE3D_BF16>(halves, vec)
                                : dtype == ROPE3D_F16 ? kernel_of<kAppend, ROPE3D_F16>(halves, vec)
                                                      : kernel_of<kAppend, ROPE3D_F32>(halves, vec);
-    const int rc = launch(fn, dim3(unsigned(std::min(tiles, sms * 16))), kThreads, smem, st, p);
+    const int rc = launch(fn, dim3(unsigned(std::min(tiles, blocks))), kThreads, smem, st, p);
     if (rc == ROPE3D_OK) t_axes_kernel = vec ? 1 : 2;
     return rc;
 }

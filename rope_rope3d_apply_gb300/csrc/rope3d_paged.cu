@@ -37,6 +37,7 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kWarpKeys = 16;                    // places of a block that one warp takes
 constexpr int kKeys = kWarpKeys * kWarps;        // places of a block
 constexpr int kRows = kFewRows;
+constexpr int kMostParts = 3 * kTileParts;       // see kPerSm
 
 // Stages of a warp's ring, and blocks that fit an SM beside one another with them.
 template <int kD> constexpr int kStagesOf = kD == 64 ? 4 : 3;
@@ -355,6 +356,7 @@ template <bool kF16, int kTile, int kKeysOf>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ AttnParams p) {
     __shared__ float4 s_v[kJoinThreads];
     __shared__ float s_l[kJoinThreads], s_m[kJoinThreads];
+    __shared__ int s_part[kJoinThreads];   // the item's parts: the part, negative (~part) in its first slot
     rope3d_tc::grid_release();
     rope3d_tc::grid_wait();
     const int c = blockIdx.x, tid = threadIdx.x;
@@ -364,8 +366,26 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     int from = c - 1;   // the part before: the item's first part, or the cut is not its first
     while (from > 0 && p.notes[from].begin == p.notes[from].end) --from;
     if (p.notes[from].begin > first) return;
-    int to = c + 1;     // the parts of the item: from, c .. to - 1
-    while (to < p.parts && p.notes[to].begin < n.item + n.cost) ++to;
+    // the parts of the item: `from`, and those from c on that begin in it (parts without
+    // blocks between them have none of it)
+    static_assert(kMostParts < kJoinThreads, "a part to a thread");
+    const int part = c + tid;
+    bool its = part < p.parts;
+    if (its) {
+        const long long begin = p.notes[part].begin;
+        its = begin < n.item + n.cost && begin < p.notes[part].end;
+    }
+    {
+        const uint32_t bits = __ballot_sync(0xffffffffu, its);
+        if ((tid & 31) == 0) s_part[tid >> 5] = __popc(bits);
+        __syncthreads();
+        int before = 1 + __popc(bits & ((1u << (tid & 31)) - 1u));
+        for (int w = 0; w < tid >> 5; ++w) before += s_part[w];
+        __syncthreads();
+        if (its) s_part[before] = ~part;
+        if (tid == 0) s_part[0] = from;
+    }
+    const int parts = __syncthreads_count(its) + 1;
 
     Item it;
     it.s = n.s;
@@ -375,7 +395,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     it.rows = int(min(uint32_t(kTile), uint32_t(it.q.n) * p.group.d - uint32_t(n.t) * kTile));
     const int row0 = blockIdx.y * kJoinRows, rows = min(kJoinRows, it.rows - row0);
     if (rows <= 0) return;
-    const int vecs = p.head_dim / 4, count = rows * vecs, parts = to - c + 1;
+    const int vecs = p.head_dim / 4, count = rows * vecs;
     int shares = 1;     // threads to a vector
     while (2 * shares * count <= kJoinThreads && 2 * shares <= parts) shares *= 2;
     for (int i0 = 0; i0 < count; i0 += kJoinThreads / shares) {
@@ -385,21 +405,23 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
         float m = -INFINITY, l = 0.f;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (on) {
-            for (int k0 = share; k0 < parts; k0 += 4 * shares) {   // four parts' loads at a time
-                float pm[4], pl[4];
-                float4 pv[4];
+            constexpr int kAtOnce = 8;   // parts' loads at a time
+            for (int k0 = share; k0 < parts; k0 += kAtOnce * shares) {
+                float pm[kAtOnce], pl[kAtOnce];
+                float4 pv[kAtOnce];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int k = k0 + j * shares, part = k == 0 ? from : c + k - 1;
+                for (int j = 0; j < kAtOnce; ++j) {
+                    const int k = k0 + j * shares;
                     pm[j] = -INFINITY;
-                    if (k >= parts || p.notes[part].begin == p.notes[part].end) continue;
-                    const float *slot = slot_of<kTile>(p, part, p.notes[part].begin > first);
+                    if (k >= parts) continue;
+                    const int of = s_part[k];
+                    const float *slot = slot_of<kTile>(p, of < 0 ? ~of : of, of < 0);
                     pm[j] = slot[vecs * kTile * 4 + r];
                     pl[j] = slot[vecs * kTile * 4 + kTile + r];
                     pv[j] = *reinterpret_cast<const float4 *>(slot + (v4 * kTile + r) * 4);
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < kAtOnce; ++j) {
                     if (pm[j] == -INFINITY) continue;
                     const float big = fmaxf(m, pm[j]), a = m == -INFINITY ? 0.f : ex2(m - big), b = ex2(pm[j] - big);
                     v.x = v.x * a + pv[j].x * b;
@@ -483,7 +505,7 @@ Choice choose(const rope3d_paged_attention_args &a) {
     Choice c{};
     c.tiles = most * group > kFewRows && tiles_fit(a);
     const int64_t rows = c.tiles ? kTileRows : kFewRows, keys = c.tiles ? 128 : kKeys;
-    const int limit = c.tiles ? kTileParts : 152 * (a.head_dim <= 64 ? kPerSm<64> : a.head_dim <= 128 ? kPerSm<128> : kPerSm<256>);
+    const int limit = c.tiles ? kTileParts : kTileParts * (a.head_dim <= 64 ? kPerSm<64> : a.head_dim <= 128 ? kPerSm<128> : kPerSm<256>);
     // no more parts than blocks there can be
     const int64_t items = (a.tokens * group + rows - 1) / rows + std::min(b.seqs, a.tokens);
     const int64_t blocks = (b.table_width * b.page_size + keys - 1) / keys;
@@ -544,6 +566,8 @@ int attention(const rope3d_paged_attention_args *a, bool go, bool check_device, 
     p.batch = device_batch(b, T);
     p.group = rope3d::make_fastdiv(uint32_t(H / K));
     p.page = rope3d::make_fastdiv(uint32_t(b.page_size));
+    p.span = rope3d::make_fastdiv(uint32_t(H / K) * (c.tiles ? 1 : kKeys / kRows));
+    p.cuts = rope3d::make_fastdiv(uint32_t(c.parts));
     // measured in _COST_
     p.item_cost = 2;
     p.kv_heads = int(K);

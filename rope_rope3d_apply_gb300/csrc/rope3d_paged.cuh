@@ -30,6 +30,8 @@ struct AttnParams {
     Batch batch;
     rope3d::FastDiv group;          // query heads of a key/value head
     rope3d::FastDiv page;           // places of a page
+    rope3d::FastDiv span;           // kKeys * group / kRows: tiles whose rows' keys end in one block
+    rope3d::FastDiv cuts;           // parts
     int item_cost;                  // what an item costs besides its blocks, in blocks
     int kv_heads, head_dim;
     int causal, window;             // window 0: none
@@ -90,20 +92,20 @@ __device__ __forceinline__ Tile tile_of(const AttnParams &p, const Seq &q, int t
 // 1) / G)) / K) = floor((a + u) / D) blocks from place 0 on, where D = K G / T and a =
 // floor((G (past + K) + T - 1) / T), and a window leaves out floor((c + u) / D) of
 // them, c = floor(G (past - window + 1) / T): sums of floors in a row.
-__device__ __forceinline__ long long floors(long long n, int d) {   // sum of floor(i / d) over 0 <= i < n
-    const long long q = n / d;
+__device__ __forceinline__ long long floors(long long n, const rope3d::FastDiv &f) {   // sum of floor(i / d) over 0 <= i < n
+    const long long d = f.d, q = n < 0x7fffffff ? (long long)udiv(uint32_t(n), f) : n / d;
     return q * (q - 1) / 2 * d + q * (n - q * d);
 }
 
 template <int kRows, int kKeys>
 __device__ long long tiles_cost(const AttnParams &p, const Seq &q, int t) {
     static_assert(kKeys % kRows == 0 && (kRows == 128 || kRows == 16), "D is whole");
-    const int d = kKeys / kRows * int(p.group.d);
+    const rope3d::FastDiv &d = p.span;
     const long long group = p.group.d, past = q.len - q.n;
     long long sum;
     if (p.causal) {   // at least 1 each
         const long long a = (group * (past + kKeys) + kRows - 1) >> (kRows == 128 ? 7 : 4);
-        const long long ones = min(max(d - a, 0ll), (long long)t);
+        const long long ones = min(max((long long)d.d - a, 0ll), (long long)t);
         sum = ones + (t > ones ? floors(a + t, d) - floors(a + ones, d) : 0);
     } else {
         sum = (long long)max((q.len + kKeys - 1) / kKeys, 1) * t;
@@ -130,10 +132,16 @@ struct Start {
     int s, h, t, off;
 };
 
+// floor(total * part / parts)
+__device__ __forceinline__ long long cut(const AttnParams &p, long long total, int part) {
+    const long long whole = total < 0x7fffffff ? (long long)udiv(uint32_t(total), p.cuts) : total / p.parts;
+    return whole * part + udiv(uint32_t(total - whole * p.parts) * uint32_t(part), p.cuts);
+}
+
 template <int kRows, int kKeys, int kThreads>
 __device__ void find_start(const AttnParams &p, int part, Start *out, long long *s_sums) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int seqs = p.batch.seqs, each = (seqs + kThreads - 1) / kThreads;
+    const int seqs = p.batch.seqs, each = (seqs + kThreads - 1) / kThreads;   // (kThreads is a constant power of two)
     const int first = min(tid * each, seqs), end = min(first + each, seqs);
     long long sum = 0;
     for (int s = first; s < end; ++s) sum += seq_cost<kRows, kKeys>(p, seq_of<kRows>(p, s)) * p.kv_heads;
@@ -151,7 +159,7 @@ __device__ void find_start(const AttnParams &p, int part, Start *out, long long 
         if (w < warp) before += s_sums[w];
         total += s_sums[w];
     }
-    const long long begin = total * part / p.parts, stop = total * (part + 1) / p.parts;
+    const long long begin = cut(p, total, part), stop = cut(p, total, part + 1);
     if (begin < stop && begin >= before && begin < before + sum) {
         for (int s = first; s < end; ++s) {
             const Seq q = seq_of<kRows>(p, s);
@@ -161,7 +169,8 @@ __device__ void find_start(const AttnParams &p, int part, Start *out, long long 
                 continue;
             }
             out->s = s;
-            out->h = int((begin - before) / head);
+            const long long in = begin - before;
+            out->h = in < 0x7fffffff && head < 0x7fffffff ? int(uint32_t(in) / uint32_t(head)) : int(in / head);
             before += out->h * head;
             int t = 0, above = q.tiles;   // the last tile that begins at or before the cut
             while (above - t > 1) {

@@ -7,9 +7,9 @@
 // SM. What is copied where is read from device memory by the blocks themselves, so
 // nothing waits for the host.
 //
-// Compaction numbers the pages with a bitmap of the pages in use. One cluster of
-// eight blocks makes it (each marks an eighth of the tables' rows in its own shared
-// memory, and merges an eighth of the words), counts it, and writes the list of
+// Compaction numbers the pages with a bitmap of the pages in use. One block, or a cluster of
+// eight for large tables, makes it (each marks its share of the tables' rows in its own shared
+// memory, and merges its share of the words), counts it, and writes the list of
 // moves: with U pages in use, the k-th page in use at U or above goes to the k-th
 // free page below U. A second kernel rewrites the tables and copies the pages.
 #include <cuda_runtime.h>
@@ -29,6 +29,7 @@ using namespace rope3d_paged;
 constexpr int kThreads = 256;
 constexpr int kPiece = kThreads * 4 * 16;   // bytes a block copies at a time
 constexpr int kMarkBlocks = 8, kMarkThreads = 1024;
+constexpr int64_t kSmallTable = 8192;             // entries of a table that one block reads; see launch
 constexpr int64_t kMaxPages = int64_t(1) << 20;   // their bitmap is 128 KB of shared memory
 
 struct Planes {
@@ -152,17 +153,27 @@ __device__ int block_scan(int v, int *s_warp, int *total) {
     return before;
 }
 
-__global__ void __cluster_dims__(kMarkBlocks, 1, 1) __launch_bounds__(kMarkThreads)
+template <int kBlocks>
+__global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kMarkThreads)
     cache_mark_kernel(const __grid_constant__ CompactParams p) {
+    constexpr int kWords = kBlocks == 1 ? 1 : 4;   // of a thread
     extern __shared__ uint32_t s_map[];   // a bit for every page
     __shared__ int s_warp[32], s_share[2];
-    const int tid = threadIdx.x, rank = int(rope3d_tc::cluster_rank());
+    const int tid = threadIdx.x, rank = kBlocks == 1 ? 0 : int(rope3d_tc::cluster_rank());
+    auto meet = [] {
+        if constexpr (kBlocks == 1) __syncthreads();
+        else rope3d_tc::cluster_sync();
+    };
+    auto of_block = [](const void *at, int r) {   // a word of block r's shared memory
+        if constexpr (kBlocks == 1) return *static_cast<const uint32_t *>(at);
+        else return ld_cluster(rope3d_tc::map_rank(rope3d_tc::smem_u32(at), uint32_t(r)));
+    };
     const int words = (p.cache.pages + 31) / 32;
     for (int w = tid; w < words; w += kMarkThreads) s_map[w] = 0;
     rope3d_tc::grid_release();
     rope3d_tc::grid_wait();
     __syncthreads();
-    for (int s = rank * (kMarkThreads / 32) + (tid >> 5); s < p.seqs; s += kMarkBlocks * (kMarkThreads / 32)) {
+    for (int s = rank * (kMarkThreads / 32) + (tid >> 5); s < p.seqs; s += kBlocks * (kMarkThreads / 32)) {
         const int n = held(p, s);
         for (int j = tid & 31; j < n; j += 32) {
             const int e = p.table[s * p.table_stride + j];
@@ -170,20 +181,20 @@ __global__ void __cluster_dims__(kMarkBlocks, 1, 1) __launch_bounds__(kMarkThrea
         }
     }
     __syncthreads();
-    rope3d_tc::cluster_sync();
+    meet();
 
     // this block's words, of all eight maps: words in a row to a thread, so that a scan orders them
-    const int mine = (words + kMarkBlocks - 1) / kMarkBlocks, first = min(rank * mine, words), end = min(first + mine, words);
-    const int each = (mine + kMarkThreads - 1) / kMarkThreads;   // up to 4
-    uint32_t map[4];
+    const int mine = (words + kBlocks - 1) / kBlocks, first = min(rank * mine, words), end = min(first + mine, words);
+    const int each = (mine + kMarkThreads - 1) / kMarkThreads;   // up to kWords
+    uint32_t map[kWords];
     int ones = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kWords; ++i) {
         const int w = first + tid * each + i;
         map[i] = 0;
         if (i < each && w < end) {
-            for (int r = 0; r < kMarkBlocks; ++r)
-                map[i] |= ld_cluster(rope3d_tc::map_rank(rope3d_tc::smem_u32(&s_map[w]), uint32_t(r)));
+            for (int r = 0; r < kBlocks; ++r)
+                map[i] |= of_block(&s_map[w], r);
             ones += __popc(map[i]);
         }
     }
@@ -191,10 +202,10 @@ __global__ void __cluster_dims__(kMarkBlocks, 1, 1) __launch_bounds__(kMarkThrea
     int before = block_scan(ones, s_warp, &sum);
     if (tid == 0) s_share[0] = sum;
     __syncthreads();
-    rope3d_tc::cluster_sync();
+    meet();
     int total = 0, earlier = 0;
-    for (int r = 0; r < kMarkBlocks; ++r) {
-        const int n = int(ld_cluster(rope3d_tc::map_rank(rope3d_tc::smem_u32(&s_share[0]), uint32_t(r))));
+    for (int r = 0; r < kBlocks; ++r) {
+        const int n = int(of_block(&s_share[0], r));
         total += n;
         if (r < rank) earlier += n;
     }
@@ -206,7 +217,7 @@ __global__ void __cluster_dims__(kMarkBlocks, 1, 1) __launch_bounds__(kMarkThrea
     {
         int b = before;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kWords; ++i) {
             const int w = first + tid * each + i;
             if (i < each && w < end) {
                 if (total >> 5 == w) s_share[1] = b + __popc(map[i] & ((1u << (total & 31)) - 1u));
@@ -215,36 +226,36 @@ __global__ void __cluster_dims__(kMarkBlocks, 1, 1) __launch_bounds__(kMarkThrea
         }
     }
     __syncthreads();
-    rope3d_tc::cluster_sync();
+    meet();
     int low = 0;
-    for (int r = 0; r < kMarkBlocks; ++r)
-        low += int(ld_cluster(rope3d_tc::map_rank(rope3d_tc::smem_u32(&s_share[1]), uint32_t(r))));
+    for (int r = 0; r < kBlocks; ++r)
+        low += int(of_block(&s_share[1], r));
     if (total >> 5 >= words) low = total;   // every page is in use
 
     int b = before;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kWords; ++i) {
         const int w = first + tid * each + i;
         if (i >= each || w >= end) continue;
-        for (int bit = 0; bit < 32; ++bit) {
-            const int page = w * 32 + bit;
-            if (page >= p.cache.pages) break;
-            if (map[i] >> bit & 1u) {
-                if (page >= total) {
-                    p.src[b - low] = page;
-                    p.rank[page] = b - low;
-                }
-                ++b;
-            } else if (page < total) {
-                p.dst[page - b] = page;
-            }
+        // pages in use at `total` or above, then free ones below it
+        const int from = total - w * 32;
+        const uint32_t below = from <= 0 ? 0u : from >= 32 ? 0xffffffffu : (1u << from) - 1u;
+        for (uint32_t high = map[i] & ~below; high; high &= high - 1) {
+            const int bit = __ffs(int(high)) - 1, place = b + __popc(map[i] & ((1u << bit) - 1u)) - low;
+            p.src[place] = w * 32 + bit;
+            p.rank[w * 32 + bit] = place;
         }
+        for (uint32_t hole = ~map[i] & below; hole; hole &= hole - 1) {
+            const int bit = __ffs(int(hole)) - 1;
+            p.dst[w * 32 + bit - b - __popc(map[i] & ((1u << bit) - 1u))] = w * 32 + bit;
+        }
+        b += __popc(map[i]);
     }
     if (rank == 0 && tid == 0) {
         *p.moves = total - low;
         *p.used = total;
     }
-    rope3d_tc::cluster_sync();   // no block leaves while another still reads its shared memory
+    if constexpr (kBlocks > 1) meet();   // no block leaves while another still reads its shared memory
 }
 
 __global__ void __launch_bounds__(kThreads) cache_move_kernel(const __grid_constant__ CompactParams p) {
@@ -390,15 +401,19 @@ int compact(const rope3d_cache_compact_args *a, bool go, bool check_device, int6
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return ROPE3D_ERR_CUDA;
     if (!ready[dev].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(cache_mark_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMaxPages / 8)) != cudaSuccess) {
+        if (cudaFuncSetAttribute(cache_mark_kernel<kMarkBlocks>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMaxPages / 8)) !=
+            cudaSuccess) {
             cudaGetLastError();
             return ROPE3D_ERR_CUDA;
         }
         ready[dev].store(true, std::memory_order_release);
     }
-    rc = launch(cache_mark_kernel, dim3(kMarkBlocks), kMarkThreads, smem, st, p);
+    const int64_t entries = a->seqs * a->table_width;
+    if (entries <= kSmallTable && a->pages <= kMarkThreads * 32) rc = launch(cache_mark_kernel<1>, dim3(1), kMarkThreads, smem, st, p);
+    else rc = launch(cache_mark_kernel<kMarkBlocks>, dim3(kMarkBlocks), kMarkThreads, smem, st, p);
     if (rc != ROPE3D_OK) return rc;
-    return launch(cache_move_kernel, dim3(unsigned(sms * 8)), kThreads, 0, st, p);
+    const int64_t most = std::max((entries + kThreads - 1) / kThreads, a->pages / 2 * p.cache.planes * p.cache.pieces);
+    return launch(cache_move_kernel, dim3(unsigned(std::min<int64_t>(std::max<int64_t>(most, 1), sms * 8))), kThreads, 0, st, p);
 }
 
 }  // namespace
