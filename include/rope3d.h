@@ -628,8 +628,8 @@ int rope3d_testing_ffn_wait_timeouts(int64_t *count, int32_t reset);
  * width), given token by token: pair j of every head of token t turns by
  *     angle = positions[axis(j)][t] * freqs[j],
  *     y_a = a cos(angle) - b sin(angle),  y_b = a sin(angle) + b cos(angle)
- * sections[x] pairs belong to axis x, in order; pairs = their sum, and channels
- * from 2 * pairs on are copied. Where rope3d_apply_pair rotates whole grids that
+ * sections[x] pairs belong to axis x, in order; pairs = their sum (1 to 1024), and
+ * channels from 2 * pairs on are copied. Where rope3d_apply_pair rotates whole grids that
  * start at 0 from tables, this takes packed clips and pictures of any sizes,
  * tiles at an offset, text among them, and K with fewer heads than Q. inverse = 1
  * turns by -angle: the gradient of the operator from the gradient of its output.

@@ -1054,33 +1054,38 @@ def rope3d_testing_ffn_wait_timeouts(reset: bool = True) -> int:
 # ---- a paged cache ---------------------------------------------------------
 
 
-def _rows3(name, t, tokens, heads, dim, dtype):
-    """(token stride, head stride) of [tokens, heads, dim]; zeros for None."""
+def _rows3(name, t, want, dtype):
+    """(token stride, head stride) of a tensor of shape `want`; zeros for None."""
     if t is None:
         return 0, 0
-    shape = t.shape
-    if len(shape) != 3 or shape[0] != tokens or shape[1] != heads or shape[2] != dim:
-        raise ValueError(f"{name} has shape {tuple(shape)}, expected {(tokens, heads, dim)}")
+    if t.shape != want:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(want)}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
     a, b, one = t.stride()
-    if one != 1 and dim > 1:
+    if one != 1 and want[2] > 1:
         raise ValueError(f"{name} must have contiguous channels")
     return a, b
 
 
-def _cache4(name, t, heads, dim, dtype, like=None):
-    """(page stride, place stride, head stride) of [pages, page_size, heads, dim]."""
-    shape = t.shape
-    if len(shape) != 4 or shape[2] != heads or shape[3] != dim or (like is not None and like.shape != shape):
-        want = tuple(like.shape) if like is not None else ("pages", "page_size", heads, dim)
-        raise ValueError(f"{name} has shape {tuple(shape)}, expected {want}")
+def _cache4(name, t, want, dtype):
+    """(page stride, place stride, head stride) of a cache of shape `want`."""
+    if t.shape != want:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(want)}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
     a, b, c, one = t.stride()
-    if one != 1 and dim > 1:
+    if one != 1 and want[3] > 1:
         raise ValueError(f"{name} must have contiguous channels")
     return a, b, c
+
+
+def _cache_shape(cache, heads, dim):
+    """[pages, page_size, heads, dim] of a cache (heads None: any)."""
+    shape = cache.shape
+    if len(shape) != 4 or shape[3] != dim or (heads is not None and shape[2] != heads):
+        raise ValueError(f"k_cache has shape {tuple(shape)}, expected [pages, page_size, {heads or 'heads'}, {dim}]")
+    return shape
 
 
 def _ints(name, t, count=None):
@@ -1089,7 +1094,8 @@ def _ints(name, t, count=None):
         return 0
     if t.dtype is not _torch.int32:
         raise TypeError(f"{name} is {t.dtype}, expected torch.int32")
-    if len(t.shape) != 1 or (count is not None and t.shape[0] != count) or (t.shape[0] > 1 and t.stride(0) != 1):
+    shape = t.shape
+    if len(shape) != 1 or (count is not None and shape[0] != count) or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous, [{'n' if count is None else count}]")
     return t.data_ptr()
 
@@ -1098,9 +1104,13 @@ def _table(name, t, seqs):
     """(entries of a row, row stride) of a page table [seqs, entries]."""
     if t.dtype is not _torch.int32:
         raise TypeError(f"{name} is {t.dtype}, expected torch.int32")
-    if len(t.shape) != 2 or t.shape[0] != seqs or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be [{seqs}, entries] with contiguous rows")
-    return t.shape[1], t.stride(0) if seqs > 1 else max(t.shape[1], 1)
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != seqs:
+        raise ValueError(f"{name} must be [{seqs}, entries]")
+    ld, one = t.stride()
+    if one != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return shape[1], ld if seqs > 1 else max(shape[1], 1)
 
 
 def _counter(name, t):
@@ -1111,19 +1121,20 @@ def _counter(name, t):
 
 
 def _batch_fields(page_table, seq_lens, q_starts, cache):
-    """The fields of rope3d_paged_batch: (addresses, sizes)."""
-    seqs = seq_lens.shape[0] if len(seq_lens.shape) == 1 else -1
+    """The fields of rope3d_paged_batch, with a cache of shape `cache`."""
+    lens = _ints("seq_lens", seq_lens)
+    seqs = seq_lens.shape[0]
     width, ld = _table("page_table", page_table, seqs)
-    return ((page_table.data_ptr(), _ints("seq_lens", seq_lens), _ints("q_starts", q_starts, seqs + 1)),
-            (seqs, width, ld, cache.shape[0], cache.shape[1]))
+    return page_table.data_ptr(), lens, _ints("q_starts", q_starts, seqs + 1), seqs, width, ld, cache[0], cache[1]
 
 
 def _rotation_fields(positions, freqs, sections, tokens):
     """(sections, position type, positions' row stride) of a rotation."""
-    if freqs.dtype is not _torch.float32 or len(freqs.shape) != 1 or (freqs.shape[0] > 1 and freqs.stride(0) != 1):
+    if freqs.dtype is not _torch.float32 or freqs.dim() != 1 or not freqs.is_contiguous():
         raise ValueError("freqs must be float32, contiguous, [pairs]")
-    sections = (freqs.shape[0], 0, 0) if sections is None else (*sections, 0, 0)[:3] if len(sections) <= 3 else None
-    if sections is None or sum(sections) != freqs.shape[0]:
+    pairs = freqs.shape[0]
+    sections = (pairs, 0, 0) if sections is None else (*sections, 0, 0)[:3] if len(sections) <= 3 else None
+    if sections is None or sections[0] + sections[1] + sections[2] != pairs:
         raise ValueError("sections must be up to three counts of pairs that make up freqs")
     if positions is None:
         return sections, 0, 0
@@ -1157,18 +1168,19 @@ def rope3d_apply_axes(q, k, positions, freqs, sections=None, pairing: int = PAIR
     if stream is not None and (there := _elsewhere(rope3d_apply_axes, dict(locals()), "q")) is not None:
         return there
     _torch or _use_torch()
-    if len(q.shape) != 3:
+    shape = q.shape
+    if len(shape) != 3:
         raise ValueError("q must be [tokens, heads, head_dim]")
-    (tokens, heads, dim), dt = q.shape, q.dtype
-    k_heads = 0 if k is None or len(k.shape) != 3 else k.shape[1]
+    (tokens, heads, dim), dt = shape, q.dtype
+    k_shape = (tokens, 0 if k is None or k.dim() != 3 else k.shape[1], dim)
     sections, kind, ld = _rotation_fields(positions, freqs, sections, tokens)
     q_out = _fresh(q) if q_out is None else q_out
     if k is not None and k_out is None:
         k_out = _fresh(k)
     args = _AxesArgs.pack(
         q.data_ptr(), _ptr_of(k), q_out.data_ptr(), _ptr_of(k_out), positions.data_ptr(), freqs.data_ptr(), tokens, heads,
-        k_heads, dim, *_rows3("q", q, tokens, heads, dim, dt), *_rows3("k", k, tokens, k_heads, dim, dt),
-        *_rows3("q_out", q_out, tokens, heads, dim, dt), *_rows3("k_out", k_out, tokens, k_heads, dim, dt), ld, *sections,
+        k_shape[1], dim, *_rows3("q", q, shape, dt), *_rows3("k", k, k_shape, dt), *_rows3("q_out", q_out, shape, dt),
+        *_rows3("k_out", k_out, k_shape, dt), ld, *sections,
         _code(q), kind, pairing, 1 if inverse else 0)
     rc = (_lib or load_library()).rope3d_apply_axes(args, _raw_stream(stream, q))
     if rc:
@@ -1196,10 +1208,12 @@ def rope3d_cache_append(q, k, v, k_cache, v_cache, page_table, seq_lens, q_start
     if stream is not None and (there := _elsewhere(lambda **a: (rope3d_cache_append(**a),), dict(locals()), "k")) is not None:
         return there[0]
     _torch or _use_torch()
-    if len(k.shape) != 3:
+    shape = k.shape
+    if len(shape) != 3:
         raise ValueError("k must be [tokens, kv_heads, head_dim]")
-    (tokens, kv, dim), dt = k.shape, k.dtype
-    heads = 0 if q is None or len(q.shape) != 3 else q.shape[1]
+    (tokens, kv, dim), dt = shape, k.dtype
+    q_shape = (tokens, 0 if q is None or q.dim() != 3 else q.shape[1], dim)
+    cache = _cache_shape(k_cache, kv, dim)
     if freqs is None:
         if sections is not None:
             raise ValueError("sections without freqs")
@@ -1208,13 +1222,11 @@ def rope3d_cache_append(q, k, v, k_cache, v_cache, page_table, seq_lens, q_start
         sections, kind, ld = _rotation_fields(positions, freqs, sections, tokens)
     if q is not None and q_out is None:
         q_out = _fresh(q)
-    pointers, sizes = _batch_fields(page_table, seq_lens, q_starts, k_cache)
     args = _AppendArgs.pack(
         _ptr_of(q), _ptr_of(q_out), k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr_of(positions),
-        _ptr_of(freqs), _counter("invalid_count", invalid_count), *pointers, *sizes, tokens, heads, kv, dim,
-        *_rows3("q", q, tokens, heads, dim, dt), *_rows3("q_out", q_out, tokens, heads, dim, dt),
-        *_rows3("k", k, tokens, kv, dim, dt), *_rows3("v", v, tokens, kv, dim, dt),
-        *_cache4("k_cache", k_cache, kv, dim, dt), *_cache4("v_cache", v_cache, kv, dim, dt, k_cache), ld, *sections,
+        _ptr_of(freqs), _counter("invalid_count", invalid_count), *_batch_fields(page_table, seq_lens, q_starts, cache), tokens,
+        q_shape[1], kv, dim, *_rows3("q", q, q_shape, dt), *_rows3("q_out", q_out, q_shape, dt), *_rows3("k", k, shape, dt),
+        *_rows3("v", v, shape, dt), *_cache4("k_cache", k_cache, cache, dt), *_cache4("v_cache", v_cache, cache, dt), ld, *sections,
         _code(k), kind, pairing)
     rc = (_lib or load_library()).rope3d_cache_append(args, _raw_stream(stream, k))
     if rc:
@@ -1237,21 +1249,21 @@ def rope3d_paged_attention(q, k_cache, v_cache, page_table, seq_lens, q_starts=N
     if stream is not None and (there := _elsewhere(rope3d_paged_attention, dict(locals()), "q")) is not None:
         return there
     _torch or _use_torch()
-    if len(q.shape) != 3:
+    shape = q.shape
+    if len(shape) != 3:
         raise ValueError("q must be [tokens, heads, head_dim]")
-    (tokens, heads, dim), dt = q.shape, q.dtype
-    kv = k_cache.shape[2] if len(k_cache.shape) == 4 else -1
+    (tokens, heads, dim), dt = shape, q.dtype
+    cache = _cache_shape(k_cache, None, dim)
     if out is None:
         out = _fresh(q)
     if lse is True:
         lse = _new((tokens, heads), _torch.float32, q)
     elif lse is False:
         lse = None
-    pointers, sizes = _batch_fields(page_table, seq_lens, q_starts, k_cache)
-    body = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), _ptr_of(lse), *pointers, *sizes, tokens, heads,
-            kv, dim, *_rows3("q", q, tokens, heads, dim, dt), *_rows3("out", out, tokens, heads, dim, dt),
-            _stride("lse", lse, tokens, heads, _torch.float32), *_cache4("k_cache", k_cache, kv, dim, dt),
-            *_cache4("v_cache", v_cache, kv, dim, dt, k_cache), window, max_new or 0)
+    body = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), _ptr_of(lse),
+            *_batch_fields(page_table, seq_lens, q_starts, cache), tokens, heads, cache[2], dim, *_rows3("q", q, shape, dt),
+            *_rows3("out", out, shape, dt), _stride("lse", lse, tokens, heads, _torch.float32),
+            *_cache4("k_cache", k_cache, cache, dt), *_cache4("v_cache", v_cache, cache, dt), window, max_new or 0)
     tail = (dim ** -0.5 if scale is None else scale, _code(q), 1 if causal else 0)
     st = _raw_stream(stream, q)
     args, ws = _workspace(_AttentionArgs, (body, tail), "rope3d_paged_attention_workspace", "rope3d_paged_attention", workspace, q)
@@ -1285,11 +1297,11 @@ def rope3d_cache_fork(cache, page_table, seq_lens, parents, children, new_pages,
     if stream is not None and _elsewhere(lambda **a: (rope3d_cache_fork(**a),), dict(locals()), "cache") is not None:
         return
     _torch or _use_torch()
-    forks = parents.shape[0] if len(parents.shape) == 1 else -1
-    seqs = seq_lens.shape[0] if len(seq_lens.shape) == 1 else -1
+    lens, of = _ints("seq_lens", seq_lens), _ints("parents", parents)
+    forks, seqs = parents.shape[0], seq_lens.shape[0]
     width, ld = _table("page_table", page_table, seqs)
     args = _ForkArgs.pack(
-        cache.data_ptr(), page_table.data_ptr(), _ints("seq_lens", seq_lens), _ints("parents", parents, forks),
+        cache.data_ptr(), page_table.data_ptr(), lens, of,
         _ints("children", children, forks), _ints("new_pages", new_pages, forks), _counter("invalid_count", invalid_count),
         *_planes(cache), seqs, width, ld, cache.shape[2] if page_size is None else page_size, forks)
     _check((_lib or load_library()).rope3d_cache_fork(args, _raw_stream(stream, cache)), "rope3d_cache_fork")
@@ -1306,14 +1318,15 @@ def rope3d_cache_compact(cache, page_table, seq_lens, *, page_size=None, reserve
     if stream is not None and (there := _elsewhere(rope3d_cache_compact, dict(locals()), "cache")) is not None:
         return there
     _torch or _use_torch()
-    seqs = seq_lens.shape[0] if len(seq_lens.shape) == 1 else -1
+    lens = _ints("seq_lens", seq_lens)
+    seqs = seq_lens.shape[0]
     width, ld = _table("page_table", page_table, seqs)
     table_out = _fresh(page_table) if table_out is None else table_out
     used = _new((1,), _torch.int32, cache) if used is None else used
     width_out, ld_out = _table("table_out", table_out, seqs)
     if width_out != width:
         raise ValueError("table_out must have page_table's shape")
-    body = (cache.data_ptr(), page_table.data_ptr(), _ints("seq_lens", seq_lens), table_out.data_ptr(), _counter("used", used),
+    body = (cache.data_ptr(), page_table.data_ptr(), lens, table_out.data_ptr(), _counter("used", used),
             *_planes(cache), seqs, width, ld, ld_out, cache.shape[2] if page_size is None else page_size, reserve)
     st = _raw_stream(stream, cache)
     args, ws = _workspace(_CompactArgs, (body, ()), "rope3d_cache_compact_workspace", "rope3d_cache_compact", workspace, cache)

@@ -17,7 +17,7 @@
 // Each block takes tiles of a few tokens: cos and sin of the tile's tokens and pairs
 // go into shared memory once (64 sincospi a token instead of 64 for each of its
 // heads), then each thread moves 16-byte vectors at one place of head rows, four loads in
-// flight. What bounds it is memory.
+// flight; warps that are done with a tile prepare the next one's while the others move. What bounds it is memory.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -61,9 +61,11 @@ struct AxesParams {
     int end0, end1;            // pairs of axis 0; of axes 0 and 1
     int heads[3];              // q, k, v
     int per_head, rotating;    // units of a head row; those that rotate (the rest are copied)
-    FastDiv heads_all;         // head rows of a token
-    FastDiv lanes;             // threads to a head row
-    uint32_t rows_at_once;     // head rows of a block at a time
+    int heads_all;             // head rows of a token
+    // How a block's threads divide a tile: `lanes` to a head row, `heads_step` head rows
+    // of `tokens_step` tokens at a time.
+    FastDiv lanes, heads_step;
+    int tokens_step;
     int position_type;         // ROPE3D_POSITIONS_*; -1: the place in the sequence
     float sign;
 };
@@ -90,20 +92,6 @@ __device__ float2 turn_far(double pos, float freq) {
     float s, c;
     sincospif(2.0f * t, &s, &c);
     return make_float2(c, s);
-}
-
-// Position of token t on `axis`: as a float where it has one, else in fp64.
-__device__ __forceinline__ bool position(const AxesParams &p, int axis, int t, float &near, double &far) {
-    const int64_t at = axis * p.positions_stride + t;
-    if (p.position_type == ROPE3D_POSITIONS_F32) {
-        near = static_cast<const float *>(p.positions)[at];
-        return true;
-    }
-    const int64_t v = p.position_type == ROPE3D_POSITIONS_I64 ? static_cast<const int64_t *>(p.positions)[at]
-                                                              : static_cast<const int32_t *>(p.positions)[at];
-    near = float(v);
-    far = double(v);
-    return v >= -(1 << 24) && v <= (1 << 24);
 }
 
 // ---- elements --------------------------------------------------------------------
@@ -185,10 +173,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks) axes_kernel(const __grid_co
     constexpr int kElem = kType == ROPE3D_F32 ? 4 : 2;
     constexpr int kV = kVec ? 16 / kElem : 1;   // elements of a vector
     constexpr int kInFlight = kVec && kHalves ? 2 : 4;   // units of a thread's loads in flight: 64 bytes
-    extern __shared__ float2 s_cs[];            // [tile][pairs], then freq / 2 pi as (hi, lo) [pairs]
-    float2 *s_freq = s_cs + size_t(p.tile) * p.pairs;
-    __shared__ int64_t s_dst[2][kMaxTile];      // append: byte offsets in the caches, -1: nowhere
-    __shared__ int s_place[kMaxTile], s_live[kMaxTile];
+    extern __shared__ float2 s_tiles[];   // cos and sin, [2][tile][pairs], then freq / 2 pi as (hi, lo) [pairs]
+    const int tile_pairs = p.tile * p.pairs;
+    float2 *s_freq = s_tiles + 2 * tile_pairs;
+    __shared__ int64_t s_dst[2][2][kMaxTile];   // append: byte offsets in the caches, -1: nowhere
+    __shared__ int s_live[2][kMaxTile];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     rope3d_tc::grid_release();
@@ -199,16 +188,18 @@ __global__ void __launch_bounds__(kThreads, kBlocks) axes_kernel(const __grid_co
         s_freq[j] = make_float2(hi, float(f - double(hi)));
     }
     const int64_t second = int64_t(p.pairs) * kElem;
-    const uint32_t row_at = fdiv(uint32_t(tid), p.lanes);
-    const int at0 = row_at < p.rows_at_once ? tid - int(row_at * p.lanes.d) : p.per_head;   // (the last few have no row)
+    const uint32_t row = fdiv(uint32_t(tid), p.lanes);
+    const int token_at = int(fdiv(row, p.heads_step)), head_at = int(row - uint32_t(token_at) * p.heads_step.d);
+    const int at0 = token_at < p.tokens_step ? tid - int(row * p.lanes.d) : p.per_head;   // (the last few have no row)
 
-    for (int t0 = blockIdx.x * p.tile; t0 < p.tokens; t0 += gridDim.x * p.tile) {
+    // A warp's tokens of the tile at t0: their places, cosines and sines
+    auto prepare = [&](int t0, int buf) {
         const int count = min(p.tile, p.tokens - t0);
-        __syncthreads();   // the tile before is done with shared memory; s_freq is there
-        if constexpr (kAppend) {
-            if (tid < count) {
+        for (int i = warp; i < count; i += kThreads / 32) {
+            const int t = t0 + i;
+            int place = 0;
+            if constexpr (kAppend) {
                 const Batch &b = p.batch;
-                const int t = t0 + tid;
                 int s = 0, lo, hi, len;
                 if (b.starts) {   // the last sequence that starts at or before t
                     int above = b.seqs;
@@ -222,46 +213,64 @@ __global__ void __launch_bounds__(kThreads, kBlocks) axes_kernel(const __grid_co
                 }
                 sequence(b, s, lo, hi, len);
                 const bool live = t >= lo && t < hi;
-                const int place = len - hi + t;
-                int64_t k = -1, v = -1;
-                if (live) {
-                    const int slot_page = place < 0 ? -1 : b.table[s * b.table_stride + place / b.page_size];
-                    if (slot_page >= 0 && slot_page < b.pages) {
-                        const int slot = place % b.page_size;
-                        k = slot_page * p.page[0] + slot * p.slot[0];
-                        v = slot_page * p.page[1] + slot * p.slot[1];
-                    } else if (p.invalid) {
-                        atomicAdd(p.invalid, 1);
+                place = len - hi + t;
+                if (lane == 0) {
+                    int64_t k = -1, v = -1;
+                    if (live) {
+                        const int page = place < 0 ? -1 : b.table[s * b.table_stride + place / b.page_size];
+                        if (page >= 0 && page < b.pages) {
+                            const int slot = place % b.page_size;
+                            k = page * p.page[0] + slot * p.slot[0];
+                            v = page * p.page[1] + slot * p.slot[1];
+                        } else if (p.invalid) {
+                            atomicAdd(p.invalid, 1);
+                        }
                     }
+                    s_dst[buf][0][i] = k;
+                    s_dst[buf][1][i] = v;
+                    s_live[buf][i] = live;
                 }
-                s_dst[0][tid] = k;
-                s_dst[1][tid] = v;
-                s_place[tid] = place;
-                s_live[tid] = live;
+                if (!live) continue;
             }
-            __syncthreads();
-        }
-        for (int i = warp; i < count; i += kThreads / 32) {
-            if (kAppend && !s_live[i]) continue;
-            for (int j = lane; j < p.pairs; j += 32) {
-                float near;
-                double far = 0.0;
-                bool exact = true;
-                if (kAppend && p.position_type < 0) {
-                    near = float(s_place[i]);
-                    far = double(s_place[i]);
-                    exact = s_place[i] <= (1 << 24);
+            // lane x has the position on axis x; as a float where that is exact
+            int64_t whole = place;
+            float near = float(place);
+            bool exact = true;
+            if (!kAppend || p.position_type >= 0) {
+                const int axis = lane < 1 || p.end0 == p.pairs ? 0 : lane < 2 || p.end1 == p.pairs ? 1 : 2;   // (those that have pairs)
+                const int64_t at = axis * p.positions_stride + t;
+                if (p.position_type == ROPE3D_POSITIONS_F32) {
+                    near = static_cast<const float *>(p.positions)[at];
                 } else {
-                    exact = position(p, j < p.end0 ? 0 : j < p.end1 ? 1 : 2, t0 + i, near, far);
+                    whole = p.position_type == ROPE3D_POSITIONS_I64 ? static_cast<const int64_t *>(p.positions)[at]
+                                                                    : static_cast<const int32_t *>(p.positions)[at];
+                    exact = whole >= -(1 << 24) && whole <= (1 << 24);
+                    near = exact ? float(int(whole)) : 0.f;
                 }
-                float2 cs = exact ? turn(near, s_freq[j].x, s_freq[j].y) : turn_far(far, p.freqs[j]);
+            } else {
+                exact = place <= (1 << 24);
+            }
+            const bool all_near = __all_sync(0xffffffffu, exact);
+            for (int j0 = 0; j0 < p.pairs; j0 += 32) {
+                const int j = j0 + lane, axis = j < p.end0 ? 0 : j < p.end1 ? 1 : 2;
+                const float at = __shfl_sync(0xffffffffu, near, axis);
+                const int64_t far = all_near ? 0 : __shfl_sync(0xffffffffu, whole, axis);
+                const bool is_near = all_near || __shfl_sync(0xffffffffu, int(exact), axis);
+                if (j >= p.pairs) continue;
+                float2 cs = is_near ? turn(at, s_freq[j].x, s_freq[j].y) : turn_far(double(far), p.freqs[j]);
                 cs.y *= p.sign;
-                s_cs[i * p.pairs + j] = cs;
+                s_tiles[buf * tile_pairs + i * p.pairs + j] = cs;
             }
         }
-        __syncthreads();
-
-        const uint32_t rows = uint32_t(count) * p.heads_all.d;
+    };
+    __syncthreads();   // s_freq is there
+    const int step = int(gridDim.x) * p.tile;
+    int t0 = blockIdx.x * p.tile;
+    if (t0 < p.tokens) prepare(t0, 0);
+    for (int buf = 0; t0 < p.tokens; t0 += step, buf ^= 1) {
+        __syncthreads();   // this tile is prepared, and the one before moved
+        const int count = min(p.tile, p.tokens - t0);
+        const float2 *const s_cs = s_tiles + buf * tile_pairs;
         for (int at = at0; at < p.per_head; at += p.lanes.d) {
             // this thread's part of each of its rows: its first element and, where it turns, its
             // first pair (interleaved units lie in order; of halves', the first parts do, and behind
@@ -273,10 +282,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) axes_kernel(const __grid_co
             const int pair = kVec && !kHalves ? at * kV / 2 : at * kV;
             // both parts of a pair, where they are two loads
             const bool two = turning && (kHalves || !kVec);
-            const int64_t off = int64_t(first) * kElem;
-            auto locate = [&](uint32_t row, const char *&src, char *&dst, const float2 *&cs) {
-                const uint32_t i = fdiv(row, p.heads_all), t = uint32_t(t0) + i;
-                int h = int(row - i * p.heads_all.d), which = 0;
+            for (int head = head_at; head < p.heads_all; head += int(p.heads_step.d)) {
+                int h = head, which = 0;
                 if (h >= p.heads[0]) {
                     h -= p.heads[0];
                     which = 1;
@@ -285,89 +292,98 @@ __global__ void __launch_bounds__(kThreads, kBlocks) axes_kernel(const __grid_co
                         which = 2;
                     }
                 }
-                src = p.in[which].p + t * p.in[which].token + h * p.in[which].head + off;
-                dst = const_cast<char *>(p.out[which].p) + h * p.out[which].head + off;
-                cs = turning && which < 2 ? s_cs + i * p.pairs + pair : nullptr;
-                if (kAppend && which > 0) {
-                    const int64_t d = s_dst[which - 1][i];
-                    dst += d;
-                    return d >= 0;
-                }
-                dst += t * p.out[which].token;
-                return !kAppend || s_live[i] != 0;
-            };
-            for (uint32_t row0 = row_at; row0 < rows; row0 += p.rows_at_once * kInFlight) {
-                const char *src;
-                char *dst[kInFlight];
-                const float2 *cs[kInFlight];
-                bool on[kInFlight];
-                if constexpr (kVec) {
-                    uint4 a[kInFlight], b[kHalves ? kInFlight : 1];
-#pragma unroll
-                    for (int q = 0; q < kInFlight; ++q) {
-                        const uint32_t row = row0 + q * p.rows_at_once;
-                        on[q] = row < rows && locate(row, src, dst[q], cs[q]);
-                        if (on[q]) {
-                            a[q] = ld_stream(src);
-                            if constexpr (kHalves)
-                                if (two) b[q] = ld_stream(src + second);
-                        }
+                const Rows &in = p.in[which], &out = p.out[which];
+                const char *const from = in.p + t0 * in.token + h * in.head + int64_t(first) * kElem;
+                char *const to = const_cast<char *>(out.p) + t0 * out.token + h * out.head + int64_t(first) * kElem;
+                const bool turns = turning && which < 2;
+                const float2 *const cs = s_cs + pair;
+                // token i's place; false where it has none
+                auto place = [&](int i, char *&dst) {
+                    if (kAppend && which > 0) {
+                        const int64_t d = s_dst[buf][which - 1][i];
+                        dst = to + d;   // (the caches' token strides are 0)
+                        return d >= 0;
                     }
+                    dst = to + i * out.token;
+                    return !kAppend || s_live[buf][i] != 0;
+                };
+                for (int i0 = token_at; i0 < count; i0 += p.tokens_step * kInFlight) {
+                    bool on[kInFlight];
+                    char *dst;
+                    if constexpr (kVec) {
+                        uint4 a[kInFlight], b[kHalves ? kInFlight : 1];
 #pragma unroll
-                    for (int q = 0; q < kInFlight; ++q) {
-                        if (!on[q]) continue;
-                        if (cs[q]) {
-                            float x[kV], y[kV];
-                            widen<kType>(a[q], x);
-                            if constexpr (kHalves) {
-                                widen<kType>(b[q], y);
-#pragma unroll
-                                for (int e = 0; e < kV; ++e) {
-                                    const float2 r = rotate(x[e], y[e], cs[q][e]);
-                                    x[e] = r.x;
-                                    y[e] = r.y;
-                                }
-                                b[q] = narrow<kType>(y);
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < kV; e += 2) {
-                                    const float2 r = rotate(x[e], x[e + 1], cs[q][e / 2]);
-                                    x[e] = r.x;
-                                    x[e + 1] = r.y;
-                                }
+                        for (int q = 0; q < kInFlight; ++q) {
+                            const int i = i0 + q * p.tokens_step;
+                            on[q] = i < count && place(i, dst);
+                            if (on[q]) {
+                                a[q] = ld_stream(from + i * in.token);
+                                if constexpr (kHalves)
+                                    if (two) b[q] = ld_stream(from + i * in.token + second);
                             }
-                            a[q] = narrow<kType>(x);
                         }
-                        __stcs(reinterpret_cast<uint4 *>(dst[q]), a[q]);
-                        if constexpr (kHalves)
-                            if (two) __stcs(reinterpret_cast<uint4 *>(dst[q] + second), b[q]);
-                    }
-                } else {
-                    const int64_t next = kHalves ? second : kElem;
-                    float x[kInFlight], y[kInFlight];
 #pragma unroll
-                    for (int q = 0; q < kInFlight; ++q) {
-                        const uint32_t row = row0 + q * p.rows_at_once;
-                        on[q] = row < rows && locate(row, src, dst[q], cs[q]);
-                        if (on[q]) {
-                            x[q] = load1<kType>(src);
-                            if (two) y[q] = load1<kType>(src + next);
-                        }
-                    }
+                        for (int q = 0; q < kInFlight; ++q) {
+                            if (!on[q]) continue;
+                            const int i = i0 + q * p.tokens_step;
+                            if (turns) {
+                                const float2 *c = cs + i * p.pairs;
+                                float x[kV], y[kV];
+                                widen<kType>(a[q], x);
+                                if constexpr (kHalves) {
+                                    widen<kType>(b[q], y);
 #pragma unroll
-                    for (int q = 0; q < kInFlight; ++q) {
-                        if (!on[q]) continue;
-                        if (cs[q]) {
-                            const float2 r = rotate(x[q], y[q], *cs[q]);
-                            x[q] = r.x;
-                            y[q] = r.y;
+                                    for (int e = 0; e < kV; ++e) {
+                                        const float2 r = rotate(x[e], y[e], c[e]);
+                                        x[e] = r.x;
+                                        y[e] = r.y;
+                                    }
+                                    b[q] = narrow<kType>(y);
+                                } else {
+#pragma unroll
+                                    for (int e = 0; e < kV; e += 2) {
+                                        const float2 r = rotate(x[e], x[e + 1], c[e / 2]);
+                                        x[e] = r.x;
+                                        x[e + 1] = r.y;
+                                    }
+                                }
+                                a[q] = narrow<kType>(x);
+                            }
+                            place(i, dst);
+                            __stcs(reinterpret_cast<uint4 *>(dst), a[q]);
+                            if constexpr (kHalves)
+                                if (two) __stcs(reinterpret_cast<uint4 *>(dst + second), b[q]);
                         }
-                        store1<kType>(dst[q], x[q]);
-                        if (two) store1<kType>(dst[q] + next, y[q]);
+                    } else {
+                        const int64_t next = kHalves ? second : kElem;
+                        float x[kInFlight], y[kInFlight];
+#pragma unroll
+                        for (int q = 0; q < kInFlight; ++q) {
+                            const int i = i0 + q * p.tokens_step;
+                            on[q] = i < count && place(i, dst);
+                            if (on[q]) {
+                                x[q] = load1<kType>(from + i * in.token);
+                                if (two) y[q] = load1<kType>(from + i * in.token + next);
+                            }
+                        }
+#pragma unroll
+                        for (int q = 0; q < kInFlight; ++q) {
+                            if (!on[q]) continue;
+                            const int i = i0 + q * p.tokens_step;
+                            if (turns) {
+                                const float2 r = rotate(x[q], y[q], cs[i * p.pairs]);
+                                x[q] = r.x;
+                                y[q] = r.y;
+                            }
+                            place(i, dst);
+                            store1<kType>(dst, x[q]);
+                            if (two) store1<kType>(dst + next, y[q]);
+                        }
                     }
                 }
             }
         }
+        if (t0 + step < p.tokens) prepare(t0 + step, buf ^ 1);   // while other warps still move this one
     }
 }
 
@@ -384,7 +400,7 @@ Kernel<kAppend> kernel_of(bool halves, bool vec) {
 
 thread_local int t_axes_kernel = 0;   // 1 vectors, 2 single pairs: this thread's last call
 
-constexpr int64_t kMaxPairs = ROPE3D_MAX_HEAD_DIM / 2;
+constexpr int64_t kMaxPairs = 1024;   // three rows of cos and sin are 24 KB of shared memory
 
 int elem_of(int32_t dtype) { return dtype == ROPE3D_F32 ? 4 : dtype == ROPE3D_BF16 || dtype == ROPE3D_F16 ? 2 : 0; }
 
@@ -394,7 +410,7 @@ int check_rotation(const int32_t *sections, int64_t head_dim, int32_t pairing, i
         if (sections[i] < 0 || sections[i] > kMaxPairs) return ROPE3D_ERR_SHAPE;
         n += sections[i];
     }
-    if (n <= 0 || 2 * n > head_dim) return ROPE3D_ERR_SHAPE;
+    if (n <= 0 || n > kMaxPairs || 2 * n > head_dim) return ROPE3D_ERR_SHAPE;
     if (pairing != ROPE3D_PAIRS_INTERLEAVED && pairing != ROPE3D_PAIRS_HALVES) return ROPE3D_ERR_ARG;
     *pairs = int(n);
     return ROPE3D_OK;
@@ -423,9 +439,11 @@ int run(AxesParams &p, int32_t dtype, bool halves, bool vec, const int32_t *sect
     const int rest = (p.head_dim - 2 * p.pairs) / v;   // units that are only copied
     p.rotating = halves || !vec ? p.pairs / v : 2 * p.pairs / v;
     p.per_head = p.rotating + rest;
-    p.heads_all = make_fastdiv(uint32_t(p.heads[0] + p.heads[1] + p.heads[2]));
+    p.heads_all = p.heads[0] + p.heads[1] + p.heads[2];
     p.lanes = make_fastdiv(uint32_t(std::min(p.per_head, kThreads)));
-    p.rows_at_once = kThreads / p.lanes.d;
+    const int rows = kThreads / int(p.lanes.d);
+    p.heads_step = make_fastdiv(uint32_t(std::min(rows, p.heads_all)));
+    p.tokens_step = rows / int(p.heads_step.d);
     p.end0 = sections[0];
     p.end1 = sections[0] + sections[1];
     // Tiles of one size for every resident block: cos and sin of a tile take 16 KB,
@@ -434,7 +452,7 @@ int run(AxesParams &p, int32_t dtype, bool halves, bool vec, const int32_t *sect
     const int rounds = int((int64_t(p.tokens) + int64_t(blocks) * most - 1) / (int64_t(blocks) * most));
     const int tile = int((int64_t(p.tokens) + int64_t(blocks) * rounds - 1) / (int64_t(blocks) * rounds));
     p.tile = tile;
-    const size_t smem = size_t(tile + 1) * p.pairs * sizeof(float2);
+    const size_t smem = size_t(2 * tile + 1) * p.pairs * sizeof(float2);
     const int tiles = (p.tokens + tile - 1) / tile;
     const Kernel<kAppend> fn = dtype == ROPE3D_BF16  ? kernel_of<kAppend, ROPE3D_BF16>(halves, vec)
                                : dtype == ROPE3D_F16 ? kernel_of<kAppend, ROPE3D_F16>(halves, vec)
