@@ -97,7 +97,7 @@ __device__ __forceinline__ uint32_t at(int r, int c) { return uint32_t(r * kD * 
 
 // log sum exp in base e of a row with maximum m (base 2) and sum l.
 __device__ __forceinline__ float lse_of(float m, float l) {
-    return l > 0.f ? (m + log2f(l)) * 0.69314718f : -INFINITY;
+    return l > 0.f ? (m + log2f(l)) * 0.69314718f : l == 0.f ? -INFINITY : l;
 }
 
 // Four results of a row, rounded.
@@ -172,33 +172,17 @@ __global__ void __launch_bounds__(kThreads) paged_rows_kernel(const __grid_const
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
 
-        int page = page_of(0);
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) {
-            const int after = page_of(i + 1);
-            issue(i, page);
-            page = after;
-        }
-
-        // the rows of q, behind one another, zeros past head_dim and past the item
+        // the rows of q, behind one another, zeros past head_dim and past the item (with step 0's copies)
         __syncthreads();   // the item before is done with shared memory
         for (int i = tid; i < kRows * kChunks; i += kThreads) {
             const int r = i / kChunks, c = i % kChunks;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (r < it.rows && c < chunks) {
-                const RowOf o = row_of<kRows>(p, it, r);
-                v = *reinterpret_cast<const uint4 *>(p.q + o.token * p.q_token + o.head * p.q_head + c * 16);
-            }
-            *reinterpret_cast<uint4 *>(sm + at<kD>(r, c)) = v;
+            const bool on = r < it.rows && c < chunks;
+            const RowOf o = row_of<kRows>(p, it, r);
+            copy16(sq + at<kD>(r, c), p.q + (on ? o.token * p.q_token + o.head * p.q_head + c * 16 : 0), on);
         }
-        __syncthreads();
         constexpr bool kKeepQ = kD <= 128;   // q's fragments in registers
         uint32_t qf[kKeepQ ? kD / 16 : 1][4];
         const int qr = (lane & 7) + (lane & 8), qc = lane >> 4;
-        if constexpr (kKeepQ) {
-#pragma unroll
-            for (int k = 0; k < kD / 16; ++k) ldm4(qf[k], sq + at<kD>(qr, 2 * k + qc));
-        }
         const RowOf r0 = row_of<kRows>(p, it, quad), r1 = row_of<kRows>(p, it, quad + 8);
 
         float o[kD / 8][4];
@@ -206,15 +190,30 @@ __global__ void __launch_bounds__(kThreads) paged_rows_kernel(const __grid_const
         for (int i = 0; i < kD / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
-        for (int step = 0; step < steps; ++step) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-            __syncwarp();
-            const int slot = step % kStages;
-            const uint32_t sk = sring + slot * kStageBytes<kD>, sv = sk + kHalf;
-            const uint32_t live = s_live[warp][slot];
+        // A step issues the copies of kStages - 1 steps on; those before 0 only fill the ring.
+        // (One piece of code for all: a call of a few microseconds waits for its instructions too.)
+        int page = page_of(0);
+#pragma unroll 1
+        for (int step = 1 - kStages; step < steps; ++step) {
+            uint32_t live = 0, sk = 0, sv = 0;
+            if (step >= 0) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+                __syncwarp();
+                const int slot = step % kStages;
+                sk = sring + slot * kStageBytes<kD>;
+                sv = sk + kHalf;
+                live = s_live[warp][slot];
+                if (step == 0) {
+                    __syncthreads();   // every warp's part of q is there
+                    if constexpr (kKeepQ) {
+#pragma unroll
+                        for (int k = 0; k < kD / 16; ++k) ldm4(qf[k], sq + at<kD>(qr, 2 * k + qc));
+                    }
+                }
+            }
             if (live) {
                 float sa[2][4] = {}, sb[2][4] = {};   // even and odd k: chains half as long
-#pragma unroll
+#pragma unroll kKeepQ ? kD / 16 : 4
                 for (int k = 0; k < kD / 16; ++k) {
                     uint32_t b[4], a[4];
                     ldm4(b, sk + at<kD>((lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
@@ -328,7 +327,7 @@ __global__ void __launch_bounds__(kThreads) paged_rows_kernel(const __grid_const
                 v.y += x.y;
                 v.z += x.z;
                 v.w += x.w;
-                if (s_max[w][r] != -INFINITY) sum += s_sum[w][r] * ex2(s_max[w][r] - big);
+                sum += s_max[w][r] == big ? s_sum[w][r] : s_sum[w][r] * ex2(s_max[w][r] - big);
             }
             if (it.whole) {
                 const RowOf row = row_of<kRows>(p, it, r);
@@ -349,115 +348,143 @@ __global__ void __launch_bounds__(kThreads) paged_rows_kernel(const __grid_const
 
 constexpr int kJoinThreads = 512, kJoinRows = 16;
 
-// Block (c, y): if the cut at the beginning of part c is the first one in an item,
-// that item's rows 16 y .. 16 y + 15 from all parts that computed some of it, in
-// order. Where there are fewer vectors than threads, threads share a vector's parts.
-template <bool kF16, int kTile, int kKeysOf>
+// The sum of weights by the greater of two maxima. (A row that saw nothing has a maximum of
+// -infinity and a sum of 0; one whose scores are all NaN, a sum of NaN.)
+__device__ __forceinline__ float joined(float m, float l, float n, float k) {
+    const float top = fmaxf(m, n);
+    return (m == top ? l : l * ex2(m - top)) + (n == top ? k : k * ex2(n - top));
+}
+
+// Block (c, y): if the cut at the beginning of part c falls into an item (behind its first
+// block), rows 16 y .. 16 y + 15 of that item from all parts that computed some of it, in
+// order; the blocks of all cuts in an item share its vectors, and where a block has fewer
+// vectors than threads, threads share a vector's parts. What bounds it is the chain of
+// loads from L2 (notes, then maxima, sums and vectors), a microsecond each: each is
+// made for all parts at once.
+template <bool kF16, int kTile>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ AttnParams p) {
-    __shared__ float4 s_v[kJoinThreads];
-    __shared__ float s_l[kJoinThreads], s_m[kJoinThreads];
-    __shared__ int s_part[kJoinThreads];   // the item's parts: the part, negative (~part) in its first slot
+    __shared__ float s_w[kJoinRows][kMostParts + 1];   // a row's maxima, then weights
+    __shared__ int s_part[kMostParts + 1];             // the item's parts: the part, negative (~part) in its first slot
+    __shared__ int s_count[kJoinThreads / 32], s_from[kJoinThreads / 32], s_mine;
     rope3d_tc::grid_release();
     rope3d_tc::grid_wait();
-    const int c = blockIdx.x, tid = threadIdx.x;
+    const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    static_assert(kMostParts <= kJoinThreads, "a part to a thread");
     const PartNote n = p.notes[c];
+    const long long begin = tid < p.parts ? p.notes[tid].begin : 0, end = tid < p.parts ? p.notes[tid].end : 0;
     const long long first = n.item + p.item_cost;   // the item's first block on the line
     if (n.begin == n.end || n.begin <= first) return;
-    int from = c - 1;   // the part before: the item's first part, or the cut is not its first
-    while (from > 0 && p.notes[from].begin == p.notes[from].end) --from;
-    if (p.notes[from].begin > first) return;
-    // the parts of the item: `from`, and those from c on that begin in it (parts without
-    // blocks between them have none of it)
-    static_assert(kMostParts < kJoinThreads, "a part to a thread");
-    const int part = c + tid;
-    bool its = part < p.parts;
-    if (its) {
-        const long long begin = p.notes[part].begin;
-        its = begin < n.item + n.cost && begin < p.notes[part].end;
+    // The item's parts: the last that begins at or before its first block, and those that begin
+    // behind that and in it (parts without blocks among them have none of it)
+    const bool its = begin > first && begin < n.item + n.cost && begin < end;
+    const uint32_t bits = __ballot_sync(0xffffffffu, its), at_first = __ballot_sync(0xffffffffu, begin <= first && begin < end);
+    if (lane == 0) {
+        s_count[warp] = __popc(bits);
+        s_from[warp] = at_first ? warp * 32 + 31 - __clz(int(at_first)) : -1;
     }
-    {
-        const uint32_t bits = __ballot_sync(0xffffffffu, its);
-        if ((tid & 31) == 0) s_part[tid >> 5] = __popc(bits);
-        __syncthreads();
-        int before = 1 + __popc(bits & ((1u << (tid & 31)) - 1u));
-        for (int w = 0; w < tid >> 5; ++w) before += s_part[w];
-        __syncthreads();
-        if (its) s_part[before] = ~part;
-        if (tid == 0) s_part[0] = from;
-    }
-    const int parts = __syncthreads_count(its) + 1;
-
     Item it;
     it.s = n.s;
     it.h = n.h;
     it.t = n.t;
     it.q = seq_of<kTile>(p, n.s);
     it.rows = int(min(uint32_t(kTile), uint32_t(it.q.n) * p.group.d - uint32_t(n.t) * kTile));
+    __syncthreads();
+    int before = 1 + __popc(bits & ((1u << lane) - 1u)), cuts = 0, from = 0;
+    for (int w = 0; w < kJoinThreads / 32; ++w) {
+        if (w < warp) before += s_count[w];
+        cuts += s_count[w];
+        from = max(from, s_from[w]);
+    }
+    if (its) s_part[before] = ~tid;
+    if (tid == 0) s_part[0] = from;
+    if (tid == c) s_mine = before - 1;   // which of the item's cuts this block's is
+    __syncthreads();
+    const int parts = cuts + 1, mine = s_mine;
     const int row0 = blockIdx.y * kJoinRows, rows = min(kJoinRows, it.rows - row0);
     if (rows <= 0) return;
-    const int vecs = p.head_dim / 4, count = rows * vecs;
+    const int vecs = p.head_dim / 4, all = rows * vecs, i_begin = all * mine / cuts, i_end = all * (mine + 1) / cuts;
+    const int count = i_end - i_begin;
+    if (count == 0 && !(p.lse && mine == 0)) return;
+    auto slot_at = [&](int k) {
+        const int of = s_part[k];
+        return slot_of<kTile>(p, of < 0 ? ~of : of, of < 0);
+    };
+
+    // each thread's first vectors are on their way while the weights are found
     int shares = 1;     // threads to a vector
-    while (2 * shares * count <= kJoinThreads && 2 * shares <= parts) shares *= 2;
-    for (int i0 = 0; i0 < count; i0 += kJoinThreads / shares) {
-        const int i = i0 + tid / shares, share = tid % shares;
-        const bool on = i < count;
-        const int r = on ? row0 + i % rows : row0, v4 = on ? i / rows : 0;
-        float m = -INFINITY, l = 0.f;
+    while (shares < 32 && 2 * shares * count <= kJoinThreads && 2 * shares <= parts) shares *= 2;
+    const int share = tid % shares;
+    constexpr int kAtOnce = 8;
+    float4 x[kAtOnce];
+    auto fetch = [&](int i, int k0) {
+        const int r = i % rows, v4 = i / rows;
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j)   // (loads that do not wait for a branch)
+            x[j] = *reinterpret_cast<const float4 *>(slot_at(min(k0 + j * shares, parts - 1)) + (v4 * kTile + row0 + r) * 4);
+    };
+    const int i_first = i_begin + tid / shares;
+    if (i_first < i_end) fetch(i_first, share);
+
+    // a warp a row: the greatest maximum, the parts' weights by it, their sum
+    if (warp < rows) {
+        float top = -INFINITY, sum = 0.f;
+        constexpr int kLoads = 4;
+        for (int k0 = lane; k0 < parts; k0 += 32 * kLoads) {
+            float m[kLoads], l[kLoads];
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                const float *of = slot_at(min(k0 + 32 * j, parts - 1)) + vecs * kTile * 4 + row0 + warp;
+                m[j] = of[0];
+                l[j] = of[kTile];
+            }
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                if (k0 + 32 * j >= parts) break;
+                s_w[warp][k0 + 32 * j] = m[j];
+                sum = joined(top, sum, m[j], l[j]);
+                top = fmaxf(top, m[j]);
+            }
+        }
+#pragma unroll
+        for (int d = 16; d; d >>= 1) {
+            const float m = __shfl_xor_sync(0xffffffffu, top, d), l = __shfl_xor_sync(0xffffffffu, sum, d);
+            sum = joined(top, sum, m, l);
+            top = fmaxf(top, m);
+        }
+        const float inv = sum > 0.f ? 1.f / sum : sum, ref = top == -INFINITY ? 0.f : top;
+        for (int k = lane; k < parts; k += 32) s_w[warp][k] = ex2(s_w[warp][k] - ref) * inv;
+        if (lane == 0 && p.lse && mine == 0) {
+            const RowOf row = row_of<kTile>(p, it, row0 + warp);
+            p.lse[row.token * p.lse_token + row.head] = lse_of(top, sum);
+        }
+    }
+    __syncthreads();
+    for (int i0 = i_begin; i0 < i_end; i0 += kJoinThreads / shares) {
+        const int i = i0 + tid / shares, r = i % rows;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (on) {
-            constexpr int kAtOnce = 8;   // parts' loads at a time
-            for (int k0 = share; k0 < parts; k0 += kAtOnce * shares) {
-                float pm[kAtOnce], pl[kAtOnce];
-                float4 pv[kAtOnce];
+        if (i < i_end) {
+            for (int k0 = share; k0 < parts; k0 += kAtOnce * shares) {   // (a part in which the row saw nothing has zeros)
+                if (i0 > i_begin || k0 > share) fetch(i, k0);
 #pragma unroll
                 for (int j = 0; j < kAtOnce; ++j) {
-                    const int k = k0 + j * shares;
-                    pm[j] = -INFINITY;
-                    if (k >= parts) continue;
-                    const int of = s_part[k];
-                    const float *slot = slot_of<kTile>(p, of < 0 ? ~of : of, of < 0);
-                    pm[j] = slot[vecs * kTile * 4 + r];
-                    pl[j] = slot[vecs * kTile * 4 + kTile + r];
-                    pv[j] = *reinterpret_cast<const float4 *>(slot + (v4 * kTile + r) * 4);
-                }
-#pragma unroll
-                for (int j = 0; j < kAtOnce; ++j) {
-                    if (pm[j] == -INFINITY) continue;
-                    const float big = fmaxf(m, pm[j]), a = m == -INFINITY ? 0.f : ex2(m - big), b = ex2(pm[j] - big);
-                    v.x = v.x * a + pv[j].x * b;
-                    v.y = v.y * a + pv[j].y * b;
-                    v.z = v.z * a + pv[j].z * b;
-                    v.w = v.w * a + pv[j].w * b;
-                    l = l * a + pl[j] * b;
-                    m = big;
+                    if (k0 + j * shares >= parts) break;
+                    const float w = s_w[r][k0 + j * shares];
+                    v.x += x[j].x * w;
+                    v.y += x[j].y * w;
+                    v.z += x[j].z * w;
+                    v.w += x[j].w * w;
                 }
             }
         }
-        if (shares > 1) {
-            __syncthreads();
-            s_v[tid] = v;
-            s_l[tid] = l;
-            s_m[tid] = m;
-            __syncthreads();
-            if (share == 0) {
-                for (int j = 1; j < shares; ++j) {
-                    const float pm = s_m[tid + j];
-                    if (pm == -INFINITY) continue;
-                    const float big = fmaxf(m, pm), a = m == -INFINITY ? 0.f : ex2(m - big), b = ex2(pm - big);
-                    const float4 x = s_v[tid + j];
-                    v.x = v.x * a + x.x * b;
-                    v.y = v.y * a + x.y * b;
-                    v.z = v.z * a + x.z * b;
-                    v.w = v.w * a + x.w * b;
-                    l = l * a + s_l[tid + j] * b;
-                    m = big;
-                }
-            }
+        for (int d = shares / 2; d; d >>= 1) {
+            v.x += __shfl_xor_sync(0xffffffffu, v.x, d);
+            v.y += __shfl_xor_sync(0xffffffffu, v.y, d);
+            v.z += __shfl_xor_sync(0xffffffffu, v.z, d);
+            v.w += __shfl_xor_sync(0xffffffffu, v.w, d);
         }
-        if (on && share == 0) {
-            const RowOf row = row_of<kTile>(p, it, r);
-            store4<kF16>(p.out + row.token * p.out_token + row.head * p.out_head + v4 * 8, v, l > 0.f ? 1.f / l : l);
-            if (v4 == 0 && p.lse) p.lse[row.token * p.lse_token + row.head] = lse_of(m, l);
+        if (i < i_end && share == 0) {
+            const RowOf row = row_of<kTile>(p, it, row0 + r);
+            store4<kF16>(p.out + row.token * p.out_token + row.head * p.out_head + i / rows * 8, v, 1.f);
         }
     }
 }
@@ -596,8 +623,8 @@ int attention(const rope3d_paged_attention_args *a, bool go, bool check_device, 
     if (rc != ROPE3D_OK) return rc;
     t_paged_kernel = c.tiles ? 2 : 1;
     const dim3 grid(unsigned(c.parts), unsigned((c.tiles ? kTileRows : kFewRows) / kJoinRows));
-    auto *join = c.tiles ? (f16 ? paged_join_kernel<true, kTileRows, 128> : paged_join_kernel<false, kTileRows, 128>)
-                         : (f16 ? paged_join_kernel<true, kFewRows, kKeys> : paged_join_kernel<false, kFewRows, kKeys>);
+    auto *join = c.tiles ? (f16 ? paged_join_kernel<true, kTileRows> : paged_join_kernel<false, kTileRows>)
+                         : (f16 ? paged_join_kernel<true, kFewRows> : paged_join_kernel<false, kFewRows>);
     return launch(join, grid, kJoinThreads, 0, st, p);
 }
 

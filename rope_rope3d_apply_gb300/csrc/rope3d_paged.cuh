@@ -98,7 +98,7 @@ __device__ __forceinline__ long long floors(long long n, const rope3d::FastDiv &
 }
 
 template <int kRows, int kKeys>
-__device__ long long tiles_cost(const AttnParams &p, const Seq &q, int t) {
+__device__ __noinline__ long long tiles_cost(const AttnParams &p, const Seq &q, int t) {
     static_assert(kKeys % kRows == 0 && (kRows == 128 || kRows == 16), "D is whole");
     const rope3d::FastDiv &d = p.span;
     const long long group = p.group.d, past = q.len - q.n;
@@ -138,15 +138,42 @@ __device__ __forceinline__ long long cut(const AttnParams &p, long long total, i
     return whole * part + udiv(uint32_t(total - whole * p.parts) * uint32_t(part), p.cuts);
 }
 
+// The item at place `begin` of the line, in a sequence whose first is `before` and whose
+// heads cost `head` each.
+template <int kRows, int kKeys>
+__device__ __forceinline__ void start_in(const AttnParams &p, int s, const Seq &q, long long before, long long head, long long begin,
+                                         Start *out) {
+    const long long in = begin - before;
+    out->s = s;
+    out->h = in < 0x7fffffff && head < 0x7fffffff ? int(uint32_t(in) / uint32_t(head)) : int(in / head);
+    before += out->h * head;
+    int t = 0, above = q.tiles;   // the last tile that begins at or before the cut
+    while (above - t > 1) {
+        const int mid = (t + above) >> 1;
+        if (before + tiles_cost<kRows, kKeys>(p, q, mid) <= begin) t = mid;
+        else above = mid;
+    }
+    if (t > 0) before += tiles_cost<kRows, kKeys>(p, q, t);
+    out->t = t;
+    out->off = int(begin - before);
+    out->item = before;
+    out->cost = tile_of<kRows, kKeys>(p, q, t).blocks() + p.item_cost;
+}
+
 template <int kRows, int kKeys, int kThreads>
 __device__ void find_start(const AttnParams &p, int part, Start *out, long long *s_sums) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int seqs = p.batch.seqs, each = (seqs + kThreads - 1) / kThreads;   // (kThreads is a constant power of two)
+    const int seqs = p.batch.seqs, each = (seqs + kThreads - 1) / kThreads;
     const int first = min(tid * each, seqs), end = min(first + each, seqs);
-    long long sum = 0;
-    for (int s = first; s < end; ++s) sum += seq_cost<kRows, kKeys>(p, seq_of<kRows>(p, s)) * p.kv_heads;
+    Seq q{0, 0, 0, 0};
+    long long sum = 0, head = 0;
+    for (int s = first; s < end; ++s) {
+        q = seq_of<kRows>(p, s);
+        head = seq_cost<kRows, kKeys>(p, q);
+        sum += head * p.kv_heads;
+    }
     long long inc = sum;
-#pragma unroll
+#pragma unroll 1
     for (int d = 1; d < 32; d <<= 1) {
         const long long o = __shfl_up_sync(0xffffffffu, inc, d);
         if (lane >= d) inc += o;
@@ -155,36 +182,22 @@ __device__ void find_start(const AttnParams &p, int part, Start *out, long long 
     if (tid == 0) out->s = -1;
     __syncthreads();
     long long before = inc - sum, total = 0;
+#pragma unroll 1
     for (int w = 0; w < kThreads / 32; ++w) {
         if (w < warp) before += s_sums[w];
         total += s_sums[w];
     }
     const long long begin = cut(p, total, part), stop = cut(p, total, part + 1);
     if (begin < stop && begin >= before && begin < before + sum) {
-        for (int s = first; s < end; ++s) {
-            const Seq q = seq_of<kRows>(p, s);
-            const long long head = seq_cost<kRows, kKeys>(p, q), all = head * p.kv_heads;
-            if (begin >= before + all) {
-                before += all;
-                continue;
-            }
-            out->s = s;
-            const long long in = begin - before;
-            out->h = in < 0x7fffffff && head < 0x7fffffff ? int(uint32_t(in) / uint32_t(head)) : int(in / head);
-            before += out->h * head;
-            int t = 0, above = q.tiles;   // the last tile that begins at or before the cut
-            while (above - t > 1) {
-                const int mid = (t + above) >> 1;
-                if (before + tiles_cost<kRows, kKeys>(p, q, mid) <= begin) t = mid;
-                else above = mid;
-            }
-            if (t > 0) before += tiles_cost<kRows, kKeys>(p, q, t);
-            out->t = t;
-            out->off = int(begin - before);
-            out->item = before;
-            out->cost = tile_of<kRows, kKeys>(p, q, t).blocks() + p.item_cost;
-            break;
+        int s = first;
+        while (each > 1) {   // which of the thread's sequences
+            q = seq_of<kRows>(p, s);
+            head = seq_cost<kRows, kKeys>(p, q);
+            if (begin < before + head * p.kv_heads) break;
+            before += head * p.kv_heads;
+            ++s;
         }
+        start_in<kRows, kKeys>(p, s, q, before, head, begin, out);
     }
     if (tid == 0) {
         out->begin = begin;

@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
             if (lane == 0) arrive(o_empty);
             if (!on) return;
             if (of.whole) {
-                if (p.lse) p.lse[o.token * p.lse_token + o.head] = sum > 0.f ? (top + log2f(sum)) * 0.69314718f : -INFINITY;
+                if (p.lse) p.lse[o.token * p.lse_token + o.head] = sum > 0.f ? (top + log2f(sum)) * 0.69314718f : sum == 0.f ? -INFINITY : sum;
             } else {
                 slot[int64_t(p.head_dim) * kRows + row] = top;
                 slot[int64_t(p.head_dim) * kRows + kRows + row] = sum;

@@ -218,6 +218,19 @@ def test_special_values():
     assert bool(got[0].isnan().all()) and bool(got[1].isfinite().all())
 
 
+@pytest.mark.parametrize("new,length", [(1, 40), (1, 5000), (200, 300), (200, 5000)])
+def test_rows_of_nan(new, length):
+    """A query row of NaN gives NaN in its own row, whole or joined from parts, and nowhere else."""
+    g = gen(20)
+    k, v, table = make_cache(g, [length], 16, 2, 64, BF)
+    q = torch.randn((new, 4, 64), generator=g, device=DEV).to(BF)
+    q[new // 2, 1] = math.nan
+    got, lse = r.rope3d_paged_attention(q, k, v, table, torch.tensor([length], dtype=torch.int32, device=DEV), lse=True)
+    bad = torch.zeros((new, 4), dtype=torch.bool, device=DEV)
+    bad[new // 2, 1] = True
+    assert torch.equal(got.isnan().all(-1), bad) and torch.equal(got.isnan().any(-1), bad) and torch.equal(lse.isnan(), bad)
+
+
 def test_damaged_lengths_and_starts_stay_inside():
     """Lengths past the table, falling and wild starts: nothing outside is read or written."""
     g = gen(19)
