@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
 
 // ---- host --------------------------------------------------------------------------
 
-thread_local int t_paged_kernel = 0;   // 1 few rows, 2 tiles
+thread_local int t_paged_kernel = 0;   // 1 few rows, 2 tiles, 3 tiles of pairs
 
 template <bool kF16, int kD>
 int launch_rows(const AttnParams &p, cudaStream_t st) {
@@ -517,11 +517,11 @@ int launch_rows(const AttnParams &p, cudaStream_t st) {
 
 int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
-// How a call is computed: the kernel, its parts and its workspace.
+// How a call is computed: the kernel (0 few rows, 1 tiles, 2 tiles of pairs), its parts and
+// its workspace.
 struct Choice {
-    bool tiles;
-    int parts;
-    int64_t slots, bytes;
+    int kind, rows, keys, parts;
+    int64_t notes, bytes;
 };
 
 Choice choose(const rope3d_paged_attention_args &a) {
@@ -530,18 +530,29 @@ Choice choose(const rope3d_paged_attention_args &a) {
     int64_t most = b.q_starts ? a.tokens : a.tokens / b.seqs;
     if (a.max_new) most = std::min(most, a.max_new);
     Choice c{};
-    c.tiles = most * group > kFewRows && tiles_fit(a);
-    const int64_t rows = c.tiles ? kTileRows : kFewRows, keys = c.tiles ? 128 : kKeys;
-    const int limit = c.tiles ? kTileParts : kTileParts * (a.head_dim <= 64 ? kPerSm<64> : a.head_dim <= 128 ? kPerSm<128> : kPerSm<256>);
+    // a pair of blocks wants more rows than one has
+    if (most * group > kFewRows && tiles_fit(a)) c.kind = most * group > kTileRows && pairs_fit(a) ? 2 : 1;
+    c.rows = c.kind == 2 ? kPairRows : c.kind ? kTileRows : kFewRows;
+    c.keys = c.kind == 2 ? 256 : c.kind ? 128 : kKeys;
+    const int limit = c.kind == 2 ? kPairParts : c.kind ? kTileParts
+                      : kTileParts * (a.head_dim <= 64 ? kPerSm<64> : a.head_dim <= 128 ? kPerSm<128> : kPerSm<256>);
     // no more parts than blocks there can be
-    const int64_t items = (a.tokens * group + rows - 1) / rows + std::min(b.seqs, a.tokens);
-    const int64_t blocks = (b.table_width * b.page_size + keys - 1) / keys;
+    const int64_t items = (a.tokens * group + c.rows - 1) / c.rows + std::min(b.seqs, a.tokens);
+    const int64_t blocks = (b.table_width * b.page_size + c.keys - 1) / c.keys;
     const int64_t most_blocks = items > limit || blocks > limit ? limit : items * blocks * a.kv_heads;
     c.parts = int(std::min<int64_t>(limit, most_blocks));
-    c.slots = up256(int64_t(c.parts) * int64_t(sizeof(PartNote)));
-    const int64_t floats = c.tiles ? slot_floats<kTileRows>(int(a.head_dim)) : slot_floats<kFewRows>(int(a.head_dim));
-    c.bytes = c.slots + up256(2 * c.parts * floats * 4);
+    c.notes = up256(int64_t(c.parts) * int64_t(sizeof(PartNote)));
+    const int d = int(a.head_dim);
+    const int64_t floats = c.kind == 2 ? slot_floats<kPairRows>(d) : c.kind ? slot_floats<kTileRows>(d) : slot_floats<kFewRows>(d);
+    c.bytes = c.notes + up256(2 * c.parts * floats * 4);
     return c;
+}
+
+template <bool kF16>
+int launch_join(const AttnParams &p, const Choice &c, cudaStream_t st) {
+    auto *join = c.kind == 2 ? paged_join_kernel<kF16, kPairRows> : c.kind ? paged_join_kernel<kF16, kTileRows>
+                                                                           : paged_join_kernel<kF16, kFewRows>;
+    return launch(join, dim3(unsigned(c.parts), unsigned(c.rows / kJoinRows)), kJoinThreads, 0, st, p);
 }
 
 int attention(const rope3d_paged_attention_args *a, bool go, bool check_device, int64_t *need, cudaStream_t st) {
@@ -593,10 +604,10 @@ int attention(const rope3d_paged_attention_args *a, bool go, bool check_device, 
     p.batch = device_batch(b, T);
     p.group = rope3d::make_fastdiv(uint32_t(H / K));
     p.page = rope3d::make_fastdiv(uint32_t(b.page_size));
-    p.span = rope3d::make_fastdiv(uint32_t(H / K) * (c.tiles ? 1 : kKeys / kRows));
+    p.span = rope3d::make_fastdiv(uint32_t(H / K) * uint32_t(c.keys / c.rows));
     p.cuts = rope3d::make_fastdiv(uint32_t(c.parts));
     // measured in _COST_
-    p.item_cost = 2;
+    p.item_cost = c.kind == 2 ? 1 : 2;
     p.kv_heads = int(K);
     p.head_dim = int(D);
     p.causal = a->causal;
@@ -616,16 +627,13 @@ int attention(const rope3d_paged_attention_args *a, bool go, bool check_device, 
     p.scale_log2 = scale;
     p.parts = c.parts;
     p.notes = static_cast<PartNote *>(a->workspace);
-    p.partial = reinterpret_cast<float *>(static_cast<char *>(a->workspace) + c.slots);
+    p.partial = reinterpret_cast<float *>(static_cast<char *>(a->workspace) + c.notes);
     const bool f16 = a->dtype == ROPE3D_F16;
-    if (c.tiles) rc = launch_tiles(p, *a, st);
+    if (c.kind) rc = launch_tiles(p, *a, c.kind == 2, st);
     else rc = f16 ? launch_rows<true>(p, st) : launch_rows<false>(p, st);
     if (rc != ROPE3D_OK) return rc;
-    t_paged_kernel = c.tiles ? 2 : 1;
-    const dim3 grid(unsigned(c.parts), unsigned((c.tiles ? kTileRows : kFewRows) / kJoinRows));
-    auto *join = c.tiles ? (f16 ? paged_join_kernel<true, kTileRows> : paged_join_kernel<false, kTileRows>)
-                         : (f16 ? paged_join_kernel<true, kFewRows> : paged_join_kernel<false, kFewRows>);
-    return launch(join, grid, kJoinThreads, 0, st, p);
+    t_paged_kernel = c.kind + 1;
+    return f16 ? launch_join<true>(p, c, st) : launch_join<false>(p, c, st);
 }
 
 }  // namespace

@@ -99,19 +99,20 @@ __device__ __forceinline__ long long floors(long long n, const rope3d::FastDiv &
 
 template <int kRows, int kKeys>
 __device__ __noinline__ long long tiles_cost(const AttnParams &p, const Seq &q, int t) {
-    static_assert(kKeys % kRows == 0 && (kRows == 128 || kRows == 16), "D is whole");
+    static_assert(kKeys % kRows == 0 && (kRows == 256 || kRows == 128 || kRows == 16), "D is whole");
+    constexpr int kShift = kRows == 256 ? 8 : kRows == 128 ? 7 : 4;
     const rope3d::FastDiv &d = p.span;
     const long long group = p.group.d, past = q.len - q.n;
     long long sum;
     if (p.causal) {   // at least 1 each
-        const long long a = (group * (past + kKeys) + kRows - 1) >> (kRows == 128 ? 7 : 4);
+        const long long a = (group * (past + kKeys) + kRows - 1) >> kShift;
         const long long ones = min(max((long long)d.d - a, 0ll), (long long)t);
         sum = ones + (t > ones ? floors(a + t, d) - floors(a + ones, d) : 0);
     } else {
         sum = (long long)max((q.len + kKeys - 1) / kKeys, 1) * t;
     }
     if (p.window) {
-        const long long c = group * (past - p.window + 1) >> (kRows == 128 ? 7 : 4);
+        const long long c = group * (past - p.window + 1) >> kShift;
         if (c + t > 0) sum -= floors(c + t, d) - floors(max(c, 0ll), d);
     }
     return sum + (long long)t * p.item_cost;
@@ -304,13 +305,16 @@ __device__ __forceinline__ void write_note(const AttnParams &p, int part, const 
     p.notes[part] = n;
 }
 
-// Launches of rope3d_paged_tc.cu.
-int launch_tiles(const AttnParams &p, const rope3d_paged_attention_args &a, cudaStream_t st);
-bool tiles_fit(const rope3d_paged_attention_args &a);
-int tiles_wait_timeouts(unsigned int *count, bool reset);
-
-constexpr int kTileRows = 128;   // rows of an item on the tensor cores
 constexpr int kFewRows = 16;     // rows of an item of the kernel for few rows
-constexpr int kTileParts = 152;  // thread blocks of the former: the GB300's SMs
+constexpr int kTileRows = 128;   // rows of an item of one block on the tensor cores
+constexpr int kPairRows = 256;   // rows of an item of a pair of blocks
+constexpr int kTileParts = 152;  // parts of the line for single blocks: the GB300's SMs
+constexpr int kPairParts = 76;   // and for pairs
+
+// Launches of rope3d_paged_tc.cu: items of kTileRows, or of kPairRows.
+int launch_tiles(const AttnParams &p, const rope3d_paged_attention_args &a, bool pair, cudaStream_t st);
+bool tiles_fit(const rope3d_paged_attention_args &a);
+bool pairs_fit(const rope3d_paged_attention_args &a);
+int tiles_wait_timeouts(unsigned int *count, bool reset);
 
 }  // namespace rope3d_paged

@@ -22,6 +22,14 @@
 // head_dim is padded to 64, 128 or 256 channels by TMA's zero fill. At 256 a block's K
 // comes as two pieces of 128 channels and its V as two of 64 places, so that five
 // pieces of 32 KB fit beside Q.
+//
+// Pairs (kPair): two blocks of a cluster share an item of 256 rows, 128 each, and its keys:
+// the products are those of cta_group::2, issued by the first block, for which each
+// block holds half of the places of K and half of the channels of V. That halves what
+// each SM loads and keeps of K and V, and reads of them for a product. A block's softmax,
+// Q and results stay its own; what the issuing threads wait for is signalled to the first
+// block's barriers, and what their products free or finish to both blocks'. An item is cut
+// between blocks of 256 places (each two of 128 here).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -43,35 +51,41 @@ namespace {
 using namespace rope3d_paged;
 using namespace rope3d_tc;
 
-constexpr int kRows = kTileRows, kKeys = 128;
+constexpr int kKeys = 128;       // places of a block of keys
+constexpr int kLanes = 128;      // rows of a block of threads: tensor memory's lanes
 constexpr int kThreads = 512, kSoftWarp = 8;
 constexpr float kLazy = 8.0f;
 // Registers of a thread: 512 threads have 128 each at launch; the softmax's 256 have
 // kSoftRegs and the others kOtherRegs, no more together.
 constexpr int kSoftRegs = 184, kOtherRegs = 72;
 static_assert(256 * (kSoftRegs + kOtherRegs) <= kThreads * 128, "no more registers than the block has");
-constexpr uint32_t kColBlock = kRows * 128;   // bytes of 64 channels of 128 rows
+constexpr uint32_t kColBlock = kLanes * 128;   // bytes of 64 channels of 128 rows
 
 __device__ unsigned int g_paged_wait_timeouts;
 
 // Shared memory and tensor memory at kD channels.
-template <int kD>
+template <int kD, bool kPair>
 struct Lay {
-    static constexpr int kPieces = kD == 256 ? 2 : 1;             // pieces of a block's K, and of its V
-    static constexpr int kKSlots = kD == 256 ? 3 : kD == 128 ? 2 : 4, kVSlots = kD == 64 ? 4 : 2;
-    static constexpr uint32_t kPiece = kD == 64 ? 16384 : 32768;
-    static constexpr int kVRows = kKeys / kPieces;                // places of a V piece
+    static constexpr int kPieces = kD == 256 && !kPair ? 2 : 1;   // pieces of a block's K, and of its V
+    static constexpr int kKRows = kPair ? 64 : 128;               // places and channels / 64 of a K piece
+    static constexpr int kKCols = kPair ? kD / 64 : (kD < 128 ? kD : 128) / 64;
+    static constexpr int kVRows = kKeys / kPieces;                // places and channels / 64 of a V piece
+    static constexpr int kVCols = kPair ? kD / 128 : kD / 64;
+    static constexpr uint32_t kKPiece = kKRows * kKCols * 128, kVPiece = kVRows * kVCols * 128;
+    static constexpr int kKSlots = kPair ? (kD == 256 ? 3 : 5) : kD == 256 ? 3 : kD == 128 ? 2 : 4;
+    static constexpr int kVSlots = kPair ? (kD == 256 ? 2 : 5) : kD == 64 ? 4 : 2;
     static constexpr int kQBufs = kD == 256 ? 1 : 2;
-    static constexpr uint32_t kQBytes = kRows * kD * 2;
+    static constexpr uint32_t kQBytes = kLanes * kD * 2;
     static constexpr int kSBufs = kD == 256 ? 2 : 3;
     static constexpr uint32_t kColO = kSBufs * 128;
-    static constexpr uint32_t kOffK = kQBufs * kQBytes, kOffV = kOffK + kKSlots * kPiece;
-    static constexpr uint32_t kOffMax = kOffV + kVSlots * kPiece;   // float [2][128]: a row's maximum, from each group
+    static constexpr uint32_t kOffK = kQBufs * kQBytes, kOffV = kOffK + kKSlots * kKPiece;
+    static constexpr uint32_t kOffMax = kOffV + kVSlots * kVPiece;   // float [2][128]: a row's maximum, from each group
     static constexpr uint32_t kOffSum = kOffMax + 2 * 128 * 4;      // float [2][128] sums, [128] maxima
     static constexpr uint32_t kOffBar = kOffSum + 3 * 128 * 4;
     static constexpr int kBars = 2 * kQBufs + 2 * kKSlots + 2 * kVSlots + 3 * kSBufs + 5;
     static constexpr uint32_t kBytes = kOffBar + kBars * 8 + 16;
     static_assert(kColO + kD <= 512, "S and O fit tensor memory");
+    static_assert(kOffMax % 1024 == 0 && kOffV % 1024 == 0 && kKPiece % 1024 == 0, "the swizzle's period");
     static_assert(kBytes <= 232448, "one block an SM");
 };
 
@@ -100,9 +114,17 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
     return w;
 }
 
-// A box of 64 channels by some places of one head and page.
+// A box of 64 channels by some places of one head and page. kPair: `bar` may be the
+// other block's.
+template <bool kPair>
 __device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap *map, int c, int slot, int head, int page, uint32_t bar) {
-    asm volatile(
+    if constexpr (kPair)
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+            "[%0], [%1, {%2, %3, %4, %5}], [%6];"
+            ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(slot), "r"(head), "r"(page), "r"(bar) : "memory");
+    else
+        asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
         ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(slot), "r"(head), "r"(page), "r"(bar) : "memory");
 }
@@ -111,12 +133,52 @@ __device__ __forceinline__ void arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// D += A B with A (128 x 16, pairs of 16 bits to a column) read from tensor memory.
+// An arrival on the first block's barrier (this block's, without pairs): with this
+// thread's writes to shared memory; or relaxed, where what it hands over lies in tensor
+// memory (complete and fenced before) or is still to be copied. (A release to the cluster waits
+// for all of the thread's writes: 1,000 clocks of each block's hand-over, measured.)
+template <bool kPair>
+__device__ __forceinline__ void arrive_first(uint32_t bar) {
+    if constexpr (kPair) mbar_arrive_cluster(map_rank(bar, 0));
+    else arrive(bar);
+}
+template <bool kPair>
+__device__ __forceinline__ void arrive_first_relaxed(uint32_t bar) {
+    if constexpr (kPair)
+        asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_rank(bar, 0)) : "memory");
+    else
+        arrive(bar);
+}
+// ... and with the bytes that copies of this block will report there.
+template <bool kPair>
+__device__ __forceinline__ void expect_first(uint32_t bar, uint32_t bytes) {
+    if constexpr (kPair)
+        asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;"
+                     ::"r"(map_rank(bar, 0)), "r"(bytes) : "memory");
+    else
+        mbar_expect_tx(bar, bytes);
+}
+
+// An arrival once this thread's products so far are done, in both blocks.
+template <bool kPair>
+__device__ __forceinline__ void commit_all(uint32_t bar) {
+    if constexpr (kPair) commit_pair(bar);
+    else commit(bar);
+}
+
+// D += A B with A (16 columns, pairs of 16 bits to one of tensor memory) read from there.
+template <bool kPair>
 __device__ __forceinline__ void mma_ta(uint32_t tmem, uint32_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(tmem), "r"(a), "l"(b), "r"(id), "r"(accumulate) : "memory");
+    if constexpr (kPair)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+            ::"r"(tmem), "r"(a), "l"(b), "r"(id), "r"(accumulate) : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+            ::"r"(tmem), "r"(a), "l"(b), "r"(id), "r"(accumulate) : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld32(float *v, uint32_t addr) {
@@ -155,17 +217,23 @@ __device__ __forceinline__ void tmem_stored() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// What the copies need besides the maps.
-struct Copies {
-    int box;      // places of a box: the greatest power of two that divides the page, 64 at most
-    int boxes;    // boxes of a block
+// The blocks of 128 places that a part of an item has.
+template <int kLine>
+struct Blocks {
+    int begin, end;
+    __device__ Blocks(const Item &it)
+        : begin(max(it.begin * (kLine / kKeys), it.tile.k0 / kKeys)),
+          end(min(it.end * (kLine / kKeys), (it.tile.k1 + kKeys - 1) / kKeys)) {}
 };
 
-template <bool kF16, int kD>
-__global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ Copies cp,
-                                                                 const __grid_constant__ CUtensorMap map_k,
-                                                                 const __grid_constant__ CUtensorMap map_v) {
-    using L = Lay<kD>;
+// box_places: places of a copy, the greatest power of two that divides the page, 64 at most
+template <bool kF16, int kD, bool kPair>
+__global__ void __cluster_dims__(kPair ? 2 : 1, 1, 1) __launch_bounds__(kThreads, 1)
+    paged_tile_kernel(const __grid_constant__ AttnParams p, const int box_places, const __grid_constant__ CUtensorMap map_k,
+                      const __grid_constant__ CUtensorMap map_v) {
+    using L = Lay<kD, kPair>;
+    constexpr int kRows = kPair ? kPairRows : kTileRows, kLine = kPair ? 256 : 128;   // of an item; places of the line's blocks
+    const int rank = kPair ? int(cluster_rank()) : 0, part = int(blockIdx.x) / (kPair ? 2 : 1);
     extern __shared__ __align__(1024) char sm[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t base = smem_u32(sm), bars = base + L::kOffBar;
@@ -189,30 +257,30 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
     grid_wait();
     {   // where this part begins, by way of the (yet unused) Q buffer
         Start *s_start = reinterpret_cast<Start *>(sm);
-        find_start<kRows, kKeys, kThreads>(p, blockIdx.x, s_start, reinterpret_cast<long long *>(sm + 256));
+        find_start<kRows, kLine, kThreads>(p, part, s_start, reinterpret_cast<long long *>(sm + 256));
     }
     const Start st = *reinterpret_cast<Start *>(sm);
     if (tid == 0) {
-        write_note<kRows, kKeys>(p, blockIdx.x, st);
+        if (rank == 0) write_note<kRows, kLine>(p, part, st);
         for (int i = 0; i < L::kQBufs; ++i) {
-            mbar_init(q_full(i), 4);
+            mbar_init(q_full(i), kPair ? 8 : 4);
             mbar_init(q_empty(i), 1);
         }
         for (int i = 0; i < L::kKSlots; ++i) {
-            mbar_init(k_full(i), 1);
+            mbar_init(k_full(i), kPair ? 2 : 1);
             mbar_init(k_empty(i), 1);
         }
         for (int i = 0; i < L::kVSlots; ++i) {
-            mbar_init(v_full(i), 1);
+            mbar_init(v_full(i), kPair ? 2 : 1);
             mbar_init(v_empty(i), 1);
         }
         for (int i = 0; i < L::kSBufs; ++i) {
             mbar_init(s_full(i), 1);
             mbar_init(s_empty(i), 1);
-            mbar_init(p_full(i), 4);
+            mbar_init(p_full(i), kPair ? 8 : 4);
         }
         mbar_init(o_full, 1);
-        mbar_init(o_empty, 4);
+        mbar_init(o_empty, kPair ? 8 : 4);
         mbar_init(sum_full, 8);
         mbar_init(sum_empty, 4);
         mbar_init(v_land, 1);
@@ -220,14 +288,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
         prefetch_map(&map_k);
         prefetch_map(&map_v);
     }
-    if (warp == 1) tmem_alloc<false>(smem_u32(tmem_slot), 512);
+    if (warp == 1) tmem_alloc<kPair>(smem_u32(tmem_slot), 512);
     tc_fence_before();
     __syncthreads();   // (also: everyone has read `st`)
+    if constexpr (kPair) cluster_sync();   // both blocks' barriers are there
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     bool dead = false;
     __syncwarp();
-    Walker<kRows, kKeys> walk(p, st);
+    Walker<kRows, kLine> walk(p, st);
     Item it;
 
     if (warp < 4) {
@@ -241,32 +310,39 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
         int n = 0, landings = 0;   // pieces so far; of them, those that were waited for here
         while (walk.next(it)) {
             const int *table = p.batch.table + it.s * p.batch.table_stride;
-            for (int b = it.begin; b < it.end; ++b) {
+            const Blocks<kLine> bl(it);
+            for (int b = bl.begin; b < bl.end; ++b) {
                 const int k0 = max(it.tile.k0 - b * kKeys, 0), k1 = min(it.tile.k1 - b * kKeys, kKeys);   // what rows see
 #pragma unroll
                 for (int piece = 0; piece < L::kPieces; ++piece, ++n) {
                     const int slot = n % slots;
                     const uint32_t full = is_v ? v_full(slot) : k_full(slot), empty = is_v ? v_empty(slot) : k_empty(slot);
-                    // boxes [from, to) of the block hold places of this piece that rows see
-                    const int row0 = is_v ? piece * L::kVRows : 0, rows = is_v ? L::kVRows : kKeys;
-                    const int from = max(k0, row0) / cp.box, to = (min(k1, row0 + rows) + cp.box - 1) / cp.box;
-                    const int count = max(to - from, 0), cols = is_v ? kD / 64 : min(kD, 128) / 64;
+                    // this piece: places row0 .. row0 + rows - 1 of the block, 64 cols channels from `channel0` on
+                    const int row0 = is_v ? piece * L::kVRows : rank * L::kKRows, rows = is_v ? L::kVRows : L::kKRows;
+                    const int cols = is_v ? L::kVCols : L::kKCols;
+                    const int channel0 = is_v ? rank * L::kVCols * 64 : piece * L::kKCols * 64;
+                    // boxes [from, to) of the block hold places of the piece that rows see
+                    const int from = max(k0, row0) / box_places, to = (min(k1, row0 + rows) + box_places - 1) / box_places;
+                    const int count = max(to - from, 0);
                     if (n >= slots) mbar_wait(empty, uint32_t(n / slots - 1) & 1u, dead, late);
                     dead = __any_sync(0xffffffffu, dead);
                     const bool clean = !is_v || (k0 <= row0 && k1 >= row0 + rows);   // nothing to be zeroed
-                    const uint32_t bar = clean ? full : v_land;
-                    const uint32_t dst = ring + uint32_t(slot) * L::kPiece;
+                    const uint32_t dst = ring + uint32_t(slot) * (is_v ? L::kVPiece : L::kKPiece);
                     if (count && !dead) {
-                        if (lane == 0) mbar_expect_tx(bar, uint32_t(count * cols * cp.box) * 128u);
+                        const uint32_t bytes = uint32_t(count * cols * box_places) * 128u;
+                        if (lane == 0) {
+                            if (clean) expect_first<kPair>(full, bytes);
+                            else mbar_expect_tx(v_land, bytes);
+                        }
                         __syncwarp();
+                        const uint32_t bar = !clean ? v_land : kPair ? map_rank(full, 0) : full;
                         for (int i = lane; i < count * cols; i += 32) {
                             const int box = from + i / cols, col = i % cols;
-                            const int place = b * kKeys + box * cp.box, index = int(udiv(uint32_t(place), p.page));
+                            const int place = b * kKeys + box * box_places, index = int(udiv(uint32_t(place), p.page));
                             int page = index < p.batch.width ? table[index] : -1;
                             if (page < 0 || page >= p.batch.pages) page = p.batch.pages;   // outside: filled with zeros
-                            const int channel = (is_v ? 0 : piece * 128) + col * 64;
-                            tma_load4(dst + uint32_t(col * rows + box * cp.box - row0) * 128u, map, channel,
-                                      place - index * p.batch.page_size, it.h, page, bar);
+                            tma_load4<kPair>(dst + uint32_t(col * rows + box * box_places - row0) * 128u, map, channel0 + col * 64,
+                                             place - index * p.batch.page_size, it.h, page, bar);
                         }
                         __syncwarp();
                     }
@@ -285,32 +361,35 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
                         }
                         fence_async_smem();
                         __syncwarp();
-                        if (lane == 0) arrive(full);
+                        if (lane == 0) arrive_first<kPair>(full);
                     } else if (!count && lane == 0) {
-                        arrive(full);
+                        arrive_first_relaxed<kPair>(full);
                     }
                 }
             }
         }
-        if (dead && lane == 0) {
+        if (dead && lane == 0 && rank == 0) {   // (the other block of a pair waits below)
             const int first = max(n - slots, 0);
             for (int i = first; i < n; ++i) {
                 bool gone = false;
                 mbar_wait(is_v ? v_full(i % slots) : k_full(i % slots), uint32_t(i / slots) & 1u, gone, late);
             }
+        }
+        if (dead && lane == 0 && is_v && landings) {
             bool gone = false;
-            if (is_v && landings) mbar_wait(v_land, uint32_t(landings - 1) & 1u, gone, late);
+            mbar_wait(v_land, uint32_t(landings - 1) & 1u, gone, late);
         }
     } else if (warp == 1) {
         // ---- O += P V
-        if (lane == 0) {
+        if (lane == 0 && rank == 0) {
             constexpr uint32_t id = idesc(kRows, kD, !kF16, false, true);
             int g = 0, n = 0, items = 0;
             while (walk.next(it)) {
                 if (it.begin >= it.end) continue;
                 if (items) mbar_wait(o_empty, uint32_t(items - 1) & 1u, dead, late);
                 ++items;
-                for (int b = it.begin; b < it.end; ++b, ++g) {
+                const Blocks<kLine> bl(it);
+                for (int b = bl.begin; b < bl.end; ++b, ++g) {
                     const int sb = g % L::kSBufs;
                     mbar_wait(p_full(sb), uint32_t(g / L::kSBufs) & 1u, dead, late);
 #pragma unroll
@@ -318,22 +397,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
                         const int slot = n % L::kVSlots;
                         mbar_wait(v_full(slot), uint32_t(n / L::kVSlots) & 1u, dead, late);
                         tc_fence_after();
-                        const uint32_t v = base + L::kOffV + uint32_t(slot) * L::kPiece;
+                        const uint32_t v = base + L::kOffV + uint32_t(slot) * L::kVPiece;
                         const uint32_t pa = tmem + uint32_t(sb * 128 + piece * (L::kVRows / 2));
 #pragma unroll
                         for (int j = 0; j < L::kVRows / 16; ++j)
-                            mma_ta(tmem + L::kColO, pa + uint32_t(8 * j), sdesc(v + uint32_t(j) * 2048u, L::kVRows * 128, 1024), id,
-                                   b > it.begin || piece > 0 || j > 0 ? 1u : 0u);
-                        commit(v_empty(slot));
+                            mma_ta<kPair>(tmem + L::kColO, pa + uint32_t(8 * j), sdesc(v + uint32_t(j) * 2048u, L::kVRows * 128, 1024),
+                                          id, b > bl.begin || piece > 0 || j > 0 ? 1u : 0u);
+                        commit_all<kPair>(v_empty(slot));
                     }
-                    commit(s_empty(sb));
-                    if (b == it.end - 1) commit(o_full);
+                    commit_all<kPair>(s_empty(sb));
+                    if (b == bl.end - 1) commit_all<kPair>(o_full);
                 }
             }
         }
     } else if (warp == 2) {
         // ---- S = Q K^T
-        if (lane == 0) {
+        if (lane == 0 && rank == 0) {
             constexpr uint32_t id = idesc(kRows, kKeys, !kF16, false, false);
             int g = 0, n = 0, items = 0;
             while (walk.next(it)) {
@@ -342,7 +421,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
                 mbar_wait(q_full(qb), uint32_t(items / L::kQBufs) & 1u, dead, late);
                 ++items;
                 const uint32_t q = base + uint32_t(qb) * L::kQBytes;
-                for (int b = it.begin; b < it.end; ++b, ++g) {
+                const Blocks<kLine> bl(it);
+                for (int b = bl.begin; b < bl.end; ++b, ++g) {
                     const int sb = g % L::kSBufs;
                     if (g >= L::kSBufs) mbar_wait(s_empty(sb), uint32_t(g / L::kSBufs - 1) & 1u, dead, late);
 #pragma unroll
@@ -350,17 +430,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
                         const int slot = n % L::kKSlots;
                         mbar_wait(k_full(slot), uint32_t(n / L::kKSlots) & 1u, dead, late);
                         tc_fence_after();
-                        const uint32_t k = base + L::kOffK + uint32_t(slot) * L::kPiece, qp = q + uint32_t(piece) * 2 * kColBlock;
+                        const uint32_t k = base + L::kOffK + uint32_t(slot) * L::kKPiece;
+                        const uint32_t qp = q + uint32_t(piece * L::kKCols) * kColBlock;
 #pragma unroll
-                        for (int j = 0; j < (kD < 128 ? kD : 128) / 16; ++j) {
-                            const uint32_t off = uint32_t(j >> 2) * kColBlock + uint32_t(j & 3) * 32u;
-                            mma<false>(tmem + uint32_t(sb * 128), sdesc(qp + off, 16, 1024), sdesc(k + off, 16, 1024), id,
-                                       piece > 0 || j > 0 ? 1u : 0u);
+                        for (int j = 0; j < 4 * L::kKCols; ++j) {
+                            const uint32_t off = uint32_t(j & 3) * 32u;
+                            mma<kPair>(tmem + uint32_t(sb * 128), sdesc(qp + uint32_t(j >> 2) * kColBlock + off, 16, 1024),
+                                       sdesc(k + uint32_t(j >> 2) * (L::kKRows * 128) + off, 16, 1024), id, piece > 0 || j > 0 ? 1u : 0u);
                         }
-                        commit(k_empty(slot));
+                        commit_all<kPair>(k_empty(slot));
                     }
-                    commit(s_full(sb));
-                    if (b == it.end - 1) commit(q_empty(qb));
+                    commit_all<kPair>(s_full(sb));
+                    if (b == bl.end - 1) commit_all<kPair>(q_empty(qb));
                 }
             }
         }
@@ -368,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
     } else if (warp < kSoftWarp) {
         // ---- Q in, results out
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        const int t = tid - 128, row = t;   // this thread's row of results
+        const int row = rank * kLanes + tid - 128;   // this thread's row of results
         const uint32_t lanes = uint32_t(warp & 3) << 21;
         constexpr int kChunks = kD / 8;
         const int chunks = p.head_dim / 8;
@@ -380,11 +461,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
             ++loads;
             // A warp copies kPer rows at once, rows kPer (4 e + warp % 4) + sub for e = 0, 1, ...;
             // lane kPer e + sub finds where row (e, sub) lies.
-            constexpr int kPer = 32 / kChunks, kSteps = kRows / (4 * kPer);
+            constexpr int kPer = 32 / kChunks, kSteps = kLanes / (4 * kPer);
             static_assert(kSteps * kPer == 32, "a row to a lane");
             const int mine = kPer * (4 * (lane / kPer) + (warp & 3)) + lane % kPer;
-            const RowOf o = row_of<kRows>(p, of, mine);
-            const long long at = mine < of.rows ? o.token * p.q_token + o.head * p.q_head : -1;
+            const RowOf o = row_of<kRows>(p, of, rank * kLanes + mine);
+            const long long at = rank * kLanes + mine < of.rows ? o.token * p.q_token + o.head * p.q_head : -1;
             const int c = lane % kChunks;
             const uint32_t to = base + uint32_t(qb) * L::kQBytes + uint32_t(c >> 3) * kColBlock;
 #pragma unroll 4
@@ -399,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
             asm volatile("cp.async.wait_all;" ::: "memory");
             fence_async_smem();
             __syncwarp();
-            if (lane == 0) arrive(q_full(qb));
+            if (lane == 0) arrive_first<kPair>(q_full(qb));
         };
         const float *sums = reinterpret_cast<const float *>(sm + L::kOffSum);
         auto finish = [&](const Item &of) {
@@ -414,13 +495,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
                 return;
             }
             mbar_wait(sum_full, uint32_t(items) & 1u, dead, late);
-            const float sum = sums[row] + sums[128 + row], top = sums[256 + row];
+            const int in = tid - 128;
+            const float sum = sums[in] + sums[128 + in], top = sums[256 + in];
             mbar_wait(o_full, uint32_t(items) & 1u, dead, late);
             ++items;
             __syncwarp();
             tc_fence_after();
             if (lane == 0) arrive(sum_empty);
-            float *slot = slot_of<kRows>(p, blockIdx.x, of.head);
+            float *slot = slot_of<kRows>(p, part, of.head);
             const float inv = sum > 0.f ? 1.f / sum : sum;
             for (int c0 = 0; c0 < p.head_dim; c0 += 32) {
                 float v[32];
@@ -444,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
             }
             __syncwarp();
             tc_fence_before();
-            if (lane == 0) arrive(o_empty);
+            if (lane == 0) arrive_first_relaxed<kPair>(o_empty);
             if (!on) return;
             if (of.whole) {
                 if (p.lse) p.lse[o.token * p.lse_token + o.head] = sum > 0.f ? (top + log2f(sum)) * 0.69314718f : sum == 0.f ? -INFINITY : sum;
@@ -464,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
     } else {
         // ---- softmax: row `row`, every second block
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-        const int group = (warp - kSoftWarp) >> 2, row = (warp & 3) * 32 + lane;
+        const int group = (warp - kSoftWarp) >> 2, row = (warp & 3) * 32 + lane;   // (of this block's)
         const uint32_t lanes = uint32_t(warp & 3) << 21;
         float *passed = reinterpret_cast<float *>(sm + L::kOffMax), *sums = reinterpret_cast<float *>(sm + L::kOffSum);
         // named barriers of the four pairs of warps, one for each direction
@@ -472,12 +554,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
         int g = 0, items = 0;
         while (walk.next(it)) {
             if (it.begin >= it.end) continue;
-            const RowOf ro = row_of<kRows>(p, it, row);
-            const bool any_row = (warp & 3) * 32 < it.rows;   // the same for the pair of warps
+            const RowOf ro = row_of<kRows>(p, it, rank * kLanes + row);
+            const bool any_row = rank * kLanes + (warp & 3) * 32 < it.rows;   // the same for the pair of warps
+            const Blocks<kLine> bl(it);
             const int *table = p.batch.table + it.s * p.batch.table_stride;
             auto page_at = [&](int b) {   // of eight places, by lane
                 const uint32_t index = udiv(uint32_t(b * kKeys + (lane & 15) * 8), p.page);
-                return b < it.end && index < uint32_t(p.batch.width) ? table[index] : -1;
+                return b < bl.end && index < uint32_t(p.batch.width) ? table[index] : -1;
             };
             float m = -INFINITY, l = 0.f;
             auto receive = [&] {   // the maximum that the other group's last block refers to
@@ -488,9 +571,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
                     m = now;
                 }
             };
-            const int mine = it.begin + ((g ^ group) & 1);   // this group's first block
+            const int mine = bl.begin + ((g ^ group) & 1);   // this group's first block
             int page = page_at(mine);
-            for (int b = it.begin; b < it.end; ++b, ++g) {
+            for (int b = bl.begin; b < bl.end; ++b, ++g) {
                 if ((g & 1) != group) continue;
                 const int sb = g % L::kSBufs, place = b * kKeys;
                 const uint32_t s = tmem + uint32_t(sb * 128) + lanes;
@@ -529,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
 #pragma unroll
                         for (int j = 0; j < 4; ++j) top[j] = max3(top[j], x[e + 2 * j], x[e + 2 * j + 1]);
                     const float best = max3(top[0], top[1], fmaxf(top[2], top[3])) * p.scale_log2;
-                    if (b > it.begin) receive();
+                    if (b > bl.begin) receive();
                     const bool move = best > m + kLazy || m == -INFINITY;
                     const bool rescale = move && m != -INFINITY;
                     float f = 1.f;
@@ -578,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive(p_full(sb));
+                if (lane == 0) arrive_first_relaxed<kPair>(p_full(sb));
             }
             const bool last = ((g - 1) & 1) == group;   // the item's last block was this group's
             if (any_row && !last) receive();
@@ -590,9 +673,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tile_kernel(const __grid_co
             if (lane == 0) arrive(sum_full);
         }
     }
+    // neither block of a pair leaves while the other may name its memory or barriers
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) tmem_free<false>(tmem, 512);
+    if constexpr (kPair) cluster_sync();
+    tc_fence_after();
+    if (warp == 1) tmem_free<kPair>(tmem, 512);
 }
 
 // ---- host --------------------------------------------------------------------------
@@ -631,26 +717,27 @@ bool make_map(CUtensorMap *map, const void *p, const rope3d_paged_attention_args
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kF16, int kD>
-int launch_tile(const AttnParams &p, const Copies &c, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t st) {
+template <bool kF16, int kD, bool kPair>
+int launch_tile(const AttnParams &p, int box, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t st) {
     static std::atomic<bool> ready[64];
+    auto *fn = paged_tile_kernel<kF16, kD, kPair>;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return ROPE3D_ERR_CUDA;
     if (!ready[dev].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(paged_tile_kernel<kF16, kD>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Lay<kD>::kBytes)) !=
-            cudaSuccess) {
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Lay<kD, kPair>::kBytes)) != cudaSuccess) {
             cudaGetLastError();
             return ROPE3D_ERR_CUDA;
         }
         ready[dev].store(true, std::memory_order_release);
     }
-    return launch(paged_tile_kernel<kF16, kD>, dim3(unsigned(p.parts)), kThreads, Lay<kD>::kBytes, st, p, c, k, v);
+    return launch(fn, dim3(unsigned(p.parts) * (kPair ? 2u : 1u)), kThreads, Lay<kD, kPair>::kBytes, st, p, box, k, v);
 }
 
 template <bool kF16>
-int launch_tile(const AttnParams &p, const Copies &c, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t st) {
-    if (p.head_dim <= 64) return launch_tile<kF16, 64>(p, c, k, v, st);
-    return p.head_dim <= 128 ? launch_tile<kF16, 128>(p, c, k, v, st) : launch_tile<kF16, 256>(p, c, k, v, st);
+int launch_tile(const AttnParams &p, bool pair, int box, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t st) {
+    if (p.head_dim <= 64) return launch_tile<kF16, 64, false>(p, box, k, v, st);
+    if (p.head_dim <= 128) return pair ? launch_tile<kF16, 128, true>(p, box, k, v, st) : launch_tile<kF16, 128, false>(p, box, k, v, st);
+    return pair ? launch_tile<kF16, 256, true>(p, box, k, v, st) : launch_tile<kF16, 256, false>(p, box, k, v, st);
 }
 
 }  // namespace
@@ -669,16 +756,17 @@ bool rope3d_paged::tiles_fit(const rope3d_paged_attention_args &a) {
     return true;
 }
 
-int rope3d_paged::launch_tiles(const AttnParams &p, const rope3d_paged_attention_args &a, cudaStream_t st) {
-    Copies c{};
-    c.box = 8;
-    while (c.box < 64 && a.batch.page_size % (2 * c.box) == 0) c.box *= 2;
-    c.boxes = kKeys / c.box;
+// A pair's blocks each hold half of the channels of V, in whole 64s.
+bool rope3d_paged::pairs_fit(const rope3d_paged_attention_args &a) { return a.head_dim > 64; }
+
+int rope3d_paged::launch_tiles(const AttnParams &p, const rope3d_paged_attention_args &a, bool pair, cudaStream_t st) {
+    int box = 8;
+    while (box < 64 && a.batch.page_size % (2 * box) == 0) box *= 2;
     CUtensorMap k, v;
-    if (!make_map(&k, a.k_cache, a, a.k_page_stride, a.k_slot_stride, a.k_cache_head_stride, c.box) ||
-        !make_map(&v, a.v_cache, a, a.v_page_stride, a.v_slot_stride, a.v_cache_head_stride, c.box))
+    if (!make_map(&k, a.k_cache, a, a.k_page_stride, a.k_slot_stride, a.k_cache_head_stride, box) ||
+        !make_map(&v, a.v_cache, a, a.v_page_stride, a.v_slot_stride, a.v_cache_head_stride, box))
         return ROPE3D_ERR_CUDA;
-    return a.dtype == ROPE3D_F16 ? launch_tile<true>(p, c, k, v, st) : launch_tile<false>(p, c, k, v, st);
+    return a.dtype == ROPE3D_F16 ? launch_tile<true>(p, pair, box, k, v, st) : launch_tile<false>(p, pair, box, k, v, st);
 }
 
 int rope3d_paged::tiles_wait_timeouts(unsigned int *count, bool reset) {

@@ -86,19 +86,30 @@ CHUNKS = [
 ]
 
 
+# a hint that makes a kernel of the call's rows: few, one block's, a pair's (or the next below)
+HINTS = {"few": 1, "tile": 128, "pair": 0}
+
+
+@pytest.mark.parametrize("kernel", list(HINTS))
 @pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "f16"])
 @pytest.mark.parametrize("case", range(len(CHUNKS)))
-def test_chunks(case, dtype):
+def test_chunks(case, dtype, kernel):
     new, lens, heads, kv, dim, page = CHUNKS[case]
-    run(100 + case, new, lens, heads, kv, dim, page, dtype, pad=case % 3)
+    group, pad = heads // kv, case % 3
+    hint = max(HINTS[kernel] // group, 1) if HINTS[kernel] else 0
+    run(100 + case, new, lens, heads, kv, dim, page, dtype, pad=pad, max_new=hint)
+    tokens = sum(new) + pad
+    rows = min(tokens, hint or tokens) * group
+    assert r.rope3d_paged_attention_last_kernel() == (1 if rows <= 16 or page % 8 else 3 if rows > 128 and dim > 64 else 2)
 
 
-@pytest.mark.parametrize("window", [1, 5, 64, 100, 1000])
+@pytest.mark.parametrize("window", [1, 5, 64, 100, 129, 300, 1000])
 @pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hint", [0, 64])
 @pytest.mark.parametrize("new,lens,page,dim", [([1, 1, 1], [90, 700, 3], 16, 128), ([150, 40, 1], [400, 40, 600], 16, 64),
-                                               ([140], [300], 8, 256)])
-def test_windows(window, causal, new, lens, page, dim):
-    run(7, new, lens, 4, 2, dim, page, HF, window=window, causal=causal)
+                                               ([140], [300], 8, 256), ([310, 1, 500], [900, 40, 800], 32, 128)])
+def test_windows(window, causal, hint, new, lens, page, dim):
+    run(7, new, lens, 4, 2, dim, page, HF, window=window, causal=causal, max_new=hint)
 
 
 @pytest.mark.parametrize("new,lens", [([40, 7], [300, 90]), ([1, 1], [300, 64]), ([200], [200])])
@@ -163,16 +174,17 @@ def test_equal_tokens_without_starts():
         close(got, want, bound)
 
 
-@pytest.mark.parametrize("new", [1, 200])
+@pytest.mark.parametrize("new,hint", [(1, 0), (200, 64), (200, 0)])
 @pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "f16"])
-def test_large_scores(new, dtype):
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_large_scores(new, hint, dtype, dim):
     """Scores of hundreds, rising along the keys, so that the maximum moves in every block."""
     g = gen(15)
     lens = [900]
-    k, v, table = make_cache(g, lens, 16, 1, 64, dtype)
+    k, v, table = make_cache(g, lens, 16, 1, dim, dtype)
     k[table[0, :57].long()] *= torch.linspace(0.1, 12, 57, device=DEV).reshape(57, 1, 1, 1).to(dtype)
-    q = (torch.randn((new, 2, 64), generator=g, device=DEV) * 4).to(dtype)
-    check_attention(r, q, k, v, table, lens, [0, new])
+    q = (torch.randn((new, 2, dim), generator=g, device=DEV) * 4).to(dtype)
+    check_attention(r, q, k, v, table, lens, [0, new], max_new=hint)
 
 
 @pytest.mark.parametrize("new", [1, 150])
