@@ -190,30 +190,31 @@ __global__ void __launch_bounds__(kThreads) paged_rows_kernel(const __grid_const
         for (int i = 0; i < kD / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
-        // A step issues the copies of kStages - 1 steps on; those before 0 only fill the ring.
-        // (One piece of code for all: a call of a few microseconds waits for its instructions too.)
+        // A step issues the copies of kStages - 1 steps on; first those of steps 0 .. kStages - 2.
         int page = page_of(0);
-#pragma unroll 1
-        for (int step = 1 - kStages; step < steps; ++step) {
-            uint32_t live = 0, sk = 0, sv = 0;
-            if (step >= 0) {
-                asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-                __syncwarp();
-                const int slot = step % kStages;
-                sk = sring + slot * kStageBytes<kD>;
-                sv = sk + kHalf;
-                live = s_live[warp][slot];
-                if (step == 0) {
-                    __syncthreads();   // every warp's part of q is there
-                    if constexpr (kKeepQ) {
+#pragma unroll 1   // (a call of a few microseconds waits for its instructions too)
+        for (int step = 0; step < kStages - 1; ++step) {
+            const int after = page_of(step + 1);
+            issue(step, page);
+            page = after;
+        }
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        __syncthreads();   // every warp's part of q is there
+        if constexpr (kKeepQ) {
 #pragma unroll
-                        for (int k = 0; k < kD / 16; ++k) ldm4(qf[k], sq + at<kD>(qr, 2 * k + qc));
-                    }
-                }
-            }
+            for (int k = 0; k < kD / 16; ++k) ldm4(qf[k], sq + at<kD>(qr, 2 * k + qc));
+        }
+
+#pragma unroll 1
+        for (int step = 0; step < steps; ++step) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+            __syncwarp();
+            const int slot = step % kStages;
+            const uint32_t sk = sring + slot * kStageBytes<kD>, sv = sk + kHalf;
+            const uint32_t live = s_live[warp][slot];
             if (live) {
                 float sa[2][4] = {}, sb[2][4] = {};   // even and odd k: chains half as long
-#pragma unroll kKeepQ ? kD / 16 : 4
+#pragma unroll
                 for (int k = 0; k < kD / 16; ++k) {
                     uint32_t b[4], a[4];
                     ldm4(b, sk + at<kD>((lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
