@@ -347,7 +347,12 @@ __global__ void __launch_bounds__(kThreads) paged_rows_kernel(const __grid_const
 
 // ---- partial results ---------------------------------------------------------------
 
-constexpr int kJoinThreads = 512, kJoinRows = 16;
+// Few rows: as many parts as 456, and little in each: blocks of many threads. Tiles: two or
+// three parts, and much: more blocks beside one another (512 threads of 88 registers left one
+// on an SM, 42 us of 224 at 8192 x 8192 x 256).
+template <int kTile> constexpr int kJoinThreadsOf = kTile == kFewRows ? 512 : 256;
+template <int kTile> constexpr int kJoinAtOnce = kTile == kFewRows ? 8 : 4;   // a thread's loads
+constexpr int kJoinRows = 16;
 
 // The sum of weights by the greater of two maxima. (A row that saw nothing has a maximum of
 // -infinity and a sum of 0; one whose scores are all NaN, a sum of NaN.)
@@ -363,14 +368,15 @@ __device__ __forceinline__ float joined(float m, float l, float n, float k) {
 // loads from L2 (notes, then maxima, sums and vectors), a microsecond each: each is
 // made for all parts at once.
 template <bool kF16, int kTile>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ AttnParams p) {
-    __shared__ float s_w[kJoinRows][kMostParts + 1];   // a row's maxima, then weights
-    __shared__ int s_part[kMostParts + 1];             // the item's parts: the part, negative (~part) in its first slot
+__global__ void __launch_bounds__(kJoinThreadsOf<kTile>, kTile == kFewRows ? 1 : 4) paged_join_kernel(const __grid_constant__ AttnParams p) {
+    constexpr int kJoinThreads = kJoinThreadsOf<kTile>, kMost = kTile == kFewRows ? kMostParts : kTileParts;
+    __shared__ float s_w[kJoinRows][kMost + 1];   // a row's maxima, then weights
+    __shared__ int s_part[kMost + 1];             // the item's parts: the part, negative (~part) in its first slot
     __shared__ int s_count[kJoinThreads / 32], s_from[kJoinThreads / 32], s_mine;
     rope3d_tc::grid_release();
     rope3d_tc::grid_wait();
     const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    static_assert(kMostParts <= kJoinThreads, "a part to a thread");
+    static_assert(kMost <= kJoinThreads, "a part to a thread");
     const PartNote n = p.notes[c];
     const long long begin = tid < p.parts ? p.notes[tid].begin : 0, end = tid < p.parts ? p.notes[tid].end : 0;
     const long long first = n.item + p.item_cost;   // the item's first block on the line
@@ -415,33 +421,36 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     int shares = 1;     // threads to a vector
     while (shares < 32 && 2 * shares * count <= kJoinThreads && 2 * shares <= parts) shares *= 2;
     const int share = tid % shares;
-    constexpr int kAtOnce = 8;
+    constexpr int kAtOnce = kJoinAtOnce<kTile>;
     float4 x[kAtOnce];
     auto fetch = [&](int i, int k0) {
         const int r = i % rows, v4 = i / rows;
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j)   // (loads that do not wait for a branch)
-            x[j] = *reinterpret_cast<const float4 *>(slot_at(min(k0 + j * shares, parts - 1)) + (v4 * kTile + row0 + r) * 4);
+        for (int j = 0; j < kAtOnce; ++j) {
+            x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k0 + j * shares < parts)
+                x[j] = *reinterpret_cast<const float4 *>(slot_at(k0 + j * shares) + (v4 * kTile + row0 + r) * 4);
+        }
     };
     const int i_first = i_begin + tid / shares;
     if (i_first < i_end) fetch(i_first, share);
 
     // a warp a row: the greatest maximum, the parts' weights by it, their sum
-    if (warp < rows) {
+    for (int r = warp; r < rows; r += kJoinThreads / 32) {
         float top = -INFINITY, sum = 0.f;
         constexpr int kLoads = 4;
         for (int k0 = lane; k0 < parts; k0 += 32 * kLoads) {
             float m[kLoads], l[kLoads];
 #pragma unroll
             for (int j = 0; j < kLoads; ++j) {
-                const float *of = slot_at(min(k0 + 32 * j, parts - 1)) + vecs * kTile * 4 + row0 + warp;
+                const float *of = slot_at(min(k0 + 32 * j, parts - 1)) + vecs * kTile * 4 + row0 + r;
                 m[j] = of[0];
                 l[j] = of[kTile];
             }
 #pragma unroll
             for (int j = 0; j < kLoads; ++j) {
                 if (k0 + 32 * j >= parts) break;
-                s_w[warp][k0 + 32 * j] = m[j];
+                s_w[r][k0 + 32 * j] = m[j];
                 sum = joined(top, sum, m[j], l[j]);
                 top = fmaxf(top, m[j]);
             }
@@ -453,9 +462,9 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
             top = fmaxf(top, m);
         }
         const float inv = sum > 0.f ? 1.f / sum : sum, ref = top == -INFINITY ? 0.f : top;
-        for (int k = lane; k < parts; k += 32) s_w[warp][k] = ex2(s_w[warp][k] - ref) * inv;
+        for (int k = lane; k < parts; k += 32) s_w[r][k] = ex2(s_w[r][k] - ref) * inv;
         if (lane == 0 && p.lse && mine == 0) {
-            const RowOf row = row_of<kTile>(p, it, row0 + warp);
+            const RowOf row = row_of<kTile>(p, it, row0 + r);
             p.lse[row.token * p.lse_token + row.head] = lse_of(top, sum);
         }
     }
@@ -553,7 +562,8 @@ template <bool kF16>
 int launch_join(const AttnParams &p, const Choice &c, cudaStream_t st) {
     auto *join = c.kind == 2 ? paged_join_kernel<kF16, kPairRows> : c.kind ? paged_join_kernel<kF16, kTileRows>
                                                                            : paged_join_kernel<kF16, kFewRows>;
-    return launch(join, dim3(unsigned(c.parts), unsigned(c.rows / kJoinRows)), kJoinThreads, 0, st, p);
+    return launch(join, dim3(unsigned(c.parts), unsigned(c.rows / kJoinRows)), c.kind ? kJoinThreadsOf<kTileRows> : kJoinThreadsOf<kFewRows>,
+                  0, st, p);
 }
 
 int attention(const rope3d_paged_attention_args *a, bool go, bool check_device, int64_t *need, cudaStream_t st) {
