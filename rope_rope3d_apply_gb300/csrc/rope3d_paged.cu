@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kThreads) paged_rows_kernel(const __grid_const
 // on an SM, 42 us of 224 at 8192 x 8192 x 256).
 template <int kTile> constexpr int kJoinThreadsOf = kTile == kFewRows ? 512 : 256;
 template <int kTile> constexpr int kJoinAtOnce = kTile == kFewRows ? 8 : 4;   // a thread's loads
-constexpr int kJoinRows = 16;
+template <int kTile> constexpr int kJoinRowsOf = kTile == kFewRows ? 16 : 32;   // of a block
 
 // The sum of weights by the greater of two maxima. (A row that saw nothing has a maximum of
 // -infinity and a sum of 0; one whose scores are all NaN, a sum of NaN.)
@@ -368,8 +368,8 @@ __device__ __forceinline__ float joined(float m, float l, float n, float k) {
 // loads from L2 (notes, then maxima, sums and vectors), a microsecond each: each is
 // made for all parts at once.
 template <bool kF16, int kTile>
-__global__ void __launch_bounds__(kJoinThreadsOf<kTile>, kTile == kFewRows ? 1 : 4) paged_join_kernel(const __grid_constant__ AttnParams p) {
-    constexpr int kJoinThreads = kJoinThreadsOf<kTile>, kMost = kTile == kFewRows ? kMostParts : kTileParts;
+__global__ void __launch_bounds__(kJoinThreadsOf<kTile>, kTile == kFewRows ? 2 : 4) paged_join_kernel(const __grid_constant__ AttnParams p) {
+    constexpr int kJoinThreads = kJoinThreadsOf<kTile>, kJoinRows = kJoinRowsOf<kTile>, kMost = kTile == kFewRows ? kMostParts : kTileParts;
     __shared__ float s_w[kJoinRows][kMost + 1];   // a row's maxima, then weights
     __shared__ int s_part[kMost + 1];             // the item's parts: the part, negative (~part) in its first slot
     __shared__ int s_count[kJoinThreads / 32], s_from[kJoinThreads / 32], s_mine;
@@ -562,7 +562,7 @@ template <bool kF16>
 int launch_join(const AttnParams &p, const Choice &c, cudaStream_t st) {
     auto *join = c.kind == 2 ? paged_join_kernel<kF16, kPairRows> : c.kind ? paged_join_kernel<kF16, kTileRows>
                                                                            : paged_join_kernel<kF16, kFewRows>;
-    return launch(join, dim3(unsigned(c.parts), unsigned(c.rows / kJoinRows)), c.kind ? kJoinThreadsOf<kTileRows> : kJoinThreadsOf<kFewRows>,
+    return launch(join, dim3(unsigned(c.parts), unsigned(c.rows / (c.kind ? kJoinRowsOf<kTileRows> : kJoinRowsOf<kFewRows>))), c.kind ? kJoinThreadsOf<kTileRows> : kJoinThreadsOf<kFewRows>,
                   0, st, p);
 }
 

@@ -92,38 +92,73 @@ __device__ __forceinline__ Tile tile_of(const AttnParams &p, const Seq &q, int t
 // 1) / G)) / K) = floor((a + u) / D) blocks from place 0 on, where D = K G / T and a =
 // floor((G (past + K) + T - 1) / T), and a window leaves out floor((c + u) / D) of
 // them, c = floor(G (past - window + 1) / T): sums of floors in a row.
-__device__ __forceinline__ long long floors(long long n, const rope3d::FastDiv &f) {   // sum of floor(i / d) over 0 <= i < n
-    const long long d = f.d, q = n < 0x7fffffff ? (long long)udiv(uint32_t(n), f) : n / d;
+template <typename T>
+__device__ __forceinline__ T floors(T n, const rope3d::FastDiv &f) {   // sum of floor(i / d) over 0 <= i < n
+    const T d = T(f.d), q = sizeof(T) == 4 || n < 0x7fffffff ? T(udiv(uint32_t(n), f)) : n / d;
     return q * (q - 1) / 2 * d + q * (n - q * d);
 }
 
-template <int kRows, int kKeys>
-__device__ __noinline__ long long tiles_cost(const AttnParams &p, const Seq &q, int t) {
-    static_assert(kKeys % kRows == 0 && (kRows == 256 || kRows == 128 || kRows == 16), "D is whole");
-    constexpr int kShift = kRows == 256 ? 8 : kRows == 128 ? 7 : 4;
-    const rope3d::FastDiv &d = p.span;
-    const long long group = p.group.d, past = q.len - q.n;
-    long long sum;
-    if (p.causal) {   // at least 1 each
-        const long long a = (group * (past + kKeys) + kRows - 1) >> kShift;
-        const long long ones = min(max((long long)d.d - a, 0ll), (long long)t);
-        sum = ones + (t > ones ? floors(a + t, d) - floors(a + ones, d) : 0);
-    } else {
-        sum = (long long)max((q.len + kKeys - 1) / kKeys, 1) * t;
+// What the cost of a sequence's tiles depends on, in T: in 32 bits where every number stays
+// below 2^31 (a call of microseconds feels the others).
+template <typename T, int kRows, int kKeys>
+struct Costs {
+    T a, c, each;   // each: blocks of a tile that is not causal
+
+    __device__ __forceinline__ Costs(const AttnParams &p, const Seq &q) {
+        static_assert(kKeys % kRows == 0 && (kRows == 256 || kRows == 128 || kRows == 16), "D is whole");
+        constexpr int kShift = kRows == 256 ? 8 : kRows == 128 ? 7 : 4;
+        const T group = T(p.group.d), past = T(q.len - q.n);
+        a = (group * (past + kKeys) + kRows - 1) >> kShift;
+        c = group * (past - p.window + 1) >> kShift;
+        each = T(max((q.len + kKeys - 1) / kKeys, 1));
     }
-    if (p.window) {
-        const long long c = group * (past - p.window + 1) >> kShift;
-        if (c + t > 0) sum -= floors(c + t, d) - floors(max(c, 0ll), d);
+
+    // of tiles 0 .. t - 1
+    __device__ __forceinline__ T at(const AttnParams &p, int t) const {
+        const T d = T(p.span.d);
+        T sum = each * t;
+        if (p.causal) {   // at least 1 each
+            const T ones = min(max(d - a, T(0)), T(t));
+            sum = ones + (T(t) > ones ? floors<T>(a + t, p.span) - floors<T>(a + ones, p.span) : T(0));
+        }
+        if (p.window && c + t > 0) sum -= floors<T>(c + t, p.span) - floors<T>(max(c, T(0)), p.span);
+        return sum + T(t) * p.item_cost;
     }
-    return sum + (long long)t * p.item_cost;
+
+    // The last of `tiles` that begins at or before place `in` of the line, and where it begins.
+    __device__ __forceinline__ int find(const AttnParams &p, int tiles, T in, T &begins) const {
+        int t = 0, above = tiles;
+        begins = 0;
+#pragma unroll 1
+        while (above - t > 1) {
+            const int mid = (t + above) >> 1;
+            const T v = at(p, mid);
+            if (v <= in) {
+                t = mid;
+                begins = v;
+            } else {
+                above = mid;
+            }
+        }
+        return t;
+    }
+};
+
+// Whether 32 bits do: group * (length + window + tiles' rows) below 2^20 makes every sum of floors
+// less than 2^31 (with 16 rows a tile, n in floors() is below 2^16).
+__device__ __forceinline__ bool small_costs(const AttnParams &p, const Seq &q) {
+    return p.group.d < 64 && q.len < (1 << 13) * 16 / int(p.group.d) && q.n < (1 << 13) * 16 / int(p.group.d) &&
+           p.window < (1 << 13) * 16;
 }
 
 // The cost of one key/value head of a sequence.
 template <int kRows, int kKeys>
-__device__ long long seq_cost(const AttnParams &p, const Seq &q) {
+__device__ __forceinline__ long long seq_cost(const AttnParams &p, const Seq &q) {
     if (q.tiles == 0) return 0;
-    return (q.tiles > 1 ? tiles_cost<kRows, kKeys>(p, q, q.tiles - 1) : 0) + tile_of<kRows, kKeys>(p, q, q.tiles - 1).blocks() +
-           p.item_cost;
+    const long long last = tile_of<kRows, kKeys>(p, q, q.tiles - 1).blocks() + p.item_cost;
+    if (q.tiles == 1) return last;
+    if (small_costs(p, q)) return last + Costs<int, kRows, kKeys>(p, q).at(p, q.tiles - 1);
+    return last + Costs<long long, kRows, kKeys>(p, q).at(p, q.tiles - 1);
 }
 
 // Where part `part` begins (one answer for all threads of the block, by way of
@@ -135,6 +170,7 @@ struct Start {
 
 // floor(total * part / parts)
 __device__ __forceinline__ long long cut(const AttnParams &p, long long total, int part) {
+    if (total < (1 << 21)) return udiv(uint32_t(total) * uint32_t(part), p.cuts);   // (fewer than 1024 parts)
     const long long whole = total < 0x7fffffff ? (long long)udiv(uint32_t(total), p.cuts) : total / p.parts;
     return whole * part + udiv(uint32_t(total - whole * p.parts) * uint32_t(part), p.cuts);
 }
@@ -148,13 +184,18 @@ __device__ __forceinline__ void start_in(const AttnParams &p, int s, const Seq &
     out->s = s;
     out->h = in < 0x7fffffff && head < 0x7fffffff ? int(uint32_t(in) / uint32_t(head)) : int(in / head);
     before += out->h * head;
-    int t = 0, above = q.tiles;   // the last tile that begins at or before the cut
-    while (above - t > 1) {
-        const int mid = (t + above) >> 1;
-        if (before + tiles_cost<kRows, kKeys>(p, q, mid) <= begin) t = mid;
-        else above = mid;
+    int t = 0;
+    if (q.tiles > 1) {
+        if (small_costs(p, q)) {
+            int at;
+            t = Costs<int, kRows, kKeys>(p, q).find(p, q.tiles, int(begin - before), at);
+            before += at;
+        } else {
+            long long at;
+            t = Costs<long long, kRows, kKeys>(p, q).find(p, q.tiles, begin - before, at);
+            before += at;
+        }
     }
-    if (t > 0) before += tiles_cost<kRows, kKeys>(p, q, t);
     out->t = t;
     out->off = int(begin - before);
     out->item = before;
@@ -183,7 +224,7 @@ __device__ void find_start(const AttnParams &p, int part, Start *out, long long 
     if (tid == 0) out->s = -1;
     __syncthreads();
     long long before = inc - sum, total = 0;
-#pragma unroll 1
+#pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
         if (w < warp) before += s_sums[w];
         total += s_sums[w];

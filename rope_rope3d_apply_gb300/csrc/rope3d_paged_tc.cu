@@ -253,15 +253,8 @@ __global__ void __cluster_dims__(kPair ? 2 : 1, 1, 1) __launch_bounds__(kThreads
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::kOffBar + L::kBars * 8);
     unsigned int *late = &g_paged_wait_timeouts;
 
-    grid_release();
-    grid_wait();
-    {   // where this part begins, by way of the (yet unused) Q buffer
-        Start *s_start = reinterpret_cast<Start *>(sm);
-        find_start<kRows, kLine, kThreads>(p, part, s_start, reinterpret_cast<long long *>(sm + 256));
-    }
-    const Start st = *reinterpret_cast<Start *>(sm);
+    // what needs nothing of earlier kernels comes before the wait for them
     if (tid == 0) {
-        if (rank == 0) write_note<kRows, kLine>(p, part, st);
         for (int i = 0; i < L::kQBufs; ++i) {
             mbar_init(q_full(i), kPair ? 8 : 4);
             mbar_init(q_empty(i), 1);
@@ -288,7 +281,13 @@ __global__ void __cluster_dims__(kPair ? 2 : 1, 1, 1) __launch_bounds__(kThreads
         prefetch_map(&map_k);
         prefetch_map(&map_v);
     }
+    grid_wait();
+    grid_release();
     if (warp == 1) tmem_alloc<kPair>(smem_u32(tmem_slot), 512);
+    // where this part begins, by way of the (yet unused) Q buffer
+    find_start<kRows, kLine, kThreads>(p, part, reinterpret_cast<Start *>(sm), reinterpret_cast<long long *>(sm + 256));
+    const Start st = *reinterpret_cast<Start *>(sm);
+    if (tid == 0 && rank == 0) write_note<kRows, kLine>(p, part, st);
     tc_fence_before();
     __syncthreads();   // (also: everyone has read `st`)
     if constexpr (kPair) cluster_sync();   // both blocks' barriers are there
