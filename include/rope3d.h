@@ -779,7 +779,7 @@ int rope3d_paged_attention_check(const rope3d_paged_attention_args *args, int32_
 /* The workspace's size; args->workspace and workspace_bytes are not read. */
 int rope3d_paged_attention_workspace(const rope3d_paged_attention_args *args, int64_t *bytes);
 /* Kernel of this thread's last attention over pages: 1 few rows (warp MMAs), 2
- * tiles of 128 rows (tcgen05), 0 none yet. */
+ * tiles of 128 rows (tcgen05), 3 tiles of 256 rows of pairs of blocks, 0 none yet. */
 int rope3d_paged_attention_last_kernel(void);
 /* How many bounded waits of its kernels ran out (0 unless something is badly
  * wrong; such a launch's output is not to be used); reset clears the count.

@@ -1367,7 +1367,8 @@ def rope3d_apply_axes_last_kernel() -> int:
 
 
 def rope3d_paged_attention_last_kernel() -> int:
-    """Kernel of this thread's last attention over pages: 1 few rows, 2 tiles."""
+    """Kernel of this thread's last attention over pages: 1 few rows, 2 tiles, 3 tiles of pairs
+    of blocks."""
     return int(load_library().rope3d_paged_attention_last_kernel())
 
 
