@@ -793,18 +793,29 @@ def _elsewhere(call, args, first="x"):
     return out
 
 
-def _workspace(cls, fields, query, what, given, like):
+_workspace_bytes = {}   # of calls by their sizes alone
+
+
+def _workspace(cls, fields, query, what, given, like, sizes=None):
     """The packed arguments of a call (`fields` ends before workspace), with its
-    workspace: `given`, or new memory of the size that `query` gives."""
+    workspace: `given`, or new memory of the size that `query` gives (asked once for each
+    `sizes`, all that the answer depends on, where those are told)."""
     body, tail = fields
     lib = _lib or load_library()
-    need = ctypes.c_int64()
     if given is None:
-        _check(getattr(lib, query)(cls.pack(*body, 0, 0, *tail), ctypes.byref(need)), what)
-        if not need.value:
+        need = None if sizes is None else _workspace_bytes.get(sizes)
+        if need is None:
+            asked = ctypes.c_int64()
+            _check(getattr(lib, query)(cls.pack(*body, 0, 0, *tail), ctypes.byref(asked)), what)
+            need = asked.value
+            if sizes is not None:
+                if len(_workspace_bytes) >= 4096:
+                    _workspace_bytes.clear()
+                _workspace_bytes[sizes] = need
+        if not need:
             return cls.pack(*body, 0, 0, *tail), None
-        given = _new((need.value,), _torch.uint8, like)
-        return cls.pack(*body, given.data_ptr(), need.value, *tail), given
+        given = _new((need,), _torch.uint8, like)
+        return cls.pack(*body, given.data_ptr(), need, *tail), given
     if not given.is_contiguous():   # (its elements' bytes have to be there, one after the other)
         raise ValueError("workspace must be contiguous")
     return cls.pack(*body, given.data_ptr(), given.numel() * given.element_size(), *tail), given
@@ -1266,7 +1277,9 @@ def rope3d_paged_attention(q, k_cache, v_cache, page_table, seq_lens, q_starts=N
             *_cache4("k_cache", k_cache, cache, dt), *_cache4("v_cache", v_cache, cache, dt), window, max_new or 0)
     tail = (dim ** -0.5 if scale is None else scale, _code(q), 1 if causal else 0)
     st = _raw_stream(stream, q)
-    args, ws = _workspace(_AttentionArgs, (body, tail), "rope3d_paged_attention_workspace", "rope3d_paged_attention", workspace, q)
+    # (what the workspace depends on: sizes, the caches' strides, whether starts are given)
+    args, ws = _workspace(_AttentionArgs, (body, tail), "rope3d_paged_attention_workspace", "rope3d_paged_attention", workspace, q,
+                          ("attention", q_starts is None, *body[8:17], *body[22:]))
     _check((_lib or load_library()).rope3d_paged_attention(args, st), "rope3d_paged_attention")
     return out if lse is None else (out, lse)
 
@@ -1329,7 +1342,8 @@ def rope3d_cache_compact(cache, page_table, seq_lens, *, page_size=None, reserve
     body = (cache.data_ptr(), page_table.data_ptr(), lens, table_out.data_ptr(), _counter("used", used),
             *_planes(cache), seqs, width, ld, ld_out, cache.shape[2] if page_size is None else page_size, reserve)
     st = _raw_stream(stream, cache)
-    args, ws = _workspace(_CompactArgs, (body, ()), "rope3d_cache_compact_workspace", "rope3d_cache_compact", workspace, cache)
+    args, ws = _workspace(_CompactArgs, (body, ()), "rope3d_cache_compact_workspace", "rope3d_cache_compact", workspace, cache,
+                          ("compact", body[6]))
     _check((_lib or load_library()).rope3d_cache_compact(args, st), "rope3d_cache_compact")
     return table_out, used
 
