@@ -152,9 +152,28 @@ __device__ __forceinline__ void store1(char *p, float v) {
     else *reinterpret_cast<__half *>(p) = __float2half_rn(v);
 }
 
-__device__ __forceinline__ float2 rotate(float a, float b, float2 cs) {
-    return make_float2(__fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y)),
-                       __fadd_rn(__fmul_rn(a, cs.y), __fmul_rn(b, cs.x)));
+__device__ __forceinline__ float2 rotate(float a, float b, float c, float s) {
+    return make_float2(__fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s)), __fadd_rn(__fmul_rn(a, s), __fmul_rn(b, c)));
+}
+
+// kN consecutive floats of shared memory, in the widest words that kN is whole in.
+template <int kN>
+__device__ __forceinline__ void load_floats(float *v, const float *from) {
+    if constexpr (kN % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < kN; i += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(from + i);
+            v[i] = f.x;
+            v[i + 1] = f.y;
+            v[i + 2] = f.z;
+            v[i + 3] = f.w;
+        }
+    } else {
+        static_assert(kN == 2, "two pairs of fp32");
+        const float2 f = *reinterpret_cast<const float2 *>(from);
+        v[0] = f.x;
+        v[1] = f.y;
+    }
 }
 
 __device__ __forceinline__ uint4 ld_stream(const char *p) {   // coherent: in place is allowed
@@ -173,9 +192,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) axes_kernel(const __grid_co
     constexpr int kElem = kType == ROPE3D_F32 ? 4 : 2;
     constexpr int kV = kVec ? 16 / kElem : 1;   // elements of a vector
     constexpr int kInFlight = kVec && kHalves ? 2 : 4;   // units of a thread's loads in flight: 64 bytes
-    extern __shared__ float2 s_tiles[];   // cos and sin, [2][tile][pairs], then freq / 2 pi as (hi, lo) [pairs]
+    // [2 buffers][cos, sin][tile][pairs], then freq / 2 pi as high and low parts [2][pairs]
+    extern __shared__ __align__(16) float s_tiles[];
     const int tile_pairs = p.tile * p.pairs;
-    float2 *s_freq = s_tiles + 2 * tile_pairs;
+    float *s_freq = s_tiles + 4 * tile_pairs;
     __shared__ int64_t s_dst[2][2][kMaxTile];   // append: byte offsets in the caches, -1: nowhere
     __shared__ int s_live[2][kMaxTile];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -185,7 +205,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) axes_kernel(const __grid_co
     for (int j = tid; j < p.pairs; j += kThreads) {
         const double f = double(p.freqs[j]) * kInvTwoPi;
         const float hi = float(f);
-        s_freq[j] = make_float2(hi, float(f - double(hi)));
+        s_freq[j] = hi;
+        s_freq[p.pairs + j] = float(f - double(hi));
     }
     const int64_t second = int64_t(p.pairs) * kElem;
     const uint32_t row = fdiv(uint32_t(tid), p.lanes);
@@ -257,9 +278,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) axes_kernel(const __grid_co
                 const int64_t far = all_near ? 0 : __shfl_sync(0xffffffffu, whole, axis);
                 const bool is_near = all_near || __shfl_sync(0xffffffffu, int(exact), axis);
                 if (j >= p.pairs) continue;
-                float2 cs = is_near ? turn(at, s_freq[j].x, s_freq[j].y) : turn_far(double(far), p.freqs[j]);
-                cs.y *= p.sign;
-                s_tiles[buf * tile_pairs + i * p.pairs + j] = cs;
+                const float2 cs = is_near ? turn(at, s_freq[j], s_freq[p.pairs + j]) : turn_far(double(far), p.freqs[j]);
+                float *to = s_tiles + 2 * buf * tile_pairs + i * p.pairs + j;
+                to[0] = cs.x;
+                to[tile_pairs] = cs.y * p.sign;
             }
         }
     };
@@ -270,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) axes_kernel(const __grid_co
     for (int buf = 0; t0 < p.tokens; t0 += step, buf ^= 1) {
         __syncthreads();   // this tile is prepared, and the one before moved
         const int count = min(p.tile, p.tokens - t0);
-        const float2 *const s_cs = s_tiles + buf * tile_pairs;
+        const float *const s_cos = s_tiles + 2 * buf * tile_pairs;
         for (int at = at0; at < p.per_head; at += p.lanes.d) {
             // this thread's part of each of its rows: its first element and, where it turns, its
             // first pair (interleaved units lie in order; of halves', the first parts do, and behind
@@ -296,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) axes_kernel(const __grid_co
                 const char *const from = in.p + t0 * in.token + h * in.head + int64_t(first) * kElem;
                 char *const to = const_cast<char *>(out.p) + t0 * out.token + h * out.head + int64_t(first) * kElem;
                 const bool turns = turning && which < 2;
-                const float2 *const cs = s_cs + pair;
+                const float *const of_pair = s_cos + pair;
                 // token i's place; false where it has none
                 auto place = [&](int i, char *&dst) {
                     if (kAppend && which > 0) {
@@ -327,14 +349,18 @@ __global__ void __launch_bounds__(kThreads, kBlocks) axes_kernel(const __grid_co
                             if (!on[q]) continue;
                             const int i = i0 + q * p.tokens_step;
                             if (turns) {
-                                const float2 *c = cs + i * p.pairs;
-                                float x[kV], y[kV];
+                                // (a thread's pairs begin at 16 bytes: they are whole vectors of elements)
+                                constexpr int kN = kHalves ? kV : kV / 2;
+                                float x[kV], y[kV], c[kN], s[kN];
+                                const float *at_pair = of_pair + i * p.pairs;
+                                load_floats<kN>(c, at_pair);
+                                load_floats<kN>(s, at_pair + tile_pairs);
                                 widen<kType>(a[q], x);
                                 if constexpr (kHalves) {
                                     widen<kType>(b[q], y);
 #pragma unroll
                                     for (int e = 0; e < kV; ++e) {
-                                        const float2 r = rotate(x[e], y[e], c[e]);
+                                        const float2 r = rotate(x[e], y[e], c[e], s[e]);
                                         x[e] = r.x;
                                         y[e] = r.y;
                                     }
@@ -342,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) axes_kernel(const __grid_co
                                 } else {
 #pragma unroll
                                     for (int e = 0; e < kV; e += 2) {
-                                        const float2 r = rotate(x[e], x[e + 1], c[e / 2]);
+                                        const float2 r = rotate(x[e], x[e + 1], c[e / 2], s[e / 2]);
                                         x[e] = r.x;
                                         x[e + 1] = r.y;
                                     }
@@ -371,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) axes_kernel(const __grid_co
                             if (!on[q]) continue;
                             const int i = i0 + q * p.tokens_step;
                             if (turns) {
-                                const float2 r = rotate(x[q], y[q], cs[i * p.pairs]);
+                                const float2 r = rotate(x[q], y[q], of_pair[i * p.pairs], of_pair[i * p.pairs + tile_pairs]);
                                 x[q] = r.x;
                                 y[q] = r.y;
                             }
@@ -452,7 +478,7 @@ int run(AxesParams &p, int32_t dtype, bool halves, bool vec, const int32_t *sect
     const int rounds = int((int64_t(p.tokens) + int64_t(blocks) * most - 1) / (int64_t(blocks) * most));
     const int tile = int((int64_t(p.tokens) + int64_t(blocks) * rounds - 1) / (int64_t(blocks) * rounds));
     p.tile = tile;
-    const size_t smem = size_t(2 * tile + 1) * p.pairs * sizeof(float2);
+    const size_t smem = size_t(2 * tile + 1) * 2 * p.pairs * sizeof(float);
     const int tiles = (p.tokens + tile - 1) / tile;
     const Kernel<kAppend> fn = dtype == ROPE3D_BF16  ? kernel_of<kAppend, ROPE3D_BF16>(halves, vec)
                                : dtype == ROPE3D_F16 ? kernel_of<kAppend, ROPE3D_F16>(halves, vec)
