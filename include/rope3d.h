@@ -1062,9 +1062,10 @@ int rope3d_testing_max_units_per_launch(int64_t n);
  * and key positions, shared-memory slots) before the access it guards; a
  * failed check adds one to an error count and skips the access, so the kernel
  * finishes. This takes the place of a memory checker where none can run. The
- * block norms' and the feed-forward's kernels have no such checks: they are the
- * same in both builds, and what holds their accesses is their tests (results of
- * every size class against 64 bits, the memory beside every output).
+ * block norms', the feed-forward's and the paged cache's kernels have no such checks
+ * (the last check page numbers, lengths and starts in both builds): they are the
+ * same in both, and what holds their accesses is their tests (results of every
+ * size class against 64 bits, the memory beside every output).
  *   errors  out: failed checks since the last reset (0 in a normal build)
  *   reset   nonzero: clear the count after reading it
  * Returns 1 when the library was built with the checks, 0 when not.

@@ -14,6 +14,11 @@
 // keeps a maximum, a sum and sums of V of its own, so that warps meet only at an
 // item's end. Products are warp MMAs (m16n8k16): at 16 rows the tensor cores have
 // next to nothing to do, and fragments come straight from the swizzled ring.
+// Measured: 64 sequences of 100 to 16,000 places of 8 heads of 128, fp16, pages of 16: 317 us,
+// 6,620 GB/s, 97.5 % of a copy; of 8192 places of 4 heads of 256, bf16: 327 us, 6,570 GB/s; of 64:
+// 97 us, 5,530 GB/s (the softmax's instructions are the same for half the bytes). One sequence
+// of 8191 places of 4 heads of 256: 15.2 us for 33.6 MB, half of it the chain of loads before the
+// first keys and behind the last.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -540,7 +545,10 @@ Choice choose(const rope3d_paged_attention_args &a) {
     int64_t most = b.q_starts ? a.tokens : a.tokens / b.seqs;
     if (a.max_new) most = std::min(most, a.max_new);
     Choice c{};
-    // a pair of blocks wants more rows than one has
+    // By the rows that share keys. 32 sequences of 8192 places of 4 heads of 128, us: 16 rows 94 as few;
+    // 24 rows 173 as few, 107 in tiles; 128 rows 112 in tiles; 160 rows 196 in tiles, 141 in pairs. (Where all
+    // is short, few rows stay ahead for longer: 32 rows of one sequence of 2000 places 14 and 19; the
+    // lengths are not known here.)
     if (most * group > kFewRows && tiles_fit(a)) c.kind = most * group > kTileRows && pairs_fit(a) ? 2 : 1;
     c.rows = c.kind == 2 ? kPairRows : c.kind ? kTileRows : kFewRows;
     c.keys = c.kind == 2 ? 256 : c.kind ? 128 : kKeys;
