@@ -643,8 +643,9 @@ int rope3d_testing_ffn_wait_timeouts(int64_t *count, int32_t reset);
  *                 pairs are read
  *   freqs         device, fp32 [pairs]: rope3d_dit_freqs_host, or
  *                 base^(-2j/d) for each axis or for all
- * The angle is reduced exactly before its cosine and sine are taken (their
- * error is a few units of 2^-24 at any position); products and sums are rounded
+ * Whole turns are taken off the product of position and frequency with its error,
+ * in fp64 where need be, before cosine and sine are taken (within 2^-22 of the true
+ * ones up to 2^50 turns); products and sums are rounded
  * by themselves in fp32, and the result once to `dtype`.
  * q_out may be exactly q, k_out exactly k (same strides); otherwise an output
  * overlaps no argument. Views of one buffer that interleave (the thirds of a

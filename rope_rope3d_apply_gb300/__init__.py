@@ -1255,7 +1255,7 @@ def rope3d_paged_attention(q, k_cache, v_cache, page_table, seq_lens, q_starts=N
     sequence where the caller knows (a better choice of kernel, never another
     result). lse: True, or a float32 [tokens, q_heads] tensor, for the rows' log sum
     exp too. Rows that see no key are zeros (lse -inf); rows behind the last sequence
-    are left as they are. Returns out, or (out, lse). workspace: a contiguous device
+    are left as they are (in a new out or lse: what the memory held). Returns out, or (out, lse). workspace: a contiguous device
     tensor of at least the bytes the call needs (allocated when None)."""
     if stream is not None and (there := _elsewhere(rope3d_paged_attention, dict(locals()), "q")) is not None:
         return there

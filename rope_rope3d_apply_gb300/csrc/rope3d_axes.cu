@@ -8,11 +8,10 @@
 // one cast. A rotation's transpose is the rotation by -angle, so the gradient
 // is the same kernel with sin negated.
 //
-// The angle is never formed: what a turn leaves over, t = frac(position * freq /
-// 2 pi), is taken from an exact product (freq / 2 pi split into two floats, the
-// product's error by fma; in fp64 where a position has no exact float), and
-// sincospi takes it from there. The error is that of sincospi, at position 2^20 as
-// at 0.
+// The angle is never formed: what whole turns leave over, frac(position * freq / 2
+// pi), is taken from a product with its error (freq / 2 pi split into two floats, the error by
+// fma; two doubles where a position has no exact float or the turns are more than 2^21), and
+// sincospi takes it from there. The error is that of sincospi, at position 2^20 as at 0.
 //
 // Each block takes tiles of a few tokens: cos and sin of the tile's tokens and pairs
 // go into shared memory once (64 sincospi a token instead of 64 for each of its
@@ -76,26 +75,32 @@ struct AxesParams {
 
 // ---- angles ----------------------------------------------------------------------
 
-constexpr double kInvTwoPi = 0.15915494309189533577;
+constexpr double kInvTwoPi = 0.15915494309189535, kInvTwoPiLow = -9.839338337591243e-18;   // 1 / 2 pi
+constexpr float kNear = 2097152.f;   // turns up to which two floats and the product's error do: 2^21
 
-// cos and sin of 2 pi position freq / (2 pi), from freq / 2 pi = hi + lo.
-__device__ __forceinline__ float2 turn(float pos, float hi, float lo) {
-    const float a = __fmul_rn(pos, hi);
-    const float e = __fmaf_rn(pos, lo, __fmaf_rn(pos, hi, -a));   // what the product dropped
-    const float whole = __fsub_rn(a, rintf(a));                   // exact
-    const float t = __fadd_rn(whole, e);
-    const float rest = __fsub_rn(e, __fsub_rn(t, whole)) * 6.2831853f;
+// cos and sin of 2 pi t, t = (whole turns +) a + e with a's whole turns taken off.
+__device__ __forceinline__ float2 of_turns(float a, float e) {
+    const float t = __fadd_rn(a, e);
+    const float rest = __fsub_rn(e, __fsub_rn(t, a)) * 6.2831853f;
     float s, c;
     sincospif(2.0f * t, &s, &c);
     return make_float2(__fmaf_rn(-s, rest, c), __fmaf_rn(c, rest, s));
 }
 
-__device__ float2 turn_far(double pos, float freq) {
-    const double a = pos * (double(freq) * kInvTwoPi);
-    const float t = float(a - rint(a));
-    float s, c;
-    sincospif(2.0f * t, &s, &c);
-    return make_float2(c, s);
+// The same of pos * freq / 2 pi in fp64, the product with what it drops.
+__device__ __noinline__ float2 turn_far(double pos, float freq) {
+    const double f = double(freq), c = f * kInvTwoPi, c_low = fma(f, kInvTwoPi, -c) + f * kInvTwoPiLow;
+    const double a = pos * c, e = fma(pos, c, -a) + pos * c_low, r = a - rint(a);   // (r exact)
+    const float hi = float(r);
+    return of_turns(hi, float(r - double(hi) + e));
+}
+
+// cos and sin of 2 pi pos freq / (2 pi), from freq / 2 pi = hi + lo; false where it is too far.
+__device__ __forceinline__ bool turn(float pos, float hi, float lo, float2 &cs) {
+    const float a = __fmul_rn(pos, hi);
+    const float e = __fmaf_rn(pos, lo, __fmaf_rn(pos, hi, -a));   // what the product dropped
+    cs = of_turns(__fsub_rn(a, rintf(a)), e);                     // (the difference is exact)
+    return fabsf(a) <= kNear;
 }
 
 // ---- elements --------------------------------------------------------------------
@@ -265,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) axes_kernel(const __grid_co
                 const int axis = lane < 1 || p.end0 == p.pairs ? 0 : lane < 2 || p.end1 == p.pairs ? 1 : 2;   // (those that have pairs)
                 const int64_t at = axis * p.positions_stride + t;
                 if (p.position_type == ROPE3D_POSITIONS_F32) {
-                    near = static_cast<const float *>(p.positions)[at];
+                    near = static_cast<const float *>(p.positions)[at];   // (`far` is made of it)
                 } else {
                     whole = p.position_type == ROPE3D_POSITIONS_I64 ? static_cast<const int64_t *>(p.positions)[at]
                                                                     : static_cast<const int32_t *>(p.positions)[at];
@@ -279,10 +284,15 @@ __global__ void __launch_bounds__(kThreads, kBlocks) axes_kernel(const __grid_co
             for (int j0 = 0; j0 < p.pairs; j0 += 32) {
                 const int j = j0 + lane, axis = j < p.end0 ? 0 : j < p.end1 ? 1 : 2;
                 const float at = __shfl_sync(0xffffffffu, near, axis);
-                const int64_t far = all_near ? 0 : __shfl_sync(0xffffffffu, whole, axis);
-                const bool is_near = all_near || __shfl_sync(0xffffffffu, int(exact), axis);
+                bool is_near = all_near || __shfl_sync(0xffffffffu, int(exact), axis);
+                const int64_t far = __shfl_sync(0xffffffffu, whole, axis);
                 if (j >= p.pairs) continue;
-                const float2 cs = is_near ? turn(at, s_freq[j], s_freq[p.pairs + j]) : turn_far(double(far), p.freqs[j]);
+                float2 cs;
+                is_near = turn(at, s_freq[j], s_freq[p.pairs + j], cs) && is_near;
+                if (!is_near) {
+                    const bool fractions = !(kAppend && p.position_type < 0) && p.position_type == ROPE3D_POSITIONS_F32;
+                    cs = turn_far(fractions ? double(at) : double(far), p.freqs[j]);
+                }
                 float *to = s_tiles + 2 * buf * tile_pairs + i * p.pairs + j;
                 to[0] = cs.x;
                 to[tile_pairs] = cs.y * p.sign;

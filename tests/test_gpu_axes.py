@@ -69,6 +69,26 @@ def test_rotation_and_gradient(case, dtype, pairing):
             assert torch.equal(y[..., 2 * pairs:], x[..., 2 * pairs:])
 
 
+@pytest.mark.parametrize("kind,far,top", [("f32", 1, 2e4), ("f32", 1 << 26, 1.0), ("i64", 1 << 20, 2e4), ("i64", 1 << 33, 1.0),
+                                          ("i32", (1 << 31) - 1, 1.0), ("i64", 1 << 12, 1e7), ("f32", 3000, 1e5)])
+def test_far_positions_and_high_frequencies(kind, far, top):
+    """Frequencies far above 1 (a vector that grows with the pair) and positions that no fp32 has:
+    against angles reduced with whole numbers."""
+    from fractions import Fraction
+
+    g, pairs, tokens = gen(40), 16, 12
+    freqs = torch.tensor([top ** (j / (pairs - 1)) if top > 1 else 10000.0 ** (-j / pairs) for j in range(pairs)], device=DEV)
+    pos = positions_of(g, kind, 1, tokens, far)
+    # 40 digits of 1 / 2 pi: the reduced angle is right to 2^-53 or so
+    inv = Fraction(1591549430918953357688837633725143620345, 10 ** 40)
+    turns = [[Fraction(p) * Fraction(f) * inv for f in freqs.tolist()] for p in pos[0].tolist()]
+    a = torch.tensor([[float(t - round(t)) for t in row] for row in turns], dtype=torch.float64, device=DEV) * (2 * math.pi)
+    q = torch.randn((tokens, 2, 2 * pairs), generator=g, device=DEV)
+    for pairing in PAIRING:
+        got, _ = r.rope3d_apply_axes(q, None, pos, freqs, pairing=PAIRING[pairing])
+        close(got, *rotate64(q, a, pairing, pairs))
+
+
 def test_agrees_with_whole_grids():
     """Positions that are a grid's coordinates, frequencies as the tables have them: the
     operator for grids within the error of the tables' rounding and the cosine's."""

@@ -59,6 +59,9 @@ ONE = [
     ([5000] + [40] * 70, 8, 2, 64, 32),
     ([999, 1024, 1025], 7, 1, 96, 128),
     ([640, 40], 20, 1, 128, 16),
+    ([300, 41], 64, 1, 64, 16),
+    ([90], 130, 1, 128, 8),
+    ([1 + 7 * (i % 11) for i in range(3000)], 2, 1, 64, 8),
 ]
 
 
@@ -83,6 +86,11 @@ CHUNKS = [
     ([90, 31], [400, 31], 4, 1, 192, 3),
     ([512], [1024], 8, 1, 128, 32),
     ([700], [700], 2, 1, 256, 64),
+    ([40, 9], [200, 9], 66, 1, 128, 16),
+    ([33, 5], [100, 700], 4, 2, 8, 8),
+    ([150], [333], 3, 1, 136, 40),
+    ([20, 3], [40000, 70000], 8, 1, 200, 128),
+    ([1, 0, 2] * 400, [3, 0, 2] * 400, 2, 1, 64, 8),
 ]
 
 
