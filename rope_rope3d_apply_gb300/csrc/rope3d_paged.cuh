@@ -144,11 +144,12 @@ struct Costs {
     }
 };
 
-// Whether 32 bits do: group * (length + window + tiles' rows) below 2^20 makes every sum of floors
-// less than 2^31 (with 16 rows a tile, n in floors() is below 2^16).
+// Whether 32 bits do: with fewer than 64 rows a token, and tokens and places times those below
+// 2^17, n in floors() is below 2^15 and every sum of theirs below 2^31 (16 rows a tile; larger
+// tiles less).
 __device__ __forceinline__ bool small_costs(const AttnParams &p, const Seq &q) {
-    return p.group.d < 64 && q.len < (1 << 13) * 16 / int(p.group.d) && q.n < (1 << 13) * 16 / int(p.group.d) &&
-           p.window < (1 << 13) * 16;
+    const int most = (1 << 17) / int(p.group.d);
+    return p.group.d < 64 && q.len < most && q.n < most && p.window < (1 << 17);
 }
 
 // The cost of one key/value head of a sequence.

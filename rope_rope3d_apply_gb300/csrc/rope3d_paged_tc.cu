@@ -134,18 +134,18 @@ __device__ __forceinline__ void arrive(uint32_t bar) {
 }
 
 // An arrival on the first block's barrier (this block's, without pairs): with this
-// thread's writes to shared memory; or relaxed, where what it hands over lies in tensor
-// memory (complete and fenced before) or is still to be copied. (A release to the cluster waits
-// for all of the thread's writes: 1,000 clocks of each block's hand-over, measured.)
+// thread's writes to shared memory, for the cluster; or light, where what it hands over lies in
+// tensor memory (complete and fenced before) or is still to be copied. (A release to the
+// cluster waits for all of the thread's writes: 1,000 clocks of each block's hand-over, measured.)
 template <bool kPair>
 __device__ __forceinline__ void arrive_first(uint32_t bar) {
     if constexpr (kPair) mbar_arrive_cluster(map_rank(bar, 0));
     else arrive(bar);
 }
 template <bool kPair>
-__device__ __forceinline__ void arrive_first_relaxed(uint32_t bar) {
+__device__ __forceinline__ void arrive_first_light(uint32_t bar) {
     if constexpr (kPair)
-        asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_rank(bar, 0)) : "memory");
+        asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(map_rank(bar, 0)) : "memory");
     else
         arrive(bar);
 }
@@ -362,7 +362,7 @@ __global__ void __cluster_dims__(kPair ? 2 : 1, 1, 1) __launch_bounds__(kThreads
                         __syncwarp();
                         if (lane == 0) arrive_first<kPair>(full);
                     } else if (!count && lane == 0) {
-                        arrive_first_relaxed<kPair>(full);
+                        arrive_first_light<kPair>(full);
                     }
                 }
             }
@@ -525,7 +525,7 @@ __global__ void __cluster_dims__(kPair ? 2 : 1, 1, 1) __launch_bounds__(kThreads
             }
             __syncwarp();
             tc_fence_before();
-            if (lane == 0) arrive_first_relaxed<kPair>(o_empty);
+            if (lane == 0) arrive_first_light<kPair>(o_empty);
             if (!on) return;
             if (of.whole) {
                 if (p.lse) p.lse[o.token * p.lse_token + o.head] = sum > 0.f ? (top + log2f(sum)) * 0.69314718f : sum == 0.f ? -INFINITY : sum;
@@ -660,7 +660,7 @@ __global__ void __cluster_dims__(kPair ? 2 : 1, 1, 1) __launch_bounds__(kThreads
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_first_relaxed<kPair>(p_full(sb));
+                if (lane == 0) arrive_first_light<kPair>(p_full(sb));
             }
             const bool last = ((g - 1) & 1) == group;   // the item's last block was this group's
             if (any_row && !last) receive();
@@ -723,7 +723,9 @@ int launch_tile(const AttnParams &p, int box, const CUtensorMap &k, const CUtens
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return ROPE3D_ERR_CUDA;
     if (!ready[dev].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Lay<kD, kPair>::kBytes)) != cudaSuccess) {
+        cudaFuncAttributes attr{};   // (a block launched with fewer registers would wait for more without an end)
+        if (cudaFuncGetAttributes(&attr, fn) != cudaSuccess || attr.numRegs * kThreads < 256 * (kSoftRegs + kOtherRegs) ||
+            cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Lay<kD, kPair>::kBytes)) != cudaSuccess) {
             cudaGetLastError();
             return ROPE3D_ERR_CUDA;
         }

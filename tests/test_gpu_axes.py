@@ -39,7 +39,7 @@ SHAPES = [
     (1, 1, 1, 16, (8, 0, 0), 1),
     (77, 4, 2, 64, (8, 12, 12), None),
     (300, 8, 4, 256, (32, 48, 48), 1),
-    (33, 24, 24, 128, (16, 24, 24), 1),
+    (33, 20, 20, 128, (16, 24, 24), 1),
     (1000, 3, 1, 80, (40,), None),
     (50, 2, 2, 48, (3, 5, 7), 2),
     (9, 5, 1, 6, (1, 1, 1), 2),
