@@ -744,7 +744,7 @@ int rope3d_cache_append_check(const rope3d_cache_append_args *args, int32_t chec
  *                 same sequence and key/value head whose mask leaves it out.)
  *   head_dim      a multiple of 8, up to 256; q_heads a multiple of kv_heads
  *   lse           fp32 [tokens, q_heads], token stride lse_stride; NULL: not kept
- *   scale         finite in fp32
+ *   scale         above 0, and finite in fp32
  *   window        0: none
  *   max_new       at least the most new tokens of a sequence, for the choice of the
  *                 kernel alone (results do not depend on it); 0: not known

@@ -768,8 +768,8 @@ def _fresh(like):
 
 def _elsewhere(call, args, first="x"):
     """The results of `call` (arguments by name, `first` on the call's device) where its
-    stream is not torch's current one, else None. It then runs with that stream current, so that the memory
-    it allocates is that stream's. (The current stream's may be memory that its pending
+    stream is not torch's current one, else None. It then runs with that stream current,
+    so that the memory it allocates is that stream's. (The current stream's may be memory that its pending
     work still reads.) What it returns is kept from other use until the current stream
     has passed it too, and what it is given until its own stream has: a temporary may be
     freed on return. (Not on streams that torch did not make, which may be gone by the
@@ -1255,8 +1255,9 @@ def rope3d_paged_attention(q, k_cache, v_cache, page_table, seq_lens, q_starts=N
     sequence where the caller knows (a better choice of kernel, never another
     result). lse: True, or a float32 [tokens, q_heads] tensor, for the rows' log sum
     exp too. Rows that see no key are zeros (lse -inf); rows behind the last sequence
-    are left as they are (in a new out or lse: what the memory held). Returns out, or (out, lse). workspace: a contiguous device
-    tensor of at least the bytes the call needs (allocated when None)."""
+    are left as they are (in a new out or lse: what the memory held). Returns out, or
+    (out, lse). workspace: a contiguous device tensor of at least the bytes the call
+    needs (allocated when None)."""
     if stream is not None and (there := _elsewhere(rope3d_paged_attention, dict(locals()), "q")) is not None:
         return there
     _torch or _use_torch()

@@ -143,10 +143,6 @@ __device__ __forceinline__ uint4 narrow(const float *f) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int kType> struct Elem { using T = float; };
-template <> struct Elem<ROPE3D_BF16> { using T = __nv_bfloat16; };
-template <> struct Elem<ROPE3D_F16> { using T = __half; };
-
 template <int kType>
 __device__ __forceinline__ float load1(const char *p) {
     if constexpr (kType == ROPE3D_F32) return *reinterpret_cast<const float *>(p);
@@ -427,11 +423,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) axes_kernel(const __grid_co
     }
 }
 
-template <bool kAppend>
 using Kernel = void (*)(AxesParams);
 
 template <bool kAppend, int kType>
-Kernel<kAppend> kernel_of(bool halves, bool vec) {
+Kernel kernel_of(bool halves, bool vec) {
     if (halves) return vec ? axes_kernel<kType, true, kAppend, true> : axes_kernel<kType, true, kAppend, false>;
     return vec ? axes_kernel<kType, false, kAppend, true> : axes_kernel<kType, false, kAppend, false>;
 }
@@ -494,9 +489,9 @@ int run(AxesParams &p, int32_t dtype, bool halves, bool vec, const int32_t *sect
     p.tile = tile;
     const size_t smem = size_t(2 * tile + 1) * 2 * p.pairs * sizeof(float);
     const int tiles = (p.tokens + tile - 1) / tile;
-    const Kernel<kAppend> fn = dtype == ROPE3D_BF16  ? kernel_of<kAppend, ROPE3D_BF16>(halves, vec)
-                               : dtype == ROPE3D_F16 ? kernel_of<kAppend, ROPE3D_F16>(halves, vec)
-                                                     : kernel_of<kAppend, ROPE3D_F32>(halves, vec);
+    const Kernel fn = dtype == ROPE3D_BF16  ? kernel_of<kAppend, ROPE3D_BF16>(halves, vec)
+                      : dtype == ROPE3D_F16 ? kernel_of<kAppend, ROPE3D_F16>(halves, vec)
+                                            : kernel_of<kAppend, ROPE3D_F32>(halves, vec);
     const int rc = launch(fn, dim3(unsigned(std::min(tiles, blocks))), kThreads, smem, st, p);
     if (rc == ROPE3D_OK) t_axes_kernel = vec ? 1 : 2;
     return rc;

@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kThreads) paged_rows_kernel(const __grid_const
     rope3d_tc::grid_wait();
     find_start<kRows, kKeys, kThreads>(p, blockIdx.x, &s_start, s_sums);
     const Start st = s_start;
-    if (tid == 0) write_note<kRows, kKeys>(p, blockIdx.x, st);
+    if (tid == 0) write_note(p, blockIdx.x, st);
     const int chunks = p.head_dim / 8;
 
     Walker<kRows, kKeys> walk(p, st);
@@ -367,7 +367,7 @@ __device__ __forceinline__ float joined(float m, float l, float n, float k) {
 }
 
 // Block (c, y): if the cut at the beginning of part c falls into an item (behind its first
-// block), rows 16 y .. 16 y + 15 of that item from all parts that computed some of it, in
+// block), rows kJoinRows y and on of that item from all parts that computed some of it, in
 // order; the blocks of all cuts in an item share its vectors, and where a block has fewer
 // vectors than threads, threads share a vector's parts. What bounds it is the chain of
 // loads from L2 (notes, then maxima, sums and vectors), a microsecond each: each is
@@ -570,8 +570,9 @@ template <bool kF16>
 int launch_join(const AttnParams &p, const Choice &c, cudaStream_t st) {
     auto *join = c.kind == 2 ? paged_join_kernel<kF16, kPairRows> : c.kind ? paged_join_kernel<kF16, kTileRows>
                                                                            : paged_join_kernel<kF16, kFewRows>;
-    return launch(join, dim3(unsigned(c.parts), unsigned(c.rows / (c.kind ? kJoinRowsOf<kTileRows> : kJoinRowsOf<kFewRows>))), c.kind ? kJoinThreadsOf<kTileRows> : kJoinThreadsOf<kFewRows>,
-                  0, st, p);
+    const int rows = c.kind ? kJoinRowsOf<kTileRows> : kJoinRowsOf<kFewRows>;
+    const int threads = c.kind ? kJoinThreadsOf<kTileRows> : kJoinThreadsOf<kFewRows>;
+    return launch(join, dim3(unsigned(c.parts), unsigned(c.rows / rows)), threads, 0, st, p);
 }
 
 int attention(const rope3d_paged_attention_args *a, bool go, bool check_device, int64_t *need, cudaStream_t st) {

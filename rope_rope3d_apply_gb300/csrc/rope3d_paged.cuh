@@ -9,9 +9,9 @@
 // beginning and ending an item. The items in order (sequence, key/value head, tile)
 // make a line that is cut into as many equal parts as there are thread blocks, wherever
 // the cuts fall: a prompt, one token over a long cache and ragged mixtures are
-// divided alike, and nothing has to be known on the host. An item that a cut divides leaves partial results (sums not
-// yet divided, with the row's maximum and sum) in the workspace, which a second
-// kernel adds in order.
+// divided alike, and nothing has to be known on the host. An item that a cut divides
+// leaves partial results (sums not yet divided, with the row's maximum and sum) in
+// the workspace, which a second kernel adds in order.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -333,7 +333,6 @@ __device__ __forceinline__ float *slot_of(const AttnParams &p, int part, bool he
     return p.partial + (2 * int64_t(part) + (head ? 0 : 1)) * slot_floats<kRows>(p.head_dim);
 }
 
-template <int kRows, int kKeys>
 __device__ __forceinline__ void write_note(const AttnParams &p, int part, const Start &st) {
     PartNote n;
     n.begin = st.begin;

@@ -125,8 +125,8 @@ __device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap *map, 
             ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(slot), "r"(head), "r"(page), "r"(bar) : "memory");
     else
         asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
-        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(slot), "r"(head), "r"(page), "r"(bar) : "memory");
+            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+            ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(slot), "r"(head), "r"(page), "r"(bar) : "memory");
 }
 
 __device__ __forceinline__ void arrive(uint32_t bar) {
@@ -287,7 +287,7 @@ __global__ void __cluster_dims__(kPair ? 2 : 1, 1, 1) __launch_bounds__(kThreads
     // where this part begins, by way of the (yet unused) Q buffer
     find_start<kRows, kLine, kThreads>(p, part, reinterpret_cast<Start *>(sm), reinterpret_cast<long long *>(sm + 256));
     const Start st = *reinterpret_cast<Start *>(sm);
-    if (tid == 0 && rank == 0) write_note<kRows, kLine>(p, part, st);
+    if (tid == 0 && rank == 0) write_note(p, part, st);
     tc_fence_before();
     __syncthreads();   // (also: everyone has read `st`)
     if constexpr (kPair) cluster_sync();   // both blocks' barriers are there
@@ -299,152 +299,152 @@ __global__ void __cluster_dims__(kPair ? 2 : 1, 1, 1) __launch_bounds__(kThreads
     Item it;
 
     if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == 0 || warp == 3) {
-        // ---- copies of K (warp 0) or V (warp 3)
-        const bool is_v = warp == 3;
-        const CUtensorMap *map = is_v ? &map_v : &map_k;
-        const int slots = is_v ? L::kVSlots : L::kKSlots;
-        const uint32_t ring = base + (is_v ? L::kOffV : L::kOffK);
-        int n = 0, landings = 0;   // pieces so far; of them, those that were waited for here
-        while (walk.next(it)) {
-            const int *table = p.batch.table + it.s * p.batch.table_stride;
-            const Blocks<kLine> bl(it);
-            for (int b = bl.begin; b < bl.end; ++b) {
-                const int k0 = max(it.tile.k0 - b * kKeys, 0), k1 = min(it.tile.k1 - b * kKeys, kKeys);   // what rows see
-#pragma unroll
-                for (int piece = 0; piece < L::kPieces; ++piece, ++n) {
-                    const int slot = n % slots;
-                    const uint32_t full = is_v ? v_full(slot) : k_full(slot), empty = is_v ? v_empty(slot) : k_empty(slot);
-                    // this piece: places row0 .. row0 + rows - 1 of the block, 64 cols channels from `channel0` on
-                    const int row0 = is_v ? piece * L::kVRows : rank * L::kKRows, rows = is_v ? L::kVRows : L::kKRows;
-                    const int cols = is_v ? L::kVCols : L::kKCols;
-                    const int channel0 = is_v ? rank * L::kVCols * 64 : piece * L::kKCols * 64;
-                    // boxes [from, to) of the block hold places of the piece that rows see
-                    const int from = max(k0, row0) / box_places, to = (min(k1, row0 + rows) + box_places - 1) / box_places;
-                    const int count = max(to - from, 0);
-                    if (n >= slots) mbar_wait(empty, uint32_t(n / slots - 1) & 1u, dead, late);
-                    dead = __any_sync(0xffffffffu, dead);
-                    const bool clean = !is_v || (k0 <= row0 && k1 >= row0 + rows);   // nothing to be zeroed
-                    const uint32_t dst = ring + uint32_t(slot) * (is_v ? L::kVPiece : L::kKPiece);
-                    if (count && !dead) {
-                        const uint32_t bytes = uint32_t(count * cols * box_places) * 128u;
-                        if (lane == 0) {
-                            if (clean) expect_first<kPair>(full, bytes);
-                            else mbar_expect_tx(v_land, bytes);
-                        }
-                        __syncwarp();
-                        const uint32_t bar = !clean ? v_land : kPair ? map_rank(full, 0) : full;
-                        for (int i = lane; i < count * cols; i += 32) {
-                            const int box = from + i / cols, col = i % cols;
-                            const int place = b * kKeys + box * box_places, index = int(udiv(uint32_t(place), p.page));
-                            int page = index < p.batch.width ? table[index] : -1;
-                            if (page < 0 || page >= p.batch.pages) page = p.batch.pages;   // outside: filled with zeros
-                            tma_load4<kPair>(dst + uint32_t(col * rows + box * box_places - row0) * 128u, map, channel0 + col * 64,
-                                             place - index * p.batch.page_size, it.h, page, bar);
-                        }
-                        __syncwarp();
-                    }
-                    if (!clean) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == 0 || warp == 3) {
+            // ---- copies of K (warp 0) or V (warp 3)
+            const bool is_v = warp == 3;
+            const CUtensorMap *map = is_v ? &map_v : &map_k;
+            const int slots = is_v ? L::kVSlots : L::kKSlots;
+            const uint32_t ring = base + (is_v ? L::kOffV : L::kOffK);
+            int n = 0, landings = 0;   // pieces so far; of them, those that were waited for here
+            while (walk.next(it)) {
+                const int *table = p.batch.table + it.s * p.batch.table_stride;
+                const Blocks<kLine> bl(it);
+                for (int b = bl.begin; b < bl.end; ++b) {
+                    const int k0 = max(it.tile.k0 - b * kKeys, 0), k1 = min(it.tile.k1 - b * kKeys, kKeys);   // what rows see
+    #pragma unroll
+                    for (int piece = 0; piece < L::kPieces; ++piece, ++n) {
+                        const int slot = n % slots;
+                        const uint32_t full = is_v ? v_full(slot) : k_full(slot), empty = is_v ? v_empty(slot) : k_empty(slot);
+                        // this piece: places row0 .. row0 + rows - 1 of the block, 64 cols channels from `channel0` on
+                        const int row0 = is_v ? piece * L::kVRows : rank * L::kKRows, rows = is_v ? L::kVRows : L::kKRows;
+                        const int cols = is_v ? L::kVCols : L::kKCols;
+                        const int channel0 = is_v ? rank * L::kVCols * 64 : piece * L::kKCols * 64;
+                        // boxes [from, to) of the block hold places of the piece that rows see
+                        const int from = max(k0, row0) / box_places, to = (min(k1, row0 + rows) + box_places - 1) / box_places;
+                        const int count = max(to - from, 0);
+                        if (n >= slots) mbar_wait(empty, uint32_t(n / slots - 1) & 1u, dead, late);
+                        dead = __any_sync(0xffffffffu, dead);
+                        const bool clean = !is_v || (k0 <= row0 && k1 >= row0 + rows);   // nothing to be zeroed
+                        const uint32_t dst = ring + uint32_t(slot) * (is_v ? L::kVPiece : L::kKPiece);
                         if (count && !dead) {
-                            mbar_wait(v_land, uint32_t(landings) & 1u, dead, late);
-                            dead = __any_sync(0xffffffffu, dead);
-                            ++landings;
+                            const uint32_t bytes = uint32_t(count * cols * box_places) * 128u;
+                            if (lane == 0) {
+                                if (clean) expect_first<kPair>(full, bytes);
+                                else mbar_expect_tx(v_land, bytes);
+                            }
+                            __syncwarp();
+                            const uint32_t bar = !clean ? v_land : kPair ? map_rank(full, 0) : full;
+                            for (int i = lane; i < count * cols; i += 32) {
+                                const int box = from + i / cols, col = i % cols;
+                                const int place = b * kKeys + box * box_places, index = int(udiv(uint32_t(place), p.page));
+                                int page = index < p.batch.width ? table[index] : -1;
+                                if (page < 0 || page >= p.batch.pages) page = p.batch.pages;   // outside: filled with zeros
+                                tma_load4<kPair>(dst + uint32_t(col * rows + box * box_places - row0) * 128u, map, channel0 + col * 64,
+                                                 place - index * p.batch.page_size, it.h, page, bar);
+                            }
+                            __syncwarp();
                         }
-                        const int a = min(max(k0 - row0, 0), rows), z = max(min(k1 - row0, rows), a);   // rows [a, z) are seen
-                        for (int i = lane; i < (rows - (z - a)) * 8 * cols; i += 32) {
-                            const int chunk = i % 8, col = i / 8 % cols, r = i / (8 * cols);
-                            const int row = r < a ? r : r + (z - a);
-                            *reinterpret_cast<uint4 *>(sm + (dst - base) + uint32_t(col * rows + row) * 128u + chunk * 16) =
-                                make_uint4(0, 0, 0, 0);
+                        if (!clean) {
+                            if (count && !dead) {
+                                mbar_wait(v_land, uint32_t(landings) & 1u, dead, late);
+                                dead = __any_sync(0xffffffffu, dead);
+                                ++landings;
+                            }
+                            const int a = min(max(k0 - row0, 0), rows), z = max(min(k1 - row0, rows), a);   // rows [a, z) are seen
+                            for (int i = lane; i < (rows - (z - a)) * 8 * cols; i += 32) {
+                                const int chunk = i % 8, col = i / 8 % cols, r = i / (8 * cols);
+                                const int row = r < a ? r : r + (z - a);
+                                *reinterpret_cast<uint4 *>(sm + (dst - base) + uint32_t(col * rows + row) * 128u + chunk * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                            }
+                            fence_async_smem();
+                            __syncwarp();
+                            if (lane == 0) arrive_first<kPair>(full);
+                        } else if (!count && lane == 0) {
+                            arrive_first_light<kPair>(full);
                         }
-                        fence_async_smem();
-                        __syncwarp();
-                        if (lane == 0) arrive_first<kPair>(full);
-                    } else if (!count && lane == 0) {
-                        arrive_first_light<kPair>(full);
                     }
                 }
             }
-        }
-        if (dead && lane == 0 && rank == 0) {   // (the other block of a pair waits below)
-            const int first = max(n - slots, 0);
-            for (int i = first; i < n; ++i) {
+            if (dead && lane == 0 && rank == 0) {   // (the other block of a pair waits below)
+                const int first = max(n - slots, 0);
+                for (int i = first; i < n; ++i) {
+                    bool gone = false;
+                    mbar_wait(is_v ? v_full(i % slots) : k_full(i % slots), uint32_t(i / slots) & 1u, gone, late);
+                }
+            }
+            if (dead && lane == 0 && is_v && landings) {
                 bool gone = false;
-                mbar_wait(is_v ? v_full(i % slots) : k_full(i % slots), uint32_t(i / slots) & 1u, gone, late);
+                mbar_wait(v_land, uint32_t(landings - 1) & 1u, gone, late);
             }
-        }
-        if (dead && lane == 0 && is_v && landings) {
-            bool gone = false;
-            mbar_wait(v_land, uint32_t(landings - 1) & 1u, gone, late);
-        }
-    } else if (warp == 1) {
-        // ---- O += P V
-        if (lane == 0 && rank == 0) {
-            constexpr uint32_t id = idesc(kRows, kD, !kF16, false, true);
-            int g = 0, n = 0, items = 0;
-            while (walk.next(it)) {
-                if (it.begin >= it.end) continue;
-                if (items) mbar_wait(o_empty, uint32_t(items - 1) & 1u, dead, late);
-                ++items;
-                const Blocks<kLine> bl(it);
-                for (int b = bl.begin; b < bl.end; ++b, ++g) {
-                    const int sb = g % L::kSBufs;
-                    mbar_wait(p_full(sb), uint32_t(g / L::kSBufs) & 1u, dead, late);
-#pragma unroll
-                    for (int piece = 0; piece < L::kPieces; ++piece, ++n) {
-                        const int slot = n % L::kVSlots;
-                        mbar_wait(v_full(slot), uint32_t(n / L::kVSlots) & 1u, dead, late);
-                        tc_fence_after();
-                        const uint32_t v = base + L::kOffV + uint32_t(slot) * L::kVPiece;
-                        const uint32_t pa = tmem + uint32_t(sb * 128 + piece * (L::kVRows / 2));
-#pragma unroll
-                        for (int j = 0; j < L::kVRows / 16; ++j)
-                            mma_ta<kPair>(tmem + L::kColO, pa + uint32_t(8 * j), sdesc(v + uint32_t(j) * 2048u, L::kVRows * 128, 1024),
-                                          id, b > bl.begin || piece > 0 || j > 0 ? 1u : 0u);
-                        commit_all<kPair>(v_empty(slot));
-                    }
-                    commit_all<kPair>(s_empty(sb));
-                    if (b == bl.end - 1) commit_all<kPair>(o_full);
-                }
-            }
-        }
-    } else if (warp == 2) {
-        // ---- S = Q K^T
-        if (lane == 0 && rank == 0) {
-            constexpr uint32_t id = idesc(kRows, kKeys, !kF16, false, false);
-            int g = 0, n = 0, items = 0;
-            while (walk.next(it)) {
-                if (it.begin >= it.end) continue;
-                const int qb = items % L::kQBufs;
-                mbar_wait(q_full(qb), uint32_t(items / L::kQBufs) & 1u, dead, late);
-                ++items;
-                const uint32_t q = base + uint32_t(qb) * L::kQBytes;
-                const Blocks<kLine> bl(it);
-                for (int b = bl.begin; b < bl.end; ++b, ++g) {
-                    const int sb = g % L::kSBufs;
-                    if (g >= L::kSBufs) mbar_wait(s_empty(sb), uint32_t(g / L::kSBufs - 1) & 1u, dead, late);
-#pragma unroll
-                    for (int piece = 0; piece < L::kPieces; ++piece, ++n) {
-                        const int slot = n % L::kKSlots;
-                        mbar_wait(k_full(slot), uint32_t(n / L::kKSlots) & 1u, dead, late);
-                        tc_fence_after();
-                        const uint32_t k = base + L::kOffK + uint32_t(slot) * L::kKPiece;
-                        const uint32_t qp = q + uint32_t(piece * L::kKCols) * kColBlock;
-#pragma unroll
-                        for (int j = 0; j < 4 * L::kKCols; ++j) {
-                            const uint32_t off = uint32_t(j & 3) * 32u;
-                            mma<kPair>(tmem + uint32_t(sb * 128), sdesc(qp + uint32_t(j >> 2) * kColBlock + off, 16, 1024),
-                                       sdesc(k + uint32_t(j >> 2) * (L::kKRows * 128) + off, 16, 1024), id, piece > 0 || j > 0 ? 1u : 0u);
+        } else if (warp == 1) {
+            // ---- O += P V
+            if (lane == 0 && rank == 0) {
+                constexpr uint32_t id = idesc(kRows, kD, !kF16, false, true);
+                int g = 0, n = 0, items = 0;
+                while (walk.next(it)) {
+                    if (it.begin >= it.end) continue;
+                    if (items) mbar_wait(o_empty, uint32_t(items - 1) & 1u, dead, late);
+                    ++items;
+                    const Blocks<kLine> bl(it);
+                    for (int b = bl.begin; b < bl.end; ++b, ++g) {
+                        const int sb = g % L::kSBufs;
+                        mbar_wait(p_full(sb), uint32_t(g / L::kSBufs) & 1u, dead, late);
+    #pragma unroll
+                        for (int piece = 0; piece < L::kPieces; ++piece, ++n) {
+                            const int slot = n % L::kVSlots;
+                            mbar_wait(v_full(slot), uint32_t(n / L::kVSlots) & 1u, dead, late);
+                            tc_fence_after();
+                            const uint32_t v = base + L::kOffV + uint32_t(slot) * L::kVPiece;
+                            const uint32_t pa = tmem + uint32_t(sb * 128 + piece * (L::kVRows / 2));
+    #pragma unroll
+                            for (int j = 0; j < L::kVRows / 16; ++j)
+                                mma_ta<kPair>(tmem + L::kColO, pa + uint32_t(8 * j), sdesc(v + uint32_t(j) * 2048u, L::kVRows * 128, 1024),
+                                              id, b > bl.begin || piece > 0 || j > 0 ? 1u : 0u);
+                            commit_all<kPair>(v_empty(slot));
                         }
-                        commit_all<kPair>(k_empty(slot));
+                        commit_all<kPair>(s_empty(sb));
+                        if (b == bl.end - 1) commit_all<kPair>(o_full);
                     }
-                    commit_all<kPair>(s_full(sb));
-                    if (b == bl.end - 1) commit_all<kPair>(q_empty(qb));
+                }
+            }
+        } else if (warp == 2) {
+            // ---- S = Q K^T
+            if (lane == 0 && rank == 0) {
+                constexpr uint32_t id = idesc(kRows, kKeys, !kF16, false, false);
+                int g = 0, n = 0, items = 0;
+                while (walk.next(it)) {
+                    if (it.begin >= it.end) continue;
+                    const int qb = items % L::kQBufs;
+                    mbar_wait(q_full(qb), uint32_t(items / L::kQBufs) & 1u, dead, late);
+                    ++items;
+                    const uint32_t q = base + uint32_t(qb) * L::kQBytes;
+                    const Blocks<kLine> bl(it);
+                    for (int b = bl.begin; b < bl.end; ++b, ++g) {
+                        const int sb = g % L::kSBufs;
+                        if (g >= L::kSBufs) mbar_wait(s_empty(sb), uint32_t(g / L::kSBufs - 1) & 1u, dead, late);
+    #pragma unroll
+                        for (int piece = 0; piece < L::kPieces; ++piece, ++n) {
+                            const int slot = n % L::kKSlots;
+                            mbar_wait(k_full(slot), uint32_t(n / L::kKSlots) & 1u, dead, late);
+                            tc_fence_after();
+                            const uint32_t k = base + L::kOffK + uint32_t(slot) * L::kKPiece;
+                            const uint32_t qp = q + uint32_t(piece * L::kKCols) * kColBlock;
+    #pragma unroll
+                            for (int j = 0; j < 4 * L::kKCols; ++j) {
+                                const uint32_t off = uint32_t(j & 3) * 32u;
+                                mma<kPair>(tmem + uint32_t(sb * 128), sdesc(qp + uint32_t(j >> 2) * kColBlock + off, 16, 1024),
+                                           sdesc(k + uint32_t(j >> 2) * (L::kKRows * 128) + off, 16, 1024), id, piece > 0 || j > 0 ? 1u : 0u);
+                            }
+                            commit_all<kPair>(k_empty(slot));
+                        }
+                        commit_all<kPair>(s_full(sb));
+                        if (b == bl.end - 1) commit_all<kPair>(q_empty(qb));
+                    }
                 }
             }
         }
-    }
     } else if (warp < kSoftWarp) {
         // ---- Q in, results out
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));

@@ -117,7 +117,7 @@ def test_turning_back_and_differences():
     turn = lambda x: r.rope3d_apply_axes(x, None, pos, freqs, sections)[0]  # noqa: E731
     grad = r.rope3d_apply_axes_backward(y, None, pos, freqs, sections)[0]
     left, right = (turn(q).double() * y.double()).sum(), (q.double() * grad.double()).sum()
-    size = float((q.abs().double().sum((0, 1)) * 0 + 1).sum()) and float((q.double().norm() * y.double().norm()))
+    size = float(q.double().norm() * y.double().norm())
     assert abs(float(left - right)) <= size * 2.0 ** -20
     d = torch.randn(q.shape, generator=g, device=DEV)
     step = ((turn(q + 0.5 * d).double() - turn(q - 0.5 * d).double()) * y.double()).sum()
