@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) axes_kernel(const __grid_co
                     near = exact ? float(int(whole)) : 0.f;
                 }
             } else {
-                exact = place <= (1 << 24);
+                exact = place >= -(1 << 24) && place <= (1 << 24);   // (below 0: a sequence shorter than its new tokens)
             }
             const bool all_near = __all_sync(0xffffffffu, exact);
             for (int j0 = 0; j0 < p.pairs; j0 += 32) {
@@ -435,7 +435,16 @@ Kernel kernel_of(bool halves, bool vec) {
 
 thread_local int t_axes_kernel = 0;   // 1 vectors, 2 single pairs: this thread's last call
 
-constexpr int64_t kMaxPairs = 1024;   // three rows of cos and sin are 24 KB of shared memory
+constexpr int64_t kMaxPairs = 1024;
+constexpr int kTilePairs = 2048;      // tokens x pairs of a tile of more than one token
+static_assert(kMaxPairs <= kTilePairs, "nor are a token's more");
+
+// Shared memory of tiles of `tile` tokens: cosines and sines of two tiles, and a token's
+// frequencies as two floats each.
+constexpr size_t tile_bytes(int64_t tile, int64_t pairs) { return size_t(2 * tile + 1) * 2 * size_t(pairs) * sizeof(float); }
+// (most where 2048 pairs are whole tiles: 40 KB, beside the kernel's static arrays)
+static_assert(tile_bytes(kTilePairs / kMaxPairs, kMaxPairs) + 2 * 2 * kMaxTile * sizeof(int64_t) + 2 * kMaxTile * sizeof(int) <= 48 * 1024,
+              "what a launch has without asking for more");
 
 int elem_of(int32_t dtype) { return dtype == ROPE3D_F32 ? 4 : dtype == ROPE3D_BF16 || dtype == ROPE3D_F16 ? 2 : 0; }
 
@@ -481,13 +490,13 @@ int run(AxesParams &p, int32_t dtype, bool halves, bool vec, const int32_t *sect
     p.tokens_step = rows / int(p.heads_step.d);
     p.end0 = sections[0];
     p.end1 = sections[0] + sections[1];
-    // Tiles of one size for every resident block: cos and sin of a tile take 16 KB,
-    // or a token's, and their frequencies as much as a token's.
-    const int most = std::min(kMaxTile, std::max(1, 2048 / std::max(p.pairs, 1))), blocks = sms * kBlocks;
+    // Tiles of one size for every resident block: cos and sin take 16 KB a tile at most, 32 KB with
+    // the next one's, and the frequencies up to 8 KB.
+    const int most = std::min(kMaxTile, kTilePairs / std::max(p.pairs, 1)), blocks = sms * kBlocks;
     const int rounds = int((int64_t(p.tokens) + int64_t(blocks) * most - 1) / (int64_t(blocks) * most));
     const int tile = int((int64_t(p.tokens) + int64_t(blocks) * rounds - 1) / (int64_t(blocks) * rounds));
     p.tile = tile;
-    const size_t smem = size_t(2 * tile + 1) * 2 * p.pairs * sizeof(float);
+    const size_t smem = tile_bytes(tile, p.pairs);
     const int tiles = (p.tokens + tile - 1) / tile;
     const Kernel fn = dtype == ROPE3D_BF16  ? kernel_of<kAppend, ROPE3D_BF16>(halves, vec)
                       : dtype == ROPE3D_F16 ? kernel_of<kAppend, ROPE3D_F16>(halves, vec)
