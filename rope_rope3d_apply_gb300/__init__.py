@@ -1144,7 +1144,7 @@ def _rotation_fields(positions, freqs, sections, tokens):
     if freqs.dtype is not _torch.float32 or freqs.dim() != 1 or not freqs.is_contiguous():
         raise ValueError("freqs must be float32, contiguous, [pairs]")
     pairs = freqs.shape[0]
-    sections = (pairs, 0, 0) if sections is None else (*sections, 0, 0)[:3] if len(sections) <= 3 else None
+    sections = (pairs, 0, 0) if sections is None else (*sections, 0, 0, 0)[:3] if len(sections) <= 3 else None
     if sections is None or sections[0] + sections[1] + sections[2] != pairs:
         raise ValueError("sections must be up to three counts of pairs that make up freqs")
     if positions is None:
