@@ -51,7 +51,14 @@ struct PartNote {
     int s, h, t, pad;
 };
 
-__device__ __forceinline__ uint32_t udiv(uint32_t n, const rope3d::FastDiv &f) { return (__umulhi(n, f.mul) + n) >> f.shift; }
+// (The arithmetic of the division is compiled for the host too, where tests run it.)
+__host__ __device__ __forceinline__ uint32_t udiv(uint32_t n, const rope3d::FastDiv &f) {
+#ifdef __CUDA_ARCH__
+    return (__umulhi(n, f.mul) + n) >> f.shift;
+#else
+    return rope3d::fastdiv_host(n, f);
+#endif
+}
 
 // A sequence as the line of blocks sees it.
 struct Seq {
@@ -59,7 +66,7 @@ struct Seq {
 };
 
 template <int kRows>
-__device__ __forceinline__ Seq seq_of(const AttnParams &p, int s) {
+__host__ __device__ __forceinline__ Seq seq_of(const AttnParams &p, int s) {
     Seq q;
     int hi;
     sequence(p.batch, s, q.lo, hi, q.len);
@@ -71,11 +78,11 @@ __device__ __forceinline__ Seq seq_of(const AttnParams &p, int s) {
 // Blocks [b0, b1) of tile t; the places [k0, k1) that its rows see.
 struct Tile {
     int b0, b1, k0, k1;
-    __device__ int blocks() const { return max(b1 - b0, 1); }
+    __host__ __device__ int blocks() const { return max(b1 - b0, 1); }
 };
 
 template <int kRows, int kKeys>
-__device__ __forceinline__ Tile tile_of(const AttnParams &p, const Seq &q, int t) {
+__host__ __device__ __forceinline__ Tile tile_of(const AttnParams &p, const Seq &q, int t) {
     const uint32_t rows = uint32_t(q.n) * p.group.d, last = min(rows, uint32_t(t + 1) * kRows) - 1;
     const int past = q.len - q.n;   // place of the first new token; negative where the length is too short
     Tile r;
@@ -93,7 +100,7 @@ __device__ __forceinline__ Tile tile_of(const AttnParams &p, const Seq &q, int t
 // floor((G (past + K) + T - 1) / T), and a window leaves out floor((c + u) / D) of
 // them, c = floor(G (past - window + 1) / T): sums of floors in a row.
 template <typename T>
-__device__ __forceinline__ T floors(T n, const rope3d::FastDiv &f) {   // sum of floor(i / d) over 0 <= i < n
+__host__ __device__ __forceinline__ T floors(T n, const rope3d::FastDiv &f) {   // sum of floor(i / d) over 0 <= i < n
     const T d = T(f.d), q = sizeof(T) == 4 || n < 0x7fffffff ? T(udiv(uint32_t(n), f)) : n / d;
     return q * (q - 1) / 2 * d + q * (n - q * d);
 }
@@ -104,7 +111,7 @@ template <typename T, int kRows, int kKeys>
 struct Costs {
     T a, c, each;   // each: blocks of a tile that is not causal
 
-    __device__ __forceinline__ Costs(const AttnParams &p, const Seq &q) {
+    __host__ __device__ __forceinline__ Costs(const AttnParams &p, const Seq &q) {
         static_assert(kKeys % kRows == 0 && (kRows == 256 || kRows == 128 || kRows == 16), "D is whole");
         constexpr int kShift = kRows == 256 ? 8 : kRows == 128 ? 7 : 4;
         const T group = T(p.group.d), past = T(q.len - q.n);
@@ -114,7 +121,7 @@ struct Costs {
     }
 
     // of tiles 0 .. t - 1
-    __device__ __forceinline__ T at(const AttnParams &p, int t) const {
+    __host__ __device__ __forceinline__ T at(const AttnParams &p, int t) const {
         const T d = T(p.span.d);
         T sum = each * t;
         if (p.causal) {   // at least 1 each
@@ -126,7 +133,7 @@ struct Costs {
     }
 
     // The last of `tiles` that begins at or before place `in` of the line, and where it begins.
-    __device__ __forceinline__ int find(const AttnParams &p, int tiles, T in, T &begins) const {
+    __host__ __device__ __forceinline__ int find(const AttnParams &p, int tiles, T in, T &begins) const {
         int t = 0, above = tiles;
         begins = 0;
 #pragma unroll 1
@@ -147,14 +154,14 @@ struct Costs {
 // Whether 32 bits do: with fewer than 64 rows a token, and tokens and places times those below
 // 2^17, n in floors() is below 2^15 and every sum of theirs below 2^31 (16 rows a tile; larger
 // tiles less).
-__device__ __forceinline__ bool small_costs(const AttnParams &p, const Seq &q) {
+__host__ __device__ __forceinline__ bool small_costs(const AttnParams &p, const Seq &q) {
     const int most = (1 << 17) / int(p.group.d);
     return p.group.d < 64 && q.len < most && q.n < most && p.window < (1 << 17);
 }
 
 // The cost of one key/value head of a sequence.
 template <int kRows, int kKeys>
-__device__ __forceinline__ long long seq_cost(const AttnParams &p, const Seq &q) {
+__host__ __device__ __forceinline__ long long seq_cost(const AttnParams &p, const Seq &q) {
     if (q.tiles == 0) return 0;
     const long long last = tile_of<kRows, kKeys>(p, q, q.tiles - 1).blocks() + p.item_cost;
     if (q.tiles == 1) return last;
@@ -170,7 +177,7 @@ struct Start {
 };
 
 // floor(total * part / parts)
-__device__ __forceinline__ long long cut(const AttnParams &p, long long total, int part) {
+__host__ __device__ __forceinline__ long long cut(const AttnParams &p, long long total, int part) {
     if (total < (1 << 21)) return udiv(uint32_t(total) * uint32_t(part), p.cuts);   // (fewer than 1024 parts)
     const long long whole = total < 0x7fffffff ? (long long)udiv(uint32_t(total), p.cuts) : total / p.parts;
     return whole * part + udiv(uint32_t(total - whole * p.parts) * uint32_t(part), p.cuts);
@@ -179,7 +186,7 @@ __device__ __forceinline__ long long cut(const AttnParams &p, long long total, i
 // The item at place `begin` of the line, in a sequence whose first is `before` and whose
 // heads cost `head` each.
 template <int kRows, int kKeys>
-__device__ __forceinline__ void start_in(const AttnParams &p, int s, const Seq &q, long long before, long long head, long long begin,
+__host__ __device__ __forceinline__ void start_in(const AttnParams &p, int s, const Seq &q, long long before, long long head, long long begin,
                                          Start *out) {
     const long long in = begin - before;
     out->s = s;
@@ -201,6 +208,23 @@ __device__ __forceinline__ void start_in(const AttnParams &p, int s, const Seq &
     out->off = int(begin - before);
     out->item = before;
     out->cost = tile_of<kRows, kKeys>(p, q, t).blocks() + p.item_cost;
+}
+
+// Sequences [first, end) of a thread, which begin at `before` and cost `sum` together: the item
+// at place `begin` of the line, if it is one of theirs. (q and head: the last of them.)
+template <int kRows, int kKeys>
+__host__ __device__ __forceinline__ void start_among(const AttnParams &p, int first, int end, Seq q, long long before, long long sum,
+                                                     long long head, long long begin, long long stop, Start *out) {
+    if (begin >= stop || begin < before || begin >= before + sum) return;
+    int s = first;
+    while (end - first > 1) {   // which of the thread's sequences
+        q = seq_of<kRows>(p, s);
+        head = seq_cost<kRows, kKeys>(p, q);
+        if (begin < before + head * p.kv_heads) break;
+        before += head * p.kv_heads;
+        ++s;
+    }
+    start_in<kRows, kKeys>(p, s, q, before, head, begin, out);
 }
 
 template <int kRows, int kKeys, int kThreads>
@@ -231,17 +255,7 @@ __device__ void find_start(const AttnParams &p, int part, Start *out, long long 
         total += s_sums[w];
     }
     const long long begin = cut(p, total, part), stop = cut(p, total, part + 1);
-    if (begin < stop && begin >= before && begin < before + sum) {
-        int s = first;
-        while (each > 1) {   // which of the thread's sequences
-            q = seq_of<kRows>(p, s);
-            head = seq_cost<kRows, kKeys>(p, q);
-            if (begin < before + head * p.kv_heads) break;
-            before += head * p.kv_heads;
-            ++s;
-        }
-        start_in<kRows, kKeys>(p, s, q, before, head, begin, out);
-    }
+    start_among<kRows, kKeys>(p, first, end, q, before, sum, head, begin, stop, out);
     if (tid == 0) {
         out->begin = begin;
         out->end = stop;
@@ -269,12 +283,12 @@ struct Walker {
     int s, h, t, off;
     Seq q;
 
-    __device__ Walker(const AttnParams &params, const Start &st)
+    __host__ __device__ Walker(const AttnParams &params, const Start &st)
         : p(params), left(st.s < 0 ? 0 : st.end - st.begin), s(st.s), h(st.h), t(st.t), off(st.off) {
         if (left) q = seq_of<kRows>(p, s);
     }
 
-    __device__ bool next(Item &it) {
+    __host__ __device__ bool next(Item &it) {
         while (left > 0) {
             while (t >= q.tiles) {   // the next head, or the next sequence with tokens
                 t = 0;
@@ -311,7 +325,7 @@ struct RowOf {
 };
 
 template <int kRows>
-__device__ __forceinline__ RowOf row_of(const AttnParams &p, const Item &it, int r) {
+__host__ __device__ __forceinline__ RowOf row_of(const AttnParams &p, const Item &it, int r) {
     const uint32_t g = uint32_t(it.t) * kRows + uint32_t(r), i = udiv(g, p.group);
     RowOf o;
     o.token = it.q.lo + int(i);

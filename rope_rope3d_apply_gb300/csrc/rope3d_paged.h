@@ -196,7 +196,7 @@ inline Batch device_batch(const rope3d_paged_batch &b, int64_t tokens) {
 #ifdef __CUDACC__
 // The new tokens [lo, hi) of sequence s, and its length with them; whatever the
 // arrays hold, they stay within the call's tokens and the table's row.
-__device__ __forceinline__ void sequence(const Batch &b, int s, int &lo, int &hi, int &len) {
+__host__ __device__ __forceinline__ void sequence(const Batch &b, int s, int &lo, int &hi, int &len) {
     if (b.starts) {
         lo = min(max(b.starts[s], 0), b.tokens);
         hi = min(max(b.starts[s + 1], lo), b.tokens);
