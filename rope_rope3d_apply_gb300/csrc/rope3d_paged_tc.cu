@@ -55,6 +55,7 @@ constexpr int kKeys = 128;       // places of a block of keys
 constexpr int kLanes = 128;      // rows of a block of threads: tensor memory's lanes
 constexpr int kThreads = 512, kSoftWarp = 8;
 constexpr float kLazy = 8.0f;
+constexpr int64_t kMostTilePlaces = int64_t(1) << 23;   // see tiles_fit
 // Registers of a thread: 512 threads have 128 each at launch; the softmax's 256 have
 // kSoftRegs and the others kOtherRegs, no more together. (Other splits between the copying, the
 // output's and the softmax's warps, 48 to 104 / 56 to 80 / 168 to 192: the same times, or up to 5 %
@@ -746,10 +747,14 @@ int launch_tile(const AttnParams &p, bool pair, int box, const CUtensorMap &k, c
 }  // namespace
 
 // What the tensor maps can describe: pages of whole groups of eight places (the
-// swizzle's period in shared memory), strides above zero.
+// swizzle's period in shared memory), strides above zero. And items that end within a
+// bounded wait: an item's result is waited for from its beginning on, for 10^9 clocks at most,
+// and a block of 128 places takes up to 5,600 (256 channels, every SM reading 128 KB of its own at
+// the memory's rate). 2^23 places are 3.7 * 10^8 clocks; longer rows go to the kernel for few rows,
+// which waits for nothing.
 bool rope3d_paged::tiles_fit(const rope3d_paged_attention_args &a) {
     const rope3d_paged_batch &b = a.batch;
-    if (b.page_size % 8 != 0) return false;
+    if (b.page_size % 8 != 0 || b.table_width * b.page_size > kMostTilePlaces) return false;
     for (const int64_t s : {a.k_slot_stride, a.v_slot_stride})
         if (b.page_size > 1 && (s <= 0 || s * 2 >= kMaxStride)) return false;
     for (const int64_t s : {a.k_cache_head_stride, a.v_cache_head_stride})
