@@ -743,18 +743,26 @@ int rope3d_cache_append_check(const rope3d_cache_append_args *args, int32_t chec
  *                 finite, at a place that one row of a call sees, may reach rows of the
  *                 same sequence and key/value head whose mask leaves it out.)
  *   head_dim      a multiple of 8, up to 256; q_heads a multiple of kv_heads
+ *   page_size     any. More than 16 rows that share keys (new tokens x q_heads /
+ *                 kv_heads) are computed in tiles where it is a multiple of 8 and
+ *                 table_width * page_size is 2^23 at most; else 16 at a time, which
+ *                 is many times slower for prompts
  *   lse           fp32 [tokens, q_heads], token stride lse_stride; NULL: not kept
  *   scale         above 0, and finite in fp32
  *   window        0: none
  *   max_new       at least the most new tokens of a sequence, for the choice of the
- *                 kernel alone (results do not depend on it); 0: not known
+ *                 kernel alone; 0: not known, which is taken for as many as the call
+ *                 has where q_starts is given (single tokens of many sequences then
+ *                 take up to about twice as long). A wrong one is slower at most. Results of
+ *                 two choices agree within rounding, not bit for bit
  *   workspace     device, 256-byte aligned, of at least the size that
  *                 rope3d_paged_attention_workspace gives for the same arguments;
  *                 its contents are not kept. Calls that may run at the same
  *                 time need workspaces of their own.
  * Scores, statistics and sums are fp32; the weights are rounded once to `dtype`
- * as an operand of the second product, and out once. The same call gives the same
- * bits. Rows of out and lse behind the last sequence are left as they were.
+ * as an operand of the second product, and out once. The same call, max_new
+ * included, gives the same bits. Rows of out and lse behind the last sequence are
+ * left as they were.
  * Two kernels on `stream`, asynchronous.
  * Errors: NULL, SHAPE, DTYPE, ARG (scale, causal, window, max_new), ALIGN, ALIAS,
  * SCRATCH, DEVICE, CUDA.

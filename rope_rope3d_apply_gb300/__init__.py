@@ -1252,8 +1252,9 @@ def rope3d_paged_attention(q, k_cache, v_cache, page_table, seq_lens, q_starts=N
     keys and values have entered the cache: softmax(scale * q k) v over the places of the
     sequence, up to the token's own where causal, and its last `window` of them where
     window > 0. scale None: head_dim ** -0.5. max_new: the most new tokens of a
-    sequence where the caller knows (a better choice of kernel, never another
-    result). lse: True, or a float32 [tokens, q_heads] tensor, for the rows' log sum
+    sequence where the caller knows, for the choice of the kernel (results agree within
+    rounding; with q_starts and without it, single tokens take up to about twice
+    as long). lse: True, or a float32 [tokens, q_heads] tensor, for the rows' log sum
     exp too. Rows that see no key are zeros (lse -inf); rows behind the last sequence
     are left as they are (in a new out or lse: what the memory held). Returns out, or
     (out, lse). workspace: a contiguous device tensor of at least the bytes the call
