@@ -733,8 +733,8 @@ int rope3d_cache_append_check(const rope3d_cache_append_args *args, int32_t chec
  *     out = sum_j softmax_j(scale * q . k_j) v_j
  *     lse = log sum_j exp(scale * q . k_j)            (optional)
  * One token a sequence, whole prompts, chunks over a long cache and mixtures of
- * them are one call. A row that sees no key gives zeros and lse = -inf. Keys on
- * absent pages are left out.
+ * them are one call. A row that sees no key, or none with a score above -inf,
+ * gives zeros and lse = -inf. Keys on absent pages are left out.
  *
  *   q, out        [tokens, q_heads, head_dim] of `dtype` (BF16 or F16); strides
  *                 and addresses multiples of 16 bytes
