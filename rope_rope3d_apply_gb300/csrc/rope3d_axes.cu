@@ -19,8 +19,10 @@
 // flight; warps that are done with a tile prepare the next one's while the others move.
 // Cosines and sines lie apart, so that a warp's 16-byte reads of either meet no bank twice.
 // What bounds it is memory: 65,536 tokens of 2 x 16 heads of 128, bf16, out of a fused projection
-// 174 us, 6,170 GB/s, 93 % of a copy on the same GPU; 5,138 new tokens of 8 / 4 heads of 256 into pages
-// 17 us, 4,950 GB/s; small calls, the launch.
+// 172 us, 6,250 GB/s, 93 % of a copy on the same GPU; fp32 334 us, 6,450 GB/s. 5,138 new tokens of 8 / 4
+// heads of 256 into pages take 20.3 us, 4,150 GB/s (16 where the inputs lie in L2): each block has one tile, whose
+// loads wait for its cosines. Small calls: the launch. Single pairs are bound by their loads of single
+// elements: the first of these with 63 pairs in halves 740 us, at odd addresses 554, in fp32 there 384.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

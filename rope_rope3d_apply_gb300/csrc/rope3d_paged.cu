@@ -13,7 +13,10 @@
 // 16-byte cp.async copies, rows outside the mask filled with zeros and not read) and
 // keeps a maximum, a sum and sums of V of its own, so that warps meet only at an
 // item's end. Products are warp MMAs (m16n8k16): at 16 rows the tensor cores have
-// next to nothing to do, and fragments come straight from the swizzled ring.
+// next to nothing to do, and fragments come straight from the swizzled ring. The weights are rounded to the
+// cache's type for the second product, as its operand has to be (their sum is of the unrounded ones): the
+// result's relative error (2-norm, against 64 bits) is 0.0020 to 0.0021 in bf16 and 0.00027 to 0.00028 in fp16
+// where that of weights kept in 32 bits is 0.0016 to 0.0017 and 0.00021, the rounding of the result itself.
 // Measured: 64 sequences of 100 to 16,000 places of 8 heads of 128, fp16, pages of 16: 317 us,
 // 6,620 GB/s, 97.5 % of a copy; of 8192 places of 4 heads of 256, bf16: 327 us, 6,570 GB/s; of 64:
 // 97 us, 5,530 GB/s (the softmax's instructions are the same for half the bytes). One sequence
@@ -545,10 +548,13 @@ Choice choose(const rope3d_paged_attention_args &a) {
     int64_t most = b.q_starts ? a.tokens : a.tokens / b.seqs;
     if (a.max_new) most = std::min(most, a.max_new);
     Choice c{};
-    // By the rows that share keys. 32 sequences of 8192 places of 4 heads of 128, us: 16 rows 94 as few;
-    // 24 rows 173 as few, 107 in tiles; 128 rows 112 in tiles; 160 rows 196 in tiles, 141 in pairs. (Where all
-    // is short, few rows stay ahead for longer: 32 rows of one sequence of 2000 places 14 and 19; the
-    // lengths are not known here.)
+    // By the rows that share keys, at the borders (us). Few rows / tiles: 32 sequences of 8192 places of 4 heads of
+    // 128, 16 rows 94 / 137 (pairs), 24 rows 172 / 106; of 4 heads of 256, 177 / 201 and 333 / 198; of 8 heads of
+    // 64, 109 / 147 and 166 / 149; 8 sequences of 2000 places of 4 heads of 256, 23 / 28 and 34 / 31. Tiles / pairs:
+    // the first of these, 128 rows 112 / 140, 160 rows 195 / 141; the second, 211 / 214 and 371 / 219; the last,
+    // 35 / 39 and 47 / 41. (Where all is short, few rows stay ahead for longer, by up to a third: 32 rows of one
+    // sequence of 2000 places of 4 heads of 128 14 and 18, of 8192 17 and 24, 8 sequences of 2000 21 and 23; the
+    // lengths are not known here. Tiles and pairs are then within 1 us of one another.)
     if (most * group > kFewRows && tiles_fit(a)) c.kind = most * group > kTileRows && pairs_fit(a) ? 2 : 1;
     c.rows = c.kind == 2 ? kPairRows : c.kind ? kTileRows : kFewRows;
     c.keys = c.kind == 2 ? 256 : c.kind ? 128 : kKeys;

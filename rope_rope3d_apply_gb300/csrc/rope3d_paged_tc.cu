@@ -16,7 +16,8 @@
 //     blocks in turn: one's exponentials run while the other waits for S, finds its maximum
 //     or hands over. The maximum that weights refer to goes from group to group through
 //     shared memory (before the exponentials); it moves only when it is exceeded by more
-//     than 2^kLazy, and O is rescaled in tensor memory then. A row's 128 scores stay in
+//     than 2^kLazy, and O is rescaled in tensor memory then (a published way to rescale seldom; the
+//     weights, up to 2^8, and their sums have the room; they are rounded as in rope3d_paged.cu). A row's 128 scores stay in
 //     registers (the other warps give some of theirs up) from one read of tensor memory to
 //     the weights, which are written over S as pairs of 16 bits.
 // head_dim is padded to 64, 128 or 256 channels by TMA's zero fill. At 256 a block's K
@@ -57,9 +58,10 @@ constexpr int kThreads = 512, kSoftWarp = 8;
 constexpr float kLazy = 8.0f;
 constexpr int64_t kMostTilePlaces = int64_t(1) << 23;   // see tiles_fit
 // Registers of a thread: 512 threads have 128 each at launch; the softmax's 256 have
-// kSoftRegs and the others kOtherRegs, no more together. (Other splits between the copying, the
-// output's and the softmax's warps, 48 to 104 / 56 to 80 / 168 to 192: the same times, or up to 5 %
-// longer where the copying and issuing warps have fewer than 72.)
+// kSoftRegs and the others kOtherRegs, no more together. (The compiler spills 8 to 10 of them, with 440 to 488
+// bytes of stores and 332 to 412 of loads in the text; of a copy without the softmax's part 2.
+// Other splits between the copying, the output's and the softmax's warps, 48 to 104 / 56 to 80 /
+// 168 to 192: the same times, or up to 5 % longer where the copying and issuing warps have fewer than 72.)
 constexpr int kSoftRegs = 184, kOtherRegs = 72;
 static_assert(256 * (kSoftRegs + kOtherRegs) <= kThreads * 128, "no more registers than the block has");
 constexpr uint32_t kColBlock = kLanes * 128;   // bytes of 64 channels of 128 rows
